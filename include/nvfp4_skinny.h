@@ -117,9 +117,10 @@ const char *nvfp4_status_string(nvfp4_status st);
 uint32_t nvfp4_layout_version(void);
 
 /*
- * Device error word: bit 0 = a kernel's bounded wait ran out of time.  Reads
- * the word (synchronously, on the current device) into *out and clears it if
- * `clear` is nonzero.
+ * Device error word: bit 0 = a kernel's bounded wait ran out of time; bit 2 = a
+ * page id or cache slot outside its pool was met (kv_append, paged_attention).
+ * Reads the word (synchronously, on the current device) into *out and clears it
+ * if `clear` is nonzero.
  */
 nvfp4_status nvfp4_device_error(uint32_t *out, int32_t clear);
 
@@ -414,6 +415,152 @@ nvfp4_status lm_head_sample_ex(const nvfp4_weight *w, const uint16_t *x, int32_t
  */
 nvfp4_status lm_head_argmax_noalloc(const nvfp4_weight *w, const uint16_t *x, int32_t m, float *max_logit,
                                     int32_t *argmax, cudaStream_t stream);
+
+/* ---------------------------------------------------------------- attention side
+ *
+ * Rotary positions, the append to a paged key/value cache, and attention over
+ * it: what a decode step runs between the products above.  The pages name these
+ * parts (gemma-cuda-hybrid README, "Everything it has": head-packed GQA
+ * attention, an FP8 E4M3 KV cache, RoPE; TensorSharp docs/models/gemma4.md:
+ * window and global attention, RoPE flavors, paged KV) without formulas; the
+ * formulas below are the usual ones, written out.
+ *
+ * Rows of heads: x [tokens, heads, head_dim] bf16 with the heads of a token
+ * contiguous and `stride` elements from one token to the next (>= heads *
+ * head_dim, a multiple of 8), so that slices of a fused projection's rows can be
+ * passed as they are.  Row pointers are 16-byte aligned.
+ */
+
+/*
+ * A paged cache (a view; the caller owns the memory).
+ *   k, v        (device) pools [num_pages, n_kv_heads, page_size, head_dim],
+ *               16-byte aligned; consecutive pages are page_stride elements apart
+ *               (>= n_kv_heads * page_size * head_dim; page_stride * element size
+ *               a multiple of 16), so k and v may share one pool.
+ *   k_scale, v_scale (device) fp32 [n_kv_heads]: an E4M3 cache holds code * scale;
+ *               NULL for all ones; must be NULL for a bf16 cache.  Positive.
+ *   page_size   16, 32, 64, 128 or 256.  head_dim 64, 128 or 256.
+ *   dtype       NVFP4_KV_BF16 or NVFP4_KV_E4M3.
+ */
+#define NVFP4_KV_BF16 0u
+#define NVFP4_KV_E4M3 1u
+typedef struct {
+  void *k;
+  void *v;
+  const float *k_scale;
+  const float *v_scale;
+  int64_t page_stride;
+  int32_t num_pages;
+  int32_t page_size;
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  uint32_t dtype;
+} nvfp4_kv_cache;
+
+/*
+ * The sequences of one attention call.
+ *   cu_tokens   (device) int32 [n_seqs + 1], ascending from 0: sequence b's new
+ *               tokens are rows cu_tokens[b] .. cu_tokens[b + 1).
+ *   kv_len      (device) int32 [n_seqs]: keys in the cache, the new tokens' own
+ *               among them.
+ *   page_table  (device) int32 [n_seqs, max_pages]: the page that holds keys
+ *               [i * page_size, (i + 1) * page_size); entries past the last key
+ *               (and, with a window, before the first one that is seen) are not read
+ *               into the result and may hold anything.
+ *   max_new     at least the most new tokens of any sequence (host value: it sizes
+ *               the launch).
+ */
+typedef struct {
+  const int32_t *cu_tokens;
+  const int32_t *kv_len;
+  const int32_t *page_table;
+  int32_t n_seqs;
+  int32_t max_pages;
+  int32_t max_new;
+} nvfp4_batch;
+
+#define NVFP4_ROPE_INTERLEAVED 1 /* pairs (2i, 2i + 1); otherwise (i, i + rot_dim / 2) */
+#define NVFP4_ROPE_INVERSE 2     /* rotate back (the gradient of the rotation) */
+
+/*
+ * Frequencies of rotary positions, in radians a position (host; synchronous; no
+ * GPU needed): w_i = theta^(-2 i / rot_dim), i < rot_dim / 2.  factor > 1
+ * stretches them for contexts beyond the trained one: with trained_context = 0
+ * every w_i is divided by factor (position interpolation); otherwise pair i, which
+ * makes r = trained_context * w_i / (2 pi) turns over the trained context, gets
+ * w_i * (g + (1 - g) / factor), g = (r - slow) / (fast - slow) clamped to [0, 1]:
+ * fast pairs keep their frequency, slow ones are interpolated.
+ *   inv_freq  (host) fp64 [rot_dim / 2].
+ * NVFP4_ERR_SHAPE: rot_dim not a multiple of 16 in [16, 512], theta <= 1, factor
+ * < 1, a negative context, fast <= slow (with a context), or not finite.
+ */
+nvfp4_status rope_frequencies(int32_t rot_dim, double theta, double factor, double trained_context, double slow,
+                              double fast, double *inv_freq);
+
+/*
+ * Rotary positions on the first rot_dim values of every head; the rest is copied:
+ *   y_a = amplitude * (x_a cos t - x_b sin t),  y_b = amplitude * (x_b cos t + x_a sin t)
+ * for pair i = (a, b) and t = positions[token] * inv_freq[i].  The angle is
+ * reduced exactly (64-bit turns), so far positions lose nothing; the products
+ * are fp32, rounded once.
+ *   x, y       (device) rows of heads; y may be x (same stride).
+ *   positions  (device) int32 [n_tokens], any sign.
+ *   inv_freq   (device) fp64 [rot_dim / 2], finite, >= 0, below 2^63.
+ *   head_dim   a multiple of 16, up to 512; rot_dim a multiple of 16 up to head_dim.
+ *   flags      NVFP4_ROPE_*; other bits: NVFP4_ERR_SHAPE.  amplitude finite.
+ * n_tokens = 0 is allowed (nothing is launched).
+ */
+nvfp4_status rope_apply(const uint16_t *x, int64_t x_stride, int32_t n_tokens, int32_t n_heads, int32_t head_dim,
+                        const int32_t *positions, const double *inv_freq, int32_t rot_dim, float amplitude,
+                        int32_t flags, uint16_t *y, int64_t y_stride, cudaStream_t stream);
+
+/*
+ * Append to a paged cache: token t's keys, rotated as by rope_apply, and values
+ * go to slot slots[t] = page * page_size + offset of every kv head; with q, the
+ * queries are rotated in the same launch.  An E4M3 cache gets the code nearest to
+ * value / scale (ties to even, saturating at 448; NaN stays NaN), rounded once
+ * from the fp32 rotation.
+ *   k, v       (device) rows of n_kv_heads heads, strides k_stride and v_stride.
+ *   slots      (device) int64 [n_tokens]; a negative slot skips its token's cache
+ *              rows (padding); one past the pool is skipped and sets bit 2 of the
+ *              device error word.  Two tokens with the same slot race.
+ *   positions, inv_freq, rot_dim, amplitude, flags: as rope_apply; rot_dim = 0
+ *              rotates nothing (positions and inv_freq may be NULL then).
+ *              NVFP4_ROPE_INVERSE is not accepted here.
+ *   q, q_out   (device) rows of n_heads heads, or both NULL; q_out may be q.
+ */
+nvfp4_status kv_append(const nvfp4_kv_cache *cache, const uint16_t *k, int64_t k_stride, const uint16_t *v,
+                       int64_t v_stride, int32_t n_tokens, const int64_t *slots, const int32_t *positions,
+                       const double *inv_freq, int32_t rot_dim, float amplitude, int32_t flags, const uint16_t *q,
+                       int64_t q_stride, int32_t n_heads, uint16_t *q_out, int64_t q_out_stride, cudaStream_t stream);
+
+/*
+ * Attention of every sequence's new tokens over its keys in the paged cache.
+ * Token i of a sequence's n new tokens is at position p = kv_len - n + i and sees
+ * keys j <= p, and with window > 0 only j > p - window; its head h reads kv head
+ * h / (n_heads / n_kv_heads):
+ *   s_j = scale * q . k_j,  with softcap > 0: s_j = softcap * tanh(s_j / softcap)
+ *   out = sum_j exp(s_j) v_j / sum_j exp(s_j),   lse = log sum_j exp(s_j)
+ * over the keys seen; a token that sees none (or only keys with s_j = -inf) gets
+ * zeros and lse = -inf.  Keys that a token does not see leave no trace in its
+ * row, whatever they hold (infinities and NaN among them).  The softmax runs in
+ * fp32; each weight is rounded to 16 bits for the product with v.
+ *   q          (device) rows of n_heads heads (n_heads a multiple of n_kv_heads).
+ *   out        (device) rows of n_heads heads; rows past cu_tokens[n_seqs] are not
+ *              written.  lse (device) fp32 [n_tokens, n_heads] or NULL.
+ *   scale      finite; softcap finite, >= 0; window >= 0 (0: all keys).
+ *   ws         (device) paged_attention_workspace_bytes() bytes, 16-byte aligned;
+ *              needs no initialisation and holds nothing between calls.
+ * kv_len is read as at most max_pages * page_size, cu_tokens as ascending and at
+ * most n_tokens.  A page id outside the pool among the keys that are seen reads
+ * as zeros and sets bit 2 of the device error word.
+ */
+size_t paged_attention_workspace_bytes(int32_t n_tokens, int32_t n_seqs, int32_t max_new, int32_t n_heads,
+                                       int32_t n_kv_heads, int32_t head_dim);
+nvfp4_status paged_attention(const nvfp4_kv_cache *cache, const nvfp4_batch *batch, const uint16_t *q,
+                             int64_t q_stride, int32_t n_tokens, int32_t n_heads, float scale, float softcap,
+                             int32_t window, uint16_t *out, int64_t out_stride, float *lse, void *ws,
+                             size_t ws_bytes, cudaStream_t stream);
 
 /*
  * The launch plan a product would use, for host-side checks of the work

@@ -18,6 +18,10 @@ from .build import LIB
 
 NVFP4_GATED = 1
 NVFP4_ROUTE_SOFTMAX_ALL = 1
+NVFP4_KV_BF16 = 0
+NVFP4_KV_E4M3 = 1
+NVFP4_ROPE_INTERLEAVED = 1
+NVFP4_ROPE_INVERSE = 2
 LAYOUT_VERSION = 2
 
 STATUS = {0: "ok", 1: "null pointer", 2: "bad shape", 3: "misaligned pointer",
@@ -30,6 +34,7 @@ EXPORTS = (
     "lm_head_workspace_bytes", "lm_head_argmax", "lm_head_argmax_noalloc", "nvfp4_plan_info",
     "lm_head_sample", "moe_route_topk_ex", "lm_head_sample_ex", "nvfp4_plan_check", "moe_router_logits",
     "nvfp4_repack_host", "nvfp4_quantize_act", "nvfp4_gemm_w4a4", "lm_head_argmax_w4a4", "moe_forward", "nvfp4_selftest_wait_timeout",
+    "rope_frequencies", "rope_apply", "kv_append", "paged_attention_workspace_bytes", "paged_attention",
 )
 
 
@@ -65,9 +70,69 @@ class Weight:
         return self.num_matrices * (self.n * self.k // 2 + self.n * self.k // 16)
 
 
+class CKVCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_uint32)]
+
+
+class CBatch(ctypes.Structure):
+    _fields_ = [("cu_tokens", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("n_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("max_new", ctypes.c_int32)]
+
+
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+class KVCache:
+    """A paged key/value cache on the GPU: pools [num_pages, n_kv_heads, page_size, head_dim] of bf16, or of
+    float8_e4m3fn holding value / scale with fp32 scales per kv head (None: ones).  Pages may be strided (k and v
+    in one pool); the rest is contiguous.  Keeps its tensors alive; make it once per pool."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor = None, v_scale: torch.Tensor = None):
+        _need(k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype and k.stride() == v.stride(),
+              "k and v: pools of one shape, type and layout, [num_pages, n_kv_heads, page_size, head_dim]")
+        _need(k.is_cuda and v.device == k.device, "k and v: pools on one GPU")
+        _need(k.dtype in (torch.bfloat16, torch.float8_e4m3fn), "k and v: bf16 or float8_e4m3fn")
+        pages, heads, page, dim = k.shape
+        _need(k.stride()[1:] == (page * dim, dim, 1), "the heads of a page have to be contiguous")
+        for s in (k_scale, v_scale):
+            _need(s is None or (s.dtype == torch.float32 and s.shape == (heads,) and s.is_contiguous()
+                                and s.device == k.device), "scales: contiguous fp32 [n_kv_heads] on the cache's GPU")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.n_kv_heads, self.page_size, self.head_dim, self.device = heads, page, dim, k.device
+        stride = k.stride(0) if pages > 1 else heads * page * dim
+        self.c = CKVCache(k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale), stride, pages, page, heads, dim,
+                          NVFP4_KV_BF16 if k.dtype == torch.bfloat16 else NVFP4_KV_E4M3)
+        self.ref = ctypes.byref(self.c)
+
+
+class Batch:
+    """The sequences of an attention call: cu_tokens int32 [n_seqs + 1], kv_len int32 [n_seqs] (new tokens
+    included), page_table int32 [n_seqs, max_pages], and max_new, a bound on the new tokens of any sequence.
+    Keeps its tensors alive; their contents may change between calls (a captured graph reads them anew)."""
+
+    def __init__(self, cu_tokens: torch.Tensor, kv_len: torch.Tensor, page_table: torch.Tensor, max_new: int):
+        n = kv_len.shape[0]
+        _need(page_table.dim() == 2 and cu_tokens.shape == (n + 1,) and kv_len.shape == (n,)
+              and page_table.shape[0] == n, "cu_tokens [n_seqs + 1], kv_len [n_seqs], page_table [n_seqs, max_pages]")
+        for x in (cu_tokens, kv_len, page_table):
+            _need(x.dtype == torch.int32 and x.is_contiguous() and x.is_cuda and x.device == kv_len.device,
+                  "cu_tokens, kv_len, page_table: contiguous int32 on one GPU")
+        self.cu_tokens, self.kv_len, self.page_table, self.max_new = cu_tokens, kv_len, page_table, int(max_new)
+        self.device = kv_len.device
+        self.c = CBatch(cu_tokens.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), n, page_table.shape[1],
+                        self.max_new)
+        self.ref = ctypes.byref(self.c)
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
 _SZ = ctypes.c_size_t
+_I64 = ctypes.c_int64
 
 
 def _sig(lib):
@@ -121,6 +186,18 @@ def _sig(lib):
     lib.lm_head_argmax_w4a4.restype = ctypes.c_int
     lib.nvfp4_repack_host.argtypes = [_P, _P, _I, _I, _I, ctypes.c_uint32, _P, _SZ]
     lib.nvfp4_repack_host.restype = ctypes.c_int
+    lib.rope_frequencies.argtypes = [_I] + [ctypes.c_double] * 5 + [_P]
+    lib.rope_frequencies.restype = ctypes.c_int
+    lib.rope_apply.argtypes = [_P, _I64, _I, _I, _I, _P, _P, _I, ctypes.c_float, _I, _P, _I64, _P]
+    lib.rope_apply.restype = ctypes.c_int
+    lib.kv_append.argtypes = [_P, _P, _I64, _P, _I64, _I, _P, _P, _P, _I, ctypes.c_float, _I, _P, _I64, _I, _P, _I64,
+                              _P]
+    lib.kv_append.restype = ctypes.c_int
+    lib.paged_attention_workspace_bytes.restype = _SZ
+    lib.paged_attention_workspace_bytes.argtypes = [_I] * 6
+    lib.paged_attention.argtypes = [_P, _P, _P, _I64, _I, _I, ctypes.c_float, ctypes.c_float, _I, _P, _I64, _P, _P,
+                                    _SZ, _P]
+    lib.paged_attention.restype = ctypes.c_int
     for name in ("nvfp4_quantize", "nvfp4_repack", "nvfp4_gemm", "moe_route_topk", "moe_ffn_grouped",
                  "lm_head_argmax", "lm_head_argmax_noalloc", "nvfp4_device_error"):
         getattr(lib, name).restype = ctypes.c_int
@@ -134,6 +211,22 @@ def _stream(stream) -> int:
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
+
+
+def _rows(x: torch.Tensor, what: str, device):
+    """Rows of heads [tokens, heads, dim]: the row stride in elements."""
+    _need(x.dim() == 3 and x.dtype == torch.bfloat16 and x.device == device, f"{what}: bf16 [tokens, heads, dim] on the "
+          "call's GPU")
+    tokens, heads, dim = x.shape
+    row, head, one = x.stride()
+    _need((one == 1 or dim == 1) and (head == dim or heads == 1), f"{what}: the heads of a token have to be contiguous")
+    return row if tokens > 1 else max(row, heads * dim)
+
+
+def _index(x: torch.Tensor, n: int, dtype, what: str, device):
+    _need(x.dtype == dtype and x.shape == (n,) and (n == 1 or x.is_contiguous()) and x.device == device,
+          f"{what}: contiguous {dtype} [{n}] on the call's GPU")
+    return x.data_ptr()
 
 
 class Library:
@@ -373,6 +466,106 @@ class Library:
             x.data_ptr(), m, top_k, probs.data_ptr(), offsets.data_ptr(), pairs.data_ptr(), ctypes.byref(cg),
             ctypes.byref(cd), sg, sd, out.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)))
         return out
+
+    # -------------------------------------------------------------- attention side
+    def rope_frequencies(self, rot_dim: int, theta: float = 10000.0, factor: float = 1.0, trained_context: float = 0.0,
+                         slow: float = 1.0, fast: float = 32.0, device=None) -> torch.Tensor:
+        """Radians a position for each rotated pair, fp64 [rot_dim / 2] (on `device`, if given).  factor > 1 stretches
+        them: all of them (trained_context 0), or those that make fewer than `fast` turns over the trained context,
+        wholly below `slow` turns."""
+        out = torch.empty((max(0, rot_dim) // 2,), dtype=torch.float64)
+        self._check("rope_frequencies", self.lib.rope_frequencies(rot_dim, theta, factor, trained_context, slow, fast,
+                                                                  out.data_ptr() or None))
+        return out if device is None else out.to(device)
+
+    def rope_apply(self, x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, interleaved: bool = False,
+                   amplitude: float = 1.0, inverse: bool = False, out: torch.Tensor = None, stream=None) -> torch.Tensor:
+        """Rotary positions on the first 2 * len(inv_freq) values of every head of x [tokens, heads, dim]; out may be x.
+        inverse rotates back, which is the gradient's way through the rotation."""
+        dev = x.device
+        stride = _rows(x, "x", dev)
+        tokens, heads, dim = x.shape
+        if out is None:
+            out = torch.empty((tokens, heads, dim), dtype=torch.bfloat16, device=dev)
+        _need(out.shape == x.shape, "out: the shape of x")
+        freq = _index(inv_freq, inv_freq.shape[0], torch.float64, "inv_freq", dev)
+        self._check("rope_apply", self.lib.rope_apply(
+            x.data_ptr(), stride, tokens, heads, dim, _index(positions, tokens, torch.int32, "positions", dev), freq,
+            2 * inv_freq.shape[0], amplitude,
+            (NVFP4_ROPE_INTERLEAVED if interleaved else 0) | (NVFP4_ROPE_INVERSE if inverse else 0), out.data_ptr(),
+            _rows(out, "out", dev), _stream(stream)))
+        return out
+
+    def kv_append(self, cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
+                  positions: torch.Tensor = None, inv_freq: torch.Tensor = None, interleaved: bool = False,
+                  amplitude: float = 1.0, q: torch.Tensor = None, q_out: torch.Tensor = None, stream=None):
+        """Write k (rotated, if inv_freq is given) and v [tokens, n_kv_heads, dim] to slots int64 [tokens] of the cache
+        (negative: skipped) and return the rotated q (None without q); q_out may be q."""
+        dev = cache.device
+        tokens, heads, dim = k.shape
+        _need(k.shape == v.shape and heads == cache.n_kv_heads and dim == cache.head_dim,
+              "k and v: [tokens, n_kv_heads, head_dim] of the cache")
+        pos = freq = None
+        rot = 0
+        if inv_freq is not None:
+            _need(positions is not None, "positions are needed with inv_freq")
+            rot = 2 * inv_freq.shape[0]
+            freq = _index(inv_freq, inv_freq.shape[0], torch.float64, "inv_freq", dev)
+            pos = _index(positions, tokens, torch.int32, "positions", dev)
+        q_heads = q_stride = q_out_stride = 0
+        if q is not None:
+            q_heads = q.shape[1]
+            _need(q.shape == (tokens, q_heads, dim), "q: [tokens, heads, head_dim] of the cache")
+            q_stride = _rows(q, "q", dev)
+            if q_out is None:
+                q_out = torch.empty((tokens, q_heads, dim), dtype=torch.bfloat16, device=dev)
+            _need(q_out.shape == q.shape, "q_out: the shape of q")
+            q_out_stride = _rows(q_out, "q_out", dev)
+        self._check("kv_append", self.lib.kv_append(
+            cache.ref, k.data_ptr(), _rows(k, "k", dev), v.data_ptr(), _rows(v, "v", dev), tokens,
+            _index(slots, tokens, torch.int64, "slots", dev), pos, freq, rot, amplitude,
+            NVFP4_ROPE_INTERLEAVED if interleaved else 0, _ptr(q), q_stride, q_heads, _ptr(q_out), q_out_stride,
+            _stream(stream)))
+        return q_out
+
+    def paged_attention(self, q: torch.Tensor, cache: KVCache, batch: Batch, scale: float = None, softcap: float = 0.0,
+                        window: int = 0, out: torch.Tensor = None, lse: torch.Tensor = None, with_lse: bool = False,
+                        stream=None):
+        """Attention of the batch's new tokens q [tokens, heads, dim] over their sequences' cached keys (scale: 1 /
+        sqrt(dim)): out, or (out, log-sum-exp fp32 [tokens, heads]) with with_lse."""
+        dev = cache.device
+        stride = _rows(q, "q", dev)
+        tokens, heads, dim = q.shape
+        _need(dim == cache.head_dim and batch.device == dev, "q: [tokens, heads, head_dim] of the cache; the batch on its "
+              "GPU")
+        if out is None:
+            out = torch.empty((tokens, heads, dim), dtype=torch.bfloat16, device=dev)
+        _need(out.shape == q.shape, "out: the shape of q")
+        if with_lse and lse is None:
+            lse = torch.empty((tokens, heads), dtype=torch.float32, device=dev)
+        _need(lse is None or (lse.shape == (tokens, heads) and lse.dtype == torch.float32 and lse.is_contiguous()
+                              and lse.device == dev), "lse: contiguous fp32 [tokens, heads]")
+        s = torch.cuda.current_stream() if stream is None else stream
+        nbytes = self.lib.paged_attention_workspace_bytes(tokens, batch.c.n_seqs, batch.max_new, heads,
+                                                          cache.n_kv_heads, dim)
+        ws = self._stream_workspace("attention", max(nbytes, 16), dev, s)
+        self._check("paged_attention", self.lib.paged_attention(
+            cache.ref, batch.ref, q.data_ptr(), stride, tokens, heads, dim ** -0.5 if scale is None else scale, softcap,
+            window, out.data_ptr(), _rows(out, "out", dev), _ptr(lse), ws.data_ptr(), ws.numel(), s.cuda_stream))
+        return (out, lse) if with_lse else out
+
+    def _stream_workspace(self, key, nbytes: int, device, stream) -> torch.Tensor:
+        """A workspace of its own for each (call kind, device, stream): calls on different streams may overlap.  It is
+        allocated on the stream that uses it, so that one that is outgrown is not reused under a running call.  A
+        captured call gets one from its graph's pool, which lives and dies with the graph."""
+        with torch.cuda.stream(stream):
+            if torch.cuda.is_current_stream_capturing():
+                return torch.empty(nbytes, dtype=torch.uint8, device=device)
+            k = (key, device, stream.cuda_stream)
+            cur = self._ws.get(k)
+            if cur is None or cur.numel() < nbytes:
+                cur = self._ws[k] = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return cur
 
     # -------------------------------------------------------------- call plans
     # Zero-argument callables with every ctypes argument built once, for timed

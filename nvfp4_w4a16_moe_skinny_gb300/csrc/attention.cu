@@ -1,0 +1,97 @@
+// paged_attention: argument checks, tensor maps of the cache, dispatch.
+#include <algorithm>
+#include <cmath>
+
+#include "attention.cuh"
+
+namespace nvfp4 {
+namespace {
+
+// Tensor map of one pool: [num_pages, n_kv_heads, page_size, head_dim] in boxes of one
+// head's `box_rows` consecutive keys by 128 bytes (or the whole row, if shorter),
+// swizzled so that eight rows of a 16-byte column fall into eight banks groups.
+bool encode_pool_map(CUtensorMap* map, const nvfp4_kv_cache* c, void* base, int box_rows) {
+  const EncodeTiledFn fn = encode_tiled();
+  if (!fn) return false;
+  const bool fp8 = c->dtype == NVFP4_KV_E4M3;
+  const cuuint64_t el = fp8 ? 1 : 2;
+  const int row = std::min<int>(128, c->head_dim * static_cast<int>(el));
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c->head_dim), static_cast<cuuint64_t>(c->page_size),
+                              static_cast<cuuint64_t>(c->n_kv_heads), static_cast<cuuint64_t>(c->num_pages)};
+  const cuuint64_t strides[3] = {c->head_dim * el, static_cast<cuuint64_t>(c->page_size) * c->head_dim * el,
+                                 static_cast<cuuint64_t>(c->page_stride) * el};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(row / el), static_cast<cuuint32_t>(box_rows), 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            row == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool sizes_ok(int n_tokens, int n_seqs, int max_new, int n_heads, int n_kv_heads, int head_dim) {
+  if (n_tokens < 0 || n_seqs < 0 || max_new < 0 || n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads) return false;
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return false;
+  // packed rows of a sequence are counted in 32 bits
+  return static_cast<int64_t>(n_tokens) * (n_heads / n_kv_heads) < (int64_t{1} << 31);
+}
+
+int64_t packed_rows(int n_tokens, int max_new, int n_heads, int n_kv_heads) {
+  return static_cast<int64_t>(std::min(n_tokens, max_new)) * (n_heads / n_kv_heads);
+}
+
+}  // namespace
+}  // namespace nvfp4
+
+using namespace nvfp4;
+
+extern "C" {
+
+size_t paged_attention_workspace_bytes(int32_t n_tokens, int32_t n_seqs, int32_t max_new, int32_t n_heads,
+                                       int32_t n_kv_heads, int32_t head_dim) {
+  if (!sizes_ok(n_tokens, n_seqs, max_new, n_heads, n_kv_heads, head_dim)) return 0;
+  const AttnShape s = attn_shape(head_dim, static_cast<int>(packed_rows(n_tokens, max_new, n_heads, n_kv_heads)));
+  return static_cast<size_t>(2) * kAttnGrid * s.tile_rows * (head_dim + 2) * sizeof(float);
+}
+
+nvfp4_status paged_attention(const nvfp4_kv_cache* cache, const nvfp4_batch* batch, const uint16_t* q,
+                             int64_t q_stride, int32_t n_tokens, int32_t n_heads, float scale, float softcap,
+                             int32_t window, uint16_t* out, int64_t out_stride, float* lse, void* ws, size_t ws_bytes,
+                             cudaStream_t stream) {
+  if (const nvfp4_status st = check_cache(cache)) return st;
+  if (!batch || !q || !out || !batch->cu_tokens || !batch->kv_len || !batch->page_table) return NVFP4_ERR_NULL;
+  const int kv = cache->n_kv_heads, dim = cache->head_dim;
+  if (!sizes_ok(n_tokens, batch->n_seqs, batch->max_new, n_heads, kv, dim) || batch->max_pages < 1)
+    return NVFP4_ERR_SHAPE;
+  // key positions are counted in 32 bits
+  if (static_cast<int64_t>(batch->max_pages) * cache->page_size >= (int64_t{1} << 30)) return NVFP4_ERR_SHAPE;
+  if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.f || window < 0) return NVFP4_ERR_SHAPE;
+  if (const nvfp4_status st = check_rows(q, q_stride, n_heads, dim)) return st;
+  if (const nvfp4_status st = check_rows(out, out_stride, n_heads, dim)) return st;
+  if (!aligned(batch->cu_tokens, 4) || !aligned(batch->kv_len, 4) || !aligned(batch->page_table, 4) ||
+      !aligned(lse, 4) || !aligned(ws, 16))
+    return NVFP4_ERR_ALIGN;
+  if (!ws || ws_bytes < paged_attention_workspace_bytes(n_tokens, batch->n_seqs, batch->max_new, n_heads, kv, dim))
+    return NVFP4_ERR_WORKSPACE;
+  if (n_tokens == 0 || batch->n_seqs == 0 || batch->max_new == 0) return NVFP4_OK;
+
+  AttnJob p{};
+  p.cu = batch->cu_tokens, p.kv_len = batch->kv_len, p.table = batch->page_table;
+  p.n_seqs = batch->n_seqs, p.max_pages = batch->max_pages, p.n_tokens = n_tokens;
+  p.n_heads = n_heads, p.n_kv = kv, p.group = n_heads / kv;
+  p.page_log2 = log2i(cache->page_size), p.num_pages = cache->num_pages;
+  p.q = q, p.q_stride = q_stride, p.out = out, p.out_stride = out_stride, p.lse = lse;
+  p.k_scale = cache->k_scale, p.v_scale = cache->v_scale;
+  p.scale = scale, p.softcap = softcap, p.window = window;
+  p.part = static_cast<float*>(ws);
+  const bool fp8 = cache->dtype == NVFP4_KV_E4M3;
+  const AttnShape s = attn_shape(dim, static_cast<int>(packed_rows(n_tokens, batch->max_new, n_heads, kv)));
+  KvMaps maps;
+  const int box = std::min(cache->page_size, attn_slice(dim, fp8, s.kw));
+  if (!encode_pool_map(&maps.k, cache, cache->k, box) || !encode_pool_map(&maps.v, cache, cache->v, box))
+    return NVFP4_ERR_CUDA;
+  if (dim == 64) return dispatch_attention<64>(p, maps, fp8, s, stream);
+  if (dim == 128) return dispatch_attention<128>(p, maps, fp8, s, stream);
+  return dispatch_attention<256>(p, maps, fp8, s, stream);
+}
+
+}  // extern "C"

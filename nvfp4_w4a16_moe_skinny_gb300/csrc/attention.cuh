@@ -1,0 +1,835 @@
+// Attention over a paged cache, few rows at a time: decode steps, verify blocks
+// and short chunks (paged_attention).
+//
+// Rows.  The heads of one kv head and the new tokens of one sequence are packed
+// into rows r = token * group + head, so the keys and values of a kv head are
+// read once for all of them; a row tile is 16 * RW of these rows.
+//
+// Split.  An item is (sequence, row tile, kv head); its keys are cut into units
+// of kKeys keys.  All units, numbered item by item, are dealt to the
+// grid in equal contiguous ranges, one CTA per SM, so ragged lengths balance by
+// themselves and a single long sequence fills the chip.  Every CTA finds its
+// range from kv_len and cu_tokens by itself (a block-wide scan), so one launch
+// geometry serves a captured graph at any lengths.  An item that lies in one range is
+// finished in registers; otherwise its pieces (unnormalised sums with their row
+// maximum and sum of weights, fp32) go to the workspace, at most two per CTA, and
+// a second grid joins them in range order: the result does not depend on timing.
+//
+// Inner loop.  One producer warp copies K and V tiles by TMA (swizzled boxes of a
+// page's rows; a page id outside the pool is an out-of-range coordinate, which
+// reads as zeros and touches no memory) into a ring of stages; the
+// consumer warps run m16n8k16 MMAs.  RW warps share a key slice and split the rows,
+// KW key slices share the rows: a decode step (one row tile of 16) uses eight
+// warps on eight key slices, each with its own running maximum and sum, joined
+// through shared memory once per piece; no barrier stops the loop between tiles.
+//
+// Numbers.  bf16 caches: bf16 products, fp32 sums, weights rounded to bf16 (half a
+// step of 2^-8, as the result itself).  E4M3 caches: codes convert to f16 exactly;
+// q is scaled by a power of two per row into f16's range (exact down to 2^-31
+// of the row's largest value) and weights are scaled by 2^15 before their rounding to f16 (2^-11).
+#pragma once
+
+#include "launch.cuh"
+#include "paged.cuh"
+
+namespace nvfp4 {
+
+constexpr int kAttnGrid = 152;  // CTAs of the split; fixed, so that workspace sizes are host-computable
+
+struct AttnJob {
+  const int32_t* cu;
+  const int32_t* kv_len;
+  const int32_t* table;
+  int n_seqs, max_pages, n_tokens;
+  int n_heads, n_kv, group;
+  int page_log2, num_pages;
+  const uint16_t* q;
+  int64_t q_stride;
+  uint16_t* out;
+  int64_t out_stride;
+  float* lse;
+  const float* k_scale;
+  const float* v_scale;
+  float scale, softcap;
+  int window;
+  float* part;  // [2 * grid][rows][dim] unnormalised sums, then [2 * grid][rows][2] (reference maximum, sum)
+};
+
+struct KvMaps {
+  CUtensorMap k, v;
+};
+
+// ------------------------------------------------------------------ work decomposition
+
+// A row tile of one sequence: positions of its first and last token and the keys
+// that any of its rows sees, [lo, hi).
+struct RowTile {
+  int row0, rows;  // first packed row and number of rows
+  int lo, hi;
+  int tile0, units;  // first key tile, number of units (at least one, so that empty rows are written)
+};
+
+struct Sequence {
+  int tok0, n, len, rows, tiles;
+};
+
+__device__ __forceinline__ Sequence sequence_of(const AttnJob& p, int b, int tile_rows) {
+  Sequence s;
+  const int a = min(max(__ldg(p.cu + b), 0), p.n_tokens), e = min(max(__ldg(p.cu + b + 1), a), p.n_tokens);
+  const int64_t most = static_cast<int64_t>(p.max_pages) << p.page_log2;
+  s.tok0 = a;
+  s.n = e - a;
+  s.len = static_cast<int>(min(static_cast<int64_t>(max(__ldg(p.kv_len + b), 0)), most));
+  s.rows = s.n * p.group;
+  s.tiles = (s.rows + tile_rows - 1) / tile_rows;
+  return s;
+}
+
+__device__ __forceinline__ RowTile row_tile(const AttnJob& p, const Sequence& s, int rt, int tile_rows, int keys) {
+  RowTile t;
+  t.row0 = rt * tile_rows;
+  t.rows = min(tile_rows, s.rows - t.row0);
+  const int p0 = s.len - s.n + t.row0 / p.group;
+  const int p1 = s.len - s.n + (t.row0 + t.rows - 1) / p.group;
+  t.hi = min(max(p1 + 1, 0), s.len);
+  t.lo = p.window > 0 ? min(max(p0 - p.window + 1, 0), t.hi) : 0;
+  t.tile0 = t.lo / keys;
+  t.units = max(1, (t.hi + keys - 1) / keys - t.tile0);
+  return t;
+}
+
+__device__ __forceinline__ long long sequence_units(const AttnJob& p, const Sequence& s, int tile_rows, int keys) {
+  long long u = 0;
+  for (int rt = 0; rt < s.tiles; ++rt) u += row_tile(p, s, rt, tile_rows, keys).units;
+  return u * p.n_kv;
+}
+
+// Block-wide search over the sequences' units: the total, and the sequence that
+// holds unit `u` with the number of units before it (u < 0: the total only).
+// Every thread of the block calls it; scratch: 34 words of shared memory.
+struct Found {
+  int seq;
+  long long before;
+};
+
+template <int kThreadsInBlock>
+__device__ __forceinline__ long long scan_units(const AttnJob& p, int tile_rows, int keys, long long u, Found* found,
+                                                long long* scratch) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int kNW = kThreadsInBlock / 32;
+  long long base = 0;
+  for (int b0 = 0; b0 < p.n_seqs; b0 += kThreadsInBlock) {
+    const int b = b0 + threadIdx.x;
+    const long long mine = b < p.n_seqs ? sequence_units(p, sequence_of(p, b, tile_rows), tile_rows, keys) : 0;
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) scratch[warp] = incl;
+    __syncthreads();
+    long long pre = base, all = 0;
+#pragma unroll
+    for (int w = 0; w < kNW; ++w) {
+      if (w < warp) pre += scratch[w];
+      all += scratch[w];
+    }
+    if (u >= 0 && mine > 0 && u >= pre + incl - mine && u < pre + incl) {
+      scratch[32] = b;
+      scratch[33] = pre + incl - mine;
+    }
+    base += all;
+    __syncthreads();
+  }
+  if (u >= 0) {
+    found->seq = static_cast<int>(scratch[32]);
+    found->before = scratch[33];
+  }
+  __syncthreads();
+  return base;
+}
+
+// The pieces of one CTA, in order: consecutive shares of items.  All roles of a
+// CTA walk the same list.
+struct Walk {
+  int b, rt, h;
+  long long item0;  // first unit of the item
+  Sequence s;
+  RowTile t;
+};
+
+__device__ __forceinline__ void walk_seq(const AttnJob& p, Walk& w, int tile_rows, int keys) {
+  w.s = sequence_of(p, w.b, tile_rows);
+  w.rt = 0, w.h = 0;
+  if (w.s.tiles > 0) w.t = row_tile(p, w.s, 0, tile_rows, keys);
+}
+
+// The item that holds unit u, searched from the first item of w.b at w.item0.
+__device__ __forceinline__ void walk_to(const AttnJob& p, Walk& w, long long u, int tile_rows, int keys) {
+  while (true) {
+    if (w.rt < w.s.tiles) {
+      const long long all = static_cast<long long>(w.t.units) * (p.n_kv - w.h);
+      if (u < w.item0 + all) {
+        const int k = static_cast<int>((u - w.item0) / w.t.units);
+        w.h += k;
+        w.item0 += static_cast<long long>(k) * w.t.units;
+        return;
+      }
+      w.item0 += all;
+      w.h = 0;
+      ++w.rt;
+      if (w.rt < w.s.tiles) w.t = row_tile(p, w.s, w.rt, tile_rows, keys);
+    } else {
+      if (++w.b >= p.n_seqs) return;  // not reached for a unit below the total
+      walk_seq(p, w, tile_rows, keys);
+    }
+  }
+}
+
+__device__ __forceinline__ long long range_start(int c, long long total, int grid) { return c * total / grid; }
+
+// ------------------------------------------------------------------ MMA helpers
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <bool kF16>
+__device__ __forceinline__ void mma_16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (kF16)
+    mma_f16(c, a, b0, b1);
+  else
+    mma_bf16(c, a, b0, b1);
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+// Two E4M3 codes (low, high half of w) -> f16x2, exact.
+__device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ void tma_load_4d_plain(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
+                                                  uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+      : "memory");
+}
+
+// Halves of packed 16-bit values that are infinite or NaN, as a mask of 0xffff.
+template <bool kF16>
+__device__ __forceinline__ uint32_t nonfinite_mask(uint32_t v) {
+  constexpr uint32_t e = kF16 ? 0x7c007c00u : 0x7f807f80u, one = kF16 ? 0x04000400u : 0x00800080u;
+  const uint32_t m = ((v & e) + one) & 0x80008000u;  // the exponent is all ones: the carry reaches the sign bit
+  return (m >> 15) * 0xffffu;
+}
+
+// ------------------------------------------------------------------ tile geometry
+
+// Keys of one warp's step (the rows of a TMA box are min(page, slice)): as many as keep
+// a stage of the ring at 64 KB or less and the scores in few registers.
+__host__ __device__ constexpr int attn_slice(int dim, bool fp8, int kw) {
+  if (kw == 1) return dim == 256 ? 32 : 64;
+  return dim == 256 || (dim == 128 && !fp8 && kw == 8) ? 16 : 32;
+}
+
+template <int kDim, bool kFp8, int kRW, int kKW>
+struct AttnTile {
+  static constexpr int kRows = 16 * kRW;
+  static constexpr int kSlice = attn_slice(kDim, kFp8, kKW);                           // keys of a warp's step
+  static constexpr int kKeys = kSlice * kKW;                                           // keys of a unit
+  static constexpr int kConsumers = kRW * kKW;
+  static constexpr int kThreadsAll = (kConsumers + 1) * 32;
+  static constexpr int kEl = kFp8 ? 1 : 2;
+  static constexpr int kRowB = kDim * kEl < 128 ? kDim * kEl : 128;  // bytes of a row of a box
+  static constexpr int kSub = kDim * kEl / kRowB;                    // boxes across a head
+  static constexpr uint32_t kSwz = kRowB == 128 ? 0x70 : 0x30;
+  static constexpr int kSubB = kSlice * kRowB;          // one box column of a slice
+  static constexpr int kSliceB = kSubB * kSub;          // K or V of a slice
+  static constexpr int kStageB = 2 * kSliceB * kKW;     // a unit's K and V
+  static constexpr int kJoinW = kKW > 4 ? 2 : kKW / 2;  // key slices that one round of the join hands over
+  static constexpr int kJoinB = kJoinW * kRW * 32 * (kDim / 2 + 4) * 4;
+  static constexpr int kFit = (227 * 1024 - 1024 - 1024 - kJoinB) / kStageB;
+  static constexpr int kStages = kFit > 6 ? 6 : kFit;
+  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageB + kJoinB + 1024;
+  static_assert(kStages >= 2, "ring too shallow");
+};
+
+// Byte offset of 16-byte chunk c of key row r in a slice (swizzled as the boxes are).
+template <typename T>
+__device__ __forceinline__ uint32_t tile_offset(int r, int c) {
+  constexpr int per = T::kRowB / 16;
+  const uint32_t o = (c / per) * T::kSubB + r * T::kRowB + (c % per) * 16;
+  return o ^ ((o >> 3) & T::kSwz);
+}
+
+// ------------------------------------------------------------------ the split kernel
+
+template <int kDim, bool kFp8, int kRW, int kKW>
+__global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, 1)
+    attn_split_kernel(const AttnJob p, const __grid_constant__ KvMaps maps) {
+  using T = AttnTile<kDim, kFp8, kRW, kKW>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t ring = (raw + 1023u) & ~1023u;
+  const uint32_t join = ring + T::kStages * T::kStageB;
+  uint8_t* tail = smem_raw + (join + T::kJoinB - raw);
+  uint64_t* full = reinterpret_cast<uint64_t*>(tail);          // [stages][kKW]
+  uint64_t* empty = full + T::kStages * kKW;                   // [stages][kKW]
+  long long* scratch = reinterpret_cast<long long*>(empty + T::kStages * kKW);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < T::kStages * kKW; ++i) mbar_init(full + i, 1), mbar_init(empty + i, kRW);
+    fence_mbar_init();
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  __syncthreads();
+
+  Found f;
+  const long long total = scan_units<T::kThreadsAll>(p, T::kRows, T::kKeys, -1, &f, scratch);
+  const int grid = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
+  if (static_cast<int>(blockIdx.x) >= grid) return;
+  const long long u0 = range_start(blockIdx.x, total, grid), u1 = range_start(blockIdx.x + 1, total, grid);
+  scan_units<T::kThreadsAll>(p, T::kRows, T::kKeys, u0, &f, scratch);
+  Walk w;
+  w.b = f.seq, w.item0 = f.before;
+  walk_seq(p, w, T::kRows, T::kKeys);
+
+  uint32_t step = 0;  // ring position, the same in every warp
+  bool ran_out = false;  // a wait reached its limit (recorded): no further waits, the roles stay in step
+  if (warp == T::kConsumers) {
+    // -------------------------------------------------------------- producer
+    const int box_rows = min(1 << p.page_log2, T::kSlice);
+    const int boxes = T::kSlice / box_rows;              // page pieces of a slice
+    const int copies = boxes * T::kSub * 2;              // TMA copies of a slice
+    for (long long u = u0; u < u1;) {
+      walk_to(p, w, u, T::kRows, T::kKeys);
+      const int first = w.t.tile0 + static_cast<int>(u - w.item0);
+      const int n = static_cast<int>(min(w.item0 + w.t.units - u, u1 - u));
+      const int32_t* table = p.table + static_cast<int64_t>(w.b) * p.max_pages;
+      for (int i = 0; i < n; ++i, ++step) {
+        const int st = step % T::kStages;
+        const uint32_t round = step / T::kStages;
+        const int key0 = (first + i) * T::kKeys;
+        for (int slice = 0; slice < kKW; ++slice) {
+          const int bar = st * kKW + slice;
+          if (round > 0 && !mbar_wait_warp(empty + bar, (round - 1) & 1)) return;
+          const int slice0 = key0 + slice * T::kSlice;
+          if (lane == 0) {  // the bytes to come: the page pieces that hold a key of [lo, hi)
+            int pieces = 0;
+            for (int j = 0; j < boxes; ++j) {
+              const int k = slice0 + j * box_rows;
+              pieces += k < w.t.hi && k + box_rows > w.t.lo;
+            }
+            mbar_arrive_expect_tx(full + bar, pieces * box_rows * T::kRowB * T::kSub * 2);
+          }
+          __syncwarp();
+          for (int c = lane; c < copies; c += 32) {
+            const int which = c & 1, sub = (c >> 1) % T::kSub, j = (c >> 1) / T::kSub;
+            const int k = slice0 + j * box_rows;
+            if (k >= w.t.hi || k + box_rows <= w.t.lo) continue;
+            int page = __ldg(table + (k >> p.page_log2));
+            if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.num_pages)) {
+              page = p.num_pages;
+              atomicOr(&g_device_error, kErrPage);
+            }
+            const uint32_t dst = ring + st * T::kStageB + slice * 2 * T::kSliceB + which * T::kSliceB +
+                                 sub * T::kSubB + j * box_rows * T::kRowB;
+            tma_load_4d_plain(dst, which ? &maps.v : &maps.k, sub * (T::kRowB / T::kEl),
+                              k & ((1 << p.page_log2) - 1), w.h, page, smem_addr(full + bar));
+          }
+        }
+      }
+      u += n;
+    }
+    return;
+  }
+
+  // ---------------------------------------------------------------- consumers
+  const int rw = warp % kRW, kw = warp / kRW;
+  const int g = lane >> 2, t4 = lane & 3;
+  constexpr int kNT = T::kSlice / 8;      // key columns of 8
+  constexpr int kDT = kDim / 8;           // value columns of 8
+  constexpr int kKS = kDim / 16;          // k steps of the first product
+  const float log2e = 1.4426950408889634f;
+  // ldmatrix addresses: lane l gives row l % 8 of matrix l / 8
+  const int lrow = lane & 7, lmat = lane >> 3;
+
+  for (long long u = u0; u < u1;) {
+    walk_to(p, w, u, T::kRows, T::kKeys);
+    const int first = w.t.tile0 + static_cast<int>(u - w.item0);
+    const int n = static_cast<int>(min(w.item0 + w.t.units - u, u1 - u));
+
+    // this thread's two rows (g and g + 8 of the warp's 16): token, head, position
+    int pos[2], tok[2], head[2];
+    bool live[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = rw * 16 + g + 8 * i;
+      live[i] = r < w.t.rows;
+      const int rr = w.t.row0 + min(r, w.t.rows - 1);
+      tok[i] = rr / p.group;
+      head[i] = w.h * p.group + rr - tok[i] * p.group;
+      pos[i] = w.s.len - w.s.n + tok[i];
+    }
+    // positions over the warp's rows: the smallest and largest
+    const int r_lo = w.t.row0 + min(rw * 16, w.t.rows - 1), r_hi = w.t.row0 + min(rw * 16 + 15, w.t.rows - 1);
+    const int pos_lo = w.s.len - w.s.n + r_lo / p.group, pos_hi = w.s.len - w.s.n + r_hi / p.group;
+    const int all_hi = min(pos_lo + 1, w.s.len);                                  // keys [all_lo, all_hi) seen by every row
+    const int all_lo = p.window > 0 ? pos_hi - p.window + 1 : 0;
+    const int any_hi = min(pos_hi + 1, w.s.len);                                  // keys [any_lo, any_hi) seen by some row
+    const int any_lo = p.window > 0 ? max(pos_lo - p.window + 1, 0) : 0;
+
+    // q as A fragments
+    uint32_t qf[kKS][4];
+    float qscale[2] = {1.f, 1.f};
+    {
+      const uint16_t* q0 = p.q + (w.s.tok0 + tok[0]) * p.q_stride + static_cast<int64_t>(head[0]) * kDim;
+      const uint16_t* q1 = p.q + (w.s.tok0 + tok[1]) * p.q_stride + static_cast<int64_t>(head[1]) * kDim;
+      if constexpr (!kFp8) {
+#pragma unroll
+        for (int k = 0; k < kKS; ++k) {
+          qf[k][0] = live[0] ? *reinterpret_cast<const uint32_t*>(q0 + 16 * k + 2 * t4) : 0u;
+          qf[k][1] = live[1] ? *reinterpret_cast<const uint32_t*>(q1 + 16 * k + 2 * t4) : 0u;
+          qf[k][2] = live[0] ? *reinterpret_cast<const uint32_t*>(q0 + 16 * k + 2 * t4 + 8) : 0u;
+          qf[k][3] = live[1] ? *reinterpret_cast<const uint32_t*>(q1 + 16 * k + 2 * t4 + 8) : 0u;
+        }
+      } else {
+        // four adjacent values per lane and k step, in the order the codes of a key
+        // come out of ldmatrix
+        float amax[2] = {0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < kKS; ++k) {
+          const uint2 a = live[0] ? *reinterpret_cast<const uint2*>(q0 + 16 * k + 4 * t4) : make_uint2(0, 0);
+          const uint2 b = live[1] ? *reinterpret_cast<const uint2*>(q1 + 16 * k + 4 * t4) : make_uint2(0, 0);
+          qf[k][0] = a.x, qf[k][2] = a.y, qf[k][1] = b.x, qf[k][3] = b.y;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            amax[j & 1] = fmaxf(amax[j & 1], fabsf(__uint_as_float(qf[k][j] << 16)));
+            amax[j & 1] = fmaxf(amax[j & 1], fabsf(__uint_as_float(qf[k][j] & 0xffff0000u)));
+          }
+        }
+        float up[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          amax[i] = fmaxf(amax[i], __shfl_xor_sync(0xffffffffu, amax[i], 1));
+          amax[i] = fmaxf(amax[i], __shfl_xor_sync(0xffffffffu, amax[i], 2));
+          const int e = pow2_rescale_exponent(amax[i]);
+          up[i] = exp2i(e);
+          qscale[i] = exp2i(-e);
+        }
+#pragma unroll
+        for (int k = 0; k < kKS; ++k)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            qf[k][j] = f32x2_to_f16x2(__uint_as_float(qf[k][j] << 16) * up[j & 1],
+                                      __uint_as_float(qf[k][j] & 0xffff0000u) * up[j & 1]);
+      }
+    }
+    const float ks = (kFp8 && p.k_scale) ? __ldg(p.k_scale + w.h) : 1.0f;
+    // logits in units of log 2: acc * mul; with a softcap, cap2 * tanh(acc * mul)
+    const bool capped = p.softcap > 0.f;
+    const float unit = p.scale * ks * (capped ? 1.0f / p.softcap : log2e);
+    const float mul[2] = {unit * qscale[0], unit * qscale[1]};
+    const float cap2 = p.softcap * log2e;
+
+    float acc[kDT][4];
+#pragma unroll
+    for (int j = 0; j < kDT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY};  // reference of the weights: weight = 2^(s - m)
+    float l[2] = {0.f, 0.f};              // this lane's share of the sum of weights
+
+    for (int i = 0; i < n; ++i, ++step) {
+      const int st = step % T::kStages;
+      ran_out = ran_out || !mbar_wait_warp(full + st * kKW + kw, (step / T::kStages) & 1);
+      const int key0 = (first + i) * T::kKeys + kw * T::kSlice;
+      if (key0 < any_hi && key0 + T::kSlice > any_lo) {
+        const uint32_t kt = ring + st * T::kStageB + kw * 2 * T::kSliceB, vt = kt + T::kSliceB;
+        const bool edge = key0 + T::kSlice > all_hi || key0 < all_lo;
+        // ---- s = q . k
+        float s[kNT][4];
+#pragma unroll
+        for (int j = 0; j < kNT; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+        if constexpr (!kFp8) {
+#pragma unroll
+          for (int k = 0; k < kKS; k += 2)
+#pragma unroll
+            for (int j = 0; j < kNT; ++j) {
+              uint32_t b[4];
+              ldsm4(b, kt + tile_offset<T>(8 * j + lrow, 2 * k + lmat));
+              mma_16<false>(s[j], qf[k], b[0], b[1]);
+              mma_16<false>(s[j], qf[k + 1], b[2], b[3]);
+            }
+        } else {
+#pragma unroll
+          for (int k = 0; k < kKS; k += 4)
+#pragma unroll
+            for (int j = 0; j < kNT; ++j) {
+              uint32_t b[4];
+              ldsm4(b, kt + tile_offset<T>(8 * j + lrow, k + lmat));
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                uint32_t b0, b1;
+                e4m3x4_to_f16x2(b[x], b0, b1);
+                mma_16<true>(s[j], qf[k + x], b0, b1);
+              }
+            }
+        }
+        // ---- logits, mask, running maximum
+        float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int j = 0; j < kNT; ++j)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            float v = s[j][x] * mul[x >> 1];
+            if (capped) v = cap2 * (1.0f - __fdividef(2.0f, exp2_approx(v * (2.0f * log2e)) + 1.0f));
+            if (edge) {
+              const int key = key0 + 8 * j + 2 * t4 + (x & 1);
+              const int ps = pos[x >> 1];
+              const bool sees = key <= ps && key < w.s.len && (p.window <= 0 || key > ps - p.window);
+              v = sees ? v : -INFINITY;
+            }
+            s[j][x] = v;
+            top[x >> 1] = fmaxf(top[x >> 1], v);
+          }
+        float alpha[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 1));
+          top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 2));
+          const float next = fmaxf(m[x], top[x] - (kFp8 ? 15.0f : 0.0f));
+          // a row that has seen nothing keeps -inf as its reference and 0 as its sum
+          alpha[x] = next == -INFINITY ? 1.0f : exp2_approx(m[x] - next);
+          m[x] = next;
+        }
+        const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+        if (__any_sync(0xffffffffu, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
+          l[0] *= alpha[0], l[1] *= alpha[1];
+#pragma unroll
+          for (int j = 0; j < kDT; ++j) {
+            acc[j][0] *= alpha[0], acc[j][1] *= alpha[0];
+            acc[j][2] *= alpha[1], acc[j][3] *= alpha[1];
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kNT; ++j)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            s[j][x] = exp2_approx(s[j][x] - ref[x >> 1]);
+            l[x >> 1] += s[j][x];
+          }
+        // ---- out += weights . v
+#pragma unroll
+        for (int k = 0; k < T::kSlice / 16; ++k) {
+          uint32_t a[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float lo = s[2 * k + (x >> 1)][2 * (x & 1)], hi = s[2 * k + (x >> 1)][2 * (x & 1) + 1];
+            a[x] = kFp8 ? f32x2_to_f16x2(lo, hi) : f32x2_to_bf16x2(lo, hi);
+          }
+          uint32_t keep[2] = {0xffffffffu, 0xffffffffu};  // value halves of keys that some row sees
+          uint32_t shown[4] = {0, 0, 0, 0};               // 1.0 where a row sees a key (edge tiles only)
+          if (edge) {
+            const uint32_t one = kFp8 ? 0x3c00u : 0x3f80u;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const int key = key0 + 16 * k + 8 * x + 2 * t4;
+              keep[x] = (key >= any_lo && key < any_hi ? 0xffffu : 0u) |
+                        (key + 1 >= any_lo && key + 1 < any_hi ? 0xffff0000u : 0u);
+#pragma unroll
+              for (int y = 0; y < 2; ++y)
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                  const int kk = key + z, ps = pos[y];
+                  if (kk <= ps && kk < w.s.len && (p.window <= 0 || kk > ps - p.window)) shown[2 * x + y] |= one << (16 * z);
+                }
+            }
+          }
+          [[maybe_unused]] uint32_t r[4];
+#pragma unroll
+          for (int c = 0; c < kDT / 2; ++c) {
+            // b: two columns of 8 values each, 16 keys (E4M3: one 16-value chunk)
+            uint32_t b[4];
+            if constexpr (!kFp8) {
+              ldsm4t(b, vt + tile_offset<T>(16 * k + (lane & 15), 2 * c + (lane >> 4)));
+            } else {
+              // matrices: (keys 0-7, chunk c), (keys 8-15, chunk c), then chunk c + 1; a word
+              // holds two keys of two adjacent values
+              static_assert(kDT % 4 == 0, "chunks come in pairs");
+              if (c % 2 == 0) ldsm4t(r, vt + tile_offset<T>(16 * k + (lane & 15), c + (lane >> 4)));
+              const uint32_t w0 = __byte_perm(r[c % 2 ? 2 : 0], 0, 0x3120), w1 = __byte_perm(r[c % 2 ? 3 : 1], 0, 0x3120);
+              e4m3x4_to_f16x2(w0, b[0], b[2]);
+              e4m3x4_to_f16x2(w1, b[1], b[3]);
+            }
+            if (edge) {
+              // keys outside every row's reach count as zeros; infinities and NaN of keys that
+              // only some rows see are taken out of the product (0 * inf is NaN) and added to
+              // the rows that see them: the product of the rows' 0/1 visibility with 0/1
+              // indicators of +inf, -inf and NaN says which
+              uint32_t bad[4];
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                b[x] &= keep[x & 1];
+                bad[x] = nonfinite_mask<kFp8>(b[x]);
+              }
+              if (__any_sync(0xffffffffu, (bad[0] | bad[1] | bad[2] | bad[3]) != 0)) {
+                const uint32_t one = kFp8 ? 0x3c003c00u : 0x3f803f80u, man = kFp8 ? 0x03ff03ffu : 0x007f007fu;
+#pragma unroll
+                for (int kind = 0; kind < 3; ++kind) {
+                  uint32_t ind[4];
+#pragma unroll
+                  for (int x = 0; x < 4; ++x) {
+                    const uint32_t frac = b[x] & man;
+                    const uint32_t nan = bad[x] & (((frac & 0xffffu) ? 0xffffu : 0u) | ((frac >> 16) ? 0xffff0000u : 0u));
+                    const uint32_t neg = ((b[x] >> 15) & 0x00010001u) * 0xffffu;
+                    const uint32_t sel = kind == 2 ? nan : bad[x] & ~nan & (kind == 1 ? neg : ~neg);
+                    ind[x] = one & sel;
+                  }
+                  float hit[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+                  mma_16<kFp8>(hit[0], shown, ind[0], ind[1]);
+                  mma_16<kFp8>(hit[1], shown, ind[2], ind[3]);
+                  const float add = kind == 0 ? INFINITY : (kind == 1 ? -INFINITY : __int_as_float(0x7fc00000));
+#pragma unroll
+                  for (int x = 0; x < 4; ++x) {
+                    if (hit[0][x] > 0.f) acc[2 * c][x] += add;
+                    if (hit[1][x] > 0.f) acc[2 * c + 1][x] += add;
+                  }
+                }
+#pragma unroll
+                for (int x = 0; x < 4; ++x) b[x] &= ~bad[x];
+              }
+            }
+            mma_16<kFp8>(acc[2 * c], a, b[0], b[1]);
+            mma_16<kFp8>(acc[2 * c + 1], a, b[2], b[3]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty + st * kKW + kw);
+    }
+
+    // ---- join the key slices of this CTA
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
+      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
+    }
+    if constexpr (kKW > 1) {
+      float* buf = reinterpret_cast<float*>(smem_raw + (join - raw));
+      int count = kKW;  // slices still to be joined: the last ones go to those before them
+#pragma unroll 1
+      while (count > 1) {
+        const int give = count / 2 < T::kJoinW ? count / 2 : T::kJoinW;
+        const int from = count - give, to = from - give;
+        asm volatile("bar.sync 1, %0;" ::"n"(T::kConsumers * 32) : "memory");
+        if (kw >= from && kw < count) {
+          float* o = buf + ((kw - from) * kRW + rw) * 32 * (kDim / 2 + 4) + lane;
+#pragma unroll
+          for (int j = 0; j < kDT; ++j)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) o[(4 * j + x) * 32] = acc[j][x];
+          o[(4 * kDT) * 32] = m[0], o[(4 * kDT + 1) * 32] = m[1];
+          o[(4 * kDT + 2) * 32] = l[0], o[(4 * kDT + 3) * 32] = l[1];
+        }
+        asm volatile("bar.sync 1, %0;" ::"n"(T::kConsumers * 32) : "memory");
+        if (kw >= to && kw < from) {
+          const float* o = buf + ((kw - to) * kRW + rw) * 32 * (kDim / 2 + 4) + lane;
+          float fa[2], fb[2];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float mo = o[(4 * kDT + x) * 32];
+            const float next = fmaxf(m[x], mo);
+            fa[x] = next == -INFINITY ? 1.0f : exp2_approx(m[x] - next);
+            fb[x] = next == -INFINITY ? 1.0f : exp2_approx(mo - next);
+            m[x] = next;
+            l[x] = l[x] * fa[x] + o[(4 * kDT + 2 + x) * 32] * fb[x];
+          }
+#pragma unroll
+          for (int j = 0; j < kDT; ++j)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) acc[j][x] = acc[j][x] * fa[x >> 1] + o[(4 * j + x) * 32] * fb[x >> 1];
+        }
+        count = from;
+      }
+    }
+    // ---- write: the finished rows, or this piece's share of them
+    if (kw == 0) {
+      const bool whole = n == w.t.units;
+      const int slot = 2 * blockIdx.x + (u == u0 ? 0 : 1);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (!live[x]) continue;
+        if (whole) {
+          const float vs = (kFp8 && p.v_scale) ? __ldg(p.v_scale + w.h) : 1.0f;
+          const float inv = l[x] == 0.f ? 0.f : vs / l[x];
+          const int64_t row = w.s.tok0 + tok[x];
+          uint16_t* o = p.out + row * p.out_stride + static_cast<int64_t>(head[x]) * kDim;
+#pragma unroll
+          for (int j = 0; j < kDT; j += 2) {
+            const float v0 = acc[j][2 * x] * inv, v1 = acc[j][2 * x + 1] * inv;
+            const float v2 = acc[j + 1][2 * x] * inv, v3 = acc[j + 1][2 * x + 1] * inv;
+            if constexpr (!kFp8) {
+              *reinterpret_cast<uint32_t*>(o + 8 * j + 2 * t4) = f32x2_to_bf16x2(v0, v1);
+              *reinterpret_cast<uint32_t*>(o + 8 * j + 8 + 2 * t4) = f32x2_to_bf16x2(v2, v3);
+            } else {
+              *reinterpret_cast<uint2*>(o + 8 * j + 4 * t4) =
+                  make_uint2(f32x2_to_bf16x2(v0, v2), f32x2_to_bf16x2(v1, v3));
+            }
+          }
+          if (p.lse && t4 == 0)
+            p.lse[row * p.n_heads + head[x]] = l[x] == 0.f ? -INFINITY : (m[x] + log2f(l[x])) * 0.6931471805599453f;
+        } else {
+          const int r = rw * 16 + g + 8 * x;
+          float* o = p.part + (static_cast<int64_t>(slot) * T::kRows + r) * kDim;
+#pragma unroll
+          for (int j = 0; j < kDT; j += 2) {
+            if constexpr (!kFp8) {
+              *reinterpret_cast<float2*>(o + 8 * j + 2 * t4) = make_float2(acc[j][2 * x], acc[j][2 * x + 1]);
+              *reinterpret_cast<float2*>(o + 8 * j + 8 + 2 * t4) = make_float2(acc[j + 1][2 * x], acc[j + 1][2 * x + 1]);
+            } else {
+              *reinterpret_cast<float4*>(o + 8 * j + 4 * t4) =
+                  make_float4(acc[j][2 * x], acc[j + 1][2 * x], acc[j][2 * x + 1], acc[j + 1][2 * x + 1]);
+            }
+          }
+          if (t4 == 0) {
+            float* ml = p.part + static_cast<int64_t>(2) * gridDim.x * T::kRows * kDim;
+            *reinterpret_cast<float2*>(ml + (static_cast<int64_t>(slot) * T::kRows + r) * 2) = make_float2(m[x], l[x]);
+          }
+        }
+      }
+    }
+    u += n;
+  }
+}
+
+// ------------------------------------------------------------------ the join
+
+constexpr int kJoinThreads = 128;
+
+// Block (c, y): if range boundary c is the first one inside an item, joins that
+// item's pieces for four of its rows (a warp a row), in range order.
+template <int kDim>
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnJob p, int split_grid, int tile_rows,
+                                                                 int keys) {
+  __shared__ long long scratch[34];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  Found f;
+  // lengths are complete before the split grid starts: only its pieces are waited for
+  const long long total = scan_units<kJoinThreads>(p, tile_rows, keys, -1, &f, scratch);
+  const int grid = static_cast<int>(min(static_cast<long long>(split_grid), total));
+  const int c = blockIdx.x + 1;
+  const long long u = c < grid ? range_start(c, total, grid) : 0;
+  if (c < grid) scan_units<kJoinThreads>(p, tile_rows, keys, u, &f, scratch);
+  pdl_launch_dependents();
+  pdl_wait();  // every block waits, so that this grid's end means that the split grid has ended
+  if (c >= grid) return;
+  Walk w;
+  w.b = f.seq, w.item0 = f.before;
+  walk_seq(p, w, tile_rows, keys);
+  walk_to(p, w, u, tile_rows, keys);
+  if (u == w.item0 || range_start(c - 1, total, grid) > w.item0) return;  // no split here, or not its first boundary
+  const int r = blockIdx.y * 4 + warp;
+  if (r >= w.t.rows) return;
+  // first and last range that hold a unit of the item
+  const int c0 = c - 1;
+  const int c1 = static_cast<int>(((w.item0 + w.t.units) * grid - 1) / total);
+  const float* ml = p.part + static_cast<int64_t>(2) * split_grid * tile_rows * kDim;
+  constexpr int kPer = kDim / 32;
+  float m = -INFINITY;
+  for (int i = c0 + lane; i <= c1; i += 32) {
+    const int slot = 2 * i + (i == c0 && w.item0 > range_start(i, total, grid) ? 1 : 0);
+    m = fmaxf(m, ml[(static_cast<int64_t>(slot) * tile_rows + r) * 2]);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float acc[kPer];
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) acc[j] = 0.f;
+  float l = 0.f;
+#pragma unroll 4
+  for (int i = c0; i <= c1; ++i) {
+    const int slot = 2 * i + (i == c0 && w.item0 > range_start(i, total, grid) ? 1 : 0);
+    const int64_t row = static_cast<int64_t>(slot) * tile_rows + r;
+    const float2 v = *reinterpret_cast<const float2*>(ml + row * 2);
+    const float a = m == -INFINITY ? 1.0f : exp2_approx(v.x - m);
+    l += a * v.y;
+    const float* o = p.part + row * kDim + lane * kPer;
+#pragma unroll
+    for (int j = 0; j < kPer; j += 2) {
+      const float2 x = *reinterpret_cast<const float2*>(o + j);
+      acc[j] += a * x.x, acc[j + 1] += a * x.y;
+    }
+  }
+  const int rr = w.t.row0 + r, tok = rr / p.group, head = w.h * p.group + rr - tok * p.group;
+  const int64_t row = w.s.tok0 + tok;
+  const float inv = l == 0.f ? 0.f : (p.v_scale ? __ldg(p.v_scale + w.h) : 1.0f) / l;
+  uint32_t* o = reinterpret_cast<uint32_t*>(p.out + row * p.out_stride + static_cast<int64_t>(head) * kDim) + lane * (kPer / 2);
+#pragma unroll
+  for (int j = 0; j < kPer; j += 2) o[j / 2] = f32x2_to_bf16x2(acc[j] * inv, acc[j + 1] * inv);
+  if (p.lse && lane == 0) p.lse[row * p.n_heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+// ------------------------------------------------------------------ launch
+
+// Warps over rows and key slices for a tile of up to `rows` packed rows: 16 rows leave
+// eight key slices to eight warps, 64 rows and more share one slice among four.
+struct AttnShape {
+  int rw, kw, tile_rows;
+};
+inline AttnShape attn_shape(int dim, int rows) {
+  if (rows <= 16) return {1, dim == 256 ? 4 : 8, 16};
+  if (rows <= 32) return {2, dim == 256 ? 2 : 4, 32};
+  return {4, 1, 64};
+}
+
+template <int kDim, bool kFp8, int kRW, int kKW>
+nvfp4_status launch_attn_split(const AttnJob& p, const KvMaps& maps, cudaStream_t stream) {
+  using T = AttnTile<kDim, kFp8, kRW, kKW>;
+  if (set_smem(attn_split_kernel<kDim, kFp8, kRW, kKW>, T::kSmem) != cudaSuccess) return NVFP4_ERR_CUDA;
+  if (launch_pdl(attn_split_kernel<kDim, kFp8, kRW, kKW>, dim3(kAttnGrid), dim3(T::kThreadsAll), T::kSmem, stream, p,
+                 maps) != cudaSuccess)
+    return NVFP4_ERR_CUDA;
+  // one unit an item: nothing can be split
+  const int64_t most = static_cast<int64_t>(p.max_pages) << p.page_log2;
+  if (most > T::kKeys) {
+    if (launch_pdl(attn_join_kernel<kDim>, dim3(kAttnGrid - 1, T::kRows / 4), dim3(kJoinThreads), 0, stream, p,
+                   kAttnGrid, T::kRows, T::kKeys) != cudaSuccess)
+      return NVFP4_ERR_CUDA;
+  }
+  return launched();
+}
+
+// The split and join grids for heads of kDim values (attention_d*.cu).
+template <int kDim>
+nvfp4_status dispatch_attention(const AttnJob& p, const KvMaps& maps, bool fp8, const AttnShape& s,
+                                cudaStream_t stream);
+
+}  // namespace nvfp4

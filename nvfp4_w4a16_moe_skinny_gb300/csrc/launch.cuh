@@ -70,6 +70,24 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// cuTensorMapEncodeTiled is a driver-API function; the library reaches it through
+// the runtime's entry-point query, so it links only the runtime.
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+inline EncodeTiledFn encode_tiled() {
+  static const EncodeTiledFn fn = []() -> EncodeTiledFn {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    return reinterpret_cast<EncodeTiledFn>(f);
+  }();
+  return fn;
+}
+
 // The streaming kernel of epilogue kEpi for this job and plan (decode kernel
 // specialised on m, or the prefill kernel for a plan with per-segment runs).
 // Defined in epi_<name>.cu.
@@ -80,5 +98,10 @@ nvfp4_status dispatch_stream(const Job& p, const WeightMaps& maps, const Plan& p
 // cleared if `clear`.  Defined in epi_<name>.cu.
 template <int kEpi>
 nvfp4_status epi_error_word(uint32_t* v, int clear);
+
+// The same for the units of the attention side (rope.cu, attention_d*.cu).
+nvfp4_status rope_error_word(uint32_t* v, int clear);
+template <int kDim>
+nvfp4_status attention_error_word(uint32_t* v, int clear);
 
 }  // namespace nvfp4

@@ -217,24 +217,6 @@ int choose_split(int m, int ng, int kc, int n_seg_est, int n_seg_max, int n_expe
 }
 
 // ------------------------------------------------------------------ TMA tensor maps
-// cuTensorMapEncodeTiled is a driver-API function; the library reaches it through
-// the runtime's entry-point query, so it links only the runtime.
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_tiled() {
-  static const EncodeTiledFn fn = []() -> EncodeTiledFn {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q{};
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return nullptr;
-    return reinterpret_cast<EncodeTiledFn>(f);
-  }();
-  return fn;
-}
-
 // The four tensor maps (boxes of 1..4 tiles, see WeightMaps) of the repacked
 // weight stack `w`: num_matrices x ceil(n/64) groups of ceil(k/64) chunks.
 bool encode_weight_maps(const nvfp4_weight* w, CUtensorMap (&maps)[4]) {
@@ -362,8 +344,10 @@ nvfp4_status nvfp4_device_error(uint32_t* out, int32_t clear) {
     if (cudaMemcpyToSymbol(g_device_error, &z, sizeof(z)) != cudaSuccess) return NVFP4_ERR_CUDA;
   }
   // the streaming kernels' translation units, one per epilogue
+  // and those of the attention side
   for (auto fn : {epi_error_word<kEpiStore>, epi_error_word<kEpiArgmax>, epi_error_word<kEpiGated>,
-                  epi_error_word<kEpiRows>, epi_error_word<kEpiSample>}) {
+                  epi_error_word<kEpiRows>, epi_error_word<kEpiSample>, rope_error_word, attention_error_word<64>,
+                  attention_error_word<128>, attention_error_word<256>}) {
     uint32_t w = 0;
     if (const nvfp4_status st = fn(&w, clear)) return st;
     v |= w;
