@@ -49,7 +49,7 @@ extern "C" {
 size_t paged_attention_workspace_bytes(int32_t n_tokens, int32_t n_seqs, int32_t max_new, int32_t n_heads,
                                        int32_t n_kv_heads, int32_t head_dim) {
   if (!sizes_ok(n_tokens, n_seqs, max_new, n_heads, n_kv_heads, head_dim)) return 0;
-  const AttnShape s = attn_shape(head_dim, static_cast<int>(packed_rows(n_tokens, max_new, n_heads, n_kv_heads)));
+  const AttnShape s = attn_shape(head_dim, false, packed_rows(n_tokens, max_new, n_heads, n_kv_heads));
   return static_cast<size_t>(2) * kAttnGrid * s.tile_rows * (head_dim + 2) * sizeof(float);
 }
 
@@ -84,14 +84,14 @@ nvfp4_status paged_attention(const nvfp4_kv_cache* cache, const nvfp4_batch* bat
   p.scale = scale, p.softcap = softcap, p.window = window;
   p.part = static_cast<float*>(ws);
   const bool fp8 = cache->dtype == NVFP4_KV_E4M3;
-  const AttnShape s = attn_shape(dim, static_cast<int>(packed_rows(n_tokens, batch->max_new, n_heads, kv)));
+  const AttnShape s = attn_shape(dim, fp8, packed_rows(n_tokens, batch->max_new, n_heads, kv));
   KvMaps maps;
-  const int box = std::min(cache->page_size, attn_slice(dim, fp8, s.kw));
+  const int box = std::min(cache->page_size, s.box_keys);
   if (!encode_pool_map(&maps.k, cache, cache->k, box) || !encode_pool_map(&maps.v, cache, cache->v, box))
     return NVFP4_ERR_CUDA;
-  if (dim == 64) return dispatch_attention<64>(p, maps, fp8, s, stream);
-  if (dim == 128) return dispatch_attention<128>(p, maps, fp8, s, stream);
-  return dispatch_attention<256>(p, maps, fp8, s, stream);
+  if (dim == 64) return dispatch_attention<64>(p, maps, cache, s, stream);
+  if (dim == 128) return dispatch_attention<128>(p, maps, cache, s, stream);
+  return dispatch_attention<256>(p, maps, cache, s, stream);
 }
 
 }  // extern "C"

@@ -98,56 +98,83 @@ __device__ __forceinline__ RowTile row_tile(const AttnJob& p, const Sequence& s,
   return t;
 }
 
-__device__ __forceinline__ long long sequence_units(const AttnJob& p, const Sequence& s, int tile_rows, int keys) {
+// Units of lane's sequence b (0 past the last): up to eight tiles by the lane itself,
+// longer ones by the whole warp, 32 tiles at a time.  All lanes of a warp call it.
+__device__ __forceinline__ long long sequence_units(const AttnJob& p, int b, int tile_rows, int keys) {
+  const int lane = threadIdx.x & 31;
+  Sequence s{};
+  if (b < p.n_seqs) s = sequence_of(p, b, tile_rows);
   long long u = 0;
-  for (int rt = 0; rt < s.tiles; ++rt) u += row_tile(p, s, rt, tile_rows, keys).units;
+  const bool large = s.tiles > 8;
+  if (!large)
+    for (int rt = 0; rt < s.tiles; ++rt) u += row_tile(p, s, rt, tile_rows, keys).units;
+  for (unsigned todo = __ballot_sync(0xffffffffu, large); todo; todo &= todo - 1) {
+    const int who = __ffs(todo) - 1;
+    const Sequence o = sequence_of(p, __shfl_sync(0xffffffffu, b, who), tile_rows);
+    long long part = 0;
+    for (int rt = lane; rt < o.tiles; rt += 32) part += row_tile(p, o, rt, tile_rows, keys).units;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) part += __shfl_xor_sync(0xffffffffu, part, d);
+    if (lane == who) u = part;
+  }
   return u * p.n_kv;
 }
 
-// Block-wide search over the sequences' units: the total, and the sequence that
-// holds unit `u` with the number of units before it (u < 0: the total only).
-// Every thread of the block calls it; scratch: 34 words of shared memory.
+// Where a CTA starts: the total number of units of the batch, and the sequence that
+// holds unit `u` with the number of units before it.
 struct Found {
   int seq;
   long long before;
 };
 
-template <int kThreadsInBlock>
-__device__ __forceinline__ long long scan_units(const AttnJob& p, int tile_rows, int keys, long long u, Found* found,
-                                                long long* scratch) {
+// Block-wide scan of the sequences' units (every thread of the block calls it; scratch:
+// 36 words of shared memory).  `unit_of(total)` says which unit is looked for
+// once the total is known (negative: none).
+template <int kThreadsInBlock, typename UnitOf>
+__device__ __forceinline__ long long scan_units(const AttnJob& p, int tile_rows, int keys, Found* found,
+                                                long long* scratch, UnitOf unit_of) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int kNW = kThreadsInBlock / 32;
-  long long base = 0;
-  for (int b0 = 0; b0 < p.n_seqs; b0 += kThreadsInBlock) {
-    const int b = b0 + threadIdx.x;
-    const long long mine = b < p.n_seqs ? sequence_units(p, sequence_of(p, b, tile_rows), tile_rows, keys) : 0;
-    long long incl = mine;
+  long long mine = 0, incl = 0, total = 0, u = -1;
+  // one pass for the total, then (again over the batch only where it is longer than
+  // the block) one that finds the unit
+  const bool once = p.n_seqs <= kThreadsInBlock;
+  for (int pass = 0; pass < 2; ++pass) {
+    long long base = 0;
+    for (int b0 = 0; b0 < p.n_seqs; b0 += kThreadsInBlock) {
+      if (pass == 0 || !once) {
+        mine = sequence_units(p, b0 + threadIdx.x, tile_rows, keys);
+        incl = mine;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    if (lane == 31) scratch[warp] = incl;
-    __syncthreads();
-    long long pre = base, all = 0;
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += v;
+        }
+        if (lane == 31) scratch[warp] = incl;
+        __syncthreads();
+        long long pre = base;
 #pragma unroll
-    for (int w = 0; w < kNW; ++w) {
-      if (w < warp) pre += scratch[w];
-      all += scratch[w];
+        for (int w = 0; w < kNW; ++w) {
+          if (w < warp) pre += scratch[w];
+          base += scratch[w];
+        }
+        incl += pre;
+      }
+      if (pass == 1 && mine > 0 && u >= incl - mine && u < incl) {
+        scratch[32] = b0 + threadIdx.x;
+        scratch[33] = incl - mine;
+      }
+      __syncthreads();
     }
-    if (u >= 0 && mine > 0 && u >= pre + incl - mine && u < pre + incl) {
-      scratch[32] = b;
-      scratch[33] = pre + incl - mine;
+    if (pass == 0) {
+      total = base;
+      u = unit_of(total);
+      if (u < 0) return total;
     }
-    base += all;
-    __syncthreads();
   }
-  if (u >= 0) {
-    found->seq = static_cast<int>(scratch[32]);
-    found->before = scratch[33];
-  }
-  __syncthreads();
-  return base;
+  found->seq = static_cast<int>(scratch[32]);
+  found->before = scratch[33];
+  return total;
 }
 
 // The pieces of one CTA, in order: consecutive shares of items.  All roles of a
@@ -165,8 +192,10 @@ __device__ __forceinline__ void walk_seq(const AttnJob& p, Walk& w, int tile_row
   if (w.s.tiles > 0) w.t = row_tile(p, w.s, 0, tile_rows, keys);
 }
 
-// The item that holds unit u, searched from the first item of w.b at w.item0.
+// The item that holds unit u, searched from where the walk is; u is below the total.
+// All lanes of a warp call it with the same arguments.
 __device__ __forceinline__ void walk_to(const AttnJob& p, Walk& w, long long u, int tile_rows, int keys) {
+  const int lane = threadIdx.x & 31;
   while (true) {
     if (w.rt < w.s.tiles) {
       const long long all = static_cast<long long>(w.t.units) * (p.n_kv - w.h);
@@ -178,8 +207,28 @@ __device__ __forceinline__ void walk_to(const AttnJob& p, Walk& w, long long u, 
       }
       w.item0 += all;
       w.h = 0;
-      ++w.rt;
-      if (w.rt < w.s.tiles) w.t = row_tile(p, w.s, w.rt, tile_rows, keys);
+      // the next row tiles, 32 at a time: the first one that ends past u
+      int rt = w.rt + 1;
+      bool here = false;
+      while (rt < w.s.tiles && !here) {
+        const bool in = rt + lane < w.s.tiles;
+        long long incl = in ? static_cast<long long>(row_tile(p, w.s, rt + lane, tile_rows, keys).units) * p.n_kv : 0;
+        const long long mine = incl;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += v;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, in && u < w.item0 + incl);
+        const int who = past ? __ffs(past) - 1 : 31;
+        const long long before = __shfl_sync(0xffffffffu, incl - mine, who);
+        const long long end = __shfl_sync(0xffffffffu, incl, 31);
+        here = past != 0;
+        w.item0 += here ? before : end;
+        rt += here ? who : 32;
+      }
+      w.rt = here ? rt : w.s.tiles;
+      if (here) w.t = row_tile(p, w.s, w.rt, tile_rows, keys);
     } else {
       if (++w.b >= p.n_seqs) return;  // not reached for a unit below the total
       walk_seq(p, w, tile_rows, keys);
@@ -314,11 +363,13 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, 1
   __syncthreads();
 
   Found f;
-  const long long total = scan_units<T::kThreadsAll>(p, T::kRows, T::kKeys, -1, &f, scratch);
-  const int grid = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
+  int grid = 0;
+  const long long total = scan_units<T::kThreadsAll>(p, T::kRows, T::kKeys, &f, scratch, [&](long long all) {
+    grid = static_cast<int>(min(static_cast<long long>(gridDim.x), all));
+    return static_cast<int>(blockIdx.x) < grid ? range_start(blockIdx.x, all, grid) : -1;
+  });
   if (static_cast<int>(blockIdx.x) >= grid) return;
   const long long u0 = range_start(blockIdx.x, total, grid), u1 = range_start(blockIdx.x + 1, total, grid);
-  scan_units<T::kThreadsAll>(p, T::kRows, T::kKeys, u0, &f, scratch);
   Walk w;
   w.b = f.seq, w.item0 = f.before;
   walk_seq(p, w, T::kRows, T::kKeys);
@@ -739,15 +790,17 @@ constexpr int kJoinThreads = 128;
 template <int kDim>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnJob p, int split_grid, int tile_rows,
                                                                  int keys) {
-  __shared__ long long scratch[34];
+  __shared__ long long scratch[36];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   Found f;
   // lengths are complete before the split grid starts: only its pieces are waited for
-  const long long total = scan_units<kJoinThreads>(p, tile_rows, keys, -1, &f, scratch);
-  const int grid = static_cast<int>(min(static_cast<long long>(split_grid), total));
   const int c = blockIdx.x + 1;
-  const long long u = c < grid ? range_start(c, total, grid) : 0;
-  if (c < grid) scan_units<kJoinThreads>(p, tile_rows, keys, u, &f, scratch);
+  int grid = 0;
+  long long u = -1;
+  const long long total = scan_units<kJoinThreads>(p, tile_rows, keys, &f, scratch, [&](long long all) {
+    grid = static_cast<int>(min(static_cast<long long>(split_grid), all));
+    return u = c < grid ? range_start(c, all, grid) : -1;
+  });
   pdl_launch_dependents();
   pdl_wait();  // every block waits, so that this grid's end means that the split grid has ended
   if (c >= grid) return;
@@ -756,58 +809,73 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnJob p
   walk_seq(p, w, tile_rows, keys);
   walk_to(p, w, u, tile_rows, keys);
   if (u == w.item0 || range_start(c - 1, total, grid) > w.item0) return;  // no split here, or not its first boundary
-  const int r = blockIdx.y * 4 + warp;
-  if (r >= w.t.rows) return;
   // first and last range that hold a unit of the item
   const int c0 = c - 1;
   const int c1 = static_cast<int>(((w.item0 + w.t.units) * grid - 1) / total);
   const float* ml = p.part + static_cast<int64_t>(2) * split_grid * tile_rows * kDim;
   constexpr int kPer = kDim / 32;
-  float m = -INFINITY;
-  for (int i = c0 + lane; i <= c1; i += 32) {
-    const int slot = 2 * i + (i == c0 && w.item0 > range_start(i, total, grid) ? 1 : 0);
-    m = fmaxf(m, ml[(static_cast<int64_t>(slot) * tile_rows + r) * 2]);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float acc[kPer];
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) acc[j] = 0.f;
-  float l = 0.f;
-#pragma unroll 4
-  for (int i = c0; i <= c1; ++i) {
-    const int slot = 2 * i + (i == c0 && w.item0 > range_start(i, total, grid) ? 1 : 0);
-    const int64_t row = static_cast<int64_t>(slot) * tile_rows + r;
-    const float2 v = *reinterpret_cast<const float2*>(ml + row * 2);
-    const float a = m == -INFINITY ? 1.0f : exp2_approx(v.x - m);
-    l += a * v.y;
-    const float* o = p.part + row * kDim + lane * kPer;
-#pragma unroll
-    for (int j = 0; j < kPer; j += 2) {
-      const float2 x = *reinterpret_cast<const float2*>(o + j);
-      acc[j] += a * x.x, acc[j + 1] += a * x.y;
+  for (int r = blockIdx.y * 4 + warp; r < w.t.rows; r += gridDim.y * 4) {
+    float m = -INFINITY;
+    for (int i = c0 + lane; i <= c1; i += 32) {
+      const int slot = 2 * i + (i == c0 && w.item0 > range_start(i, total, grid) ? 1 : 0);
+      m = fmaxf(m, ml[(static_cast<int64_t>(slot) * tile_rows + r) * 2]);
     }
-  }
-  const int rr = w.t.row0 + r, tok = rr / p.group, head = w.h * p.group + rr - tok * p.group;
-  const int64_t row = w.s.tok0 + tok;
-  const float inv = l == 0.f ? 0.f : (p.v_scale ? __ldg(p.v_scale + w.h) : 1.0f) / l;
-  uint32_t* o = reinterpret_cast<uint32_t*>(p.out + row * p.out_stride + static_cast<int64_t>(head) * kDim) + lane * (kPer / 2);
 #pragma unroll
-  for (int j = 0; j < kPer; j += 2) o[j / 2] = f32x2_to_bf16x2(acc[j] * inv, acc[j + 1] * inv);
-  if (p.lse && lane == 0) p.lse[row * p.n_heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float acc[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) acc[j] = 0.f;
+    float l = 0.f;
+#pragma unroll 4
+    for (int i = c0; i <= c1; ++i) {
+      const int slot = 2 * i + (i == c0 && w.item0 > range_start(i, total, grid) ? 1 : 0);
+      const int64_t row = static_cast<int64_t>(slot) * tile_rows + r;
+      const float2 v = *reinterpret_cast<const float2*>(ml + row * 2);
+      const float a = m == -INFINITY ? 1.0f : exp2_approx(v.x - m);
+      l += a * v.y;
+      const float* o = p.part + row * kDim + lane * kPer;
+#pragma unroll
+      for (int j = 0; j < kPer; j += 2) {
+        const float2 x = *reinterpret_cast<const float2*>(o + j);
+        acc[j] += a * x.x, acc[j + 1] += a * x.y;
+      }
+    }
+    const int rr = w.t.row0 + r, tok = rr / p.group, head = w.h * p.group + rr - tok * p.group;
+    const int64_t row = w.s.tok0 + tok;
+    const float inv = l == 0.f ? 0.f : (p.v_scale ? __ldg(p.v_scale + w.h) : 1.0f) / l;
+    uint32_t* o = reinterpret_cast<uint32_t*>(p.out + row * p.out_stride + static_cast<int64_t>(head) * kDim) + lane * (kPer / 2);
+#pragma unroll
+    for (int j = 0; j < kPer; j += 2) o[j / 2] = f32x2_to_bf16x2(acc[j] * inv, acc[j + 1] * inv);
+    if (p.lse && lane == 0) p.lse[row * p.n_heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+  }
 }
 
 // ------------------------------------------------------------------ launch
 
-// Warps over rows and key slices for a tile of up to `rows` packed rows: 16 rows leave
-// eight key slices to eight warps, 64 rows and more share one slice among four.
+// Which kernel and tile serve up to `rows` packed rows per sequence and kv head.  16 rows
+// leave eight key slices to eight warps, 64 rows share one slice among four; more
+// go to the tcgen05 kernel (attention_chunk.cuh).
 struct AttnShape {
-  int rw, kw, tile_rows;
+  int rw, kw, tile_rows, box_keys;
+  bool chunk;
 };
-inline AttnShape attn_shape(int dim, int rows) {
-  if (rows <= 16) return {1, dim == 256 ? 4 : 8, 16};
-  if (rows <= 32) return {2, dim == 256 ? 2 : 4, 32};
-  return {4, 1, 64};
+inline AttnShape attn_shape(int dim, bool fp8, int64_t rows) {
+  if (rows > 64) return {0, 0, dim == 256 ? 128 : 256, dim == 256 ? 64 : 128, true};
+  const int rw = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
+  const int kw = rw == 4 ? 1 : (dim == 256 ? 4 : 8) / rw;
+  return {rw, kw, 16 * rw, attn_slice(dim, fp8, kw), false};
+}
+
+template <int kDim>
+nvfp4_status launch_attn_join(const AttnJob& p, int tile_rows, int keys, cudaStream_t stream) {
+  // one unit an item: nothing can be split
+  if ((static_cast<int64_t>(p.max_pages) << p.page_log2) > keys) {
+    const int rows = tile_rows / 4 < 16 ? tile_rows / 4 : 16;
+    if (launch_pdl(attn_join_kernel<kDim>, dim3(kAttnGrid - 1, rows), dim3(kJoinThreads), 0, stream, p, kAttnGrid,
+                   tile_rows, keys) != cudaSuccess)
+      return NVFP4_ERR_CUDA;
+  }
+  return launched();
 }
 
 template <int kDim, bool kFp8, int kRW, int kKW>
@@ -817,19 +885,12 @@ nvfp4_status launch_attn_split(const AttnJob& p, const KvMaps& maps, cudaStream_
   if (launch_pdl(attn_split_kernel<kDim, kFp8, kRW, kKW>, dim3(kAttnGrid), dim3(T::kThreadsAll), T::kSmem, stream, p,
                  maps) != cudaSuccess)
     return NVFP4_ERR_CUDA;
-  // one unit an item: nothing can be split
-  const int64_t most = static_cast<int64_t>(p.max_pages) << p.page_log2;
-  if (most > T::kKeys) {
-    if (launch_pdl(attn_join_kernel<kDim>, dim3(kAttnGrid - 1, T::kRows / 4), dim3(kJoinThreads), 0, stream, p,
-                   kAttnGrid, T::kRows, T::kKeys) != cudaSuccess)
-      return NVFP4_ERR_CUDA;
-  }
-  return launched();
+  return launch_attn_join<kDim>(p, T::kRows, T::kKeys, stream);
 }
 
 // The split and join grids for heads of kDim values (attention_d*.cu).
 template <int kDim>
-nvfp4_status dispatch_attention(const AttnJob& p, const KvMaps& maps, bool fp8, const AttnShape& s,
+nvfp4_status dispatch_attention(const AttnJob& p, const KvMaps& maps, const nvfp4_kv_cache* cache, const AttnShape& s,
                                 cudaStream_t stream);
 
 }  // namespace nvfp4

@@ -1,0 +1,682 @@
+// Attention over a paged cache, many rows at a time: prefill chunks and whole
+// prompts (paged_attention), on tcgen05 tensor cores with accumulators in TMEM.
+//
+// The same packed rows, units, ranges and join as the split kernel
+// (attention.cuh), with tiles of 128 rows per softmax warpgroup (two of them for
+// heads of 64 and 128 values, one for 256) by kKeys keys.
+//
+// Roles of a CTA (one per SM).  Warp 0 copies K and V tiles by TMA into two-stage
+// rings; one thread of warp 1 issues every MMA and commits it to mbarriers; warps
+// 2 and 3 make tiles fit for the tensor cores (below); each softmax warpgroup owns
+// 128 rows, a thread a row, so maxima and sums need no exchange.  Per tile: S = Q K^T
+// into TMEM; the row's thread reads S, takes weights 2^(s - m), writes them back as
+// 16-bit P over S; O += P V with P read from TMEM.  With two row groups the
+// tensor cores run one group's products while the other group is in its softmax;
+// with one (256 values) S is double-buffered and the next Q K^T runs meanwhile.
+//
+// The reference m of a row's weights follows its maximum lazily: only when a new
+// maximum exceeds it by 2^8 are the row's sums scaled down, so O rarely leaves the
+// tensor cores' hands; weights stay below 2^8 (bf16 holds them as exactly as those below
+// 1; f16 weights, for E4M3 caches, are offset by 2^7 and stay below 2^15).
+//
+// Warps 2 and 3.  For an E4M3 cache they convert tiles to f16 (exact).  For both
+// kinds they clean V in tiles that some row does not wholly see: keys outside
+// every row's reach become zeros (the pool may hold anything there, and 0 * inf is
+// NaN), and an infinity or NaN in a key that only some rows see is taken out of the
+// product and noted; the rows that see it add it at the end from the pool itself.
+#pragma once
+
+#include "attention.cuh"
+
+namespace nvfp4 {
+
+template <int kDim, bool kFp8>
+struct ChunkTile {
+  static constexpr int kGroups = kDim == 256 ? 1 : 2;      // softmax warpgroups of 128 rows
+  static constexpr int kRows = 128 * kGroups;
+  static constexpr int kKeys = kDim == 256 ? 64 : 128;
+  static constexpr int kSBuf = kDim == 256 ? 2 : 1;        // S buffers per group
+  static constexpr int kThreadsAll = 128 + 128 * kGroups;
+  static constexpr int kEl = kFp8 ? 1 : 2;
+  // boxes of the pool (as AttnTile names them, for tile_offset)
+  static constexpr int kRowB = kDim * kEl < 128 ? kDim * kEl : 128;
+  static constexpr int kSub = kDim * kEl / kRowB;
+  static constexpr uint32_t kSwz = kRowB == 128 ? 0x70 : 0x30;
+  static constexpr int kSubB = kKeys * kRowB;
+  static constexpr int kRawB = kSubB * kSub;               // a K or V tile as it is in the pool
+  static constexpr int kTileB = kKeys * kDim * 2;          // a 16-bit tile: [kDim / 64][kKeys][128 bytes]
+  static constexpr int kQB = 128 * kDim * 2;               // a group's Q: [kDim / 64][128][128 bytes]
+  static constexpr int kRing = kGroups * kQB;              // offset of the K ring
+  static constexpr int kRaw = kRing + 4 * kTileB;
+  static constexpr int kBars = kRaw + (kFp8 ? 2 * kRawB : 0);
+  static constexpr size_t kSmem = 1024 + kBars + 1024;
+  // TMEM columns: O of each group, then the S buffers
+  static constexpr int kSCol = kGroups * kDim;
+  static_assert(kSCol + kGroups * kSBuf * kKeys <= 512, "TMEM");
+  static_assert(kSmem <= kMaxSmem, "shared memory");
+};
+
+// ------------------------------------------------------------------ tcgen05
+
+// Shared-memory matrix descriptor, 128-byte swizzle: start, leading and stride byte
+// offsets in units of 16 bytes, version 1.  K-major: rows of 128 bytes, `stride`
+// between groups of eight rows.  MN-major: `lead` between blocks of 64 values,
+// `stride` between groups of eight k rows.
+__device__ __forceinline__ uint64_t umma_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3fff) | static_cast<uint64_t>((lead >> 4) & 0x3fff) << 16 |
+         static_cast<uint64_t>((stride >> 4) & 0x3fff) << 32 | (1ull << 46) | (2ull << 61);
+}
+
+// Instruction descriptor: fp32 accumulator, A and B f16 (0) or bf16 (1), B MN-major or
+// K-major, N and M.
+__device__ __forceinline__ constexpr uint32_t umma_idesc(bool bf16, bool b_mn, int n, int m) {
+  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u) |
+         (static_cast<uint32_t>(n / 8) << 17) | (static_cast<uint32_t>(m / 16) << 24);
+}
+
+__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+      : "memory");
+}
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+               : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Loaded values are used only after the wait: ties them to this place in the program.
+template <int kN>
+__device__ __forceinline__ void tmem_loaded(float (&r)[kN]) {
+  tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < kN; ++i) asm volatile("" : "+f"(r[i]));
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 32 columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld32(float* r, uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
+      "%30,%31}, [%32];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
+        "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
+        "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const float* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
+      "%30,%31};" ::"f"(r[0]),
+      "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]), "f"(r[8]), "f"(r[9]), "f"(r[10]),
+      "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15]), "f"(r[16]), "f"(r[17]), "f"(r[18]), "f"(r[19]),
+      "f"(r[20]), "f"(r[21]), "f"(r[22]), "f"(r[23]), "f"(r[24]), "f"(r[25]), "f"(r[26]), "f"(r[27]), "f"(r[28]),
+      "f"(r[29]), "f"(r[30]), "f"(r[31]), "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
+      : "memory");
+}
+
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// Byte offset of 16-byte chunk c of row r in a 16-bit tile of `rows` rows of 128 bytes
+// per block of 64 values.
+__device__ __forceinline__ uint32_t umma_offset(int rows, int r, int c) {
+  return (c >> 3) * rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+}
+
+// What the warps of a CTA share besides tiles: barriers of the rings and hand-overs.
+struct ChunkBars {
+  uint64_t k_full[2], k_ready[2], k_empty[2];
+  uint64_t v_full[2], v_ready[2], v_empty[2];
+  uint64_t raw_full[2], raw_empty[2];
+  uint64_t q_full[2];
+  uint64_t s_full[2], p_full[2];  // one per group, or per S buffer
+  uint64_t o_full[2];             // products with V done: one per group, or in turn
+  long long scratch[36];
+  uint32_t tmem;
+  int noted;  // an infinity or NaN was taken out of V, in this CTA's items so far
+};
+
+// ------------------------------------------------------------------ the kernel
+
+// Keys that every row of an item sees, [all_lo, all_hi), and that some row sees, [any_lo, any_hi).
+struct KeyRange {
+  int all_lo, all_hi, any_lo, any_hi;
+};
+
+__device__ __forceinline__ KeyRange key_range(const AttnJob& p, const Walk& w) {
+  KeyRange r;
+  const int first = w.s.len - w.s.n + w.t.row0 / p.group;
+  const int last = w.s.len - w.s.n + (w.t.row0 + w.t.rows - 1) / p.group;
+  r.all_hi = min(first + 1, w.s.len);
+  r.all_lo = p.window > 0 ? last - p.window + 1 : 0;
+  r.any_hi = w.t.hi;
+  r.any_lo = w.t.lo;
+  return r;
+}
+
+__device__ __forceinline__ bool partly_seen(const KeyRange& r, int key0, int keys) {
+  return key0 + keys > r.all_hi || key0 < r.all_lo;
+}
+
+// One 16-byte chunk of V (eight 16-bit values) of a key: nothing if no row sees it, and
+// without infinities and NaN.
+template <bool kF16>
+__device__ __forceinline__ uint4 clean_chunk(uint4 v, bool seen, bool& noted) {
+  if (!seen) return make_uint4(0, 0, 0, 0);
+  const uint32_t a = nonfinite_mask<kF16>(v.x), b = nonfinite_mask<kF16>(v.y);
+  const uint32_t c = nonfinite_mask<kF16>(v.z), d = nonfinite_mask<kF16>(v.w);
+  noted = noted || (a | b | c | d) != 0;
+  return make_uint4(v.x & ~a, v.y & ~b, v.z & ~c, v.w & ~d);
+}
+
+template <int kDim, bool kFp8>
+__global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
+    attn_chunk_kernel(const AttnJob p, const __grid_constant__ KvMaps maps, const void* v_pool, int64_t page_stride) {
+  using T = ChunkTile<kDim, kFp8>;
+  constexpr int kG = T::kGroups, kKeys = T::kKeys;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw0 = smem_addr(smem_raw);
+  const uint32_t base = (raw0 + 1023u) & ~1023u;
+  ChunkBars* bars = reinterpret_cast<ChunkBars*>(smem_raw + (base - raw0) + T::kBars);
+  static_assert(sizeof(ChunkBars) <= 1024, "barriers");
+  const uint32_t q_at = base, k_at = base + T::kRing, v_at = k_at + 2 * T::kTileB, raw_at = base + T::kRaw;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bars->k_full + i, 1), mbar_init(bars->k_ready + i, 2), mbar_init(bars->k_empty + i, 1);
+      mbar_init(bars->v_full + i, 1), mbar_init(bars->v_ready + i, 2), mbar_init(bars->v_empty + i, 1);
+      mbar_init(bars->raw_full + i, 1), mbar_init(bars->raw_empty + i, 2);
+      mbar_init(bars->q_full + i, 4), mbar_init(bars->s_full + i, 1), mbar_init(bars->p_full + i, 4);
+      mbar_init(bars->o_full + i, 1);
+    }
+    bars->noted = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&bars->tmem))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    tc_fence_before();
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *static_cast<volatile uint32_t*>(&bars->tmem);
+
+  Found f;
+  int grid = 0;
+  const long long total = scan_units<T::kThreadsAll>(p, T::kRows, kKeys, &f, bars->scratch, [&](long long all) {
+    grid = static_cast<int>(min(static_cast<long long>(gridDim.x), all));
+    return static_cast<int>(blockIdx.x) < grid ? range_start(blockIdx.x, all, grid) : -1;
+  });
+  const bool idle = static_cast<int>(blockIdx.x) >= grid;
+  const long long u0 = idle ? 0 : range_start(blockIdx.x, total, grid);
+  const long long u1 = idle ? 0 : range_start(blockIdx.x + 1, total, grid);
+  Walk w;
+  w.b = f.seq, w.item0 = f.before;
+  if (!idle) walk_seq(p, w, T::kRows, kKeys);
+  bool ran_out = false;  // a wait reached its limit (recorded): no further waits, the roles stay in step
+#define NVFP4_WAIT(bar, parity) ran_out = ran_out || !mbar_wait_warp(bar, parity)
+
+  // tile counts over all items so far: ring positions and phases
+  uint32_t nt = 0;
+  if (warp < 4) {
+    if constexpr (kG == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 0) {
+      // ------------------------------------------------------------ copies
+      const int box_rows = min(1 << p.page_log2, kKeys);
+      const int boxes = kKeys / box_rows;
+      uint32_t raw = 0;
+      for (long long u = u0; u < u1;) {
+        walk_to(p, w, u, T::kRows, kKeys);
+        const int first = w.t.tile0 + static_cast<int>(u - w.item0);
+        const int n = static_cast<int>(min(w.item0 + w.t.units - u, u1 - u));
+        const int32_t* table = p.table + static_cast<int64_t>(w.b) * p.max_pages;
+        // order: K 0, then K j + 1 and V j
+        for (int c = 0; c < 2 * n; ++c) {
+          const bool is_v = c == 2 * n - 1 || (c > 0 && c % 2 == 0);
+          const int j = c == 0 ? 0 : (is_v ? (c == 2 * n - 1 ? n - 1 : c / 2 - 1) : (c + 1) / 2);
+          const uint32_t g = nt + j;  // of its own ring
+          uint64_t* full;
+          uint32_t dst;
+          if constexpr (kFp8) {
+            const uint32_t st = raw & 1;
+            if (raw >= 2) NVFP4_WAIT(bars->raw_empty + st, ((raw >> 1) - 1) & 1);
+            full = bars->raw_full + st;
+            dst = raw_at + st * T::kRawB;
+            ++raw;
+          } else {
+            const uint32_t st = g & 1;
+            if (g >= 2) NVFP4_WAIT((is_v ? bars->v_empty : bars->k_empty) + st, ((g >> 1) - 1) & 1);
+            full = (is_v ? bars->v_full : bars->k_full) + st;
+            dst = (is_v ? v_at : k_at) + st * T::kTileB;
+          }
+          const int key0 = (first + j) * kKeys;
+          if (lane == 0) {
+            int pieces = 0;
+            for (int i = 0; i < boxes; ++i) {
+              const int k = key0 + i * box_rows;
+              pieces += k < w.t.hi && k + box_rows > w.t.lo;
+            }
+            mbar_arrive_expect_tx(full, pieces * box_rows * T::kRowB * T::kSub);
+          }
+          __syncwarp();
+          for (int i = lane; i < boxes * T::kSub; i += 32) {
+            const int sub = i % T::kSub, piece = i / T::kSub;
+            const int k = key0 + piece * box_rows;
+            if (k >= w.t.hi || k + box_rows <= w.t.lo) continue;
+            int page = __ldg(table + (k >> p.page_log2));
+            if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.num_pages)) {
+              page = p.num_pages;
+              atomicOr(&g_device_error, kErrPage);
+            }
+            tma_load_4d_plain(dst + sub * T::kSubB + piece * box_rows * T::kRowB, is_v ? &maps.v : &maps.k,
+                              sub * (T::kRowB / T::kEl), k & ((1 << p.page_log2) - 1), w.h, page, smem_addr(full));
+          }
+        }
+        nt += n;
+        u += n;
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ MMA issue
+      const uint32_t id_qk = umma_idesc(!kFp8, false, kKeys, 128), id_pv = umma_idesc(!kFp8, true, kDim, 128);
+      uint32_t nq[2] = {0, 0}, np[2] = {0, 0};  // completed hand-overs of Q and P per group (or P per S buffer)
+      const auto qk = [&](int g, uint32_t t) {
+        const uint32_t d = tmem + T::kSCol + (kG == 2 ? g : (t & 1)) * kKeys;
+        const uint32_t a = q_at + g * T::kQB, b = k_at + (t & 1) * T::kTileB;
+        if (lane == 0) {
+#pragma unroll
+          for (int k = 0; k < kDim / 16; ++k)
+            umma_ss(d, umma_desc(a + (k >> 2) * (128 * 128) + (k & 3) * 32, 16, 1024),
+                    umma_desc(b + (k >> 2) * (kKeys * 128) + (k & 3) * 32, 16, 1024), id_qk, k > 0);
+          umma_commit(bars->s_full + (kG == 2 ? g : (t & 1)));
+        }
+        __syncwarp();
+      };
+      const auto pv = [&](int g, uint32_t t, bool add) {
+        const uint32_t a = tmem + T::kSCol + (kG == 2 ? g : (t & 1)) * kKeys;
+        const uint32_t b = v_at + (t & 1) * T::kTileB;
+        if (lane == 0) {
+#pragma unroll
+          for (int k = 0; k < kKeys / 16; ++k)
+            umma_ts(tmem + g * kDim, a + 8 * k, umma_desc(b + k * 2048, kKeys * 128, 1024), id_pv, add || k > 0);
+          umma_commit(bars->o_full + (kG == 2 ? g : (t & 1)));
+        }
+        __syncwarp();
+      };
+      const auto wait_k = [&](uint32_t t) {
+        NVFP4_WAIT((kFp8 ? bars->k_ready : bars->k_full) + (t & 1), (t >> 1) & 1);
+      };
+      for (long long u = u0; u < u1;) {
+        walk_to(p, w, u, T::kRows, kKeys);
+        const int n = static_cast<int>(min(w.item0 + w.t.units - u, u1 - u));
+        const int groups = kG == 2 && w.t.rows > 128 ? 2 : 1;
+        for (int g = 0; g < groups; ++g) {
+          NVFP4_WAIT(bars->q_full + g, nq[g] & 1);
+          ++nq[g];
+        }
+        wait_k(nt);
+        tc_fence_after();
+        for (int g = 0; g < groups; ++g) qk(g, nt);
+        if (lane == 0) umma_commit(bars->k_empty + (nt & 1));
+        for (int j = 0; j < n; ++j) {
+          const uint32_t t = nt + j;
+          if (kG == 1 && j + 1 < n) {
+            wait_k(t + 1);
+            tc_fence_after();
+            qk(0, t + 1);
+            if (lane == 0) umma_commit(bars->k_empty + ((t + 1) & 1));
+          }
+          NVFP4_WAIT(bars->v_ready + (t & 1), (t >> 1) & 1);
+          if constexpr (!kFp8) NVFP4_WAIT(bars->v_full + (t & 1), (t >> 1) & 1);
+          if (kG == 2 && j + 1 < n) wait_k(t + 1);
+          for (int g = 0; g < groups; ++g) {
+            const int pb = kG == 2 ? g : (t & 1);
+            NVFP4_WAIT(bars->p_full + pb, np[pb] & 1);
+            ++np[pb];
+            tc_fence_after();
+            pv(g, t, j > 0);
+            if (kG == 2 && j + 1 < n) qk(g, t + 1);
+          }
+          if (lane == 0) {
+            umma_commit(bars->v_empty + (t & 1));
+            if (kG == 2 && j + 1 < n) umma_commit(bars->k_empty + ((t + 1) & 1));
+          }
+        }
+        nt += n;
+        u += n;
+      }
+    } else {
+      // ------------------------------------------------------------ tiles made fit
+      const int who = (warp - 2) * 32 + lane;
+      uint32_t raw = 0;
+      for (long long u = u0; u < u1;) {
+        walk_to(p, w, u, T::kRows, kKeys);
+        const int first = w.t.tile0 + static_cast<int>(u - w.item0);
+        const int n = static_cast<int>(min(w.item0 + w.t.units - u, u1 - u));
+        const KeyRange kr = key_range(p, w);
+        bool noted = false;
+        if constexpr (!kFp8) {
+          for (int j = 0; j < n; ++j) {
+            const uint32_t t = nt + j, st = t & 1;
+            NVFP4_WAIT(bars->v_full + st, (t >> 1) & 1);
+            const int key0 = (first + j) * kKeys;
+            if (partly_seen(kr, key0, kKeys)) {
+              const uint32_t tile = v_at + st * T::kTileB;
+              for (int r = who; r < kKeys; r += 64) {
+                const bool seen = key0 + r >= kr.any_lo && key0 + r < kr.any_hi;
+#pragma unroll 4
+                for (int c = 0; c < kDim / 8; ++c) {
+                  const uint32_t at = tile + umma_offset(kKeys, r, c);
+                  sts128(at, clean_chunk<false>(lds128(at), seen, noted));
+                }
+              }
+              if (noted) *static_cast<volatile int*>(&bars->noted) = 1;
+              fence_proxy_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars->v_ready + st);
+          }
+        } else {
+          for (int c = 0; c < 2 * n; ++c, ++raw) {
+            const bool is_v = c == 2 * n - 1 || (c > 0 && c % 2 == 0);
+            const int j = c == 0 ? 0 : (is_v ? (c == 2 * n - 1 ? n - 1 : c / 2 - 1) : (c + 1) / 2);
+            const uint32_t t = nt + j, st = t & 1, rst = raw & 1;
+            NVFP4_WAIT(bars->raw_full + rst, (raw >> 1) & 1);
+            if (t >= 2) NVFP4_WAIT((is_v ? bars->v_empty : bars->k_empty) + st, ((t >> 1) - 1) & 1);
+            const int key0 = (first + j) * kKeys;
+            const bool clean = is_v && partly_seen(kr, key0, kKeys);
+            const uint32_t from = raw_at + rst * T::kRawB, to = (is_v ? v_at : k_at) + st * T::kTileB;
+            for (int r = who; r < kKeys; r += 64) {
+              const bool seen = key0 + r >= kr.any_lo && key0 + r < kr.any_hi;
+#pragma unroll 4
+              for (int x = 0; x < kDim / 16; ++x) {
+                const uint4 v = lds128(from + tile_offset<T>(r, x));
+                uint4 a, b;
+                e4m3x4_to_f16x2(v.x, a.x, a.y);
+                e4m3x4_to_f16x2(v.y, a.z, a.w);
+                e4m3x4_to_f16x2(v.z, b.x, b.y);
+                e4m3x4_to_f16x2(v.w, b.z, b.w);
+                if (clean) a = clean_chunk<true>(a, seen, noted), b = clean_chunk<true>(b, seen, noted);
+                sts128(to + umma_offset(kKeys, r, 2 * x), a);
+                sts128(to + umma_offset(kKeys, r, 2 * x + 1), b);
+              }
+            }
+            if (noted) *static_cast<volatile int*>(&bars->noted) = 1;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(bars->raw_empty + rst);
+              mbar_arrive((is_v ? bars->v_ready : bars->k_ready) + st);
+            }
+          }
+        }
+        nt += n;
+        u += n;
+      }
+    }
+  } else {
+    // -------------------------------------------------------------- softmax
+    if constexpr (kG == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    const int g = (warp - 4) >> 2;
+    const int row = (warp & 3) * 32 + lane;              // of the group: its TMEM lane
+    const uint32_t lane_at = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t o_at = tmem + lane_at + g * kDim;
+    const float log2e = 1.4426950408889634f;
+    const float kOffset = kFp8 ? 7.0f : 0.0f;
+    uint32_t mine = 0;  // this group's tiles so far
+    for (long long u = u0; u < u1;) {
+      walk_to(p, w, u, T::kRows, kKeys);
+      const int first = w.t.tile0 + static_cast<int>(u - w.item0);
+      const int n = static_cast<int>(min(w.item0 + w.t.units - u, u1 - u));
+      if (g * 128 >= w.t.rows) {  // this group has no rows here
+        nt += n, u += n;
+        continue;
+      }
+      const int r = g * 128 + row;
+      const bool live = r < w.t.rows;
+      const int rr = w.t.row0 + min(r, w.t.rows - 1);
+      const int tok = rr / p.group, head = w.h * p.group + rr - tok * p.group;
+      const int pos = w.s.len - w.s.n + tok;
+      const int64_t token = w.s.tok0 + tok;
+
+      // ---- Q of this row to shared memory (scaled into f16's range for an E4M3 cache;
+      // a negative scale turns its sign, a zero one makes it zero)
+      float qscale = 1.0f;
+      {
+        const uint16_t* q = p.q + token * p.q_stride + static_cast<int64_t>(head) * kDim;
+        const uint32_t sign = p.scale < 0.f ? 0x80008000u : 0u;
+        const bool zero = !live || p.scale == 0.f;
+        float up = 1.0f;
+        if constexpr (kFp8) {
+          float amax = 0.f;
+#pragma unroll 8
+          for (int c = 0; c < kDim / 8; ++c) {
+            const uint4 v = zero ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(q + 8 * c);
+            const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(x[i] << 16)), fabsf(__uint_as_float(x[i] & 0xffff0000u))));
+          }
+          const int e = pow2_rescale_exponent(amax);
+          up = exp2i(e);
+          qscale = exp2i(-e);
+        }
+#pragma unroll 8
+        for (int c = 0; c < kDim / 8; ++c) {
+          uint4 v = zero ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(q + 8 * c);
+          uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            x[i] ^= sign;
+            if constexpr (kFp8)
+              x[i] = f32x2_to_f16x2(__uint_as_float(x[i] << 16) * up, __uint_as_float(x[i] & 0xffff0000u) * up);
+          }
+          sts128(q_at + g * T::kQB + umma_offset(128, row, c), make_uint4(x[0], x[1], x[2], x[3]));
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars->q_full + g);
+      }
+      const float ks = (kFp8 && p.k_scale) ? __ldg(p.k_scale + w.h) : 1.0f;
+      const bool capped = p.softcap > 0.f;
+      const float scale = p.scale == 0.f ? 1.0f : fabsf(p.scale);
+      // logits in units of log 2: s * mul; with a softcap, cap2 * tanh(s * unit)
+      const float unit = scale * ks * qscale * (capped ? 1.0f / p.softcap : log2e);
+      const float mul = capped ? 1.0f : fmaxf(unit, 1.2e-38f);  // (-inf * 0 would be NaN)
+      const float cap2 = p.softcap * log2e;
+      // keys that this row sees, and those that all rows of the warp see
+      const int see_hi = min(pos + 1, w.s.len), see_lo = p.window > 0 ? pos - p.window + 1 : -(1 << 30);
+
+      float m = -INFINITY, l = 0.f;  // reference of the weights, this row's sum
+      for (int j = 0; j < n; ++j, ++mine) {
+        const uint32_t t = nt + j;
+        const int sb = kG == 2 ? g : (t & 1);
+        NVFP4_WAIT(bars->s_full + sb, (kG == 2 ? mine : (t >> 1)) & 1);
+        tc_fence_after();
+        const uint32_t s_at = tmem + lane_at + T::kSCol + sb * kKeys;
+        float s[kKeys];
+#pragma unroll
+        for (int c = 0; c < kKeys; c += 32) tmem_ld32(s + c, s_at + c);
+        tmem_loaded(s);
+        const int key0 = (first + j) * kKeys;
+        if (capped) {
+#pragma unroll
+          for (int c = 0; c < kKeys; ++c)
+            s[c] = cap2 * (1.0f - __fdividef(2.0f, exp2_approx(s[c] * (unit * 2.0f * log2e)) + 1.0f));
+        }
+        if (__any_sync(0xffffffffu, key0 + kKeys > see_hi || key0 < see_lo)) {
+          const int hi = see_hi - key0, lo = see_lo - key0;
+#pragma unroll
+          for (int c = 0; c < kKeys; ++c) s[c] = c >= lo && c < hi ? s[c] : -INFINITY;
+        }
+        float top[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int c = 4; c < kKeys; ++c) top[c & 3] = fmaxf(top[c & 3], s[c]);
+        const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * mul - kOffset;
+        const bool move = high > m + 8.0f || m == -INFINITY;
+        if (__any_sync(0xffffffffu, move && j > 0 && high > m)) {
+          // the row's sums follow its maximum: everything up to the tile before is in O
+          if constexpr (kG == 1) {
+            NVFP4_WAIT(bars->o_full + ((t - 1) & 1), ((t - 1) >> 1) & 1);
+            tc_fence_after();
+          }
+          const float a = move && high > m ? exp2_approx(m - high) : 1.0f;
+          l *= a;
+#pragma unroll 1
+          for (int c = 0; c < kDim; c += 32) {
+            float o[32];
+            tmem_ld32(o, o_at + c);
+            tmem_loaded(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= a;
+            tmem_st32(o_at + c, o);
+          }
+          tmem_wait_st();
+        }
+        if (move && high > m) m = high;
+        const float ref = m == -INFINITY ? 0.f : m;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < kKeys; c += 32) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float a = exp2_approx(fmaf(s[c + 2 * i], mul, -ref));
+            const float b = exp2_approx(fmaf(s[c + 2 * i + 1], mul, -ref));
+            sum[i & 3] += a + b;
+            pk[i] = kFp8 ? f32x2_to_f16x2(a, b) : f32x2_to_bf16x2(a, b);
+          }
+          tmem_st16(s_at + c / 2, pk);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars->p_full + sb);
+      }
+      nt += n;
+
+      // ---- write: the finished row, or this piece's share of it
+      if constexpr (kG == 2)
+        NVFP4_WAIT(bars->o_full + g, (mine - 1) & 1);
+      else
+        NVFP4_WAIT(bars->o_full + ((nt - 1) & 1), ((nt - 1) >> 1) & 1);
+      tc_fence_after();
+      const bool whole = n == w.t.units;
+      const int slot = 2 * blockIdx.x + (u == u0 ? 0 : 1);
+      const float vs = (kFp8 && p.v_scale) ? __ldg(p.v_scale + w.h) : 1.0f;
+      const float inv = !whole ? 1.0f : (l == 0.f ? 0.f : vs / l);
+      uint16_t* out = p.out + token * p.out_stride + static_cast<int64_t>(head) * kDim;
+      float* part = p.part + (static_cast<int64_t>(slot) * T::kRows + r) * kDim;
+      const bool noted = *static_cast<volatile int*>(&bars->noted) != 0;
+      const KeyRange kr = key_range(p, w);
+#pragma unroll 1
+      for (int c = 0; c < kDim; c += 32) {
+        float o[32];
+        tmem_ld32(o, o_at + c);
+        tmem_loaded(o);
+        if (noted && live) {
+          // infinities and NaN that were taken out of V, from the pool
+          for (int j = 0; j < n; ++j) {
+            const int key0 = (first + j) * kKeys;
+            if (!partly_seen(kr, key0, kKeys)) continue;
+            for (int key = max(key0, see_lo); key < min(key0 + kKeys, see_hi); ++key) {
+              if (key < 0) continue;
+              const int page = __ldg(p.table + static_cast<int64_t>(w.b) * p.max_pages + (key >> p.page_log2));
+              if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.num_pages)) continue;
+              const int64_t at = page * page_stride + ((static_cast<int64_t>(w.h) << p.page_log2) +
+                                                       (key & ((1 << p.page_log2) - 1))) * kDim + c;
+              for (int i = 0; i < 32; i += 2) {
+                float a, b;
+                if constexpr (kFp8) {
+                  uint32_t x, y;
+                  e4m3x4_to_f16x2(*reinterpret_cast<const uint16_t*>(static_cast<const uint8_t*>(v_pool) + at + i), x, y);
+                  a = f16lo_to_f32(x), b = f16hi_to_f32(x);
+                } else {
+                  const uint32_t x = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(v_pool) + at + i);
+                  a = __uint_as_float(x << 16), b = __uint_as_float(x & 0xffff0000u);
+                }
+#pragma unroll
+                for (int z = 0; z < 32; z += 2)
+                  if (z == i) {
+                    if (!isfinite(a)) o[z] += a;
+                    if (!isfinite(b)) o[z + 1] += b;
+                  }
+              }
+            }
+          }
+        }
+        if (!live) continue;
+        if (whole) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 8)
+            *reinterpret_cast<uint4*>(out + c + i) =
+                make_uint4(f32x2_to_bf16x2(o[i] * inv, o[i + 1] * inv), f32x2_to_bf16x2(o[i + 2] * inv, o[i + 3] * inv),
+                           f32x2_to_bf16x2(o[i + 4] * inv, o[i + 5] * inv), f32x2_to_bf16x2(o[i + 6] * inv, o[i + 7] * inv));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<float4*>(part + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+        }
+      }
+      if (live) {
+        if (!whole) {
+          float* ml = p.part + static_cast<int64_t>(2) * gridDim.x * T::kRows * kDim;
+          *reinterpret_cast<float2*>(ml + (static_cast<int64_t>(slot) * T::kRows + r) * 2) = make_float2(m, l);
+        } else if (p.lse) {
+          p.lse[token * p.n_heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+        }
+      }
+      tc_fence_before();  // O has been read before the next item's first P is handed over
+      u += n;
+    }
+  }
+#undef NVFP4_WAIT
+  if (ran_out) {  // copies may still be under way: give them time to land before the CTA ends
+    for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  }
+}
+
+template <int kDim, bool kFp8>
+nvfp4_status launch_attn_chunk(const AttnJob& p, const KvMaps& maps, const void* v_pool, int64_t page_stride,
+                               cudaStream_t stream) {
+  using T = ChunkTile<kDim, kFp8>;
+  if (set_smem(attn_chunk_kernel<kDim, kFp8>, T::kSmem) != cudaSuccess) return NVFP4_ERR_CUDA;
+  if (launch_pdl(attn_chunk_kernel<kDim, kFp8>, dim3(kAttnGrid), dim3(T::kThreadsAll), T::kSmem, stream, p, maps,
+                 v_pool, page_stride) != cudaSuccess)
+    return NVFP4_ERR_CUDA;
+  return launch_attn_join<kDim>(p, T::kRows, T::kKeys, stream);
+}
+
+}  // namespace nvfp4

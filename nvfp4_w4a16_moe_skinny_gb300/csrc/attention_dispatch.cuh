@@ -2,22 +2,25 @@
 // translation unit, which instantiates them for its head size only.
 #pragma once
 
-#include "attention.cuh"
+#include "attention_chunk.cuh"
 
 namespace nvfp4 {
 
 template <int kDim, bool kFp8>
-nvfp4_status dispatch_rows(const AttnJob& p, const KvMaps& maps, const AttnShape& s, cudaStream_t stream) {
+nvfp4_status dispatch_rows(const AttnJob& p, const KvMaps& maps, const nvfp4_kv_cache* cache, const AttnShape& s,
+                           cudaStream_t stream) {
   constexpr int kWide = kDim == 256 ? 4 : 8;
+  if (s.chunk) return launch_attn_chunk<kDim, kFp8>(p, maps, cache->v, cache->page_stride, stream);
   if (s.rw == 1) return launch_attn_split<kDim, kFp8, 1, kWide>(p, maps, stream);
   if (s.rw == 2) return launch_attn_split<kDim, kFp8, 2, kWide / 2>(p, maps, stream);
   return launch_attn_split<kDim, kFp8, 4, 1>(p, maps, stream);
 }
 
 template <int kDim>
-nvfp4_status dispatch_attention(const AttnJob& p, const KvMaps& maps, bool fp8, const AttnShape& s,
+nvfp4_status dispatch_attention(const AttnJob& p, const KvMaps& maps, const nvfp4_kv_cache* cache, const AttnShape& s,
                                 cudaStream_t stream) {
-  return fp8 ? dispatch_rows<kDim, true>(p, maps, s, stream) : dispatch_rows<kDim, false>(p, maps, s, stream);
+  return cache->dtype == NVFP4_KV_E4M3 ? dispatch_rows<kDim, true>(p, maps, cache, s, stream)
+                                       : dispatch_rows<kDim, false>(p, maps, cache, s, stream);
 }
 
 template <int kDim>
