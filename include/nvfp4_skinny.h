@@ -549,7 +549,7 @@ nvfp4_status kv_append(const nvfp4_kv_cache *cache, const uint16_t *k, int64_t k
  *   out        (device) rows of n_heads heads; rows past cu_tokens[n_seqs] are not
  *              written.  lse (device) fp32 [n_tokens, n_heads] or NULL.
  *   scale      finite; softcap finite, >= 0; window >= 0 (0: all keys).
- *   ws         (device) paged_attention_workspace_bytes() bytes, 16-byte aligned;
+ *   ws         (device) paged_attention_workspace_bytes() bytes, 32-byte aligned;
  *              needs no initialisation and holds nothing between calls.
  * kv_len is read as at most max_pages * page_size, cu_tokens as ascending and at
  * most n_tokens.  A page id outside the pool among the keys that are seen reads

@@ -68,7 +68,7 @@ nvfp4_status paged_attention(const nvfp4_kv_cache* cache, const nvfp4_batch* bat
   if (const nvfp4_status st = check_rows(q, q_stride, n_heads, dim)) return st;
   if (const nvfp4_status st = check_rows(out, out_stride, n_heads, dim)) return st;
   if (!aligned(batch->cu_tokens, 4) || !aligned(batch->kv_len, 4) || !aligned(batch->page_table, 4) ||
-      !aligned(lse, 4) || !aligned(ws, 16))
+      !aligned(lse, 4) || !aligned(ws, 32))
     return NVFP4_ERR_ALIGN;
   if (!ws || ws_bytes < paged_attention_workspace_bytes(n_tokens, batch->n_seqs, batch->max_new, n_heads, kv, dim))
     return NVFP4_ERR_WORKSPACE;
@@ -77,7 +77,7 @@ nvfp4_status paged_attention(const nvfp4_kv_cache* cache, const nvfp4_batch* bat
   AttnJob p{};
   p.cu = batch->cu_tokens, p.kv_len = batch->kv_len, p.table = batch->page_table;
   p.n_seqs = batch->n_seqs, p.max_pages = batch->max_pages, p.n_tokens = n_tokens;
-  p.n_heads = n_heads, p.n_kv = kv, p.group = n_heads / kv;
+  p.n_heads = n_heads, p.n_kv = kv, p.group = n_heads / kv, p.by_group = fast_div(n_heads / kv);
   p.page_log2 = log2i(cache->page_size), p.num_pages = cache->num_pages;
   p.q = q, p.q_stride = q_stride, p.out = out, p.out_stride = out_stride, p.lse = lse;
   p.k_scale = cache->k_scale, p.v_scale = cache->v_scale;

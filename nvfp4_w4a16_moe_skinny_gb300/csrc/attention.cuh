@@ -36,12 +36,27 @@ namespace nvfp4 {
 
 constexpr int kAttnGrid = 152;  // CTAs of the split; fixed, so that workspace sizes are host-computable
 
+// Division by a number that a launch knows: x / g = umulhi(x, mul) >> shift for
+// x < 2^31 (shift < 0: g = 1).
+struct FastDiv {
+  uint32_t mul;
+  int shift;
+};
+
+inline FastDiv fast_div(int g) {
+  if (g == 1) return {0, -1};
+  int s = 0;
+  while ((int64_t{1} << s) < g) ++s;
+  return {static_cast<uint32_t>(((uint64_t{1} << (31 + s)) + g - 1) / g), s - 1};
+}
+
 struct AttnJob {
   const int32_t* cu;
   const int32_t* kv_len;
   const int32_t* table;
   int n_seqs, max_pages, n_tokens;
   int n_heads, n_kv, group;
+  FastDiv by_group;
   int page_log2, num_pages;
   const uint16_t* q;
   int64_t q_stride;
@@ -61,58 +76,69 @@ struct KvMaps {
 
 // ------------------------------------------------------------------ work decomposition
 
-// A row tile of one sequence: positions of its first and last token and the keys
-// that any of its rows sees, [lo, hi).
-struct RowTile {
-  int row0, rows;  // first packed row and number of rows
-  int lo, hi;
-  int tile0, units;  // first key tile, number of units (at least one, so that empty rows are written)
+// Tiling of one kernel: rows of a row tile, keys of a unit, and what starting and
+// finishing an item costs, counted in units (the ranges are balanced with it).
+struct Tiling {
+  int rows, keys, over;
 };
+
+// Quotient of x < 2^31 by the divisor that `d` was made for (fast_div): a multiply by the
+// rounded-up reciprocal and a shift.
+__device__ __forceinline__ int div_by(const FastDiv d, int x) {
+  return d.shift < 0 ? x : static_cast<int>(__umulhi(static_cast<uint32_t>(x), d.mul) >> d.shift);
+}
 
 struct Sequence {
   int tok0, n, len, rows, tiles;
 };
 
-__device__ __forceinline__ Sequence sequence_of(const AttnJob& p, int b, int tile_rows) {
+__device__ __forceinline__ Sequence sequence_of(const AttnJob& p, int b, const Tiling& g) {
   Sequence s;
-  const int a = min(max(__ldg(p.cu + b), 0), p.n_tokens), e = min(max(__ldg(p.cu + b + 1), a), p.n_tokens);
-  const int64_t most = static_cast<int64_t>(p.max_pages) << p.page_log2;
-  s.tok0 = a;
-  s.n = e - a;
-  s.len = static_cast<int>(min(static_cast<int64_t>(max(__ldg(p.kv_len + b), 0)), most));
+  const int lo = __ldg(p.cu + b), hi = __ldg(p.cu + b + 1), len = __ldg(p.kv_len + b);
+  s.tok0 = min(max(lo, 0), p.n_tokens);
+  s.n = min(max(hi, s.tok0), p.n_tokens) - s.tok0;
+  s.len = min(max(len, 0), p.max_pages << p.page_log2);
   s.rows = s.n * p.group;
-  s.tiles = (s.rows + tile_rows - 1) / tile_rows;
+  s.tiles = (s.rows + g.rows - 1) / g.rows;
   return s;
 }
 
-__device__ __forceinline__ RowTile row_tile(const AttnJob& p, const Sequence& s, int rt, int tile_rows, int keys) {
+// A row tile of one sequence and the keys that any of its rows sees, [lo, hi).
+struct RowTile {
+  int row0, rows;    // first packed row and number of rows
+  int lo, hi;
+  int tile0, units;  // first key tile, number of units (at least one, so that empty rows are written)
+};
+
+__device__ __forceinline__ RowTile row_tile(const AttnJob& p, const Sequence& s, int rt, const Tiling& g) {
   RowTile t;
-  t.row0 = rt * tile_rows;
-  t.rows = min(tile_rows, s.rows - t.row0);
-  const int p0 = s.len - s.n + t.row0 / p.group;
-  const int p1 = s.len - s.n + (t.row0 + t.rows - 1) / p.group;
+  t.row0 = rt * g.rows;
+  t.rows = min(g.rows, s.rows - t.row0);
+  const int p0 = s.len - s.n + div_by(p.by_group, t.row0);
+  const int p1 = s.len - s.n + div_by(p.by_group, t.row0 + t.rows - 1);
   t.hi = min(max(p1 + 1, 0), s.len);
   t.lo = p.window > 0 ? min(max(p0 - p.window + 1, 0), t.hi) : 0;
-  t.tile0 = t.lo / keys;
-  t.units = max(1, (t.hi + keys - 1) / keys - t.tile0);
+  t.tile0 = t.lo / g.keys;
+  t.units = max(1, (t.hi + g.keys - 1) / g.keys - t.tile0);
   return t;
 }
 
-// Units of lane's sequence b (0 past the last): up to eight tiles by the lane itself,
-// longer ones by the whole warp, 32 tiles at a time.  All lanes of a warp call it.
-__device__ __forceinline__ long long sequence_units(const AttnJob& p, int b, int tile_rows, int keys) {
+// Units, overheads included, of each lane's sequence b (0 past the last): up to eight
+// row tiles by the lane itself, longer ones by the whole warp, 32 tiles at a time.  All lanes
+// of a warp call it.
+__device__ __forceinline__ long long sequence_units(const AttnJob& p, int b, const Tiling& g) {
   const int lane = threadIdx.x & 31;
   Sequence s{};
-  if (b < p.n_seqs) s = sequence_of(p, b, tile_rows);
+  if (b < p.n_seqs) s = sequence_of(p, b, g);
   long long u = 0;
   const bool large = s.tiles > 8;
   if (!large)
-    for (int rt = 0; rt < s.tiles; ++rt) u += row_tile(p, s, rt, tile_rows, keys).units;
+    for (int rt = 0; rt < s.tiles; ++rt) u += row_tile(p, s, rt, g).units + g.over;
   for (unsigned todo = __ballot_sync(0xffffffffu, large); todo; todo &= todo - 1) {
     const int who = __ffs(todo) - 1;
-    const Sequence o = sequence_of(p, __shfl_sync(0xffffffffu, b, who), tile_rows);
+    const Sequence o = sequence_of(p, __shfl_sync(0xffffffffu, b, who), g);
     long long part = 0;
-    for (int rt = lane; rt < o.tiles; rt += 32) part += row_tile(p, o, rt, tile_rows, keys).units;
+    for (int rt = lane; rt < o.tiles; rt += 32) part += row_tile(p, o, rt, g).units + g.over;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) part += __shfl_xor_sync(0xffffffffu, part, d);
     if (lane == who) u = part;
@@ -120,30 +146,56 @@ __device__ __forceinline__ long long sequence_units(const AttnJob& p, int b, int
   return u * p.n_kv;
 }
 
-// Where a CTA starts: the total number of units of the batch, and the sequence that
-// holds unit `u` with the number of units before it.
+// The split of all units into contiguous ranges, one per CTA.
+struct Ranges {
+  long long total, each;
+  int grid, more;  // ranges in use; the first `more` of them hold each + 1 units
+  __device__ __forceinline__ void set(long long all, int ctas) {
+    total = all;
+    grid = static_cast<int>(min(static_cast<long long>(ctas), all));
+    if (grid < 1) {
+      each = more = 0;
+    } else if (all >> 31) {
+      each = all / grid;
+      more = static_cast<int>(all - each * grid);
+    } else {
+      const uint32_t q = static_cast<uint32_t>(all) / static_cast<uint32_t>(grid);
+      each = q;
+      more = static_cast<int>(static_cast<uint32_t>(all) - q * grid);
+    }
+  }
+  __device__ __forceinline__ long long start(int c) const { return c * each + min(c, more); }
+  __device__ __forceinline__ int holder(long long u) const {
+    const long long cut = more * (each + 1);
+    return static_cast<int>(u < cut ? u / (each + 1) : more + (u - cut) / each);
+  }
+};
+
+// Where a CTA starts: the sequence that holds its first unit, and the units before it.
 struct Found {
   int seq;
   long long before;
 };
 
 // Block-wide scan of the sequences' units (every thread of the block calls it; scratch:
-// 36 words of shared memory).  `unit_of(total)` says which unit is looked for
-// once the total is known (negative: none).
-template <int kThreadsInBlock, typename UnitOf>
-__device__ __forceinline__ long long scan_units(const AttnJob& p, int tile_rows, int keys, Found* found,
-                                                long long* scratch, UnitOf unit_of) {
+// 36 words of shared memory).  Sets the ranges and, if range c is in use, finds where
+// its first unit lies.
+template <int kThreadsInBlock>
+__device__ __forceinline__ void find_range(const AttnJob& p, const Tiling& g, int ctas, int c, Ranges* ranges,
+                                           Found* found, long long* scratch) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int kNW = kThreadsInBlock / 32;
-  long long mine = 0, incl = 0, total = 0, u = -1;
+  long long mine = 0, incl = 0;
   // one pass for the total, then (again over the batch only where it is longer than
   // the block) one that finds the unit
   const bool once = p.n_seqs <= kThreadsInBlock;
+#pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
     long long base = 0;
+#pragma unroll 1
     for (int b0 = 0; b0 < p.n_seqs; b0 += kThreadsInBlock) {
       if (pass == 0 || !once) {
-        mine = sequence_units(p, b0 + threadIdx.x, tile_rows, keys);
+        mine = sequence_units(p, b0 + threadIdx.x, g);
         incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -153,32 +205,34 @@ __device__ __forceinline__ long long scan_units(const AttnJob& p, int tile_rows,
         if (lane == 31) scratch[warp] = incl;
         __syncthreads();
         long long pre = base;
-#pragma unroll
+#pragma unroll 1
         for (int w = 0; w < kNW; ++w) {
-          if (w < warp) pre += scratch[w];
-          base += scratch[w];
+          const long long v = scratch[w];
+          if (w < warp) pre += v;
+          base += v;
         }
         incl += pre;
       }
-      if (pass == 1 && mine > 0 && u >= incl - mine && u < incl) {
-        scratch[32] = b0 + threadIdx.x;
-        scratch[33] = incl - mine;
+      if (pass == 1) {
+        const long long u = ranges->start(c);
+        if (mine > 0 && u >= incl - mine && u < incl) {
+          scratch[32] = b0 + threadIdx.x;
+          scratch[33] = incl - mine;
+        }
       }
       __syncthreads();
     }
     if (pass == 0) {
-      total = base;
-      u = unit_of(total);
-      if (u < 0) return total;
+      ranges->set(base, ctas);
+      if (c >= ranges->grid) return;
     }
   }
   found->seq = static_cast<int>(scratch[32]);
   found->before = scratch[33];
-  return total;
 }
 
-// The pieces of one CTA, in order: consecutive shares of items.  All roles of a
-// CTA walk the same list.
+// A place in the list of items (sequence, row tile, kv head).  All roles of a CTA walk
+// the same list.
 struct Walk {
   int b, rt, h;
   long long item0;  // first unit of the item
@@ -186,23 +240,30 @@ struct Walk {
   RowTile t;
 };
 
-__device__ __forceinline__ void walk_seq(const AttnJob& p, Walk& w, int tile_rows, int keys) {
-  w.s = sequence_of(p, w.b, tile_rows);
+__device__ __forceinline__ void walk_seq(const AttnJob& p, Walk& w, const Tiling& g) {
+  w.s = sequence_of(p, w.b, g);
   w.rt = 0, w.h = 0;
-  if (w.s.tiles > 0) w.t = row_tile(p, w.s, 0, tile_rows, keys);
+  if (w.s.tiles > 0) w.t = row_tile(p, w.s, 0, g);
 }
 
 // The item that holds unit u, searched from where the walk is; u is below the total.
 // All lanes of a warp call it with the same arguments.
-__device__ __forceinline__ void walk_to(const AttnJob& p, Walk& w, long long u, int tile_rows, int keys) {
+__device__ __forceinline__ void walk_to(const AttnJob& p, Walk& w, long long u, const Tiling& g) {
   const int lane = threadIdx.x & 31;
   while (true) {
     if (w.rt < w.s.tiles) {
-      const long long all = static_cast<long long>(w.t.units) * (p.n_kv - w.h);
+      const int span = w.t.units + g.over;
+      // one after the other in the usual case; far jumps (a CTA's first item) by division
+      if (u < w.item0 + span) return;
+      if (w.h + 1 < p.n_kv && u < w.item0 + 2 * static_cast<long long>(span)) {
+        w.item0 += span, ++w.h;
+        return;
+      }
+      const long long all = static_cast<long long>(span) * (p.n_kv - w.h);
       if (u < w.item0 + all) {
-        const int k = static_cast<int>((u - w.item0) / w.t.units);
+        const int k = static_cast<int>((u - w.item0) / span);
         w.h += k;
-        w.item0 += static_cast<long long>(k) * w.t.units;
+        w.item0 += static_cast<long long>(k) * span;
         return;
       }
       w.item0 += all;
@@ -210,10 +271,11 @@ __device__ __forceinline__ void walk_to(const AttnJob& p, Walk& w, long long u, 
       // the next row tiles, 32 at a time: the first one that ends past u
       int rt = w.rt + 1;
       bool here = false;
+#pragma unroll 1
       while (rt < w.s.tiles && !here) {
         const bool in = rt + lane < w.s.tiles;
-        long long incl = in ? static_cast<long long>(row_tile(p, w.s, rt + lane, tile_rows, keys).units) * p.n_kv : 0;
-        const long long mine = incl;
+        const long long mine = in ? static_cast<long long>(row_tile(p, w.s, rt + lane, g).units + g.over) * p.n_kv : 0;
+        long long incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const long long v = __shfl_up_sync(0xffffffffu, incl, o);
@@ -228,15 +290,34 @@ __device__ __forceinline__ void walk_to(const AttnJob& p, Walk& w, long long u, 
         rt += here ? who : 32;
       }
       w.rt = here ? rt : w.s.tiles;
-      if (here) w.t = row_tile(p, w.s, w.rt, tile_rows, keys);
+      if (here) w.t = row_tile(p, w.s, w.rt, g);
     } else {
       if (++w.b >= p.n_seqs) return;  // not reached for a unit below the total
-      walk_seq(p, w, tile_rows, keys);
+      walk_seq(p, w, g);
     }
   }
 }
 
-__device__ __forceinline__ long long range_start(int c, long long total, int grid) { return c * total / grid; }
+// The share of the walk's item that range [u0, u1) of CTA c holds, from unit u on: key tiles
+// [first, first + n) (none, if only the item's overhead falls into the range), and
+// where an unfinished share goes.
+struct Share {
+  int first, n, slot;
+  bool whole;
+  long long end;
+};
+
+__device__ __forceinline__ Share share_at(const Walk& w, long long u, long long u0, long long u1, int c,
+                                          const Tiling& g) {
+  Share q;
+  const int from = static_cast<int>(u - w.item0);
+  q.end = min(w.item0 + w.t.units + g.over, u1);
+  q.n = max(0, min(w.t.units, static_cast<int>(q.end - w.item0)) - from);
+  q.first = w.t.tile0 + from;
+  q.whole = q.n == w.t.units;
+  q.slot = 2 * c + (u == u0 ? 0 : 1);
+  return q;
+}
 
 // ------------------------------------------------------------------ MMA helpers
 
@@ -315,6 +396,7 @@ struct AttnTile {
   static constexpr int kKeys = kSlice * kKW;                                           // keys of a unit
   static constexpr int kConsumers = kRW * kKW;
   static constexpr int kThreadsAll = (kConsumers + 1) * 32;
+  static constexpr int kOver = 1;                                                       // an item's own cost, in units
   static constexpr int kEl = kFp8 ? 1 : 2;
   static constexpr int kRowB = kDim * kEl < 128 ? kDim * kEl : 128;  // bytes of a row of a box
   static constexpr int kSub = kDim * kEl / kRowB;                    // boxes across a head
@@ -362,17 +444,15 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, 1
   pdl_launch_dependents();
   __syncthreads();
 
+  constexpr Tiling kTiling{T::kRows, T::kKeys, T::kOver};
   Found f;
-  int grid = 0;
-  const long long total = scan_units<T::kThreadsAll>(p, T::kRows, T::kKeys, &f, scratch, [&](long long all) {
-    grid = static_cast<int>(min(static_cast<long long>(gridDim.x), all));
-    return static_cast<int>(blockIdx.x) < grid ? range_start(blockIdx.x, all, grid) : -1;
-  });
-  if (static_cast<int>(blockIdx.x) >= grid) return;
-  const long long u0 = range_start(blockIdx.x, total, grid), u1 = range_start(blockIdx.x + 1, total, grid);
+  Ranges ranges;
+  find_range<T::kThreadsAll>(p, kTiling, gridDim.x, blockIdx.x, &ranges, &f, scratch);
+  if (static_cast<int>(blockIdx.x) >= ranges.grid) return;
+  const long long u0 = ranges.start(blockIdx.x), u1 = ranges.start(blockIdx.x + 1);
   Walk w;
   w.b = f.seq, w.item0 = f.before;
-  walk_seq(p, w, T::kRows, T::kKeys);
+  walk_seq(p, w, kTiling);
 
   uint32_t step = 0;  // ring position, the same in every warp
   bool ran_out = false;  // a wait reached its limit (recorded): no further waits, the roles stay in step
@@ -382,14 +462,14 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, 1
     const int boxes = T::kSlice / box_rows;              // page pieces of a slice
     const int copies = boxes * T::kSub * 2;              // TMA copies of a slice
     for (long long u = u0; u < u1;) {
-      walk_to(p, w, u, T::kRows, T::kKeys);
-      const int first = w.t.tile0 + static_cast<int>(u - w.item0);
-      const int n = static_cast<int>(min(w.item0 + w.t.units - u, u1 - u));
+      walk_to(p, w, u, kTiling);
+      const Share pc = share_at(w, u, u0, u1, blockIdx.x, kTiling);
+      u = pc.end;
       const int32_t* table = p.table + static_cast<int64_t>(w.b) * p.max_pages;
-      for (int i = 0; i < n; ++i, ++step) {
+      for (int i = 0; i < pc.n; ++i, ++step) {
         const int st = step % T::kStages;
         const uint32_t round = step / T::kStages;
-        const int key0 = (first + i) * T::kKeys;
+        const int key0 = (pc.first + i) * T::kKeys;
         for (int slice = 0; slice < kKW; ++slice) {
           const int bar = st * kKW + slice;
           if (round > 0 && !mbar_wait_warp(empty + bar, (round - 1) & 1)) return;
@@ -419,7 +499,6 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, 1
           }
         }
       }
-      u += n;
     }
     return;
   }
@@ -435,9 +514,10 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, 1
   const int lrow = lane & 7, lmat = lane >> 3;
 
   for (long long u = u0; u < u1;) {
-    walk_to(p, w, u, T::kRows, T::kKeys);
-    const int first = w.t.tile0 + static_cast<int>(u - w.item0);
-    const int n = static_cast<int>(min(w.item0 + w.t.units - u, u1 - u));
+    walk_to(p, w, u, kTiling);
+    const Share pc = share_at(w, u, u0, u1, blockIdx.x, kTiling);
+    u = pc.end;
+    if (pc.n == 0) continue;
 
     // this thread's two rows (g and g + 8 of the warp's 16): token, head, position
     int pos[2], tok[2], head[2];
@@ -447,13 +527,14 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, 1
       const int r = rw * 16 + g + 8 * i;
       live[i] = r < w.t.rows;
       const int rr = w.t.row0 + min(r, w.t.rows - 1);
-      tok[i] = rr / p.group;
+      tok[i] = div_by(p.by_group, rr);
       head[i] = w.h * p.group + rr - tok[i] * p.group;
       pos[i] = w.s.len - w.s.n + tok[i];
     }
     // positions over the warp's rows: the smallest and largest
     const int r_lo = w.t.row0 + min(rw * 16, w.t.rows - 1), r_hi = w.t.row0 + min(rw * 16 + 15, w.t.rows - 1);
-    const int pos_lo = w.s.len - w.s.n + r_lo / p.group, pos_hi = w.s.len - w.s.n + r_hi / p.group;
+    const int pos_lo = w.s.len - w.s.n + div_by(p.by_group, r_lo);
+    const int pos_hi = w.s.len - w.s.n + div_by(p.by_group, r_hi);
     const int all_hi = min(pos_lo + 1, w.s.len);                                  // keys [all_lo, all_hi) seen by every row
     const int all_lo = p.window > 0 ? pos_hi - p.window + 1 : 0;
     const int any_hi = min(pos_hi + 1, w.s.len);                                  // keys [any_lo, any_hi) seen by some row
@@ -518,10 +599,10 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, 1
     float m[2] = {-INFINITY, -INFINITY};  // reference of the weights: weight = 2^(s - m)
     float l[2] = {0.f, 0.f};              // this lane's share of the sum of weights
 
-    for (int i = 0; i < n; ++i, ++step) {
+    for (int i = 0; i < pc.n; ++i, ++step) {
       const int st = step % T::kStages;
       ran_out = ran_out || !mbar_wait_warp(full + st * kKW + kw, (step / T::kStages) & 1);
-      const int key0 = (first + i) * T::kKeys + kw * T::kSlice;
+      const int key0 = (pc.first + i) * T::kKeys + kw * T::kSlice;
       if (key0 < any_hi && key0 + T::kSlice > any_lo) {
         const uint32_t kt = ring + st * T::kStageB + kw * 2 * T::kSliceB, vt = kt + T::kSliceB;
         const bool edge = key0 + T::kSlice > all_hi || key0 < all_lo;
@@ -733,12 +814,10 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, 1
     }
     // ---- write: the finished rows, or this piece's share of them
     if (kw == 0) {
-      const bool whole = n == w.t.units;
-      const int slot = 2 * blockIdx.x + (u == u0 ? 0 : 1);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         if (!live[x]) continue;
-        if (whole) {
+        if (pc.whole) {
           const float vs = (kFp8 && p.v_scale) ? __ldg(p.v_scale + w.h) : 1.0f;
           const float inv = l[x] == 0.f ? 0.f : vs / l[x];
           const int64_t row = w.s.tok0 + tok[x];
@@ -759,7 +838,7 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, 1
             p.lse[row * p.n_heads + head[x]] = l[x] == 0.f ? -INFINITY : (m[x] + log2f(l[x])) * 0.6931471805599453f;
         } else {
           const int r = rw * 16 + g + 8 * x;
-          float* o = p.part + (static_cast<int64_t>(slot) * T::kRows + r) * kDim;
+          float* o = p.part + (static_cast<int64_t>(pc.slot) * T::kRows + r) * kDim;
 #pragma unroll
           for (int j = 0; j < kDT; j += 2) {
             if constexpr (!kFp8) {
@@ -772,12 +851,11 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, 1
           }
           if (t4 == 0) {
             float* ml = p.part + static_cast<int64_t>(2) * gridDim.x * T::kRows * kDim;
-            *reinterpret_cast<float2*>(ml + (static_cast<int64_t>(slot) * T::kRows + r) * 2) = make_float2(m[x], l[x]);
+            *reinterpret_cast<float2*>(ml + (static_cast<int64_t>(pc.slot) * T::kRows + r) * 2) = make_float2(m[x], l[x]);
           }
         }
       }
     }
-    u += n;
   }
 }
 
@@ -788,36 +866,37 @@ constexpr int kJoinThreads = 128;
 // Block (c, y): if range boundary c is the first one inside an item, joins that
 // item's pieces for four of its rows (a warp a row), in range order.
 template <int kDim>
-__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnJob p, int split_grid, int tile_rows,
-                                                                 int keys) {
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnJob p, int split_grid, const Tiling g) {
   __shared__ long long scratch[36];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tile_rows = g.rows;
   Found f;
+  Ranges ranges;
   // lengths are complete before the split grid starts: only its pieces are waited for
   const int c = blockIdx.x + 1;
-  int grid = 0;
-  long long u = -1;
-  const long long total = scan_units<kJoinThreads>(p, tile_rows, keys, &f, scratch, [&](long long all) {
-    grid = static_cast<int>(min(static_cast<long long>(split_grid), all));
-    return u = c < grid ? range_start(c, all, grid) : -1;
-  });
+  find_range<kJoinThreads>(p, g, split_grid, c, &ranges, &f, scratch);
+  Walk w;
+  bool first = false;
+  if (c < ranges.grid) {
+    w.b = f.seq, w.item0 = f.before;
+    walk_seq(p, w, g);
+    const long long u = ranges.start(c);
+    walk_to(p, w, u, g);
+    // a boundary among the item's tiles, and the first one
+    first = u > w.item0 && u < w.item0 + w.t.units && ranges.start(c - 1) <= w.item0;
+  }
   pdl_launch_dependents();
   pdl_wait();  // every block waits, so that this grid's end means that the split grid has ended
-  if (c >= grid) return;
-  Walk w;
-  w.b = f.seq, w.item0 = f.before;
-  walk_seq(p, w, tile_rows, keys);
-  walk_to(p, w, u, tile_rows, keys);
-  if (u == w.item0 || range_start(c - 1, total, grid) > w.item0) return;  // no split here, or not its first boundary
-  // first and last range that hold a unit of the item
-  const int c0 = c - 1;
-  const int c1 = static_cast<int>(((w.item0 + w.t.units) * grid - 1) / total);
+  if (!first) return;
+  // first and last range that hold a tile of the item
+  const int c0 = c - 1, c1 = ranges.holder(w.item0 + w.t.units - 1);
+  const int skip = w.item0 > ranges.start(c0) ? 1 : 0;  // the first share is its range's second slot
   const float* ml = p.part + static_cast<int64_t>(2) * split_grid * tile_rows * kDim;
   constexpr int kPer = kDim / 32;
   for (int r = blockIdx.y * 4 + warp; r < w.t.rows; r += gridDim.y * 4) {
     float m = -INFINITY;
     for (int i = c0 + lane; i <= c1; i += 32) {
-      const int slot = 2 * i + (i == c0 && w.item0 > range_start(i, total, grid) ? 1 : 0);
+      const int slot = 2 * i + (i == c0 ? skip : 0);
       m = fmaxf(m, ml[(static_cast<int64_t>(slot) * tile_rows + r) * 2]);
     }
 #pragma unroll
@@ -828,7 +907,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnJob p
     float l = 0.f;
 #pragma unroll 4
     for (int i = c0; i <= c1; ++i) {
-      const int slot = 2 * i + (i == c0 && w.item0 > range_start(i, total, grid) ? 1 : 0);
+      const int slot = 2 * i + (i == c0 ? skip : 0);
       const int64_t row = static_cast<int64_t>(slot) * tile_rows + r;
       const float2 v = *reinterpret_cast<const float2*>(ml + row * 2);
       const float a = m == -INFINITY ? 1.0f : exp2_approx(v.x - m);
@@ -840,7 +919,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnJob p
         acc[j] += a * x.x, acc[j + 1] += a * x.y;
       }
     }
-    const int rr = w.t.row0 + r, tok = rr / p.group, head = w.h * p.group + rr - tok * p.group;
+    const int rr = w.t.row0 + r, tok = div_by(p.by_group, rr), head = w.h * p.group + rr - tok * p.group;
     const int64_t row = w.s.tok0 + tok;
     const float inv = l == 0.f ? 0.f : (p.v_scale ? __ldg(p.v_scale + w.h) : 1.0f) / l;
     uint32_t* o = reinterpret_cast<uint32_t*>(p.out + row * p.out_stride + static_cast<int64_t>(head) * kDim) + lane * (kPer / 2);
@@ -867,12 +946,12 @@ inline AttnShape attn_shape(int dim, bool fp8, int64_t rows) {
 }
 
 template <int kDim>
-nvfp4_status launch_attn_join(const AttnJob& p, int tile_rows, int keys, cudaStream_t stream) {
+nvfp4_status launch_attn_join(const AttnJob& p, const Tiling& g, cudaStream_t stream) {
   // one unit an item: nothing can be split
-  if ((static_cast<int64_t>(p.max_pages) << p.page_log2) > keys) {
-    const int rows = tile_rows / 4 < 16 ? tile_rows / 4 : 16;
+  if ((static_cast<int64_t>(p.max_pages) << p.page_log2) > g.keys) {
+    const int rows = g.rows / 4 < 16 ? g.rows / 4 : 16;
     if (launch_pdl(attn_join_kernel<kDim>, dim3(kAttnGrid - 1, rows), dim3(kJoinThreads), 0, stream, p, kAttnGrid,
-                   tile_rows, keys) != cudaSuccess)
+                   g) != cudaSuccess)
       return NVFP4_ERR_CUDA;
   }
   return launched();
@@ -885,7 +964,7 @@ nvfp4_status launch_attn_split(const AttnJob& p, const KvMaps& maps, cudaStream_
   if (launch_pdl(attn_split_kernel<kDim, kFp8, kRW, kKW>, dim3(kAttnGrid), dim3(T::kThreadsAll), T::kSmem, stream, p,
                  maps) != cudaSuccess)
     return NVFP4_ERR_CUDA;
-  return launch_attn_join<kDim>(p, T::kRows, T::kKeys, stream);
+  return launch_attn_join<kDim>(p, Tiling{T::kRows, T::kKeys, T::kOver}, stream);
 }
 
 // The split and join grids for heads of kDim values (attention_d*.cu).

@@ -36,6 +36,7 @@ struct ChunkTile {
   static constexpr int kRows = 128 * kGroups;
   static constexpr int kKeys = kDim == 256 ? 64 : 128;
   static constexpr int kSBuf = kDim == 256 ? 2 : 1;        // S buffers per group
+  static constexpr int kOver = 3;                          // an item's own cost, in units
   static constexpr int kThreadsAll = 128 + 128 * kGroups;
   static constexpr int kEl = kFp8 ? 1 : 2;
   // boxes of the pool (as AttnTile names them, for tile_offset)
@@ -73,6 +74,8 @@ __device__ __forceinline__ constexpr uint32_t umma_idesc(bool bf16, bool b_mn, i
   return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u) |
          (static_cast<uint32_t>(n / 8) << 17) | (static_cast<uint32_t>(m / 16) << 24);
 }
+
+constexpr uint32_t kNegateA = 1u << 13;
 
 __device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
   asm volatile(
@@ -140,6 +143,13 @@ __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
+// 32 bytes to a 32-byte aligned address: a whole sector a thread.
+__device__ __forceinline__ void stg256(void* p, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+               "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 // Byte offset of 16-byte chunk c of row r in a 16-bit tile of `rows` rows of 128 bytes
 // per block of 64 values.
 __device__ __forceinline__ uint32_t umma_offset(int rows, int r, int c) {
@@ -168,8 +178,8 @@ struct KeyRange {
 
 __device__ __forceinline__ KeyRange key_range(const AttnJob& p, const Walk& w) {
   KeyRange r;
-  const int first = w.s.len - w.s.n + w.t.row0 / p.group;
-  const int last = w.s.len - w.s.n + (w.t.row0 + w.t.rows - 1) / p.group;
+  const int first = w.s.len - w.s.n + div_by(p.by_group, w.t.row0);
+  const int last = w.s.len - w.s.n + div_by(p.by_group, w.t.row0 + w.t.rows - 1);
   r.all_hi = min(first + 1, w.s.len);
   r.all_lo = p.window > 0 ? last - p.window + 1 : 0;
   r.any_hi = w.t.hi;
@@ -228,18 +238,15 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
   tc_fence_after();
   const uint32_t tmem = *static_cast<volatile uint32_t*>(&bars->tmem);
 
+  constexpr Tiling kTiling{T::kRows, T::kKeys, T::kOver};
   Found f;
-  int grid = 0;
-  const long long total = scan_units<T::kThreadsAll>(p, T::kRows, kKeys, &f, bars->scratch, [&](long long all) {
-    grid = static_cast<int>(min(static_cast<long long>(gridDim.x), all));
-    return static_cast<int>(blockIdx.x) < grid ? range_start(blockIdx.x, all, grid) : -1;
-  });
-  const bool idle = static_cast<int>(blockIdx.x) >= grid;
-  const long long u0 = idle ? 0 : range_start(blockIdx.x, total, grid);
-  const long long u1 = idle ? 0 : range_start(blockIdx.x + 1, total, grid);
+  Ranges ranges;
+  find_range<T::kThreadsAll>(p, kTiling, gridDim.x, blockIdx.x, &ranges, &f, bars->scratch);
+  const bool idle = static_cast<int>(blockIdx.x) >= ranges.grid;
+  const long long u0 = idle ? 0 : ranges.start(blockIdx.x), u1 = idle ? 0 : ranges.start(blockIdx.x + 1);
   Walk w;
   w.b = f.seq, w.item0 = f.before;
-  if (!idle) walk_seq(p, w, T::kRows, kKeys);
+  if (!idle) walk_seq(p, w, kTiling);
   bool ran_out = false;  // a wait reached its limit (recorded): no further waits, the roles stay in step
 #define NVFP4_WAIT(bar, parity) ran_out = ran_out || !mbar_wait_warp(bar, parity)
 
@@ -253,9 +260,11 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
       const int boxes = kKeys / box_rows;
       uint32_t raw = 0;
       for (long long u = u0; u < u1;) {
-        walk_to(p, w, u, T::kRows, kKeys);
-        const int first = w.t.tile0 + static_cast<int>(u - w.item0);
-        const int n = static_cast<int>(min(w.item0 + w.t.units - u, u1 - u));
+        walk_to(p, w, u, kTiling);
+        const Share pc = share_at(w, u, u0, u1, blockIdx.x, kTiling);
+        u = pc.end;
+        if (pc.n == 0) continue;
+        const int first = pc.first, n = pc.n;
         const int32_t* table = p.table + static_cast<int64_t>(w.b) * p.max_pages;
         // order: K 0, then K j + 1 and V j
         for (int c = 0; c < 2 * n; ++c) {
@@ -300,11 +309,11 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
           }
         }
         nt += n;
-        u += n;
       }
     } else if (warp == 1) {
       // ------------------------------------------------------------ MMA issue
-      const uint32_t id_qk = umma_idesc(!kFp8, false, kKeys, 128), id_pv = umma_idesc(!kFp8, true, kDim, 128);
+      const uint32_t id_qk = umma_idesc(!kFp8, false, kKeys, 128) | (p.scale < 0.f ? kNegateA : 0u);
+      const uint32_t id_pv = umma_idesc(!kFp8, true, kDim, 128);
       uint32_t nq[2] = {0, 0}, np[2] = {0, 0};  // completed hand-overs of Q and P per group (or P per S buffer)
       const auto qk = [&](int g, uint32_t t) {
         const uint32_t d = tmem + T::kSCol + (kG == 2 ? g : (t & 1)) * kKeys;
@@ -333,8 +342,11 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
         NVFP4_WAIT((kFp8 ? bars->k_ready : bars->k_full) + (t & 1), (t >> 1) & 1);
       };
       for (long long u = u0; u < u1;) {
-        walk_to(p, w, u, T::kRows, kKeys);
-        const int n = static_cast<int>(min(w.item0 + w.t.units - u, u1 - u));
+        walk_to(p, w, u, kTiling);
+        const Share pc = share_at(w, u, u0, u1, blockIdx.x, kTiling);
+        u = pc.end;
+        if (pc.n == 0) continue;
+        const int n = pc.n;
         const int groups = kG == 2 && w.t.rows > 128 ? 2 : 1;
         for (int g = 0; g < groups; ++g) {
           NVFP4_WAIT(bars->q_full + g, nq[g] & 1);
@@ -369,16 +381,17 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
           }
         }
         nt += n;
-        u += n;
       }
     } else {
       // ------------------------------------------------------------ tiles made fit
       const int who = (warp - 2) * 32 + lane;
       uint32_t raw = 0;
       for (long long u = u0; u < u1;) {
-        walk_to(p, w, u, T::kRows, kKeys);
-        const int first = w.t.tile0 + static_cast<int>(u - w.item0);
-        const int n = static_cast<int>(min(w.item0 + w.t.units - u, u1 - u));
+        walk_to(p, w, u, kTiling);
+        const Share pc = share_at(w, u, u0, u1, blockIdx.x, kTiling);
+        u = pc.end;
+        if (pc.n == 0) continue;
+        const int first = pc.first, n = pc.n;
         const KeyRange kr = key_range(p, w);
         bool noted = false;
         if constexpr (!kFp8) {
@@ -437,7 +450,6 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
           }
         }
         nt += n;
-        u += n;
       }
     }
   } else {
@@ -450,62 +462,82 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
     const float log2e = 1.4426950408889634f;
     const float kOffset = kFp8 ? 7.0f : 0.0f;
     uint32_t mine = 0;  // this group's tiles so far
+    // Q of this thread's row of the walk's item: copied as it is into the tile that the
+    // products with K read
+    const auto fetch_q = [&](const Walk& o) {
+      const int r = g * 128 + row;
+      const int rr = o.t.row0 + min(r, o.t.rows - 1);
+      const int tok = div_by(p.by_group, rr), head = o.h * p.group + rr - tok * p.group;
+      const uint16_t* q = p.q + (o.s.tok0 + tok) * p.q_stride + static_cast<int64_t>(head) * kDim;
+      const uint32_t bytes = r < o.t.rows ? 16 : 0;  // rows past the tile's last one: zeros
+#pragma unroll 8
+      for (int c = 0; c < kDim / 8; ++c)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(q_at + g * T::kQB + umma_offset(128, row, c)),
+                     "l"(q + 8 * c), "r"(bytes)
+                     : "memory");
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    // hands the copied tile over; for an E4M3 cache scaled by a power of two into f16's range.
+    // Returns the factor that undoes the scaling.
+    const auto hand_q = [&]() {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      float back = 1.0f;
+      if constexpr (kFp8) {
+        float amax = 0.f;
+#pragma unroll 8
+        for (int c = 0; c < kDim / 8; ++c) {
+          const uint4 v = lds128(q_at + g * T::kQB + umma_offset(128, row, c));
+          const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(x[i] << 16)), fabsf(__uint_as_float(x[i] & 0xffff0000u))));
+        }
+        const int e = pow2_rescale_exponent(amax);
+        const float up = exp2i(e);
+        back = exp2i(-e);
+#pragma unroll 8
+        for (int c = 0; c < kDim / 8; ++c) {
+          const uint32_t at = q_at + g * T::kQB + umma_offset(128, row, c);
+          const uint4 v = lds128(at);
+          uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            x[i] = f32x2_to_f16x2(__uint_as_float(x[i] << 16) * up, __uint_as_float(x[i] & 0xffff0000u) * up);
+          sts128(at, make_uint4(x[0], x[1], x[2], x[3]));
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars->q_full + g);
+      return back;
+    };
+
+    float qscale = 1.0f;
+    bool ready = false;  // Q of the walk's item has been handed over already
     for (long long u = u0; u < u1;) {
-      walk_to(p, w, u, T::kRows, kKeys);
-      const int first = w.t.tile0 + static_cast<int>(u - w.item0);
-      const int n = static_cast<int>(min(w.item0 + w.t.units - u, u1 - u));
+      walk_to(p, w, u, kTiling);
+      const Share pc = share_at(w, u, u0, u1, blockIdx.x, kTiling);
+      u = pc.end;
+      if (pc.n == 0) continue;
+      const int first = pc.first, n = pc.n;
       if (g * 128 >= w.t.rows) {  // this group has no rows here
-        nt += n, u += n;
+        nt += n;
         continue;
       }
+      if (!ready) {
+        fetch_q(w);
+        qscale = hand_q();
+      }
+      ready = false;
       const int r = g * 128 + row;
       const bool live = r < w.t.rows;
       const int rr = w.t.row0 + min(r, w.t.rows - 1);
-      const int tok = rr / p.group, head = w.h * p.group + rr - tok * p.group;
+      const int tok = div_by(p.by_group, rr), head = w.h * p.group + rr - tok * p.group;
       const int pos = w.s.len - w.s.n + tok;
       const int64_t token = w.s.tok0 + tok;
-
-      // ---- Q of this row to shared memory (scaled into f16's range for an E4M3 cache;
-      // a negative scale turns its sign, a zero one makes it zero)
-      float qscale = 1.0f;
-      {
-        const uint16_t* q = p.q + token * p.q_stride + static_cast<int64_t>(head) * kDim;
-        const uint32_t sign = p.scale < 0.f ? 0x80008000u : 0u;
-        const bool zero = !live || p.scale == 0.f;
-        float up = 1.0f;
-        if constexpr (kFp8) {
-          float amax = 0.f;
-#pragma unroll 8
-          for (int c = 0; c < kDim / 8; ++c) {
-            const uint4 v = zero ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(q + 8 * c);
-            const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(x[i] << 16)), fabsf(__uint_as_float(x[i] & 0xffff0000u))));
-          }
-          const int e = pow2_rescale_exponent(amax);
-          up = exp2i(e);
-          qscale = exp2i(-e);
-        }
-#pragma unroll 8
-        for (int c = 0; c < kDim / 8; ++c) {
-          uint4 v = zero ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(q + 8 * c);
-          uint32_t x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            x[i] ^= sign;
-            if constexpr (kFp8)
-              x[i] = f32x2_to_f16x2(__uint_as_float(x[i] << 16) * up, __uint_as_float(x[i] & 0xffff0000u) * up);
-          }
-          sts128(q_at + g * T::kQB + umma_offset(128, row, c), make_uint4(x[0], x[1], x[2], x[3]));
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bars->q_full + g);
-      }
       const float ks = (kFp8 && p.k_scale) ? __ldg(p.k_scale + w.h) : 1.0f;
       const bool capped = p.softcap > 0.f;
-      const float scale = p.scale == 0.f ? 1.0f : fabsf(p.scale);
+      const float scale = fabsf(p.scale);  // its sign is in the product
       // logits in units of log 2: s * mul; with a softcap, cap2 * tanh(s * unit)
       const float unit = scale * ks * qscale * (capped ? 1.0f / p.softcap : log2e);
       const float mul = capped ? 1.0f : fmaxf(unit, 1.2e-38f);  // (-inf * 0 would be NaN)
@@ -525,6 +557,10 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
         for (int c = 0; c < kKeys; c += 32) tmem_ld32(s + c, s_at + c);
         tmem_loaded(s);
         const int key0 = (first + j) * kKeys;
+        if (p.scale == 0.f) {
+#pragma unroll
+          for (int c = 0; c < kKeys; ++c) s[c] = 0.f;
+        }
         if (capped) {
 #pragma unroll
           for (int c = 0; c < kKeys; ++c)
@@ -582,16 +618,30 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
       }
       nt += n;
 
+      // ---- the next item's Q while the last product with V runs (all products with this
+      // item's Q are done: their last S has been read)
+      Walk next = w;
+      bool more = false;
+      for (long long v = u; v < u1 && !more;) {
+        walk_to(p, next, v, kTiling);
+        const Share q = share_at(next, v, u0, u1, blockIdx.x, kTiling);
+        more = q.n > 0;
+        v = q.end;
+      }
+      more = more && g * 128 < next.t.rows;
+      if (more) fetch_q(next);
+
       // ---- write: the finished row, or this piece's share of it
       if constexpr (kG == 2)
         NVFP4_WAIT(bars->o_full + g, (mine - 1) & 1);
       else
         NVFP4_WAIT(bars->o_full + ((nt - 1) & 1), ((nt - 1) >> 1) & 1);
       tc_fence_after();
-      const bool whole = n == w.t.units;
-      const int slot = 2 * blockIdx.x + (u == u0 ? 0 : 1);
+      const bool whole = pc.whole;
+      const int slot = pc.slot;
       const float vs = (kFp8 && p.v_scale) ? __ldg(p.v_scale + w.h) : 1.0f;
       const float inv = !whole ? 1.0f : (l == 0.f ? 0.f : vs / l);
+      const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0 && (p.out_stride & 15) == 0;
       uint16_t* out = p.out + token * p.out_stride + static_cast<int64_t>(head) * kDim;
       float* part = p.part + (static_cast<int64_t>(slot) * T::kRows + r) * kDim;
       const bool noted = *static_cast<volatile int*>(&bars->noted) != 0;
@@ -632,17 +682,27 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
             }
           }
         }
+        if (c == 0 && more) {  // the next item's first product may start
+          tc_fence_before();
+          qscale = hand_q();
+          ready = true;
+        }
         if (!live) continue;
         if (whole) {
+          uint32_t x[16];
 #pragma unroll
-          for (int i = 0; i < 32; i += 8)
-            *reinterpret_cast<uint4*>(out + c + i) =
-                make_uint4(f32x2_to_bf16x2(o[i] * inv, o[i + 1] * inv), f32x2_to_bf16x2(o[i + 2] * inv, o[i + 3] * inv),
-                           f32x2_to_bf16x2(o[i + 4] * inv, o[i + 5] * inv), f32x2_to_bf16x2(o[i + 6] * inv, o[i + 7] * inv));
+          for (int i = 0; i < 16; ++i) x[i] = f32x2_to_bf16x2(o[2 * i] * inv, o[2 * i + 1] * inv);
+          if (wide) {
+            stg256(out + c, x);
+            stg256(out + c + 16, x + 8);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+              *reinterpret_cast<uint4*>(out + c + 2 * i) = make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+          }
         } else {
 #pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<float4*>(part + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          for (int i = 0; i < 32; i += 8) stg256(part + c + i, reinterpret_cast<const uint32_t*>(o) + i);
         }
       }
       if (live) {
@@ -654,7 +714,6 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
         }
       }
       tc_fence_before();  // O has been read before the next item's first P is handed over
-      u += n;
     }
   }
 #undef NVFP4_WAIT
@@ -676,7 +735,7 @@ nvfp4_status launch_attn_chunk(const AttnJob& p, const KvMaps& maps, const void*
   if (launch_pdl(attn_chunk_kernel<kDim, kFp8>, dim3(kAttnGrid), dim3(T::kThreadsAll), T::kSmem, stream, p, maps,
                  v_pool, page_stride) != cudaSuccess)
     return NVFP4_ERR_CUDA;
-  return launch_attn_join<kDim>(p, T::kRows, T::kKeys, stream);
+  return launch_attn_join<kDim>(p, Tiling{T::kRows, T::kKeys, T::kOver}, stream);
 }
 
 }  // namespace nvfp4
