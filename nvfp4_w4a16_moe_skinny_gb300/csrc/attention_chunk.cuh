@@ -95,6 +95,15 @@ __device__ __forceinline__ void umma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
                : "memory");
 }
+// One lane of a converged warp, chosen by the hardware: unlike a lane test it leaves the
+// branch uniform, so that descriptors stay in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+  return ok != 0;
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
@@ -214,7 +223,7 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
   static_assert(sizeof(ChunkBars) <= 1024, "barriers");
   const uint32_t q_at = base, k_at = base + T::kRing, v_at = k_at + 2 * T::kTileB, raw_at = base + T::kRaw;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = static_cast<int>(uniform(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(bars->k_full + i, 1), mbar_init(bars->k_ready + i, 2), mbar_init(bars->k_empty + i, 1);
@@ -236,7 +245,7 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
   pdl_launch_dependents();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *static_cast<volatile uint32_t*>(&bars->tmem);
+  const uint32_t tmem = uniform(*static_cast<volatile uint32_t*>(&bars->tmem));
 
   constexpr Tiling kTiling{T::kRows, T::kKeys, T::kOver};
   Found f;
@@ -315,27 +324,34 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
       const uint32_t id_qk = umma_idesc(!kFp8, false, kKeys, 128) | (p.scale < 0.f ? kNegateA : 0u);
       const uint32_t id_pv = umma_idesc(!kFp8, true, kDim, 128);
       uint32_t nq[2] = {0, 0}, np[2] = {0, 0};  // completed hand-overs of Q and P per group (or P per S buffer)
+      // descriptors: the start address is the low 14 bits, in units of 16 bytes
+      const uint64_t q_desc = umma_desc(q_at, 16, 1024), k_desc = umma_desc(k_at, 16, 1024);
+      const uint64_t v_desc = umma_desc(v_at, kKeys * 128, 1024);
       const auto qk = [&](int g, uint32_t t) {
         const uint32_t d = tmem + T::kSCol + (kG == 2 ? g : (t & 1)) * kKeys;
-        const uint32_t a = q_at + g * T::kQB, b = k_at + (t & 1) * T::kTileB;
-        if (lane == 0) {
+        const uint64_t a = q_desc + g * (T::kQB >> 4), b = k_desc + (t & 1) * (T::kTileB >> 4);
+        if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < kDim / 16; ++k)
-            umma_ss(d, umma_desc(a + (k >> 2) * (128 * 128) + (k & 3) * 32, 16, 1024),
-                    umma_desc(b + (k >> 2) * (kKeys * 128) + (k & 3) * 32, 16, 1024), id_qk, k > 0);
+            umma_ss(d, a + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4),
+                    b + (((k >> 2) * (kKeys * 128) + (k & 3) * 32) >> 4), id_qk, k > 0);
           umma_commit(bars->s_full + (kG == 2 ? g : (t & 1)));
         }
         __syncwarp();
       };
       const auto pv = [&](int g, uint32_t t, bool add) {
         const uint32_t a = tmem + T::kSCol + (kG == 2 ? g : (t & 1)) * kKeys;
-        const uint32_t b = v_at + (t & 1) * T::kTileB;
-        if (lane == 0) {
+        const uint64_t b = v_desc + (t & 1) * (T::kTileB >> 4);
+        if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < kKeys / 16; ++k)
-            umma_ts(tmem + g * kDim, a + 8 * k, umma_desc(b + k * 2048, kKeys * 128, 1024), id_pv, add || k > 0);
+            umma_ts(tmem + g * kDim, a + 8 * k, b + k * (2048 >> 4), id_pv, add || k > 0);
           umma_commit(bars->o_full + (kG == 2 ? g : (t & 1)));
         }
+        __syncwarp();
+      };
+      const auto free_tile = [&](uint64_t* bar) {
+        if (elect_one()) umma_commit(bar);
         __syncwarp();
       };
       const auto wait_k = [&](uint32_t t) {
@@ -345,9 +361,9 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
         walk_to(p, w, u, kTiling);
         const Share pc = share_at(w, u, u0, u1, blockIdx.x, kTiling);
         u = pc.end;
-        if (pc.n == 0) continue;
-        const int n = pc.n;
-        const int groups = kG == 2 && w.t.rows > 128 ? 2 : 1;
+        const int n = static_cast<int>(uniform(pc.n));
+        if (n == 0) continue;
+        const int groups = kG == 2 && uniform(w.t.rows) > 128 ? 2 : 1;
         for (int g = 0; g < groups; ++g) {
           NVFP4_WAIT(bars->q_full + g, nq[g] & 1);
           ++nq[g];
@@ -355,14 +371,14 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
         wait_k(nt);
         tc_fence_after();
         for (int g = 0; g < groups; ++g) qk(g, nt);
-        if (lane == 0) umma_commit(bars->k_empty + (nt & 1));
+        free_tile(bars->k_empty + (nt & 1));
         for (int j = 0; j < n; ++j) {
           const uint32_t t = nt + j;
           if (kG == 1 && j + 1 < n) {
             wait_k(t + 1);
             tc_fence_after();
             qk(0, t + 1);
-            if (lane == 0) umma_commit(bars->k_empty + ((t + 1) & 1));
+            free_tile(bars->k_empty + ((t + 1) & 1));
           }
           NVFP4_WAIT(bars->v_ready + (t & 1), (t >> 1) & 1);
           if constexpr (!kFp8) NVFP4_WAIT(bars->v_full + (t & 1), (t >> 1) & 1);
@@ -375,10 +391,8 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
             pv(g, t, j > 0);
             if (kG == 2 && j + 1 < n) qk(g, t + 1);
           }
-          if (lane == 0) {
-            umma_commit(bars->v_empty + (t & 1));
-            if (kG == 2 && j + 1 < n) umma_commit(bars->k_empty + ((t + 1) & 1));
-          }
+          free_tile(bars->v_empty + (t & 1));
+          if (kG == 2 && j + 1 < n) free_tile(bars->k_empty + ((t + 1) & 1));
         }
         nt += n;
       }
