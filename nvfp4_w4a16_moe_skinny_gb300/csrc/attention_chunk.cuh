@@ -159,6 +159,31 @@ __device__ __forceinline__ void stg256(void* p, const uint32_t* r) {
                : "memory");
 }
 
+// Pairs of floats in one 64-bit register: one instruction for two fp32 operations.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pack2(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float lo2(f32x2 v) { return __uint_as_float(static_cast<uint32_t>(v)); }
+__device__ __forceinline__ float hi2(f32x2 v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // Byte offset of 16-byte chunk c of row r in a 16-bit tile of `rows` rows of 128 bytes
 // per block of 64 values.
 __device__ __forceinline__ uint32_t umma_offset(int rows, int r, int c) {
@@ -171,7 +196,8 @@ struct ChunkBars {
   uint64_t v_full[2], v_ready[2], v_empty[2];
   uint64_t raw_full[2], raw_empty[2];
   uint64_t q_full[2];
-  uint64_t s_full[2], p_full[2];  // one per group, or per S buffer
+  uint64_t s_full[2];             // one per group, or per S buffer
+  uint64_t p_full[2][2];          // the same, for each half of the keys
   uint64_t o_full[2];             // products with V done: one per group, or in turn
   long long scratch[36];
   uint32_t tmem;
@@ -229,7 +255,8 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
       mbar_init(bars->k_full + i, 1), mbar_init(bars->k_ready + i, 2), mbar_init(bars->k_empty + i, 1);
       mbar_init(bars->v_full + i, 1), mbar_init(bars->v_ready + i, 2), mbar_init(bars->v_empty + i, 1);
       mbar_init(bars->raw_full + i, 1), mbar_init(bars->raw_empty + i, 2);
-      mbar_init(bars->q_full + i, 4), mbar_init(bars->s_full + i, 1), mbar_init(bars->p_full + i, 4);
+      mbar_init(bars->q_full + i, 4), mbar_init(bars->s_full + i, 1);
+      mbar_init(&bars->p_full[i][0], 4), mbar_init(&bars->p_full[i][1], 4);
       mbar_init(bars->o_full + i, 1);
     }
     bars->noted = 0;
@@ -339,14 +366,16 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
         }
         __syncwarp();
       };
-      const auto pv = [&](int g, uint32_t t, bool add) {
+      const auto pv = [&](int g, uint32_t t, int half, bool add) {
         const uint32_t a = tmem + T::kSCol + (kG == 2 ? g : (t & 1)) * kKeys;
         const uint64_t b = v_desc + (t & 1) * (T::kTileB >> 4);
         if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < kKeys / 16; ++k)
-            umma_ts(tmem + g * kDim, a + 8 * k, b + k * (2048 >> 4), id_pv, add || k > 0);
-          umma_commit(bars->o_full + (kG == 2 ? g : (t & 1)));
+          for (int i = 0; i < kKeys / 32; ++i) {
+            const int k = half * (kKeys / 32) + i;
+            umma_ts(tmem + g * kDim, a + 8 * k, b + k * (2048 >> 4), id_pv, add || i > 0);
+          }
+          if (half == 1) umma_commit(bars->o_full + (kG == 2 ? g : (t & 1)));
         }
         __syncwarp();
       };
@@ -385,10 +414,13 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
           if (kG == 2 && j + 1 < n) wait_k(t + 1);
           for (int g = 0; g < groups; ++g) {
             const int pb = kG == 2 ? g : (t & 1);
-            NVFP4_WAIT(bars->p_full + pb, np[pb] & 1);
+            NVFP4_WAIT(&bars->p_full[pb][0], np[pb] & 1);
+            tc_fence_after();
+            pv(g, t, 0, j > 0);
+            NVFP4_WAIT(&bars->p_full[pb][1], np[pb] & 1);
             ++np[pb];
             tc_fence_after();
-            pv(g, t, j > 0);
+            pv(g, t, 1, true);
             if (kG == 2 && j + 1 < n) qk(g, t + 1);
           }
           free_tile(bars->v_empty + (t & 1));
@@ -587,7 +619,11 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
         }
         float top[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int c = 4; c < kKeys; ++c) top[c & 3] = fmaxf(top[c & 3], s[c]);
+        for (int c = 4; c + 8 <= kKeys; c += 8)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) top[i] = max3(top[i], s[c + i], s[c + 4 + i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top[i] = fmaxf(top[i], s[kKeys - 4 + i]);
         const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * mul - kOffset;
         const bool move = high > m + 8.0f || m == -INFINITY;
         if (__any_sync(0xffffffffu, move && j > 0 && high > m)) {
@@ -611,24 +647,30 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
         }
         if (move && high > m) m = high;
         const float ref = m == -INFINITY ? 0.f : m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        // weights, handed over in two halves: the product with V starts on the first one
+        const f32x2 mul2 = pack2(mul, mul), ref2 = pack2(-ref, -ref);
+        f32x2 sum[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
 #pragma unroll
-        for (int c = 0; c < kKeys; c += 32) {
-          uint32_t pk[16];
+        for (int half = 0; half < 2; ++half) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float a = exp2_approx(fmaf(s[c + 2 * i], mul, -ref));
-            const float b = exp2_approx(fmaf(s[c + 2 * i + 1], mul, -ref));
-            sum[i & 3] += a + b;
-            pk[i] = kFp8 ? f32x2_to_f16x2(a, b) : f32x2_to_bf16x2(a, b);
+          for (int c = half * kKeys / 2; c < (half + 1) * kKeys / 2; c += 32) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const f32x2 e = fma2(pack2(s[c + 2 * i], s[c + 2 * i + 1]), mul2, ref2);
+              const float a = exp2_approx(lo2(e)), b = exp2_approx(hi2(e));
+              sum[i & 1] = add2(sum[i & 1], pack2(a, b));
+              pk[i] = kFp8 ? f32x2_to_f16x2(a, b) : f32x2_to_bf16x2(a, b);
+            }
+            tmem_st16(s_at + c / 2, pk);
           }
-          tmem_st16(s_at + c / 2, pk);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->p_full[sb][half]);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bars->p_full + sb);
+        const f32x2 both = add2(sum[0], sum[1]);
+        l += lo2(both) + hi2(both);
       }
       nt += n;
 
