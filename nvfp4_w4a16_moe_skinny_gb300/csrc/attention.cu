@@ -7,24 +7,25 @@
 namespace nvfp4 {
 namespace {
 
-// Tensor map of one pool: [num_pages, n_kv_heads, page_size, head_dim] in boxes of one
-// head's `box_rows` consecutive keys by 128 bytes (or the whole row, if shorter),
-// swizzled so that eight rows of a 16-byte column fall into eight banks groups.
-bool encode_pool_map(CUtensorMap* map, const nvfp4_kv_cache* c, void* base, int box_rows) {
+// Tensor map of one pool, [num_pages, n_kv_heads, page_size, head_dim], whose rows are
+// seen as blocks of 128 bytes (or one shorter block): boxes of one head's `box_rows`
+// consecutive keys by one block, or by all blocks of the row.  Swizzled, so that eight
+// rows of a 16-byte column fall into eight different groups of banks.
+bool encode_pool_map(CUtensorMap* map, const nvfp4_kv_cache* c, void* base, int box_rows, bool whole_rows) {
   const EncodeTiledFn fn = encode_tiled();
   if (!fn) return false;
   const bool fp8 = c->dtype == NVFP4_KV_E4M3;
-  const cuuint64_t el = fp8 ? 1 : 2;
-  const int row = std::min<int>(128, c->head_dim * static_cast<int>(el));
-  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c->head_dim), static_cast<cuuint64_t>(c->page_size),
+  const cuuint64_t el = fp8 ? 1 : 2, row = c->head_dim * el, block = std::min<cuuint64_t>(128, row);
+  const cuuint64_t dims[5] = {block / el, static_cast<cuuint64_t>(c->page_size), row / block,
                               static_cast<cuuint64_t>(c->n_kv_heads), static_cast<cuuint64_t>(c->num_pages)};
-  const cuuint64_t strides[3] = {c->head_dim * el, static_cast<cuuint64_t>(c->page_size) * c->head_dim * el,
+  const cuuint64_t strides[4] = {row, block, static_cast<cuuint64_t>(c->page_size) * row,
                                  static_cast<cuuint64_t>(c->page_stride) * el};
-  const cuuint32_t box[4] = {static_cast<cuuint32_t>(row / el), static_cast<cuuint32_t>(box_rows), 1, 1};
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  return fn(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box,
+  const cuuint32_t box[5] = {static_cast<cuuint32_t>(block / el), static_cast<cuuint32_t>(box_rows),
+                             whole_rows ? static_cast<cuuint32_t>(row / block) : 1, 1, 1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return fn(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, base, dims, strides, box,
             estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            row == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            block == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -49,7 +50,7 @@ extern "C" {
 size_t paged_attention_workspace_bytes(int32_t n_tokens, int32_t n_seqs, int32_t max_new, int32_t n_heads,
                                        int32_t n_kv_heads, int32_t head_dim) {
   if (!sizes_ok(n_tokens, n_seqs, max_new, n_heads, n_kv_heads, head_dim)) return 0;
-  const AttnShape s = attn_shape(head_dim, false, packed_rows(n_tokens, max_new, n_heads, n_kv_heads));
+  const AttnShape s = attn_shape(head_dim, packed_rows(n_tokens, max_new, n_heads, n_kv_heads));
   return static_cast<size_t>(2) * kAttnGrid * s.tile_rows * (head_dim + 2) * sizeof(float);
 }
 
@@ -83,11 +84,10 @@ nvfp4_status paged_attention(const nvfp4_kv_cache* cache, const nvfp4_batch* bat
   p.k_scale = cache->k_scale, p.v_scale = cache->v_scale;
   p.scale = scale, p.softcap = softcap, p.window = window;
   p.part = static_cast<float*>(ws);
-  const bool fp8 = cache->dtype == NVFP4_KV_E4M3;
-  const AttnShape s = attn_shape(dim, fp8, packed_rows(n_tokens, batch->max_new, n_heads, kv));
+  const AttnShape s = attn_shape(dim, packed_rows(n_tokens, batch->max_new, n_heads, kv));
   KvMaps maps;
   const int box = std::min(cache->page_size, s.box_keys);
-  if (!encode_pool_map(&maps.k, cache, cache->k, box) || !encode_pool_map(&maps.v, cache, cache->v, box))
+  if (!encode_pool_map(&maps.k, cache, cache->k, box, !s.chunk) || !encode_pool_map(&maps.v, cache, cache->v, box, !s.chunk))
     return NVFP4_ERR_CUDA;
   if (dim == 64) return dispatch_attention<64>(p, maps, cache, s, stream);
   if (dim == 128) return dispatch_attention<128>(p, maps, cache, s, stream);

@@ -363,14 +363,25 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return r;
 }
 
-__device__ __forceinline__ void tma_load_4d_plain(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
-                                                  uint32_t bar) {
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3, int c4,
+                                            uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar)
       : "memory");
 }
+
+// One lane of a converged warp, chosen by the hardware: unlike a lane test it leaves the
+// branch uniform, so that descriptors and addresses stay in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+  return ok != 0;
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+__host__ __device__ constexpr int log2c(int v) { return v <= 1 ? 0 : 1 + log2c(v / 2); }
 
 // Halves of packed 16-bit values that are infinite or NaN, as a mask of 0xffff.
 template <bool kF16>
@@ -382,42 +393,58 @@ __device__ __forceinline__ uint32_t nonfinite_mask(uint32_t v) {
 
 // ------------------------------------------------------------------ tile geometry
 
-// Keys of one warp's step (the rows of a TMA box are min(page, slice)): as many as keep
-// a stage of the ring at 64 KB or less and the scores in few registers.
-__host__ __device__ constexpr int attn_slice(int dim, bool fp8, int kw) {
+// Keys of one warp's step: as many as keep the scores in few registers.
+__host__ __device__ constexpr int attn_slice(int dim, int kw) {
   if (kw == 1) return dim == 256 ? 32 : 64;
-  return dim == 256 || (dim == 128 && !fp8 && kw == 8) ? 16 : 32;
+  return dim == 256 ? 16 : 32;
 }
 
 template <int kDim, bool kFp8, int kRW, int kKW>
 struct AttnTile {
   static constexpr int kRows = 16 * kRW;
-  static constexpr int kSlice = attn_slice(kDim, kFp8, kKW);                           // keys of a warp's step
-  static constexpr int kKeys = kSlice * kKW;                                           // keys of a unit
+  static constexpr int kSlice = attn_slice(kDim, kKW);               // keys of a warp's step
+  static constexpr int kKeys = kSlice * kKW;                         // keys of a unit
   static constexpr int kConsumers = kRW * kKW;
   static constexpr int kThreadsAll = (kConsumers + 1) * 32;
-  static constexpr int kOver = 1;                                                       // an item's own cost, in units
+  static constexpr int kOver = 1;                                    // an item's own cost, in units
   static constexpr int kEl = kFp8 ? 1 : 2;
-  static constexpr int kRowB = kDim * kEl < 128 ? kDim * kEl : 128;  // bytes of a row of a box
-  static constexpr int kSub = kDim * kEl / kRowB;                    // boxes across a head
+  static constexpr int kRowB = kDim * kEl < 128 ? kDim * kEl : 128;  // bytes of a row of a block
+  static constexpr int kSub = kDim * kEl / kRowB;                    // blocks across a head
   static constexpr uint32_t kSwz = kRowB == 128 ? 0x70 : 0x30;
-  static constexpr int kSubB = kSlice * kRowB;          // one box column of a slice
-  static constexpr int kSliceB = kSubB * kSub;          // K or V of a slice
-  static constexpr int kStageB = 2 * kSliceB * kKW;     // a unit's K and V
-  static constexpr int kJoinW = kKW > 4 ? 2 : kKW / 2;  // key slices that one round of the join hands over
-  static constexpr int kJoinB = kJoinW * kRW * 32 * (kDim / 2 + 4) * 4;
+  static constexpr int kTileB = kKeys * kDim * kEl;                  // K or V of a unit: page pieces of [kSub][rows][kRowB]
+  static constexpr int kStageB = 2 * kTileB;
+  static constexpr int kJoinB = (kKW / 2) * kRW * 32 * (kDim / 2 + 4) * 4;
   static constexpr int kFit = (227 * 1024 - 1024 - 1024 - kJoinB) / kStageB;
   static constexpr int kStages = kFit > 6 ? 6 : kFit;
   static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageB + kJoinB + 1024;
   static_assert(kStages >= 2, "ring too shallow");
 };
 
-// Byte offset of 16-byte chunk c of key row r in a slice (swizzled as the boxes are).
+// Byte offset of chunk c (16 bytes) of row r in a block of rows, swizzled as the boxes are.
 template <typename T>
-__device__ __forceinline__ uint32_t tile_offset(int r, int c) {
-  constexpr int per = T::kRowB / 16;
-  const uint32_t o = (c / per) * T::kSubB + r * T::kRowB + (c % per) * 16;
+__device__ __forceinline__ uint32_t swizzled(int r, int c) {
+  const uint32_t o = r * T::kRowB + c * 16;
   return o ^ ((o >> 3) & T::kSwz);
+}
+
+// Byte offset of the first block's row r (a multiple of 8) in a unit's K or V, which lies
+// there in page pieces of [kSub][1 << piece_log2][kRowB].
+template <typename T>
+__device__ __forceinline__ uint32_t rows_at(int r, int piece_log2) {
+  return r * T::kRowB + ((r >> piece_log2) * (T::kSub - 1) << piece_log2) * T::kRowB;
+}
+
+// The page of piece `piece` (1 << piece_log2 keys) of a sequence, or -1 if it holds no
+// key of the tile; a page id outside the pool becomes num_pages, a coordinate past the
+// tensor map's end, which reads as zeros.
+__device__ __forceinline__ int piece_page(const AttnJob& p, const int32_t* table, int piece, int piece_log2,
+                                          const RowTile& t) {
+  const int k = piece << piece_log2;
+  if (k >= t.hi || k + (1 << piece_log2) <= t.lo) return -1;  // holds no key of [lo, hi): not copied
+  const int page = __ldg(table + (k >> p.page_log2));
+  if (static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages)) return page;
+  atomicOr(&g_device_error, kErrPage);
+  return p.num_pages;
 }
 
 // ------------------------------------------------------------------ the split kernel
@@ -431,13 +458,13 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, 1
   const uint32_t ring = (raw + 1023u) & ~1023u;
   const uint32_t join = ring + T::kStages * T::kStageB;
   uint8_t* tail = smem_raw + (join + T::kJoinB - raw);
-  uint64_t* full = reinterpret_cast<uint64_t*>(tail);          // [stages][kKW]
-  uint64_t* empty = full + T::kStages * kKW;                   // [stages][kKW]
-  long long* scratch = reinterpret_cast<long long*>(empty + T::kStages * kKW);
+  uint64_t* full = reinterpret_cast<uint64_t*>(tail);  // [stages]
+  uint64_t* empty = full + T::kStages;                 // [stages]
+  long long* scratch = reinterpret_cast<long long*>(empty + T::kStages);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = static_cast<int>(uniform(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < T::kStages * kKW; ++i) mbar_init(full + i, 1), mbar_init(empty + i, kRW);
+    for (int i = 0; i < T::kStages; ++i) mbar_init(full + i, 1), mbar_init(empty + i, T::kConsumers);
     fence_mbar_init();
   }
   pdl_wait();
@@ -454,50 +481,43 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, 1
   w.b = f.seq, w.item0 = f.before;
   walk_seq(p, w, kTiling);
 
-  uint32_t step = 0;  // ring position, the same in every warp
   bool ran_out = false;  // a wait reached its limit (recorded): no further waits, the roles stay in step
   if (warp == T::kConsumers) {
     // -------------------------------------------------------------- producer
-    const int box_rows = min(1 << p.page_log2, T::kSlice);
-    const int boxes = T::kSlice / box_rows;              // page pieces of a slice
-    const int copies = boxes * T::kSub * 2;              // TMA copies of a slice
+    const int piece_log2 = min(p.page_log2, log2c(T::kKeys));
+    const int pieces = T::kKeys >> piece_log2;  // of a unit: at most 16
+    const uint32_t bytes = 2u << piece_log2 << log2c(kDim * T::kEl);
+    int st = 0;
+    uint32_t round = 0;
     for (long long u = u0; u < u1;) {
       walk_to(p, w, u, kTiling);
       const Share pc = share_at(w, u, u0, u1, blockIdx.x, kTiling);
       u = pc.end;
+      const int n = static_cast<int>(uniform(pc.n)), head = static_cast<int>(uniform(w.h));
       const int32_t* table = p.table + static_cast<int64_t>(w.b) * p.max_pages;
-      for (int i = 0; i < pc.n; ++i, ++step) {
-        const int st = step % T::kStages;
-        const uint32_t round = step / T::kStages;
-        const int key0 = (pc.first + i) * T::kKeys;
-        for (int slice = 0; slice < kKW; ++slice) {
-          const int bar = st * kKW + slice;
-          if (round > 0 && !mbar_wait_warp(empty + bar, (round - 1) & 1)) return;
-          const int slice0 = key0 + slice * T::kSlice;
-          if (lane == 0) {  // the bytes to come: the page pieces that hold a key of [lo, hi)
-            int pieces = 0;
-            for (int j = 0; j < boxes; ++j) {
-              const int k = slice0 + j * box_rows;
-              pieces += k < w.t.hi && k + box_rows > w.t.lo;
-            }
-            mbar_arrive_expect_tx(full + bar, pieces * box_rows * T::kRowB * T::kSub * 2);
+      // lane i holds the page of piece i of the unit, looked up a unit ahead
+      int page = lane < pieces && n > 0 ? piece_page(p, table, pc.first * pieces + lane, piece_log2, w.t) : -1;
+      for (int i = 0; i < n; ++i) {
+        const int later = lane < pieces && i + 1 < n
+                              ? piece_page(p, table, (pc.first + i + 1) * pieces + lane, piece_log2, w.t) : -1;
+        if (round > 0 && !mbar_wait_warp(empty + st, (round - 1) & 1)) return;
+        uint32_t todo = __ballot_sync(0xffffffffu, page >= 0);
+        const uint32_t bar = smem_addr(full + st);
+        if (elect_one()) mbar_arrive_expect_tx_s(bar, bytes * __popc(todo));
+        __syncwarp();
+        for (; todo; todo &= todo - 1) {
+          const int j = __ffs(todo) - 1;
+          const int at = static_cast<int>(__shfl_sync(0xffffffffu, page, j));
+          const uint32_t dst = ring + st * T::kStageB + (j << piece_log2) * (kDim * T::kEl);
+          const int row = (((pc.first + i) * pieces + j) << piece_log2) & ((1 << p.page_log2) - 1);
+          if (elect_one()) {
+            tma_load_5d(dst, &maps.k, 0, row, 0, head, at, bar);
+            tma_load_5d(dst + T::kTileB, &maps.v, 0, row, 0, head, at, bar);
           }
           __syncwarp();
-          for (int c = lane; c < copies; c += 32) {
-            const int which = c & 1, sub = (c >> 1) % T::kSub, j = (c >> 1) / T::kSub;
-            const int k = slice0 + j * box_rows;
-            if (k >= w.t.hi || k + box_rows <= w.t.lo) continue;
-            int page = __ldg(table + (k >> p.page_log2));
-            if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.num_pages)) {
-              page = p.num_pages;
-              atomicOr(&g_device_error, kErrPage);
-            }
-            const uint32_t dst = ring + st * T::kStageB + slice * 2 * T::kSliceB + which * T::kSliceB +
-                                 sub * T::kSubB + j * box_rows * T::kRowB;
-            tma_load_4d_plain(dst, which ? &maps.v : &maps.k, sub * (T::kRowB / T::kEl),
-                              k & ((1 << p.page_log2) - 1), w.h, page, smem_addr(full + bar));
-          }
         }
+        page = later;
+        if (++st == T::kStages) st = 0, ++round;
       }
     }
     return;
@@ -510,8 +530,13 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, 1
   constexpr int kDT = kDim / 8;           // value columns of 8
   constexpr int kKS = kDim / 16;          // k steps of the first product
   const float log2e = 1.4426950408889634f;
-  // ldmatrix addresses: lane l gives row l % 8 of matrix l / 8
-  const int lrow = lane & 7, lmat = lane >> 3;
+  // ldmatrix addresses: for K lane l gives row l % 8 of chunk l / 8, for V row l % 16 of
+  // chunk l / 16; chunk c of a row lies at c * 16 bytes, its low bits exchanged by the row's
+  const int piece_log2 = min(p.page_log2, log2c(T::kKeys));
+  const uint32_t block = T::kRowB << piece_log2;  // bytes from one 128-byte block of a piece to the next
+  const uint32_t k_lane = swizzled<T>(lane & 7, lane >> 3), v_lane = swizzled<T>(lane & 15, lane >> 4);
+  int st = 0;
+  uint32_t round = 0;
 
   for (long long u = u0; u < u1;) {
     walk_to(p, w, u, kTiling);
@@ -599,24 +624,26 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, 1
     float m[2] = {-INFINITY, -INFINITY};  // reference of the weights: weight = 2^(s - m)
     float l[2] = {0.f, 0.f};              // this lane's share of the sum of weights
 
-    for (int i = 0; i < pc.n; ++i, ++step) {
-      const int st = step % T::kStages;
-      ran_out = ran_out || !mbar_wait_warp(full + st * kKW + kw, (step / T::kStages) & 1);
+    for (int i = 0; i < pc.n; ++i) {
+      ran_out = ran_out || !mbar_wait_warp(full + st, round & 1);
       const int key0 = (pc.first + i) * T::kKeys + kw * T::kSlice;
       if (key0 < any_hi && key0 + T::kSlice > any_lo) {
-        const uint32_t kt = ring + st * T::kStageB + kw * 2 * T::kSliceB, vt = kt + T::kSliceB;
+        const uint32_t kt = ring + st * T::kStageB, vt = kt + T::kTileB;
         const bool edge = key0 + T::kSlice > all_hi || key0 < all_lo;
         // ---- s = q . k
         float s[kNT][4];
 #pragma unroll
         for (int j = 0; j < kNT; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+        uint32_t at[kNT];
+#pragma unroll
+        for (int j = 0; j < kNT; ++j) at[j] = kt + rows_at<T>(kw * T::kSlice + 8 * j, piece_log2);
         if constexpr (!kFp8) {
 #pragma unroll
           for (int k = 0; k < kKS; k += 2)
 #pragma unroll
             for (int j = 0; j < kNT; ++j) {
               uint32_t b[4];
-              ldsm4(b, kt + tile_offset<T>(8 * j + lrow, 2 * k + lmat));
+              ldsm4(b, at[j] + (k / 4) * block + (k_lane ^ ((k & 2) << 5)));
               mma_16<false>(s[j], qf[k], b[0], b[1]);
               mma_16<false>(s[j], qf[k + 1], b[2], b[3]);
             }
@@ -626,7 +653,7 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, 1
 #pragma unroll
             for (int j = 0; j < kNT; ++j) {
               uint32_t b[4];
-              ldsm4(b, kt + tile_offset<T>(8 * j + lrow, k + lmat));
+              ldsm4(b, at[j] + (k / 8) * block + (k_lane ^ (T::kRowB == 128 ? (k & 4) << 4 : 0)));
 #pragma unroll
               for (int x = 0; x < 4; ++x) {
                 uint32_t b0, b1;
@@ -706,17 +733,18 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, 1
             }
           }
           [[maybe_unused]] uint32_t r[4];
+          const uint32_t rows = vt + rows_at<T>(kw * T::kSlice + 16 * k, piece_log2);
 #pragma unroll
           for (int c = 0; c < kDT / 2; ++c) {
             // b: two columns of 8 values each, 16 keys (E4M3: one 16-value chunk)
             uint32_t b[4];
             if constexpr (!kFp8) {
-              ldsm4t(b, vt + tile_offset<T>(16 * k + (lane & 15), 2 * c + (lane >> 4)));
+              ldsm4t(b, rows + (c / 4) * block + (v_lane ^ ((c & 3) << 5)));
             } else {
               // matrices: (keys 0-7, chunk c), (keys 8-15, chunk c), then chunk c + 1; a word
               // holds two keys of two adjacent values
               static_assert(kDT % 4 == 0, "chunks come in pairs");
-              if (c % 2 == 0) ldsm4t(r, vt + tile_offset<T>(16 * k + (lane & 15), c + (lane >> 4)));
+              if (c % 2 == 0) ldsm4t(r, rows + (T::kRowB == 128 ? c / 8 : 0) * block + (v_lane ^ ((c & 6) << 4)));
               const uint32_t w0 = __byte_perm(r[c % 2 ? 2 : 0], 0, 0x3120), w1 = __byte_perm(r[c % 2 ? 3 : 1], 0, 0x3120);
               e4m3x4_to_f16x2(w0, b[0], b[2]);
               e4m3x4_to_f16x2(w1, b[1], b[3]);
@@ -765,7 +793,8 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, 1
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(empty + st * kKW + kw);
+      if (lane == 0) mbar_arrive(empty + st);
+      if (++st == T::kStages) st = 0, ++round;
     }
 
     // ---- join the key slices of this CTA
@@ -776,14 +805,11 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, 1
     }
     if constexpr (kKW > 1) {
       float* buf = reinterpret_cast<float*>(smem_raw + (join - raw));
-      int count = kKW;  // slices still to be joined: the last ones go to those before them
-#pragma unroll 1
-      while (count > 1) {
-        const int give = count / 2 < T::kJoinW ? count / 2 : T::kJoinW;
-        const int from = count - give, to = from - give;
+#pragma unroll
+      for (int half = kKW / 2; half >= 1; half >>= 1) {
         asm volatile("bar.sync 1, %0;" ::"n"(T::kConsumers * 32) : "memory");
-        if (kw >= from && kw < count) {
-          float* o = buf + ((kw - from) * kRW + rw) * 32 * (kDim / 2 + 4) + lane;
+        if (kw >= half && kw < 2 * half) {
+          float* o = buf + ((kw - half) * kRW + rw) * 32 * (kDim / 2 + 4) + lane;
 #pragma unroll
           for (int j = 0; j < kDT; ++j)
 #pragma unroll
@@ -792,8 +818,8 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, 1
           o[(4 * kDT + 2) * 32] = l[0], o[(4 * kDT + 3) * 32] = l[1];
         }
         asm volatile("bar.sync 1, %0;" ::"n"(T::kConsumers * 32) : "memory");
-        if (kw >= to && kw < from) {
-          const float* o = buf + ((kw - to) * kRW + rw) * 32 * (kDim / 2 + 4) + lane;
+        if (kw < half) {
+          const float* o = buf + (kw * kRW + rw) * 32 * (kDim / 2 + 4) + lane;
           float fa[2], fb[2];
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
@@ -809,7 +835,6 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, 1
 #pragma unroll
             for (int x = 0; x < 4; ++x) acc[j][x] = acc[j][x] * fa[x >> 1] + o[(4 * j + x) * 32] * fb[x >> 1];
         }
-        count = from;
       }
     }
     // ---- write: the finished rows, or this piece's share of them
@@ -932,17 +957,17 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnJob p
 // ------------------------------------------------------------------ launch
 
 // Which kernel and tile serve up to `rows` packed rows per sequence and kv head.  16 rows
-// leave eight key slices to eight warps, 64 rows share one slice among four; more
-// go to the tcgen05 kernel (attention_chunk.cuh).
+// leave four key slices to four warps, 64 rows share one slice among four; more go
+// to the tcgen05 kernel (attention_chunk.cuh).
 struct AttnShape {
   int rw, kw, tile_rows, box_keys;
   bool chunk;
 };
-inline AttnShape attn_shape(int dim, bool fp8, int64_t rows) {
+inline AttnShape attn_shape(int dim, int64_t rows) {
   if (rows > 64) return {0, 0, dim == 256 ? 128 : 256, dim == 256 ? 64 : 128, true};
   const int rw = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
-  const int kw = rw == 4 ? 1 : (dim == 256 ? 4 : 8) / rw;
-  return {rw, kw, 16 * rw, attn_slice(dim, fp8, kw), false};
+  const int kw = 4 / rw;
+  return {rw, kw, 16 * rw, attn_slice(dim, kw) * kw, false};
 }
 
 template <int kDim>

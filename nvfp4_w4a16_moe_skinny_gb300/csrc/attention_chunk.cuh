@@ -95,15 +95,6 @@ __device__ __forceinline__ void umma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
                : "memory");
 }
-// One lane of a converged warp, chosen by the hardware: unlike a lane test it leaves the
-// branch uniform, so that descriptors stay in uniform registers.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t ok;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
-  return ok != 0;
-}
-__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
-
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
@@ -182,6 +173,15 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
+}
+
+// Byte offset of 16-byte chunk c of key row r in a tile as it is in the pool, swizzled as
+// the boxes are.
+template <typename T>
+__device__ __forceinline__ uint32_t tile_offset(int r, int c) {
+  constexpr int per = T::kRowB / 16;
+  const uint32_t o = (c / per) * T::kSubB + r * T::kRowB + (c % per) * 16;
+  return o ^ ((o >> 3) & T::kSwz);
 }
 
 // Byte offset of 16-byte chunk c of row r in a 16-bit tile of `rows` rows of 128 bytes
@@ -292,16 +292,21 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
     if constexpr (kG == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 0) {
       // ------------------------------------------------------------ copies
-      const int box_rows = min(1 << p.page_log2, kKeys);
-      const int boxes = kKeys / box_rows;
+      const int piece_log2 = min(p.page_log2, log2c(kKeys));
+      const int pieces = kKeys >> piece_log2;  // of a tile: at most 8
       uint32_t raw = 0;
       for (long long u = u0; u < u1;) {
         walk_to(p, w, u, kTiling);
         const Share pc = share_at(w, u, u0, u1, blockIdx.x, kTiling);
         u = pc.end;
-        if (pc.n == 0) continue;
-        const int first = pc.first, n = pc.n;
+        const int n = static_cast<int>(uniform(pc.n)), head = static_cast<int>(uniform(w.h));
+        if (n == 0) continue;
         const int32_t* table = p.table + static_cast<int64_t>(w.b) * p.max_pages;
+        // lane i holds the page of piece i of a tile, looked up a tile ahead of its K
+        const auto look_up = [&](int j) {
+          return lane < pieces && j < n ? piece_page(p, table, (pc.first + j) * pieces + lane, piece_log2, w.t) : -1;
+        };
+        int page_k = look_up(0), page_v = page_k, page_next = look_up(1);
         // order: K 0, then K j + 1 and V j
         for (int c = 0; c < 2 * n; ++c) {
           const bool is_v = c == 2 * n - 1 || (c > 0 && c % 2 == 0);
@@ -321,27 +326,27 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
             full = (is_v ? bars->v_full : bars->k_full) + st;
             dst = (is_v ? v_at : k_at) + st * T::kTileB;
           }
-          const int key0 = (first + j) * kKeys;
-          if (lane == 0) {
-            int pieces = 0;
-            for (int i = 0; i < boxes; ++i) {
-              const int k = key0 + i * box_rows;
-              pieces += k < w.t.hi && k + box_rows > w.t.lo;
-            }
-            mbar_arrive_expect_tx(full, pieces * box_rows * T::kRowB * T::kSub);
+          if (!is_v && c > 0) {
+            page_v = page_k, page_k = page_next;
+            page_next = look_up(j + 1);
           }
+          const int page = is_v && c == 2 * n - 1 ? page_k : (is_v ? page_v : page_k);
+          uint32_t todo = __ballot_sync(0xffffffffu, page >= 0);
+          const uint32_t bar = smem_addr(full);
+          if (elect_one())
+            mbar_arrive_expect_tx_s(bar, __popc(todo) << piece_log2 << log2c(T::kRowB * T::kSub));
           __syncwarp();
-          for (int i = lane; i < boxes * T::kSub; i += 32) {
-            const int sub = i % T::kSub, piece = i / T::kSub;
-            const int k = key0 + piece * box_rows;
-            if (k >= w.t.hi || k + box_rows <= w.t.lo) continue;
-            int page = __ldg(table + (k >> p.page_log2));
-            if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.num_pages)) {
-              page = p.num_pages;
-              atomicOr(&g_device_error, kErrPage);
+          for (; todo; todo &= todo - 1) {
+            const int i = __ffs(todo) - 1;
+            const int at = static_cast<int>(__shfl_sync(0xffffffffu, page, i));
+            const int key = (pc.first + j) * kKeys + (i << piece_log2);
+            if (elect_one()) {
+#pragma unroll
+              for (int sub = 0; sub < T::kSub; ++sub)
+                tma_load_5d(dst + sub * T::kSubB + (i << piece_log2) * T::kRowB, is_v ? &maps.v : &maps.k, 0,
+                            key & ((1 << p.page_log2) - 1), sub, head, at, bar);
             }
-            tma_load_4d_plain(dst + sub * T::kSubB + piece * box_rows * T::kRowB, is_v ? &maps.v : &maps.k,
-                              sub * (T::kRowB / T::kEl), k & ((1 << p.page_log2) - 1), w.h, page, smem_addr(full));
+            __syncwarp();
           }
         }
         nt += n;

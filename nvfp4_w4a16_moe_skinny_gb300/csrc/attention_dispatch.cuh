@@ -9,10 +9,9 @@ namespace nvfp4 {
 template <int kDim, bool kFp8>
 nvfp4_status dispatch_rows(const AttnJob& p, const KvMaps& maps, const nvfp4_kv_cache* cache, const AttnShape& s,
                            cudaStream_t stream) {
-  constexpr int kWide = kDim == 256 ? 4 : 8;
   if (s.chunk) return launch_attn_chunk<kDim, kFp8>(p, maps, cache->v, cache->page_stride, stream);
-  if (s.rw == 1) return launch_attn_split<kDim, kFp8, 1, kWide>(p, maps, stream);
-  if (s.rw == 2) return launch_attn_split<kDim, kFp8, 2, kWide / 2>(p, maps, stream);
+  if (s.rw == 1) return launch_attn_split<kDim, kFp8, 1, 4>(p, maps, stream);
+  if (s.rw == 2) return launch_attn_split<kDim, kFp8, 2, 2>(p, maps, stream);
   return launch_attn_split<kDim, kFp8, 4, 1>(p, maps, stream);
 }
 
