@@ -50,8 +50,9 @@ extern "C" {
 size_t paged_attention_workspace_bytes(int32_t n_tokens, int32_t n_seqs, int32_t max_new, int32_t n_heads,
                                        int32_t n_kv_heads, int32_t head_dim) {
   if (!sizes_ok(n_tokens, n_seqs, max_new, n_heads, n_kv_heads, head_dim)) return 0;
-  const AttnShape s = attn_shape(head_dim, packed_rows(n_tokens, max_new, n_heads, n_kv_heads));
-  return static_cast<size_t>(2) * kAttnGrid * s.tile_rows * (head_dim + 2) * sizeof(float);
+  const AttnShape s = attn_shape(head_dim, false, packed_rows(n_tokens, max_new, n_heads, n_kv_heads));
+  const int grid = kAttnGrid * (s.chunk ? 1 : attn_ctas(head_dim));
+  return static_cast<size_t>(2) * grid * s.tile_rows * (head_dim + 2) * sizeof(float);
 }
 
 nvfp4_status paged_attention(const nvfp4_kv_cache* cache, const nvfp4_batch* batch, const uint16_t* q,
@@ -84,7 +85,7 @@ nvfp4_status paged_attention(const nvfp4_kv_cache* cache, const nvfp4_batch* bat
   p.k_scale = cache->k_scale, p.v_scale = cache->v_scale;
   p.scale = scale, p.softcap = softcap, p.window = window;
   p.part = static_cast<float*>(ws);
-  const AttnShape s = attn_shape(dim, packed_rows(n_tokens, batch->max_new, n_heads, kv));
+  const AttnShape s = attn_shape(dim, cache->dtype == NVFP4_KV_E4M3, packed_rows(n_tokens, batch->max_new, n_heads, kv));
   KvMaps maps;
   const int box = std::min(cache->page_size, s.box_keys);
   if (!encode_pool_map(&maps.k, cache, cache->k, box, !s.chunk) || !encode_pool_map(&maps.v, cache, cache->v, box, !s.chunk))

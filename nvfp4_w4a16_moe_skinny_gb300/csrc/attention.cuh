@@ -34,7 +34,7 @@
 
 namespace nvfp4 {
 
-constexpr int kAttnGrid = 152;  // CTAs of the split; fixed, so that workspace sizes are host-computable
+constexpr int kAttnGrid = 152;  // SMs that the split is made for; fixed, so that workspace sizes are host-computable
 
 // Division by a number that a launch knows: x / g = umulhi(x, mul) >> shift for
 // x < 2^31 (shift < 0: g = 1).
@@ -393,16 +393,20 @@ __device__ __forceinline__ uint32_t nonfinite_mask(uint32_t v) {
 
 // ------------------------------------------------------------------ tile geometry
 
-// Keys of one warp's step: as many as keep the scores in few registers.
-__host__ __device__ constexpr int attn_slice(int dim, int kw) {
-  if (kw == 1) return dim == 256 ? 32 : 64;
-  return dim == 256 ? 16 : 32;
+// CTAs of the split kernel on one SM.
+__host__ __device__ constexpr int attn_ctas(int dim) { return dim == 256 ? 1 : 2; }
+
+// Keys of one warp's step: few enough that three units fit in a CTA's shared memory and the
+// scores in few registers.
+__host__ __device__ constexpr int attn_slice(int dim, bool fp8, int kw) {
+  if (kw == 1) return dim == 256 || (dim == 128 && !fp8) ? 32 : 64;
+  return dim == 256 || (dim == 128 && !fp8) ? 16 : 32;
 }
 
 template <int kDim, bool kFp8, int kRW, int kKW>
 struct AttnTile {
   static constexpr int kRows = 16 * kRW;
-  static constexpr int kSlice = attn_slice(kDim, kKW);               // keys of a warp's step
+  static constexpr int kSlice = attn_slice(kDim, kFp8, kKW);              // keys of a warp's step
   static constexpr int kKeys = kSlice * kKW;                         // keys of a unit
   static constexpr int kConsumers = kRW * kKW;
   static constexpr int kThreadsAll = (kConsumers + 1) * 32;
@@ -413,8 +417,9 @@ struct AttnTile {
   static constexpr uint32_t kSwz = kRowB == 128 ? 0x70 : 0x30;
   static constexpr int kTileB = kKeys * kDim * kEl;                  // K or V of a unit: page pieces of [kSub][rows][kRowB]
   static constexpr int kStageB = 2 * kTileB;
-  static constexpr int kJoinB = (kKW / 2) * kRW * 32 * (kDim / 2 + 4) * 4;
-  static constexpr int kFit = (227 * 1024 - 1024 - 1024 - kJoinB) / kStageB;
+  static constexpr int kCtas = attn_ctas(kDim);
+  static constexpr int kJoinB = kKW > 1 ? kRW * 32 * (kDim / 2 + 4) * 4 : 0;  // one slice's sums
+  static constexpr int kFit = ((kCtas == 1 ? 227 : 113) * 1024 - 1024 - 1024 - kJoinB) / kStageB;
   static constexpr int kStages = kFit > 6 ? 6 : kFit;
   static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageB + kJoinB + 1024;
   static_assert(kStages >= 2, "ring too shallow");
@@ -450,7 +455,7 @@ __device__ __forceinline__ int piece_page(const AttnJob& p, const int32_t* table
 // ------------------------------------------------------------------ the split kernel
 
 template <int kDim, bool kFp8, int kRW, int kKW>
-__global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, 1)
+__global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, attn_ctas(kDim))
     attn_split_kernel(const AttnJob p, const __grid_constant__ KvMaps maps) {
   using T = AttnTile<kDim, kFp8, kRW, kKW>;
   extern __shared__ uint8_t smem_raw[];
@@ -805,11 +810,11 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, 1
     }
     if constexpr (kKW > 1) {
       float* buf = reinterpret_cast<float*>(smem_raw + (join - raw));
-#pragma unroll
-      for (int half = kKW / 2; half >= 1; half >>= 1) {
+#pragma unroll 1
+      for (int from = kKW - 1; from > 0; --from) {  // each slice's sums go to the one before it
         asm volatile("bar.sync 1, %0;" ::"n"(T::kConsumers * 32) : "memory");
-        if (kw >= half && kw < 2 * half) {
-          float* o = buf + ((kw - half) * kRW + rw) * 32 * (kDim / 2 + 4) + lane;
+        if (kw == from) {
+          float* o = buf + rw * 32 * (kDim / 2 + 4) + lane;
 #pragma unroll
           for (int j = 0; j < kDT; ++j)
 #pragma unroll
@@ -818,8 +823,8 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, 1
           o[(4 * kDT + 2) * 32] = l[0], o[(4 * kDT + 3) * 32] = l[1];
         }
         asm volatile("bar.sync 1, %0;" ::"n"(T::kConsumers * 32) : "memory");
-        if (kw < half) {
-          const float* o = buf + (kw * kRW + rw) * 32 * (kDim / 2 + 4) + lane;
+        if (kw == from - 1) {
+          const float* o = buf + rw * 32 * (kDim / 2 + 4) + lane;
           float fa[2], fb[2];
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
@@ -963,20 +968,19 @@ struct AttnShape {
   int rw, kw, tile_rows, box_keys;
   bool chunk;
 };
-inline AttnShape attn_shape(int dim, int64_t rows) {
+inline AttnShape attn_shape(int dim, bool fp8, int64_t rows) {
   if (rows > 64) return {0, 0, dim == 256 ? 128 : 256, dim == 256 ? 64 : 128, true};
   const int rw = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
   const int kw = 4 / rw;
-  return {rw, kw, 16 * rw, attn_slice(dim, kw) * kw, false};
+  return {rw, kw, 16 * rw, attn_slice(dim, fp8, kw) * kw, false};
 }
 
 template <int kDim>
-nvfp4_status launch_attn_join(const AttnJob& p, const Tiling& g, cudaStream_t stream) {
+nvfp4_status launch_attn_join(const AttnJob& p, const Tiling& g, int grid, cudaStream_t stream) {
   // one unit an item: nothing can be split
   if ((static_cast<int64_t>(p.max_pages) << p.page_log2) > g.keys) {
     const int rows = g.rows / 4 < 16 ? g.rows / 4 : 16;
-    if (launch_pdl(attn_join_kernel<kDim>, dim3(kAttnGrid - 1, rows), dim3(kJoinThreads), 0, stream, p, kAttnGrid,
-                   g) != cudaSuccess)
+    if (launch_pdl(attn_join_kernel<kDim>, dim3(grid - 1, rows), dim3(kJoinThreads), 0, stream, p, grid, g) != cudaSuccess)
       return NVFP4_ERR_CUDA;
   }
   return launched();
@@ -986,10 +990,10 @@ template <int kDim, bool kFp8, int kRW, int kKW>
 nvfp4_status launch_attn_split(const AttnJob& p, const KvMaps& maps, cudaStream_t stream) {
   using T = AttnTile<kDim, kFp8, kRW, kKW>;
   if (set_smem(attn_split_kernel<kDim, kFp8, kRW, kKW>, T::kSmem) != cudaSuccess) return NVFP4_ERR_CUDA;
-  if (launch_pdl(attn_split_kernel<kDim, kFp8, kRW, kKW>, dim3(kAttnGrid), dim3(T::kThreadsAll), T::kSmem, stream, p,
-                 maps) != cudaSuccess)
+  if (launch_pdl(attn_split_kernel<kDim, kFp8, kRW, kKW>, dim3(kAttnGrid * T::kCtas), dim3(T::kThreadsAll), T::kSmem,
+                 stream, p, maps) != cudaSuccess)
     return NVFP4_ERR_CUDA;
-  return launch_attn_join<kDim>(p, Tiling{T::kRows, T::kKeys, T::kOver}, stream);
+  return launch_attn_join<kDim>(p, Tiling{T::kRows, T::kKeys, T::kOver}, kAttnGrid * T::kCtas, stream);
 }
 
 // The split and join grids for heads of kDim values (attention_d*.cu).

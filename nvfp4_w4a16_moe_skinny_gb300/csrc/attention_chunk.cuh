@@ -796,7 +796,7 @@ nvfp4_status launch_attn_chunk(const AttnJob& p, const KvMaps& maps, const void*
   if (launch_pdl(attn_chunk_kernel<kDim, kFp8>, dim3(kAttnGrid), dim3(T::kThreadsAll), T::kSmem, stream, p, maps,
                  v_pool, page_stride) != cudaSuccess)
     return NVFP4_ERR_CUDA;
-  return launch_attn_join<kDim>(p, Tiling{T::kRows, T::kKeys, T::kOver}, stream);
+  return launch_attn_join<kDim>(p, Tiling{T::kRows, T::kKeys, T::kOver}, kAttnGrid, stream);
 }
 
 }  // namespace nvfp4
