@@ -82,17 +82,19 @@ nvfp4_status paged_attention(const nvfp4_kv_cache* cache, const nvfp4_batch* bat
   p.n_heads = n_heads, p.n_kv = kv, p.group = n_heads / kv, p.by_group = fast_div(n_heads / kv);
   p.page_log2 = log2i(cache->page_size), p.num_pages = cache->num_pages;
   p.q = q, p.q_stride = q_stride, p.out = out, p.out_stride = out_stride, p.lse = lse;
+  p.v_pool = cache->v, p.page_stride = cache->page_stride;
   p.k_scale = cache->k_scale, p.v_scale = cache->v_scale;
   p.scale = scale, p.softcap = softcap, p.window = window;
   p.part = static_cast<float*>(ws);
-  const AttnShape s = attn_shape(dim, cache->dtype == NVFP4_KV_E4M3, packed_rows(n_tokens, batch->max_new, n_heads, kv));
+  const bool fp8 = cache->dtype == NVFP4_KV_E4M3;
+  const AttnShape s = attn_shape(dim, fp8, packed_rows(n_tokens, batch->max_new, n_heads, kv));
   KvMaps maps;
   const int box = std::min(cache->page_size, s.box_keys);
   if (!encode_pool_map(&maps.k, cache, cache->k, box, !s.chunk) || !encode_pool_map(&maps.v, cache, cache->v, box, !s.chunk))
     return NVFP4_ERR_CUDA;
-  if (dim == 64) return dispatch_attention<64>(p, maps, cache, s, stream);
-  if (dim == 128) return dispatch_attention<128>(p, maps, cache, s, stream);
-  return dispatch_attention<256>(p, maps, cache, s, stream);
+  if (dim == 64) return dispatch_attention<64>(p, maps, fp8, s, stream);
+  if (dim == 128) return dispatch_attention<128>(p, maps, fp8, s, stream);
+  return dispatch_attention<256>(p, maps, fp8, s, stream);
 }
 
 }  // extern "C"

@@ -63,6 +63,8 @@ struct AttnJob {
   uint16_t* out;
   int64_t out_stride;
   float* lse;
+  const void* v_pool;
+  int64_t page_stride;
   const float* k_scale;
   const float* v_scale;
   float scale, softcap;
@@ -418,12 +420,76 @@ struct AttnTile {
   static constexpr int kTileB = kKeys * kDim * kEl;                  // K or V of a unit: page pieces of [kSub][rows][kRowB]
   static constexpr int kStageB = 2 * kTileB;
   static constexpr int kCtas = attn_ctas(kDim);
+  static constexpr int kQB = kRows * kDim * 2;                       // Q: [kDim / 64][kRows][128 bytes]
   static constexpr int kJoinB = kKW > 1 ? kRW * 32 * (kDim / 2 + 4) * 4 : 0;  // one slice's sums
-  static constexpr int kFit = ((kCtas == 1 ? 227 : 113) * 1024 - 1024 - 1024 - kJoinB) / kStageB;
+  static constexpr int kFit = ((kCtas == 1 ? 227 : 113) * 1024 - 1024 - 1024 - kJoinB - kQB) / kStageB;
   static constexpr int kStages = kFit > 6 ? 6 : kFit;
-  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageB + kJoinB + 1024;
+  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageB + kQB + kJoinB + 1024;
   static_assert(kStages >= 2, "ring too shallow");
 };
+
+// Keys that every row of an item sees, [all_lo, all_hi), and that some row sees, [any_lo, any_hi).
+struct KeyRange {
+  int all_lo, all_hi, any_lo, any_hi;
+};
+
+__device__ __forceinline__ KeyRange key_range(const AttnJob& p, const Walk& w) {
+  KeyRange r;
+  const int first = w.s.len - w.s.n + div_by(p.by_group, w.t.row0);
+  const int last = w.s.len - w.s.n + div_by(p.by_group, w.t.row0 + w.t.rows - 1);
+  r.all_hi = min(first + 1, w.s.len);
+  r.all_lo = p.window > 0 ? last - p.window + 1 : 0;
+  r.any_hi = w.t.hi;
+  r.any_lo = w.t.lo;
+  return r;
+}
+
+__device__ __forceinline__ bool partly_seen(const KeyRange& r, int key0, int keys) {
+  return key0 + keys > r.all_hi || key0 < r.all_lo;
+}
+
+// One 16-byte chunk of V of a key (eight 16-bit values): nothing if no row sees it, and
+// without infinities and NaN.
+template <bool kF16>
+__device__ __forceinline__ uint4 clean_chunk(uint4 v, bool seen, bool& noted) {
+  if (!seen) return make_uint4(0, 0, 0, 0);
+  const uint32_t a = nonfinite_mask<kF16>(v.x), b = nonfinite_mask<kF16>(v.y);
+  const uint32_t c = nonfinite_mask<kF16>(v.z), d = nonfinite_mask<kF16>(v.w);
+  noted = noted || (a | b | c | d) != 0;
+  return make_uint4(v.x & ~a, v.y & ~b, v.z & ~c, v.w & ~d);
+}
+
+// The same for 16 E4M3 codes (NaN is 0x7f or 0xff; there are no infinities).
+__device__ __forceinline__ uint4 clean_codes(uint4 v, bool seen, bool& noted) {
+  if (!seen) return make_uint4(0, 0, 0, 0);
+  const auto nan = [](uint32_t x) { return (((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7; };
+  const uint32_t a = nan(v.x), b = nan(v.y), c = nan(v.z), d = nan(v.w);
+  noted = noted || (a | b | c | d) != 0;
+  return make_uint4(v.x & ~(a * 0xffu), v.y & ~(b * 0xffu), v.z & ~(c * 0xffu), v.w & ~(d * 0xffu));
+}
+
+// Element offset of a key's first value of kv head h, and one value of a pool.
+__device__ __forceinline__ int64_t value_at(const AttnJob& p, int page, int h, int key, int dim) {
+  return page * p.page_stride +
+         ((static_cast<int64_t>(h) << p.page_log2) + (key & ((1 << p.page_log2) - 1))) * dim;
+}
+template <bool kFp8>
+__device__ __forceinline__ float pool_value(const void* pool, int64_t at) {
+  if constexpr (kFp8) {
+    uint32_t x, y;
+    e4m3x4_to_f16x2(*(static_cast<const uint8_t*>(pool) + at), x, y);
+    return f16lo_to_f32(x);
+  } else {
+    return bf16_bits_to_f32(*(static_cast<const uint16_t*>(pool) + at));
+  }
+}
+
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ void sts64(uint32_t a, uint32_t x, uint32_t y) {
+  asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(a), "r"(x), "r"(y) : "memory");
+}
 
 // Byte offset of chunk c (16 bytes) of row r in a block of rows, swizzled as the boxes are.
 template <typename T>
@@ -461,15 +527,19 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, a
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t ring = (raw + 1023u) & ~1023u;
-  const uint32_t join = ring + T::kStages * T::kStageB;
+  const uint32_t q_at = ring + T::kStages * T::kStageB, join = q_at + T::kQB;
   uint8_t* tail = smem_raw + (join + T::kJoinB - raw);
   uint64_t* full = reinterpret_cast<uint64_t*>(tail);  // [stages]
   uint64_t* empty = full + T::kStages;                 // [stages]
   long long* scratch = reinterpret_cast<long long*>(empty + T::kStages);
+  float* q_back = reinterpret_cast<float*>(scratch + 36);  // [kRows] undoes the scaling of a row of Q
+  // an infinity or NaN was taken out of V, in this CTA's items so far
+  volatile int* noted_flag = reinterpret_cast<volatile int*>(q_back + T::kRows);
 
   const int warp = static_cast<int>(uniform(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < T::kStages; ++i) mbar_init(full + i, 1), mbar_init(empty + i, T::kConsumers);
+    *noted_flag = 0;
     fence_mbar_init();
   }
   pdl_wait();
@@ -535,11 +605,12 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, a
   constexpr int kDT = kDim / 8;           // value columns of 8
   constexpr int kKS = kDim / 16;          // k steps of the first product
   const float log2e = 1.4426950408889634f;
-  // ldmatrix addresses: for K lane l gives row l % 8 of chunk l / 8, for V row l % 16 of
-  // chunk l / 16; chunk c of a row lies at c * 16 bytes, its low bits exchanged by the row's
+  // ldmatrix addresses: for K lane l gives row l % 8 of chunk l / 8, for V and Q row l % 16
+  // of chunk l / 16; chunk c of a row lies at c * 16 bytes, its low bits exchanged by the row's
   const int piece_log2 = min(p.page_log2, log2c(T::kKeys));
   const uint32_t block = T::kRowB << piece_log2;  // bytes from one 128-byte block of a piece to the next
   const uint32_t k_lane = swizzled<T>(lane & 7, lane >> 3), v_lane = swizzled<T>(lane & 15, lane >> 4);
+  const uint32_t q_lane = q_at + rw * 16 * 128 + ((lane & 15) * 128 | (((lane >> 4) ^ (lane & 7)) << 4));
   int st = 0;
   uint32_t round = 0;
 
@@ -570,58 +641,72 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, a
     const int any_hi = min(pos_hi + 1, w.s.len);                                  // keys [any_lo, any_hi) seen by some row
     const int any_lo = p.window > 0 ? max(pos_lo - p.window + 1, 0) : 0;
 
-    // q as A fragments
-    uint32_t qf[kKS][4];
-    float qscale[2] = {1.f, 1.f};
-    {
-      const uint16_t* q0 = p.q + (w.s.tok0 + tok[0]) * p.q_stride + static_cast<int64_t>(head[0]) * kDim;
-      const uint16_t* q1 = p.q + (w.s.tok0 + tok[1]) * p.q_stride + static_cast<int64_t>(head[1]) * kDim;
+    // keys that every row of the item sees, or some row (the tiles between are cleaned)
+    const KeyRange kr = key_range(p, w);
+
+    // Q to shared memory, each warp a quarter of the rows, eight lanes a row
+    if constexpr (kKW > 1) asm volatile("bar.sync 1, %0;" ::"n"(T::kConsumers * 32) : "memory");  // the last item's Q is read
+#pragma unroll
+    for (int it = 0; it < T::kRows / (4 * T::kConsumers); ++it) {
+      const int r = (kKW > 1 ? warp : rw) * (T::kRows / T::kConsumers) + 4 * it + (lane >> 3);
+      const int rr = w.t.row0 + min(r, w.t.rows - 1);
+      const int tk = div_by(p.by_group, rr), hd = w.h * p.group + rr - tk * p.group;
+      const uint16_t* q = p.q + (w.s.tok0 + tk) * p.q_stride + static_cast<int64_t>(hd) * kDim;
+      const bool zero = r >= w.t.rows || p.scale == 0.f;
+      uint4 v[kDim / 64];
+#pragma unroll
+      for (int c = 0; c < kDim / 64; ++c)
+        v[c] = zero ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(q + 64 * c + 8 * (lane & 7));
+      const uint32_t sign = p.scale < 0.f ? 0x80008000u : 0u;  // a negative scale turns q's sign
       if constexpr (!kFp8) {
 #pragma unroll
-        for (int k = 0; k < kKS; ++k) {
-          qf[k][0] = live[0] ? *reinterpret_cast<const uint32_t*>(q0 + 16 * k + 2 * t4) : 0u;
-          qf[k][1] = live[1] ? *reinterpret_cast<const uint32_t*>(q1 + 16 * k + 2 * t4) : 0u;
-          qf[k][2] = live[0] ? *reinterpret_cast<const uint32_t*>(q0 + 16 * k + 2 * t4 + 8) : 0u;
-          qf[k][3] = live[1] ? *reinterpret_cast<const uint32_t*>(q1 + 16 * k + 2 * t4 + 8) : 0u;
-        }
+        for (int c = 0; c < kDim / 64; ++c)
+          sts128(q_at + c * T::kRows * 128 + r * 128 + (((lane & 7) ^ (r & 7)) << 4),
+                 make_uint4(v[c].x ^ sign, v[c].y ^ sign, v[c].z ^ sign, v[c].w ^ sign));
       } else {
-        // four adjacent values per lane and k step, in the order the codes of a key
-        // come out of ldmatrix
-        float amax[2] = {0.f, 0.f};
+        // scaled into f16's range; the pairs of 16 values in the order in which the codes of a
+        // key come out of ldmatrix (pairs 0, 2, 4, 6, then 1, 3, 5, 7)
+        float amax = 0.f;
 #pragma unroll
-        for (int k = 0; k < kKS; ++k) {
-          const uint2 a = live[0] ? *reinterpret_cast<const uint2*>(q0 + 16 * k + 4 * t4) : make_uint2(0, 0);
-          const uint2 b = live[1] ? *reinterpret_cast<const uint2*>(q1 + 16 * k + 4 * t4) : make_uint2(0, 0);
-          qf[k][0] = a.x, qf[k][2] = a.y, qf[k][1] = b.x, qf[k][3] = b.y;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            amax[j & 1] = fmaxf(amax[j & 1], fabsf(__uint_as_float(qf[k][j] << 16)));
-            amax[j & 1] = fmaxf(amax[j & 1], fabsf(__uint_as_float(qf[k][j] & 0xffff0000u)));
-          }
-        }
-        float up[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          amax[i] = fmaxf(amax[i], __shfl_xor_sync(0xffffffffu, amax[i], 1));
-          amax[i] = fmaxf(amax[i], __shfl_xor_sync(0xffffffffu, amax[i], 2));
-          const int e = pow2_rescale_exponent(amax[i]);
-          up[i] = exp2i(e);
-          qscale[i] = exp2i(-e);
-        }
-#pragma unroll
-        for (int k = 0; k < kKS; ++k)
+        for (int c = 0; c < kDim / 64; ++c) {
+          const uint32_t x[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            qf[k][j] = f32x2_to_f16x2(__uint_as_float(qf[k][j] << 16) * up[j & 1],
-                                      __uint_as_float(qf[k][j] & 0xffff0000u) * up[j & 1]);
+            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(x[j] << 16)), fabsf(__uint_as_float(x[j] & 0xffff0000u))));
+        }
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const int e = pow2_rescale_exponent(amax);
+        const float up = exp2i(e);
+        if ((lane & 7) == 0) q_back[r] = exp2i(-e);
+#pragma unroll
+        for (int c = 0; c < kDim / 64; ++c) {
+          uint32_t x[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            x[j] ^= sign;
+            x[j] = f32x2_to_f16x2(__uint_as_float(x[j] << 16) * up, __uint_as_float(x[j] & 0xffff0000u) * up);
+          }
+          const uint32_t row = q_at + c * T::kRows * 128 + r * 128 + 8 * (lane & 1);
+          const int even = lane & 6;
+          sts64(row + ((even ^ (r & 7)) << 4), x[0], x[2]);
+          sts64(row + (((even + 1) ^ (r & 7)) << 4), x[1], x[3]);
+        }
       }
     }
+    if constexpr (kKW > 1)
+      asm volatile("bar.sync 1, %0;" ::"n"(T::kConsumers * 32) : "memory");
+    else
+      __syncwarp();
     const float ks = (kFp8 && p.k_scale) ? __ldg(p.k_scale + w.h) : 1.0f;
     // logits in units of log 2: acc * mul; with a softcap, cap2 * tanh(acc * mul)
     const bool capped = p.softcap > 0.f;
-    const float unit = p.scale * ks * (capped ? 1.0f / p.softcap : log2e);
-    const float mul[2] = {unit * qscale[0], unit * qscale[1]};
+    const float unit = (p.scale == 0.f ? 1.0f : fabsf(p.scale)) * ks * (capped ? 1.0f / p.softcap : log2e);
+    float mul[2] = {unit, unit};
+    if constexpr (kFp8) mul[0] *= q_back[rw * 16 + g], mul[1] *= q_back[rw * 16 + g + 8];
     const float cap2 = p.softcap * log2e;
+    // with a softcap the logits are finished before the maximum is taken
+    const float fac[2] = {capped ? 1.0f : fmaxf(mul[0], 1.2e-38f), capped ? 1.0f : fmaxf(mul[1], 1.2e-38f)};
 
     float acc[kDT][4];
 #pragma unroll
@@ -634,7 +719,6 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, a
       const int key0 = (pc.first + i) * T::kKeys + kw * T::kSlice;
       if (key0 < any_hi && key0 + T::kSlice > any_lo) {
         const uint32_t kt = ring + st * T::kStageB, vt = kt + T::kTileB;
-        const bool edge = key0 + T::kSlice > all_hi || key0 < all_lo;
         // ---- s = q . k
         float s[kNT][4];
 #pragma unroll
@@ -644,17 +728,24 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, a
         for (int j = 0; j < kNT; ++j) at[j] = kt + rows_at<T>(kw * T::kSlice + 8 * j, piece_log2);
         if constexpr (!kFp8) {
 #pragma unroll
-          for (int k = 0; k < kKS; k += 2)
+          for (int k = 0; k < kKS; k += 2) {
+            uint32_t a0[4], a1[4];
+            ldsm4(a0, q_lane + (k / 4) * T::kRows * 128 ^ ((k & 2) << 5));
+            ldsm4(a1, q_lane + (k / 4) * T::kRows * 128 ^ ((k & 2) << 5 | 32));
 #pragma unroll
             for (int j = 0; j < kNT; ++j) {
               uint32_t b[4];
               ldsm4(b, at[j] + (k / 4) * block + (k_lane ^ ((k & 2) << 5)));
-              mma_16<false>(s[j], qf[k], b[0], b[1]);
-              mma_16<false>(s[j], qf[k + 1], b[2], b[3]);
+              mma_16<false>(s[j], a0, b[0], b[1]);
+              mma_16<false>(s[j], a1, b[2], b[3]);
             }
+          }
         } else {
 #pragma unroll
-          for (int k = 0; k < kKS; k += 4)
+          for (int k = 0; k < kKS; k += 4) {
+            uint32_t a[4][4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) ldsm4(a[x], q_lane + (k / 4) * T::kRows * 128 ^ (x << 5));
 #pragma unroll
             for (int j = 0; j < kNT; ++j) {
               uint32_t b[4];
@@ -663,33 +754,40 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, a
               for (int x = 0; x < 4; ++x) {
                 uint32_t b0, b1;
                 e4m3x4_to_f16x2(b[x], b0, b1);
-                mma_16<true>(s[j], qf[k + x], b0, b1);
+                mma_16<true>(s[j], a[x], b0, b1);
               }
             }
+          }
         }
-        // ---- logits, mask, running maximum
+        // ---- softcap, mask, running maximum
+        if (capped) {
+#pragma unroll
+          for (int j = 0; j < kNT; ++j)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              s[j][x] = cap2 * (1.0f - __fdividef(2.0f, exp2_approx(s[j][x] * (mul[x >> 1] * 2.0f * log2e)) + 1.0f));
+        }
+        if (key0 + T::kSlice > all_hi || key0 < all_lo) {
+#pragma unroll
+          for (int j = 0; j < kNT; ++j)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int key = key0 + 8 * j + 2 * t4 + (x & 1), ps = pos[x >> 1];
+              const bool sees = key <= ps && key < w.s.len && (p.window <= 0 || key > ps - p.window);
+              s[j][x] = sees ? s[j][x] : -INFINITY;
+            }
+        }
         float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
         for (int j = 0; j < kNT; ++j)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            float v = s[j][x] * mul[x >> 1];
-            if (capped) v = cap2 * (1.0f - __fdividef(2.0f, exp2_approx(v * (2.0f * log2e)) + 1.0f));
-            if (edge) {
-              const int key = key0 + 8 * j + 2 * t4 + (x & 1);
-              const int ps = pos[x >> 1];
-              const bool sees = key <= ps && key < w.s.len && (p.window <= 0 || key > ps - p.window);
-              v = sees ? v : -INFINITY;
-            }
-            s[j][x] = v;
-            top[x >> 1] = fmaxf(top[x >> 1], v);
-          }
+          for (int x = 0; x < 4; ++x) top[x >> 1] = fmaxf(top[x >> 1], s[j][x]);
         float alpha[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 1));
           top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 2));
-          const float next = fmaxf(m[x], top[x] - (kFp8 ? 15.0f : 0.0f));
+          const float next = fmaxf(m[x], top[x] * fac[x] - (kFp8 ? 15.0f : 0.0f));
           // a row that has seen nothing keeps -inf as its reference and 0 as its sum
           alpha[x] = next == -INFINITY ? 1.0f : exp2_approx(m[x] - next);
           m[x] = next;
@@ -707,10 +805,29 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, a
         for (int j = 0; j < kNT; ++j)
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            s[j][x] = exp2_approx(s[j][x] - ref[x >> 1]);
+            s[j][x] = exp2_approx(fmaf(s[j][x], fac[x >> 1], -ref[x >> 1]));
             l[x >> 1] += s[j][x];
           }
-        // ---- out += weights . v
+        // ---- out += weights . v, with V cleaned where some row of the item does not see all of
+        // the slice: keys that no row sees become zeros (0 * inf is NaN), infinities and NaN
+        // are taken out and noted
+        if (partly_seen(kr, key0, T::kSlice)) {
+          constexpr int kChunks = kDim * T::kEl / 16;
+          bool noted = false;
+          for (int i = lane; i < T::kSlice * kChunks; i += 32) {
+            const int r = kw * T::kSlice + i / kChunks, c = i % kChunks, key = key0 + i / kChunks;
+            const uint32_t o = (r & 15) * T::kRowB + (c % (T::kRowB / 16)) * 16;
+            const uint32_t a = vt + rows_at<T>(r & ~15, piece_log2) + c / (T::kRowB / 16) * block + (o ^ ((o >> 3) & T::kSwz));
+            const bool seen = key >= kr.any_lo && key < kr.any_hi;
+            if constexpr (kFp8)
+              sts128(a, clean_codes(lds128(a), seen, noted));
+            else
+              sts128(a, clean_chunk<false>(lds128(a), seen, noted));
+          }
+          if (noted) *noted_flag = 1;
+          fence_proxy_async_smem();  // the stage's next copy comes after these writes
+          __syncwarp();
+        }
 #pragma unroll
         for (int k = 0; k < T::kSlice / 16; ++k) {
           uint32_t a[4];
@@ -718,24 +835,6 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, a
           for (int x = 0; x < 4; ++x) {
             const float lo = s[2 * k + (x >> 1)][2 * (x & 1)], hi = s[2 * k + (x >> 1)][2 * (x & 1) + 1];
             a[x] = kFp8 ? f32x2_to_f16x2(lo, hi) : f32x2_to_bf16x2(lo, hi);
-          }
-          uint32_t keep[2] = {0xffffffffu, 0xffffffffu};  // value halves of keys that some row sees
-          uint32_t shown[4] = {0, 0, 0, 0};               // 1.0 where a row sees a key (edge tiles only)
-          if (edge) {
-            const uint32_t one = kFp8 ? 0x3c00u : 0x3f80u;
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const int key = key0 + 16 * k + 8 * x + 2 * t4;
-              keep[x] = (key >= any_lo && key < any_hi ? 0xffffu : 0u) |
-                        (key + 1 >= any_lo && key + 1 < any_hi ? 0xffff0000u : 0u);
-#pragma unroll
-              for (int y = 0; y < 2; ++y)
-#pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                  const int kk = key + z, ps = pos[y];
-                  if (kk <= ps && kk < w.s.len && (p.window <= 0 || kk > ps - p.window)) shown[2 * x + y] |= one << (16 * z);
-                }
-            }
           }
           [[maybe_unused]] uint32_t r[4];
           const uint32_t rows = vt + rows_at<T>(kw * T::kSlice + 16 * k, piece_log2);
@@ -754,44 +853,6 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, a
               e4m3x4_to_f16x2(w0, b[0], b[2]);
               e4m3x4_to_f16x2(w1, b[1], b[3]);
             }
-            if (edge) {
-              // keys outside every row's reach count as zeros; infinities and NaN of keys that
-              // only some rows see are taken out of the product (0 * inf is NaN) and added to
-              // the rows that see them: the product of the rows' 0/1 visibility with 0/1
-              // indicators of +inf, -inf and NaN says which
-              uint32_t bad[4];
-#pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                b[x] &= keep[x & 1];
-                bad[x] = nonfinite_mask<kFp8>(b[x]);
-              }
-              if (__any_sync(0xffffffffu, (bad[0] | bad[1] | bad[2] | bad[3]) != 0)) {
-                const uint32_t one = kFp8 ? 0x3c003c00u : 0x3f803f80u, man = kFp8 ? 0x03ff03ffu : 0x007f007fu;
-#pragma unroll
-                for (int kind = 0; kind < 3; ++kind) {
-                  uint32_t ind[4];
-#pragma unroll
-                  for (int x = 0; x < 4; ++x) {
-                    const uint32_t frac = b[x] & man;
-                    const uint32_t nan = bad[x] & (((frac & 0xffffu) ? 0xffffu : 0u) | ((frac >> 16) ? 0xffff0000u : 0u));
-                    const uint32_t neg = ((b[x] >> 15) & 0x00010001u) * 0xffffu;
-                    const uint32_t sel = kind == 2 ? nan : bad[x] & ~nan & (kind == 1 ? neg : ~neg);
-                    ind[x] = one & sel;
-                  }
-                  float hit[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-                  mma_16<kFp8>(hit[0], shown, ind[0], ind[1]);
-                  mma_16<kFp8>(hit[1], shown, ind[2], ind[3]);
-                  const float add = kind == 0 ? INFINITY : (kind == 1 ? -INFINITY : __int_as_float(0x7fc00000));
-#pragma unroll
-                  for (int x = 0; x < 4; ++x) {
-                    if (hit[0][x] > 0.f) acc[2 * c][x] += add;
-                    if (hit[1][x] > 0.f) acc[2 * c + 1][x] += add;
-                  }
-                }
-#pragma unroll
-                for (int x = 0; x < 4; ++x) b[x] &= ~bad[x];
-              }
-            }
             mma_16<kFp8>(acc[2 * c], a, b[0], b[1]);
             mma_16<kFp8>(acc[2 * c + 1], a, b[2], b[3]);
           }
@@ -800,6 +861,33 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, a
       __syncwarp();
       if (lane == 0) mbar_arrive(empty + st);
       if (++st == T::kStages) st = 0, ++round;
+    }
+
+    // ---- infinities and NaN that were taken out of V, to the rows that see them
+    // (warps that share a slice may each have found it clean already: the flag tells)
+    if constexpr (kRW > 1) asm volatile("bar.sync 1, %0;" ::"n"(T::kConsumers * 32) : "memory");
+    if (*noted_flag) {
+      for (int i = 0; i < pc.n; ++i) {
+        const int key0 = (pc.first + i) * T::kKeys + kw * T::kSlice;
+        if (!partly_seen(kr, key0, T::kSlice)) continue;
+        for (int key = max(key0, kr.any_lo); key < min(key0 + T::kSlice, kr.any_hi); ++key) {
+          const int page = __ldg(p.table + static_cast<int64_t>(w.b) * p.max_pages + (key >> p.page_log2));
+          if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.num_pages)) continue;
+          const int64_t at = value_at(p, page, w.h, key, kDim);
+#pragma unroll
+          for (int j = 0; j < kDT; ++j)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              // the column of acc[j][x] (E4M3: see the store below)
+              const int col = kFp8 ? 16 * (j / 2) + 4 * t4 + 2 * x + (j & 1) : 8 * j + 2 * t4 + x;
+              const float v = pool_value<kFp8>(p.v_pool, at + col);
+              if (isfinite(v)) continue;
+#pragma unroll
+              for (int y = 0; y < 2; ++y)
+                if (key <= pos[y] && key < w.s.len && (p.window <= 0 || key > pos[y] - p.window)) acc[j][2 * y + x] += v;
+            }
+        }
+      }
     }
 
     // ---- join the key slices of this CTA
@@ -998,7 +1086,7 @@ nvfp4_status launch_attn_split(const AttnJob& p, const KvMaps& maps, cudaStream_
 
 // The split and join grids for heads of kDim values (attention_d*.cu).
 template <int kDim>
-nvfp4_status dispatch_attention(const AttnJob& p, const KvMaps& maps, const nvfp4_kv_cache* cache, const AttnShape& s,
+nvfp4_status dispatch_attention(const AttnJob& p, const KvMaps& maps, bool fp8, const AttnShape& s,
                                 cudaStream_t stream);
 
 }  // namespace nvfp4

@@ -139,10 +139,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
       : "memory");
 }
 
-__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
-  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-
 // 32 bytes to a 32-byte aligned address: a whole sector a thread.
 __device__ __forceinline__ void stg256(void* p, const uint32_t* r) {
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
@@ -206,40 +202,9 @@ struct ChunkBars {
 
 // ------------------------------------------------------------------ the kernel
 
-// Keys that every row of an item sees, [all_lo, all_hi), and that some row sees, [any_lo, any_hi).
-struct KeyRange {
-  int all_lo, all_hi, any_lo, any_hi;
-};
-
-__device__ __forceinline__ KeyRange key_range(const AttnJob& p, const Walk& w) {
-  KeyRange r;
-  const int first = w.s.len - w.s.n + div_by(p.by_group, w.t.row0);
-  const int last = w.s.len - w.s.n + div_by(p.by_group, w.t.row0 + w.t.rows - 1);
-  r.all_hi = min(first + 1, w.s.len);
-  r.all_lo = p.window > 0 ? last - p.window + 1 : 0;
-  r.any_hi = w.t.hi;
-  r.any_lo = w.t.lo;
-  return r;
-}
-
-__device__ __forceinline__ bool partly_seen(const KeyRange& r, int key0, int keys) {
-  return key0 + keys > r.all_hi || key0 < r.all_lo;
-}
-
-// One 16-byte chunk of V (eight 16-bit values) of a key: nothing if no row sees it, and
-// without infinities and NaN.
-template <bool kF16>
-__device__ __forceinline__ uint4 clean_chunk(uint4 v, bool seen, bool& noted) {
-  if (!seen) return make_uint4(0, 0, 0, 0);
-  const uint32_t a = nonfinite_mask<kF16>(v.x), b = nonfinite_mask<kF16>(v.y);
-  const uint32_t c = nonfinite_mask<kF16>(v.z), d = nonfinite_mask<kF16>(v.w);
-  noted = noted || (a | b | c | d) != 0;
-  return make_uint4(v.x & ~a, v.y & ~b, v.z & ~c, v.w & ~d);
-}
-
 template <int kDim, bool kFp8>
 __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
-    attn_chunk_kernel(const AttnJob p, const __grid_constant__ KvMaps maps, const void* v_pool, int64_t page_stride) {
+    attn_chunk_kernel(const AttnJob p, const __grid_constant__ KvMaps maps) {
   using T = ChunkTile<kDim, kFp8>;
   constexpr int kG = T::kGroups, kKeys = T::kKeys;
   extern __shared__ uint8_t smem_raw[];
@@ -721,24 +686,11 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
               if (key < 0) continue;
               const int page = __ldg(p.table + static_cast<int64_t>(w.b) * p.max_pages + (key >> p.page_log2));
               if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.num_pages)) continue;
-              const int64_t at = page * page_stride + ((static_cast<int64_t>(w.h) << p.page_log2) +
-                                                       (key & ((1 << p.page_log2) - 1))) * kDim + c;
-              for (int i = 0; i < 32; i += 2) {
-                float a, b;
-                if constexpr (kFp8) {
-                  uint32_t x, y;
-                  e4m3x4_to_f16x2(*reinterpret_cast<const uint16_t*>(static_cast<const uint8_t*>(v_pool) + at + i), x, y);
-                  a = f16lo_to_f32(x), b = f16hi_to_f32(x);
-                } else {
-                  const uint32_t x = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(v_pool) + at + i);
-                  a = __uint_as_float(x << 16), b = __uint_as_float(x & 0xffff0000u);
-                }
+              const int64_t at = value_at(p, page, w.h, key, kDim) + c;
 #pragma unroll
-                for (int z = 0; z < 32; z += 2)
-                  if (z == i) {
-                    if (!isfinite(a)) o[z] += a;
-                    if (!isfinite(b)) o[z + 1] += b;
-                  }
+              for (int i = 0; i < 32; ++i) {
+                const float v = pool_value<kFp8>(p.v_pool, at + i);
+                if (!isfinite(v)) o[i] += v;
               }
             }
           }
@@ -789,12 +741,10 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
 }
 
 template <int kDim, bool kFp8>
-nvfp4_status launch_attn_chunk(const AttnJob& p, const KvMaps& maps, const void* v_pool, int64_t page_stride,
-                               cudaStream_t stream) {
+nvfp4_status launch_attn_chunk(const AttnJob& p, const KvMaps& maps, cudaStream_t stream) {
   using T = ChunkTile<kDim, kFp8>;
   if (set_smem(attn_chunk_kernel<kDim, kFp8>, T::kSmem) != cudaSuccess) return NVFP4_ERR_CUDA;
-  if (launch_pdl(attn_chunk_kernel<kDim, kFp8>, dim3(kAttnGrid), dim3(T::kThreadsAll), T::kSmem, stream, p, maps,
-                 v_pool, page_stride) != cudaSuccess)
+  if (launch_pdl(attn_chunk_kernel<kDim, kFp8>, dim3(kAttnGrid), dim3(T::kThreadsAll), T::kSmem, stream, p, maps) != cudaSuccess)
     return NVFP4_ERR_CUDA;
   return launch_attn_join<kDim>(p, Tiling{T::kRows, T::kKeys, T::kOver}, kAttnGrid, stream);
 }

@@ -3,7 +3,6 @@
 #include "attention_dispatch.cuh"
 
 namespace nvfp4 {
-template nvfp4_status dispatch_attention<64>(const AttnJob&, const KvMaps&, const nvfp4_kv_cache*, const AttnShape&,
-                                            cudaStream_t);
+template nvfp4_status dispatch_attention<64>(const AttnJob&, const KvMaps&, bool, const AttnShape&, cudaStream_t);
 template nvfp4_status attention_error_word<64>(uint32_t*, int);
 }  // namespace nvfp4
