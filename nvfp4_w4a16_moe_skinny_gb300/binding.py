@@ -123,7 +123,7 @@ class Batch:
             _need(x.dtype == torch.int32 and x.is_contiguous() and x.is_cuda and x.device == kv_len.device,
                   "cu_tokens, kv_len, page_table: contiguous int32 on one GPU")
         self.cu_tokens, self.kv_len, self.page_table, self.max_new = cu_tokens, kv_len, page_table, int(max_new)
-        self.device = kv_len.device
+        self.n_seqs, self.device = n, kv_len.device
         self.c = CBatch(cu_tokens.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), n, page_table.shape[1],
                         self.max_new)
         self.ref = ctypes.byref(self.c)
@@ -213,20 +213,25 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _rows(x: torch.Tensor, what: str, device):
+def _raw_stream(stream, device) -> int:
+    """The stream's handle; the current stream of `device` without building a Stream object."""
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+
+
+def _rows(x: torch.Tensor, what: str, device) -> int:
     """Rows of heads [tokens, heads, dim]: the row stride in elements."""
-    _need(x.dim() == 3 and x.dtype == torch.bfloat16 and x.device == device, f"{what}: bf16 [tokens, heads, dim] on the "
-          "call's GPU")
-    tokens, heads, dim = x.shape
-    row, head, one = x.stride()
-    _need((one == 1 or dim == 1) and (head == dim or heads == 1), f"{what}: the heads of a token have to be contiguous")
-    return row if tokens > 1 else max(row, heads * dim)
+    shape = x.shape
+    if len(shape) == 3 and x.dtype is torch.bfloat16 and x.device == device:
+        row, head, one = x.stride()
+        if one == 1 and (head == shape[2] or shape[1] == 1):
+            return row if shape[0] > 1 else shape[1] * shape[2]
+    raise ValueError(f"{what}: bf16 [tokens, heads, dim] on the call's GPU, the heads of a token contiguous")
 
 
-def _index(x: torch.Tensor, n: int, dtype, what: str, device):
-    _need(x.dtype == dtype and x.shape == (n,) and (n == 1 or x.is_contiguous()) and x.device == device,
-          f"{what}: contiguous {dtype} [{n}] on the call's GPU")
-    return x.data_ptr()
+def _index(x: torch.Tensor, n: int, dtype, what: str, device) -> int:
+    if x.dtype is dtype and x.shape == (n,) and x.device == device and (n < 2 or x.stride(0) == 1):
+        return x.data_ptr()
+    raise ValueError(f"{what}: contiguous {dtype} [{n}] on the call's GPU")
 
 
 class Library:
@@ -485,15 +490,20 @@ class Library:
         dev = x.device
         stride = _rows(x, "x", dev)
         tokens, heads, dim = x.shape
+        pairs = inv_freq.shape[0]
         if out is None:
             out = torch.empty((tokens, heads, dim), dtype=torch.bfloat16, device=dev)
-        _need(out.shape == x.shape, "out: the shape of x")
-        freq = _index(inv_freq, inv_freq.shape[0], torch.float64, "inv_freq", dev)
-        self._check("rope_apply", self.lib.rope_apply(
-            x.data_ptr(), stride, tokens, heads, dim, _index(positions, tokens, torch.int32, "positions", dev), freq,
-            2 * inv_freq.shape[0], amplitude,
+            out_stride = heads * dim
+        else:
+            _need(out.shape == x.shape, "out: the shape of x")
+            out_stride = _rows(out, "out", dev)
+        st = self.lib.rope_apply(
+            x.data_ptr(), stride, tokens, heads, dim, _index(positions, tokens, torch.int32, "positions", dev),
+            _index(inv_freq, pairs, torch.float64, "inv_freq", dev), 2 * pairs, amplitude,
             (NVFP4_ROPE_INTERLEAVED if interleaved else 0) | (NVFP4_ROPE_INVERSE if inverse else 0), out.data_ptr(),
-            _rows(out, "out", dev), _stream(stream)))
+            out_stride, _raw_stream(stream, dev))
+        if st:
+            raise NVFP4Error("rope_apply", st)
         return out
 
     def kv_append(self, cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
@@ -512,20 +522,26 @@ class Library:
             rot = 2 * inv_freq.shape[0]
             freq = _index(inv_freq, inv_freq.shape[0], torch.float64, "inv_freq", dev)
             pos = _index(positions, tokens, torch.int32, "positions", dev)
-        q_heads = q_stride = q_out_stride = 0
+        q_ptr = out_ptr = None
+        q_heads = q_stride = out_stride = 0
         if q is not None:
             q_heads = q.shape[1]
             _need(q.shape == (tokens, q_heads, dim), "q: [tokens, heads, head_dim] of the cache")
-            q_stride = _rows(q, "q", dev)
+            q_ptr, q_stride = q.data_ptr(), _rows(q, "q", dev)
             if q_out is None:
                 q_out = torch.empty((tokens, q_heads, dim), dtype=torch.bfloat16, device=dev)
-            _need(q_out.shape == q.shape, "q_out: the shape of q")
-            q_out_stride = _rows(q_out, "q_out", dev)
-        self._check("kv_append", self.lib.kv_append(
+                out_stride = q_heads * dim
+            else:
+                _need(q_out.shape == q.shape, "q_out: the shape of q")
+                out_stride = _rows(q_out, "q_out", dev)
+            out_ptr = q_out.data_ptr()
+        st = self.lib.kv_append(
             cache.ref, k.data_ptr(), _rows(k, "k", dev), v.data_ptr(), _rows(v, "v", dev), tokens,
             _index(slots, tokens, torch.int64, "slots", dev), pos, freq, rot, amplitude,
-            NVFP4_ROPE_INTERLEAVED if interleaved else 0, _ptr(q), q_stride, q_heads, _ptr(q_out), q_out_stride,
-            _stream(stream)))
+            NVFP4_ROPE_INTERLEAVED if interleaved else 0, q_ptr, q_stride, q_heads, out_ptr, out_stride,
+            _raw_stream(stream, dev))
+        if st:
+            raise NVFP4Error("kv_append", st)
         return q_out
 
     def paged_attention(self, q: torch.Tensor, cache: KVCache, batch: Batch, scale: float = None, softcap: float = 0.0,
@@ -536,35 +552,41 @@ class Library:
         dev = cache.device
         stride = _rows(q, "q", dev)
         tokens, heads, dim = q.shape
-        _need(dim == cache.head_dim and batch.device == dev, "q: [tokens, heads, head_dim] of the cache; the batch on its "
-              "GPU")
+        _need(dim == cache.head_dim and batch.device == dev,
+              "q: [tokens, heads, head_dim] of the cache; the batch on its GPU")
         if out is None:
             out = torch.empty((tokens, heads, dim), dtype=torch.bfloat16, device=dev)
-        _need(out.shape == q.shape, "out: the shape of q")
-        if with_lse and lse is None:
+            out_stride = heads * dim
+        else:
+            _need(out.shape == q.shape, "out: the shape of q")
+            out_stride = _rows(out, "out", dev)
+        if lse is not None:
+            _need(lse.shape == (tokens, heads) and lse.dtype is torch.float32 and lse.is_contiguous()
+                  and lse.device == dev, "lse: contiguous fp32 [tokens, heads]")
+        elif with_lse:
             lse = torch.empty((tokens, heads), dtype=torch.float32, device=dev)
-        _need(lse is None or (lse.shape == (tokens, heads) and lse.dtype == torch.float32 and lse.is_contiguous()
-                              and lse.device == dev), "lse: contiguous fp32 [tokens, heads]")
-        s = torch.cuda.current_stream() if stream is None else stream
-        nbytes = self.lib.paged_attention_workspace_bytes(tokens, batch.c.n_seqs, batch.max_new, heads,
-                                                          cache.n_kv_heads, dim)
-        ws = self._stream_workspace("attention", max(nbytes, 16), dev, s)
-        self._check("paged_attention", self.lib.paged_attention(
+        raw = _raw_stream(stream, dev)
+        nbytes = self.lib.paged_attention_workspace_bytes(tokens, batch.n_seqs, batch.max_new, heads, cache.n_kv_heads,
+                                                          dim)
+        ws = self._stream_workspace("attention", nbytes, dev, raw, stream)
+        st = self.lib.paged_attention(
             cache.ref, batch.ref, q.data_ptr(), stride, tokens, heads, dim ** -0.5 if scale is None else scale, softcap,
-            window, out.data_ptr(), _rows(out, "out", dev), _ptr(lse), ws.data_ptr(), ws.numel(), s.cuda_stream))
+            window, out.data_ptr(), out_stride, None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), raw)
+        if st:
+            raise NVFP4Error("paged_attention", st)
         return (out, lse) if with_lse else out
 
-    def _stream_workspace(self, key, nbytes: int, device, stream) -> torch.Tensor:
+    def _stream_workspace(self, key, nbytes: int, device, raw: int, stream) -> torch.Tensor:
         """A workspace of its own for each (call kind, device, stream): calls on different streams may overlap.  It is
         allocated on the stream that uses it, so that one that is outgrown is not reused under a running call.  A
         captured call gets one from its graph's pool, which lives and dies with the graph."""
-        with torch.cuda.stream(stream):
-            if torch.cuda.is_current_stream_capturing():
-                return torch.empty(nbytes, dtype=torch.uint8, device=device)
-            k = (key, device, stream.cuda_stream)
-            cur = self._ws.get(k)
-            if cur is None or cur.numel() < nbytes:
-                cur = self._ws[k] = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        cur = self._ws.get((key, device, raw))
+        if cur is not None and cur.numel() >= nbytes and not torch.cuda.is_current_stream_capturing():
+            return cur
+        with torch.cuda.stream(torch.cuda.current_stream(device) if stream is None else stream):
+            cur = torch.empty(max(nbytes, 32), dtype=torch.uint8, device=device)
+            if not torch.cuda.is_current_stream_capturing():
+                self._ws[(key, device, raw)] = cur
         return cur
 
     # -------------------------------------------------------------- call plans

@@ -412,7 +412,7 @@ struct AttnTile {
   static constexpr int kKeys = kSlice * kKW;                         // keys of a unit
   static constexpr int kConsumers = kRW * kKW;
   static constexpr int kThreadsAll = (kConsumers + 1) * 32;
-  static constexpr int kOver = 1;                                    // an item's own cost, in units
+  static constexpr int kOver = 3;                                    // an item's own cost, in units
   static constexpr int kEl = kFp8 ? 1 : 2;
   static constexpr int kRowB = kDim * kEl < 128 ? kDim * kEl : 128;  // bytes of a row of a block
   static constexpr int kSub = kDim * kEl / kRowB;                    // blocks across a head

@@ -36,7 +36,7 @@ struct ChunkTile {
   static constexpr int kRows = 128 * kGroups;
   static constexpr int kKeys = kDim == 256 ? 64 : 128;
   static constexpr int kSBuf = kDim == 256 ? 2 : 1;        // S buffers per group
-  static constexpr int kOver = 3;                          // an item's own cost, in units
+  static constexpr int kOver = 4;                          // an item's own cost, in units
   static constexpr int kThreadsAll = 128 + 128 * kGroups;
   static constexpr int kEl = kFp8 ? 1 : 2;
   // boxes of the pool (as AttnTile names them, for tile_offset)
