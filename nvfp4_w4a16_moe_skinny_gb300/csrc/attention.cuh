@@ -80,8 +80,10 @@ struct KvMaps {
 
 // Tiling of one kernel: rows of a row tile, keys of a unit, and what starting and
 // finishing an item costs, counted in units (the ranges are balanced with it).
+// `snap`: a range boundary that falls this close to an item's end moves there, so that no
+// item is split for a few units.
 struct Tiling {
-  int rows, keys, over;
+  int rows, keys, over, snap;
 };
 
 // Quotient of x < 2^31 by the divisor that `d` was made for (fast_div): a multiply by the
@@ -125,26 +127,11 @@ __device__ __forceinline__ RowTile row_tile(const AttnJob& p, const Sequence& s,
   return t;
 }
 
-// Units, overheads included, of each lane's sequence b (0 past the last): up to eight
-// row tiles by the lane itself, longer ones by the whole warp, 32 tiles at a time.  All lanes
-// of a warp call it.
-__device__ __forceinline__ long long sequence_units(const AttnJob& p, int b, const Tiling& g) {
-  const int lane = threadIdx.x & 31;
-  Sequence s{};
-  if (b < p.n_seqs) s = sequence_of(p, b, g);
+// Units of `s`, overheads included, by one lane or (lane, step) by the lanes of a warp.
+__device__ __forceinline__ long long tile_units(const AttnJob& p, const Sequence& s, int first, int step, const Tiling& g) {
   long long u = 0;
-  const bool large = s.tiles > 8;
-  if (!large)
-    for (int rt = 0; rt < s.tiles; ++rt) u += row_tile(p, s, rt, g).units + g.over;
-  for (unsigned todo = __ballot_sync(0xffffffffu, large); todo; todo &= todo - 1) {
-    const int who = __ffs(todo) - 1;
-    const Sequence o = sequence_of(p, __shfl_sync(0xffffffffu, b, who), g);
-    long long part = 0;
-    for (int rt = lane; rt < o.tiles; rt += 32) part += row_tile(p, o, rt, g).units + g.over;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) part += __shfl_xor_sync(0xffffffffu, part, d);
-    if (lane == who) u = part;
-  }
+#pragma unroll 1
+  for (int rt = first; rt < s.tiles; rt += step) u += row_tile(p, s, rt, g).units + g.over;
   return u * p.n_kv;
 }
 
@@ -179,12 +166,19 @@ struct Found {
   long long before;
 };
 
-// Block-wide scan of the sequences' units (every thread of the block calls it; scratch:
-// 36 words of shared memory).  Sets the ranges and, if range c is in use, finds where
-// its first unit lies.
+// What find_range keeps in shared memory.
+struct RangeScratch {
+  long long warp_sum[32], before;
+  int seq, n_long;
+};
+
+// Block-wide scan of the sequences' units (every thread of the block calls it).  Sets the
+// ranges and, if range c is in use, finds where its first unit lies.  A thread sums its
+// sequence's row tiles itself if they are few; long sequences go through a list (kList
+// entries of scratch memory) to whole warps.
 template <int kThreadsInBlock>
 __device__ __forceinline__ void find_range(const AttnJob& p, const Tiling& g, int ctas, int c, Ranges* ranges,
-                                           Found* found, long long* scratch) {
+                                           Found* found, RangeScratch* sh, longlong2* list) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int kNW = kThreadsInBlock / 32;
   long long mine = 0, incl = 0;
@@ -197,19 +191,40 @@ __device__ __forceinline__ void find_range(const AttnJob& p, const Tiling& g, in
 #pragma unroll 1
     for (int b0 = 0; b0 < p.n_seqs; b0 += kThreadsInBlock) {
       if (pass == 0 || !once) {
-        mine = sequence_units(p, b0 + threadIdx.x, g);
+        const int b = b0 + threadIdx.x;
+        Sequence s{};
+        if (b < p.n_seqs) s = sequence_of(p, b, g);
+        const bool is_long = s.tiles > 4;
+        mine = is_long ? 0 : tile_units(p, s, 0, 1, g);
+        if (threadIdx.x == 0) sh->n_long = 0;
+        if (__syncthreads_or(is_long)) {
+          int at = 0;
+          if (is_long) {
+            at = atomicAdd(&sh->n_long, 1);
+            list[at].x = b;
+          }
+          __syncthreads();
+          for (int i = warp; i < sh->n_long; i += kNW) {
+            long long part = tile_units(p, sequence_of(p, static_cast<int>(list[i].x), g), lane, 32, g);
+#pragma unroll 1
+            for (int d = 16; d > 0; d >>= 1) part += __shfl_xor_sync(0xffffffffu, part, d);
+            if (lane == 0) list[i].y = part;
+          }
+          __syncthreads();
+          if (is_long) mine = list[at].y;
+        }
         incl = mine;
-#pragma unroll
+#pragma unroll 1
         for (int o = 1; o < 32; o <<= 1) {
           const long long v = __shfl_up_sync(0xffffffffu, incl, o);
           if (lane >= o) incl += v;
         }
-        if (lane == 31) scratch[warp] = incl;
+        if (lane == 31) sh->warp_sum[warp] = incl;
         __syncthreads();
         long long pre = base;
 #pragma unroll 1
         for (int w = 0; w < kNW; ++w) {
-          const long long v = scratch[w];
+          const long long v = sh->warp_sum[w];
           if (w < warp) pre += v;
           base += v;
         }
@@ -218,8 +233,8 @@ __device__ __forceinline__ void find_range(const AttnJob& p, const Tiling& g, in
       if (pass == 1) {
         const long long u = ranges->start(c);
         if (mine > 0 && u >= incl - mine && u < incl) {
-          scratch[32] = b0 + threadIdx.x;
-          scratch[33] = incl - mine;
+          sh->seq = b0 + threadIdx.x;
+          sh->before = incl - mine;
         }
       }
       __syncthreads();
@@ -229,8 +244,8 @@ __device__ __forceinline__ void find_range(const AttnJob& p, const Tiling& g, in
       if (c >= ranges->grid) return;
     }
   }
-  found->seq = static_cast<int>(scratch[32]);
-  found->before = scratch[33];
+  found->seq = sh->seq;
+  found->before = sh->before;
 }
 
 // A place in the list of items (sequence, row tile, kv head).  All roles of a CTA walk
@@ -278,7 +293,7 @@ __device__ __forceinline__ void walk_to(const AttnJob& p, Walk& w, long long u, 
         const bool in = rt + lane < w.s.tiles;
         const long long mine = in ? static_cast<long long>(row_tile(p, w.s, rt + lane, g).units + g.over) * p.n_kv : 0;
         long long incl = mine;
-#pragma unroll
+#pragma unroll 1
         for (int o = 1; o < 32; o <<= 1) {
           const long long v = __shfl_up_sync(0xffffffffu, incl, o);
           if (lane >= o) incl += v;
@@ -300,9 +315,16 @@ __device__ __forceinline__ void walk_to(const AttnJob& p, Walk& w, long long u, 
   }
 }
 
+// Where a range boundary d units into an item of `units` tiles lies after snapping: 0, the
+// whole span, or d.
+__device__ __forceinline__ int snapped(int d, int units, const Tiling& g) {
+  const int span = units + g.over, t = min(g.snap, (span - 1) / 2);
+  return d <= t ? 0 : (d >= span - t ? span : d);
+}
+
 // The share of the walk's item that range [u0, u1) of CTA c holds, from unit u on: key tiles
-// [first, first + n) (none, if only the item's overhead falls into the range), and
-// where an unfinished share goes.
+// [first, first + n) (none, if only the item's overhead falls into the range, or if the
+// boundary has moved), and where an unfinished share goes.
 struct Share {
   int first, n, slot;
   bool whole;
@@ -312,12 +334,14 @@ struct Share {
 __device__ __forceinline__ Share share_at(const Walk& w, long long u, long long u0, long long u1, int c,
                                           const Tiling& g) {
   Share q;
-  const int from = static_cast<int>(u - w.item0);
-  q.end = min(w.item0 + w.t.units + g.over, u1);
-  q.n = max(0, min(w.t.units, static_cast<int>(q.end - w.item0)) - from);
+  const int units = w.t.units, span = units + g.over;
+  const int from = u == u0 ? snapped(static_cast<int>(u - w.item0), units, g) : 0;
+  const int to = u1 < w.item0 + span ? snapped(static_cast<int>(u1 - w.item0), units, g) : span;
+  q.end = min(w.item0 + span, u1);
+  q.n = max(0, min(units, to) - from);
   q.first = w.t.tile0 + from;
-  q.whole = q.n == w.t.units;
-  q.slot = 2 * c + (u == u0 ? 0 : 1);
+  q.whole = q.n == units;
+  q.slot = 2 * c + (from > 0 ? 0 : 1);  // a range starts inside at most one item and ends inside one
   return q;
 }
 
@@ -412,7 +436,7 @@ struct AttnTile {
   static constexpr int kKeys = kSlice * kKW;                         // keys of a unit
   static constexpr int kConsumers = kRW * kKW;
   static constexpr int kThreadsAll = (kConsumers + 1) * 32;
-  static constexpr int kOver = 3;                                    // an item's own cost, in units
+  static constexpr int kOver = 3, kSnap = 2;                         // an item's own cost, in units (Tiling)
   static constexpr int kEl = kFp8 ? 1 : 2;
   static constexpr int kRowB = kDim * kEl < 128 ? kDim * kEl : 128;  // bytes of a row of a block
   static constexpr int kSub = kDim * kEl / kRowB;                    // blocks across a head
@@ -421,7 +445,8 @@ struct AttnTile {
   static constexpr int kStageB = 2 * kTileB;
   static constexpr int kCtas = attn_ctas(kDim);
   static constexpr int kQB = kRows * kDim * 2;                       // Q: [kDim / 64][kRows][128 bytes]
-  static constexpr int kJoinB = kKW > 1 ? kRW * 32 * (kDim / 2 + 4) * 4 : 0;  // one slice's sums
+  // a quarter (kKW = 4) or half of the columns of each warp's sums, its reference and sum
+  static constexpr int kJoinB = kKW > 1 ? kConsumers * 32 * (kDim / 2 / kKW + 4) * 4 : 0;
   static constexpr int kFit = ((kCtas == 1 ? 227 : 113) * 1024 - 1024 - 1024 - kJoinB - kQB) / kStageB;
   static constexpr int kStages = kFit > 6 ? 6 : kFit;
   static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageB + kQB + kJoinB + 1024;
@@ -531,8 +556,8 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, a
   uint8_t* tail = smem_raw + (join + T::kJoinB - raw);
   uint64_t* full = reinterpret_cast<uint64_t*>(tail);  // [stages]
   uint64_t* empty = full + T::kStages;                 // [stages]
-  long long* scratch = reinterpret_cast<long long*>(empty + T::kStages);
-  float* q_back = reinterpret_cast<float*>(scratch + 36);  // [kRows] undoes the scaling of a row of Q
+  RangeScratch* scratch = reinterpret_cast<RangeScratch*>(empty + T::kStages);
+  float* q_back = reinterpret_cast<float*>(scratch + 1);  // [kRows] undoes the scaling of a row of Q
   // an infinity or NaN was taken out of V, in this CTA's items so far
   volatile int* noted_flag = reinterpret_cast<volatile int*>(q_back + T::kRows);
 
@@ -546,10 +571,14 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, a
   pdl_launch_dependents();
   __syncthreads();
 
-  constexpr Tiling kTiling{T::kRows, T::kKeys, T::kOver};
+  constexpr Tiling kTiling{T::kRows, T::kKeys, T::kOver, T::kSnap};
   Found f;
   Ranges ranges;
-  find_range<T::kThreadsAll>(p, kTiling, gridDim.x, blockIdx.x, &ranges, &f, scratch);
+  find_range<T::kThreadsAll>(p, kTiling, gridDim.x, blockIdx.x, &ranges, &f, scratch,
+                             reinterpret_cast<longlong2*>(smem_raw + (ring - raw)));
+  // (the list lies where the first tiles will: its last reads come before the copies)
+  fence_proxy_async_smem();
+  __syncthreads();
   if (static_cast<int>(blockIdx.x) >= ranges.grid) return;
   const long long u0 = ranges.start(blockIdx.x), u1 = ranges.start(blockIdx.x + 1);
   Walk w;
@@ -898,79 +927,97 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, a
     }
     if constexpr (kKW > 1) {
       float* buf = reinterpret_cast<float*>(smem_raw + (join - raw));
-#pragma unroll 1
-      for (int from = kKW - 1; from > 0; --from) {  // each slice's sums go to the one before it
-        asm volatile("bar.sync 1, %0;" ::"n"(T::kConsumers * 32) : "memory");
-        if (kw == from) {
-          float* o = buf + rw * 32 * (kDim / 2 + 4) + lane;
+      float4* ml = reinterpret_cast<float4*>(buf + T::kJoinB / 4) - T::kConsumers * 32;  // at the end of the buffer
+      ml[warp * 32 + lane] = make_float4(m[0], m[1], l[0], l[1]);
+      asm volatile("bar.sync 1, %0;" ::"n"(T::kConsumers * 32) : "memory");
+      // one reference and sum for all slices; every warp scales its sums to it
+      float f[2];
+      float4 o[kKW];
 #pragma unroll
-          for (int j = 0; j < kDT; ++j)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) o[(4 * j + x) * 32] = acc[j][x];
-          o[(4 * kDT) * 32] = m[0], o[(4 * kDT + 1) * 32] = m[1];
-          o[(4 * kDT + 2) * 32] = l[0], o[(4 * kDT + 3) * 32] = l[1];
-        }
-        asm volatile("bar.sync 1, %0;" ::"n"(T::kConsumers * 32) : "memory");
-        if (kw == from - 1) {
-          const float* o = buf + rw * 32 * (kDim / 2 + 4) + lane;
-          float fa[2], fb[2];
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const float mo = o[(4 * kDT + x) * 32];
-            const float next = fmaxf(m[x], mo);
-            fa[x] = next == -INFINITY ? 1.0f : exp2_approx(m[x] - next);
-            fb[x] = next == -INFINITY ? 1.0f : exp2_approx(mo - next);
-            m[x] = next;
-            l[x] = l[x] * fa[x] + o[(4 * kDT + 2 + x) * 32] * fb[x];
-          }
-#pragma unroll
-          for (int j = 0; j < kDT; ++j)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) acc[j][x] = acc[j][x] * fa[x >> 1] + o[(4 * j + x) * 32] * fb[x >> 1];
-        }
-      }
-    }
-    // ---- write: the finished rows, or this piece's share of them
-    if (kw == 0) {
+      for (int i = 0; i < kKW; ++i) o[i] = ml[(i * kRW + rw) * 32 + lane];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        if (!live[x]) continue;
-        if (pc.whole) {
-          const float vs = (kFp8 && p.v_scale) ? __ldg(p.v_scale + w.h) : 1.0f;
-          const float inv = l[x] == 0.f ? 0.f : vs / l[x];
-          const int64_t row = w.s.tok0 + tok[x];
-          uint16_t* o = p.out + row * p.out_stride + static_cast<int64_t>(head[x]) * kDim;
+        float next = -INFINITY, sum = 0.f;
 #pragma unroll
-          for (int j = 0; j < kDT; j += 2) {
-            const float v0 = acc[j][2 * x] * inv, v1 = acc[j][2 * x + 1] * inv;
-            const float v2 = acc[j + 1][2 * x] * inv, v3 = acc[j + 1][2 * x + 1] * inv;
-            if constexpr (!kFp8) {
-              *reinterpret_cast<uint32_t*>(o + 8 * j + 2 * t4) = f32x2_to_bf16x2(v0, v1);
-              *reinterpret_cast<uint32_t*>(o + 8 * j + 8 + 2 * t4) = f32x2_to_bf16x2(v2, v3);
-            } else {
-              *reinterpret_cast<uint2*>(o + 8 * j + 4 * t4) =
-                  make_uint2(f32x2_to_bf16x2(v0, v2), f32x2_to_bf16x2(v1, v3));
+        for (int i = 0; i < kKW; ++i) next = fmaxf(next, x ? o[i].y : o[i].x);
+#pragma unroll
+        for (int i = 0; i < kKW; ++i)
+          sum += (x ? o[i].w : o[i].z) * (next == -INFINITY ? 1.0f : exp2_approx((x ? o[i].y : o[i].x) - next));
+        f[x] = next == -INFINITY ? 1.0f : exp2_approx(m[x] - next);
+        m[x] = next, l[x] = sum;
+      }
+#pragma unroll
+      for (int j = 0; j < kDT; ++j) acc[j][0] *= f[0], acc[j][1] *= f[0], acc[j][2] *= f[1], acc[j][3] *= f[1];
+      // each slice's warp ends with the columns [kw, kw + 1) * kDT / kKW of all slices: in
+      // round r it hands slice kw + r that slice's columns
+      constexpr int kPart = kDT / kKW;
+#pragma unroll 1
+      for (int r = 1; r < kKW; ++r) {
+        const int dest = (kw + r) % kKW;
+        float4* give = reinterpret_cast<float4*>(buf) + (dest * kRW + rw) * 32 * kPart + lane;
+#pragma unroll
+        for (int q = 0; q < kKW; ++q)
+          if (q == dest) {
+#pragma unroll
+            for (int j = 0; j < kPart; ++j)
+              give[j * 32] = make_float4(acc[q * kPart + j][0], acc[q * kPart + j][1], acc[q * kPart + j][2], acc[q * kPart + j][3]);
+          }
+        asm volatile("bar.sync 1, %0;" ::"n"(T::kConsumers * 32) : "memory");
+        const float4* take = reinterpret_cast<const float4*>(buf) + (kw * kRW + rw) * 32 * kPart + lane;
+#pragma unroll
+        for (int q = 0; q < kKW; ++q)
+          if (q == kw) {
+#pragma unroll
+            for (int j = 0; j < kPart; ++j) {
+              const float4 v = take[j * 32];
+              acc[q * kPart + j][0] += v.x, acc[q * kPart + j][1] += v.y;
+              acc[q * kPart + j][2] += v.z, acc[q * kPart + j][3] += v.w;
             }
           }
-          if (p.lse && t4 == 0)
-            p.lse[row * p.n_heads + head[x]] = l[x] == 0.f ? -INFINITY : (m[x] + log2f(l[x])) * 0.6931471805599453f;
-        } else {
-          const int r = rw * 16 + g + 8 * x;
-          float* o = p.part + (static_cast<int64_t>(pc.slot) * T::kRows + r) * kDim;
+        asm volatile("bar.sync 1, %0;" ::"n"(T::kConsumers * 32) : "memory");
+      }
+    }
+    // ---- write: the finished rows, or this share of them; each key slice's warp its columns
+    constexpr int kOut = kDT / kKW;
+    float vs = 1.0f;
+    if constexpr (kFp8) vs = p.v_scale ? __ldg(p.v_scale + w.h) : 1.0f;
 #pragma unroll
-          for (int j = 0; j < kDT; j += 2) {
+    for (int x = 0; x < 2; ++x) {
+      if (!live[x]) continue;
+      const int64_t row = w.s.tok0 + tok[x];
+      const int r = rw * 16 + g + 8 * x;
+      const float inv = l[x] == 0.f ? 0.f : vs / l[x];
+      uint16_t* o = p.out + row * p.out_stride + static_cast<int64_t>(head[x]) * kDim;
+      float* part = p.part + (static_cast<int64_t>(pc.slot) * T::kRows + r) * kDim;
+#pragma unroll
+      for (int q = 0; q < kKW; ++q)
+        if (q == kw) {
+#pragma unroll
+          for (int j = q * kOut; j < (q + 1) * kOut; j += 2) {
+            const float v0 = acc[j][2 * x], v1 = acc[j][2 * x + 1], v2 = acc[j + 1][2 * x], v3 = acc[j + 1][2 * x + 1];
             if constexpr (!kFp8) {
-              *reinterpret_cast<float2*>(o + 8 * j + 2 * t4) = make_float2(acc[j][2 * x], acc[j][2 * x + 1]);
-              *reinterpret_cast<float2*>(o + 8 * j + 8 + 2 * t4) = make_float2(acc[j + 1][2 * x], acc[j + 1][2 * x + 1]);
-            } else {
-              *reinterpret_cast<float4*>(o + 8 * j + 4 * t4) =
-                  make_float4(acc[j][2 * x], acc[j + 1][2 * x], acc[j][2 * x + 1], acc[j + 1][2 * x + 1]);
+              if (pc.whole) {
+                *reinterpret_cast<uint32_t*>(o + 8 * j + 2 * t4) = f32x2_to_bf16x2(v0 * inv, v1 * inv);
+                *reinterpret_cast<uint32_t*>(o + 8 * j + 8 + 2 * t4) = f32x2_to_bf16x2(v2 * inv, v3 * inv);
+              } else {
+                *reinterpret_cast<float2*>(part + 8 * j + 2 * t4) = make_float2(v0, v1);
+                *reinterpret_cast<float2*>(part + 8 * j + 8 + 2 * t4) = make_float2(v2, v3);
+              }
+            } else {  // (columns j and j + 1 hold alternate values)
+              if (pc.whole)
+                *reinterpret_cast<uint2*>(o + 8 * j + 4 * t4) =
+                    make_uint2(f32x2_to_bf16x2(v0 * inv, v2 * inv), f32x2_to_bf16x2(v1 * inv, v3 * inv));
+              else
+                *reinterpret_cast<float4*>(part + 8 * j + 4 * t4) = make_float4(v0, v2, v1, v3);
             }
           }
-          if (t4 == 0) {
-            float* ml = p.part + static_cast<int64_t>(2) * gridDim.x * T::kRows * kDim;
-            *reinterpret_cast<float2*>(ml + (static_cast<int64_t>(pc.slot) * T::kRows + r) * 2) = make_float2(m[x], l[x]);
-          }
+        }
+      if (kw == 0 && t4 == 0) {
+        if (!pc.whole) {
+          float* ml = p.part + static_cast<int64_t>(2) * gridDim.x * T::kRows * kDim;
+          *reinterpret_cast<float2*>(ml + (static_cast<int64_t>(pc.slot) * T::kRows + r) * 2) = make_float2(m[x], l[x]);
+        } else if (p.lse) {
+          p.lse[row * p.n_heads + head[x]] = l[x] == 0.f ? -INFINITY : (m[x] + log2f(l[x])) * 0.6931471805599453f;
         }
       }
     }
@@ -982,17 +1029,21 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, a
 constexpr int kJoinThreads = 128;
 
 // Block (c, y): if range boundary c is the first one inside an item, joins that
-// item's pieces for four of its rows (a warp a row), in range order.
-template <int kDim>
+// item's pieces in range order, for some of its rows.  The split kernel's shares are
+// rows of kDim sums, joined a warp a row; the chunk kernel's (kColumns) come as blocks of
+// eight columns of all rows, as its threads hold a row each, and are joined a thread a
+// row and block.
+template <int kDim, bool kColumns>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnJob p, int split_grid, const Tiling g) {
-  __shared__ long long scratch[36];
+  __shared__ RangeScratch scratch;
+  __shared__ longlong2 list[kJoinThreads];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int tile_rows = g.rows;
   Found f;
   Ranges ranges;
   // lengths are complete before the split grid starts: only its pieces are waited for
   const int c = blockIdx.x + 1;
-  find_range<kJoinThreads>(p, g, split_grid, c, &ranges, &f, scratch);
+  find_range<kJoinThreads>(p, g, split_grid, c, &ranges, &f, &scratch, list);
   Walk w;
   bool first = false;
   if (c < ranges.grid) {
@@ -1001,20 +1052,60 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnJob p
     const long long u = ranges.start(c);
     walk_to(p, w, u, g);
     // a boundary among the item's tiles, and the first one
-    first = u > w.item0 && u < w.item0 + w.t.units && ranges.start(c - 1) <= w.item0;
+    const int d = snapped(static_cast<int>(u - w.item0), w.t.units, g);
+    const long long before = ranges.start(c - 1) - w.item0;
+    first = d > 0 && d < w.t.units && (before <= 0 || snapped(static_cast<int>(before), w.t.units, g) == 0);
   }
   pdl_launch_dependents();
   pdl_wait();  // every block waits, so that this grid's end means that the split grid has ended
   if (!first) return;
   // first and last range that hold a tile of the item
-  const int c0 = c - 1, c1 = ranges.holder(w.item0 + w.t.units - 1);
-  const int skip = w.item0 > ranges.start(c0) ? 1 : 0;  // the first share is its range's second slot
+  const int span = w.t.units + g.over, cut = min(w.t.units, span - min(g.snap, (span - 1) / 2));
+  const int c0 = c - 1, c1 = ranges.holder(w.item0 + cut - 1);
   const float* ml = p.part + static_cast<int64_t>(2) * split_grid * tile_rows * kDim;
+  if constexpr (kColumns) {
+    for (int i = blockIdx.y * kJoinThreads + threadIdx.x; i < tile_rows * (kDim / 16); i += gridDim.y * kJoinThreads) {
+      const int r = i % tile_rows, block = i / tile_rows * 2;
+      if (r >= w.t.rows) continue;
+      float m = -INFINITY;
+      for (int j = c0; j <= c1; ++j)
+        m = fmaxf(m, ml[(static_cast<int64_t>(2 * j + (j == c0 ? 1 : 0)) * tile_rows + r) * 2]);
+      float acc[16], l = 0.f;
+#pragma unroll
+      for (int x = 0; x < 16; ++x) acc[x] = 0.f;
+#pragma unroll 2
+      for (int j = c0; j <= c1; ++j) {
+        const int64_t slot = 2 * j + (j == c0 ? 1 : 0);
+        const float2 v = *reinterpret_cast<const float2*>(ml + (slot * tile_rows + r) * 2);
+        const float a = m == -INFINITY ? 1.0f : exp2_approx(v.x - m);
+        l += a * v.y;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float4* o = reinterpret_cast<const float4*>(p.part + slot * tile_rows * kDim +
+                                                            (static_cast<int64_t>(block + h) * tile_rows + r) * 8);
+          const float4 x = o[0], y = o[1];
+          acc[8 * h] += a * x.x, acc[8 * h + 1] += a * x.y, acc[8 * h + 2] += a * x.z, acc[8 * h + 3] += a * x.w;
+          acc[8 * h + 4] += a * y.x, acc[8 * h + 5] += a * y.y, acc[8 * h + 6] += a * y.z, acc[8 * h + 7] += a * y.w;
+        }
+      }
+      const int rr = w.t.row0 + r, tok = div_by(p.by_group, rr), head = w.h * p.group + rr - tok * p.group;
+      const int64_t row = w.s.tok0 + tok;
+      const float inv = l == 0.f ? 0.f : (p.v_scale ? __ldg(p.v_scale + w.h) : 1.0f) / l;
+      uint4* o = reinterpret_cast<uint4*>(p.out + row * p.out_stride + static_cast<int64_t>(head) * kDim + block * 8);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        o[h] = make_uint4(f32x2_to_bf16x2(acc[8 * h] * inv, acc[8 * h + 1] * inv), f32x2_to_bf16x2(acc[8 * h + 2] * inv, acc[8 * h + 3] * inv),
+                          f32x2_to_bf16x2(acc[8 * h + 4] * inv, acc[8 * h + 5] * inv), f32x2_to_bf16x2(acc[8 * h + 6] * inv, acc[8 * h + 7] * inv));
+      if (p.lse && block == 0)
+        p.lse[row * p.n_heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    }
+    return;
+  }
   constexpr int kPer = kDim / 32;
   for (int r = blockIdx.y * 4 + warp; r < w.t.rows; r += gridDim.y * 4) {
     float m = -INFINITY;
     for (int i = c0 + lane; i <= c1; i += 32) {
-      const int slot = 2 * i + (i == c0 ? skip : 0);
+      const int slot = 2 * i + (i == c0 ? 1 : 0);
       m = fmaxf(m, ml[(static_cast<int64_t>(slot) * tile_rows + r) * 2]);
     }
 #pragma unroll
@@ -1025,7 +1116,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnJob p
     float l = 0.f;
 #pragma unroll 4
     for (int i = c0; i <= c1; ++i) {
-      const int slot = 2 * i + (i == c0 ? skip : 0);
+      const int slot = 2 * i + (i == c0 ? 1 : 0);
       const int64_t row = static_cast<int64_t>(slot) * tile_rows + r;
       const float2 v = *reinterpret_cast<const float2*>(ml + row * 2);
       const float a = m == -INFINITY ? 1.0f : exp2_approx(v.x - m);
@@ -1063,12 +1154,12 @@ inline AttnShape attn_shape(int dim, bool fp8, int64_t rows) {
   return {rw, kw, 16 * rw, attn_slice(dim, fp8, kw) * kw, false};
 }
 
-template <int kDim>
+template <int kDim, bool kColumns>
 nvfp4_status launch_attn_join(const AttnJob& p, const Tiling& g, int grid, cudaStream_t stream) {
   // one unit an item: nothing can be split
   if ((static_cast<int64_t>(p.max_pages) << p.page_log2) > g.keys) {
     const int rows = g.rows / 4 < 16 ? g.rows / 4 : 16;
-    if (launch_pdl(attn_join_kernel<kDim>, dim3(grid - 1, rows), dim3(kJoinThreads), 0, stream, p, grid, g) != cudaSuccess)
+    if (launch_pdl(attn_join_kernel<kDim, kColumns>, dim3(grid - 1, rows), dim3(kJoinThreads), 0, stream, p, grid, g) != cudaSuccess)
       return NVFP4_ERR_CUDA;
   }
   return launched();
@@ -1081,7 +1172,7 @@ nvfp4_status launch_attn_split(const AttnJob& p, const KvMaps& maps, cudaStream_
   if (launch_pdl(attn_split_kernel<kDim, kFp8, kRW, kKW>, dim3(kAttnGrid * T::kCtas), dim3(T::kThreadsAll), T::kSmem,
                  stream, p, maps) != cudaSuccess)
     return NVFP4_ERR_CUDA;
-  return launch_attn_join<kDim>(p, Tiling{T::kRows, T::kKeys, T::kOver}, kAttnGrid * T::kCtas, stream);
+  return launch_attn_join<kDim, false>(p, Tiling{T::kRows, T::kKeys, T::kOver, T::kSnap}, kAttnGrid * T::kCtas, stream);
 }
 
 // The split and join grids for heads of kDim values (attention_d*.cu).

@@ -36,7 +36,7 @@ struct ChunkTile {
   static constexpr int kRows = 128 * kGroups;
   static constexpr int kKeys = kDim == 256 ? 64 : 128;
   static constexpr int kSBuf = kDim == 256 ? 2 : 1;        // S buffers per group
-  static constexpr int kOver = 4;                          // an item's own cost, in units
+  static constexpr int kOver = 4, kSnap = 4;               // an item's own cost, in units (Tiling)
   static constexpr int kThreadsAll = 128 + 128 * kGroups;
   static constexpr int kEl = kFp8 ? 1 : 2;
   // boxes of the pool (as AttnTile names them, for tile_offset)
@@ -195,7 +195,7 @@ struct ChunkBars {
   uint64_t s_full[2];             // one per group, or per S buffer
   uint64_t p_full[2][2];          // the same, for each half of the keys
   uint64_t o_full[2];             // products with V done: one per group, or in turn
-  long long scratch[36];
+  RangeScratch scratch;
   uint32_t tmem;
   int noted;  // an infinity or NaN was taken out of V, in this CTA's items so far
 };
@@ -239,10 +239,14 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
   tc_fence_after();
   const uint32_t tmem = uniform(*static_cast<volatile uint32_t*>(&bars->tmem));
 
-  constexpr Tiling kTiling{T::kRows, T::kKeys, T::kOver};
+  constexpr Tiling kTiling{T::kRows, T::kKeys, T::kOver, T::kSnap};
   Found f;
   Ranges ranges;
-  find_range<T::kThreadsAll>(p, kTiling, gridDim.x, blockIdx.x, &ranges, &f, bars->scratch);
+  find_range<T::kThreadsAll>(p, kTiling, gridDim.x, blockIdx.x, &ranges, &f, &bars->scratch,
+                             reinterpret_cast<longlong2*>(smem_raw + (base - raw0)));
+  // (the list lies where the first tiles will: its last reads come before the copies)
+  fence_proxy_async_smem();
+  __syncthreads();
   const bool idle = static_cast<int>(blockIdx.x) >= ranges.grid;
   const long long u0 = idle ? 0 : ranges.start(blockIdx.x), u1 = idle ? 0 : ranges.start(blockIdx.x + 1);
   Walk w;
@@ -419,10 +423,14 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
               const uint32_t tile = v_at + st * T::kTileB;
               for (int r = who; r < kKeys; r += 64) {
                 const bool seen = key0 + r >= kr.any_lo && key0 + r < kr.any_hi;
-#pragma unroll 4
-                for (int c = 0; c < kDim / 8; ++c) {
-                  const uint32_t at = tile + umma_offset(kKeys, r, c);
-                  sts128(at, clean_chunk<false>(lds128(at), seen, noted));
+#pragma unroll 1
+                for (int c0 = 0; c0 < kDim / 8; c0 += 8) {  // (eight loads in flight)
+                  uint4 v[8];
+#pragma unroll
+                  for (int c = 0; c < 8; ++c) v[c] = lds128(tile + umma_offset(kKeys, r, c0 + c));
+#pragma unroll
+                  for (int c = 0; c < 8; ++c)
+                    sts128(tile + umma_offset(kKeys, r, c0 + c), clean_chunk<false>(v[c], seen, noted));
                 }
               }
               if (noted) *static_cast<volatile int*>(&bars->noted) = 1;
@@ -443,17 +451,22 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
             const uint32_t from = raw_at + rst * T::kRawB, to = (is_v ? v_at : k_at) + st * T::kTileB;
             for (int r = who; r < kKeys; r += 64) {
               const bool seen = key0 + r >= kr.any_lo && key0 + r < kr.any_hi;
-#pragma unroll 4
-              for (int x = 0; x < kDim / 16; ++x) {
-                const uint4 v = lds128(from + tile_offset<T>(r, x));
-                uint4 a, b;
-                e4m3x4_to_f16x2(v.x, a.x, a.y);
-                e4m3x4_to_f16x2(v.y, a.z, a.w);
-                e4m3x4_to_f16x2(v.z, b.x, b.y);
-                e4m3x4_to_f16x2(v.w, b.z, b.w);
-                if (clean) a = clean_chunk<true>(a, seen, noted), b = clean_chunk<true>(b, seen, noted);
-                sts128(to + umma_offset(kKeys, r, 2 * x), a);
-                sts128(to + umma_offset(kKeys, r, 2 * x + 1), b);
+#pragma unroll 1
+              for (int x0 = 0; x0 < kDim / 16; x0 += 4) {  // (four loads in flight)
+                uint4 v[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) v[x] = lds128(from + tile_offset<T>(r, x0 + x));
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                  if (clean) v[x] = clean_codes(v[x], seen, noted);
+                  uint4 a, b;
+                  e4m3x4_to_f16x2(v[x].x, a.x, a.y);
+                  e4m3x4_to_f16x2(v[x].y, a.z, a.w);
+                  e4m3x4_to_f16x2(v[x].z, b.x, b.y);
+                  e4m3x4_to_f16x2(v[x].w, b.z, b.w);
+                  sts128(to + umma_offset(kKeys, r, 2 * (x0 + x)), a);
+                  sts128(to + umma_offset(kKeys, r, 2 * (x0 + x) + 1), b);
+                }
               }
             }
             if (noted) *static_cast<volatile int*>(&bars->noted) = 1;
@@ -669,7 +682,8 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
       const float inv = !whole ? 1.0f : (l == 0.f ? 0.f : vs / l);
       const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0 && (p.out_stride & 15) == 0;
       uint16_t* out = p.out + token * p.out_stride + static_cast<int64_t>(head) * kDim;
-      float* part = p.part + (static_cast<int64_t>(slot) * T::kRows + r) * kDim;
+      // blocks of eight columns of all rows: neighbouring threads write neighbouring addresses
+      float* part = p.part + static_cast<int64_t>(slot) * T::kRows * kDim + r * 8;
       const bool noted = *static_cast<volatile int*>(&bars->noted) != 0;
       const KeyRange kr = key_range(p, w);
 #pragma unroll 1
@@ -715,7 +729,8 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) stg256(part + c + i, reinterpret_cast<const uint32_t*>(o) + i);
+          for (int i = 0; i < 32; i += 8)
+            stg256(part + static_cast<int64_t>((c + i) / 8) * T::kRows * 8, reinterpret_cast<const uint32_t*>(o) + i);
         }
       }
       if (live) {
@@ -746,7 +761,7 @@ nvfp4_status launch_attn_chunk(const AttnJob& p, const KvMaps& maps, cudaStream_
   if (set_smem(attn_chunk_kernel<kDim, kFp8>, T::kSmem) != cudaSuccess) return NVFP4_ERR_CUDA;
   if (launch_pdl(attn_chunk_kernel<kDim, kFp8>, dim3(kAttnGrid), dim3(T::kThreadsAll), T::kSmem, stream, p, maps) != cudaSuccess)
     return NVFP4_ERR_CUDA;
-  return launch_attn_join<kDim>(p, Tiling{T::kRows, T::kKeys, T::kOver}, kAttnGrid, stream);
+  return launch_attn_join<kDim, true>(p, Tiling{T::kRows, T::kKeys, T::kOver, T::kSnap}, kAttnGrid, stream);
 }
 
 }  // namespace nvfp4
