@@ -550,7 +550,10 @@ nvfp4_status kv_append(const nvfp4_kv_cache *cache, const uint16_t *k, int64_t k
  *              written.  lse (device) fp32 [n_tokens, n_heads] or NULL.
  *   scale      finite; softcap finite, >= 0; window >= 0 (0: all keys).
  *   ws         (device) paged_attention_workspace_bytes() bytes, 32-byte aligned;
- *              needs no initialisation and holds nothing between calls.
+ *              its first 4 KiB are arrival counters and must be zero before the
+ *              first call on it (for example cudaMemsetAsync once after
+ *              allocation); every completed call leaves them zero again, so one
+ *              workspace of the largest size needed serves calls of any shape.
  * kv_len is read as at most max_pages * page_size, cu_tokens as ascending and at
  * most n_tokens.  A page id outside the pool among the keys that are seen reads
  * as zeros and sets bit 2 of the device error word.

@@ -22,6 +22,7 @@ NVFP4_KV_BF16 = 0
 NVFP4_KV_E4M3 = 1
 NVFP4_ROPE_INTERLEAVED = 1
 NVFP4_ROPE_INVERSE = 2
+COUNTER_BYTES = 4096  # arrival counters at the start of an attention workspace
 LAYOUT_VERSION = 2
 
 STATUS = {0: "ok", 1: "null pointer", 2: "bad shape", 3: "misaligned pointer",
@@ -578,13 +579,15 @@ class Library:
 
     def _stream_workspace(self, key, nbytes: int, device, raw: int, stream) -> torch.Tensor:
         """A workspace of its own for each (call kind, device, stream): calls on different streams may overlap.  It is
-        allocated on the stream that uses it, so that one that is outgrown is not reused under a running call.  A
-        captured call gets one from its graph's pool, which lives and dies with the graph."""
+        allocated, and its counters cleared, on the stream that uses it, so that one that is outgrown is not reused under a
+        running call.  A captured call gets one from its graph's pool, which lives and dies with the graph and whose
+        counters are cleared at every replay."""
         cur = self._ws.get((key, device, raw))
         if cur is not None and cur.numel() >= nbytes and not torch.cuda.is_current_stream_capturing():
             return cur
         with torch.cuda.stream(torch.cuda.current_stream(device) if stream is None else stream):
-            cur = torch.empty(max(nbytes, 32), dtype=torch.uint8, device=device)
+            cur = torch.empty(max(nbytes, COUNTER_BYTES), dtype=torch.uint8, device=device)
+            cur[:COUNTER_BYTES].zero_()
             if not torch.cuda.is_current_stream_capturing():
                 self._ws[(key, device, raw)] = cur
         return cur

@@ -52,7 +52,7 @@ size_t paged_attention_workspace_bytes(int32_t n_tokens, int32_t n_seqs, int32_t
   if (!sizes_ok(n_tokens, n_seqs, max_new, n_heads, n_kv_heads, head_dim)) return 0;
   const AttnShape s = attn_shape(head_dim, false, packed_rows(n_tokens, max_new, n_heads, n_kv_heads));
   const int grid = kAttnGrid * (s.chunk ? 1 : attn_ctas(head_dim));
-  return static_cast<size_t>(2) * grid * s.tile_rows * (head_dim + 2) * sizeof(float);
+  return kAttnCounterBytes + static_cast<size_t>(2) * grid * s.tile_rows * (head_dim + 2) * sizeof(float);
 }
 
 nvfp4_status paged_attention(const nvfp4_kv_cache* cache, const nvfp4_batch* batch, const uint16_t* q,
@@ -85,7 +85,8 @@ nvfp4_status paged_attention(const nvfp4_kv_cache* cache, const nvfp4_batch* bat
   p.v_pool = cache->v, p.page_stride = cache->page_stride;
   p.k_scale = cache->k_scale, p.v_scale = cache->v_scale;
   p.scale = scale, p.softcap = softcap, p.window = window;
-  p.part = static_cast<float*>(ws);
+  p.counters = static_cast<unsigned*>(ws);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kAttnCounterBytes);
   const bool fp8 = cache->dtype == NVFP4_KV_E4M3;
   const AttnShape s = attn_shape(dim, fp8, packed_rows(n_tokens, batch->max_new, n_heads, kv));
   KvMaps maps;

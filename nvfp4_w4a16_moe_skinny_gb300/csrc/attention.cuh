@@ -11,9 +11,10 @@
 // themselves and a single long sequence fills the chip.  Every CTA finds its
 // range from kv_len and cu_tokens by itself (a block-wide scan), so one launch
 // geometry serves a captured graph at any lengths.  An item that lies in one range is
-// finished in registers; otherwise its pieces (unnormalised sums with their row
-// maximum and sum of weights, fp32) go to the workspace, at most two per CTA, and
-// a second grid joins them in range order: the result does not depend on timing.
+// finished in registers; otherwise its holders write their shares (unnormalised sums with
+// their row maximum and sum of weights, fp32) to the workspace, at most two per CTA, and
+// the last of them to arrive at the item's counter joins all shares in range order: the
+// result does not depend on which one it is, and no CTA waits for another.
 //
 // Inner loop.  One producer warp copies K and V tiles by TMA (swizzled boxes of a
 // page's rows; a page id outside the pool is an out-of-range coordinate, which
@@ -34,6 +35,7 @@
 
 namespace nvfp4 {
 
+constexpr size_t kAttnCounterBytes = 4096;  // at the start of the workspace
 constexpr int kAttnGrid = 152;  // SMs that the split is made for; fixed, so that workspace sizes are host-computable
 
 // Division by a number that a launch knows: x / g = umulhi(x, mul) >> shift for
@@ -69,6 +71,7 @@ struct AttnJob {
   const float* v_scale;
   float scale, softcap;
   int window;
+  unsigned* counters;  // arrivals at the join of each split item, by the range that holds its start
   float* part;  // [2 * grid][rows][dim] unnormalised sums, then [2 * grid][rows][2] (reference maximum, sum)
 };
 
@@ -155,8 +158,10 @@ struct Ranges {
   }
   __device__ __forceinline__ long long start(int c) const { return c * each + min(c, more); }
   __device__ __forceinline__ int holder(long long u) const {
-    const long long cut = more * (each + 1);
-    return static_cast<int>(u < cut ? u / (each + 1) : more + (u - cut) / each);
+    const long long cut = more * (each + 1), by = u < cut ? each + 1 : each, at = u < cut ? u : u - cut;
+    const int before = u < cut ? 0 : more;
+    if (total >> 31) return before + static_cast<int>(at / by);
+    return before + static_cast<int>(static_cast<uint32_t>(at) / static_cast<uint32_t>(by));
   }
 };
 
@@ -182,6 +187,24 @@ __device__ __forceinline__ void find_range(const AttnJob& p, const Tiling& g, in
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int kNW = kThreadsInBlock / 32;
   long long mine = 0, incl = 0;
+  if (p.n_seqs <= 32) {  // few short sequences: every warp finds the same by itself
+    Sequence s{};
+    if (lane < p.n_seqs) s = sequence_of(p, lane, g);
+    if (!__any_sync(0xffffffffu, s.tiles > 4)) {
+      mine = incl = tile_units(p, s, 0, 1, g);
+#pragma unroll 1
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      ranges->set(__shfl_sync(0xffffffffu, incl, 31), ctas);
+      const long long u = ranges->start(c);
+      const unsigned here = __ballot_sync(0xffffffffu, u >= incl - mine && u < incl);
+      found->seq = here ? __ffs(here) - 1 : 0;
+      found->before = __shfl_sync(0xffffffffu, incl - mine, found->seq);
+      return;
+    }
+  }
   // one pass for the total, then (again over the batch only where it is longer than
   // the block) one that finds the unit
   const bool once = p.n_seqs <= kThreadsInBlock;
@@ -343,6 +366,36 @@ __device__ __forceinline__ Share share_at(const Walk& w, long long u, long long 
   q.whole = q.n == units;
   q.slot = 2 * c + (from > 0 ? 0 : 1);  // a range starts inside at most one item and ends inside one
   return q;
+}
+
+// The ranges [c0, c1] that hold tiles of an item (c0 != c1: it is split).
+struct Holders {
+  int c0, c1;
+};
+__device__ __forceinline__ Holders holders_of(const Walk& w, const Ranges& r, const Tiling& g) {
+  const int span = w.t.units + g.over, t = min(g.snap, (span - 1) / 2);
+  Holders h;
+  h.c0 = r.holder(w.item0 + t);  // boundaries up to t units in have moved to the item's start
+  h.c1 = max(h.c0, r.holder(w.item0 + min(w.t.units, span - t) - 1));
+  return h;
+}
+
+// Takes part in the join of an item: called by the kThreadsIn threads (named barrier `bar`)
+// that have written a share of it, and true for the last of its holders to arrive, whose
+// threads then see all shares.  Counters return to zero.  Nobody waits for another CTA.
+template <int kThreadsIn>
+__device__ __forceinline__ bool last_to_arrive(unsigned* counter, int holders, int bar, volatile int* say) {
+  __threadfence();
+  asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(kThreadsIn) : "memory");
+  if (threadIdx.x % kThreadsIn == 0) {
+    const bool last = atomicAdd(counter, 1u) == static_cast<unsigned>(holders - 1);
+    if (last) *counter = 0;
+    *say = last;
+  }
+  asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(kThreadsIn) : "memory");
+  const bool last = *say != 0;
+  if (last) __threadfence();
+  return last;
 }
 
 // ------------------------------------------------------------------ MMA helpers
@@ -560,6 +613,7 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, a
   float* q_back = reinterpret_cast<float*>(scratch + 1);  // [kRows] undoes the scaling of a row of Q
   // an infinity or NaN was taken out of V, in this CTA's items so far
   volatile int* noted_flag = reinterpret_cast<volatile int*>(q_back + T::kRows);
+  volatile int* say = noted_flag + 1;  // last_to_arrive's answer
 
   const int warp = static_cast<int>(uniform(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -1021,120 +1075,65 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, a
         }
       }
     }
-  }
-}
 
-// ------------------------------------------------------------------ the join
-
-constexpr int kJoinThreads = 128;
-
-// Block (c, y): if range boundary c is the first one inside an item, joins that
-// item's pieces in range order, for some of its rows.  The split kernel's shares are
-// rows of kDim sums, joined a warp a row; the chunk kernel's (kColumns) come as blocks of
-// eight columns of all rows, as its threads hold a row each, and are joined a thread a
-// row and block.
-template <int kDim, bool kColumns>
-__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnJob p, int split_grid, const Tiling g) {
-  __shared__ RangeScratch scratch;
-  __shared__ longlong2 list[kJoinThreads];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int tile_rows = g.rows;
-  Found f;
-  Ranges ranges;
-  // lengths are complete before the split grid starts: only its pieces are waited for
-  const int c = blockIdx.x + 1;
-  find_range<kJoinThreads>(p, g, split_grid, c, &ranges, &f, &scratch, list);
-  Walk w;
-  bool first = false;
-  if (c < ranges.grid) {
-    w.b = f.seq, w.item0 = f.before;
-    walk_seq(p, w, g);
-    const long long u = ranges.start(c);
-    walk_to(p, w, u, g);
-    // a boundary among the item's tiles, and the first one
-    const int d = snapped(static_cast<int>(u - w.item0), w.t.units, g);
-    const long long before = ranges.start(c - 1) - w.item0;
-    first = d > 0 && d < w.t.units && (before <= 0 || snapped(static_cast<int>(before), w.t.units, g) == 0);
-  }
-  pdl_launch_dependents();
-  pdl_wait();  // every block waits, so that this grid's end means that the split grid has ended
-  if (!first) return;
-  // first and last range that hold a tile of the item
-  const int span = w.t.units + g.over, cut = min(w.t.units, span - min(g.snap, (span - 1) / 2));
-  const int c0 = c - 1, c1 = ranges.holder(w.item0 + cut - 1);
-  const float* ml = p.part + static_cast<int64_t>(2) * split_grid * tile_rows * kDim;
-  if constexpr (kColumns) {
-    for (int i = blockIdx.y * kJoinThreads + threadIdx.x; i < tile_rows * (kDim / 16); i += gridDim.y * kJoinThreads) {
-      const int r = i % tile_rows, block = i / tile_rows * 2;
-      if (r >= w.t.rows) continue;
-      float m = -INFINITY;
-      for (int j = c0; j <= c1; ++j)
-        m = fmaxf(m, ml[(static_cast<int64_t>(2 * j + (j == c0 ? 1 : 0)) * tile_rows + r) * 2]);
-      float acc[16], l = 0.f;
+    // ---- the last holder of a split item joins its shares, in range order
+    if (!pc.whole) {
+      const Holders h = holders_of(w, ranges, kTiling);
+      if (last_to_arrive<T::kConsumers * 32>(p.counters + h.c0, h.c1 - h.c0 + 1, 1, say)) {
+        const float* ml = p.part + static_cast<int64_t>(2) * gridDim.x * T::kRows * kDim;
+        // kR rows a thread, four columns of each, sixteen loads of shares in flight
+        constexpr int kLanes = kDim / 4, kSlots = T::kConsumers * 32 / kLanes;
+        constexpr int kMost = kRW == 1 ? 2 : (kDim == 256 ? 16 : 8), kR = T::kRows / kSlots < kMost ? T::kRows / kSlots : kMost;
+        constexpr int kB = 16 / kR;  // shares at a time
+        const int col = threadIdx.x % kLanes * 4;
+#pragma unroll 1
+        for (int r0 = threadIdx.x / kLanes; r0 < w.t.rows; r0 += kR * kSlots) {
+          float top[kR], all[kR];
+          float4 sum[kR];
 #pragma unroll
-      for (int x = 0; x < 16; ++x) acc[x] = 0.f;
-#pragma unroll 2
-      for (int j = c0; j <= c1; ++j) {
-        const int64_t slot = 2 * j + (j == c0 ? 1 : 0);
-        const float2 v = *reinterpret_cast<const float2*>(ml + (slot * tile_rows + r) * 2);
-        const float a = m == -INFINITY ? 1.0f : exp2_approx(v.x - m);
-        l += a * v.y;
+          for (int y = 0; y < kR; ++y) top[y] = -INFINITY, all[y] = 0.f, sum[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+          for (int c0 = h.c0; c0 <= h.c1; c0 += kB) {
+            float2 v[kB][kR];
+            float4 o[kB][kR];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float4* o = reinterpret_cast<const float4*>(p.part + slot * tile_rows * kDim +
-                                                            (static_cast<int64_t>(block + h) * tile_rows + r) * 8);
-          const float4 x = o[0], y = o[1];
-          acc[8 * h] += a * x.x, acc[8 * h + 1] += a * x.y, acc[8 * h + 2] += a * x.z, acc[8 * h + 3] += a * x.w;
-          acc[8 * h + 4] += a * y.x, acc[8 * h + 5] += a * y.y, acc[8 * h + 6] += a * y.z, acc[8 * h + 7] += a * y.w;
+            for (int i = 0; i < kB; ++i)
+#pragma unroll
+              for (int y = 0; y < kR; ++y) {
+                const int c = min(c0 + i, h.c1), r = min(r0 + y * kSlots, w.t.rows - 1);
+                const int64_t at = static_cast<int64_t>(2 * c + (c == h.c0)) * T::kRows + r;
+                v[i][y] = __ldcg(reinterpret_cast<const float2*>(ml + at * 2));
+                o[i][y] = __ldcg(reinterpret_cast<const float4*>(p.part + at * kDim + col));
+              }
+#pragma unroll
+            for (int i = 0; i < kB; ++i)
+              if (c0 + i <= h.c1) {
+#pragma unroll
+                for (int y = 0; y < kR; ++y) {
+                  const float next = fmaxf(top[y], v[i][y].x);
+                  const float a = next == -INFINITY ? 1.0f : exp2_approx(top[y] - next);
+                  const float b = next == -INFINITY ? 1.0f : exp2_approx(v[i][y].x - next);
+                  top[y] = next;
+                  all[y] = all[y] * a + v[i][y].y * b;
+                  sum[y].x = sum[y].x * a + o[i][y].x * b, sum[y].y = sum[y].y * a + o[i][y].y * b;
+                  sum[y].z = sum[y].z * a + o[i][y].z * b, sum[y].w = sum[y].w * a + o[i][y].w * b;
+                }
+              }
+          }
+#pragma unroll
+          for (int y = 0; y < kR; ++y) {
+            if (r0 + y * kSlots >= w.t.rows) break;
+            const int rr = w.t.row0 + r0 + y * kSlots, tk = div_by(p.by_group, rr), hd = w.h * p.group + rr - tk * p.group;
+            const int64_t row = w.s.tok0 + tk;
+            const float inv = all[y] == 0.f ? 0.f : vs / all[y];
+            *reinterpret_cast<uint2*>(p.out + row * p.out_stride + static_cast<int64_t>(hd) * kDim + col) =
+                make_uint2(f32x2_to_bf16x2(sum[y].x * inv, sum[y].y * inv), f32x2_to_bf16x2(sum[y].z * inv, sum[y].w * inv));
+            if (p.lse && col == 0)
+              p.lse[row * p.n_heads + hd] = all[y] == 0.f ? -INFINITY : (top[y] + log2f(all[y])) * 0.6931471805599453f;
+          }
         }
       }
-      const int rr = w.t.row0 + r, tok = div_by(p.by_group, rr), head = w.h * p.group + rr - tok * p.group;
-      const int64_t row = w.s.tok0 + tok;
-      const float inv = l == 0.f ? 0.f : (p.v_scale ? __ldg(p.v_scale + w.h) : 1.0f) / l;
-      uint4* o = reinterpret_cast<uint4*>(p.out + row * p.out_stride + static_cast<int64_t>(head) * kDim + block * 8);
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        o[h] = make_uint4(f32x2_to_bf16x2(acc[8 * h] * inv, acc[8 * h + 1] * inv), f32x2_to_bf16x2(acc[8 * h + 2] * inv, acc[8 * h + 3] * inv),
-                          f32x2_to_bf16x2(acc[8 * h + 4] * inv, acc[8 * h + 5] * inv), f32x2_to_bf16x2(acc[8 * h + 6] * inv, acc[8 * h + 7] * inv));
-      if (p.lse && block == 0)
-        p.lse[row * p.n_heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
     }
-    return;
-  }
-  constexpr int kPer = kDim / 32;
-  for (int r = blockIdx.y * 4 + warp; r < w.t.rows; r += gridDim.y * 4) {
-    float m = -INFINITY;
-    for (int i = c0 + lane; i <= c1; i += 32) {
-      const int slot = 2 * i + (i == c0 ? 1 : 0);
-      m = fmaxf(m, ml[(static_cast<int64_t>(slot) * tile_rows + r) * 2]);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float acc[kPer];
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) acc[j] = 0.f;
-    float l = 0.f;
-#pragma unroll 4
-    for (int i = c0; i <= c1; ++i) {
-      const int slot = 2 * i + (i == c0 ? 1 : 0);
-      const int64_t row = static_cast<int64_t>(slot) * tile_rows + r;
-      const float2 v = *reinterpret_cast<const float2*>(ml + row * 2);
-      const float a = m == -INFINITY ? 1.0f : exp2_approx(v.x - m);
-      l += a * v.y;
-      const float* o = p.part + row * kDim + lane * kPer;
-#pragma unroll
-      for (int j = 0; j < kPer; j += 2) {
-        const float2 x = *reinterpret_cast<const float2*>(o + j);
-        acc[j] += a * x.x, acc[j + 1] += a * x.y;
-      }
-    }
-    const int rr = w.t.row0 + r, tok = div_by(p.by_group, rr), head = w.h * p.group + rr - tok * p.group;
-    const int64_t row = w.s.tok0 + tok;
-    const float inv = l == 0.f ? 0.f : (p.v_scale ? __ldg(p.v_scale + w.h) : 1.0f) / l;
-    uint32_t* o = reinterpret_cast<uint32_t*>(p.out + row * p.out_stride + static_cast<int64_t>(head) * kDim) + lane * (kPer / 2);
-#pragma unroll
-    for (int j = 0; j < kPer; j += 2) o[j / 2] = f32x2_to_bf16x2(acc[j] * inv, acc[j + 1] * inv);
-    if (p.lse && lane == 0) p.lse[row * p.n_heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
   }
 }
 
@@ -1154,17 +1153,6 @@ inline AttnShape attn_shape(int dim, bool fp8, int64_t rows) {
   return {rw, kw, 16 * rw, attn_slice(dim, fp8, kw) * kw, false};
 }
 
-template <int kDim, bool kColumns>
-nvfp4_status launch_attn_join(const AttnJob& p, const Tiling& g, int grid, cudaStream_t stream) {
-  // one unit an item: nothing can be split
-  if ((static_cast<int64_t>(p.max_pages) << p.page_log2) > g.keys) {
-    const int rows = g.rows / 4 < 16 ? g.rows / 4 : 16;
-    if (launch_pdl(attn_join_kernel<kDim, kColumns>, dim3(grid - 1, rows), dim3(kJoinThreads), 0, stream, p, grid, g) != cudaSuccess)
-      return NVFP4_ERR_CUDA;
-  }
-  return launched();
-}
-
 template <int kDim, bool kFp8, int kRW, int kKW>
 nvfp4_status launch_attn_split(const AttnJob& p, const KvMaps& maps, cudaStream_t stream) {
   using T = AttnTile<kDim, kFp8, kRW, kKW>;
@@ -1172,7 +1160,7 @@ nvfp4_status launch_attn_split(const AttnJob& p, const KvMaps& maps, cudaStream_
   if (launch_pdl(attn_split_kernel<kDim, kFp8, kRW, kKW>, dim3(kAttnGrid * T::kCtas), dim3(T::kThreadsAll), T::kSmem,
                  stream, p, maps) != cudaSuccess)
     return NVFP4_ERR_CUDA;
-  return launch_attn_join<kDim, false>(p, Tiling{T::kRows, T::kKeys, T::kOver, T::kSnap}, kAttnGrid * T::kCtas, stream);
+  return launched();
 }
 
 // The split and join grids for heads of kDim values (attention_d*.cu).

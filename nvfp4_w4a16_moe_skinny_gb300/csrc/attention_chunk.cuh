@@ -197,6 +197,7 @@ struct ChunkBars {
   uint64_t o_full[2];             // products with V done: one per group, or in turn
   RangeScratch scratch;
   uint32_t tmem;
+  int say[2];  // last_to_arrive's answers, by group
   int noted;  // an infinity or NaN was taken out of V, in this CTA's items so far
 };
 
@@ -741,6 +742,47 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
           p.lse[token * p.n_heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
         }
       }
+      // ---- the last holder of a split item joins its shares of these rows, in range order
+      if (!pc.whole) {
+        const Holders h = holders_of(w, ranges, kTiling);
+        if (last_to_arrive<128>(p.counters + 2 * h.c0 + g, h.c1 - h.c0 + 1, 1 + g, &bars->say[g]) && live) {
+          const float* ml = p.part + static_cast<int64_t>(2) * gridDim.x * T::kRows * kDim;
+          float high = -INFINITY, all = 0.f;
+          for (int c = h.c0; c <= h.c1; ++c)
+            high = fmaxf(high, __ldcg(ml + (static_cast<int64_t>(2 * c + (c == h.c0)) * T::kRows + r) * 2));
+          for (int c = h.c0; c <= h.c1; ++c) {
+            const float2 v = __ldcg(reinterpret_cast<const float2*>(ml + (static_cast<int64_t>(2 * c + (c == h.c0)) * T::kRows + r) * 2));
+            all += v.y * (high == -INFINITY ? 1.0f : exp2_approx(v.x - high));
+          }
+          const float unit_out = all == 0.f ? 0.f : vs / all;
+#pragma unroll 1
+          for (int c0 = 0; c0 < kDim; c0 += 32) {
+            float o[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = 0.f;
+#pragma unroll 2
+            for (int c = h.c0; c <= h.c1; ++c) {
+              const int64_t at = 2 * c + (c == h.c0);
+              const float v = __ldcg(ml + (at * T::kRows + r) * 2);
+              const float a = high == -INFINITY ? 1.0f : exp2_approx(v - high);
+              const float4* x = reinterpret_cast<const float4*>(p.part + at * T::kRows * kDim +
+                                                                (static_cast<int64_t>(c0 / 8) * T::kRows + r) * 8);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float4 y = __ldcg(x + (i / 2) * T::kRows * 2 + (i & 1));
+                o[4 * i] += a * y.x, o[4 * i + 1] += a * y.y, o[4 * i + 2] += a * y.z, o[4 * i + 3] += a * y.w;
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 32; i += 8)
+              *reinterpret_cast<uint4*>(out + c0 + i) =
+                  make_uint4(f32x2_to_bf16x2(o[i] * unit_out, o[i + 1] * unit_out), f32x2_to_bf16x2(o[i + 2] * unit_out, o[i + 3] * unit_out),
+                             f32x2_to_bf16x2(o[i + 4] * unit_out, o[i + 5] * unit_out), f32x2_to_bf16x2(o[i + 6] * unit_out, o[i + 7] * unit_out));
+          }
+          if (p.lse)
+            p.lse[token * p.n_heads + head] = all == 0.f ? -INFINITY : (high + log2f(all)) * 0.6931471805599453f;
+        }
+      }
       tc_fence_before();  // O has been read before the next item's first P is handed over
     }
   }
@@ -761,7 +803,7 @@ nvfp4_status launch_attn_chunk(const AttnJob& p, const KvMaps& maps, cudaStream_
   if (set_smem(attn_chunk_kernel<kDim, kFp8>, T::kSmem) != cudaSuccess) return NVFP4_ERR_CUDA;
   if (launch_pdl(attn_chunk_kernel<kDim, kFp8>, dim3(kAttnGrid), dim3(T::kThreadsAll), T::kSmem, stream, p, maps) != cudaSuccess)
     return NVFP4_ERR_CUDA;
-  return launch_attn_join<kDim, true>(p, Tiling{T::kRows, T::kKeys, T::kOver, T::kSnap}, kAttnGrid, stream);
+  return launched();
 }
 
 }  // namespace nvfp4
