@@ -52,7 +52,8 @@ size_t paged_attention_workspace_bytes(int32_t n_tokens, int32_t n_seqs, int32_t
   if (!sizes_ok(n_tokens, n_seqs, max_new, n_heads, n_kv_heads, head_dim)) return 0;
   const AttnShape s = attn_shape(head_dim, false, packed_rows(n_tokens, max_new, n_heads, n_kv_heads));
   const int grid = kAttnGrid * (s.chunk ? 1 : attn_ctas(head_dim));
-  return kAttnCounterBytes + static_cast<size_t>(2) * grid * s.tile_rows * (head_dim + 2) * sizeof(float);
+  const size_t share = static_cast<size_t>(s.tile_rows) * (head_dim + 2);  // sums of a row tile, references and sums of weights
+  return kAttnCounterBytes + 2 * grid * share * sizeof(float);
 }
 
 nvfp4_status paged_attention(const nvfp4_kv_cache* cache, const nvfp4_batch* batch, const uint16_t* q,

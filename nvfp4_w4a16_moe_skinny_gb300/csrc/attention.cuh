@@ -13,7 +13,7 @@
 // geometry serves a captured graph at any lengths.  An item that lies in one range is
 // finished in registers; otherwise its holders write their shares (unnormalised sums with
 // their row maximum and sum of weights, fp32) to the workspace, at most two per CTA, and
-// the last of them to arrive at the item's counter joins all shares in range order: the
+// the last of them to arrive at a counter joins the shares in range order (join_step): the
 // result does not depend on which one it is, and no CTA waits for another.
 //
 // Inner loop.  One producer warp copies K and V tiles by TMA (swizzled boxes of a
@@ -72,7 +72,7 @@ struct AttnJob {
   float scale, softcap;
   int window;
   unsigned* counters;  // arrivals at the join of each split item, by the range that holds its start
-  float* part;  // [2 * grid][rows][dim] unnormalised sums, then [2 * grid][rows][2] (reference maximum, sum)
+  float* part;         // shares: unnormalised sums, reference maxima and sums of weights of a row tile, two per CTA
 };
 
 struct KvMaps {
@@ -380,24 +380,6 @@ __device__ __forceinline__ Holders holders_of(const Walk& w, const Ranges& r, co
   return h;
 }
 
-// Takes part in the join of an item: called by the kThreadsIn threads (named barrier `bar`)
-// that have written a share of it, and true for the last of its holders to arrive, whose
-// threads then see all shares.  Counters return to zero.  Nobody waits for another CTA.
-template <int kThreadsIn>
-__device__ __forceinline__ bool last_to_arrive(unsigned* counter, int holders, int bar, volatile int* say) {
-  __threadfence();
-  asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(kThreadsIn) : "memory");
-  if (threadIdx.x % kThreadsIn == 0) {
-    const bool last = atomicAdd(counter, 1u) == static_cast<unsigned>(holders - 1);
-    if (last) *counter = 0;
-    *say = last;
-  }
-  asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(kThreadsIn) : "memory");
-  const bool last = *say != 0;
-  if (last) __threadfence();
-  return last;
-}
-
 // ------------------------------------------------------------------ MMA helpers
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -613,7 +595,6 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, a
   float* q_back = reinterpret_cast<float*>(scratch + 1);  // [kRows] undoes the scaling of a row of Q
   // an infinity or NaN was taken out of V, in this CTA's items so far
   volatile int* noted_flag = reinterpret_cast<volatile int*>(q_back + T::kRows);
-  volatile int* say = noted_flag + 1;  // last_to_arrive's answer
 
   const int warp = static_cast<int>(uniform(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -1075,65 +1056,80 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, a
         }
       }
     }
+  }
+}
 
-    // ---- the last holder of a split item joins its shares, in range order
-    if (!pc.whole) {
-      const Holders h = holders_of(w, ranges, kTiling);
-      if (last_to_arrive<T::kConsumers * 32>(p.counters + h.c0, h.c1 - h.c0 + 1, 1, say)) {
-        const float* ml = p.part + static_cast<int64_t>(2) * gridDim.x * T::kRows * kDim;
-        // kR rows a thread, four columns of each, sixteen loads of shares in flight
-        constexpr int kLanes = kDim / 4, kSlots = T::kConsumers * 32 / kLanes;
-        constexpr int kMost = kRW == 1 ? 2 : (kDim == 256 ? 16 : 8), kR = T::kRows / kSlots < kMost ? T::kRows / kSlots : kMost;
-        constexpr int kB = 16 / kR;  // shares at a time
-        const int col = threadIdx.x % kLanes * 4;
-#pragma unroll 1
-        for (int r0 = threadIdx.x / kLanes; r0 < w.t.rows; r0 += kR * kSlots) {
-          float top[kR], all[kR];
-          float4 sum[kR];
+// ------------------------------------------------------------------ the join
+
+constexpr int kJoinThreads = 128;
+
+// Block (c, y): if range boundary c is the first one inside an item, joins that
+// item's shares in range order, a warp a row.  (The chunk kernel joins its few and large
+// shares itself; here many small ones would keep one CTA busy for long, while a second
+// grid spreads them over the chip: verify blocks of 30 rows of 256 values in a window of
+// 1,024 keys take 15.9 us this way and 23.1 us with the join in the split kernel.)
+template <int kDim>
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnJob p, int split_grid, const Tiling g) {
+  __shared__ RangeScratch scratch;
+  __shared__ longlong2 list[kJoinThreads];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tile_rows = g.rows;
+  Found f;
+  Ranges ranges;
+  // lengths are complete before the split grid starts: only its pieces are waited for
+  const int c = blockIdx.x + 1;
+  find_range<kJoinThreads>(p, g, split_grid, c, &ranges, &f, &scratch, list);
+  Walk w;
+  bool first = false;
+  if (c < ranges.grid) {
+    w.b = f.seq, w.item0 = f.before;
+    walk_seq(p, w, g);
+    const long long u = ranges.start(c);
+    walk_to(p, w, u, g);
+    // a boundary among the item's tiles, and the first one
+    const int d = snapped(static_cast<int>(u - w.item0), w.t.units, g);
+    const long long before = ranges.start(c - 1) - w.item0;
+    first = d > 0 && d < w.t.units && (before <= 0 || snapped(static_cast<int>(before), w.t.units, g) == 0);
+  }
+  pdl_launch_dependents();
+  pdl_wait();  // every block waits, so that this grid's end means that the split grid has ended
+  if (!first) return;
+  const auto [c0, c1] = holders_of(w, ranges, g);
+  const float* ml = p.part + static_cast<int64_t>(2) * split_grid * tile_rows * kDim;
+  constexpr int kPer = kDim / 32;
+  for (int r = blockIdx.y * 4 + warp; r < w.t.rows; r += gridDim.y * 4) {
+    float m = -INFINITY;
+    for (int i = c0 + lane; i <= c1; i += 32) {
+      const int slot = 2 * i + (i == c0 ? 1 : 0);
+      m = fmaxf(m, ml[(static_cast<int64_t>(slot) * tile_rows + r) * 2]);
+    }
 #pragma unroll
-          for (int y = 0; y < kR; ++y) top[y] = -INFINITY, all[y] = 0.f, sum[y] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-          for (int c0 = h.c0; c0 <= h.c1; c0 += kB) {
-            float2 v[kB][kR];
-            float4 o[kB][kR];
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float acc[kPer];
 #pragma unroll
-            for (int i = 0; i < kB; ++i)
+    for (int j = 0; j < kPer; ++j) acc[j] = 0.f;
+    float l = 0.f;
+#pragma unroll 4
+    for (int i = c0; i <= c1; ++i) {
+      const int slot = 2 * i + (i == c0 ? 1 : 0);
+      const int64_t row = static_cast<int64_t>(slot) * tile_rows + r;
+      const float2 v = *reinterpret_cast<const float2*>(ml + row * 2);
+      const float a = m == -INFINITY ? 1.0f : exp2_approx(v.x - m);
+      l += a * v.y;
+      const float* o = p.part + row * kDim + lane * kPer;
 #pragma unroll
-              for (int y = 0; y < kR; ++y) {
-                const int c = min(c0 + i, h.c1), r = min(r0 + y * kSlots, w.t.rows - 1);
-                const int64_t at = static_cast<int64_t>(2 * c + (c == h.c0)) * T::kRows + r;
-                v[i][y] = __ldcg(reinterpret_cast<const float2*>(ml + at * 2));
-                o[i][y] = __ldcg(reinterpret_cast<const float4*>(p.part + at * kDim + col));
-              }
-#pragma unroll
-            for (int i = 0; i < kB; ++i)
-              if (c0 + i <= h.c1) {
-#pragma unroll
-                for (int y = 0; y < kR; ++y) {
-                  const float next = fmaxf(top[y], v[i][y].x);
-                  const float a = next == -INFINITY ? 1.0f : exp2_approx(top[y] - next);
-                  const float b = next == -INFINITY ? 1.0f : exp2_approx(v[i][y].x - next);
-                  top[y] = next;
-                  all[y] = all[y] * a + v[i][y].y * b;
-                  sum[y].x = sum[y].x * a + o[i][y].x * b, sum[y].y = sum[y].y * a + o[i][y].y * b;
-                  sum[y].z = sum[y].z * a + o[i][y].z * b, sum[y].w = sum[y].w * a + o[i][y].w * b;
-                }
-              }
-          }
-#pragma unroll
-          for (int y = 0; y < kR; ++y) {
-            if (r0 + y * kSlots >= w.t.rows) break;
-            const int rr = w.t.row0 + r0 + y * kSlots, tk = div_by(p.by_group, rr), hd = w.h * p.group + rr - tk * p.group;
-            const int64_t row = w.s.tok0 + tk;
-            const float inv = all[y] == 0.f ? 0.f : vs / all[y];
-            *reinterpret_cast<uint2*>(p.out + row * p.out_stride + static_cast<int64_t>(hd) * kDim + col) =
-                make_uint2(f32x2_to_bf16x2(sum[y].x * inv, sum[y].y * inv), f32x2_to_bf16x2(sum[y].z * inv, sum[y].w * inv));
-            if (p.lse && col == 0)
-              p.lse[row * p.n_heads + hd] = all[y] == 0.f ? -INFINITY : (top[y] + log2f(all[y])) * 0.6931471805599453f;
-          }
-        }
+      for (int j = 0; j < kPer; j += 2) {
+        const float2 x = *reinterpret_cast<const float2*>(o + j);
+        acc[j] += a * x.x, acc[j + 1] += a * x.y;
       }
     }
+    const int rr = w.t.row0 + r, tok = div_by(p.by_group, rr), head = w.h * p.group + rr - tok * p.group;
+    const int64_t row = w.s.tok0 + tok;
+    const float inv = l == 0.f ? 0.f : (p.v_scale ? __ldg(p.v_scale + w.h) : 1.0f) / l;
+    uint32_t* o = reinterpret_cast<uint32_t*>(p.out + row * p.out_stride + static_cast<int64_t>(head) * kDim) + lane * (kPer / 2);
+#pragma unroll
+    for (int j = 0; j < kPer; j += 2) o[j / 2] = f32x2_to_bf16x2(acc[j] * inv, acc[j + 1] * inv);
+    if (p.lse && lane == 0) p.lse[row * p.n_heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
   }
 }
 
@@ -1153,6 +1149,17 @@ inline AttnShape attn_shape(int dim, bool fp8, int64_t rows) {
   return {rw, kw, 16 * rw, attn_slice(dim, fp8, kw) * kw, false};
 }
 
+template <int kDim>
+nvfp4_status launch_attn_join(const AttnJob& p, const Tiling& g, int grid, cudaStream_t stream) {
+  // one unit an item: nothing can be split
+  if ((static_cast<int64_t>(p.max_pages) << p.page_log2) > g.keys) {
+    const int rows = g.rows / 4 < 16 ? g.rows / 4 : 16;
+    if (launch_pdl(attn_join_kernel<kDim>, dim3(grid - 1, rows), dim3(kJoinThreads), 0, stream, p, grid, g) != cudaSuccess)
+      return NVFP4_ERR_CUDA;
+  }
+  return launched();
+}
+
 template <int kDim, bool kFp8, int kRW, int kKW>
 nvfp4_status launch_attn_split(const AttnJob& p, const KvMaps& maps, cudaStream_t stream) {
   using T = AttnTile<kDim, kFp8, kRW, kKW>;
@@ -1160,7 +1167,7 @@ nvfp4_status launch_attn_split(const AttnJob& p, const KvMaps& maps, cudaStream_
   if (launch_pdl(attn_split_kernel<kDim, kFp8, kRW, kKW>, dim3(kAttnGrid * T::kCtas), dim3(T::kThreadsAll), T::kSmem,
                  stream, p, maps) != cudaSuccess)
     return NVFP4_ERR_CUDA;
-  return launched();
+  return launch_attn_join<kDim>(p, Tiling{T::kRows, T::kKeys, T::kOver, T::kSnap}, kAttnGrid * T::kCtas, stream);
 }
 
 // The split and join grids for heads of kDim values (attention_d*.cu).

@@ -201,6 +201,49 @@ struct ChunkBars {
   int noted;  // an infinity or NaN was taken out of V, in this CTA's items so far
 };
 
+// ------------------------------------------------------------------ the join of split items
+
+// The join of a split item's shares, in groups of eight: the last holder of a group to
+// arrive at its counter joins the group's shares in range order and goes on with the result
+// as one of the next level's.  So nobody waits for another CTA, the result does not depend on
+// the order of arrival, few shares take one step, and no CTA reads more than eight of
+// them at a step.
+constexpr int kJoinGroup = 8;
+
+// One step up: shares [start, start + stride * kJoinGroup) of the item, `stride` apart
+// (kJoinGroup ^ level).  Called by the kThreadsIn threads (named barrier `bar`) that have
+// written share `mine`; true for the last to arrive, whose threads then see all of
+// them.  Counters return to zero.
+template <int kThreadsIn>
+__device__ __forceinline__ bool last_to_arrive(unsigned* counter, int arrivals, int bar, volatile int* say) {
+  __threadfence();
+  asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(kThreadsIn) : "memory");
+  if (threadIdx.x % kThreadsIn == 0) {
+    const bool last = atomicAdd(counter, 1u) == static_cast<unsigned>(arrivals - 1);
+    if (last) *counter = 0;
+    *say = last;
+  }
+  asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(kThreadsIn) : "memory");
+  const bool last = *say != 0;
+  if (last) __threadfence();
+  return last;
+}
+
+struct JoinStep {
+  int start, stride, count, counter;  // shares start, start + stride, ... (count of them); the group's counter
+  bool top;                           // the item is whole after this step
+};
+__device__ __forceinline__ JoinStep join_step(int mine, int level, int holders) {
+  JoinStep s;
+  s.stride = level == 0 ? 1 : (level == 1 ? kJoinGroup : kJoinGroup * kJoinGroup);
+  const int size = s.stride * kJoinGroup;
+  s.start = mine / size * size;
+  s.count = min(kJoinGroup, (holders - s.start + s.stride - 1) / s.stride);
+  s.counter = s.start + level;  // distinct over groups and levels: start is a multiple of 8 ^ (level + 1)
+  s.top = size >= holders;
+  return s;
+}
+
 // ------------------------------------------------------------------ the kernel
 
 template <int kDim, bool kFp8>
@@ -685,6 +728,20 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
       uint16_t* out = p.out + token * p.out_stride + static_cast<int64_t>(head) * kDim;
       // blocks of eight columns of all rows: neighbouring threads write neighbouring addresses
       float* part = p.part + static_cast<int64_t>(slot) * T::kRows * kDim + r * 8;
+      const auto write_out = [&](const float (&o)[32], int c, float unit_out) {  // columns [c, c + 32) of this row
+        if (!live) return;
+        uint32_t x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = f32x2_to_bf16x2(o[2 * i] * unit_out, o[2 * i + 1] * unit_out);
+        if (wide) {
+          stg256(out + c, x);
+          stg256(out + c + 16, x + 8);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; i += 4)
+            *reinterpret_cast<uint4*>(out + c + 2 * i) = make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+        }
+      };
       const bool noted = *static_cast<volatile int*>(&bars->noted) != 0;
       const KeyRange kr = key_range(p, w);
 #pragma unroll 1
@@ -715,54 +772,46 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
           qscale = hand_q();
           ready = true;
         }
-        if (!live) continue;
         if (whole) {
-          uint32_t x[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] = f32x2_to_bf16x2(o[2 * i] * inv, o[2 * i + 1] * inv);
-          if (wide) {
-            stg256(out + c, x);
-            stg256(out + c + 16, x + 8);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 16; i += 4)
-              *reinterpret_cast<uint4*>(out + c + 2 * i) = make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-          }
+          write_out(o, c, inv);
         } else {
 #pragma unroll
           for (int i = 0; i < 32; i += 8)
             stg256(part + static_cast<int64_t>((c + i) / 8) * T::kRows * 8, reinterpret_cast<const uint32_t*>(o) + i);
         }
       }
-      if (live) {
-        if (!whole) {
-          float* ml = p.part + static_cast<int64_t>(2) * gridDim.x * T::kRows * kDim;
-          *reinterpret_cast<float2*>(ml + (static_cast<int64_t>(slot) * T::kRows + r) * 2) = make_float2(m, l);
-        } else if (p.lse) {
-          p.lse[token * p.n_heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-        }
-      }
-      // ---- the last holder of a split item joins its shares of these rows, in range order
+      float* ml = p.part + static_cast<int64_t>(2) * gridDim.x * T::kRows * kDim;  // references and sums, after all shares
+      if (!whole)
+        *reinterpret_cast<float2*>(ml + (static_cast<int64_t>(slot) * T::kRows + r) * 2) = make_float2(m, l);
+      else if (live && p.lse)
+        p.lse[token * p.n_heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+      // ---- the join's steps of a split item, for as long as this group is the last to arrive
       if (!pc.whole) {
         const Holders h = holders_of(w, ranges, kTiling);
-        if (last_to_arrive<128>(p.counters + 2 * h.c0 + g, h.c1 - h.c0 + 1, 1 + g, &bars->say[g]) && live) {
-          const float* ml = p.part + static_cast<int64_t>(2) * gridDim.x * T::kRows * kDim;
+        int mine = static_cast<int>(blockIdx.x) - h.c0;
+        for (int level = 0;; ++level) {
+          const JoinStep s = join_step(mine, level, h.c1 - h.c0 + 1);
+          if (!last_to_arrive<128>(p.counters + 2 * (h.c0 + s.counter) + g, s.count, 1 + g, &bars->say[g])) break;
+          const auto slot_of = [&](int i) {
+            const int share = s.start + i * s.stride;
+            return static_cast<int64_t>(2 * (h.c0 + share) + (share == 0));
+          };
           float high = -INFINITY, all = 0.f;
-          for (int c = h.c0; c <= h.c1; ++c)
-            high = fmaxf(high, __ldcg(ml + (static_cast<int64_t>(2 * c + (c == h.c0)) * T::kRows + r) * 2));
-          for (int c = h.c0; c <= h.c1; ++c) {
-            const float2 v = __ldcg(reinterpret_cast<const float2*>(ml + (static_cast<int64_t>(2 * c + (c == h.c0)) * T::kRows + r) * 2));
+          for (int i = 0; i < s.count; ++i) high = fmaxf(high, __ldcg(ml + (slot_of(i) * T::kRows + r) * 2));
+          for (int i = 0; i < s.count; ++i) {
+            const float2 v = __ldcg(reinterpret_cast<const float2*>(ml + (slot_of(i) * T::kRows + r) * 2));
             all += v.y * (high == -INFINITY ? 1.0f : exp2_approx(v.x - high));
           }
-          const float unit_out = all == 0.f ? 0.f : vs / all;
+          const float unit_out = !s.top ? 1.0f : (all == 0.f ? 0.f : vs / all);
+          float* into = p.part + slot_of(0) * T::kRows * kDim + r * 8;
 #pragma unroll 1
           for (int c0 = 0; c0 < kDim; c0 += 32) {
             float o[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = 0.f;
 #pragma unroll 2
-            for (int c = h.c0; c <= h.c1; ++c) {
-              const int64_t at = 2 * c + (c == h.c0);
+            for (int c = 0; c < s.count; ++c) {
+              const int64_t at = slot_of(c);
               const float v = __ldcg(ml + (at * T::kRows + r) * 2);
               const float a = high == -INFINITY ? 1.0f : exp2_approx(v - high);
               const float4* x = reinterpret_cast<const float4*>(p.part + at * T::kRows * kDim +
@@ -773,14 +822,20 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
                 o[4 * i] += a * y.x, o[4 * i + 1] += a * y.y, o[4 * i + 2] += a * y.z, o[4 * i + 3] += a * y.w;
               }
             }
+            if (s.top)
+              write_out(o, c0, unit_out);
+            else
 #pragma unroll
-            for (int i = 0; i < 32; i += 8)
-              *reinterpret_cast<uint4*>(out + c0 + i) =
-                  make_uint4(f32x2_to_bf16x2(o[i] * unit_out, o[i + 1] * unit_out), f32x2_to_bf16x2(o[i + 2] * unit_out, o[i + 3] * unit_out),
-                             f32x2_to_bf16x2(o[i + 4] * unit_out, o[i + 5] * unit_out), f32x2_to_bf16x2(o[i + 6] * unit_out, o[i + 7] * unit_out));
+              for (int i = 0; i < 32; i += 8)
+                stg256(into + static_cast<int64_t>((c0 + i) / 8) * T::kRows * 8, reinterpret_cast<const uint32_t*>(o) + i);
           }
-          if (p.lse)
-            p.lse[token * p.n_heads + head] = all == 0.f ? -INFINITY : (high + log2f(all)) * 0.6931471805599453f;
+          if (s.top) {
+            if (live && p.lse)
+              p.lse[token * p.n_heads + head] = all == 0.f ? -INFINITY : (high + log2f(all)) * 0.6931471805599453f;
+            break;
+          }
+          *reinterpret_cast<float2*>(ml + (slot_of(0) * T::kRows + r) * 2) = make_float2(high, all);
+          mine = s.start;  // the joined share takes the place of the group's first
         }
       }
       tc_fence_before();  // O has been read before the next item's first P is handed over
