@@ -30,6 +30,17 @@
 
 namespace nvfp4 {
 
+// A ring of stages: the place of tile t, the phase in which it is filled, and the phase in which
+// the tile that was there before it is released.
+template <int kN>
+struct Ring {
+  static constexpr int kStages = kN, kLog2 = log2c(kN);
+  static __device__ __forceinline__ uint32_t at(uint32_t t) { return t & (kN - 1); }
+  static __device__ __forceinline__ uint32_t phase(uint32_t t) { return (t >> kLog2) & 1; }
+  static __device__ __forceinline__ bool reused(uint32_t t) { return t >= kN; }
+  static __device__ __forceinline__ uint32_t before(uint32_t t) { return ((t >> kLog2) - 1) & 1; }
+};
+
 template <int kDim, bool kFp8>
 struct ChunkTile {
   static constexpr int kGroups = kDim == 256 ? 1 : 2;      // softmax warpgroups of 128 rows
@@ -47,9 +58,14 @@ struct ChunkTile {
   static constexpr int kRawB = kSubB * kSub;               // a K or V tile as it is in the pool
   static constexpr int kTileB = kKeys * kDim * 2;          // a 16-bit tile: [kDim / 64][kKeys][128 bytes]
   static constexpr int kQB = 128 * kDim * 2;               // a group's Q: [kDim / 64][128][128 bytes]
-  static constexpr int kRing = kGroups * kQB;              // offset of the K ring
-  static constexpr int kRaw = kRing + 4 * kTileB;
-  static constexpr int kBars = kRaw + (kFp8 ? 2 * kRawB : 0);
+  // stages of the rings (K and V as the products read them, E4M3 tiles as they are copied):
+  // powers of two, as many as fit
+  using KRing = Ring<kDim == 64 ? 4 : (kFp8 ? 1 : 2)>;
+  using VRing = Ring<kDim == 64 ? 4 : 2>;
+  using RawRing = Ring<4>;
+  static constexpr int kKAt = kGroups * kQB, kVAt = kKAt + KRing::kStages * kTileB;
+  static constexpr int kRaw = kVAt + VRing::kStages * kTileB;
+  static constexpr int kBars = kRaw + (kFp8 ? RawRing::kStages * kRawB : 0);
   static constexpr size_t kSmem = 1024 + kBars + 1024;
   // TMEM columns: O of each group, then the S buffers
   static constexpr int kSCol = kGroups * kDim;
@@ -188,9 +204,9 @@ __device__ __forceinline__ uint32_t umma_offset(int rows, int r, int c) {
 
 // What the warps of a CTA share besides tiles: barriers of the rings and hand-overs.
 struct ChunkBars {
-  uint64_t k_full[2], k_ready[2], k_empty[2];
-  uint64_t v_full[2], v_ready[2], v_empty[2];
-  uint64_t raw_full[2], raw_empty[2];
+  uint64_t k_full[4], k_ready[4], k_empty[4];
+  uint64_t v_full[4], v_ready[4], v_empty[4];
+  uint64_t raw_full[4], raw_empty[4];
   uint64_t q_full[2];
   uint64_t s_full[2];             // one per group, or per S buffer
   uint64_t p_full[2][2];          // the same, for each half of the keys
@@ -250,20 +266,25 @@ template <int kDim, bool kFp8>
 __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
     attn_chunk_kernel(const AttnJob p, const __grid_constant__ KvMaps maps) {
   using T = ChunkTile<kDim, kFp8>;
+  using KRing = typename T::KRing;
+  using VRing = typename T::VRing;
+  using RawRing = typename T::RawRing;
   constexpr int kG = T::kGroups, kKeys = T::kKeys;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw0 = smem_addr(smem_raw);
   const uint32_t base = (raw0 + 1023u) & ~1023u;
   ChunkBars* bars = reinterpret_cast<ChunkBars*>(smem_raw + (base - raw0) + T::kBars);
   static_assert(sizeof(ChunkBars) <= 1024, "barriers");
-  const uint32_t q_at = base, k_at = base + T::kRing, v_at = k_at + 2 * T::kTileB, raw_at = base + T::kRaw;
+  const uint32_t q_at = base, k_at = base + T::kKAt, v_at = base + T::kVAt, raw_at = base + T::kRaw;
 
   const int warp = static_cast<int>(uniform(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(bars->k_full + i, 1), mbar_init(bars->k_ready + i, 2), mbar_init(bars->k_empty + i, 1);
       mbar_init(bars->v_full + i, 1), mbar_init(bars->v_ready + i, 2), mbar_init(bars->v_empty + i, 1);
       mbar_init(bars->raw_full + i, 1), mbar_init(bars->raw_empty + i, 2);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(bars->q_full + i, 4), mbar_init(bars->s_full + i, 1);
       mbar_init(&bars->p_full[i][0], 4), mbar_init(&bars->p_full[i][1], 4);
       mbar_init(bars->o_full + i, 1);
@@ -328,14 +349,15 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
           uint64_t* full;
           uint32_t dst;
           if constexpr (kFp8) {
-            const uint32_t st = raw & 1;
-            if (raw >= 2) NVFP4_WAIT(bars->raw_empty + st, ((raw >> 1) - 1) & 1);
+            const uint32_t st = RawRing::at(raw);
+            if (RawRing::reused(raw)) NVFP4_WAIT(bars->raw_empty + st, RawRing::before(raw));
             full = bars->raw_full + st;
             dst = raw_at + st * T::kRawB;
             ++raw;
           } else {
-            const uint32_t st = g & 1;
-            if (g >= 2) NVFP4_WAIT((is_v ? bars->v_empty : bars->k_empty) + st, ((g >> 1) - 1) & 1);
+            const uint32_t st = is_v ? VRing::at(g) : KRing::at(g);
+            if (is_v ? VRing::reused(g) : KRing::reused(g))
+              NVFP4_WAIT((is_v ? bars->v_empty : bars->k_empty) + st, is_v ? VRing::before(g) : KRing::before(g));
             full = (is_v ? bars->v_full : bars->k_full) + st;
             dst = (is_v ? v_at : k_at) + st * T::kTileB;
           }
@@ -374,7 +396,7 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
       const uint64_t v_desc = umma_desc(v_at, kKeys * 128, 1024);
       const auto qk = [&](int g, uint32_t t) {
         const uint32_t d = tmem + T::kSCol + (kG == 2 ? g : (t & 1)) * kKeys;
-        const uint64_t a = q_desc + g * (T::kQB >> 4), b = k_desc + (t & 1) * (T::kTileB >> 4);
+        const uint64_t a = q_desc + g * (T::kQB >> 4), b = k_desc + KRing::at(t) * (T::kTileB >> 4);
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < kDim / 16; ++k)
@@ -386,7 +408,7 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
       };
       const auto pv = [&](int g, uint32_t t, int half, bool add) {
         const uint32_t a = tmem + T::kSCol + (kG == 2 ? g : (t & 1)) * kKeys;
-        const uint64_t b = v_desc + (t & 1) * (T::kTileB >> 4);
+        const uint64_t b = v_desc + VRing::at(t) * (T::kTileB >> 4);
         if (elect_one()) {
 #pragma unroll
           for (int i = 0; i < kKeys / 32; ++i) {
@@ -402,7 +424,7 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
         __syncwarp();
       };
       const auto wait_k = [&](uint32_t t) {
-        NVFP4_WAIT((kFp8 ? bars->k_ready : bars->k_full) + (t & 1), (t >> 1) & 1);
+        NVFP4_WAIT((kFp8 ? bars->k_ready : bars->k_full) + KRing::at(t), KRing::phase(t));
       };
       for (long long u = u0; u < u1;) {
         walk_to(p, w, u, kTiling);
@@ -418,17 +440,17 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
         wait_k(nt);
         tc_fence_after();
         for (int g = 0; g < groups; ++g) qk(g, nt);
-        free_tile(bars->k_empty + (nt & 1));
+        free_tile(bars->k_empty + KRing::at(nt));
         for (int j = 0; j < n; ++j) {
           const uint32_t t = nt + j;
           if (kG == 1 && j + 1 < n) {
             wait_k(t + 1);
             tc_fence_after();
             qk(0, t + 1);
-            free_tile(bars->k_empty + ((t + 1) & 1));
+            free_tile(bars->k_empty + KRing::at(t + 1));
           }
-          NVFP4_WAIT(bars->v_ready + (t & 1), (t >> 1) & 1);
-          if constexpr (!kFp8) NVFP4_WAIT(bars->v_full + (t & 1), (t >> 1) & 1);
+          NVFP4_WAIT(bars->v_ready + VRing::at(t), VRing::phase(t));
+          if constexpr (!kFp8) NVFP4_WAIT(bars->v_full + VRing::at(t), VRing::phase(t));
           if (kG == 2 && j + 1 < n) wait_k(t + 1);
           for (int g = 0; g < groups; ++g) {
             const int pb = kG == 2 ? g : (t & 1);
@@ -441,8 +463,8 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
             pv(g, t, 1, true);
             if (kG == 2 && j + 1 < n) qk(g, t + 1);
           }
-          free_tile(bars->v_empty + (t & 1));
-          if (kG == 2 && j + 1 < n) free_tile(bars->k_empty + ((t + 1) & 1));
+          free_tile(bars->v_empty + VRing::at(t));
+          if (kG == 2 && j + 1 < n) free_tile(bars->k_empty + KRing::at(t + 1));
         }
         nt += n;
       }
@@ -460,8 +482,8 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
         bool noted = false;
         if constexpr (!kFp8) {
           for (int j = 0; j < n; ++j) {
-            const uint32_t t = nt + j, st = t & 1;
-            NVFP4_WAIT(bars->v_full + st, (t >> 1) & 1);
+            const uint32_t t = nt + j, st = VRing::at(t);
+            NVFP4_WAIT(bars->v_full + st, VRing::phase(t));
             const int key0 = (first + j) * kKeys;
             if (partly_seen(kr, key0, kKeys)) {
               const uint32_t tile = v_at + st * T::kTileB;
@@ -487,32 +509,40 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
           for (int c = 0; c < 2 * n; ++c, ++raw) {
             const bool is_v = c == 2 * n - 1 || (c > 0 && c % 2 == 0);
             const int j = c == 0 ? 0 : (is_v ? (c == 2 * n - 1 ? n - 1 : c / 2 - 1) : (c + 1) / 2);
-            const uint32_t t = nt + j, st = t & 1, rst = raw & 1;
-            NVFP4_WAIT(bars->raw_full + rst, (raw >> 1) & 1);
-            if (t >= 2) NVFP4_WAIT((is_v ? bars->v_empty : bars->k_empty) + st, ((t >> 1) - 1) & 1);
+            const uint32_t t = nt + j, st = is_v ? VRing::at(t) : KRing::at(t), rst = RawRing::at(raw);
+            NVFP4_WAIT(bars->raw_full + rst, RawRing::phase(raw));
+            if (is_v ? VRing::reused(t) : KRing::reused(t))
+              NVFP4_WAIT((is_v ? bars->v_empty : bars->k_empty) + st, is_v ? VRing::before(t) : KRing::before(t));
             const int key0 = (first + j) * kKeys;
             const bool clean = is_v && partly_seen(kr, key0, kKeys);
             const uint32_t from = raw_at + rst * T::kRawB, to = (is_v ? v_at : k_at) + st * T::kTileB;
-            for (int r = who; r < kKeys; r += 64) {
-              const bool seen = key0 + r >= kr.any_lo && key0 + r < kr.any_hi;
+            const auto convert = [&](auto cleaning) {
 #pragma unroll 1
-              for (int x0 = 0; x0 < kDim / 16; x0 += 4) {  // (four loads in flight)
-                uint4 v[4];
+              for (int r = who; r < kKeys; r += 64) {
+                const bool seen = key0 + r >= kr.any_lo && key0 + r < kr.any_hi;
+#pragma unroll 1
+                for (int x0 = 0; x0 < kDim / 16; x0 += 4) {  // (four loads in flight)
+                  uint4 v[4];
 #pragma unroll
-                for (int x = 0; x < 4; ++x) v[x] = lds128(from + tile_offset<T>(r, x0 + x));
+                  for (int x = 0; x < 4; ++x) v[x] = lds128(from + tile_offset<T>(r, x0 + x));
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                  if (clean) v[x] = clean_codes(v[x], seen, noted);
-                  uint4 a, b;
-                  e4m3x4_to_f16x2(v[x].x, a.x, a.y);
-                  e4m3x4_to_f16x2(v[x].y, a.z, a.w);
-                  e4m3x4_to_f16x2(v[x].z, b.x, b.y);
-                  e4m3x4_to_f16x2(v[x].w, b.z, b.w);
-                  sts128(to + umma_offset(kKeys, r, 2 * (x0 + x)), a);
-                  sts128(to + umma_offset(kKeys, r, 2 * (x0 + x) + 1), b);
+                  for (int x = 0; x < 4; ++x) {
+                    if constexpr (decltype(cleaning)::value) v[x] = clean_codes(v[x], seen, noted);
+                    uint4 a, b;
+                    e4m3x4_to_f16x2(v[x].x, a.x, a.y);
+                    e4m3x4_to_f16x2(v[x].y, a.z, a.w);
+                    e4m3x4_to_f16x2(v[x].z, b.x, b.y);
+                    e4m3x4_to_f16x2(v[x].w, b.z, b.w);
+                    sts128(to + umma_offset(kKeys, r, 2 * (x0 + x)), a);
+                    sts128(to + umma_offset(kKeys, r, 2 * (x0 + x) + 1), b);
+                  }
                 }
               }
-            }
+            };
+            if (clean)
+              convert(std::true_type{});
+            else
+              convert(std::false_type{});
             if (noted) *static_cast<volatile int*>(&bars->noted) = 1;
             fence_proxy_async_smem();
             __syncwarp();
