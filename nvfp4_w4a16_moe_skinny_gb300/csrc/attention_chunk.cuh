@@ -6,8 +6,8 @@
 // heads of 64 and 128 values, one for 256) by kKeys keys.
 //
 // Roles of a CTA (one per SM).  Warp 0 copies K and V tiles by TMA into two-stage
-// rings; one thread of warp 1 issues every MMA and commits it to mbarriers; warps
-// 2 and 3 make tiles fit for the tensor cores (below); each softmax warpgroup owns
+// rings; one thread of warp 1 issues every MMA and commits it to mbarriers; two or
+// four warps make tiles fit for the tensor cores (below); each softmax warpgroup owns
 // 128 rows, a thread a row, so maxima and sums need no exchange.  Per tile: S = Q K^T
 // into TMEM; the row's thread reads S, takes weights 2^(s - m), writes them back as
 // 16-bit P over S; O += P V with P read from TMEM.  With two row groups the
@@ -19,8 +19,8 @@
 // tensor cores' hands; weights stay below 2^8 (bf16 holds them as exactly as those below
 // 1; f16 weights, for E4M3 caches, are offset by 2^7 and stay below 2^15).
 //
-// Warps 2 and 3.  For an E4M3 cache they convert tiles to f16 (exact).  For both
-// kinds they clean V in tiles that some row does not wholly see: keys outside
+// Fit tiles.  For an E4M3 cache the tiles are converted to f16 (exact).  For both
+// kinds of cache V is cleaned in tiles that some row does not wholly see: keys outside
 // every row's reach become zeros (the pool may hold anything there, and 0 * inf is
 // NaN), and an infinity or NaN in a key that only some rows see is taken out of the
 // product and noted; the rows that see it add it at the end from the pool itself.
@@ -48,7 +48,12 @@ struct ChunkTile {
   static constexpr int kKeys = kDim == 256 ? 64 : 128;
   static constexpr int kSBuf = kDim == 256 ? 2 : 1;        // S buffers per group
   static constexpr int kOver = 4, kSnap = 4;               // an item's own cost, in units (Tiling)
-  static constexpr int kThreadsAll = 128 + 128 * kGroups;
+  // warps that make tiles fit: two beside the copies and the products, or (E4M3 and 128 values:
+  // 256 conversions a row and tile; 1,404 us with two warps, 1,162 with four, for 2,048 tokens over
+  // 32,768 keys) a warpgroup of their own; the softmax warpgroups follow
+  static constexpr bool kFitGroup = kFp8 && kDim == 128;
+  static constexpr int kFit0 = kFitGroup ? 4 : 2, kFits = kFitGroup ? 4 : 2, kSoft0 = kFit0 + kFits;
+  static constexpr int kThreadsAll = 32 * kSoft0 + 128 * kGroups;
   static constexpr int kEl = kFp8 ? 1 : 2;
   // boxes of the pool (as AttnTile names them, for tile_offset)
   static constexpr int kRowB = kDim * kEl < 128 ? kDim * kEl : 128;
@@ -280,9 +285,9 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
   const int warp = static_cast<int>(uniform(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 4; ++i) {
-      mbar_init(bars->k_full + i, 1), mbar_init(bars->k_ready + i, 2), mbar_init(bars->k_empty + i, 1);
-      mbar_init(bars->v_full + i, 1), mbar_init(bars->v_ready + i, 2), mbar_init(bars->v_empty + i, 1);
-      mbar_init(bars->raw_full + i, 1), mbar_init(bars->raw_empty + i, 2);
+      mbar_init(bars->k_full + i, 1), mbar_init(bars->k_ready + i, T::kFits), mbar_init(bars->k_empty + i, 1);
+      mbar_init(bars->v_full + i, 1), mbar_init(bars->v_ready + i, T::kFits), mbar_init(bars->v_empty + i, 1);
+      mbar_init(bars->raw_full + i, 1), mbar_init(bars->raw_empty + i, T::kFits);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bars->q_full + i, 4), mbar_init(bars->s_full + i, 1);
@@ -322,8 +327,11 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
 
   // tile counts over all items so far: ring positions and phases
   uint32_t nt = 0;
-  if (warp < 4) {
-    if constexpr (kG == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+  // Registers: with two softmax warpgroups the others give theirs to them (the shares add up to
+  // what the block was launched with: 384 * 168 = 128 * (72 + 2 * 216), 512 * 128 = 128 * (64 + 64 + 2 * 192))
+  if (warp < T::kSoft0) {
+    if constexpr (kG == 2 && !T::kFitGroup) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if constexpr (kG == 2 && T::kFitGroup) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 0) {
       // ------------------------------------------------------------ copies
       const int piece_log2 = min(p.page_log2, log2c(kKeys));
@@ -468,9 +476,10 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
         }
         nt += n;
       }
-    } else {
+    } else if (warp >= T::kFit0) {
       // ------------------------------------------------------------ tiles made fit
-      const int who = (warp - 2) * 32 + lane;
+      constexpr int kWho = 32 * T::kFits;
+      const int who = (warp - T::kFit0) * 32 + lane;
       uint32_t raw = 0;
       for (long long u = u0; u < u1;) {
         walk_to(p, w, u, kTiling);
@@ -487,7 +496,7 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
             const int key0 = (first + j) * kKeys;
             if (partly_seen(kr, key0, kKeys)) {
               const uint32_t tile = v_at + st * T::kTileB;
-              for (int r = who; r < kKeys; r += 64) {
+              for (int r = who; r < kKeys; r += kWho) {
                 const bool seen = key0 + r >= kr.any_lo && key0 + r < kr.any_hi;
 #pragma unroll 1
                 for (int c0 = 0; c0 < kDim / 8; c0 += 8) {  // (eight loads in flight)
@@ -518,7 +527,7 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
             const uint32_t from = raw_at + rst * T::kRawB, to = (is_v ? v_at : k_at) + st * T::kTileB;
             const auto convert = [&](auto cleaning) {
 #pragma unroll 1
-              for (int r = who; r < kKeys; r += 64) {
+              for (int r = who; r < kKeys; r += kWho) {
                 const bool seen = key0 + r >= kr.any_lo && key0 + r < kr.any_hi;
 #pragma unroll 1
                 for (int x0 = 0; x0 < kDim / 16; x0 += 4) {  // (four loads in flight)
@@ -557,8 +566,9 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
     }
   } else {
     // -------------------------------------------------------------- softmax
-    if constexpr (kG == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-    const int g = (warp - 4) >> 2;
+    if constexpr (kG == 2 && !T::kFitGroup) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    if constexpr (kG == 2 && T::kFitGroup) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    const int g = (warp - T::kSoft0) >> 2;
     const int row = (warp & 3) * 32 + lane;              // of the group: its TMEM lane
     const uint32_t lane_at = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t o_at = tmem + lane_at + g * kDim;
