@@ -187,11 +187,23 @@ __device__ __forceinline__ void find_range(const AttnJob& p, const Tiling& g, in
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int kNW = kThreadsInBlock / 32;
   long long mine = 0, incl = 0;
-  if (p.n_seqs <= 32) {  // few short sequences: every warp finds the same by itself
+  if (p.n_seqs <= 32) {  // few sequences, few of them long: every warp finds the same by itself
     Sequence s{};
     if (lane < p.n_seqs) s = sequence_of(p, lane, g);
-    if (!__any_sync(0xffffffffu, s.tiles > 4)) {
-      mine = incl = tile_units(p, s, 0, 1, g);
+    unsigned longs = __ballot_sync(0xffffffffu, s.tiles > 4);
+    if (__popc(longs) <= 2) {
+      mine = s.tiles > 4 ? 0 : tile_units(p, s, 0, 1, g);
+      for (; longs; longs &= longs - 1) {
+        const int who = __ffs(longs) - 1;
+        Sequence o;
+        o.n = __shfl_sync(0xffffffffu, s.n, who), o.len = __shfl_sync(0xffffffffu, s.len, who);
+        o.rows = __shfl_sync(0xffffffffu, s.rows, who), o.tiles = __shfl_sync(0xffffffffu, s.tiles, who);
+        long long part = tile_units(p, o, lane, 32, g);
+#pragma unroll 1
+        for (int d = 16; d > 0; d >>= 1) part += __shfl_xor_sync(0xffffffffu, part, d);
+        if (lane == who) mine = part;
+      }
+      incl = mine;
 #pragma unroll 1
       for (int o = 1; o < 32; o <<= 1) {
         const long long v = __shfl_up_sync(0xffffffffu, incl, o);
@@ -301,7 +313,8 @@ __device__ __forceinline__ void walk_to(const AttnJob& p, Walk& w, long long u, 
       }
       const long long all = static_cast<long long>(span) * (p.n_kv - w.h);
       if (u < w.item0 + all) {
-        const int k = static_cast<int>((u - w.item0) / span);
+        const int k = all >> 32 ? static_cast<int>((u - w.item0) / span)
+                                : static_cast<int>(static_cast<uint32_t>(u - w.item0) / static_cast<uint32_t>(span));
         w.h += k;
         w.item0 += static_cast<long long>(k) * span;
         return;
@@ -624,7 +637,8 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, a
   if (warp == T::kConsumers) {
     // -------------------------------------------------------------- producer
     const int piece_log2 = min(p.page_log2, log2c(T::kKeys));
-    const int pieces = T::kKeys >> piece_log2;  // of a unit: at most 16
+    constexpr int kMostPieces = T::kKeys / 16;
+    const int pieces = T::kKeys >> piece_log2;  // of a unit: at most kMostPieces
     const uint32_t bytes = 2u << piece_log2 << log2c(kDim * T::kEl);
     int st = 0;
     uint32_t round = 0;
@@ -640,21 +654,24 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, a
         const int later = lane < pieces && i + 1 < n
                               ? piece_page(p, table, (pc.first + i + 1) * pieces + lane, piece_log2, w.t) : -1;
         if (round > 0 && !mbar_wait_warp(empty + st, (round - 1) & 1)) return;
-        uint32_t todo = __ballot_sync(0xffffffffu, page >= 0);
         const uint32_t bar = smem_addr(full + st);
-        if (elect_one()) mbar_arrive_expect_tx_s(bar, bytes * __popc(todo));
-        __syncwarp();
-        for (; todo; todo &= todo - 1) {
-          const int j = __ffs(todo) - 1;
-          const int at = static_cast<int>(__shfl_sync(0xffffffffu, page, j));
-          const uint32_t dst = ring + st * T::kStageB + (j << piece_log2) * (kDim * T::kEl);
-          const int row = (((pc.first + i) * pieces + j) << piece_log2) & ((1 << p.page_log2) - 1);
-          if (elect_one()) {
-            tma_load_5d(dst, &maps.k, 0, row, 0, head, at, bar);
-            tma_load_5d(dst + T::kTileB, &maps.v, 0, row, 0, head, at, bar);
+        const uint32_t all = bytes * __popc(__ballot_sync(0xffffffffu, page >= 0));
+        int at[kMostPieces];  // all pieces' pages first, then the copies back to back
+#pragma unroll
+        for (int j = 0; j < kMostPieces; ++j) at[j] = __shfl_sync(0xffffffffu, page, j);
+        if (elect_one()) {
+          mbar_arrive_expect_tx_s(bar, all);
+#pragma unroll
+          for (int j = 0; j < kMostPieces; ++j) {
+            if (j >= pieces) break;
+            if (at[j] < 0) continue;
+            const uint32_t dst = ring + st * T::kStageB + (j << piece_log2) * (kDim * T::kEl);
+            const int row = (((pc.first + i) * pieces + j) << piece_log2) & ((1 << p.page_log2) - 1);
+            tma_load_5d(dst, &maps.k, 0, row, 0, head, at[j], bar);
+            tma_load_5d(dst + T::kTileB, &maps.v, 0, row, 0, head, at[j], bar);
           }
-          __syncwarp();
         }
+        __syncwarp();
         page = later;
         if (++st == T::kStages) st = 0, ++round;
       }

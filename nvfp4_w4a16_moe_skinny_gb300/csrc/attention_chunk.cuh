@@ -335,7 +335,8 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
     if (warp == 0) {
       // ------------------------------------------------------------ copies
       const int piece_log2 = min(p.page_log2, log2c(kKeys));
-      const int pieces = kKeys >> piece_log2;  // of a tile: at most 8
+      constexpr int kMostPieces = kKeys / 16;
+      const int pieces = kKeys >> piece_log2;  // of a tile: at most kMostPieces
       uint32_t raw = 0;
       for (long long u = u0; u < u1;) {
         walk_to(p, w, u, kTiling);
@@ -374,23 +375,25 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
             page_next = look_up(j + 1);
           }
           const int page = is_v && c == 2 * n - 1 ? page_k : (is_v ? page_v : page_k);
-          uint32_t todo = __ballot_sync(0xffffffffu, page >= 0);
           const uint32_t bar = smem_addr(full);
-          if (elect_one())
-            mbar_arrive_expect_tx_s(bar, __popc(todo) << piece_log2 << log2c(T::kRowB * T::kSub));
-          __syncwarp();
-          for (; todo; todo &= todo - 1) {
-            const int i = __ffs(todo) - 1;
-            const int at = static_cast<int>(__shfl_sync(0xffffffffu, page, i));
-            const int key = (pc.first + j) * kKeys + (i << piece_log2);
-            if (elect_one()) {
+          const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, page >= 0)) << piece_log2 << log2c(T::kRowB * T::kSub);
+          int at[kMostPieces];  // all pieces' pages first, then the copies back to back
+#pragma unroll
+          for (int i = 0; i < kMostPieces; ++i) at[i] = __shfl_sync(0xffffffffu, page, i);
+          if (elect_one()) {
+            mbar_arrive_expect_tx_s(bar, bytes);
+#pragma unroll
+            for (int i = 0; i < kMostPieces; ++i) {
+              if (i >= pieces) break;
+              if (at[i] < 0) continue;
+              const int key = (pc.first + j) * kKeys + (i << piece_log2);
 #pragma unroll
               for (int sub = 0; sub < T::kSub; ++sub)
                 tma_load_5d(dst + sub * T::kSubB + (i << piece_log2) * T::kRowB, is_v ? &maps.v : &maps.k, 0,
-                            key & ((1 << p.page_log2) - 1), sub, head, at, bar);
+                            key & ((1 << p.page_log2) - 1), sub, head, at[i], bar);
             }
-            __syncwarp();
           }
+          __syncwarp();
         }
         nt += n;
       }

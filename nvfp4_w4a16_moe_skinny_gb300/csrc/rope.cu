@@ -18,6 +18,7 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kRopeThreads = 128;
+constexpr int kBatch = 4;  // heads whose loads a thread has in flight
 
 // What one launch does: up to three groups of heads per token (queries, keys,
 // values), each read from rows and written to rows or to cache slots.
@@ -144,41 +145,55 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeJob p) {
   const int64_t page = slot >> p.page_log2, off = slot & ((1 << p.page_log2) - 1);
   const int64_t base = kind ? page * p.page_stride + off * p.dim : t * p.y_stride;
   const int64_t head_step = kind ? static_cast<int64_t>(p.dim) << p.page_log2 : p.dim;
-#pragma unroll 4
-  for (int h = h0; h < h1; ++h) {
-    const uint4 va = *reinterpret_cast<const uint4*>(x + h * p.dim + a);
-    const uint4 vb = *reinterpret_cast<const uint4*>(x + h * p.dim + b);
-    float fa[8], fb[8];
-    unpack8(va, fa);
-    unpack8(vb, fb);
-    if (split) {
+  // four heads' loads first: a store could alias a later load for all the compiler knows
+  for (int hh = h0; hh < h1; hh += kBatch) {
+    uint4 va[kBatch], vb[kBatch];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float u = fa[i] * c[i] - fb[i] * s[i];
-        fb[i] = fb[i] * c[i] + fa[i] * s[i];
-        fa[i] = u;
-      }
-    } else if (turn) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float u = fa[2 * i] * c[i] - fa[2 * i + 1] * s[i];
-        fa[2 * i + 1] = fa[2 * i + 1] * c[i] + fa[2 * i] * s[i];
-        fa[2 * i] = u;
-        const float w = fb[2 * i] * c[4 + i] - fb[2 * i + 1] * s[4 + i];
-        fb[2 * i + 1] = fb[2 * i + 1] * c[4 + i] + fb[2 * i] * s[4 + i];
-        fb[2 * i] = w;
-      }
+    for (int k = 0; k < kBatch; ++k) {
+      const int h = min(hh + k, h1 - 1);
+      va[k] = *reinterpret_cast<const uint4*>(x + h * p.dim + a);
+      vb[k] = *reinterpret_cast<const uint4*>(x + h * p.dim + b);
     }
-    const int64_t o = base + h * head_step;
-    if (kE4M3 && kind > 0) {
-      const float sc = p.scale[kind - 1] ? __ldg(p.scale[kind - 1] + h) : 1.0f;
-      *reinterpret_cast<uint2*>(p.cache[kind - 1] + o + a) = pack8_e4m3(fa, sc);
-      *reinterpret_cast<uint2*>(p.cache[kind - 1] + o + b) = pack8_e4m3(fb, sc);
-    } else {
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int h = hh + k;
+      if (h >= h1) break;
+      const int64_t o = base + h * head_step;
       uint16_t* y = kind ? reinterpret_cast<uint16_t*>(p.cache[kind - 1]) : p.y;
-      // values that nothing turns are copied as they are
-      *reinterpret_cast<uint4*>(y + o + a) = turn ? pack8(fa) : va;
-      *reinterpret_cast<uint4*>(y + o + b) = turn ? pack8(fb) : vb;
+      if (!turn && !(kE4M3 && kind > 0)) {  // values that nothing turns are copied as they are
+        *reinterpret_cast<uint4*>(y + o + a) = va[k];
+        *reinterpret_cast<uint4*>(y + o + b) = vb[k];
+        continue;
+      }
+      float fa[8], fb[8];
+      unpack8(va[k], fa);
+      unpack8(vb[k], fb);
+      if (split) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float u = fa[i] * c[i] - fb[i] * s[i];
+          fb[i] = fb[i] * c[i] + fa[i] * s[i];
+          fa[i] = u;
+        }
+      } else if (turn) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float u = fa[2 * i] * c[i] - fa[2 * i + 1] * s[i];
+          fa[2 * i + 1] = fa[2 * i + 1] * c[i] + fa[2 * i] * s[i];
+          fa[2 * i] = u;
+          const float w = fb[2 * i] * c[4 + i] - fb[2 * i + 1] * s[4 + i];
+          fb[2 * i + 1] = fb[2 * i + 1] * c[4 + i] + fb[2 * i] * s[4 + i];
+          fb[2 * i] = w;
+        }
+      }
+      if (kE4M3 && kind > 0) {
+        const float sc = p.scale[kind - 1] ? __ldg(p.scale[kind - 1] + h) : 1.0f;
+        *reinterpret_cast<uint2*>(p.cache[kind - 1] + o + a) = pack8_e4m3(fa, sc);
+        *reinterpret_cast<uint2*>(p.cache[kind - 1] + o + b) = pack8_e4m3(fb, sc);
+      } else {
+        *reinterpret_cast<uint4*>(y + o + a) = pack8(fa);
+        *reinterpret_cast<uint4*>(y + o + b) = pack8(fb);
+      }
     }
   }
 }
