@@ -441,6 +441,9 @@ nvfp4_status lm_head_argmax_noalloc(const nvfp4_weight *w, const uint16_t *x, in
  *               NULL for all ones; must be NULL for a bf16 cache.  Positive.
  *   page_size   16, 32, 64, 128 or 256.  head_dim 64, 128 or 256.
  *   dtype       NVFP4_KV_BF16 or NVFP4_KV_E4M3.
+ *   maps        (host) NULL, or NVFP4_KV_MAPS_BYTES written by kv_cache_maps() for
+ *               these very pools, pages and sizes: attention then copies its TMA
+ *               descriptors from there instead of encoding them at every call.
  */
 #define NVFP4_KV_BF16 0u
 #define NVFP4_KV_E4M3 1u
@@ -455,7 +458,18 @@ typedef struct {
   int32_t n_kv_heads;
   int32_t head_dim;
   uint32_t dtype;
+  const void *maps;
 } nvfp4_kv_cache;
+
+/*
+ * Encodes a cache's TMA descriptors once, for nvfp4_kv_cache.maps (host;
+ * synchronous; needs the CUDA driver, no device work).
+ *   maps  (host) NVFP4_KV_MAPS_BYTES, 128-byte aligned; the caller keeps it as long as
+ *         a cache structure points to it, and encodes again when anything but the
+ *         scales of the structure changes.  cache->maps is not read.
+ */
+#define NVFP4_KV_MAPS_BYTES 1024
+nvfp4_status kv_cache_maps(const nvfp4_kv_cache *cache, void *maps);
 
 /*
  * The sequences of one attention call.

@@ -22,6 +22,7 @@ NVFP4_KV_BF16 = 0
 NVFP4_KV_E4M3 = 1
 NVFP4_ROPE_INTERLEAVED = 1
 NVFP4_ROPE_INVERSE = 2
+KV_MAPS_BYTES = 1024
 COUNTER_BYTES = 4096  # arrival counters at the start of an attention workspace
 LAYOUT_VERSION = 2
 
@@ -35,7 +36,7 @@ EXPORTS = (
     "lm_head_workspace_bytes", "lm_head_argmax", "lm_head_argmax_noalloc", "nvfp4_plan_info",
     "lm_head_sample", "moe_route_topk_ex", "lm_head_sample_ex", "nvfp4_plan_check", "moe_router_logits",
     "nvfp4_repack_host", "nvfp4_quantize_act", "nvfp4_gemm_w4a4", "lm_head_argmax_w4a4", "moe_forward", "nvfp4_selftest_wait_timeout",
-    "rope_frequencies", "rope_apply", "kv_append", "paged_attention_workspace_bytes", "paged_attention",
+    "rope_frequencies", "rope_apply", "kv_append", "kv_cache_maps", "paged_attention_workspace_bytes", "paged_attention",
 )
 
 
@@ -75,7 +76,7 @@ class CKVCache(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
                 ("v_scale", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("num_pages", ctypes.c_int32),
                 ("page_size", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
-                ("dtype", ctypes.c_uint32)]
+                ("dtype", ctypes.c_uint32), ("maps", ctypes.c_void_p)]
 
 
 class CBatch(ctypes.Structure):
@@ -91,7 +92,7 @@ def _need(ok: bool, what: str):
 class KVCache:
     """A paged key/value cache on the GPU: pools [num_pages, n_kv_heads, page_size, head_dim] of bf16, or of
     float8_e4m3fn holding value / scale with fp32 scales per kv head (None: ones).  Pages may be strided (k and v
-    in one pool); the rest is contiguous.  Keeps its tensors alive; make it once per pool."""
+    in one pool); the rest is contiguous.  Keeps its tensors and its TMA descriptors; make it once per pool."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor = None, v_scale: torch.Tensor = None):
         _need(k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype and k.stride() == v.stride(),
@@ -109,6 +110,12 @@ class KVCache:
         self.c = CKVCache(k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale), stride, pages, page, heads, dim,
                           NVFP4_KV_BF16 if k.dtype == torch.bfloat16 else NVFP4_KV_E4M3)
         self.ref = ctypes.byref(self.c)
+        self._maps = ctypes.create_string_buffer(KV_MAPS_BYTES + 128)
+        at = -(-ctypes.addressof(self._maps) // 128) * 128
+        st = load().lib.kv_cache_maps(self.ref, at)
+        if st:
+            raise NVFP4Error("kv_cache_maps", st)
+        self.c.maps = at
 
 
 class Batch:
@@ -194,6 +201,8 @@ def _sig(lib):
     lib.kv_append.argtypes = [_P, _P, _I64, _P, _I64, _I, _P, _P, _P, _I, ctypes.c_float, _I, _P, _I64, _I, _P, _I64,
                               _P]
     lib.kv_append.restype = ctypes.c_int
+    lib.kv_cache_maps.argtypes = [_P, _P]
+    lib.kv_cache_maps.restype = ctypes.c_int
     lib.paged_attention_workspace_bytes.restype = _SZ
     lib.paged_attention_workspace_bytes.argtypes = [_I] * 6
     lib.paged_attention.argtypes = [_P, _P, _P, _I64, _I, _I, ctypes.c_float, ctypes.c_float, _I, _P, _I64, _P, _P,
@@ -246,6 +255,7 @@ class Library:
         self.lib = ctypes.CDLL(path)
         _sig(self.lib)
         self._ws = {}
+        self._attention_bytes = {}  # workspace sizes by the sizes of a call
 
     # -------------------------------------------------------------- plumbing
     def _check(self, call, st):
@@ -567,8 +577,12 @@ class Library:
         elif with_lse:
             lse = torch.empty((tokens, heads), dtype=torch.float32, device=dev)
         raw = _raw_stream(stream, dev)
-        nbytes = self.lib.paged_attention_workspace_bytes(tokens, batch.n_seqs, batch.max_new, heads, cache.n_kv_heads,
-                                                          dim)
+        sizes = (tokens, batch.n_seqs, batch.max_new, heads, cache.n_kv_heads, dim)
+        nbytes = self._attention_bytes.get(sizes)
+        if nbytes is None:
+            if len(self._attention_bytes) > 4096:
+                self._attention_bytes.clear()
+            nbytes = self._attention_bytes[sizes] = self.lib.paged_attention_workspace_bytes(*sizes)
         ws = self._stream_workspace("attention", nbytes, dev, raw, stream)
         st = self.lib.paged_attention(
             cache.ref, batch.ref, q.data_ptr(), stride, tokens, heads, dim ** -0.5 if scale is None else scale, softcap,

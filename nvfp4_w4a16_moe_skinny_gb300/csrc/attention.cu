@@ -29,6 +29,12 @@ bool encode_pool_map(CUtensorMap* map, const nvfp4_kv_cache* c, void* base, int 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The maps of both pools for the kernel and tile of `s`.
+bool encode_maps(KvMaps* maps, const nvfp4_kv_cache* c, const AttnShape& s) {
+  const int box = std::min(c->page_size, s.box_keys);
+  return encode_pool_map(&maps->k, c, c->k, box, !s.chunk) && encode_pool_map(&maps->v, c, c->v, box, !s.chunk);
+}
+
 bool sizes_ok(int n_tokens, int n_seqs, int max_new, int n_heads, int n_kv_heads, int head_dim) {
   if (n_tokens < 0 || n_seqs < 0 || max_new < 0 || n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads) return false;
   if (head_dim != 64 && head_dim != 128 && head_dim != 256) return false;
@@ -46,6 +52,20 @@ int64_t packed_rows(int n_tokens, int max_new, int n_heads, int n_kv_heads) {
 using namespace nvfp4;
 
 extern "C" {
+
+nvfp4_status kv_cache_maps(const nvfp4_kv_cache* cache, void* maps) {
+  static_assert(sizeof(KvMaps) * kMapPairs == NVFP4_KV_MAPS_BYTES && alignof(KvMaps) <= 128, "maps");
+  if (const nvfp4_status st = check_cache(cache)) return st;
+  if (!maps) return NVFP4_ERR_NULL;
+  if (!aligned(maps, 128)) return NVFP4_ERR_ALIGN;
+  KvMaps all[kMapPairs];
+  for (int64_t rows : {16, 32, 64, 65}) {  // one row count of each kind
+    const AttnShape s = attn_shape(cache->head_dim, cache->dtype == NVFP4_KV_E4M3, rows);
+    if (!encode_maps(&all[s.maps], cache, s)) return NVFP4_ERR_CUDA;
+  }
+  std::copy(all, all + kMapPairs, static_cast<KvMaps*>(maps));
+  return NVFP4_OK;
+}
 
 size_t paged_attention_workspace_bytes(int32_t n_tokens, int32_t n_seqs, int32_t max_new, int32_t n_heads,
                                        int32_t n_kv_heads, int32_t head_dim) {
@@ -91,8 +111,9 @@ nvfp4_status paged_attention(const nvfp4_kv_cache* cache, const nvfp4_batch* bat
   const bool fp8 = cache->dtype == NVFP4_KV_E4M3;
   const AttnShape s = attn_shape(dim, fp8, packed_rows(n_tokens, batch->max_new, n_heads, kv));
   KvMaps maps;
-  const int box = std::min(cache->page_size, s.box_keys);
-  if (!encode_pool_map(&maps.k, cache, cache->k, box, !s.chunk) || !encode_pool_map(&maps.v, cache, cache->v, box, !s.chunk))
+  if (cache->maps)
+    maps = static_cast<const KvMaps*>(cache->maps)[s.maps];
+  else if (!encode_maps(&maps, cache, s))
     return NVFP4_ERR_CUDA;
   if (dim == 64) return dispatch_attention<64>(p, maps, fp8, s, stream);
   if (dim == 128) return dispatch_attention<128>(p, maps, fp8, s, stream);

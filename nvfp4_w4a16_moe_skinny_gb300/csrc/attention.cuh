@@ -1158,12 +1158,14 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnJob p
 struct AttnShape {
   int rw, kw, tile_rows, box_keys;
   bool chunk;
+  int maps;  // which of a cache's pairs of tensor maps
 };
+constexpr int kMapPairs = 4;
 inline AttnShape attn_shape(int dim, bool fp8, int64_t rows) {
-  if (rows > 64) return {0, 0, dim == 256 ? 128 : 256, dim == 256 ? 64 : 128, true};
+  if (rows > 64) return {0, 0, dim == 256 ? 128 : 256, dim == 256 ? 64 : 128, true, 3};
   const int rw = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
   const int kw = 4 / rw;
-  return {rw, kw, 16 * rw, attn_slice(dim, fp8, kw) * kw, false};
+  return {rw, kw, 16 * rw, attn_slice(dim, fp8, kw) * kw, false, rw / 2};
 }
 
 template <int kDim>

@@ -33,7 +33,7 @@ inline nvfp4_status check_cache(const nvfp4_kv_cache* c) {
   const int size = c->dtype == NVFP4_KV_BF16 ? 2 : 1;
   if (!aligned(c->k, 16) || !aligned(c->v, 16) || (c->page_stride * size) % 16) return NVFP4_ERR_ALIGN;
   if (c->dtype == NVFP4_KV_BF16 && (c->k_scale || c->v_scale)) return NVFP4_ERR_LAYOUT;
-  if (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4)) return NVFP4_ERR_ALIGN;
+  if (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4) || !aligned(c->maps, 128)) return NVFP4_ERR_ALIGN;
   return NVFP4_OK;
 }
 

@@ -24,7 +24,7 @@ def so():
 def cache(**kw):
     from nvfp4_w4a16_moe_skinny_gb300.binding import CKVCache
     a = dict(k=P, v=P, k_scale=None, v_scale=None, page_stride=None, num_pages=8, page_size=16, n_kv_heads=2,
-             head_dim=64, dtype=0)
+             head_dim=64, dtype=0, maps=None)
     a.update(kw)
     if a["page_stride"] is None:
         a["page_stride"] = a["n_kv_heads"] * a["page_size"] * a["head_dim"]
@@ -87,11 +87,18 @@ def append_args(c, **kw):
     (dict(k=None), NULL), (dict(v=None), NULL), (dict(page_stride=2 * 16 * 64 - 8), SHAPE), (dict(num_pages=0), SHAPE),
     (dict(page_size=8), SHAPE), (dict(page_size=48), SHAPE), (dict(page_size=512), SHAPE), (dict(head_dim=96), SHAPE),
     (dict(n_kv_heads=0, page_stride=4096), SHAPE), (dict(dtype=2), LAYOUT), (dict(k_scale=P), LAYOUT),
-    (dict(k=P + 8), ALIGN), (dict(page_stride=2 * 16 * 64 + 4), ALIGN), (dict(dtype=1, v_scale=P + 2), ALIGN)])
+    (dict(k=P + 8), ALIGN), (dict(page_stride=2 * 16 * 64 + 4), ALIGN), (dict(dtype=1, v_scale=P + 2), ALIGN), (dict(maps=P + 64), ALIGN)])
 def test_caches_are_refused(so, kw, status):
     c = cache(**kw)
     assert so.kv_append(*append_args(c)) == status
     assert so.paged_attention(*attention_args(c)) == status
+    assert so.kv_cache_maps(ctypes.byref(c), P) == status
+
+
+def test_maps_refuse(so):
+    assert so.kv_cache_maps(None, P) == NULL
+    assert so.kv_cache_maps(ctypes.byref(cache()), None) == NULL
+    assert so.kv_cache_maps(ctypes.byref(cache()), P + 64) == ALIGN
 
 
 @pytest.mark.parametrize("kw,status", [
