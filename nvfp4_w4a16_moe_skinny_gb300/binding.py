@@ -255,7 +255,8 @@ class Library:
         self.lib = ctypes.CDLL(path)
         _sig(self.lib)
         self._ws = {}
-        self._attention_bytes = {}  # workspace sizes by the sizes of a call
+        self._attention_bytes = {}  # attention workspaces: their sizes by the sizes of a call,
+        self._attention_ws = {}     # and one for each (device, stream)
 
     # -------------------------------------------------------------- plumbing
     def _check(self, call, st):
@@ -562,20 +563,24 @@ class Library:
         sqrt(dim)): out, or (out, log-sum-exp fp32 [tokens, heads]) with with_lse."""
         dev = cache.device
         stride = _rows(q, "q", dev)
-        tokens, heads, dim = q.shape
-        _need(dim == cache.head_dim and batch.device == dev,
-              "q: [tokens, heads, head_dim] of the cache; the batch on its GPU")
+        shape = q.shape
+        tokens, heads, dim = shape
+        if dim != cache.head_dim or batch.device != dev:
+            raise ValueError("q: [tokens, heads, head_dim] of the cache; the batch on its GPU")
         if out is None:
-            out = torch.empty((tokens, heads, dim), dtype=torch.bfloat16, device=dev)
+            out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
             out_stride = heads * dim
         else:
-            _need(out.shape == q.shape, "out: the shape of q")
+            _need(out.shape == shape, "out: the shape of q")
             out_stride = _rows(out, "out", dev)
+        lse_ptr = None
         if lse is not None:
             _need(lse.shape == (tokens, heads) and lse.dtype is torch.float32 and lse.is_contiguous()
                   and lse.device == dev, "lse: contiguous fp32 [tokens, heads]")
+            lse_ptr = lse.data_ptr()
         elif with_lse:
             lse = torch.empty((tokens, heads), dtype=torch.float32, device=dev)
+            lse_ptr = lse.data_ptr()
         raw = _raw_stream(stream, dev)
         sizes = (tokens, batch.n_seqs, batch.max_new, heads, cache.n_kv_heads, dim)
         nbytes = self._attention_bytes.get(sizes)
@@ -583,27 +588,29 @@ class Library:
             if len(self._attention_bytes) > 4096:
                 self._attention_bytes.clear()
             nbytes = self._attention_bytes[sizes] = self.lib.paged_attention_workspace_bytes(*sizes)
-        ws = self._stream_workspace("attention", nbytes, dev, raw, stream)
+        ws, ws_ptr, ws_bytes = self._stream_workspace(nbytes, dev, raw, stream)
         st = self.lib.paged_attention(
             cache.ref, batch.ref, q.data_ptr(), stride, tokens, heads, dim ** -0.5 if scale is None else scale, softcap,
-            window, out.data_ptr(), out_stride, None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), raw)
+            window, out.data_ptr(), out_stride, lse_ptr, ws_ptr, ws_bytes, raw)
         if st:
             raise NVFP4Error("paged_attention", st)
         return (out, lse) if with_lse else out
 
-    def _stream_workspace(self, key, nbytes: int, device, raw: int, stream) -> torch.Tensor:
-        """A workspace of its own for each (call kind, device, stream): calls on different streams may overlap.  It is
-        allocated, and its counters cleared, on the stream that uses it, so that one that is outgrown is not reused under a
-        running call.  A captured call gets one from its graph's pool, which lives and dies with the graph and whose
-        counters are cleared at every replay."""
-        cur = self._ws.get((key, device, raw))
-        if cur is not None and cur.numel() >= nbytes and not torch.cuda.is_current_stream_capturing():
+    def _stream_workspace(self, nbytes: int, device, raw: int, stream):
+        """(tensor, address, bytes) of an attention workspace.  Each (device, stream) has its own: calls on different
+        streams may overlap.  It is allocated, and its counters cleared, on the stream that uses it, so that one that
+        is outgrown is not reused under a running call.  A captured call gets one from its graph's pool, which lives
+        and dies with the graph and whose counters are cleared at every replay."""
+        key = (device.index, raw)
+        cur = self._attention_ws.get(key)
+        if cur is not None and cur[2] >= nbytes and not torch.cuda.is_current_stream_capturing():
             return cur
         with torch.cuda.stream(torch.cuda.current_stream(device) if stream is None else stream):
-            cur = torch.empty(max(nbytes, COUNTER_BYTES), dtype=torch.uint8, device=device)
-            cur[:COUNTER_BYTES].zero_()
+            ws = torch.empty(max(nbytes, COUNTER_BYTES), dtype=torch.uint8, device=device)
+            ws[:COUNTER_BYTES].zero_()
+            cur = (ws, ws.data_ptr(), ws.numel())
             if not torch.cuda.is_current_stream_capturing():
-                self._ws[(key, device, raw)] = cur
+                self._attention_ws[key] = cur
         return cur
 
     # -------------------------------------------------------------- call plans
