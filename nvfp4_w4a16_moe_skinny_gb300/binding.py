@@ -228,6 +228,23 @@ def _raw_stream(stream, device) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
+def _empty(shape, dtype, device, stream):
+    """An output, allocated on the stream that writes it: memory that another stream's work may still use is not
+    written before that work is done."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _used_on(stream, *tensors):
+    """Tensors that a call on an explicitly given stream uses: their memory is not given away before that stream is
+    done with it."""
+    for x in tensors:
+        if x is not None:
+            x.record_stream(stream)
+
+
 def _rows(x: torch.Tensor, what: str, device) -> int:
     """Rows of heads [tokens, heads, dim]: the row stride in elements."""
     shape = x.shape
@@ -504,7 +521,7 @@ class Library:
         tokens, heads, dim = x.shape
         pairs = inv_freq.shape[0]
         if out is None:
-            out = torch.empty((tokens, heads, dim), dtype=torch.bfloat16, device=dev)
+            out = _empty((tokens, heads, dim), torch.bfloat16, dev, stream)
             out_stride = heads * dim
         else:
             _need(out.shape == x.shape, "out: the shape of x")
@@ -516,6 +533,8 @@ class Library:
             out_stride, _raw_stream(stream, dev))
         if st:
             raise NVFP4Error("rope_apply", st)
+        if stream is not None:
+            _used_on(stream, x, positions, inv_freq, out)
         return out
 
     def kv_append(self, cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
@@ -541,7 +560,7 @@ class Library:
             _need(q.shape == (tokens, q_heads, dim), "q: [tokens, heads, head_dim] of the cache")
             q_ptr, q_stride = q.data_ptr(), _rows(q, "q", dev)
             if q_out is None:
-                q_out = torch.empty((tokens, q_heads, dim), dtype=torch.bfloat16, device=dev)
+                q_out = _empty((tokens, q_heads, dim), torch.bfloat16, dev, stream)
                 out_stride = q_heads * dim
             else:
                 _need(q_out.shape == q.shape, "q_out: the shape of q")
@@ -554,6 +573,8 @@ class Library:
             _raw_stream(stream, dev))
         if st:
             raise NVFP4Error("kv_append", st)
+        if stream is not None:
+            _used_on(stream, k, v, slots, positions, inv_freq, q, q_out, cache.k, cache.v, cache.k_scale, cache.v_scale)
         return q_out
 
     def paged_attention(self, q: torch.Tensor, cache: KVCache, batch: Batch, scale: float = None, softcap: float = 0.0,
@@ -568,7 +589,7 @@ class Library:
         if dim != cache.head_dim or batch.device != dev:
             raise ValueError("q: [tokens, heads, head_dim] of the cache; the batch on its GPU")
         if out is None:
-            out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+            out = _empty(shape, torch.bfloat16, dev, stream)
             out_stride = heads * dim
         else:
             _need(out.shape == shape, "out: the shape of q")
@@ -579,7 +600,7 @@ class Library:
                   and lse.device == dev, "lse: contiguous fp32 [tokens, heads]")
             lse_ptr = lse.data_ptr()
         elif with_lse:
-            lse = torch.empty((tokens, heads), dtype=torch.float32, device=dev)
+            lse = _empty((tokens, heads), torch.float32, dev, stream)
             lse_ptr = lse.data_ptr()
         raw = _raw_stream(stream, dev)
         sizes = (tokens, batch.n_seqs, batch.max_new, heads, cache.n_kv_heads, dim)
@@ -594,6 +615,9 @@ class Library:
             window, out.data_ptr(), out_stride, lse_ptr, ws_ptr, ws_bytes, raw)
         if st:
             raise NVFP4Error("paged_attention", st)
+        if stream is not None:
+            _used_on(stream, q, out, lse, cache.k, cache.v, cache.k_scale, cache.v_scale, batch.cu_tokens, batch.kv_len,
+                     batch.page_table)
         return (out, lse) if with_lse else out
 
     def _stream_workspace(self, nbytes: int, device, raw: int, stream):

@@ -38,8 +38,8 @@ bool encode_maps(KvMaps* maps, const nvfp4_kv_cache* c, const AttnShape& s) {
 bool sizes_ok(int n_tokens, int n_seqs, int max_new, int n_heads, int n_kv_heads, int head_dim) {
   if (n_tokens < 0 || n_seqs < 0 || max_new < 0 || n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads) return false;
   if (head_dim != 64 && head_dim != 128 && head_dim != 256) return false;
-  // packed rows of a sequence are counted in 32 bits
-  return static_cast<int64_t>(n_tokens) * (n_heads / n_kv_heads) < (int64_t{1} << 31);
+  // positions and packed rows of a sequence are counted in 32 bits
+  return n_tokens < (1 << 30) && static_cast<int64_t>(n_tokens) * (n_heads / n_kv_heads) < (int64_t{1} << 31) - 1024;
 }
 
 int64_t packed_rows(int n_tokens, int max_new, int n_heads, int n_kv_heads) {
@@ -105,7 +105,8 @@ nvfp4_status paged_attention(const nvfp4_kv_cache* cache, const nvfp4_batch* bat
   p.q = q, p.q_stride = q_stride, p.out = out, p.out_stride = out_stride, p.lse = lse;
   p.v_pool = cache->v, p.page_stride = cache->page_stride;
   p.k_scale = cache->k_scale, p.v_scale = cache->v_scale;
-  p.scale = scale, p.softcap = softcap, p.window = window;
+  p.scale = scale, p.softcap = softcap;
+  p.window = window < (1 << 30) ? window : 0;  // (no sequence is that long: all keys)
   p.counters = static_cast<unsigned*>(ws);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kAttnCounterBytes);
   const bool fp8 = cache->dtype == NVFP4_KV_E4M3;

@@ -1108,8 +1108,8 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnJob p
     const long long before = ranges.start(c - 1) - w.item0;
     first = d > 0 && d < w.t.units && (before <= 0 || snapped(static_cast<int>(before), w.t.units, g) == 0);
   }
-  pdl_launch_dependents();
   pdl_wait();  // every block waits, so that this grid's end means that the split grid has ended
+  pdl_launch_dependents();
   if (!first) return;
   const auto [c0, c1] = holders_of(w, ranges, g);
   const float* ml = p.part + static_cast<int64_t>(2) * split_grid * tile_rows * kDim;

@@ -145,5 +145,6 @@ def test_workspace_sizes(so):
     assert f(16, 16, 1, 32, 8, 128) > 0
     assert f(16, 16, 1, 32, 8, 128) <= f(4096, 4, 2048, 32, 8, 128)
     for bad in ((-1, 1, 1, 4, 2, 64), (1, -1, 1, 4, 2, 64), (1, 1, -1, 4, 2, 64), (1, 1, 1, 5, 2, 64), (1, 1, 1, 4, 0, 64),
-                (1, 1, 1, 4, 2, 96), (1 << 30, 1, 1, 4, 2, 64)):
+                (1, 1, 1, 4, 2, 96), (1 << 30, 1, 1, 4, 2, 64), (1 << 30, 1, 1, 4, 4, 64),
+                ((1 << 30) - 100, 1, 1, 4, 2, 64)):
         assert f(*bad) == 0

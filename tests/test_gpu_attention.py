@@ -243,6 +243,35 @@ def test_bad_pages_read_as_zeros(lib, fp8, new):
         assert torch.equal(out, zeros[0]) and torch.equal(lse, zeros[1])
 
 
+def test_a_window_past_every_sequence_is_no_window(lib):
+    c = Case([(3, 200), (70, 100), (2, 0)], 4, 2, 128, 32, False, seed=18)
+    ref = run(lib, c)
+    for window in (200, 1 << 29, (1 << 30) + 5, 2 ** 31 - 1):
+        out, lse = run(lib, c, window=window)
+        assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1])
+
+
+def test_tensors_given_away_while_another_stream_uses_them(lib):
+    """A call on a stream of its own, whose inputs are dropped and whose memory is asked for again at once: the call
+    still reads what it was given."""
+    c = Case([(1, 4000), (40, 900)], 8, 2, 128, 64, False, seed=31)
+    ref, _ = run(lib, c)
+    cache, batch = c.cache(), c.batch()
+    s = torch.cuda.Stream()
+    big = torch.empty(1 << 28, dtype=torch.uint8, device=dev())
+    for _ in range(10):
+        q = c.q.clone()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            big.fill_(1)                       # keeps the call waiting
+        out = lib.paged_attention(q, cache, batch, stream=s)
+        del q
+        junk = [torch.full_like(c.q, float("nan")) for _ in range(4)]
+        s.synchronize()
+        assert torch.equal(out, ref)
+        del junk
+
+
 def test_window_skips_freed_pages(lib):
     """Table entries wholly before the window may hold anything."""
     c = Case([(3, 500)], 4, 2, 128, 16, False, seed=8)
