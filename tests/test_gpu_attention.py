@@ -148,6 +148,63 @@ def test_long_and_ragged_split(lib, fp8):
     c.check(*run(lib, c))
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("new,heads,kv,dim,context", [
+    (1, 16, 1, 128, 60000), (1, 3, 1, 64, 90000), (2, 16, 1, 256, 21000),       # few rows: over all CTAs of the split kernel
+    (100, 2, 1, 128, 41000), (200, 1, 1, 64, 45000), (70, 2, 1, 256, 22000),    # a chunk: joined in groups, three levels
+    (130, 2, 2, 128, 9000), (300, 4, 2, 64, 5000)])
+def test_one_item_over_many_ctas(lib, fp8, new, heads, kv, dim, context):
+    c = Case([(new, new + context)], heads, kv, dim, 64, fp8, seed=new + dim)
+    out, lse = run(lib, c)
+    keep = sorted({0, 1, new // 2, new - 1} & set(range(new)))     # the oracle walks these tokens only
+    q = c.q[keep].double().cpu().numpy()
+    k, v = c.keys(0, 0), c.keys(0, 1)
+    for i, tok in enumerate(keep):
+        want, wlse, spread, size = OA.attention(q[i:i + 1], k, v, context + tok, dim ** -0.5)
+        n = context + new
+        delta = dim * 2.0 ** -22 * size
+        bound = 2.0 ** -8 * np.abs(want) + spread * (2.0 ** (-11 if fp8 else -8) + 2.0 * delta[..., None] + 2.0 ** -20 + n * 2.0 ** -22)
+        assert np.all(np.abs(out[tok:tok + 1].double().cpu().numpy() - want) <= bound), tok
+        err = np.abs(lse[tok].double().cpu().numpy() - wlse[0])
+        assert np.all(err <= delta[0] + 2.0 ** -20 + n * 2.0 ** -22 + 2.0 ** -22 * np.abs(wlse[0]))
+    again = run(lib, c)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("growth", [3.0, 40.0, -40.0, 600.0])
+@pytest.mark.parametrize("lens,heads,kv,dim", [([(1, 700)], 4, 2, 128), ([(20, 700)], 2, 1, 64), ([(150, 900)], 2, 1, 128),
+                                               ([(90, 700)], 4, 2, 64), ([(140, 600)], 1, 1, 256)])
+def test_maxima_that_grow_and_fall(lib, fp8, growth, lens, heads, kv, dim):
+    """Keys whose logits climb (or fall) over the sequence by hundreds: the running references move, far and often."""
+    c = Case(lens, heads, kv, dim, 32, fp8, seed=77)
+    length = lens[0][1]
+    c.q = c.q * 0.1
+    c.q[..., 0] = 8.0
+    ramp = torch.linspace(0, 1, length, device=dev()) if growth > 0 else torch.linspace(1, 0, length, device=dev())
+    ramp = ramp * abs(growth) * math.sqrt(dim) / 8.0               # logits 0 .. |growth| in the first value's direction
+    raw = c.pools.float()
+    for i in range(-(-length // 32)):
+        part = ramp[i * 32:(i + 1) * 32]
+        for h in range(kv):
+            s = 1.0 if not fp8 else float(c.scales[0][h])
+            raw[0, int(c.table[0, i]), h, :part.numel(), 0] = (part / s).clamp(max=440.0 if fp8 else 1e9)
+    c.pools = raw.to(c.pools.dtype)
+    out, lse = run(lib, c)
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    c.check(out, lse)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("window", [0, 1, 100, 257])
+@pytest.mark.parametrize("lens,heads,kv,dim,page", [([(300, 300), (1, 90), (257, 800)], 2, 1, 128, 16),
+                                                    ([(129, 640), (5, 5)], 7, 1, 128, 128), ([(400, 1000)], 1, 1, 64, 256),
+                                                    ([(130, 500), (3, 77)], 3, 1, 256, 16)])
+def test_large_chunks(lib, fp8, window, lens, heads, kv, dim, page):
+    c = Case(lens, heads, kv, dim, page, fp8, seed=window + dim)
+    c.check(*run(lib, c, window=window), window=window)
+
+
 @pytest.mark.parametrize("n_seqs", [151, 300, 700])
 def test_many_sequences(lib, n_seqs):
     rng = np.random.default_rng(n_seqs)
