@@ -85,8 +85,9 @@ struct KvMaps {
 // finishing an item costs, counted in units (the ranges are balanced with it).
 // `snap`: a range boundary that falls this close to an item's end moves there, so that no
 // item is split for a few units.
+// `least`: units that a range holds at least, as far as there are any.
 struct Tiling {
-  int rows, keys, over, snap;
+  int rows, keys, over, snap, least;
 };
 
 // Quotient of x < 2^31 by the divisor that `d` was made for (fast_div): a multiply by the
@@ -142,9 +143,9 @@ __device__ __forceinline__ long long tile_units(const AttnJob& p, const Sequence
 struct Ranges {
   long long total, each;
   int grid, more;  // ranges in use; the first `more` of them hold each + 1 units
-  __device__ __forceinline__ void set(long long all, int ctas) {
+  __device__ __forceinline__ void set(long long all, int ctas, int least) {
     total = all;
-    grid = static_cast<int>(min(static_cast<long long>(ctas), all));
+    grid = all >= static_cast<long long>(ctas) * least ? ctas : (static_cast<int>(all) + least - 1) / least;
     if (grid < 1) {
       each = more = 0;
     } else if (all >> 31) {
@@ -209,7 +210,7 @@ __device__ __forceinline__ void find_range(const AttnJob& p, const Tiling& g, in
         const long long v = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += v;
       }
-      ranges->set(__shfl_sync(0xffffffffu, incl, 31), ctas);
+      ranges->set(__shfl_sync(0xffffffffu, incl, 31), ctas, g.least);
       const long long u = ranges->start(c);
       const unsigned here = __ballot_sync(0xffffffffu, u >= incl - mine && u < incl);
       found->seq = here ? __ffs(here) - 1 : 0;
@@ -275,7 +276,7 @@ __device__ __forceinline__ void find_range(const AttnJob& p, const Tiling& g, in
       __syncthreads();
     }
     if (pass == 0) {
-      ranges->set(base, ctas);
+      ranges->set(base, ctas, g.least);
       if (c >= ranges->grid) return;
     }
   }
@@ -484,7 +485,7 @@ struct AttnTile {
   static constexpr int kKeys = kSlice * kKW;                         // keys of a unit
   static constexpr int kConsumers = kRW * kKW;
   static constexpr int kThreadsAll = (kConsumers + 1) * 32;
-  static constexpr int kOver = 3, kSnap = 2;                         // an item's own cost, in units (Tiling)
+  static constexpr int kOver = 3, kSnap = 2, kLeast = 1;             // costs in units (Tiling)
   static constexpr int kEl = kFp8 ? 1 : 2;
   static constexpr int kRowB = kDim * kEl < 128 ? kDim * kEl : 128;  // bytes of a row of a block
   static constexpr int kSub = kDim * kEl / kRowB;                    // blocks across a head
@@ -619,7 +620,7 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, a
   pdl_launch_dependents();
   __syncthreads();
 
-  constexpr Tiling kTiling{T::kRows, T::kKeys, T::kOver, T::kSnap};
+  constexpr Tiling kTiling{T::kRows, T::kKeys, T::kOver, T::kSnap, T::kLeast};
   Found f;
   Ranges ranges;
   find_range<T::kThreadsAll>(p, kTiling, gridDim.x, blockIdx.x, &ranges, &f, scratch,
@@ -1186,7 +1187,7 @@ nvfp4_status launch_attn_split(const AttnJob& p, const KvMaps& maps, cudaStream_
   if (launch_pdl(attn_split_kernel<kDim, kFp8, kRW, kKW>, dim3(kAttnGrid * T::kCtas), dim3(T::kThreadsAll), T::kSmem,
                  stream, p, maps) != cudaSuccess)
     return NVFP4_ERR_CUDA;
-  return launch_attn_join<kDim>(p, Tiling{T::kRows, T::kKeys, T::kOver, T::kSnap}, kAttnGrid * T::kCtas, stream);
+  return launch_attn_join<kDim>(p, Tiling{T::kRows, T::kKeys, T::kOver, T::kSnap, T::kLeast}, kAttnGrid * T::kCtas, stream);
 }
 
 // The split and join grids for heads of kDim values (attention_d*.cu).

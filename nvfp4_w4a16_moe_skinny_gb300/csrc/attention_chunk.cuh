@@ -47,7 +47,7 @@ struct ChunkTile {
   static constexpr int kRows = 128 * kGroups;
   static constexpr int kKeys = kDim == 256 ? 64 : 128;
   static constexpr int kSBuf = kDim == 256 ? 2 : 1;        // S buffers per group
-  static constexpr int kOver = 4, kSnap = 4;               // an item's own cost, in units (Tiling)
+  static constexpr int kOver = 4, kSnap = 4, kLeast = kDim == 256 ? 8 : 4;  // in units (Tiling)
   // warps that make tiles fit: two beside the copies and the products, or (E4M3 and 128 values:
   // 256 conversions a row and tile; 1,404 us with two warps, 1,162 with four, for 2,048 tokens over
   // 32,768 keys) a warpgroup of their own; the softmax warpgroups follow
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
   tc_fence_after();
   const uint32_t tmem = uniform(*static_cast<volatile uint32_t*>(&bars->tmem));
 
-  constexpr Tiling kTiling{T::kRows, T::kKeys, T::kOver, T::kSnap};
+  constexpr Tiling kTiling{T::kRows, T::kKeys, T::kOver, T::kSnap, T::kLeast};
   Found f;
   Ranges ranges;
   find_range<T::kThreadsAll>(p, kTiling, gridDim.x, blockIdx.x, &ranges, &f, &bars->scratch,
