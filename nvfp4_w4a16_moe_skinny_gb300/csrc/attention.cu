@@ -60,7 +60,7 @@ nvfp4_status kv_cache_maps(const nvfp4_kv_cache* cache, void* maps) {
   if (!aligned(maps, 128)) return NVFP4_ERR_ALIGN;
   KvMaps all[kMapPairs];
   for (int64_t rows : {16, 32, 64, 65}) {  // one row count of each kind
-    const AttnShape s = attn_shape(cache->head_dim, cache->dtype == NVFP4_KV_E4M3, rows);
+    const AttnShape s = attn_shape(cache->head_dim, cache->dtype == NVFP4_KV_E4M3, rows, 1);
     if (!encode_maps(&all[s.maps], cache, s)) return NVFP4_ERR_CUDA;
   }
   std::copy(all, all + kMapPairs, static_cast<KvMaps*>(maps));
@@ -70,10 +70,11 @@ nvfp4_status kv_cache_maps(const nvfp4_kv_cache* cache, void* maps) {
 size_t paged_attention_workspace_bytes(int32_t n_tokens, int32_t n_seqs, int32_t max_new, int32_t n_heads,
                                        int32_t n_kv_heads, int32_t head_dim) {
   if (!sizes_ok(n_tokens, n_seqs, max_new, n_heads, n_kv_heads, head_dim)) return 0;
-  const AttnShape s = attn_shape(head_dim, false, packed_rows(n_tokens, max_new, n_heads, n_kv_heads));
-  const int grid = kAttnGrid * (s.chunk ? 1 : attn_ctas(head_dim));
+  const AttnShape s = attn_shape(head_dim, false, packed_rows(n_tokens, max_new, n_heads, n_kv_heads),
+                                 static_cast<int64_t>(n_seqs) * n_kv_heads);
+  const int grid = kAttnGrid * (s.chunk ? 1 : attn_ctas(head_dim, false, s.rw));
   const size_t share = static_cast<size_t>(s.tile_rows) * (head_dim + 2);  // sums of a row tile, references and sums of weights
-  return kAttnCounterBytes + 2 * grid * share * sizeof(float);
+  return kAttnCounterBytes + kAttnSplitBytes + 2 * grid * share * sizeof(float);
 }
 
 nvfp4_status paged_attention(const nvfp4_kv_cache* cache, const nvfp4_batch* batch, const uint16_t* q,
@@ -108,9 +109,11 @@ nvfp4_status paged_attention(const nvfp4_kv_cache* cache, const nvfp4_batch* bat
   p.scale = scale, p.softcap = softcap;
   p.window = window < (1 << 30) ? window : 0;  // (no sequence is that long: all keys)
   p.counters = static_cast<unsigned*>(ws);
-  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kAttnCounterBytes);
+  p.split = reinterpret_cast<int4*>(static_cast<uint8_t*>(ws) + kAttnCounterBytes);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kAttnCounterBytes + kAttnSplitBytes);
   const bool fp8 = cache->dtype == NVFP4_KV_E4M3;
-  const AttnShape s = attn_shape(dim, fp8, packed_rows(n_tokens, batch->max_new, n_heads, kv));
+  const AttnShape s = attn_shape(dim, fp8, packed_rows(n_tokens, batch->max_new, n_heads, kv),
+                                 static_cast<int64_t>(batch->n_seqs) * kv);
   KvMaps maps;
   if (cache->maps)
     maps = static_cast<const KvMaps*>(cache->maps)[s.maps];

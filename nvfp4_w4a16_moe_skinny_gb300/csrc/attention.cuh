@@ -36,6 +36,7 @@
 namespace nvfp4 {
 
 constexpr size_t kAttnCounterBytes = 4096;  // at the start of the workspace
+constexpr size_t kAttnSplitBytes = 8192;    // after them: a split_item of every CTA of the split kernel
 constexpr int kAttnGrid = 152;  // SMs that the split is made for; fixed, so that workspace sizes are host-computable
 
 // Division by a number that a launch knows: x / g = umulhi(x, mul) >> shift for
@@ -73,6 +74,7 @@ struct AttnJob {
   int window;
   unsigned* counters;  // arrivals at the join of each split item, by the range that holds its start
   float* part;         // shares: unnormalised sums, reference maxima and sums of weights of a row tile, two per CTA
+  int4* split;         // the split kernel's split items, by the range that holds their start (split_item)
 };
 
 struct KvMaps {
@@ -394,6 +396,14 @@ __device__ __forceinline__ Holders holders_of(const Walk& w, const Ranges& r, co
   return h;
 }
 
+// What the join needs of a split item, written by the CTA whose range holds its start: the
+// last range that holds a share and the rows (9 and 7 bits), the kv head, the first packed
+// row, the sequence's first token.
+__device__ __forceinline__ int4 split_item(const Walk& w, int c1) {
+  static_assert(2 * kAttnGrid <= 512, "nine bits");
+  return make_int4(c1 | w.t.rows << 9, w.h, w.t.row0, w.s.tok0);
+}
+
 // ------------------------------------------------------------------ MMA helpers
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -469,7 +479,9 @@ __device__ __forceinline__ uint32_t nonfinite_mask(uint32_t v) {
 // ------------------------------------------------------------------ tile geometry
 
 // CTAs of the split kernel on one SM.
-__host__ __device__ constexpr int attn_ctas(int dim) { return dim == 256 ? 1 : 2; }
+__host__ __device__ constexpr int attn_ctas(int dim, bool fp8, int rw) {
+  return dim == 256 || (dim == 128 && fp8 && rw == 4) ? 1 : 2;
+}
 
 // Keys of one warp's step: few enough that three units fit in a CTA's shared memory and the
 // scores in few registers.
@@ -481,6 +493,7 @@ __host__ __device__ constexpr int attn_slice(int dim, bool fp8, int kw) {
 template <int kDim, bool kFp8, int kRW, int kKW>
 struct AttnTile {
   static constexpr int kRows = 16 * kRW;
+  static constexpr int kCtas = attn_ctas(kDim, kFp8, kRW);
   static constexpr int kSlice = attn_slice(kDim, kFp8, kKW);              // keys of a warp's step
   static constexpr int kKeys = kSlice * kKW;                         // keys of a unit
   static constexpr int kConsumers = kRW * kKW;
@@ -492,7 +505,6 @@ struct AttnTile {
   static constexpr uint32_t kSwz = kRowB == 128 ? 0x70 : 0x30;
   static constexpr int kTileB = kKeys * kDim * kEl;                  // K or V of a unit: page pieces of [kSub][rows][kRowB]
   static constexpr int kStageB = 2 * kTileB;
-  static constexpr int kCtas = attn_ctas(kDim);
   static constexpr int kQB = kRows * kDim * 2;                       // Q: [kDim / 64][kRows][128 bytes]
   // a quarter (kKW = 4) or half of the columns of each warp's sums, its reference and sum
   static constexpr int kJoinB = kKW > 1 ? kConsumers * 32 * (kDim / 2 / kKW + 4) * 4 : 0;
@@ -595,7 +607,7 @@ __device__ __forceinline__ int piece_page(const AttnJob& p, const int32_t* table
 // ------------------------------------------------------------------ the split kernel
 
 template <int kDim, bool kFp8, int kRW, int kKW>
-__global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, attn_ctas(kDim))
+__global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, attn_ctas(kDim, kFp8, kRW))
     attn_split_kernel(const AttnJob p, const __grid_constant__ KvMaps maps) {
   using T = AttnTile<kDim, kFp8, kRW, kKW>;
   extern __shared__ uint8_t smem_raw[];
@@ -628,6 +640,7 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, a
   // (the list lies where the first tiles will: its last reads come before the copies)
   fence_proxy_async_smem();
   __syncthreads();
+  if (threadIdx.x == T::kConsumers * 32) p.split[blockIdx.x] = make_int4(0, 0, 0, 0);  // none, until this thread finds one
   if (static_cast<int>(blockIdx.x) >= ranges.grid) return;
   const long long u0 = ranges.start(blockIdx.x), u1 = ranges.start(blockIdx.x + 1);
   Walk w;
@@ -648,6 +661,8 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, a
       const Share pc = share_at(w, u, u0, u1, blockIdx.x, kTiling);
       u = pc.end;
       const int n = static_cast<int>(uniform(pc.n)), head = static_cast<int>(uniform(w.h));
+      if (n > 0 && !pc.whole && pc.first == w.t.tile0 && lane == 0)
+        p.split[blockIdx.x] = split_item(w, holders_of(w, ranges, kTiling).c1);
       const int32_t* table = p.table + static_cast<int64_t>(w.b) * p.max_pages;
       // lane i holds the page of piece i of the unit, looked up a unit ahead
       int page = lane < pieces && n > 0 ? piece_page(p, table, pc.first * pieces + lane, piece_log2, w.t) : -1;
@@ -1079,104 +1094,150 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, a
 
 // ------------------------------------------------------------------ the join
 
-constexpr int kJoinThreads = 128;
+constexpr int kJoinRows = 2, kJoinSlices = 4;  // rows of a block's pass, warps on each
+constexpr int kJoinThreads = 32 * kJoinRows * kJoinSlices, kJoinGrid = 4 * kAttnGrid;
 
-// Block (c, y): if range boundary c is the first one inside an item, joins that
-// item's shares in range order, a warp a row.  (The chunk kernel joins its few and large
-// shares itself; here many small ones would keep one CTA busy for long, while a second
-// grid spreads them over the chip: verify blocks of 30 rows of 256 values in a window of
-// 1,024 keys take 15.9 us this way and 23.1 us with the join in the split kernel.)
+// Joins the shares of the split kernel's split items.  Every block compacts the list of split
+// items, and their rows, kJoinRows at a time, are dealt to the grid.
 template <int kDim>
-__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnJob p, int split_grid, const Tiling g) {
-  __shared__ RangeScratch scratch;
-  __shared__ longlong2 list[kJoinThreads];
+__global__ void __launch_bounds__(kJoinThreads, 4) attn_join_kernel(const AttnJob p, int split_grid, int tile_rows) {
+  __shared__ int warp_sum[(2 * kAttnGrid + kJoinThreads - 1) / kJoinThreads * kJoinThreads / 32];
+  __shared__ int4 list[kAttnGrid * 2];
+  __shared__ float sums[kJoinRows][kJoinSlices][kDim];
+  __shared__ float2 refs[kJoinRows][kJoinSlices];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int tile_rows = g.rows;
-  Found f;
-  Ranges ranges;
-  // lengths are complete before the split grid starts: only its pieces are waited for
-  const int c = blockIdx.x + 1;
-  find_range<kJoinThreads>(p, g, split_grid, c, &ranges, &f, &scratch, list);
-  Walk w;
-  bool first = false;
-  if (c < ranges.grid) {
-    w.b = f.seq, w.item0 = f.before;
-    walk_seq(p, w, g);
-    const long long u = ranges.start(c);
-    walk_to(p, w, u, g);
-    // a boundary among the item's tiles, and the first one
-    const int d = snapped(static_cast<int>(u - w.item0), w.t.units, g);
-    const long long before = ranges.start(c - 1) - w.item0;
-    first = d > 0 && d < w.t.units && (before <= 0 || snapped(static_cast<int>(before), w.t.units, g) == 0);
-  }
-  pdl_wait();  // every block waits, so that this grid's end means that the split grid has ended
+  pdl_wait();
   pdl_launch_dependents();
-  if (!first) return;
-  const auto [c0, c1] = holders_of(w, ranges, g);
-  const float* ml = p.part + static_cast<int64_t>(2) * split_grid * tile_rows * kDim;
-  constexpr int kPer = kDim / 32;
-  for (int r = blockIdx.y * 4 + warp; r < w.t.rows; r += gridDim.y * 4) {
-    float m = -INFINITY;
-    for (int i = c0 + lane; i <= c1; i += 32) {
-      const int slot = 2 * i + (i == c0 ? 1 : 0);
-      m = fmaxf(m, ml[(static_cast<int64_t>(slot) * tile_rows + r) * 2]);
-    }
+  constexpr int kSpan = (2 * kAttnGrid + kJoinThreads - 1) / kJoinThreads, kWarps = kJoinThreads / 32;
+  int4 mine[kSpan];
+  unsigned all[kSpan];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float acc[kPer];
+  for (int b = 0; b < kSpan; ++b) {
+    const int c = b * kJoinThreads + threadIdx.x;
+    mine[b] = c < split_grid ? __ldcg(p.split + c) : make_int4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int b = 0; b < kSpan; ++b) {
+    all[b] = __ballot_sync(0xffffffffu, mine[b].x != 0);
+    if (lane == 0) warp_sum[b * kWarps + warp] = __popc(all[b]);
+  }
+  __syncthreads();
+  int items = 0;
+#pragma unroll
+  for (int b = 0; b < kSpan; ++b) {
+    int at = __popc(all[b] & ((1u << lane) - 1));
+#pragma unroll
+    for (int x = 0; x < kWarps; ++x) {
+      if (x == warp) at += items;
+      items += warp_sum[b * kWarps + x];
+    }
+    if (mine[b].x != 0) list[at] = make_int4(mine[b].x | (b * kJoinThreads + threadIdx.x) << 16, mine[b].y, mine[b].z, mine[b].w);
+  }
+  __syncthreads();
+  const float* ml = p.part + static_cast<int64_t>(2) * split_grid * tile_rows * kDim;
+  // a row's shares are dealt to kJoinSlices warps, each with kBatch of them in flight (one item
+  // of 32,000 keys over the whole grid has 76 shares)
+  constexpr int kPer = kDim / 32, kBatch = kDim == 256 ? 4 : 8;
+  const int slice = warp % kJoinSlices, sub = warp / kJoinSlices;
+  for (int x = blockIdx.x; x < items * (tile_rows / kJoinRows); x += gridDim.x) {
+    const int r0 = x / items * kJoinRows;
+    const int4 it = list[x - x / items * items];
+    const int c0 = it.x >> 16, c1 = it.x & 0x1ff, rows = it.x >> 9 & 0x7f;
+    if (r0 >= rows) continue;
+    const int r = min(r0 + sub, rows - 1);
+    float m = -INFINITY, l = 0.f, acc[kPer];
 #pragma unroll
     for (int j = 0; j < kPer; ++j) acc[j] = 0.f;
-    float l = 0.f;
-#pragma unroll 4
-    for (int i = c0; i <= c1; ++i) {
-      const int slot = 2 * i + (i == c0 ? 1 : 0);
-      const int64_t row = static_cast<int64_t>(slot) * tile_rows + r;
-      const float2 v = *reinterpret_cast<const float2*>(ml + row * 2);
-      const float a = m == -INFINITY ? 1.0f : exp2_approx(v.x - m);
-      l += a * v.y;
-      const float* o = p.part + row * kDim + lane * kPer;
+    for (int i0 = c0 + slice; i0 <= c1; i0 += kJoinSlices * kBatch) {
+      float2 v[kBatch];
+      float2 x[kBatch][kPer / 2];
 #pragma unroll
-      for (int j = 0; j < kPer; j += 2) {
-        const float2 x = *reinterpret_cast<const float2*>(o + j);
-        acc[j] += a * x.x, acc[j + 1] += a * x.y;
+      for (int k = 0; k < kBatch; ++k) {
+        const int i = i0 + k * kJoinSlices <= c1 ? i0 + k * kJoinSlices : i0;
+        const int64_t row = static_cast<int64_t>(2 * i + (i == c0 ? 1 : 0)) * tile_rows + r;
+        v[k] = *reinterpret_cast<const float2*>(ml + row * 2);
+        const float2* o = reinterpret_cast<const float2*>(p.part + row * kDim + lane * kPer);
+#pragma unroll
+        for (int j = 0; j < kPer / 2; ++j) x[k][j] = o[j];
       }
-    }
-    const int rr = w.t.row0 + r, tok = div_by(p.by_group, rr), head = w.h * p.group + rr - tok * p.group;
-    const int64_t row = w.s.tok0 + tok;
-    const float inv = l == 0.f ? 0.f : (p.v_scale ? __ldg(p.v_scale + w.h) : 1.0f) / l;
-    uint32_t* o = reinterpret_cast<uint32_t*>(p.out + row * p.out_stride + static_cast<int64_t>(head) * kDim) + lane * (kPer / 2);
+      float next = m;
 #pragma unroll
-    for (int j = 0; j < kPer; j += 2) o[j / 2] = f32x2_to_bf16x2(acc[j] * inv, acc[j + 1] * inv);
-    if (p.lse && lane == 0) p.lse[row * p.n_heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+      for (int k = 0; k < kBatch; ++k) next = fmaxf(next, v[k].x);
+      const float a0 = next == -INFINITY ? 1.0f : exp2_approx(m - next);
+      l *= a0;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) acc[j] *= a0;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        if (i0 + k * kJoinSlices > c1) break;
+        const float a = next == -INFINITY ? 1.0f : exp2_approx(v[k].x - next);
+        l += a * v[k].y;
+#pragma unroll
+        for (int j = 0; j < kPer; j += 2) acc[j] += a * x[k][j / 2].x, acc[j + 1] += a * x[k][j / 2].y;
+      }
+      m = next;
+    }
+#pragma unroll
+    for (int j = 0; j < kPer; j += 2) *reinterpret_cast<float2*>(&sums[sub][slice][lane * kPer + j]) = make_float2(acc[j], acc[j + 1]);
+    if (lane == 0) refs[sub][slice] = make_float2(m, l);
+    __syncthreads();
+    if (slice == 0 && r0 + sub < rows) {
+#pragma unroll
+      for (int k = 1; k < kJoinSlices; ++k) m = fmaxf(m, refs[sub][k].x);
+      l = 0.f;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) acc[j] = 0.f;
+#pragma unroll
+      for (int k = 0; k < kJoinSlices; ++k) {
+        const float a = m == -INFINITY ? 1.0f : exp2_approx(refs[sub][k].x - m);
+        l += a * refs[sub][k].y;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) acc[j] += a * sums[sub][k][lane * kPer + j];
+      }
+      const int rr = it.z + r, tok = div_by(p.by_group, rr), head = it.y * p.group + rr - tok * p.group;
+      const int64_t row = it.w + tok;
+      const float inv = l == 0.f ? 0.f : (p.v_scale ? __ldg(p.v_scale + it.y) : 1.0f) / l;
+      uint32_t* o = reinterpret_cast<uint32_t*>(p.out + row * p.out_stride + static_cast<int64_t>(head) * kDim) + lane * (kPer / 2);
+#pragma unroll
+      for (int j = 0; j < kPer; j += 2) o[j / 2] = f32x2_to_bf16x2(acc[j] * inv, acc[j + 1] * inv);
+      if (p.lse && lane == 0) p.lse[row * p.n_heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    }
+    __syncthreads();
   }
 }
 
 // ------------------------------------------------------------------ launch
 
-// Which kernel and tile serve up to `rows` packed rows per sequence and kv head.  16 rows
-// leave four key slices to four warps, 64 rows share one slice among four; more go
-// to the tcgen05 kernel (attention_chunk.cuh).
+// Which kernel and tile serve up to `rows` packed rows per sequence and kv head, in `items`
+// pairs of those.
+// Rows above 64 go to the tcgen05 kernel (attention_chunk.cuh), and rows above 32 where the
+// batch alone fills the chip: 16 sequences of 8,000 keys and 4 kv heads with 64 rows of 128
+// bf16 values take 67 us there and 76 here (256 values: 107 and 134), 32 of 500 keys 16 and 33,
+// but one of 32,000 keys 45 and 33 us, two of 2,000 24 and 17: its tiles of 256 rows start and
+// join slowly.  (Eight sequences are even: 18 and 22 us, 256 values 29 and 25, at 1,000 keys.)
+// Up to 32 rows this kernel is ahead in every batch measured.
+// A tile of 16 rows leaves four key slices to four warps, 32 rows two, 64 rows share one: the smallest
+// that holds the rows.  16 sequences of 8,000 keys, 8 rows, 128 values: 51.7, 56.1 and 69.4 us
+// with tiles of 16, 32 and 64 rows (E4M3 35.7, 44.4, 92.6); 32 rows: 62.6 and 72.9 us with the latter two.
 struct AttnShape {
   int rw, kw, tile_rows, box_keys;
   bool chunk;
   int maps;  // which of a cache's pairs of tensor maps
 };
 constexpr int kMapPairs = 4;
-inline AttnShape attn_shape(int dim, bool fp8, int64_t rows) {
-  if (rows > 64) return {0, 0, dim == 256 ? 128 : 256, dim == 256 ? 64 : 128, true, 3};
+inline AttnShape attn_shape(int dim, bool fp8, int64_t rows, int64_t items) {
+  if (rows > 64 || (rows > 32 && items >= 48)) return {0, 0, dim == 256 ? 128 : 256, dim == 256 ? 64 : 128, true, 3};
   const int rw = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
   const int kw = 4 / rw;
   return {rw, kw, 16 * rw, attn_slice(dim, fp8, kw) * kw, false, rw / 2};
 }
 
 template <int kDim>
-nvfp4_status launch_attn_join(const AttnJob& p, const Tiling& g, int grid, cudaStream_t stream) {
+nvfp4_status launch_attn_join(const AttnJob& p, int tile_rows, int keys, int grid, cudaStream_t stream) {
   // one unit an item: nothing can be split
-  if ((static_cast<int64_t>(p.max_pages) << p.page_log2) > g.keys) {
-    const int rows = g.rows / 4 < 16 ? g.rows / 4 : 16;
-    if (launch_pdl(attn_join_kernel<kDim>, dim3(grid - 1, rows), dim3(kJoinThreads), 0, stream, p, grid, g) != cudaSuccess)
-      return NVFP4_ERR_CUDA;
-  }
+  if ((static_cast<int64_t>(p.max_pages) << p.page_log2) > keys &&
+      launch_pdl(attn_join_kernel<kDim>, dim3(kJoinGrid), dim3(kJoinThreads), 0, stream, p, grid, tile_rows) != cudaSuccess)
+    return NVFP4_ERR_CUDA;
   return launched();
 }
 
@@ -1187,7 +1248,7 @@ nvfp4_status launch_attn_split(const AttnJob& p, const KvMaps& maps, cudaStream_
   if (launch_pdl(attn_split_kernel<kDim, kFp8, kRW, kKW>, dim3(kAttnGrid * T::kCtas), dim3(T::kThreadsAll), T::kSmem,
                  stream, p, maps) != cudaSuccess)
     return NVFP4_ERR_CUDA;
-  return launch_attn_join<kDim>(p, Tiling{T::kRows, T::kKeys, T::kOver, T::kSnap, T::kLeast}, kAttnGrid * T::kCtas, stream);
+  return launch_attn_join<kDim>(p, T::kRows, T::kKeys, kAttnGrid * T::kCtas, stream);
 }
 
 // The split and join grids for heads of kDim values (attention_d*.cu).

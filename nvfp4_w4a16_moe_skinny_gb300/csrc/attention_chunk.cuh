@@ -47,7 +47,7 @@ struct ChunkTile {
   static constexpr int kRows = 128 * kGroups;
   static constexpr int kKeys = kDim == 256 ? 64 : 128;
   static constexpr int kSBuf = kDim == 256 ? 2 : 1;        // S buffers per group
-  static constexpr int kOver = 4, kSnap = 4, kLeast = kDim == 256 ? 8 : 4;  // in units (Tiling)
+  static constexpr int kOver = 4, kSnap = kFp8 && kDim == 128 ? 1 : 4, kLeast = kDim == 256 ? 8 : 4;  // in units (Tiling)
   // warps that make tiles fit: two beside the copies and the products, or (E4M3 and 128 values:
   // 256 conversions a row and tile; 1,404 us with two warps, 1,162 with four, for 2,048 tokens over
   // 32,768 keys) a warpgroup of their own; the softmax warpgroups follow

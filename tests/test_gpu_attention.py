@@ -172,6 +172,25 @@ def test_one_item_over_many_ctas(lib, fp8, new, heads, kv, dim, context):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("new,heads,kv,dim,context", [
+    (4, 16, 1, 128, 30000), (8, 4, 1, 64, 41000), (3, 12, 1, 256, 12000), (1, 33, 1, 128, 9000), (17, 2, 1, 64, 20000)])
+def test_tiles_of_32_and_64_rows_over_many_ctas(lib, fp8, new, heads, kv, dim, context):
+    """Every row of one item whose shares lie in every CTA."""
+    c = Case([(new, new + context)], heads, kv, dim, 32, fp8, seed=new * dim)
+    c.check(*run(lib, c))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n_seqs,new,heads,kv,dim", [(24, 17, 4, 2, 128), (47, 33, 1, 1, 64), (48, 33, 1, 1, 64), (12, 5, 32, 4, 256),
+                                                     (11, 5, 32, 4, 256), (64, 32, 2, 1, 128)])
+def test_33_to_64_rows_in_small_and_large_batches(lib, fp8, n_seqs, new, heads, kv, dim):
+    """Rows that one kernel serves in few (sequence, kv head) pairs and the other in many: both sides of the rule."""
+    lens = [(new if b % 5 else 1 + b % new, new + (b * 37) % 400) for b in range(n_seqs)]
+    c = Case(lens, heads, kv, dim, 64, fp8, seed=n_seqs + new)
+    c.check(*run(lib, c))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("growth", [3.0, 40.0, -40.0, 600.0])
 @pytest.mark.parametrize("lens,heads,kv,dim", [([(1, 700)], 4, 2, 128), ([(20, 700)], 2, 1, 64), ([(150, 900)], 2, 1, 128),
                                                ([(90, 700)], 4, 2, 64), ([(140, 600)], 1, 1, 256)])
