@@ -1100,7 +1100,7 @@ constexpr int kJoinThreads = 32 * kJoinRows * kJoinSlices, kJoinGrid = 4 * kAttn
 // Joins the shares of the split kernel's split items.  Every block compacts the list of split
 // items, and their rows, kJoinRows at a time, are dealt to the grid.
 template <int kDim>
-__global__ void __launch_bounds__(kJoinThreads, 4) attn_join_kernel(const AttnJob p, int split_grid, int tile_rows) {
+__global__ void __launch_bounds__(kJoinThreads, 2) attn_join_kernel(const AttnJob p, int split_grid, int tile_rows) {
   __shared__ int warp_sum[(2 * kAttnGrid + kJoinThreads - 1) / kJoinThreads * kJoinThreads / 32];
   __shared__ int4 list[kAttnGrid * 2];
   __shared__ float sums[kJoinRows][kJoinSlices][kDim];
@@ -1149,11 +1149,12 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attn_join_kernel(const AttnJo
 #pragma unroll
     for (int j = 0; j < kPer; ++j) acc[j] = 0.f;
     for (int i0 = c0 + slice; i0 <= c1; i0 += kJoinSlices * kBatch) {
-      float2 v[kBatch];
-      float2 x[kBatch][kPer / 2];
+      float2 v[kBatch], x[kBatch][kPer / 2];
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        const int i = i0 + k * kJoinSlices <= c1 ? i0 + k * kJoinSlices : i0;
+        const int i = i0 + k * kJoinSlices;
+        v[k] = make_float2(-INFINITY, 0.f);
+        if (i > c1) continue;
         const int64_t row = static_cast<int64_t>(2 * i + (i == c0 ? 1 : 0)) * tile_rows + r;
         v[k] = *reinterpret_cast<const float2*>(ml + row * 2);
         const float2* o = reinterpret_cast<const float2*>(p.part + row * kDim + lane * kPer);
