@@ -654,10 +654,9 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
       const float ks = (kFp8 && p.k_scale) ? __ldg(p.k_scale + w.h) : 1.0f;
       const bool capped = p.softcap > 0.f;
       const float scale = fabsf(p.scale);  // its sign is in the product
-      // logits in units of log 2: s * mul; with a softcap, cap2 * tanh(s * unit)
+      // logits in units of log 2: s * mul; with a softcap, mul * tanh(s * unit)
       const float unit = scale * ks * qscale * (capped ? 1.0f / p.softcap : log2e);
-      const float mul = capped ? 1.0f : fmaxf(unit, 1.2e-38f);  // (-inf * 0 would be NaN)
-      const float cap2 = p.softcap * log2e;
+      const float mul = fmaxf(capped ? p.softcap * log2e : unit, 1.2e-38f);  // (-inf * 0 would be NaN)
       // keys that this row sees, and those that all rows of the warp see
       const int see_hi = min(pos + 1, w.s.len), see_lo = p.window > 0 ? pos - p.window + 1 : -(1 << 30);
 
@@ -668,20 +667,32 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
         NVFP4_WAIT(bars->s_full + sb, (kG == 2 ? mine : (t >> 1)) & 1);
         tc_fence_after();
         const uint32_t s_at = tmem + lane_at + T::kSCol + sb * kKeys;
+        if (capped || p.scale == 0.f) {
+          // in TMEM, before the rest reads it: two paths of tanh over a whole row would cost every
+          // other call registers (a prompt of 4,096 tokens 140 us instead of 137)
+#pragma unroll 1
+          for (int c = 0; c < kKeys; c += 32) {
+            float x[32], high = 0.f;
+            tmem_ld32(x, s_at + c);
+            tmem_loaded(x);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = p.scale == 0.f ? 0.f : x[i] * unit, high = fmaxf(high, fabsf(x[i]));
+            if (__any_sync(0xffffffffu, high >= kTanhSmall)) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) x[i] = tanh_any(x[i]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) x[i] = tanh_small(x[i]);
+            }
+            tmem_st32(s_at + c, x);
+          }
+          tmem_wait_st();
+        }
         float s[kKeys];
 #pragma unroll
         for (int c = 0; c < kKeys; c += 32) tmem_ld32(s + c, s_at + c);
         tmem_loaded(s);
         const int key0 = (first + j) * kKeys;
-        if (p.scale == 0.f) {
-#pragma unroll
-          for (int c = 0; c < kKeys; ++c) s[c] = 0.f;
-        }
-        if (capped) {
-#pragma unroll
-          for (int c = 0; c < kKeys; ++c)
-            s[c] = cap2 * (1.0f - __fdividef(2.0f, exp2_approx(s[c] * (unit * 2.0f * log2e)) + 1.0f));
-        }
         if (__any_sync(0xffffffffu, key0 + kKeys > see_hi || key0 < see_lo)) {
           const int hi = see_hi - key0, lo = see_lo - key0;
 #pragma unroll

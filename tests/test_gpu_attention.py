@@ -469,3 +469,23 @@ def test_binding_refuses(lib):
             bad()
     with pytest.raises(binding.NVFP4Error):
         lib.paged_attention(c.q[:, :3].contiguous(), cache, batch)      # heads not a multiple of the kv heads
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("cap", [0.5, 20.0, 100000.0])
+@pytest.mark.parametrize("lens,heads,kv,dim", [([(1, 300), (2, 40)], 4, 2, 128), ([(20, 90)], 2, 1, 64), ([(90, 200)], 2, 1, 128),
+                                               ([(70, 150)], 2, 1, 256)])
+def test_a_softcap_keeps_fp32_digits(lib, fp8, cap, lens, heads, kv, dim):
+    """The log-sum-exp under a softcap far above the logits, around them and below: tanh is good to 2^-22 of its value
+    (2^-24 of a polynomial below a half, and above it 2^-22 of 1 - 2 / (e^2x + 1) >= 0.46, hence 2^-21), the product of
+    a logit 2^-23, and the rest as without one."""
+    c = Case(lens, heads, kv, dim, 32, fp8, seed=11)
+    _, lse = run(lib, c, softcap=cap)
+    lse = lse.double().cpu().numpy()
+    q = c.q.double().cpu().numpy()
+    for b, (n, length) in enumerate(lens):
+        at = slice(c.cu[b], c.cu[b + 1])
+        _, want, _, size = OA.attention(q[at], c.keys(b, 0), c.keys(b, 1), length - n, dim ** -0.5, cap)
+        capped = np.minimum(cap, size)                               # a bound on the capped logits
+        bound = dim * 2.0 ** -22 * size + capped * 2.0 ** -20 + length * 2.0 ** -22 + 2.0 ** -21 + 2.0 ** -22 * np.abs(want)
+        assert np.all(np.abs(lse[at] - want) <= bound), f"{np.max(np.abs(lse[at] - want) / bound)} of the bound"
