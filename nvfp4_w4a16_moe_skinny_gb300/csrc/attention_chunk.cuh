@@ -667,7 +667,9 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
         NVFP4_WAIT(bars->s_full + sb, (kG == 2 ? mine : (t >> 1)) & 1);
         tc_fence_after();
         const uint32_t s_at = tmem + lane_at + T::kSCol + sb * kKeys;
-        if (capped || p.scale == 0.f) {
+        const int key0 = (first + j) * kKeys;
+        const bool partly = __any_sync(0xffffffffu, key0 + kKeys > see_hi || key0 < see_lo);
+        if (partly || capped || p.scale == 0.f) {
           // in TMEM, before the rest reads it: two paths of tanh over a whole row would cost every
           // other call registers (a prompt of 4,096 tokens 140 us instead of 137)
 #pragma unroll 1
@@ -676,13 +678,22 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
             tmem_ld32(x, s_at + c);
             tmem_loaded(x);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = p.scale == 0.f ? 0.f : x[i] * unit, high = fmaxf(high, fabsf(x[i]));
-            if (__any_sync(0xffffffffu, high >= kTanhSmall)) {
+            for (int i = 0; i < 32; ++i) x[i] = p.scale == 0.f ? 0.f : x[i];
+            if (capped) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) x[i] = tanh_any(x[i]);
-            } else {
+              for (int i = 0; i < 32; ++i) x[i] *= unit, high = fmaxf(high, fabsf(x[i]));
+              if (__any_sync(0xffffffffu, high >= kTanhSmall)) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) x[i] = tanh_small(x[i]);
+                for (int i = 0; i < 32; ++i) x[i] = tanh_any(x[i]);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = tanh_small(x[i]);
+              }
+            }
+            if (partly) {
+              const int hi = see_hi - key0 - c, lo = see_lo - key0 - c;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) x[i] = i >= lo && i < hi ? x[i] : -INFINITY;
             }
             tmem_st32(s_at + c, x);
           }
@@ -692,12 +703,6 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
 #pragma unroll
         for (int c = 0; c < kKeys; c += 32) tmem_ld32(s + c, s_at + c);
         tmem_loaded(s);
-        const int key0 = (first + j) * kKeys;
-        if (__any_sync(0xffffffffu, key0 + kKeys > see_hi || key0 < see_lo)) {
-          const int hi = see_hi - key0, lo = see_lo - key0;
-#pragma unroll
-          for (int c = 0; c < kKeys; ++c) s[c] = c >= lo && c < hi ? s[c] : -INFINITY;
-        }
         float top[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
         for (int c = 4; c + 8 <= kKeys; c += 8)
