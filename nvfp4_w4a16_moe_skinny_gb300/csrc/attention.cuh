@@ -1,33 +1,42 @@
 // Attention over a paged cache, few rows at a time: decode steps, verify blocks
-// and short chunks (paged_attention).
+// and short chunks (paged_attention); and what both attention kernels share.
+//
+// One pass over the keys.  With the running maximum m of a row's logits s_j (in units of log 2),
+//   l = sum_j 2^(s_j - m),   o = sum_j 2^(s_j - m) v_j,   out = o / l,   lse = (m + log2 l) ln 2,
+// and when m grows, l and o are multiplied by 2^(m_old - m).  Sums over disjoint keys join the same way.
 //
 // Rows.  The heads of one kv head and the new tokens of one sequence are packed
 // into rows r = token * group + head, so the keys and values of a kv head are
 // read once for all of them; a row tile is 16 * RW of these rows.
 //
 // Split.  An item is (sequence, row tile, kv head); its keys are cut into units
-// of kKeys keys.  All units, numbered item by item, are dealt to the
-// grid in equal contiguous ranges, one CTA per SM, so ragged lengths balance by
-// themselves and a single long sequence fills the chip.  Every CTA finds its
-// range from kv_len and cu_tokens by itself (a block-wide scan), so one launch
-// geometry serves a captured graph at any lengths.  An item that lies in one range is
-// finished in registers; otherwise its holders write their shares (unnormalised sums with
-// their row maximum and sum of weights, fp32) to the workspace, at most two per CTA, and
-// the last of them to arrive at a counter joins the shares in range order (join_step): the
-// result does not depend on which one it is, and no CTA waits for another.
+// of kKeys keys.  All units, numbered item by item, are dealt to the grid in contiguous
+// ranges of equal length, so ragged lengths balance by themselves and a single long sequence
+// fills the chip.  Every CTA finds its range from kv_len and cu_tokens by itself (a block-wide
+// scan), so one launch geometry serves a captured graph at any lengths.  An item that lies in one range is
+// finished in registers; otherwise its holders write their shares (o, m and l, fp32) to the
+// workspace, at most two per CTA, and a second grid joins them in range order: the
+// result does not depend on timing, and no CTA waits for another.
 //
 // Inner loop.  One producer warp copies K and V tiles by TMA (swizzled boxes of a
 // page's rows; a page id outside the pool is an out-of-range coordinate, which
-// reads as zeros and touches no memory) into a ring of stages; the
+// reads as zeros and touches no memory) into a ring of stages; four
 // consumer warps run m16n8k16 MMAs.  RW warps share a key slice and split the rows,
-// KW key slices share the rows: a decode step (one row tile of 16) uses eight
-// warps on eight key slices, each with its own running maximum and sum, joined
-// through shared memory once per piece; no barrier stops the loop between tiles.
+// KW = 4 / RW key slices share the rows: a decode step (one row tile of 16) has four
+// slices, each with its own running maximum and sum, joined through shared memory once per
+// item; no barrier stops the loop between tiles.  Q lies in shared memory and comes by ldmatrix like K, so that
+// registers suffice for two CTAs an SM.
 //
 // Numbers.  bf16 caches: bf16 products, fp32 sums, weights rounded to bf16 (half a
 // step of 2^-8, as the result itself).  E4M3 caches: codes convert to f16 exactly;
 // q is scaled by a power of two per row into f16's range (exact down to 2^-31
 // of the row's largest value) and weights are scaled by 2^15 before their rounding to f16 (2^-11).
+//
+// What bounds it.  Memory, where the keys are many: 64 sequences of up to 16K keys (32 heads on 8
+// kv heads of 128 bf16 values, 520 MB) take 89 us, 85% of the rate of a plain copy, two
+// of 131,071 keys over an E4M3 cache (537 MB) 90 us, 88%.  The chain of two launches, the search for the
+// range, the first page look-ups and copies and the join elsewhere: one sequence of 1,000 keys 10.4 us.
+// A row tile is too thin for tcgen05: its products take 128 rows at a time, and the same time for 16.
 #pragma once
 
 #include "launch.cuh"
@@ -88,6 +97,7 @@ struct KvMaps {
 // `snap`: a range boundary that falls this close to an item's end moves there, so that no
 // item is split for a few units.
 // `least`: units that a range holds at least, as far as there are any.
+// What they are worth is measured at AttnTile and ChunkTile.
 struct Tiling {
   int rows, keys, over, snap, least;
 };
@@ -495,12 +505,15 @@ __device__ __forceinline__ uint32_t nonfinite_mask(uint32_t v) {
 
 // ------------------------------------------------------------------ tile geometry
 
-// CTAs of the split kernel on one SM.
+// CTAs of the split kernel on one SM.  Two hide more of each other's waits: 64 sequences of up
+// to 16K keys 91 us against 107 with one (128 bf16 values), 16 of 8,000 with 64 rows 76 against 90.
+// Heads of 256 values have shared memory for one (a stage is 64 KB), and 64 rows of 128 over an
+// E4M3 cache registers (16 sequences of 8,000 keys: 82 us against 103 with two, which spill).
 __host__ __device__ constexpr int attn_ctas(int dim, bool fp8, int rw) {
   return dim == 256 || (dim == 128 && fp8 && rw == 4) ? 1 : 2;
 }
 
-// Keys of one warp's step: few enough that three units fit in a CTA's shared memory and the
+// Keys of one warp's step: few enough that two stages or more fit in a CTA's shared memory and the
 // scores in few registers.
 __host__ __device__ constexpr int attn_slice(int dim, bool fp8, int kw) {
   if (kw == 1) return dim == 256 || (dim == 128 && !fp8) ? 32 : 64;
@@ -515,7 +528,11 @@ struct AttnTile {
   static constexpr int kKeys = kSlice * kKW;                         // keys of a unit
   static constexpr int kConsumers = kRW * kKW;
   static constexpr int kThreadsAll = (kConsumers + 1) * 32;
-  static constexpr int kOver = 3, kSnap = 2, kLeast = 1;             // costs in units (Tiling)
+  // in units (Tiling).  An item counted as its units alone: 112 us for the 64 ragged sequences
+  // above, with three more 87.  Ranges of four units save shares where there is little to do, two
+  // sequences of 2,000 keys with 64 rows 23 us against 33 before the join's present form, but cost verify blocks 7%.
+  // Boundaries that move (two units) make no difference here.
+  static constexpr int kOver = 3, kSnap = 0, kLeast = 1;
   static constexpr int kEl = kFp8 ? 1 : 2;
   static constexpr int kRowB = kDim * kEl < 128 ? kDim * kEl : 128;  // bytes of a row of a block
   static constexpr int kSub = kDim * kEl / kRowB;                    // blocks across a head
@@ -1126,7 +1143,13 @@ constexpr int kJoinRows = 2, kJoinSlices = 4;  // rows of a block's pass, warps 
 constexpr int kJoinThreads = 32 * kJoinRows * kJoinSlices, kJoinGrid = 4 * kAttnGrid;
 
 // Joins the shares of the split kernel's split items.  Every block compacts the list of split
-// items, and their rows, kJoinRows at a time, are dealt to the grid.
+// items, and their rows, kJoinRows at a time, are dealt to the grid.  Bound by latency: the list,
+// then a row's shares, kBatch loads a lane in flight (128 registers; with 64 the loads go in turn, and one
+// sequence of 32,000 keys, 76 shares, 8 rows of 128 values, takes 26.5 us instead of 22.5).
+// Eight warps a row: 21.3 us there, but verify blocks of 30 rows of 256 values 17.1 instead of
+// 15.9; two (before the last step): 31.9 against 26.1; a block for every range boundary, most of
+// them idle, and a warp a row: 38.4.  Joined by the last CTA to arrive, without this grid,
+// verify blocks take 23 us, as one CTA then reads all shares of 30 rows.
 template <int kDim>
 __global__ void __launch_bounds__(kJoinThreads, 2) attn_join_kernel(const AttnJob p, int split_grid, int tile_rows) {
   __shared__ int warp_sum[(2 * kAttnGrid + kJoinThreads - 1) / kJoinThreads * kJoinThreads / 32];

@@ -1,18 +1,20 @@
 // Attention over a paged cache, many rows at a time: prefill chunks and whole
 // prompts (paged_attention), on tcgen05 tensor cores with accumulators in TMEM.
 //
-// The same packed rows, units, ranges and join as the split kernel
+// The same mathematics, packed rows, units and ranges as the split kernel
 // (attention.cuh), with tiles of 128 rows per softmax warpgroup (two of them for
 // heads of 64 and 128 values, one for 256) by kKeys keys.
 //
-// Roles of a CTA (one per SM).  Warp 0 copies K and V tiles by TMA into two-stage
-// rings; one thread of warp 1 issues every MMA and commits it to mbarriers; two or
+// Roles of a CTA (one per SM).  Warp 0 copies K and V tiles by TMA into rings;
+// one thread of warp 1 issues every MMA and commits it to mbarriers; two or
 // four warps make tiles fit for the tensor cores (below); each softmax warpgroup owns
 // 128 rows, a thread a row, so maxima and sums need no exchange.  Per tile: S = Q K^T
 // into TMEM; the row's thread reads S, takes weights 2^(s - m), writes them back as
-// 16-bit P over S; O += P V with P read from TMEM.  With two row groups the
-// tensor cores run one group's products while the other group is in its softmax;
-// with one (256 values) S is double-buffered and the next Q K^T runs meanwhile.
+// 16-bit P over S, in two halves; O += P V with P read from TMEM, started on the first half.
+// With two row groups the tensor cores run one group's products while the other group is in its
+// softmax; with one (256 values: O takes half of TMEM) S is double-buffered and the next
+// Q K^T runs meanwhile.  Softcaps and masks rewrite S in TMEM first, so that the common path
+// has the registers to hold a whole row of S.
 //
 // The reference m of a row's weights follows its maximum lazily: only when a new
 // maximum exceeds it by 2^8 are the row's sums scaled down, so O rarely leaves the
@@ -24,6 +26,13 @@
 // every row's reach become zeros (the pool may hold anything there, and 0 * inf is
 // NaN), and an infinity or NaN in a key that only some rows see is taken out of the
 // product and noted; the rows that see it add it at the end from the pool itself.
+//
+// What bounds it.  The last 2,048 tokens over 32,768 keys (32 heads on 8 kv heads of 128 bf16
+// values, 1.07 PFLOP) take 703 us, 1.51 PFLOP/s or 79% of cuBLAS's burst rate (768 us under the power cap in a
+// long loop, 81% of its sustained one): the softmax of a tile, 128 exponentials a thread, is as
+// long as its products.  Short of that, items: a prompt of 4,096 tokens is 256 of them over 152
+// CTAs, each with Q to fetch, a first S to wait for and O to write (133 us, 54%).  Heads of 64 values halve the
+// products of a tile but not its softmax.  Heads of 256 values are bound by L2: every CTA reads its own tiles.
 #pragma once
 
 #include "attention.cuh"
@@ -47,6 +56,11 @@ struct ChunkTile {
   static constexpr int kRows = 128 * kGroups;
   static constexpr int kKeys = kDim == 256 ? 64 : 128;
   static constexpr int kSBuf = kDim == 256 ? 2 : 1;        // S buffers per group
+  // An item counted as its units alone: a prompt of 4,096 tokens 166 us, with four more 153 (at that
+  // step; five more add 2 to 5% to the shorter prompts, two more make it 168).  Boundaries that move up to four
+  // units instead of one: 512 tokens in a window of 1,024 keys of 256 values 34.6 us against 35.9, but
+  // E4M3 tiles of 128 values, whose units are slow, balance better with one (2,048 tokens 50.8 against 56.7).
+  // Ranges of at least kLeast units: 31 tokens over 2,000 keys 25.7 us against 32.8, 33.6 against 46.9 for 256 values.
   static constexpr int kOver = 4, kSnap = kFp8 && kDim == 128 ? 1 : 4, kLeast = kDim == 256 ? 8 : 4;  // in units (Tiling)
   // warps that make tiles fit: two beside the copies and the products, or (E4M3 and 128 values:
   // 256 conversions a row and tile; 1,404 us with two warps, 1,162 with four, for 2,048 tokens over
@@ -64,7 +78,8 @@ struct ChunkTile {
   static constexpr int kTileB = kKeys * kDim * 2;          // a 16-bit tile: [kDim / 64][kKeys][128 bytes]
   static constexpr int kQB = 128 * kDim * 2;               // a group's Q: [kDim / 64][128][128 bytes]
   // stages of the rings (K and V as the products read them, E4M3 tiles as they are copied):
-  // powers of two, as many as fit
+  // powers of two, as many as fit.  E4M3 heads of 64 values: 2,048 tokens 34.2 us against 41.0 with one
+  // stage of K and two of V; four stages of copies against two: 2% for 1,500-token pieces.
   using KRing = Ring<kDim == 64 ? 4 : (kFp8 ? 1 : 2)>;
   using VRing = Ring<kDim == 64 ? 4 : 2>;
   using RawRing = Ring<4>;

