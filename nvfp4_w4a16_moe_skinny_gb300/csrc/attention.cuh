@@ -1139,27 +1139,29 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, a
 
 // ------------------------------------------------------------------ the join
 
-constexpr int kJoinRows = 2, kJoinSlices = 4;  // rows of a block's pass, warps on each
-constexpr int kJoinThreads = 32 * kJoinRows * kJoinSlices, kJoinGrid = 4 * kAttnGrid;
+constexpr int kJoinWarps = 8, kJoinThreads = 32 * kJoinWarps, kJoinGrid = 4 * kAttnGrid;
+constexpr int kJoinSlices = 4;  // warps on a row's shares, where rows are few
 
 // Joins the shares of the split kernel's split items.  Every block compacts the list of split
-// items, and their rows, kJoinRows at a time, are dealt to the grid.  Bound by latency: the list,
+// items, and their rows are dealt to the grid: a warp a row where that keeps the grid busy (48
+// sequences of 1,000 keys with 64 rows of 64 values: 43 us with four warps a row, 28 with one),
+// else kJoinSlices.  Bound by latency: the list,
 // then a row's shares, kBatch loads a lane in flight (128 registers; with 64 the loads go in turn, and one
 // sequence of 32,000 keys, 76 shares, 8 rows of 128 values, takes 26.5 us instead of 22.5).
 // Eight warps a row: 21.3 us there, but verify blocks of 30 rows of 256 values 17.1 instead of
-// 15.9; two (before the last step): 31.9 against 26.1; a block for every range boundary, most of
+// 15.9; two (before that step): 31.9 against 26.1; a block for every range boundary, most of
 // them idle, and a warp a row: 38.4.  Joined by the last CTA to arrive, without this grid,
 // verify blocks take 23 us, as one CTA then reads all shares of 30 rows.
 template <int kDim>
 __global__ void __launch_bounds__(kJoinThreads, 2) attn_join_kernel(const AttnJob p, int split_grid, int tile_rows) {
-  __shared__ int warp_sum[(2 * kAttnGrid + kJoinThreads - 1) / kJoinThreads * kJoinThreads / 32];
+  __shared__ int warp_sum[(2 * kAttnGrid + kJoinThreads - 1) / kJoinThreads * kJoinWarps];
   __shared__ int4 list[kAttnGrid * 2];
-  __shared__ float sums[kJoinRows][kJoinSlices][kDim];
-  __shared__ float2 refs[kJoinRows][kJoinSlices];
+  __shared__ float sums[kJoinWarps][kDim];
+  __shared__ float2 refs[kJoinWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
   pdl_launch_dependents();
-  constexpr int kSpan = (2 * kAttnGrid + kJoinThreads - 1) / kJoinThreads, kWarps = kJoinThreads / 32;
+  constexpr int kSpan = (2 * kAttnGrid + kJoinThreads - 1) / kJoinThreads;
   int4 mine[kSpan];
   unsigned all[kSpan];
 #pragma unroll
@@ -1170,7 +1172,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) attn_join_kernel(const AttnJo
 #pragma unroll
   for (int b = 0; b < kSpan; ++b) {
     all[b] = __ballot_sync(0xffffffffu, mine[b].x != 0);
-    if (lane == 0) warp_sum[b * kWarps + warp] = __popc(all[b]);
+    if (lane == 0) warp_sum[b * kJoinWarps + warp] = __popc(all[b]);
   }
   __syncthreads();
   int items = 0;
@@ -1178,20 +1180,21 @@ __global__ void __launch_bounds__(kJoinThreads, 2) attn_join_kernel(const AttnJo
   for (int b = 0; b < kSpan; ++b) {
     int at = __popc(all[b] & ((1u << lane) - 1));
 #pragma unroll
-    for (int x = 0; x < kWarps; ++x) {
+    for (int x = 0; x < kJoinWarps; ++x) {
       if (x == warp) at += items;
-      items += warp_sum[b * kWarps + x];
+      items += warp_sum[b * kJoinWarps + x];
     }
     if (mine[b].x != 0) list[at] = make_int4(mine[b].x | (b * kJoinThreads + threadIdx.x) << 16, mine[b].y, mine[b].z, mine[b].w);
   }
   __syncthreads();
   const float* ml = p.part + static_cast<int64_t>(2) * split_grid * tile_rows * kDim;
-  // a row's shares are dealt to kJoinSlices warps, each with kBatch of them in flight (one item
+  // kBatch of a row's shares are in flight in each of the warps that they are dealt to (one item
   // of 32,000 keys over the whole grid has 76 shares)
   constexpr int kPer = kDim / 32, kBatch = kDim == 256 ? 4 : 8;
-  const int slice = warp % kJoinSlices, sub = warp / kJoinSlices;
-  for (int x = blockIdx.x; x < items * (tile_rows / kJoinRows); x += gridDim.x) {
-    const int r0 = x / items * kJoinRows;
+  const int slices = items * tile_rows >= kJoinGrid * kJoinWarps ? 1 : kJoinSlices, per = kJoinWarps / slices;
+  const int slice = warp % slices, sub = warp / slices;
+  for (int x = blockIdx.x; x < items * (tile_rows / per); x += gridDim.x) {
+    const int r0 = x / items * per;
     const int4 it = list[x - x / items * items];
     const int c0 = it.x >> 16, c1 = it.x & 0x1ff, rows = it.x >> 9 & 0x7f;
     if (r0 >= rows) continue;
@@ -1199,11 +1202,11 @@ __global__ void __launch_bounds__(kJoinThreads, 2) attn_join_kernel(const AttnJo
     float m = -INFINITY, l = 0.f, acc[kPer];
 #pragma unroll
     for (int j = 0; j < kPer; ++j) acc[j] = 0.f;
-    for (int i0 = c0 + slice; i0 <= c1; i0 += kJoinSlices * kBatch) {
+    for (int i0 = c0 + slice; i0 <= c1; i0 += slices * kBatch) {
       float2 v[kBatch], x[kBatch][kPer / 2];
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        const int i = i0 + k * kJoinSlices;
+        const int i = i0 + k * slices;
         v[k] = make_float2(-INFINITY, 0.f);
         if (i > c1) continue;
         const int64_t row = static_cast<int64_t>(2 * i + (i == c0 ? 1 : 0)) * tile_rows + r;
@@ -1221,7 +1224,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) attn_join_kernel(const AttnJo
       for (int j = 0; j < kPer; ++j) acc[j] *= a0;
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        if (i0 + k * kJoinSlices > c1) break;
+        if (i0 + k * slices > c1) break;
         const float a = next == -INFINITY ? 1.0f : exp2_approx(v[k].x - next);
         l += a * v[k].y;
 #pragma unroll
@@ -1229,23 +1232,29 @@ __global__ void __launch_bounds__(kJoinThreads, 2) attn_join_kernel(const AttnJo
       }
       m = next;
     }
+    if (slices > 1) {  // the slices in their order
 #pragma unroll
-    for (int j = 0; j < kPer; j += 2) *reinterpret_cast<float2*>(&sums[sub][slice][lane * kPer + j]) = make_float2(acc[j], acc[j + 1]);
-    if (lane == 0) refs[sub][slice] = make_float2(m, l);
-    __syncthreads();
-    if (slice == 0 && r0 + sub < rows) {
+      for (int j = 0; j < kPer; j += 2)
+        *reinterpret_cast<float2*>(&sums[warp][lane * kPer + j]) = make_float2(acc[j], acc[j + 1]);
+      if (lane == 0) refs[warp] = make_float2(m, l);
+      __syncthreads();
+      if (slice == 0) {
 #pragma unroll
-      for (int k = 1; k < kJoinSlices; ++k) m = fmaxf(m, refs[sub][k].x);
-      l = 0.f;
+        for (int k = 1; k < kJoinSlices; ++k) m = fmaxf(m, refs[warp + k].x);
+        l = 0.f;
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) acc[j] = 0.f;
+        for (int j = 0; j < kPer; ++j) acc[j] = 0.f;
 #pragma unroll
-      for (int k = 0; k < kJoinSlices; ++k) {
-        const float a = m == -INFINITY ? 1.0f : exp2_approx(refs[sub][k].x - m);
-        l += a * refs[sub][k].y;
+        for (int k = 0; k < kJoinSlices; ++k) {
+          const float a = m == -INFINITY ? 1.0f : exp2_approx(refs[warp + k].x - m);
+          l += a * refs[warp + k].y;
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) acc[j] += a * sums[sub][k][lane * kPer + j];
+          for (int j = 0; j < kPer; ++j) acc[j] += a * sums[warp + k][lane * kPer + j];
+        }
       }
+      __syncthreads();
+    }
+    if (slice == 0 && r0 + sub < rows) {
       const int rr = it.z + r, tok = div_by(p.by_group, rr), head = it.y * p.group + rr - tok * p.group;
       const int64_t row = it.w + tok;
       const float inv = l == 0.f ? 0.f : (p.v_scale ? __ldg(p.v_scale + it.y) : 1.0f) / l;
@@ -1254,7 +1263,6 @@ __global__ void __launch_bounds__(kJoinThreads, 2) attn_join_kernel(const AttnJo
       for (int j = 0; j < kPer; j += 2) o[j / 2] = f32x2_to_bf16x2(acc[j] * inv, acc[j + 1] * inv);
       if (p.lse && lane == 0) p.lse[row * p.n_heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
     }
-    __syncthreads();
   }
 }
 
@@ -1262,11 +1270,13 @@ __global__ void __launch_bounds__(kJoinThreads, 2) attn_join_kernel(const AttnJo
 
 // Which kernel and tile serve up to `rows` packed rows per sequence and kv head, in `items`
 // pairs of those.
-// Rows above 64 go to the tcgen05 kernel (attention_chunk.cuh), and rows above 32 where the
-// batch alone fills the chip: 16 sequences of 8,000 keys and 4 kv heads with 64 rows of 128
-// bf16 values take 67 us there and 76 here (256 values: 107 and 134), 32 of 500 keys 16 and 33,
-// but one of 32,000 keys 45 and 33 us, two of 2,000 24 and 17: its tiles of 256 rows start and
-// join slowly.  (Eight sequences are even: 18 and 22 us, 256 values 29 and 25, at 1,000 keys.)
+// Rows above 64 go to the tcgen05 kernel (attention_chunk.cuh): 8 sequences of 8,000 keys (128 values,
+// bf16), 124 rows: 41 us there, 54 with tiles of 64 rows here.  Heads of 256 values go there above
+// 32 rows too, where the batch alone fills the chip: 64 ragged sequences of up to 4,000 keys and 4 kv
+// heads, 40 rows, 47 us there and 57 here, 16 of 8,000 keys with 64 rows 107 and 136 (E4M3 106 and 152); but one of
+// 32,000 keys 68 and 48, two of 2,000 31 and 19.  With 128 values the ragged batch takes
+// 39 us there and 31 here, 48 sequences of 1,000 keys 41 and 43, and only equal lengths gain (16 of
+// 8,000 keys 67 and 76, 32 of 500 keys 16 and 24); 64 values likewise (32 and 20, 31 and 28).
 // Up to 32 rows this kernel is ahead in every batch measured.
 // A tile of 16 rows leaves four key slices to four warps, 32 rows two, 64 rows share one: the smallest
 // that holds the rows.  16 sequences of 8,000 keys, 8 rows, 128 values: 51.7, 56.1 and 69.4 us
@@ -1278,7 +1288,7 @@ struct AttnShape {
 };
 constexpr int kMapPairs = 4;
 inline AttnShape attn_shape(int dim, bool fp8, int64_t rows, int64_t items) {
-  if (rows > 64 || (rows > 32 && items >= 48)) return {0, 0, dim == 256 ? 128 : 256, dim == 256 ? 64 : 128, true, 3};
+  if (rows > 64 || (dim == 256 && rows > 32 && items >= 48)) return {0, 0, dim == 256 ? 128 : 256, dim == 256 ? 64 : 128, true, 3};
   const int rw = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
   const int kw = 4 / rw;
   return {rw, kw, 16 * rw, attn_slice(dim, fp8, kw) * kw, false, rw / 2};

@@ -182,7 +182,7 @@ def test_tiles_of_32_and_64_rows_over_many_ctas(lib, fp8, new, heads, kv, dim, c
 
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("n_seqs,new,heads,kv,dim", [(24, 17, 4, 2, 128), (47, 33, 1, 1, 64), (48, 33, 1, 1, 64), (12, 5, 32, 4, 256),
-                                                     (11, 5, 32, 4, 256), (64, 32, 2, 1, 128)])
+                                                     (11, 5, 32, 4, 256), (64, 32, 2, 1, 128), (130, 60, 1, 1, 128), (47, 33, 1, 1, 256), (48, 33, 1, 1, 256)])
 def test_33_to_64_rows_in_small_and_large_batches(lib, fp8, n_seqs, new, heads, kv, dim):
     """Rows that one kernel serves in few (sequence, kv head) pairs and the other in many: both sides of the rule."""
     lens = [(new if b % 5 else 1 + b % new, new + (b * 37) % 400) for b in range(n_seqs)]
