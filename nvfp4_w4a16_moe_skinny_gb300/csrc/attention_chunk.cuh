@@ -63,7 +63,7 @@ struct ChunkTile {
   // Ranges of at least kLeast units: 31 tokens over 2,000 keys 25.7 us against 32.8, 33.6 against 46.9 for 256 values.
   static constexpr int kOver = 4, kSnap = kFp8 && kDim == 128 ? 1 : 4, kLeast = kDim == 256 ? 8 : 4;  // in units (Tiling)
   // warps that make tiles fit: two beside the copies and the products, or (E4M3 and 128 values:
-  // 256 conversions a row and tile; 1,404 us with two warps, 1,162 with four, for 2,048 tokens over
+  // 256 conversions a row and tile; 830 us with two warps, 705 with four, for 2,048 tokens over
   // 32,768 keys) a warpgroup of their own; the softmax warpgroups follow
   static constexpr bool kFitGroup = kFp8 && kDim == 128;
   static constexpr int kFit0 = kFitGroup ? 4 : 2, kFits = kFitGroup ? 4 : 2, kSoft0 = kFit0 + kFits;
@@ -79,10 +79,12 @@ struct ChunkTile {
   static constexpr int kQB = 128 * kDim * 2;               // a group's Q: [kDim / 64][128][128 bytes]
   // stages of the rings (K and V as the products read them, E4M3 tiles as they are copied):
   // powers of two, as many as fit.  E4M3 heads of 64 values: 2,048 tokens 34.2 us against 41.0 with one
-  // stage of K and two of V; four stages of copies against two: 2% for 1,500-token pieces.
-  using KRing = Ring<kDim == 64 ? 4 : (kFp8 ? 1 : 2)>;
+  // stage of K and two of V; four stages of copies against two: 2% for 1,500-token pieces.  128 values:
+  // 2,048 tokens over 32,768 keys 705 us with two stages of K and two of copies, 1,117 with one and four;
+  // 256 values, whose row group waits for copies more than for K, 2,538 and 2,403.
+  using KRing = Ring<kDim == 64 ? 4 : (kFp8 && kDim == 256 ? 1 : 2)>;
   using VRing = Ring<kDim == 64 ? 4 : 2>;
-  using RawRing = Ring<4>;
+  using RawRing = Ring<kDim == 128 ? 2 : 4>;
   static constexpr int kKAt = kGroups * kQB, kVAt = kKAt + KRing::kStages * kTileB;
   static constexpr int kRaw = kVAt + VRing::kStages * kTileB;
   static constexpr int kBars = kRaw + (kFp8 ? RawRing::kStages * kRawB : 0);
