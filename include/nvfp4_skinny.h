@@ -580,6 +580,27 @@ nvfp4_status paged_attention(const nvfp4_kv_cache *cache, const nvfp4_batch *bat
                              size_t ws_bytes, cudaStream_t stream);
 
 /*
+ * Host-side walk of the split that an attention call would make, through the
+ * kernels' own arithmetic, for host-side checks (no device work; no CUDA call).
+ *   cache, n_tokens, n_heads, window  as for paged_attention (pools are not read).
+ *   batch   cu_tokens and kv_len in host memory; page_table is not read.
+ *   orders  how many orders of the CTAs' arrivals to play through the joins of
+ *           calls of many rows (the first two: ascending and descending).
+ *   out     (host) int32 [9]: 1 if every key tile of every (sequence, row tile, kv
+ *           head) item is in exactly one share, every share where its join looks
+ *           for it, no arrival counter belongs to two items, and every item was
+ *           joined once, from all of its shares, with all counters zero at the end,
+ *           in every order (else 0); the rows of a row tile; the ranges in use; the
+ *           items; the split items; the most shares of an item; the uses of a
+ *           counter by a second item; the failures of the orders; 1 if the kernel
+ *           for many rows serves the call.
+ * Returns NVFP4_ERR_SHAPE for sizes that the call rejects or above 2^22 items.
+ */
+nvfp4_status paged_attention_plan_check(const nvfp4_kv_cache *cache, const nvfp4_batch *batch, int32_t n_tokens,
+                                        int32_t n_heads, int32_t window, int32_t orders, int32_t *out,
+                                        int32_t out_len);
+
+/*
  * The launch plan a product would use, for host-side checks of the work
  * decomposition (no device work; no CUDA call).
  *   product  0 dense GEMM (n x k), 1 lm_head (n x k), 2 MoE gate+up (n = 2*inter,

@@ -37,6 +37,7 @@ EXPORTS = (
     "lm_head_sample", "moe_route_topk_ex", "lm_head_sample_ex", "nvfp4_plan_check", "moe_router_logits",
     "nvfp4_repack_host", "nvfp4_quantize_act", "nvfp4_gemm_w4a4", "lm_head_argmax_w4a4", "moe_forward", "nvfp4_selftest_wait_timeout",
     "rope_frequencies", "rope_apply", "kv_append", "kv_cache_maps", "paged_attention_workspace_bytes", "paged_attention",
+    "paged_attention_plan_check",
 )
 
 
@@ -208,6 +209,8 @@ def _sig(lib):
     lib.paged_attention.argtypes = [_P, _P, _P, _I64, _I, _I, ctypes.c_float, ctypes.c_float, _I, _P, _I64, _P, _P,
                                     _SZ, _P]
     lib.paged_attention.restype = ctypes.c_int
+    lib.paged_attention_plan_check.argtypes = [_P, _P, _I, _I, _I, _I, ctypes.POINTER(ctypes.c_int32), _I]
+    lib.paged_attention_plan_check.restype = ctypes.c_int
     for name in ("nvfp4_quantize", "nvfp4_repack", "nvfp4_gemm", "moe_route_topk", "moe_ffn_grouped",
                  "lm_head_argmax", "lm_head_argmax_noalloc", "nvfp4_device_error"):
         getattr(lib, name).restype = ctypes.c_int

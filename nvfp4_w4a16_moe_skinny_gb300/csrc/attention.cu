@@ -35,17 +35,6 @@ bool encode_maps(KvMaps* maps, const nvfp4_kv_cache* c, const AttnShape& s) {
   return encode_pool_map(&maps->k, c, c->k, box, !s.chunk) && encode_pool_map(&maps->v, c, c->v, box, !s.chunk);
 }
 
-bool sizes_ok(int n_tokens, int n_seqs, int max_new, int n_heads, int n_kv_heads, int head_dim) {
-  if (n_tokens < 0 || n_seqs < 0 || max_new < 0 || n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads) return false;
-  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return false;
-  // positions and packed rows of a sequence are counted in 32 bits
-  return n_tokens < (1 << 30) && static_cast<int64_t>(n_tokens) * (n_heads / n_kv_heads) < (int64_t{1} << 31) - 1024;
-}
-
-int64_t packed_rows(int n_tokens, int max_new, int n_heads, int n_kv_heads) {
-  return static_cast<int64_t>(std::min(n_tokens, max_new)) * (n_heads / n_kv_heads);
-}
-
 }  // namespace
 }  // namespace nvfp4
 
@@ -69,7 +58,7 @@ nvfp4_status kv_cache_maps(const nvfp4_kv_cache* cache, void* maps) {
 
 size_t paged_attention_workspace_bytes(int32_t n_tokens, int32_t n_seqs, int32_t max_new, int32_t n_heads,
                                        int32_t n_kv_heads, int32_t head_dim) {
-  if (!sizes_ok(n_tokens, n_seqs, max_new, n_heads, n_kv_heads, head_dim)) return 0;
+  if (!attn_rows_ok(n_tokens, n_seqs, max_new, n_heads, n_kv_heads, head_dim)) return 0;
   const AttnShape s = attn_shape(head_dim, false, packed_rows(n_tokens, max_new, n_heads, n_kv_heads),
                                  static_cast<int64_t>(n_seqs) * n_kv_heads);
   const int grid = kAttnGrid * (s.chunk ? 1 : attn_ctas(head_dim, false, s.rw));
@@ -84,10 +73,8 @@ nvfp4_status paged_attention(const nvfp4_kv_cache* cache, const nvfp4_batch* bat
   if (const nvfp4_status st = check_cache(cache)) return st;
   if (!batch || !q || !out || !batch->cu_tokens || !batch->kv_len || !batch->page_table) return NVFP4_ERR_NULL;
   const int kv = cache->n_kv_heads, dim = cache->head_dim;
-  if (!sizes_ok(n_tokens, batch->n_seqs, batch->max_new, n_heads, kv, dim) || batch->max_pages < 1)
+  if (!attn_sizes_ok(n_tokens, batch->n_seqs, batch->max_new, n_heads, kv, dim, batch->max_pages, cache->page_size))
     return NVFP4_ERR_SHAPE;
-  // key positions are counted in 32 bits
-  if (static_cast<int64_t>(batch->max_pages) * cache->page_size >= (int64_t{1} << 30)) return NVFP4_ERR_SHAPE;
   if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.f || window < 0) return NVFP4_ERR_SHAPE;
   if (const nvfp4_status st = check_rows(q, q_stride, n_heads, dim)) return st;
   if (const nvfp4_status st = check_rows(out, out_stride, n_heads, dim)) return st;
@@ -107,7 +94,7 @@ nvfp4_status paged_attention(const nvfp4_kv_cache* cache, const nvfp4_batch* bat
   p.v_pool = cache->v, p.page_stride = cache->page_stride;
   p.k_scale = cache->k_scale, p.v_scale = cache->v_scale;
   p.scale = scale, p.softcap = softcap;
-  p.window = window < (1 << 30) ? window : 0;  // (no sequence is that long: all keys)
+  p.window = attn_window(window);
   p.counters = static_cast<unsigned*>(ws);
   p.split = reinterpret_cast<int4*>(static_cast<uint8_t*>(ws) + kAttnCounterBytes);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kAttnCounterBytes + kAttnSplitBytes);

@@ -92,6 +92,9 @@ struct KvMaps {
 
 // ------------------------------------------------------------------ work decomposition
 
+// What the kernels and the host-side check of the split (paged_attention_plan_check) share is
+// compiled for both.
+//
 // Tiling of one kernel: rows of a row tile, keys of a unit, and what starting and
 // finishing an item costs, counted in units (the ranges are balanced with it).
 // `snap`: a range boundary that falls this close to an item's end moves there, so that no
@@ -104,23 +107,31 @@ struct Tiling {
 
 // Quotient of x < 2^31 by the divisor that `d` was made for (fast_div): a multiply by the
 // rounded-up reciprocal and a shift.
-__device__ __forceinline__ int div_by(const FastDiv d, int x) {
+__host__ __device__ __forceinline__ int div_by(const FastDiv d, int x) {
+#ifdef __CUDA_ARCH__
   return d.shift < 0 ? x : static_cast<int>(__umulhi(static_cast<uint32_t>(x), d.mul) >> d.shift);
+#else
+  const uint64_t product = static_cast<uint64_t>(static_cast<uint32_t>(x)) * d.mul;
+  return d.shift < 0 ? x : static_cast<int>(static_cast<uint32_t>(product >> 32) >> d.shift);
+#endif
 }
 
 struct Sequence {
   int tok0, n, len, rows, tiles;
 };
 
-__device__ __forceinline__ Sequence sequence_of(const AttnJob& p, int b, const Tiling& g) {
+// From cu_tokens[b], cu_tokens[b + 1] and kv_len[b].
+__host__ __device__ __forceinline__ Sequence sequence_from(const AttnJob& p, int lo, int hi, int len, const Tiling& g) {
   Sequence s;
-  const int lo = __ldg(p.cu + b), hi = __ldg(p.cu + b + 1), len = __ldg(p.kv_len + b);
   s.tok0 = min(max(lo, 0), p.n_tokens);
   s.n = min(max(hi, s.tok0), p.n_tokens) - s.tok0;
   s.len = min(max(len, 0), p.max_pages << p.page_log2);
   s.rows = s.n * p.group;
   s.tiles = (s.rows + g.rows - 1) / g.rows;
   return s;
+}
+__device__ __forceinline__ Sequence sequence_of(const AttnJob& p, int b, const Tiling& g) {
+  return sequence_from(p, __ldg(p.cu + b), __ldg(p.cu + b + 1), __ldg(p.kv_len + b), g);
 }
 
 // A row tile of one sequence and the keys that any of its rows sees, [lo, hi).
@@ -130,7 +141,7 @@ struct RowTile {
   int tile0, units;  // first key tile, number of units (at least one, so that empty rows are written)
 };
 
-__device__ __forceinline__ RowTile row_tile(const AttnJob& p, const Sequence& s, int rt, const Tiling& g) {
+__host__ __device__ __forceinline__ RowTile row_tile(const AttnJob& p, const Sequence& s, int rt, const Tiling& g) {
   RowTile t;
   t.row0 = rt * g.rows;
   t.rows = min(g.rows, s.rows - t.row0);
@@ -155,7 +166,7 @@ __device__ __forceinline__ long long tile_units(const AttnJob& p, const Sequence
 struct Ranges {
   long long total, each;
   int grid, more;  // ranges in use; the first `more` of them hold each + 1 units
-  __device__ __forceinline__ void set(long long all, int ctas, int least) {
+  __host__ __device__ __forceinline__ void set(long long all, int ctas, int least) {
     total = all;
     grid = all >= static_cast<long long>(ctas) * least ? ctas : (static_cast<int>(all) + least - 1) / least;
     if (grid < 1) {
@@ -169,8 +180,8 @@ struct Ranges {
       more = static_cast<int>(static_cast<uint32_t>(all) - q * grid);
     }
   }
-  __device__ __forceinline__ long long start(int c) const { return c * each + min(c, more); }
-  __device__ __forceinline__ int holder(long long u) const {
+  __host__ __device__ __forceinline__ long long start(int c) const { return c * each + min(c, more); }
+  __host__ __device__ __forceinline__ int holder(long long u) const {
     const long long cut = more * (each + 1), by = u < cut ? each + 1 : each, at = u < cut ? u : u - cut;
     const int before = u < cut ? 0 : more;
     if (total >> 31) return before + static_cast<int>(at / by);
@@ -366,7 +377,7 @@ __device__ __forceinline__ void walk_to(const AttnJob& p, Walk& w, long long u, 
 
 // Where a range boundary d units into an item of `units` tiles lies after snapping: 0, the
 // whole span, or d.
-__device__ __forceinline__ int snapped(int d, int units, const Tiling& g) {
+__host__ __device__ __forceinline__ int snapped(int d, int units, const Tiling& g) {
   const int span = units + g.over, t = min(g.snap, (span - 1) / 2);
   return d <= t ? 0 : (d >= span - t ? span : d);
 }
@@ -380,7 +391,7 @@ struct Share {
   long long end;
 };
 
-__device__ __forceinline__ Share share_at(const Walk& w, long long u, long long u0, long long u1, int c,
+__host__ __device__ __forceinline__ Share share_at(const Walk& w, long long u, long long u0, long long u1, int c,
                                           const Tiling& g) {
   Share q;
   const int units = w.t.units, span = units + g.over;
@@ -398,7 +409,7 @@ __device__ __forceinline__ Share share_at(const Walk& w, long long u, long long 
 struct Holders {
   int c0, c1;
 };
-__device__ __forceinline__ Holders holders_of(const Walk& w, const Ranges& r, const Tiling& g) {
+__host__ __device__ __forceinline__ Holders holders_of(const Walk& w, const Ranges& r, const Tiling& g) {
   const int span = w.t.units + g.over, t = min(g.snap, (span - 1) / 2);
   Holders h;
   h.c0 = r.holder(w.item0 + t);  // boundaries up to t units in have moved to the item's start
@@ -533,6 +544,7 @@ struct AttnTile {
   // sequences of 2,000 keys with 64 rows 23 us against 33 before the join's present form, but cost verify blocks 7%.
   // Boundaries that move (two units) make no difference here.
   static constexpr int kOver = 3, kSnap = 0, kLeast = 1;
+  static constexpr __host__ __device__ Tiling tiling() { return {kRows, kKeys, kOver, kSnap, kLeast}; }
   static constexpr int kEl = kFp8 ? 1 : 2;
   static constexpr int kRowB = kDim * kEl < 128 ? kDim * kEl : 128;  // bytes of a row of a block
   static constexpr int kSub = kDim * kEl / kRowB;                    // blocks across a head
@@ -666,7 +678,7 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, a
   pdl_launch_dependents();
   __syncthreads();
 
-  constexpr Tiling kTiling{T::kRows, T::kKeys, T::kOver, T::kSnap, T::kLeast};
+  constexpr Tiling kTiling = T::tiling();
   Found f;
   Ranges ranges;
   find_range<T::kThreadsAll>(p, kTiling, gridDim.x, blockIdx.x, &ranges, &f, scratch,
@@ -1293,6 +1305,26 @@ inline AttnShape attn_shape(int dim, bool fp8, int64_t rows, int64_t items) {
   const int kw = 4 / rw;
   return {rw, kw, 16 * rw, attn_slice(dim, fp8, kw) * kw, false, rw / 2};
 }
+
+// Checks of an attention call's sizes.
+inline bool attn_rows_ok(int n_tokens, int n_seqs, int max_new, int n_heads, int n_kv_heads, int head_dim) {
+  if (n_tokens < 0 || n_seqs < 0 || max_new < 0 || n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads) return false;
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return false;
+  // positions and packed rows of a sequence are counted in 32 bits
+  return n_tokens < (1 << 30) && static_cast<int64_t>(n_tokens) * (n_heads / n_kv_heads) < (int64_t{1} << 31) - 1024;
+}
+inline bool attn_sizes_ok(int n_tokens, int n_seqs, int max_new, int n_heads, int n_kv_heads, int head_dim,
+                          int max_pages, int page_size) {
+  // key positions are counted in 32 bits
+  return attn_rows_ok(n_tokens, n_seqs, max_new, n_heads, n_kv_heads, head_dim) && max_pages >= 1 &&
+         static_cast<int64_t>(max_pages) * page_size < (int64_t{1} << 30);
+}
+
+inline int64_t packed_rows(int n_tokens, int max_new, int n_heads, int n_kv_heads) {
+  return static_cast<int64_t>(n_tokens < max_new ? n_tokens : max_new) * (n_heads / n_kv_heads);
+}
+
+inline int attn_window(int window) { return window < (1 << 30) ? window : 0; }  // (no sequence is that long: all keys)
 
 template <int kDim>
 nvfp4_status launch_attn_join(const AttnJob& p, int tile_rows, int keys, int grid, cudaStream_t stream) {

@@ -62,6 +62,7 @@ struct ChunkTile {
   // E4M3 tiles of 128 values, whose units are slow, balance better with one (2,048 tokens 50.8 against 56.7).
   // Ranges of at least kLeast units: 31 tokens over 2,000 keys 25.7 us against 32.8, 33.6 against 46.9 for 256 values.
   static constexpr int kOver = 4, kSnap = kFp8 && kDim == 128 ? 1 : 4, kLeast = kDim == 256 ? 8 : 4;  // in units (Tiling)
+  static constexpr __host__ __device__ Tiling tiling() { return {kRows, kKeys, kOver, kSnap, kLeast}; }
   // warps that make tiles fit: two beside the copies and the products, or (E4M3 and 128 values:
   // 256 conversions a row and tile; 830 us with two warps, 705 with four, for 2,048 tokens over
   // 32,768 keys) a warpgroup of their own; the softmax warpgroups follow
@@ -267,17 +268,25 @@ __device__ __forceinline__ bool last_to_arrive(unsigned* counter, int arrivals, 
   return last;
 }
 
+// A group of one has nothing to join and nobody to wait for: its share goes up a level without a
+// counter.  With that, counters of different items never meet, although an item that ends
+// in range c1 and the next one that starts there have shares of the same CTA: a group of
+// two or more starts at least one share before its item's last, so that an item of shares c0 .. c1
+// uses counters c0 .. c1 - 1, and the next one's begin at c1.  (The top group of a split item always has
+// two or more.)
 struct JoinStep {
-  int start, stride, count, counter;  // shares start, start + stride, ... (count of them); the group's counter
+  int start, stride, count, counter;  // shares start, start + stride, ... (count of them); the group's counter or -1
   bool top;                           // the item is whole after this step
 };
-__device__ __forceinline__ JoinStep join_step(int mine, int level, int holders) {
+__host__ __device__ __forceinline__ JoinStep join_step(int mine, int level, int holders) {
   JoinStep s;
   s.stride = level == 0 ? 1 : (level == 1 ? kJoinGroup : kJoinGroup * kJoinGroup);
   const int size = s.stride * kJoinGroup;
   s.start = mine / size * size;
   s.count = min(kJoinGroup, (holders - s.start + s.stride - 1) / s.stride);
-  s.counter = s.start + level;  // distinct over groups and levels: start is a multiple of 8 ^ (level + 1)
+  // distinct over groups and levels (start is a multiple of 8 ^ (level + 1)), and below the item's last
+  // share: a group of two or more has its second one at start + 8 ^ level
+  s.counter = s.count > 1 ? s.start + level : -1;
   s.top = size >= holders;
   return s;
 }
@@ -326,7 +335,7 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
   tc_fence_after();
   const uint32_t tmem = uniform(*static_cast<volatile uint32_t*>(&bars->tmem));
 
-  constexpr Tiling kTiling{T::kRows, T::kKeys, T::kOver, T::kSnap, T::kLeast};
+  constexpr Tiling kTiling = T::tiling();
   Found f;
   Ranges ranges;
   find_range<T::kThreadsAll>(p, kTiling, gridDim.x, blockIdx.x, &ranges, &f, &bars->scratch,
@@ -867,6 +876,10 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
         int mine = static_cast<int>(blockIdx.x) - h.c0;
         for (int level = 0;; ++level) {
           const JoinStep s = join_step(mine, level, h.c1 - h.c0 + 1);
+          if (s.counter < 0) {
+            mine = s.start;
+            continue;
+          }
           if (!last_to_arrive<128>(p.counters + 2 * (h.c0 + s.counter) + g, s.count, 1 + g, &bars->say[g])) break;
           const auto slot_of = [&](int i) {
             const int share = s.start + i * s.stride;

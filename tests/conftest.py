@@ -21,3 +21,16 @@ def lib():
         pytest.skip("no CUDA device")
     from nvfp4_w4a16_moe_skinny_gb300 import binding
     return binding.load()
+
+
+@pytest.fixture(autouse=True)
+def attention_counters_are_left_zero(request):
+    """After every GPU test: the arrival counters of all attention workspaces are zero, as a completed call leaves them."""
+    yield
+    if "lib" not in request.fixturenames:
+        return
+    import torch
+    lib = request.getfixturevalue("lib")
+    torch.cuda.synchronize()
+    for key, ws in lib._attention_ws.items():
+        assert not ws[0][:4096].any(), f"arrival counters of the workspace of {key}"
