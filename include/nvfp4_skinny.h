@@ -514,9 +514,11 @@ nvfp4_status rope_frequencies(int32_t rot_dim, double theta, double factor, doub
 /*
  * Rotary positions on the first rot_dim values of every head; the rest is copied:
  *   y_a = amplitude * (x_a cos t - x_b sin t),  y_b = amplitude * (x_b cos t + x_a sin t)
- * for pair i = (a, b) and t = positions[token] * inv_freq[i].  The angle is
- * reduced exactly (64-bit turns), so far positions lose nothing; the products
- * are fp32, rounded once.
+ * for pair i = (a, b) and t = positions[token] * inv_freq[i].  A frequency is held
+ * as a 64-bit fraction of a turn (off by less than 2^-63 of a turn a position, for
+ * frequencies below 4; twice that for each power of two above) and the angle reduced
+ * in integers, so far positions lose nothing and small angles keep fp32's digits;
+ * the products are fp32, rounded once.
  *   x, y       (device) rows of heads; y may be x (same stride).
  *   positions  (device) int32 [n_tokens], any sign.
  *   inv_freq   (device) fp64 [rot_dim / 2], finite, >= 0, below 2^63.

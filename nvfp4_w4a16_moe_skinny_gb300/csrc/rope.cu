@@ -62,13 +62,12 @@ __device__ __forceinline__ uint64_t turns_per_position(double w) {
 
 __device__ __forceinline__ void angle_of(const RopeJob& p, int pos, int pair, float& c, float& s) {
   const uint64_t t = static_cast<uint64_t>(static_cast<int64_t>(pos)) * turns_per_position(__ldg(p.inv_freq + pair));
-  // the nearest quarter turn is taken off as an integer, so that the fp32 rest
-  // keeps its 24 bits near the axes
-  const int32_t phase = static_cast<int32_t>(t >> 32);
-  const uint32_t quarter = (static_cast<uint32_t>(phase) + (1u << 29)) >> 30;
-  const int32_t rest = static_cast<int32_t>(static_cast<uint32_t>(phase) - (quarter << 30));
+  // the nearest quarter turn is taken off as an integer, and the rest keeps all of its bits until it
+  // becomes fp32, so that it has 24 of them near the axes too (a slow pair at position 1 turns by 2^-30)
+  const uint32_t quarter = static_cast<uint32_t>((t + (1ull << 61)) >> 62);
+  const int64_t rest = static_cast<int64_t>(t - (static_cast<uint64_t>(quarter) << 62));
   float sr, cr;
-  sincospif(static_cast<float>(rest) * (1.0f / 2147483648.0f), &sr, &cr);
+  sincospif(__ll2float_rn(rest) * 0x1p-63f, &sr, &cr);
   const bool swap = quarter & 1;
   const float cc = swap ? sr : cr, ss = swap ? cr : sr;
   c = (quarter == 1 || quarter == 2) ? -cc : cc;
