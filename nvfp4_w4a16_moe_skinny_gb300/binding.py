@@ -231,6 +231,18 @@ def _raw_stream(stream, device) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
+def _current_device() -> int:
+    return torch._C._cuda_getDevice()
+
+
+def _on_current(device, stream):
+    """The library launches on the current device; a default stream's handle is the same on every one."""
+    if device.type != "cuda" or device.index != _current_device():
+        raise ValueError(f"tensors on {device}: they have to be on the current GPU (torch.cuda.device(...) makes it so)")
+    if stream is not None and stream.device_index != device.index:
+        raise ValueError("stream: of another GPU than the tensors")
+
+
 def _empty(shape, dtype, device, stream):
     """An output, allocated on the stream that writes it: memory that another stream's work may still use is not
     written before that work is done."""
@@ -520,6 +532,7 @@ class Library:
         """Rotary positions on the first 2 * len(inv_freq) values of every head of x [tokens, heads, dim]; out may be x.
         inverse rotates back, which is the gradient's way through the rotation."""
         dev = x.device
+        _on_current(dev, stream)
         stride = _rows(x, "x", dev)
         tokens, heads, dim = x.shape
         pairs = inv_freq.shape[0]
@@ -546,6 +559,7 @@ class Library:
         """Write k (rotated, if inv_freq is given) and v [tokens, n_kv_heads, dim] to slots int64 [tokens] of the cache
         (negative: skipped) and return the rotated q (None without q); q_out may be q."""
         dev = cache.device
+        _on_current(dev, stream)
         tokens, heads, dim = k.shape
         _need(k.shape == v.shape and heads == cache.n_kv_heads and dim == cache.head_dim,
               "k and v: [tokens, n_kv_heads, head_dim] of the cache")
@@ -586,6 +600,7 @@ class Library:
         """Attention of the batch's new tokens q [tokens, heads, dim] over their sequences' cached keys (scale: 1 /
         sqrt(dim)): out, or (out, log-sum-exp fp32 [tokens, heads]) with with_lse."""
         dev = cache.device
+        _on_current(dev, stream)
         stride = _rows(q, "q", dev)
         shape = q.shape
         tokens, heads, dim = shape
