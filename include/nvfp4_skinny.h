@@ -429,6 +429,9 @@ nvfp4_status lm_head_argmax_noalloc(const nvfp4_weight *w, const uint16_t *x, in
  * contiguous and `stride` elements from one token to the next (>= heads *
  * head_dim, a multiple of 8), so that slices of a fused projection's rows can be
  * passed as they are.  Row pointers are 16-byte aligned.
+ *
+ * Calls without tokens (n_tokens = 0) or without sequences (n_seqs = 0) check their
+ * other arguments and launch nothing; what would hold those rows may be NULL then.
  */
 
 /*
@@ -524,7 +527,6 @@ nvfp4_status rope_frequencies(int32_t rot_dim, double theta, double factor, doub
  *   inv_freq   (device) fp64 [rot_dim / 2], finite, >= 0, below 2^63.
  *   head_dim   a multiple of 16, up to 512; rot_dim a multiple of 16 up to head_dim.
  *   flags      NVFP4_ROPE_*; other bits: NVFP4_ERR_SHAPE.  amplitude finite.
- * n_tokens = 0 is allowed (nothing is launched).
  */
 nvfp4_status rope_apply(const uint16_t *x, int64_t x_stride, int32_t n_tokens, int32_t n_heads, int32_t head_dim,
                         const int32_t *positions, const double *inv_freq, int32_t rot_dim, float amplitude,

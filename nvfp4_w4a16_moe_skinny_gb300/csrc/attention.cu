@@ -71,7 +71,8 @@ nvfp4_status paged_attention(const nvfp4_kv_cache* cache, const nvfp4_batch* bat
                              int32_t window, uint16_t* out, int64_t out_stride, float* lse, void* ws, size_t ws_bytes,
                              cudaStream_t stream) {
   if (const nvfp4_status st = check_cache(cache)) return st;
-  if (!batch || !q || !out || !batch->cu_tokens || !batch->kv_len || !batch->page_table) return NVFP4_ERR_NULL;
+  if (!batch || (n_tokens != 0 && (!q || !out)) || !batch->cu_tokens) return NVFP4_ERR_NULL;
+  if (batch->n_seqs != 0 && (!batch->kv_len || !batch->page_table)) return NVFP4_ERR_NULL;
   const int kv = cache->n_kv_heads, dim = cache->head_dim;
   if (!attn_sizes_ok(n_tokens, batch->n_seqs, batch->max_new, n_heads, kv, dim, batch->max_pages, cache->page_size))
     return NVFP4_ERR_SHAPE;

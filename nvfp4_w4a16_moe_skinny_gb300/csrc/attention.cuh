@@ -1316,7 +1316,7 @@ inline bool attn_rows_ok(int n_tokens, int n_seqs, int max_new, int n_heads, int
 inline bool attn_sizes_ok(int n_tokens, int n_seqs, int max_new, int n_heads, int n_kv_heads, int head_dim,
                           int max_pages, int page_size) {
   // key positions are counted in 32 bits
-  return attn_rows_ok(n_tokens, n_seqs, max_new, n_heads, n_kv_heads, head_dim) && max_pages >= 1 &&
+  return attn_rows_ok(n_tokens, n_seqs, max_new, n_heads, n_kv_heads, head_dim) && (max_pages >= 1 || n_seqs == 0) &&
          static_cast<int64_t>(max_pages) * page_size < (int64_t{1} << 30);
 }
 

@@ -220,11 +220,11 @@ nvfp4_status launch_rope(RopeJob p, bool e4m3, cudaStream_t stream) {
   return launched();
 }
 
-nvfp4_status check_rotation(int dim, const int32_t* positions, const double* inv_freq, int rot, float amplitude,
-                            int flags, int allowed) {
+nvfp4_status check_rotation(int n_tokens, int dim, const int32_t* positions, const double* inv_freq, int rot,
+                            float amplitude, int flags, int allowed) {
   if (flags & ~allowed) return NVFP4_ERR_SHAPE;
   if (rot < 0 || (rot % 16) || rot > dim || !std::isfinite(amplitude)) return NVFP4_ERR_SHAPE;
-  if (rot > 0 && (!positions || !inv_freq)) return NVFP4_ERR_NULL;
+  if (rot > 0 && ((!positions && n_tokens != 0) || !inv_freq)) return NVFP4_ERR_NULL;
   if (rot > 0 && (!aligned(positions, 4) || !aligned(inv_freq, 8))) return NVFP4_ERR_ALIGN;
   return NVFP4_OK;
 }
@@ -263,12 +263,12 @@ nvfp4_status rope_frequencies(int32_t rot_dim, double theta, double factor, doub
 nvfp4_status rope_apply(const uint16_t* x, int64_t x_stride, int32_t n_tokens, int32_t n_heads, int32_t head_dim,
                         const int32_t* positions, const double* inv_freq, int32_t rot_dim, float amplitude,
                         int32_t flags, uint16_t* y, int64_t y_stride, cudaStream_t stream) {
-  if (!x || !y) return NVFP4_ERR_NULL;
+  if (n_tokens != 0 && (!x || !y)) return NVFP4_ERR_NULL;
   if (n_tokens < 0 || n_heads < 1 || head_dim < 16 || head_dim > 512 || (head_dim % 16) || rot_dim < 16)
     return NVFP4_ERR_SHAPE;
   if (const nvfp4_status st = check_rows(x, x_stride, n_heads, head_dim)) return st;
   if (const nvfp4_status st = check_rows(y, y_stride, n_heads, head_dim)) return st;
-  if (const nvfp4_status st = check_rotation(head_dim, positions, inv_freq, rot_dim, amplitude, flags,
+  if (const nvfp4_status st = check_rotation(n_tokens, head_dim, positions, inv_freq, rot_dim, amplitude, flags,
                                              NVFP4_ROPE_INTERLEAVED | NVFP4_ROPE_INVERSE))
     return st;
   RopeJob p{};
@@ -285,7 +285,7 @@ nvfp4_status kv_append(const nvfp4_kv_cache* cache, const uint16_t* k, int64_t k
                        const double* inv_freq, int32_t rot_dim, float amplitude, int32_t flags, const uint16_t* q,
                        int64_t q_stride, int32_t n_heads, uint16_t* q_out, int64_t q_out_stride, cudaStream_t stream) {
   if (const nvfp4_status st = check_cache(cache)) return st;
-  if (!k || !v || !slots || (q && !q_out) || (!q && q_out)) return NVFP4_ERR_NULL;
+  if (n_tokens != 0 && (!k || !v || !slots || (q && !q_out) || (!q && q_out))) return NVFP4_ERR_NULL;
   if (n_tokens < 0 || (q && n_heads < 1)) return NVFP4_ERR_SHAPE;
   if (!aligned(slots, 8)) return NVFP4_ERR_ALIGN;
   if (const nvfp4_status st = check_rows(k, k_stride, cache->n_kv_heads, cache->head_dim)) return st;
@@ -294,7 +294,7 @@ nvfp4_status kv_append(const nvfp4_kv_cache* cache, const uint16_t* k, int64_t k
     if (const nvfp4_status st = check_rows(q, q_stride, n_heads, cache->head_dim)) return st;
     if (const nvfp4_status st = check_rows(q_out, q_out_stride, n_heads, cache->head_dim)) return st;
   }
-  if (const nvfp4_status st = check_rotation(cache->head_dim, positions, inv_freq, rot_dim, amplitude, flags,
+  if (const nvfp4_status st = check_rotation(n_tokens, cache->head_dim, positions, inv_freq, rot_dim, amplitude, flags,
                                              NVFP4_ROPE_INTERLEAVED))
     return st;
   RopeJob p{};
