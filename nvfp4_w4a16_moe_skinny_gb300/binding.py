@@ -90,6 +90,12 @@ def _need(ok: bool, what: str):
         raise ValueError(what)
 
 
+def _need_int32(value: int, what: str):
+    """ctypes cuts an integer to the 32 bits of its parameter without a word."""
+    if not -2 ** 31 <= value < 2 ** 31:
+        raise ValueError(f"{what}: beyond 32 bits")
+
+
 class KVCache:
     """A paged key/value cache on the GPU: pools [num_pages, n_kv_heads, page_size, head_dim] of bf16, or of
     float8_e4m3fn holding value / scale with fp32 scales per kv head (None: ones).  Pages may be strided (k and v
@@ -131,6 +137,7 @@ class Batch:
         for x in (cu_tokens, kv_len, page_table):
             _need(x.dtype == torch.int32 and x.is_contiguous() and x.is_cuda and x.device == kv_len.device,
                   "cu_tokens, kv_len, page_table: contiguous int32 on one GPU")
+        _need_int32(max_new, "max_new")
         self.cu_tokens, self.kv_len, self.page_table, self.max_new = cu_tokens, kv_len, page_table, int(max_new)
         self.n_seqs, self.device = n, kv_len.device
         self.c = CBatch(cu_tokens.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), n, page_table.shape[1],
@@ -522,6 +529,7 @@ class Library:
         """Radians a position for each rotated pair, fp64 [rot_dim / 2] (on `device`, if given).  factor > 1 stretches
         them: all of them (trained_context 0), or those that make fewer than `fast` turns over the trained context,
         wholly below `slow` turns."""
+        _need_int32(rot_dim, "rot_dim")
         out = torch.empty((max(0, rot_dim) // 2,), dtype=torch.float64)
         self._check("rope_frequencies", self.lib.rope_frequencies(rot_dim, theta, factor, trained_context, slow, fast,
                                                                   out.data_ptr() or None))
@@ -606,6 +614,7 @@ class Library:
         tokens, heads, dim = shape
         if dim != cache.head_dim or batch.device != dev:
             raise ValueError("q: [tokens, heads, head_dim] of the cache; the batch on its GPU")
+        _need_int32(window, "window")
         if out is None:
             out = _empty(shape, torch.bfloat16, dev, stream)
             out_stride = heads * dim

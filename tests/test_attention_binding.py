@@ -93,3 +93,19 @@ def test_calls_elsewhere_are_refused(fake, device, s):
         with pytest.raises(ValueError):
             call()
     assert fake.lib.launches() == []
+
+
+@pytest.mark.parametrize("value", [2 ** 31, 2 ** 32, 2 ** 32 + 100, -2 ** 31 - 1])
+def test_sizes_beyond_32_bits_are_refused(fake, value):
+    """The library takes them as int32: a window of 2^32 + 100 must not become one of 100, nor a bound on the new
+    tokens of 2^32 one of none."""
+    q, k = Tensor((4, 8, 64), BF16, "cuda:0"), Tensor((4, 8, 64), BF16, "cuda:0")
+    cache = types.SimpleNamespace(device=q.device, n_kv_heads=2, head_dim=64, ref=None, k=k, v=k, k_scale=None, v_scale=None)
+    batch = types.SimpleNamespace(device=q.device, n_seqs=1, max_new=4, ref=None, cu_tokens=k, kv_len=k, page_table=k)
+    with pytest.raises(ValueError):
+        fake.paged_attention(q, cache, batch, window=value, out=k, stream=stream())
+    with pytest.raises(ValueError):
+        binding.Batch(Tensor((2,), I32, "cuda:0"), Tensor((1,), I32, "cuda:0"), Tensor((1, 1), I32, "cuda:0"), value)
+    with pytest.raises(ValueError):
+        fake.rope_frequencies(value)
+    assert fake.lib.launches() == []
