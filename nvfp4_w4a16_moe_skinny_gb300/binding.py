@@ -250,6 +250,14 @@ def _on_current(device, stream):
         raise ValueError("stream: of another GPU than the tensors")
 
 
+def _is_capturing(stream) -> bool:
+    """Whether the stream of a call (None: the current one) is being captured into a graph."""
+    if stream is None:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _empty(shape, dtype, device, stream):
     """An output, allocated on the stream that writes it: memory that another stream's work may still use is not
     written before that work is done."""
@@ -654,13 +662,14 @@ class Library:
         and dies with the graph and whose counters are cleared at every replay."""
         key = (device.index, raw)
         cur = self._attention_ws.get(key)
-        if cur is not None and cur[2] >= nbytes and not torch.cuda.is_current_stream_capturing():
+        capturing = _is_capturing(stream)
+        if cur is not None and cur[2] >= nbytes and not capturing:
             return cur
         with torch.cuda.stream(torch.cuda.current_stream(device) if stream is None else stream):
             ws = torch.empty(max(nbytes, COUNTER_BYTES), dtype=torch.uint8, device=device)
             ws[:COUNTER_BYTES].zero_()
             cur = (ws, ws.data_ptr(), ws.numel())
-            if not torch.cuda.is_current_stream_capturing():
+            if not capturing:
                 self._attention_ws[key] = cur
         return cur
 
