@@ -514,6 +514,13 @@ __device__ __forceinline__ uint32_t nonfinite_mask(uint32_t v) {
   return (m >> 15) * 0xffffu;
 }
 
+// bf16 values of q for a scale of zero: zeros, and NaN for infinities and NaN (0 * inf is NaN), so
+// that the products carry 0 * NaN from both sides into the logits.
+__device__ __forceinline__ uint4 zero_or_nan(uint4 v) {
+  return make_uint4(nonfinite_mask<false>(v.x), nonfinite_mask<false>(v.y), nonfinite_mask<false>(v.z),
+                    nonfinite_mask<false>(v.w));
+}
+
 // ------------------------------------------------------------------ tile geometry
 
 // CTAs of the split kernel on one SM.  Two hide more of each other's waits: 64 sequences of up
@@ -795,11 +802,15 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, a
       const int rr = w.t.row0 + min(r, w.t.rows - 1);
       const int tk = div_by(p.by_group, rr), hd = w.h * p.group + rr - tk * p.group;
       const uint16_t* q = p.q + (w.s.tok0 + tk) * p.q_stride + static_cast<int64_t>(hd) * kDim;
-      const bool zero = r >= w.t.rows || p.scale == 0.f;
+      const bool zero = r >= w.t.rows;
       uint4 v[kDim / 64];
 #pragma unroll
       for (int c = 0; c < kDim / 64; ++c)
         v[c] = zero ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(q + 64 * c + 8 * (lane & 7));
+      if (p.scale == 0.f) {
+#pragma unroll
+        for (int c = 0; c < kDim / 64; ++c) v[c] = zero_or_nan(v[c]);
+      }
       const uint32_t sign = p.scale < 0.f ? 0x80008000u : 0u;  // a negative scale turns q's sign
       if constexpr (!kFp8) {
 #pragma unroll

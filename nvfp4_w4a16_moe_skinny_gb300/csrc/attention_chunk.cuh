@@ -623,6 +623,13 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
     // Returns the factor that undoes the scaling.
     const auto hand_q = [&]() {
       asm volatile("cp.async.wait_group 0;" ::: "memory");
+      if (p.scale == 0.f) {
+#pragma unroll 1
+        for (int c = 0; c < kDim / 8; ++c) {
+          const uint32_t at = q_at + g * T::kQB + umma_offset(128, row, c);
+          sts128(at, zero_or_nan(lds128(at)));
+        }
+      }
       float back = 1.0f;
       if constexpr (kFp8) {
         float amax = 0.f;
@@ -695,7 +702,7 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
         const uint32_t s_at = tmem + lane_at + T::kSCol + sb * kKeys;
         const int key0 = (first + j) * kKeys;
         const bool partly = __any_sync(0xffffffffu, key0 + kKeys > see_hi || key0 < see_lo);
-        if (partly || capped || p.scale == 0.f) {
+        if (partly || capped) {
           // in TMEM, before the rest reads it: two paths of tanh over a whole row would cost every
           // other call registers (a prompt of 4,096 tokens 140 us instead of 137)
 #pragma unroll 1
@@ -703,8 +710,6 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
             float x[32], high = 0.f;
             tmem_ld32(x, s_at + c);
             tmem_loaded(x);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = p.scale == 0.f ? 0.f : x[i];
             if (capped) {
 #pragma unroll
               for (int i = 0; i < 32; ++i) x[i] *= unit, high = fmaxf(high, fabsf(x[i]));
