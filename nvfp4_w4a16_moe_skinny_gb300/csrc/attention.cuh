@@ -607,6 +607,28 @@ __device__ __forceinline__ uint4 clean_codes(uint4 v, bool seen, bool& noted) {
   return make_uint4(v.x & ~(a * 0xffu), v.y & ~(b * 0xffu), v.z & ~(c * 0xffu), v.w & ~(d * 0xffu));
 }
 
+// Tiles of this CTA out of whose V an infinity or NaN was taken.  Tiles are counted over all items; `last` is one past
+// the last such tile, and a slot holds the same for the tiles that fall on it.  Entries only
+// grow: one that a later tile has overwritten says yes for an earlier one too, which then is looked
+// at without need, and nothing has to be cleared between items.
+struct NotedTiles {
+  static constexpr int kSlots = 64;
+  uint32_t last, slot[kSlots];
+  __device__ __forceinline__ void clear(int i) {  // by threads 0 .. kSlots
+    if (i < kSlots)
+      slot[i] = 0;
+    else if (i == kSlots)
+      last = 0;
+  }
+  __device__ __forceinline__ void note(uint32_t t) {
+    *static_cast<volatile uint32_t*>(&slot[t % kSlots]) = t + 1;  // (warps are less than kSlots tiles apart)
+    atomicMax(&last, t + 1);                                      // a slower warp may note the tile before
+  }
+  // one answer for the warp: another one may be noting a later tile meanwhile
+  __device__ __forceinline__ bool any_since(uint32_t t) const volatile { return __any_sync(0xffffffffu, last > t); }
+  __device__ __forceinline__ bool at(uint32_t t) const volatile { return __any_sync(0xffffffffu, slot[t % kSlots] > t); }
+};
+
 // Element offset of a key's first value of kv head h, and one value of a pool.
 __device__ __forceinline__ int64_t value_at(const AttnJob& p, int page, int h, int key, int dim) {
   return page * p.page_stride +
@@ -621,6 +643,22 @@ __device__ __forceinline__ float pool_value(const void* pool, int64_t at) {
   } else {
     return bf16_bits_to_f32(*(static_cast<const uint16_t*>(pool) + at));
   }
+}
+
+// Whether kValues values of a pool from element `at` on (16-byte aligned) hold an infinity or NaN.
+template <bool kFp8, int kValues>
+__device__ __forceinline__ bool holds_nonfinite(const void* pool, int64_t at) {
+  constexpr int kEl = kFp8 ? 1 : 2;
+  const uint4* v = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(pool) + at * kEl);
+  bool noted = false;
+#pragma unroll 4
+  for (int i = 0; i < kValues * kEl / 16; ++i) {
+    if constexpr (kFp8)
+      clean_codes(v[i], true, noted);
+    else
+      clean_chunk<false>(v[i], true, noted);
+  }
+  return noted;
 }
 
 __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
@@ -672,15 +710,15 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, a
   uint64_t* empty = full + T::kStages;                 // [stages]
   RangeScratch* scratch = reinterpret_cast<RangeScratch*>(empty + T::kStages);
   float* q_back = reinterpret_cast<float*>(scratch + 1);  // [kRows] undoes the scaling of a row of Q
-  // an infinity or NaN was taken out of V, in this CTA's items so far
-  volatile int* noted_flag = reinterpret_cast<volatile int*>(q_back + T::kRows);
+  NotedTiles* const noted_tiles = reinterpret_cast<NotedTiles*>(q_back + T::kRows);
+  static_assert(2 * 6 * sizeof(uint64_t) + sizeof(RangeScratch) + 64 * sizeof(float) + sizeof(NotedTiles) <= 1024, "tail");
 
   const int warp = static_cast<int>(uniform(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < T::kStages; ++i) mbar_init(full + i, 1), mbar_init(empty + i, T::kConsumers);
-    *noted_flag = 0;
     fence_mbar_init();
   }
+  noted_tiles->clear(threadIdx.x);
   pdl_wait();
   pdl_launch_dependents();
   __syncthreads();
@@ -989,7 +1027,7 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, a
             else
               sts128(a, clean_chunk<false>(lds128(a), seen, noted));
           }
-          if (noted) *noted_flag = 1;
+          if (noted) noted_tiles->note(round * T::kStages + st);
           fence_proxy_async_smem();  // the stage's next copy comes after these writes
           __syncwarp();
         }
@@ -1029,28 +1067,43 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, a
     }
 
     // ---- infinities and NaN that were taken out of V, to the rows that see them
-    // (warps that share a slice may each have found it clean already: the flag tells)
+    // (warps that share a slice may each have found it clean already: the note tells)
     if constexpr (kRW > 1) asm volatile("bar.sync 1, %0;" ::"n"(T::kConsumers * 32) : "memory");
-    if (*noted_flag) {
+    const volatile NotedTiles* const notes = noted_tiles;
+    const uint32_t unit0 = round * T::kStages + st - pc.n;  // this item's first unit
+    if (notes->any_since(unit0)) {
       for (int i = 0; i < pc.n; ++i) {
         const int key0 = (pc.first + i) * T::kKeys + kw * T::kSlice;
-        if (!partly_seen(kr, key0, T::kSlice)) continue;
-        for (int key = max(key0, kr.any_lo); key < min(key0 + T::kSlice, kr.any_hi); ++key) {
-          const int page = __ldg(p.table + static_cast<int64_t>(w.b) * p.max_pages + (key >> p.page_log2));
-          if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.num_pages)) continue;
-          const int64_t at = value_at(p, page, w.h, key, kDim);
+        if (!notes->at(unit0 + i) || !partly_seen(kr, key0, T::kSlice)) continue;
+        // each lane looks at one key, then all of them at those that hold any
+        const int hi = min(key0 + T::kSlice, kr.any_hi);
+#pragma unroll 1
+        for (int k0 = max(key0, kr.any_lo); k0 < hi; k0 += 32) {
+          int64_t mine = 0;
+          bool holds = false;
+          if (k0 + lane < hi) {
+            const int page = __ldg(p.table + static_cast<int64_t>(w.b) * p.max_pages + ((k0 + lane) >> p.page_log2));
+            mine = value_at(p, page, w.h, k0 + lane, kDim);
+            holds = static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages) &&
+                    holds_nonfinite<kFp8, kDim>(p.v_pool, mine);
+          }
+#pragma unroll 1
+          for (unsigned left = __ballot_sync(0xffffffffu, holds); left; left &= left - 1) {
+            const int who = __ffs(left) - 1, key = k0 + who;
+            const int64_t at = __shfl_sync(0xffffffffu, mine, who);
 #pragma unroll
-          for (int j = 0; j < kDT; ++j)
+            for (int j = 0; j < kDT; ++j)
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              // the column of acc[j][x] (E4M3: see the store below)
-              const int col = kFp8 ? 16 * (j / 2) + 4 * t4 + 2 * x + (j & 1) : 8 * j + 2 * t4 + x;
-              const float v = pool_value<kFp8>(p.v_pool, at + col);
-              if (isfinite(v)) continue;
+              for (int x = 0; x < 2; ++x) {
+                // the column of acc[j][x] (E4M3: see the store below)
+                const int col = kFp8 ? 16 * (j / 2) + 4 * t4 + 2 * x + (j & 1) : 8 * j + 2 * t4 + x;
+                const float v = pool_value<kFp8>(p.v_pool, at + col);
+                if (isfinite(v)) continue;
 #pragma unroll
-              for (int y = 0; y < 2; ++y)
-                if (key <= pos[y] && key < w.s.len && (p.window <= 0 || key > pos[y] - p.window)) acc[j][2 * y + x] += v;
-            }
+                for (int y = 0; y < 2; ++y)
+                  if (key <= pos[y] && key < w.s.len && (p.window <= 0 || key > pos[y] - p.window)) acc[j][2 * y + x] += v;
+              }
+          }
         }
       }
     }
