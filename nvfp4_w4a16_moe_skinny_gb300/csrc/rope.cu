@@ -66,8 +66,12 @@ __device__ __forceinline__ void angle_of(const RopeJob& p, int pos, int pair, fl
   // becomes fp32, so that it has 24 of them near the axes too (a slow pair at position 1 turns by 2^-30)
   const uint32_t quarter = static_cast<uint32_t>((t + (1ull << 61)) >> 62);
   const int64_t rest = static_cast<int64_t>(t - (static_cast<uint64_t>(quarter) << 62));
+  // |rest| from its halves: a conversion of 64 bits is longer (small calls 2.75 us against 2.65, the long prompt 46.3 against 46.0)
+  const uint64_t size = rest < 0 ? -static_cast<uint64_t>(rest) : static_cast<uint64_t>(rest);
+  const float half_turns = fmaf(__uint2float_rn(static_cast<uint32_t>(size >> 32)), 0x1p-31f,
+                                __uint2float_rn(static_cast<uint32_t>(size)) * 0x1p-63f);
   float sr, cr;
-  sincospif(__ll2float_rn(rest) * 0x1p-63f, &sr, &cr);
+  sincospif(rest < 0 ? -half_turns : half_turns, &sr, &cr);
   const bool swap = quarter & 1;
   const float cc = swap ? sr : cr, ss = swap ? cr : sr;
   c = (quarter == 1 || quarter == 2) ? -cc : cc;

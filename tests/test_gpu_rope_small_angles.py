@@ -2,7 +2,7 @@
 result where the other value of the pair is zero.
 
 Bound.  x_b = 0: y_b = x_a sin t.  The frequency as a 64-bit fraction of a turn is off by less than 2^-63 of a turn a
-position, the rest by fp32 roundings: the fraction's 2^-24, its scaling exact, sin 2^-22 (two units), product 2^-24; with the
+position, the rest by fp32 roundings: the fraction's 2^-23, its scaling exact, sin 2^-22 (two units), product 2^-24; with the
 amplitude's 2^-24 below 2^-21 of the value together.  Then bf16, 2^-8."""
 
 import math
