@@ -536,8 +536,9 @@ nvfp4_status rope_apply(const uint16_t *x, int64_t x_stride, int32_t n_tokens, i
  * Append to a paged cache: token t's keys, rotated as by rope_apply, and values
  * go to slot slots[t] = page * page_size + offset of every kv head; with q, the
  * queries are rotated in the same launch.  An E4M3 cache gets the code nearest to
- * value * (1 / scale), product and reciprocal in fp32 (ties to even, saturating at
- * 448; NaN stays NaN), rounded to 8 bits once, from the fp32 rotation.
+ * value * (1 / scale), product and reciprocal rounded to fp32 (for every positive
+ * scale, subnormal ones too; ties to even, saturating at 448; NaN stays NaN), then
+ * to 8 bits once, from the fp32 rotation.
  *   k, v       (device) rows of n_kv_heads heads, strides k_stride and v_stride.
  *   slots      (device) int64 [n_tokens]; a negative slot skips its token's cache
  *              rows (padding); one past the pool is skipped and sets bit 2 of the

@@ -98,11 +98,27 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return v;
 }
 
-// Eight values times r as E4M3 codes, nearest-even, saturating at 448 (NaN stays NaN).
-// r is the fp32 reciprocal of the head's scale: a product is off by at most 2^-23 of the quotient, which
-// moves a code only where the quotient is that near to the middle of two.  (A division a value
-// took 36.3 us instead of 33.0 for 8,191 tokens of 8 kv and 32 query heads.)
-__device__ __forceinline__ uint2 pack8_e4m3(const float (&f)[8], float r) {
+// The reciprocal of a head's scale for products with values.  Those of scales near the ends of fp32 are not
+// fp32's (the reciprocal of a subnormal is infinite, and zero times that NaN): there the scale, and
+// with it the values, are first multiplied by `unit`, 2^64 or 2^-64.
+struct HeadScale {
+  float unit, inverse;
+};
+__device__ __forceinline__ HeadScale head_scale(float s) {
+  const float unit = s < 0x1p-60f ? 0x1p64f : (s > 0x1p60f ? 0x1p-64f : 1.0f);
+  return {unit, __frcp_rn(s * unit)};
+}
+
+// Eight values times the reciprocal of their head's scale as E4M3 codes, nearest-even, saturating at 448 (NaN
+// stays NaN).  The reciprocal is rounded to fp32 once: a product is off by at most 2^-23 of the quotient, which
+// moves a code only where the quotient is that near to the middle of two.  (For 8,191 tokens of 8 kv and 32 query
+// heads a division a value took 36.3 us instead of 33.0, the rounded quotient by the product's remainder 34.2.)
+__device__ __forceinline__ uint2 pack8_e4m3(float (&f)[8], const HeadScale s) {
+  if (s.unit != 1.0f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] *= s.unit;
+  }
+  const float r = s.inverse;
   uint2 v;
   v.x = f32x2_to_e4m3x2(f[0] * r, f[1] * r) | f32x2_to_e4m3x2(f[2] * r, f[3] * r) << 16;
   v.y = f32x2_to_e4m3x2(f[4] * r, f[5] * r) | f32x2_to_e4m3x2(f[6] * r, f[7] * r) << 16;
@@ -194,7 +210,7 @@ __global__ void __launch_bounds__(kRopeThreads, 8) rope_kernel(const RopeJob p) 
         }
       }
       if (kE4M3 && kind > 0) {
-        const float sc = p.scale[kind - 1] ? __frcp_rn(__ldg(p.scale[kind - 1] + h)) : 1.0f;
+        const HeadScale sc = head_scale(p.scale[kind - 1] ? __ldg(p.scale[kind - 1] + h) : 1.0f);
         *reinterpret_cast<uint2*>(p.cache[kind - 1] + o + a) = pack8_e4m3(fa, sc);
         *reinterpret_cast<uint2*>(p.cache[kind - 1] + o + b) = pack8_e4m3(fb, sc);
       } else {
