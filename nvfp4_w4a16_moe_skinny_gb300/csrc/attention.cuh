@@ -747,7 +747,7 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, a
     const uint32_t bytes = 2u << piece_log2 << log2c(kDim * T::kEl);
     int st = 0;
     uint32_t round = 0;
-    for (long long u = u0; u < u1;) {
+    for (long long u = u0; u < u1 && !ran_out;) {
       walk_to(p, w, u, kTiling);
       const Share pc = share_at(w, u, u0, u1, blockIdx.x, kTiling);
       u = pc.end;
@@ -760,7 +760,8 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, a
       for (int i = 0; i < n; ++i) {
         const int later = lane < pieces && i + 1 < n
                               ? piece_page(p, table, (pc.first + i + 1) * pieces + lane, piece_log2, w.t) : -1;
-        if (round > 0 && !mbar_wait_warp(empty + st, (round - 1) & 1)) return;
+        ran_out = round > 0 && !mbar_wait_warp(empty + st, (round - 1) & 1);
+        if (ran_out) break;
         const uint32_t bar = smem_addr(full + st);
         const uint32_t all = bytes * __popc(__ballot_sync(0xffffffffu, page >= 0));
         int at[kMostPieces];  // all pieces' pages first, then the copies back to back
@@ -783,6 +784,10 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, a
         if (++st == T::kStages) st = 0, ++round;
       }
     }
+    // the CTA's shared memory is its own until its last copies have landed, whatever ran out (bounded)
+    const uint32_t issued = round * T::kStages + st;
+    for (uint32_t i = issued > T::kStages ? issued - T::kStages : 0; i < issued; ++i)
+      (void)mbar_wait_warp(full + i % T::kStages, i / T::kStages & 1);
     return;
   }
 

@@ -434,8 +434,8 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
       const int piece_log2 = min(p.page_log2, log2c(kKeys));
       constexpr int kMostPieces = kKeys / 16;
       const int pieces = kKeys >> piece_log2;  // of a tile: at most kMostPieces
-      uint32_t raw = 0;
-      for (long long u = u0; u < u1;) {
+      uint32_t raw = 0, k_tiles = 0, v_tiles = 0;  // copied so far
+      for (long long u = u0; u < u1 && !ran_out;) {
         walk_to(p, w, u, kTiling);
         const Share pc = share_at(w, u, u0, u1, blockIdx.x, kTiling);
         u = pc.end;
@@ -459,7 +459,6 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
             if (RawRing::reused(raw)) NVFP4_WAIT(bars->raw_empty + st, RawRing::before(raw));
             full = bars->raw_full + st;
             dst = raw_at + st * T::kRawB;
-            ++raw;
           } else {
             const uint32_t st = is_v ? VRing::at(g) : KRing::at(g);
             if (is_v ? VRing::reused(g) : KRing::reused(g))
@@ -467,6 +466,9 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
             full = (is_v ? bars->v_full : bars->k_full) + st;
             dst = (is_v ? v_at : k_at) + st * T::kTileB;
           }
+          if (ran_out) break;  // the place is still in use: no further copies
+          ++raw;
+          (is_v ? v_tiles : k_tiles) = g + 1;
           if (!is_v && c > 0) {
             page_v = page_k, page_k = page_next;
             page_next = look_up(j + 1);
@@ -494,6 +496,16 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
         }
         nt += n;
       }
+      // the CTA's shared memory is its own until its last copies have landed, whatever ran out (bounded)
+      const auto land = [&](uint64_t* full, uint32_t tiles, auto ring) {
+        using R = decltype(ring);
+        for (uint32_t t = R::reused(tiles) ? tiles - R::kStages : 0; t < tiles; ++t)
+          (void)mbar_wait_warp(full + R::at(t), R::phase(t));
+      };
+      if constexpr (kFp8)
+        land(bars->raw_full, raw, RawRing{});
+      else
+        land(bars->k_full, k_tiles, KRing{}), land(bars->v_full, v_tiles, VRing{});
     } else if (warp == 1) {
       // ------------------------------------------------------------ MMA issue
       const uint32_t id_qk = umma_idesc(!kFp8, false, kKeys, 128) | (p.scale < 0.f ? kNegateA : 0u);
@@ -992,7 +1004,7 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
     }
   }
 #undef NVFP4_WAIT
-  if (ran_out) {  // copies may still be under way: give them time to land before the CTA ends
+  if (ran_out) {  // products may still be under way: give them time to end before TMEM is given back
     for (int i = 0; i < 1000; ++i) __nanosleep(1000);
   }
   __syncthreads();
