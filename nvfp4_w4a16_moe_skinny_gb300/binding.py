@@ -238,8 +238,7 @@ def _raw_stream(stream, device) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
-def _current_device() -> int:
-    return torch._C._cuda_getDevice()
+_current_device = getattr(torch._C, "_cuda_getDevice", None)  # (a CPU build of torch can still import the package)
 
 
 def _on_current(device, stream):
@@ -251,9 +250,7 @@ def _on_current(device, stream):
 
 
 def _is_capturing(stream) -> bool:
-    """Whether the stream of a call (None: the current one) is being captured into a graph."""
-    if stream is None:
-        return torch.cuda.is_current_stream_capturing()
+    """Whether a stream is being captured into a graph."""
     with torch.cuda.stream(stream):
         return torch.cuda.is_current_stream_capturing()
 
@@ -548,7 +545,8 @@ class Library:
         """Rotary positions on the first 2 * len(inv_freq) values of every head of x [tokens, heads, dim]; out may be x.
         inverse rotates back, which is the gradient's way through the rotation."""
         dev = x.device
-        _on_current(dev, stream)
+        if dev.index != _current_device() or stream is not None:
+            _on_current(dev, stream)
         stride = _rows(x, "x", dev)
         tokens, heads, dim = x.shape
         pairs = inv_freq.shape[0]
@@ -575,7 +573,8 @@ class Library:
         """Write k (rotated, if inv_freq is given) and v [tokens, n_kv_heads, dim] to slots int64 [tokens] of the cache
         (negative: skipped) and return the rotated q (None without q); q_out may be q."""
         dev = cache.device
-        _on_current(dev, stream)
+        if dev.index != _current_device() or stream is not None:
+            _on_current(dev, stream)
         tokens, heads, dim = k.shape
         _need(k.shape == v.shape and heads == cache.n_kv_heads and dim == cache.head_dim,
               "k and v: [tokens, n_kv_heads, head_dim] of the cache")
@@ -616,13 +615,15 @@ class Library:
         """Attention of the batch's new tokens q [tokens, heads, dim] over their sequences' cached keys (scale: 1 /
         sqrt(dim)): out, or (out, log-sum-exp fp32 [tokens, heads]) with with_lse."""
         dev = cache.device
-        _on_current(dev, stream)
+        if dev.index != _current_device() or stream is not None:
+            _on_current(dev, stream)
         stride = _rows(q, "q", dev)
         shape = q.shape
         tokens, heads, dim = shape
         if dim != cache.head_dim or batch.device != dev:
             raise ValueError("q: [tokens, heads, head_dim] of the cache; the batch on its GPU")
-        _need_int32(window, "window")
+        if not -2 ** 31 <= window < 2 ** 31:
+            raise ValueError("window: beyond 32 bits")
         if out is None:
             out = _empty(shape, torch.bfloat16, dev, stream)
             out_stride = heads * dim
@@ -662,7 +663,7 @@ class Library:
         and dies with the graph and whose counters are cleared at every replay."""
         key = (device.index, raw)
         cur = self._attention_ws.get(key)
-        capturing = _is_capturing(stream)
+        capturing = torch.cuda.is_current_stream_capturing() if stream is None else _is_capturing(stream)
         if cur is not None and cur[2] >= nbytes and not capturing:
             return cur
         with torch.cuda.stream(torch.cuda.current_stream(device) if stream is None else stream):
