@@ -96,10 +96,12 @@ struct KvMaps {
 // compiled for both.
 //
 // Tiling of one kernel: rows of a row tile, keys of a unit, and what starting and
-// finishing an item costs, counted in units (the ranges are balanced with it).
+// finishing an item counts for, in units (the ranges are balanced with it).
 // `snap`: a range boundary that falls this close to an item's end moves there, so that no
 // item is split for a few units.
-// `least`: units that a range holds at least, as far as there are any.
+// `least`: a call of fewer units than this for each CTA takes one range for every `least` units
+// or part of them, equal ones, so that a range may hold a little less (nine units by fours: three ranges
+// of three).
 // What they are worth is measured at AttnTile and ChunkTile.
 struct Tiling {
   int rows, keys, over, snap, least;

@@ -60,7 +60,7 @@ struct ChunkTile {
   // step; five more add 2 to 5% to the shorter prompts, two more make it 168).  Boundaries that move up to four
   // units instead of one: 512 tokens in a window of 1,024 keys of 256 values 34.6 us against 35.9, but
   // E4M3 tiles of 128 values, whose units are slow, balance better with one (2,048 tokens 50.8 against 56.7).
-  // Ranges of at least kLeast units: 31 tokens over 2,000 keys 25.7 us against 32.8, 33.6 against 46.9 for 256 values.
+  // Ranges of kLeast units or a little less where there are few: 31 tokens over 2,000 keys 25.7 us against 32.8, 33.6 against 46.9 for 256 values.
   static constexpr int kOver = 4, kSnap = kFp8 && kDim == 128 ? 1 : 4, kLeast = kDim == 256 ? 8 : 4;  // in units (Tiling)
   static constexpr __host__ __device__ Tiling tiling() { return {kRows, kKeys, kOver, kSnap, kLeast}; }
   // warps that make tiles fit: two beside the copies and the products, or (E4M3 and 128 values:

@@ -4,6 +4,7 @@
 // orders of arrival.  (The kernels find a range's first item by a scan over the sequences,
 // find_range; here the items are numbered one after the other.)
 #include <algorithm>
+#include <new>
 #include <vector>
 
 #include "attention_chunk.cuh"
@@ -99,9 +100,8 @@ struct Arrivals {
 
 using namespace nvfp4;
 
-extern "C" nvfp4_status paged_attention_plan_check(const nvfp4_kv_cache* cache, const nvfp4_batch* batch,
-                                                   int32_t n_tokens, int32_t n_heads, int32_t window, int32_t orders,
-                                                   int32_t* out, int32_t out_len) {
+static nvfp4_status plan_check(const nvfp4_kv_cache* cache, const nvfp4_batch* batch, int32_t n_tokens, int32_t n_heads,
+                               int32_t window, int32_t orders, int32_t* out, int32_t out_len) {
   if (const nvfp4_status st = check_cache(cache)) return st;
   if (!batch || !out || !batch->cu_tokens || !batch->kv_len) return NVFP4_ERR_NULL;
   const int kv = cache->n_kv_heads, dim = cache->head_dim;
@@ -198,4 +198,14 @@ extern "C" nvfp4_status paged_attention_plan_check(const nvfp4_kv_cache* cache, 
   out[7] = fits(unjoined);
   out[8] = shape.chunk ? 1 : 0;
   return NVFP4_OK;
+}
+
+extern "C" nvfp4_status paged_attention_plan_check(const nvfp4_kv_cache* cache, const nvfp4_batch* batch,
+                                                   int32_t n_tokens, int32_t n_heads, int32_t window, int32_t orders,
+                                                   int32_t* out, int32_t out_len) {
+  try {
+    return plan_check(cache, batch, n_tokens, n_heads, window, orders, out, out_len);
+  } catch (const std::bad_alloc&) {  // (nothing else is thrown)
+    return NVFP4_ERR_WORKSPACE;
+  }
 }
