@@ -28,10 +28,11 @@
 // product and noted; the rows that see it add it at the end from the pool itself.
 //
 // What bounds it.  The last 2,048 tokens over 32,768 keys (32 heads on 8 kv heads of 128 bf16
-// values, 1.07 PFLOP) take 703 us, 1.51 PFLOP/s or 79% of cuBLAS's burst rate (768 us under the power cap in a
+// values, 1.07 PFLOP) take 695 us, 1.53 PFLOP/s or 80% of cuBLAS's burst rate (768 us under the power cap in a
 // long loop, 81% of its sustained one): the softmax of a tile, 128 exponentials a thread, is as
-// long as its products.  Short of that, items: a prompt of 4,096 tokens is 256 of them over 152
-// CTAs, each with Q to fetch, a first S to wait for and O to write (133 us, 54%).  Heads of 64 values halve the
+// long as its products.  Short of that, items: a prompt of 4,096 tokens is 512 of them over 152
+// CTAs, each with Q to fetch, a first S to wait for and O to write (131 us, 55%; its units alone would take
+// 93 at that long chunk's price of one, so that an item's start and end are about 10 us).  Heads of 64 values halve the
 // products of a tile but not its softmax.  Heads of 256 values are bound by L2: every CTA reads its own tiles.
 #pragma once
 

@@ -1,8 +1,8 @@
 // Rotary positions (rope_apply) and the append to a paged key/value cache with
 // the rotation on the way (kv_append): one kernel over (token, head, chunk of 16
 // values), bound by memory at prompt sizes and by the launch at decode sizes: 16,381 tokens of 32
-// heads of 128 values (268 MB) take 45.8 us, 5.9 TB/s or 86% of the rate of a plain copy, 8,191 tokens
-// quantized into a cache with their queries 32.7 us (83%); 16 tokens 2.9 us.
+// heads of 128 values (268 MB) take 46.0 us, 5.8 TB/s or 86% of the rate of a plain copy, 8,191 tokens
+// quantized into a cache with their queries 33.0 us (82%); 16 tokens 2.9 us.
 //
 // The angle of pair i at position p is p * w_i radians.  In fp32 that product
 // loses the angle at far positions (2^-24 of 131,072 radians is 0.008), so it is
