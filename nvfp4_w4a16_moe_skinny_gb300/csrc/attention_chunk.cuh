@@ -307,6 +307,7 @@ __device__ __noinline__ void restore_nonfinite(uint32_t o_at, const volatile Not
         }
       }
     }
+    __syncwarp();  // the rows that see a key have gone their own way: TMEM is written by a whole warp
     tmem_st32(o_at + c, o);
   }
   tmem_wait_st();
