@@ -118,7 +118,9 @@ uint32_t nvfp4_layout_version(void);
 
 /*
  * Device error word: bit 0 = a kernel's bounded wait ran out of time; bit 2 = a
- * page id or cache slot outside its pool was met (kv_append, paged_attention).
+ * page id or cache slot outside its pool was met (kv_append, paged_attention); bit
+ * 3 = kv_assign or kv_accept met a request, tree or path that they could not serve
+ * whole (see there).
  * Reads the word (synchronously, on the current device) into *out and clears it
  * if `clear` is nonzero.
  */
@@ -552,6 +554,141 @@ nvfp4_status kv_append(const nvfp4_kv_cache *cache, const uint16_t *k, int64_t k
                        int64_t v_stride, int32_t n_tokens, const int64_t *slots, const int32_t *positions,
                        const double *inv_freq, int32_t rot_dim, float amplitude, int32_t flags, const uint16_t *q,
                        int64_t q_stride, int32_t n_heads, uint16_t *q_out, int64_t q_out_stride, cudaStream_t stream);
+
+/*
+ * Norms of queries and keys for each head, with rotary positions in the same pass:
+ *   n_i = x_i * w_i / sqrt(mean(x^2) + eps),   y = rope(n) as by rope_apply
+ * over each head of head_dim values, with one weight vector for all heads of q and one
+ * for those of k.  Sums, root and products are fp32 (heads whose mean square leaves
+ * fp32's middle are scaled by a power of two first), each value rounded once.
+ *   q_weight, k_weight  (device) [head_dim], both of weight_dtype.
+ *   eps                 finite, >= 0 (a head of zeros with eps = 0 gives NaN).
+ */
+#define NVFP4_NORM_BF16 0u
+#define NVFP4_NORM_FP32 1u
+typedef struct {
+  const void *q_weight;
+  const void *k_weight;
+  uint32_t weight_dtype;
+  float eps;
+} nvfp4_qk_norm;
+
+/*
+ *   q, q_out   (device) rows of n_heads heads; q_out may be q (same stride).
+ *   k, k_out   (device) the same with n_kv_heads heads; n_kv_heads = 0: no keys (the
+ *              pointers and k_weight may be NULL).
+ *   head_dim, positions, inv_freq, rot_dim, amplitude, flags: as rope_apply; rot_dim =
+ *              0 rotates nothing.  NVFP4_ROPE_INVERSE is not accepted.
+ */
+nvfp4_status qk_norm_rope(const nvfp4_qk_norm *norm, const uint16_t *q, int64_t q_stride, int32_t n_heads,
+                          const uint16_t *k, int64_t k_stride, int32_t n_kv_heads, int32_t n_tokens, int32_t head_dim,
+                          const int32_t *positions, const double *inv_freq, int32_t rot_dim, float amplitude,
+                          int32_t flags, uint16_t *q_out, int64_t q_out_stride, uint16_t *k_out, int64_t k_out_stride,
+                          cudaStream_t stream);
+
+/*
+ * The way back through qk_norm_rope, for q and k as they went in: with u the gradient
+ * dq (dk) rotated back, z = u * w and r = 1 / sqrt(mean(x^2) + eps),
+ *   dq_out = r * (z - x r * mean(z x r)),   dq_weight = sum over tokens and heads of u x r.
+ * The sums over tokens are taken in fp32, block by block in an order that depends on the sizes
+ * alone: the same call gives the same bits.
+ *   dq, dk           (device) rows, the gradients of qk_norm_rope's outputs.
+ *   dq_out, dk_out   (device) rows; dq_out may be dq or q, dk_out dk or k (same strides).
+ *   dq_weight, dk_weight  (device) fp32 [head_dim], written (zeros without tokens).
+ *   ws               (device) qk_norm_rope_workspace_bytes() bytes, 16-byte aligned; any contents.
+ */
+size_t qk_norm_rope_workspace_bytes(int32_t n_tokens, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim);
+nvfp4_status qk_norm_rope_backward(const nvfp4_qk_norm *norm, const uint16_t *dq, int64_t dq_stride, const uint16_t *q,
+                                   int64_t q_stride, int32_t n_heads, const uint16_t *dk, int64_t dk_stride,
+                                   const uint16_t *k, int64_t k_stride, int32_t n_kv_heads, int32_t n_tokens,
+                                   int32_t head_dim, const int32_t *positions, const double *inv_freq, int32_t rot_dim,
+                                   float amplitude, int32_t flags, uint16_t *dq_out, int64_t dq_out_stride,
+                                   uint16_t *dk_out, int64_t dk_out_stride, float *dq_weight, float *dk_weight, void *ws,
+                                   size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * kv_append with the keys (and, with q, the queries) normalised as by qk_norm_rope
+ * before their rotation, in the same launch.  norm->q_weight may be NULL without q.
+ */
+nvfp4_status kv_append_norm(const nvfp4_kv_cache *cache, const nvfp4_qk_norm *norm, const uint16_t *k, int64_t k_stride,
+                            const uint16_t *v, int64_t v_stride, int32_t n_tokens, const int64_t *slots,
+                            const int32_t *positions, const double *inv_freq, int32_t rot_dim, float amplitude,
+                            int32_t flags, const uint16_t *q, int64_t q_stride, int32_t n_heads, uint16_t *q_out,
+                            int64_t q_out_stride, cudaStream_t stream);
+
+/*
+ * The page tables of a batch of requests, and the free pages (all device, caller-owned;
+ * kv_assign updates the contents).
+ *   page_table  int32 [n_seqs, max_pages]: entries [0, held[b]) of row b are its pages.
+ *   held        int32 [n_seqs].
+ *   free_pages  int32 [num_free]: a stack, its first free_count[0] entries are free pages.
+ *   page_size   as in nvfp4_kv_cache.  n_seqs at most 16,384; max_pages * page_size < 2^30.
+ */
+typedef struct {
+  int32_t *page_table;
+  int32_t *held;
+  int32_t *free_pages;
+  int32_t *free_count;
+  int32_t n_seqs;
+  int32_t max_pages;
+  int32_t page_size;
+  int32_t num_free;
+} nvfp4_page_table;
+
+/*
+ * What a step's calls read (all device, caller-owned, written by kv_assign).
+ *   slots      int64 [n_tokens] and positions int32 [n_tokens] for kv_append.
+ *   cu_tokens  int32 [n_seqs + 1] and kv_len int32 [n_seqs] for nvfp4_batch.
+ *   masks      int64 [n_tokens, words] for tree_attention, or NULL.  words at most 64.
+ */
+typedef struct {
+  int64_t *slots;
+  int32_t *positions;
+  int32_t *cu_tokens;
+  int32_t *kv_len;
+  int64_t *masks;
+  int32_t n_tokens;
+  int32_t words;
+} nvfp4_step;
+
+/*
+ * A step's bookkeeping on the device, in one launch: request b has kv_len[b] committed
+ * keys and asks for new_tokens[b] more (0: idle; < 0: finished).
+ *   cu_tokens, kv_len   the running sums of the new tokens, and the lengths with them.
+ *   page_table, held    grown to hold them; the pages come off the top of the free list,
+ *                       request by request in order.  A finished request's pages go on top of what
+ *                       is left, in order (for later calls), its held and kv_len become 0.
+ *   slots, positions    of request b's i-th new token: its place in the cache, and kv_len[b] + i.
+ *                       Rows past the last new token get slot -1 (skipped by kv_append), position 0.
+ *   parents  int32 [n_tokens] or NULL: the new tokens are drafted trees, parents[row] the index
+ *            among its request's new tokens of the one before it, less than its own, -1 after the
+ *            committed keys.  Positions are then kv_len[b] + depth (a root's depth is 0), and bit x
+ *            of a row's mask (bit x % 64 of word x / 64) is set for its own index and its
+ *            ancestors'; rows past the last one get zeros.  At most 64 * words tokens a request.
+ * kv_len and step->kv_len may be the same; no other two arrays may overlap.
+ * What cannot be served sets bit 3 of the device error word: new tokens past n_tokens rows are
+ * dropped (cu_tokens and kv_len count those that have rows); tokens past max_pages * page_size, or
+ * for which no free page is left, get slot -1 (kv_len counts them); a parent out of range counts as -1, a
+ * token's ancestors past 64 * words are left out; a finished request's pages past num_free are dropped.
+ */
+nvfp4_status kv_assign(const nvfp4_page_table *pages, const int32_t *kv_len, const int32_t *new_tokens,
+                       const int32_t *parents, const nvfp4_step *step, cudaStream_t stream);
+
+/*
+ * Keeps an accepted path of every sequence's new tokens: with n new tokens (the last n of
+ * kv_len[b] keys) and ctx = kv_len[b] - n, the cache rows of key ctx + path[d] move to key ctx + d for
+ * d = 0, 1, ... in every kv head of k and v, and kv_len_out[b] = ctx + the path's length.  The rows
+ * keep their rotation: a token at depth d of its tree was rotated to position ctx + d.
+ *   batch       cu_tokens, kv_len and page_table are read.  n_seqs at most 65,535.
+ *   paths       (device) int32 [n_seqs, path_len], indices among the sequence's new tokens, ascending
+ *               (a tree's parents come before their children); the first negative entry ends a
+ *               path.  path_len at most 1,024.  An entry that does not ascend or is not below n ends
+ *               the path too, and sets bit 3 of the device error word; so does a row without a page, which
+ *               is not moved.
+ *   kv_len_out  (device) int32 [n_seqs], not batch->kv_len.
+ */
+nvfp4_status kv_accept(const nvfp4_kv_cache *cache, const nvfp4_batch *batch, const int32_t *paths, int32_t path_len,
+                       int32_t *kv_len_out, cudaStream_t stream);
 
 /*
  * Attention of every sequence's new tokens over its keys in the paged cache.

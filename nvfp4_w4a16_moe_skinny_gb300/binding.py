@@ -22,6 +22,8 @@ NVFP4_KV_BF16 = 0
 NVFP4_KV_E4M3 = 1
 NVFP4_ROPE_INTERLEAVED = 1
 NVFP4_ROPE_INVERSE = 2
+NVFP4_NORM_BF16 = 0
+NVFP4_NORM_FP32 = 1
 KV_MAPS_BYTES = 1024
 COUNTER_BYTES = 4096  # arrival counters at the start of an attention workspace
 LAYOUT_VERSION = 2
@@ -37,7 +39,8 @@ EXPORTS = (
     "lm_head_sample", "moe_route_topk_ex", "lm_head_sample_ex", "nvfp4_plan_check", "moe_router_logits",
     "nvfp4_repack_host", "nvfp4_quantize_act", "nvfp4_gemm_w4a4", "lm_head_argmax_w4a4", "moe_forward", "nvfp4_selftest_wait_timeout",
     "rope_frequencies", "rope_apply", "kv_append", "kv_cache_maps", "paged_attention_workspace_bytes", "paged_attention",
-    "paged_attention_plan_check",
+    "paged_attention_plan_check", "qk_norm_rope", "qk_norm_rope_workspace_bytes", "qk_norm_rope_backward",
+    "kv_append_norm", "kv_assign", "kv_accept",
 )
 
 
@@ -78,6 +81,23 @@ class CKVCache(ctypes.Structure):
                 ("v_scale", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("num_pages", ctypes.c_int32),
                 ("page_size", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("dtype", ctypes.c_uint32), ("maps", ctypes.c_void_p)]
+
+
+class CQKNorm(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("weight_dtype", ctypes.c_uint32),
+                ("eps", ctypes.c_float)]
+
+
+class CPageTable(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("held", ctypes.c_void_p), ("free_pages", ctypes.c_void_p),
+                ("free_count", ctypes.c_void_p), ("n_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("num_free", ctypes.c_int32)]
+
+
+class CStep(ctypes.Structure):
+    _fields_ = [("slots", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("cu_tokens", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("masks", ctypes.c_void_p), ("n_tokens", ctypes.c_int32),
+                ("words", ctypes.c_int32)]
 
 
 class CBatch(ctypes.Structure):
@@ -145,6 +165,49 @@ class Batch:
         self.ref = ctypes.byref(self.c)
 
 
+class PageTable:
+    """The page tables of a batch of requests and the free pages, updated by `kv_assign`: page_table int32
+    [n_seqs, max_pages], held int32 [n_seqs] (pages of each row in use), free_pages int32 [num_pages] (a stack) and
+    free_count int32 [1].  Keeps its tensors alive."""
+
+    def __init__(self, page_table: torch.Tensor, held: torch.Tensor, free_pages: torch.Tensor, free_count: torch.Tensor,
+                 page_size: int):
+        _need(page_table.dim() == 2 and held.shape == (page_table.shape[0],) and free_pages.dim() == 1
+              and free_count.shape == (1,), "page_table [n_seqs, max_pages], held [n_seqs], free_pages [num], free_count [1]")
+        for x in (page_table, held, free_pages, free_count):
+            _need(x.dtype == torch.int32 and x.is_contiguous() and x.is_cuda and x.device == page_table.device,
+                  "page_table, held, free_pages, free_count: contiguous int32 on one GPU")
+        _need_int32(page_size, "page_size")
+        self.page_table, self.held, self.free_pages, self.free_count = page_table, held, free_pages, free_count
+        self.page_size, self.n_seqs, self.device = int(page_size), page_table.shape[0], page_table.device
+        self.c = CPageTable(page_table.data_ptr(), held.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(),
+                            self.n_seqs, page_table.shape[1], self.page_size, free_pages.shape[0])
+        self.ref = ctypes.byref(self.c)
+
+
+class Step:
+    """What a step's calls read, written by `kv_assign` for up to `tokens` new tokens of n_seqs requests: slots int64
+    [tokens], positions int32 [tokens], cu_tokens int32 [n_seqs + 1], kv_len int32 [n_seqs] and, for drafted trees of up
+    to 64 * words tokens, masks int64 [tokens, words].  Make it once and use it step after step (a captured graph has to)."""
+
+    def __init__(self, n_seqs: int, tokens: int, words: int = 0, device="cuda"):
+        _need_int32(tokens, "tokens")
+        self.slots = torch.full((tokens,), -1, dtype=torch.int64, device=device)
+        self.positions = torch.zeros((tokens,), dtype=torch.int32, device=device)
+        self.cu_tokens = torch.zeros((n_seqs + 1,), dtype=torch.int32, device=device)
+        self.kv_len = torch.zeros((n_seqs,), dtype=torch.int32, device=device)
+        self.masks = torch.zeros((tokens, words), dtype=torch.int64, device=device)
+        self.n_seqs, self.tokens, self.words, self.device = n_seqs, tokens, words, self.slots.device
+        _need(self.device.type == "cuda", "device: a GPU")
+        self.c = CStep(self.slots.data_ptr(), self.positions.data_ptr(), self.cu_tokens.data_ptr(),
+                       self.kv_len.data_ptr(), self.masks.data_ptr() or None, tokens, words)
+        self.ref = ctypes.byref(self.c)
+
+    def batch(self, page_table: torch.Tensor, max_new: int) -> Batch:
+        """The attention batch of this step's sequences (made once, like the step)."""
+        return Batch(self.cu_tokens, self.kv_len, page_table, max_new)
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
 _SZ = ctypes.c_size_t
@@ -209,6 +272,20 @@ def _sig(lib):
     lib.kv_append.argtypes = [_P, _P, _I64, _P, _I64, _I, _P, _P, _P, _I, ctypes.c_float, _I, _P, _I64, _I, _P, _I64,
                               _P]
     lib.kv_append.restype = ctypes.c_int
+    rotation = [_P, _P, _I, ctypes.c_float, _I]
+    lib.kv_append_norm.argtypes = [_P, _P, _P, _I64, _P, _I64, _I, _P, *rotation, _P, _I64, _I, _P, _I64, _P]
+    lib.kv_append_norm.restype = ctypes.c_int
+    lib.qk_norm_rope.argtypes = [_P, _P, _I64, _I, _P, _I64, _I, _I, _I, *rotation, _P, _I64, _P, _I64, _P]
+    lib.qk_norm_rope.restype = ctypes.c_int
+    lib.qk_norm_rope_workspace_bytes.restype = _SZ
+    lib.qk_norm_rope_workspace_bytes.argtypes = [_I] * 4
+    lib.qk_norm_rope_backward.argtypes = [_P, _P, _I64, _P, _I64, _I, _P, _I64, _P, _I64, _I, _I, _I, *rotation, _P,
+                                          _I64, _P, _I64, _P, _P, _P, _SZ, _P]
+    lib.qk_norm_rope_backward.restype = ctypes.c_int
+    lib.kv_assign.argtypes = [_P] * 6
+    lib.kv_assign.restype = ctypes.c_int
+    lib.kv_accept.argtypes = [_P, _P, _P, _I, _P, _P]
+    lib.kv_accept.restype = ctypes.c_int
     lib.kv_cache_maps.argtypes = [_P, _P]
     lib.kv_cache_maps.restype = ctypes.c_int
     lib.paged_attention_workspace_bytes.restype = _SZ
@@ -280,6 +357,20 @@ def _rows(x: torch.Tensor, what: str, device) -> int:
         if one == 1 and (head == shape[2] or shape[1] == 1):
             return row if shape[0] > 1 else shape[1] * shape[2]
     raise ValueError(f"{what}: bf16 [tokens, heads, dim] on the call's GPU, the heads of a token contiguous")
+
+
+def _norm(q_norm, k_norm, dim: int, eps: float, device) -> CQKNorm:
+    """The norm weights of a call: bf16 or fp32 [dim], both of one type (None: not used)."""
+    kind = None
+    for w in (q_norm, k_norm):
+        if w is None:
+            continue
+        if w.shape != (dim,) or w.device != device or w.stride(0) != 1 or w.dtype is not (kind or w.dtype):
+            raise ValueError("q_norm and k_norm: contiguous [head_dim] on the call's GPU, of one type")
+        kind = w.dtype
+    if kind is not torch.bfloat16 and kind is not torch.float32:
+        raise ValueError("q_norm and k_norm: bf16 or fp32")
+    return CQKNorm(_ptr(q_norm), _ptr(k_norm), NVFP4_NORM_BF16 if kind is torch.bfloat16 else NVFP4_NORM_FP32, eps)
 
 
 def _index(x: torch.Tensor, n: int, dtype, what: str, device) -> int:
@@ -569,9 +660,11 @@ class Library:
 
     def kv_append(self, cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
                   positions: torch.Tensor = None, inv_freq: torch.Tensor = None, interleaved: bool = False,
-                  amplitude: float = 1.0, q: torch.Tensor = None, q_out: torch.Tensor = None, stream=None):
+                  amplitude: float = 1.0, q: torch.Tensor = None, q_out: torch.Tensor = None, stream=None,
+                  q_norm: torch.Tensor = None, k_norm: torch.Tensor = None, eps: float = 1e-6):
         """Write k (rotated, if inv_freq is given) and v [tokens, n_kv_heads, dim] to slots int64 [tokens] of the cache
-        (negative: skipped) and return the rotated q (None without q); q_out may be q."""
+        (negative: skipped) and return the rotated q (None without q); q_out may be q.  With k_norm (and, with q, q_norm),
+        bf16 or fp32 [dim], every head of k and q is normalised first: x / sqrt(mean(x^2) + eps) times the weights."""
         dev = cache.device
         if dev.index != _current_device() or stream is not None:
             _on_current(dev, stream)
@@ -598,6 +691,20 @@ class Library:
                 _need(q_out.shape == q.shape, "q_out: the shape of q")
                 out_stride = _rows(q_out, "q_out", dev)
             out_ptr = q_out.data_ptr()
+        if k_norm is not None or q_norm is not None:
+            _need(k_norm is not None and (q_norm is None) == (q is None), "k_norm, and q_norm where there is a q")
+            norm = _norm(q_norm, k_norm, dim, eps, dev)
+            st = self.lib.kv_append_norm(
+                cache.ref, ctypes.byref(norm), k.data_ptr(), _rows(k, "k", dev), v.data_ptr(), _rows(v, "v", dev), tokens,
+                _index(slots, tokens, torch.int64, "slots", dev), pos, freq, rot, amplitude,
+                NVFP4_ROPE_INTERLEAVED if interleaved else 0, q_ptr, q_stride, q_heads, out_ptr, out_stride,
+                _raw_stream(stream, dev))
+            if st:
+                raise NVFP4Error("kv_append_norm", st)
+            if stream is not None:
+                _used_on(stream, k, v, slots, positions, inv_freq, q, q_out, cache.k, cache.v, cache.k_scale,
+                         cache.v_scale, q_norm, k_norm)
+            return q_out
         st = self.lib.kv_append(
             cache.ref, k.data_ptr(), _rows(k, "k", dev), v.data_ptr(), _rows(v, "v", dev), tokens,
             _index(slots, tokens, torch.int64, "slots", dev), pos, freq, rot, amplitude,
@@ -608,6 +715,149 @@ class Library:
         if stream is not None:
             _used_on(stream, k, v, slots, positions, inv_freq, q, q_out, cache.k, cache.v, cache.k_scale, cache.v_scale)
         return q_out
+
+    def _rotation(self, tokens, positions, inv_freq, dev):
+        """positions, inv_freq and rot_dim of a call (inv_freq None: nothing is rotated)."""
+        if inv_freq is None:
+            return None, None, 0
+        _need(positions is not None, "positions are needed with inv_freq")
+        pairs = inv_freq.shape[0]
+        return (_index(positions, tokens, torch.int32, "positions", dev),
+                _index(inv_freq, pairs, torch.float64, "inv_freq", dev), 2 * pairs)
+
+    def _rows_out(self, out, like, what, dev, stream):
+        """An output of rows of heads (a new one, if none is given) and its stride."""
+        if out is None:
+            return _empty(like.shape, torch.bfloat16, dev, stream), like.shape[1] * like.shape[2]
+        _need(out.shape == like.shape, f"{what}: the shape of its input")
+        return out, _rows(out, what, dev)
+
+    def qk_norm_rope(self, q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
+                     q_norm: torch.Tensor, k_norm: torch.Tensor = None, eps: float = 1e-6, interleaved: bool = False,
+                     amplitude: float = 1.0, q_out: torch.Tensor = None, k_out: torch.Tensor = None, stream=None):
+        """Norms of queries and keys [tokens, heads, dim] for each head, x / sqrt(mean(x^2) + eps) times q_norm or k_norm
+        (bf16 or fp32 [dim]), and rotary positions as by rope_apply (none without inv_freq): (q, k).  k may be None;
+        q_out may be q, k_out k."""
+        dev = q.device
+        if dev.index != _current_device() or stream is not None:
+            _on_current(dev, stream)
+        q_stride = _rows(q, "q", dev)
+        tokens, heads, dim = q.shape
+        pos, freq, rot = self._rotation(tokens, positions, inv_freq, dev)
+        norm = _norm(q_norm, None if k is None else k_norm, dim, eps, dev)
+        q_out, q_out_stride = self._rows_out(q_out, q, "q_out", dev, stream)
+        k_ptr = k_out_ptr = None
+        kv = k_stride = k_out_stride = 0
+        if k is not None:
+            kv = k.shape[1]
+            _need(k.shape == (tokens, kv, dim) and kv > 0, "k: [tokens, heads, dim] with q's tokens and dim")
+            k_ptr, k_stride = k.data_ptr(), _rows(k, "k", dev)
+            k_out, k_out_stride = self._rows_out(k_out, k, "k_out", dev, stream)
+            k_out_ptr = k_out.data_ptr()
+        else:
+            _need(k_out is None, "k_out: without k")
+        st = self.lib.qk_norm_rope(
+            ctypes.byref(norm), q.data_ptr(), q_stride, heads, k_ptr, k_stride, kv, tokens, dim, pos, freq, rot, amplitude,
+            NVFP4_ROPE_INTERLEAVED if interleaved else 0, q_out.data_ptr(), q_out_stride, k_out_ptr, k_out_stride,
+            _raw_stream(stream, dev))
+        if st:
+            raise NVFP4Error("qk_norm_rope", st)
+        if stream is not None:
+            _used_on(stream, q, k, positions, inv_freq, q_norm, k_norm, q_out, k_out)
+        return q_out, k_out
+
+    def qk_norm_rope_backward(self, dq: torch.Tensor, dk: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
+                              positions: torch.Tensor, inv_freq: torch.Tensor, q_norm: torch.Tensor,
+                              k_norm: torch.Tensor = None, eps: float = 1e-6, interleaved: bool = False,
+                              amplitude: float = 1.0, dq_out: torch.Tensor = None, dk_out: torch.Tensor = None, stream=None):
+        """The gradients (dq, dk, dq_norm, dk_norm) of qk_norm_rope's inputs q and k (as they went in) and weights, from
+        those of its outputs; those of the weights are fp32 [dim].  k and dk may be None (then dk and dk_norm are); dq_out
+        may be dq or q, dk_out dk or k."""
+        dev = q.device
+        if dev.index != _current_device() or stream is not None:
+            _on_current(dev, stream)
+        q_stride = _rows(q, "q", dev)
+        tokens, heads, dim = q.shape
+        _need(dq.shape == q.shape and (k is None) == (dk is None), "dq and dk: the shapes of q and k")
+        pos, freq, rot = self._rotation(tokens, positions, inv_freq, dev)
+        norm = _norm(q_norm, None if k is None else k_norm, dim, eps, dev)
+        dq_out, dq_out_stride = self._rows_out(dq_out, q, "dq_out", dev, stream)
+        weights = _empty((1 if k is None else 2, dim), torch.float32, dev, stream)
+        k_ptr = dk_ptr = dk_out_ptr = dkn_ptr = None
+        kv = k_stride = dk_stride = dk_out_stride = 0
+        if k is not None:
+            kv = k.shape[1]
+            _need(k.shape == (tokens, kv, dim) and kv > 0 and dk.shape == k.shape, "k and dk: [tokens, heads, dim] with q's tokens and dim")
+            k_ptr, k_stride = k.data_ptr(), _rows(k, "k", dev)
+            dk_ptr, dk_stride = dk.data_ptr(), _rows(dk, "dk", dev)
+            dk_out, dk_out_stride = self._rows_out(dk_out, k, "dk_out", dev, stream)
+            dk_out_ptr, dkn_ptr = dk_out.data_ptr(), weights[1].data_ptr()
+        else:
+            _need(dk_out is None, "dk_out: without k")
+        raw = _raw_stream(stream, dev)
+        nbytes = self.lib.qk_norm_rope_workspace_bytes(tokens, heads, kv, dim)
+        # past the attention calls' arrival counters
+        ws, ws_ptr, ws_bytes = self._stream_workspace(COUNTER_BYTES + nbytes, dev, raw, stream)
+        st = self.lib.qk_norm_rope_backward(
+            ctypes.byref(norm), dq.data_ptr(), _rows(dq, "dq", dev), q.data_ptr(), q_stride, heads, dk_ptr, dk_stride, k_ptr,
+            k_stride, kv, tokens, dim, pos, freq, rot, amplitude, NVFP4_ROPE_INTERLEAVED if interleaved else 0,
+            dq_out.data_ptr(), dq_out_stride, dk_out_ptr, dk_out_stride, weights.data_ptr(), dkn_ptr,
+            ws_ptr + COUNTER_BYTES, ws_bytes - COUNTER_BYTES, raw)
+        if st:
+            raise NVFP4Error("qk_norm_rope_backward", st)
+        if stream is not None:
+            _used_on(stream, dq, dk, q, k, positions, inv_freq, q_norm, k_norm, dq_out, dk_out, weights)
+        return dq_out, dk_out, weights[0], weights[1] if k is not None else None
+
+    def kv_assign(self, pages: PageTable, kv_len: torch.Tensor, new_tokens: torch.Tensor, step: Step,
+                  parents: torch.Tensor = None, stream=None) -> Step:
+        """A step's page tables, slots, positions and lengths on the GPU: request b, with kv_len[b] committed keys, gets
+        room for new_tokens[b] more (0: idle, < 0: finished, its pages go back), int32 [n_seqs] each.  With parents int32
+        [step.tokens] the new tokens are trees: the index of each one's parent among its request's new tokens, below its
+        own, or -1; positions follow depth and step.masks holds the ancestors.  Returns step; kv_len may be step.kv_len.
+        What cannot be served (no free page, no row) gets slot -1 and sets bit 3 of device_error()."""
+        dev = pages.device
+        if dev.index != _current_device() or stream is not None:
+            _on_current(dev, stream)
+        n = pages.n_seqs
+        if step.n_seqs != n or step.device != dev:
+            raise ValueError("step: of the page table's requests, on its GPU")
+        up = None
+        if parents is not None:
+            if step.words < 1:
+                raise ValueError("step: without words for masks")
+            up = _index(parents, step.tokens, torch.int32, "parents", dev)
+        st = self.lib.kv_assign(pages.ref, _index(kv_len, n, torch.int32, "kv_len", dev),
+                                _index(new_tokens, n, torch.int32, "new_tokens", dev), up, step.ref,
+                                _raw_stream(stream, dev))
+        if st:
+            raise NVFP4Error("kv_assign", st)
+        if stream is not None:
+            _used_on(stream, pages.page_table, pages.held, pages.free_pages, pages.free_count, kv_len, new_tokens, parents,
+                     step.slots, step.positions, step.cu_tokens, step.kv_len, step.masks)
+        return step
+
+    def kv_accept(self, cache: KVCache, batch: Batch, paths: torch.Tensor, out: torch.Tensor = None,
+                  stream=None) -> torch.Tensor:
+        """Keep the accepted path of every sequence's new tokens: the cache rows of tokens paths[b] (int32 [n_seqs, most],
+        ascending indices among the sequence's new tokens, ended by a negative one) move next to each other behind its
+        context.  Returns the new lengths int32 [n_seqs] (`out`; not batch.kv_len)."""
+        dev = cache.device
+        if dev.index != _current_device() or stream is not None:
+            _on_current(dev, stream)
+        n = batch.n_seqs
+        if (paths.dim() != 2 or paths.shape[0] != n or paths.dtype is not torch.int32 or paths.device != dev
+                or not paths.is_contiguous() or batch.device != dev):
+            raise ValueError("paths: contiguous int32 [n_seqs, most] on the cache's GPU; the batch on it")
+        if out is None:
+            out = _empty((n,), torch.int32, dev, stream)
+        st = self.lib.kv_accept(cache.ref, batch.ref, paths.data_ptr(), paths.shape[1],
+                                _index(out, n, torch.int32, "out", dev), _raw_stream(stream, dev))
+        if st:
+            raise NVFP4Error("kv_accept", st)
+        if stream is not None:
+            _used_on(stream, cache.k, cache.v, batch.cu_tokens, batch.kv_len, batch.page_table, paths, out)
+        return out
 
     def paged_attention(self, q: torch.Tensor, cache: KVCache, batch: Batch, scale: float = None, softcap: float = 0.0,
                         window: int = 0, out: torch.Tensor = None, lse: torch.Tensor = None, with_lse: bool = False,
