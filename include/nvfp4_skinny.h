@@ -722,6 +722,21 @@ nvfp4_status paged_attention(const nvfp4_kv_cache *cache, const nvfp4_batch *bat
                              size_t ws_bytes, cudaStream_t stream);
 
 /*
+ * Attention of trees of drafted tokens: as paged_attention, but a new token sees every key
+ * before its sequence's new ones and, of the new ones, those that its mask says (in any order, its
+ * own not by itself): with n new tokens, key j < kv_len - n, and key kv_len - n + t where bit t of
+ * its mask (bit t % 64 of word t / 64) is set, t < n.  With window > 0 only the last `window` of
+ * the keys that it sees so: for the ancestors of a token, those less than `window` positions back.
+ *   masks  (device) int64 [n_tokens, words], as kv_assign writes them.
+ *   words  1 to 64; batch->max_new is at most 64 * words.
+ * The rest, and the workspace, as for paged_attention.
+ */
+nvfp4_status tree_attention(const nvfp4_kv_cache *cache, const nvfp4_batch *batch, const int64_t *masks, int32_t words,
+                            const uint16_t *q, int64_t q_stride, int32_t n_tokens, int32_t n_heads, float scale,
+                            float softcap, int32_t window, uint16_t *out, int64_t out_stride, float *lse, void *ws,
+                            size_t ws_bytes, cudaStream_t stream);
+
+/*
  * Host-side walk of the split that an attention call would make, through the
  * kernels' own arithmetic, for host-side checks (no device work; no CUDA call).
  *   cache, n_tokens, n_heads, window  as for paged_attention (pools are not read).
@@ -741,6 +756,11 @@ nvfp4_status paged_attention(const nvfp4_kv_cache *cache, const nvfp4_batch *bat
 nvfp4_status paged_attention_plan_check(const nvfp4_kv_cache *cache, const nvfp4_batch *batch, int32_t n_tokens,
                                         int32_t n_heads, int32_t window, int32_t orders, int32_t *out,
                                         int32_t out_len);
+
+/* The same for a tree_attention call. */
+nvfp4_status tree_attention_plan_check(const nvfp4_kv_cache *cache, const nvfp4_batch *batch, int32_t n_tokens,
+                                       int32_t n_heads, int32_t window, int32_t orders, int32_t *out,
+                                       int32_t out_len);
 
 /*
  * The launch plan a product would use, for host-side checks of the work

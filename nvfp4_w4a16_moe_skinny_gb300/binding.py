@@ -40,7 +40,7 @@ EXPORTS = (
     "nvfp4_repack_host", "nvfp4_quantize_act", "nvfp4_gemm_w4a4", "lm_head_argmax_w4a4", "moe_forward", "nvfp4_selftest_wait_timeout",
     "rope_frequencies", "rope_apply", "kv_append", "kv_cache_maps", "paged_attention_workspace_bytes", "paged_attention",
     "paged_attention_plan_check", "qk_norm_rope", "qk_norm_rope_workspace_bytes", "qk_norm_rope_backward",
-    "kv_append_norm", "kv_assign", "kv_accept",
+    "kv_append_norm", "kv_assign", "kv_accept", "tree_attention", "tree_attention_plan_check",
 )
 
 
@@ -293,6 +293,11 @@ def _sig(lib):
     lib.paged_attention.argtypes = [_P, _P, _P, _I64, _I, _I, ctypes.c_float, ctypes.c_float, _I, _P, _I64, _P, _P,
                                     _SZ, _P]
     lib.paged_attention.restype = ctypes.c_int
+    lib.tree_attention.argtypes = [_P, _P, _P, _I, _P, _I64, _I, _I, ctypes.c_float, ctypes.c_float, _I, _P, _I64, _P, _P,
+                                   _SZ, _P]
+    lib.tree_attention.restype = ctypes.c_int
+    lib.tree_attention_plan_check.argtypes = [_P, _P, _I, _I, _I, _I, ctypes.POINTER(ctypes.c_int32), _I]
+    lib.tree_attention_plan_check.restype = ctypes.c_int
     lib.paged_attention_plan_check.argtypes = [_P, _P, _I, _I, _I, _I, ctypes.POINTER(ctypes.c_int32), _I]
     lib.paged_attention_plan_check.restype = ctypes.c_int
     for name in ("nvfp4_quantize", "nvfp4_repack", "nvfp4_gemm", "moe_route_topk", "moe_ffn_grouped",
@@ -903,6 +908,56 @@ class Library:
             raise NVFP4Error("paged_attention", st)
         if stream is not None:
             _used_on(stream, q, out, lse, cache.k, cache.v, cache.k_scale, cache.v_scale, batch.cu_tokens, batch.kv_len,
+                     batch.page_table)
+        return (out, lse) if with_lse else out
+
+    def tree_attention(self, q: torch.Tensor, cache: KVCache, batch: Batch, masks: torch.Tensor, scale: float = None,
+                       softcap: float = 0.0, window: int = 0, out: torch.Tensor = None, lse: torch.Tensor = None,
+                       with_lse: bool = False, stream=None):
+        """paged_attention for trees of drafted tokens: a new token sees every key before its sequence's new ones and, of
+        the new ones, those whose bits are set in its row of masks, int64 [tokens, words] (kv_assign's; batch.max_new is at
+        most 64 * words); with a window the last `window` of these."""
+        dev = cache.device
+        if dev.index != _current_device() or stream is not None:
+            _on_current(dev, stream)
+        stride = _rows(q, "q", dev)
+        shape = q.shape
+        tokens, heads, dim = shape
+        if dim != cache.head_dim or batch.device != dev:
+            raise ValueError("q: [tokens, heads, head_dim] of the cache; the batch on its GPU")
+        if not -2 ** 31 <= window < 2 ** 31:
+            raise ValueError("window: beyond 32 bits")
+        if masks.dim() != 2 or masks.shape[0] != tokens or masks.dtype is not torch.int64 or masks.device != dev or not masks.is_contiguous():
+            raise ValueError("masks: contiguous int64 [tokens, words] on the call's GPU")
+        if out is None:
+            out = _empty(shape, torch.bfloat16, dev, stream)
+            out_stride = heads * dim
+        else:
+            _need(out.shape == shape, "out: the shape of q")
+            out_stride = _rows(out, "out", dev)
+        lse_ptr = None
+        if lse is not None:
+            _need(lse.shape == (tokens, heads) and lse.dtype is torch.float32 and lse.is_contiguous()
+                  and lse.device == dev, "lse: contiguous fp32 [tokens, heads]")
+            lse_ptr = lse.data_ptr()
+        elif with_lse:
+            lse = _empty((tokens, heads), torch.float32, dev, stream)
+            lse_ptr = lse.data_ptr()
+        raw = _raw_stream(stream, dev)
+        sizes = (tokens, batch.n_seqs, batch.max_new, heads, cache.n_kv_heads, dim)
+        nbytes = self._attention_bytes.get(sizes)
+        if nbytes is None:
+            if len(self._attention_bytes) > 4096:
+                self._attention_bytes.clear()
+            nbytes = self._attention_bytes[sizes] = self.lib.paged_attention_workspace_bytes(*sizes)
+        ws, ws_ptr, ws_bytes = self._stream_workspace(nbytes, dev, raw, stream)
+        st = self.lib.tree_attention(
+            cache.ref, batch.ref, masks.data_ptr(), masks.shape[1], q.data_ptr(), stride, tokens, heads, dim ** -0.5 if scale is None else scale, softcap,
+            window, out.data_ptr(), out_stride, lse_ptr, ws_ptr, ws_bytes, raw)
+        if st:
+            raise NVFP4Error("tree_attention", st)
+        if stream is not None:
+            _used_on(stream, masks, q, out, lse, cache.k, cache.v, cache.k_scale, cache.v_scale, batch.cu_tokens, batch.kv_len,
                      batch.page_table)
         return (out, lse) if with_lse else out
 

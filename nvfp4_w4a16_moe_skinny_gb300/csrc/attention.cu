@@ -1,4 +1,4 @@
-// paged_attention: argument checks, tensor maps of the cache, dispatch.
+// paged_attention and tree_attention: argument checks, tensor maps of the cache, dispatch.
 #include <algorithm>
 #include <cmath>
 
@@ -33,6 +33,59 @@ bool encode_pool_map(CUtensorMap* map, const nvfp4_kv_cache* c, void* base, int 
 bool encode_maps(KvMaps* maps, const nvfp4_kv_cache* c, const AttnShape& s) {
   const int box = std::min(c->page_size, s.box_keys);
   return encode_pool_map(&maps->k, c, c->k, box, !s.chunk) && encode_pool_map(&maps->v, c, c->v, box, !s.chunk);
+}
+
+template <bool kTree>
+nvfp4_status dispatch_dim(int dim, const AttnJob& p, const KvMaps& maps, bool fp8, const AttnShape& s, cudaStream_t stream) {
+  if (dim == 64) return dispatch_attention<64, kTree>(p, maps, fp8, s, stream);
+  if (dim == 128) return dispatch_attention<128, kTree>(p, maps, fp8, s, stream);
+  return dispatch_attention<256, kTree>(p, maps, fp8, s, stream);
+}
+
+// Attention of a batch's new tokens: causal (words 0), or by masks of `words` 64-bit words a token.
+nvfp4_status attend(const nvfp4_kv_cache* cache, const nvfp4_batch* batch, const int64_t* masks, int words,
+                    const uint16_t* q, int64_t q_stride, int32_t n_tokens, int32_t n_heads, float scale, float softcap,
+                    int32_t window, uint16_t* out, int64_t out_stride, float* lse, void* ws, size_t ws_bytes,
+                    cudaStream_t stream) {
+  if (const nvfp4_status st = check_cache(cache)) return st;
+  if (!batch || (n_tokens != 0 && (!q || !out)) || !batch->cu_tokens) return NVFP4_ERR_NULL;
+  if (batch->n_seqs != 0 && (!batch->kv_len || !batch->page_table)) return NVFP4_ERR_NULL;
+  const int kv = cache->n_kv_heads, dim = cache->head_dim;
+  if (!attn_sizes_ok(n_tokens, batch->n_seqs, batch->max_new, n_heads, kv, dim, batch->max_pages, cache->page_size))
+    return NVFP4_ERR_SHAPE;
+  if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.f || window < 0) return NVFP4_ERR_SHAPE;
+  if (const nvfp4_status st = check_rows(q, q_stride, n_heads, dim)) return st;
+  if (const nvfp4_status st = check_rows(out, out_stride, n_heads, dim)) return st;
+  if (!aligned(batch->cu_tokens, 4) || !aligned(batch->kv_len, 4) || !aligned(batch->page_table, 4) ||
+      !aligned(lse, 4) || !aligned(ws, 32))
+    return NVFP4_ERR_ALIGN;
+  if (!ws || ws_bytes < paged_attention_workspace_bytes(n_tokens, batch->n_seqs, batch->max_new, n_heads, kv, dim))
+    return NVFP4_ERR_WORKSPACE;
+  if (n_tokens == 0 || batch->n_seqs == 0 || batch->max_new == 0) return NVFP4_OK;
+
+  AttnJob p{};
+  p.cu = batch->cu_tokens, p.kv_len = batch->kv_len, p.table = batch->page_table;
+  p.n_seqs = batch->n_seqs, p.max_pages = batch->max_pages, p.n_tokens = n_tokens;
+  p.n_heads = n_heads, p.n_kv = kv, p.group = n_heads / kv, p.by_group = fast_div(n_heads / kv);
+  p.page_log2 = log2i(cache->page_size), p.num_pages = cache->num_pages;
+  p.q = q, p.q_stride = q_stride, p.out = out, p.out_stride = out_stride, p.lse = lse;
+  p.v_pool = cache->v, p.page_stride = cache->page_stride;
+  p.k_scale = cache->k_scale, p.v_scale = cache->v_scale;
+  p.scale = scale, p.softcap = softcap;
+  p.window = attn_window(window);
+  p.masks = reinterpret_cast<const uint32_t*>(masks), p.mask_words = 2 * words;
+  p.counters = static_cast<unsigned*>(ws);
+  p.split = reinterpret_cast<int4*>(static_cast<uint8_t*>(ws) + kAttnCounterBytes);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kAttnCounterBytes + kAttnSplitBytes);
+  const bool fp8 = cache->dtype == NVFP4_KV_E4M3;
+  const AttnShape s = attn_shape(dim, fp8, packed_rows(n_tokens, batch->max_new, n_heads, kv),
+                                 static_cast<int64_t>(batch->n_seqs) * kv);
+  KvMaps maps;
+  if (cache->maps)
+    maps = static_cast<const KvMaps*>(cache->maps)[s.maps];
+  else if (!encode_maps(&maps, cache, s))
+    return NVFP4_ERR_CUDA;
+  return words > 0 ? dispatch_dim<true>(dim, p, maps, fp8, s, stream) : dispatch_dim<false>(dim, p, maps, fp8, s, stream);
 }
 
 }  // namespace
@@ -70,46 +123,19 @@ nvfp4_status paged_attention(const nvfp4_kv_cache* cache, const nvfp4_batch* bat
                              int64_t q_stride, int32_t n_tokens, int32_t n_heads, float scale, float softcap,
                              int32_t window, uint16_t* out, int64_t out_stride, float* lse, void* ws, size_t ws_bytes,
                              cudaStream_t stream) {
-  if (const nvfp4_status st = check_cache(cache)) return st;
-  if (!batch || (n_tokens != 0 && (!q || !out)) || !batch->cu_tokens) return NVFP4_ERR_NULL;
-  if (batch->n_seqs != 0 && (!batch->kv_len || !batch->page_table)) return NVFP4_ERR_NULL;
-  const int kv = cache->n_kv_heads, dim = cache->head_dim;
-  if (!attn_sizes_ok(n_tokens, batch->n_seqs, batch->max_new, n_heads, kv, dim, batch->max_pages, cache->page_size))
-    return NVFP4_ERR_SHAPE;
-  if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.f || window < 0) return NVFP4_ERR_SHAPE;
-  if (const nvfp4_status st = check_rows(q, q_stride, n_heads, dim)) return st;
-  if (const nvfp4_status st = check_rows(out, out_stride, n_heads, dim)) return st;
-  if (!aligned(batch->cu_tokens, 4) || !aligned(batch->kv_len, 4) || !aligned(batch->page_table, 4) ||
-      !aligned(lse, 4) || !aligned(ws, 32))
-    return NVFP4_ERR_ALIGN;
-  if (!ws || ws_bytes < paged_attention_workspace_bytes(n_tokens, batch->n_seqs, batch->max_new, n_heads, kv, dim))
-    return NVFP4_ERR_WORKSPACE;
-  if (n_tokens == 0 || batch->n_seqs == 0 || batch->max_new == 0) return NVFP4_OK;
+  return attend(cache, batch, nullptr, 0, q, q_stride, n_tokens, n_heads, scale, softcap, window, out, out_stride, lse, ws,
+                ws_bytes, stream);
+}
 
-  AttnJob p{};
-  p.cu = batch->cu_tokens, p.kv_len = batch->kv_len, p.table = batch->page_table;
-  p.n_seqs = batch->n_seqs, p.max_pages = batch->max_pages, p.n_tokens = n_tokens;
-  p.n_heads = n_heads, p.n_kv = kv, p.group = n_heads / kv, p.by_group = fast_div(n_heads / kv);
-  p.page_log2 = log2i(cache->page_size), p.num_pages = cache->num_pages;
-  p.q = q, p.q_stride = q_stride, p.out = out, p.out_stride = out_stride, p.lse = lse;
-  p.v_pool = cache->v, p.page_stride = cache->page_stride;
-  p.k_scale = cache->k_scale, p.v_scale = cache->v_scale;
-  p.scale = scale, p.softcap = softcap;
-  p.window = attn_window(window);
-  p.counters = static_cast<unsigned*>(ws);
-  p.split = reinterpret_cast<int4*>(static_cast<uint8_t*>(ws) + kAttnCounterBytes);
-  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kAttnCounterBytes + kAttnSplitBytes);
-  const bool fp8 = cache->dtype == NVFP4_KV_E4M3;
-  const AttnShape s = attn_shape(dim, fp8, packed_rows(n_tokens, batch->max_new, n_heads, kv),
-                                 static_cast<int64_t>(batch->n_seqs) * kv);
-  KvMaps maps;
-  if (cache->maps)
-    maps = static_cast<const KvMaps*>(cache->maps)[s.maps];
-  else if (!encode_maps(&maps, cache, s))
-    return NVFP4_ERR_CUDA;
-  if (dim == 64) return dispatch_attention<64>(p, maps, fp8, s, stream);
-  if (dim == 128) return dispatch_attention<128>(p, maps, fp8, s, stream);
-  return dispatch_attention<256>(p, maps, fp8, s, stream);
+nvfp4_status tree_attention(const nvfp4_kv_cache* cache, const nvfp4_batch* batch, const int64_t* masks, int32_t words,
+                            const uint16_t* q, int64_t q_stride, int32_t n_tokens, int32_t n_heads, float scale,
+                            float softcap, int32_t window, uint16_t* out, int64_t out_stride, float* lse, void* ws,
+                            size_t ws_bytes, cudaStream_t stream) {
+  if (!batch || (n_tokens != 0 && !masks)) return NVFP4_ERR_NULL;
+  if (words < 1 || words > 64 || batch->max_new > 64 * words) return NVFP4_ERR_SHAPE;
+  if (!aligned(masks, 8)) return NVFP4_ERR_ALIGN;
+  return attend(cache, batch, masks, words, q, q_stride, n_tokens, n_heads, scale, softcap, window, out, out_stride, lse, ws,
+                ws_bytes, stream);
 }
 
 }  // extern "C"

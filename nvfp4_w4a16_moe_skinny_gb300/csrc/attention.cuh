@@ -84,6 +84,8 @@ struct AttnJob {
   unsigned* counters;  // arrivals at the join of each split item, by the range that holds its start
   float* part;         // shares: unnormalised sums, reference maxima and sums of weights of a row tile, two per CTA
   int4* split;         // the split kernel's split items, by the range that holds their start (split_item)
+  const uint32_t* masks;  // tree_attention: which new tokens each new token sees, mask_words 32-bit words a token
+  int mask_words;
 };
 
 struct KvMaps {
@@ -103,8 +105,11 @@ struct KvMaps {
 // or part of them, equal ones, so that a range may hold a little less (nine units by fours: three ranges
 // of three).
 // What they are worth is measured at AttnTile and ChunkTile.
+// `tree`: a token sees all keys before the new ones and, of those, what its mask says
+// (tree_attention); otherwise the keys up to its own.
 struct Tiling {
   int rows, keys, over, snap, least;
+  bool tree;
 };
 
 // Quotient of x < 2^31 by the divisor that `d` was made for (fast_div): a multiply by the
@@ -147,6 +152,13 @@ __host__ __device__ __forceinline__ RowTile row_tile(const AttnJob& p, const Seq
   RowTile t;
   t.row0 = rt * g.rows;
   t.rows = min(g.rows, s.rows - t.row0);
+  if (g.tree) {  // (a row sees its window's last keys: a mask of nothing, the context's)
+    t.hi = s.len;
+    t.lo = p.window > 0 ? min(max(max(s.len - s.n, 0) - p.window, 0), t.hi) : 0;
+    t.tile0 = t.lo / g.keys;
+    t.units = max(1, (t.hi + g.keys - 1) / g.keys - t.tile0);
+    return t;
+  }
   const int p0 = s.len - s.n + div_by(p.by_group, t.row0);
   const int p1 = s.len - s.n + div_by(p.by_group, t.row0 + t.rows - 1);
   t.hi = min(max(p1 + 1, 0), s.len);
@@ -427,6 +439,50 @@ __device__ __forceinline__ int4 split_item(const Walk& w, int c1) {
   return make_int4(c1 | w.t.rows << 9, w.h, w.t.row0, w.s.tok0);
 }
 
+// ------------------------------------------------------------------ trees
+
+// Bits [0, n) of a word.
+__device__ __forceinline__ uint32_t bits_below(int n) { return n >= 32 ? ~0u : (n <= 0 ? 0u : (1u << n) - 1); }
+
+// What a new token of a tree sees: keys [lo, ctx) of the context, and new token t (key ctx + t) where bit
+// t of its mask is set, t >= from.  With a window those are the last of the keys that the mask leaves.
+struct TreeRow {
+  const uint32_t* mask;
+  int words, ctx, n, lo, from;
+  __device__ __forceinline__ uint32_t word(int i) const {
+    return static_cast<unsigned>(i) < static_cast<unsigned>(words) ? __ldg(mask + i) : 0u;
+  }
+  // keys [key0, key0 + 32), a bit each
+  __device__ __forceinline__ uint32_t bits(int key0) const {
+    uint32_t m = bits_below(ctx - key0) & ~bits_below(lo - key0);
+    const int t0 = key0 - ctx;
+    if (t0 > -32)
+      m |= __funnelshift_r(word(t0 >> 5), word((t0 >> 5) + 1), t0 & 31) & bits_below(n - t0) & ~bits_below(from - t0);
+    return m;
+  }
+  __device__ __forceinline__ bool sees(int key) const { return bits(key) & 1; }
+};
+
+__device__ __forceinline__ TreeRow tree_row(const AttnJob& p, const Sequence& s, int tok) {
+  TreeRow r;
+  r.mask = p.masks + static_cast<int64_t>(s.tok0 + tok) * p.mask_words;
+  r.words = p.mask_words, r.ctx = s.len - s.n, r.n = s.n;
+  r.lo = 0, r.from = max(0, -r.ctx);
+  if (p.window > 0) {
+    int all = 0;
+#pragma unroll 1
+    for (int t = 0; t < r.n; t += 32) all += __popc(r.word(t >> 5) & bits_below(r.n - t) & ~bits_below(r.from - t));
+    r.lo = max(r.ctx, 0) + all - p.window;
+#pragma unroll 1
+    for (int t = 0; all > p.window; t += 32) {  // the first ones fall out of the window
+      uint32_t v = r.word(t >> 5) & bits_below(r.n - t) & ~bits_below(r.from - t);
+#pragma unroll 1
+      for (; v && all > p.window; v &= v - 1) r.from = t + __ffs(v), --all;
+    }
+  }
+  return r;
+}
+
 // ------------------------------------------------------------------ MMA helpers
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -553,7 +609,7 @@ struct AttnTile {
   // sequences of 2,000 keys with 64 rows 23 us against 33 before the join's present form, but cost verify blocks 7%.
   // Boundaries that move (two units) make no difference here.
   static constexpr int kOver = 3, kSnap = 0, kLeast = 1;
-  static constexpr __host__ __device__ Tiling tiling() { return {kRows, kKeys, kOver, kSnap, kLeast}; }
+  static constexpr __host__ __device__ Tiling tiling(bool tree) { return {kRows, kKeys, kOver, kSnap, kLeast, tree}; }
   static constexpr int kEl = kFp8 ? 1 : 2;
   static constexpr int kRowB = kDim * kEl < 128 ? kDim * kEl : 128;  // bytes of a row of a block
   static constexpr int kSub = kDim * kEl / kRowB;                    // blocks across a head
@@ -574,8 +630,16 @@ struct KeyRange {
   int all_lo, all_hi, any_lo, any_hi;
 };
 
+template <bool kTree>
 __device__ __forceinline__ KeyRange key_range(const AttnJob& p, const Walk& w) {
   KeyRange r;
+  if constexpr (kTree) {
+    r.all_hi = max(w.s.len - w.s.n, 0);
+    r.all_lo = p.window > 0 ? r.all_hi + w.s.n - p.window : 0;  // (a mask holds n tokens at most)
+    r.any_hi = w.t.hi;
+    r.any_lo = w.t.lo;
+    return r;
+  }
   const int first = w.s.len - w.s.n + div_by(p.by_group, w.t.row0);
   const int last = w.s.len - w.s.n + div_by(p.by_group, w.t.row0 + w.t.rows - 1);
   r.all_hi = min(first + 1, w.s.len);
@@ -699,7 +763,7 @@ __device__ __forceinline__ int piece_page(const AttnJob& p, const int32_t* table
 
 // ------------------------------------------------------------------ the split kernel
 
-template <int kDim, bool kFp8, int kRW, int kKW>
+template <int kDim, bool kFp8, int kRW, int kKW, bool kTree>
 __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, attn_ctas(kDim, kFp8, kRW))
     attn_split_kernel(const AttnJob p, const __grid_constant__ KvMaps maps) {
   using T = AttnTile<kDim, kFp8, kRW, kKW>;
@@ -725,7 +789,7 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, a
   pdl_launch_dependents();
   __syncthreads();
 
-  constexpr Tiling kTiling = T::tiling();
+  constexpr Tiling kTiling = T::tiling(kTree);
   Found f;
   Ranges ranges;
   find_range<T::kThreadsAll>(p, kTiling, gridDim.x, blockIdx.x, &ranges, &f, scratch,
@@ -831,13 +895,14 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, a
     const int r_lo = w.t.row0 + min(rw * 16, w.t.rows - 1), r_hi = w.t.row0 + min(rw * 16 + 15, w.t.rows - 1);
     const int pos_lo = w.s.len - w.s.n + div_by(p.by_group, r_lo);
     const int pos_hi = w.s.len - w.s.n + div_by(p.by_group, r_hi);
-    const int all_hi = min(pos_lo + 1, w.s.len);                                  // keys [all_lo, all_hi) seen by every row
-    const int all_lo = p.window > 0 ? pos_hi - p.window + 1 : 0;
-    const int any_hi = min(pos_hi + 1, w.s.len);                                  // keys [any_lo, any_hi) seen by some row
-    const int any_lo = p.window > 0 ? max(pos_lo - p.window + 1, 0) : 0;
+    int all_hi = min(pos_lo + 1, w.s.len);                                        // keys [all_lo, all_hi) seen by every row
+    int all_lo = p.window > 0 ? pos_hi - p.window + 1 : 0;
+    int any_hi = min(pos_hi + 1, w.s.len);                                        // keys [any_lo, any_hi) seen by some row
+    int any_lo = p.window > 0 ? max(pos_lo - p.window + 1, 0) : 0;
 
     // keys that every row of the item sees, or some row (the tiles between are cleaned)
-    const KeyRange kr = key_range(p, w);
+    const KeyRange kr = key_range<kTree>(p, w);
+    if constexpr (kTree) all_hi = kr.all_hi, all_lo = kr.all_lo, any_hi = kr.any_hi, any_lo = kr.any_lo;
 
     // Q to shared memory, each warp a quarter of the rows, eight lanes a row
     if constexpr (kKW > 1) asm volatile("bar.sync 1, %0;" ::"n"(T::kConsumers * 32) : "memory");  // the last item's Q is read
@@ -977,7 +1042,21 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, a
               for (int x = 0; x < 4; ++x) s[j][x] = cap2 * tanh_small(s[j][x]);
           }
         }
-        if (key0 + T::kSlice > all_hi || key0 < all_lo) {
+        if (kTree && (key0 + T::kSlice > all_hi || key0 < all_lo)) {
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const TreeRow row = tree_row(p, w.s, tok[y]);
+#pragma unroll
+            for (int j0 = 0; j0 < kNT; j0 += 4) {
+              const uint32_t seen = row.bits(key0 + 8 * j0) >> (2 * t4);
+#pragma unroll
+              for (int j = j0; j < kNT && j < j0 + 4; ++j)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) s[j][2 * y + x] = seen >> (8 * (j - j0) + x) & 1 ? s[j][2 * y + x] : -INFINITY;
+            }
+          }
+        }
+        if (!kTree && (key0 + T::kSlice > all_hi || key0 < all_lo)) {
 #pragma unroll
           for (int j = 0; j < kNT; ++j)
 #pragma unroll
@@ -1098,6 +1177,11 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, a
           for (unsigned left = __ballot_sync(0xffffffffu, holds); left; left &= left - 1) {
             const int who = __ffs(left) - 1, key = k0 + who;
             const int64_t at = __shfl_sync(0xffffffffu, mine, who);
+            [[maybe_unused]] bool sees[2];
+            if constexpr (kTree) {
+#pragma unroll
+              for (int y = 0; y < 2; ++y) sees[y] = tree_row(p, w.s, tok[y]).sees(key);
+            }
 #pragma unroll
             for (int j = 0; j < kDT; ++j)
 #pragma unroll
@@ -1107,8 +1191,13 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, a
                 const float v = pool_value<kFp8>(p.v_pool, at + col);
                 if (isfinite(v)) continue;
 #pragma unroll
-                for (int y = 0; y < 2; ++y)
-                  if (key <= pos[y] && key < w.s.len && (p.window <= 0 || key > pos[y] - p.window)) acc[j][2 * y + x] += v;
+                for (int y = 0; y < 2; ++y) {
+                  if constexpr (kTree) {
+                    if (sees[y]) acc[j][2 * y + x] += v;
+                  } else {
+                    if (key <= pos[y] && key < w.s.len && (p.window <= 0 || key > pos[y] - p.window)) acc[j][2 * y + x] += v;
+                  }
+                }
               }
           }
         }
@@ -1406,18 +1495,18 @@ nvfp4_status launch_attn_join(const AttnJob& p, int tile_rows, int keys, int gri
   return launched();
 }
 
-template <int kDim, bool kFp8, int kRW, int kKW>
+template <int kDim, bool kFp8, int kRW, int kKW, bool kTree>
 nvfp4_status launch_attn_split(const AttnJob& p, const KvMaps& maps, cudaStream_t stream) {
   using T = AttnTile<kDim, kFp8, kRW, kKW>;
-  if (set_smem(attn_split_kernel<kDim, kFp8, kRW, kKW>, T::kSmem) != cudaSuccess) return NVFP4_ERR_CUDA;
-  if (launch_pdl(attn_split_kernel<kDim, kFp8, kRW, kKW>, dim3(kAttnGrid * T::kCtas), dim3(T::kThreadsAll), T::kSmem,
-                 stream, p, maps) != cudaSuccess)
+  if (set_smem(attn_split_kernel<kDim, kFp8, kRW, kKW, kTree>, T::kSmem) != cudaSuccess) return NVFP4_ERR_CUDA;
+  if (launch_pdl(attn_split_kernel<kDim, kFp8, kRW, kKW, kTree>, dim3(kAttnGrid * T::kCtas), dim3(T::kThreadsAll),
+                 T::kSmem, stream, p, maps) != cudaSuccess)
     return NVFP4_ERR_CUDA;
   return launch_attn_join<kDim>(p, T::kRows, T::kKeys, kAttnGrid * T::kCtas, stream);
 }
 
-// The split and join grids for heads of kDim values (attention_d*.cu).
-template <int kDim>
+// The split and join grids for heads of kDim values (attention_d*.cu, attention_tree_d*.cu).
+template <int kDim, bool kTree>
 nvfp4_status dispatch_attention(const AttnJob& p, const KvMaps& maps, bool fp8, const AttnShape& s,
                                 cudaStream_t stream);
 

@@ -63,7 +63,7 @@ struct ChunkTile {
   // E4M3 tiles of 128 values, whose units are slow, balance better with one (2,048 tokens 50.8 against 56.7).
   // Ranges of kLeast units or a little less where there are few: 31 tokens over 2,000 keys 25.7 us against 32.8, 33.6 against 46.9 for 256 values.
   static constexpr int kOver = 4, kSnap = kFp8 && kDim == 128 ? 1 : 4, kLeast = kDim == 256 ? 8 : 4;  // in units (Tiling)
-  static constexpr __host__ __device__ Tiling tiling() { return {kRows, kKeys, kOver, kSnap, kLeast}; }
+  static constexpr __host__ __device__ Tiling tiling(bool tree) { return {kRows, kKeys, kOver, kSnap, kLeast, tree}; }
   // warps that make tiles fit: two beside the copies and the products, or (E4M3 and 128 values:
   // 256 conversions a row and tile; 830 us with two warps, 705 with four, for 2,048 tokens over
   // 32,768 keys) a warpgroup of their own; the softmax warpgroups follow
@@ -268,17 +268,22 @@ __device__ __forceinline__ void add_nonfinite(float (&o)[32], const void* pool, 
   }
 }
 
+// The keys [lo, hi) that a row sees.
+struct KeySpan {
+  int lo, hi;
+  __device__ __forceinline__ bool sees(int key) const { return key >= lo && key < hi; }
+};
+
 // Infinities and NaN that were taken out of V in an item's n tiles from tile `tile0` of the
-// CTA and key tile `first` on: from the pool into O of this thread's row, for the keys [see_lo, see_hi)
-// that it sees.  Each lane looks at one key, then all of them at those that hold any in
+// CTA and key tile `first` on: from the pool into O of this thread's row, for the keys that it
+// sees.  Each lane looks at one key, then all of them at those that hold any in
 // the columns at hand.  `head` is the offset of the kv head in a page.  (A function of its own
 // that works on TMEM: inside the loop that writes the rows the mixed batch of 64-value heads took 146.0 us and
 // 2,048 tokens over 32,768 E4M3 keys of 128 values 713, with it 145.4 and 710.)
-template <int kDim, bool kFp8, int kKeys>
+template <int kDim, bool kFp8, int kKeys, typename Row>
 __device__ __noinline__ void restore_nonfinite(uint32_t o_at, const volatile NotedTiles* notes, uint32_t tile0, int n,
-                                               int first, KeyRange kr, int see_lo, int see_hi, const int32_t* table,
-                                               const void* pool, int64_t head, int64_t page_stride, int page_log2,
-                                               int num_pages) {
+                                               int first, KeyRange kr, Row row, const int32_t* table, const void* pool,
+                                               int64_t head, int64_t page_stride, int page_log2, int num_pages) {
   const int lane = threadIdx.x & 31;
 #pragma unroll 1
   for (int c = 0; c < kDim; c += 32) {
@@ -303,7 +308,7 @@ __device__ __noinline__ void restore_nonfinite(uint32_t o_at, const volatile Not
         for (unsigned left = __ballot_sync(0xffffffffu, holds); left; left &= left - 1) {
           const int who = __ffs(left) - 1, key = k0 + who;
           const int64_t from = __shfl_sync(0xffffffffu, at, who);
-          if (key >= see_lo && key < see_hi) add_nonfinite<kFp8>(o, pool, from);
+          if (row.sees(key)) add_nonfinite<kFp8>(o, pool, from);
         }
       }
     }
@@ -366,7 +371,7 @@ __host__ __device__ __forceinline__ JoinStep join_step(int mine, int level, int 
 
 // ------------------------------------------------------------------ the kernel
 
-template <int kDim, bool kFp8>
+template <int kDim, bool kFp8, bool kTree>
 __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
     attn_chunk_kernel(const AttnJob p, const __grid_constant__ KvMaps maps) {
   using T = ChunkTile<kDim, kFp8>;
@@ -408,7 +413,7 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
   tc_fence_after();
   const uint32_t tmem = uniform(*static_cast<volatile uint32_t*>(&bars->tmem));
 
-  constexpr Tiling kTiling = T::tiling();
+  constexpr Tiling kTiling = T::tiling(kTree);
   Found f;
   Ranges ranges;
   find_range<T::kThreadsAll>(p, kTiling, gridDim.x, blockIdx.x, &ranges, &f, &bars->scratch,
@@ -601,7 +606,7 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
         u = pc.end;
         if (pc.n == 0) continue;
         const int first = pc.first, n = pc.n;
-        const KeyRange kr = key_range(p, w);
+        const KeyRange kr = key_range<kTree>(p, w);
         if constexpr (!kFp8) {
           for (int j = 0; j < n; ++j) {
             const uint32_t t = nt + j, st = VRing::at(t);
@@ -776,8 +781,10 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
       // logits in units of log 2: s * mul; with a softcap, mul * tanh(s * unit)
       const float unit = scale * ks * qscale * (capped ? 1.0f / p.softcap : log2e);
       const float mul = fmaxf(capped ? p.softcap * log2e : unit, 1.2e-38f);  // (-inf * 0 would be NaN)
-      // keys that this row sees, and those that all rows of the warp see
-      const int see_hi = min(pos + 1, w.s.len), see_lo = p.window > 0 ? pos - p.window + 1 : -(1 << 30);
+      // keys [see_lo, see_hi) that this row sees (of a tree's: that every row sees)
+      const int ctx = max(w.s.len - w.s.n, 0);
+      const int see_hi = kTree ? ctx : min(pos + 1, w.s.len);
+      const int see_lo = p.window > 0 ? (kTree ? ctx + w.s.n : pos + 1) - p.window : -(1 << 30);
 
       float m = -INFINITY, l = 0.f;  // reference of the weights, this row's sum
       for (int j = 0; j < n; ++j, ++mine) {
@@ -807,7 +814,12 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
                 for (int i = 0; i < 32; ++i) x[i] = tanh_small(x[i]);
               }
             }
-            if (partly) {
+            if (kTree && partly) {
+              const uint32_t seen = tree_row(p, w.s, tok).bits(key0 + c);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) x[i] = seen >> i & 1 ? x[i] : -INFINITY;
+            }
+            if (!kTree && partly) {
               const int hi = see_hi - key0 - c, lo = see_lo - key0 - c;
 #pragma unroll
               for (int i = 0; i < 32; ++i) x[i] = i >= lo && i < hi ? x[i] : -INFINITY;
@@ -918,10 +930,17 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
             *reinterpret_cast<uint4*>(out + c + 2 * i) = make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]);
         }
       };
-      if (bars->noted.any_since(nt - n))
-        restore_nonfinite<kDim, kFp8, kKeys>(o_at, &bars->noted, nt - n, n, first, key_range(p, w), see_lo, see_hi,
-                                             p.table + static_cast<int64_t>(w.b) * p.max_pages, p.v_pool,
-                                             value_at(p, 0, w.h, 0, kDim), p.page_stride, p.page_log2, p.num_pages);
+      if (bars->noted.any_since(nt - n)) {
+        const auto restore = [&](auto seen) {
+          restore_nonfinite<kDim, kFp8, kKeys>(o_at, &bars->noted, nt - n, n, first, key_range<kTree>(p, w), seen,
+                                               p.table + static_cast<int64_t>(w.b) * p.max_pages, p.v_pool,
+                                               value_at(p, 0, w.h, 0, kDim), p.page_stride, p.page_log2, p.num_pages);
+        };
+        if constexpr (kTree)
+          restore(tree_row(p, w.s, tok));
+        else
+          restore(KeySpan{see_lo, see_hi});
+      }
 #pragma unroll 1
       for (int c = 0; c < kDim; c += 32) {
         float o[32];
@@ -1016,11 +1035,12 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
   }
 }
 
-template <int kDim, bool kFp8>
+template <int kDim, bool kFp8, bool kTree>
 nvfp4_status launch_attn_chunk(const AttnJob& p, const KvMaps& maps, cudaStream_t stream) {
   using T = ChunkTile<kDim, kFp8>;
-  if (set_smem(attn_chunk_kernel<kDim, kFp8>, T::kSmem) != cudaSuccess) return NVFP4_ERR_CUDA;
-  if (launch_pdl(attn_chunk_kernel<kDim, kFp8>, dim3(kAttnGrid), dim3(T::kThreadsAll), T::kSmem, stream, p, maps) != cudaSuccess)
+  if (set_smem(attn_chunk_kernel<kDim, kFp8, kTree>, T::kSmem) != cudaSuccess) return NVFP4_ERR_CUDA;
+  if (launch_pdl(attn_chunk_kernel<kDim, kFp8, kTree>, dim3(kAttnGrid), dim3(T::kThreadsAll), T::kSmem, stream, p, maps) !=
+      cudaSuccess)
     return NVFP4_ERR_CUDA;
   return launched();
 }

@@ -3,6 +3,6 @@
 #include "attention_dispatch.cuh"
 
 namespace nvfp4 {
-template nvfp4_status dispatch_attention<128>(const AttnJob&, const KvMaps&, bool, const AttnShape&, cudaStream_t);
-template nvfp4_status attention_error_word<128>(uint32_t*, int);
+template nvfp4_status dispatch_attention<128, false>(const AttnJob&, const KvMaps&, bool, const AttnShape&, cudaStream_t);
+template nvfp4_status attention_error_word<128, false>(uint32_t*, int);
 }  // namespace nvfp4

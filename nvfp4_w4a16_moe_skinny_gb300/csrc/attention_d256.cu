@@ -3,6 +3,6 @@
 #include "attention_dispatch.cuh"
 
 namespace nvfp4 {
-template nvfp4_status dispatch_attention<256>(const AttnJob&, const KvMaps&, bool, const AttnShape&, cudaStream_t);
-template nvfp4_status attention_error_word<256>(uint32_t*, int);
+template nvfp4_status dispatch_attention<256, false>(const AttnJob&, const KvMaps&, bool, const AttnShape&, cudaStream_t);
+template nvfp4_status attention_error_word<256, false>(uint32_t*, int);
 }  // namespace nvfp4

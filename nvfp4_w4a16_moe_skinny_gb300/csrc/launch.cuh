@@ -99,11 +99,12 @@ nvfp4_status dispatch_stream(const Job& p, const WeightMaps& maps, const Plan& p
 template <int kEpi>
 nvfp4_status epi_error_word(uint32_t* v, int clear);
 
-// The same for the units of the attention side (rope.cu, head_norm.cu, kv_step.cu, attention_d*.cu).
+// The same for the units of the attention side (rope.cu, head_norm.cu, kv_step.cu,
+// attention_d*.cu, attention_tree_d*.cu).
 nvfp4_status rope_error_word(uint32_t* v, int clear);
 nvfp4_status norm_error_word(uint32_t* v, int clear);
 nvfp4_status step_error_word(uint32_t* v, int clear);
-template <int kDim>
+template <int kDim, bool kTree>
 nvfp4_status attention_error_word(uint32_t* v, int clear);
 
 }  // namespace nvfp4

@@ -346,8 +346,10 @@ nvfp4_status nvfp4_device_error(uint32_t* out, int32_t clear) {
   // the streaming kernels' translation units, one per epilogue
   // and those of the attention side
   for (auto fn : {epi_error_word<kEpiStore>, epi_error_word<kEpiArgmax>, epi_error_word<kEpiGated>,
-                  epi_error_word<kEpiRows>, epi_error_word<kEpiSample>, rope_error_word, attention_error_word<64>,
-                  attention_error_word<128>, attention_error_word<256>, norm_error_word, step_error_word}) {
+                  epi_error_word<kEpiRows>, epi_error_word<kEpiSample>, rope_error_word, norm_error_word,
+                  step_error_word, attention_error_word<64, false>, attention_error_word<128, false>,
+                  attention_error_word<256, false>, attention_error_word<64, true>, attention_error_word<128, true>,
+                  attention_error_word<256, true>}) {
     uint32_t w = 0;
     if (const nvfp4_status st = fn(&w, clear)) return st;
     v |= w;
