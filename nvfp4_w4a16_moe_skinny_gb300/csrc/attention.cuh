@@ -39,6 +39,8 @@
 // A row tile is too thin for tcgen05: its products take 128 rows at a time, and the same time for 16.
 #pragma once
 
+#include <type_traits>
+
 #include "launch.cuh"
 #include "paged.cuh"
 
@@ -105,12 +107,23 @@ struct KvMaps {
 // or part of them, equal ones, so that a range may hold a little less (nine units by fours: three ranges
 // of three).
 // What they are worth is measured at AttnTile and ChunkTile.
-// `tree`: a token sees all keys before the new ones and, of those, what its mask says
-// (tree_attention); otherwise the keys up to its own.
 struct Tiling {
   int rows, keys, over, snap, least;
-  bool tree;
 };
+
+// The tiling of a tree_attention call: a token sees all keys before the new ones and, of those, what
+// its mask says.  (A type of its own, so that the causal kernels compile as if there were no trees: a
+// member that says it cost them registers, 16 sequences of 8,000 keys with 64 rows 130 us instead of 127.)
+struct TreeTiling : Tiling {};
+template <typename G>
+constexpr bool kIsTree = std::is_same_v<G, TreeTiling>;
+template <bool kTree>
+__host__ __device__ constexpr auto tiling_for(const Tiling& t) {
+  if constexpr (kTree)
+    return TreeTiling{t};
+  else
+    return t;
+}
 
 // Quotient of x < 2^31 by the divisor that `d` was made for (fast_div): a multiply by the
 // rounded-up reciprocal and a shift.
@@ -148,28 +161,28 @@ struct RowTile {
   int tile0, units;  // first key tile, number of units (at least one, so that empty rows are written)
 };
 
-__host__ __device__ __forceinline__ RowTile row_tile(const AttnJob& p, const Sequence& s, int rt, const Tiling& g) {
+template <typename G>
+__host__ __device__ __forceinline__ RowTile row_tile(const AttnJob& p, const Sequence& s, int rt, const G& g) {
   RowTile t;
   t.row0 = rt * g.rows;
   t.rows = min(g.rows, s.rows - t.row0);
-  if (g.tree) {  // (a row sees its window's last keys: a mask of nothing, the context's)
+  if constexpr (kIsTree<G>) {  // (a row whose mask is empty sees the context's last keys)
     t.hi = s.len;
     t.lo = p.window > 0 ? min(max(max(s.len - s.n, 0) - p.window, 0), t.hi) : 0;
-    t.tile0 = t.lo / g.keys;
-    t.units = max(1, (t.hi + g.keys - 1) / g.keys - t.tile0);
-    return t;
+  } else {
+    const int p0 = s.len - s.n + div_by(p.by_group, t.row0);
+    const int p1 = s.len - s.n + div_by(p.by_group, t.row0 + t.rows - 1);
+    t.hi = min(max(p1 + 1, 0), s.len);
+    t.lo = p.window > 0 ? min(max(p0 - p.window + 1, 0), t.hi) : 0;
   }
-  const int p0 = s.len - s.n + div_by(p.by_group, t.row0);
-  const int p1 = s.len - s.n + div_by(p.by_group, t.row0 + t.rows - 1);
-  t.hi = min(max(p1 + 1, 0), s.len);
-  t.lo = p.window > 0 ? min(max(p0 - p.window + 1, 0), t.hi) : 0;
   t.tile0 = t.lo / g.keys;
   t.units = max(1, (t.hi + g.keys - 1) / g.keys - t.tile0);
   return t;
 }
 
 // Units of `s`, overheads included, by one lane or (lane, step) by the lanes of a warp.
-__device__ __forceinline__ long long tile_units(const AttnJob& p, const Sequence& s, int first, int step, const Tiling& g) {
+template <typename G>
+__device__ __forceinline__ long long tile_units(const AttnJob& p, const Sequence& s, int first, int step, const G& g) {
   long long u = 0;
 #pragma unroll 1
   for (int rt = first; rt < s.tiles; rt += step) u += row_tile(p, s, rt, g).units + g.over;
@@ -219,8 +232,8 @@ struct RangeScratch {
 // ranges and, if range c is in use, finds where its first unit lies.  A thread sums its
 // sequence's row tiles itself if they are few; long sequences go through a list (kList
 // entries of scratch memory) to whole warps.
-template <int kThreadsInBlock>
-__device__ __forceinline__ void find_range(const AttnJob& p, const Tiling& g, int ctas, int c, Ranges* ranges,
+template <int kThreadsInBlock, typename G>
+__device__ __forceinline__ void find_range(const AttnJob& p, const G& g, int ctas, int c, Ranges* ranges,
                                            Found* found, RangeScratch* sh, longlong2* list) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int kNW = kThreadsInBlock / 32;
@@ -330,7 +343,8 @@ struct Walk {
   RowTile t;
 };
 
-__device__ __forceinline__ void walk_seq(const AttnJob& p, Walk& w, const Tiling& g) {
+template <typename G>
+__device__ __forceinline__ void walk_seq(const AttnJob& p, Walk& w, const G& g) {
   w.s = sequence_of(p, w.b, g);
   w.rt = 0, w.h = 0;
   if (w.s.tiles > 0) w.t = row_tile(p, w.s, 0, g);
@@ -338,7 +352,8 @@ __device__ __forceinline__ void walk_seq(const AttnJob& p, Walk& w, const Tiling
 
 // The item that holds unit u, searched from where the walk is; u is below the total.
 // All lanes of a warp call it with the same arguments.
-__device__ __forceinline__ void walk_to(const AttnJob& p, Walk& w, long long u, const Tiling& g) {
+template <typename G>
+__device__ __forceinline__ void walk_to(const AttnJob& p, Walk& w, long long u, const G& g) {
   const int lane = threadIdx.x & 31;
   while (true) {
     if (w.rt < w.s.tiles) {
@@ -609,7 +624,7 @@ struct AttnTile {
   // sequences of 2,000 keys with 64 rows 23 us against 33 before the join's present form, but cost verify blocks 7%.
   // Boundaries that move (two units) make no difference here.
   static constexpr int kOver = 3, kSnap = 0, kLeast = 1;
-  static constexpr __host__ __device__ Tiling tiling(bool tree) { return {kRows, kKeys, kOver, kSnap, kLeast, tree}; }
+  static constexpr __host__ __device__ Tiling tiling() { return {kRows, kKeys, kOver, kSnap, kLeast}; }
   static constexpr int kEl = kFp8 ? 1 : 2;
   static constexpr int kRowB = kDim * kEl < 128 ? kDim * kEl : 128;  // bytes of a row of a block
   static constexpr int kSub = kDim * kEl / kRowB;                    // blocks across a head
@@ -789,7 +804,7 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, a
   pdl_launch_dependents();
   __syncthreads();
 
-  constexpr Tiling kTiling = T::tiling(kTree);
+  constexpr auto kTiling = tiling_for<kTree>(T::tiling());
   Found f;
   Ranges ranges;
   find_range<T::kThreadsAll>(p, kTiling, gridDim.x, blockIdx.x, &ranges, &f, scratch,

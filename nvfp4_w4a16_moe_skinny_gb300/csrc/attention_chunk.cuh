@@ -63,7 +63,7 @@ struct ChunkTile {
   // E4M3 tiles of 128 values, whose units are slow, balance better with one (2,048 tokens 50.8 against 56.7).
   // Ranges of kLeast units or a little less where there are few: 31 tokens over 2,000 keys 25.7 us against 32.8, 33.6 against 46.9 for 256 values.
   static constexpr int kOver = 4, kSnap = kFp8 && kDim == 128 ? 1 : 4, kLeast = kDim == 256 ? 8 : 4;  // in units (Tiling)
-  static constexpr __host__ __device__ Tiling tiling(bool tree) { return {kRows, kKeys, kOver, kSnap, kLeast, tree}; }
+  static constexpr __host__ __device__ Tiling tiling() { return {kRows, kKeys, kOver, kSnap, kLeast}; }
   // warps that make tiles fit: two beside the copies and the products, or (E4M3 and 128 values:
   // 256 conversions a row and tile; 830 us with two warps, 705 with four, for 2,048 tokens over
   // 32,768 keys) a warpgroup of their own; the softmax warpgroups follow
@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
   tc_fence_after();
   const uint32_t tmem = uniform(*static_cast<volatile uint32_t*>(&bars->tmem));
 
-  constexpr Tiling kTiling = T::tiling(kTree);
+  constexpr auto kTiling = tiling_for<kTree>(T::tiling());
   Found f;
   Ranges ranges;
   find_range<T::kThreadsAll>(p, kTiling, gridDim.x, blockIdx.x, &ranges, &f, &bars->scratch,

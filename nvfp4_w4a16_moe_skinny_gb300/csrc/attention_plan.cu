@@ -13,17 +13,17 @@ namespace nvfp4 {
 namespace {
 
 template <int kDim, bool kFp8>
-Tiling tiling_at(const AttnShape& s, bool tree) {
-  if (s.chunk) return ChunkTile<kDim, kFp8>::tiling(tree);
-  if (s.rw == 1) return AttnTile<kDim, kFp8, 1, 4>::tiling(tree);
-  if (s.rw == 2) return AttnTile<kDim, kFp8, 2, 2>::tiling(tree);
-  return AttnTile<kDim, kFp8, 4, 1>::tiling(tree);
+Tiling tiling_at(const AttnShape& s) {
+  if (s.chunk) return ChunkTile<kDim, kFp8>::tiling();
+  if (s.rw == 1) return AttnTile<kDim, kFp8, 1, 4>::tiling();
+  if (s.rw == 2) return AttnTile<kDim, kFp8, 2, 2>::tiling();
+  return AttnTile<kDim, kFp8, 4, 1>::tiling();
 }
 
-Tiling tiling_of(int dim, bool fp8, const AttnShape& s, bool tree) {
-  if (dim == 64) return fp8 ? tiling_at<64, true>(s, tree) : tiling_at<64, false>(s, tree);
-  if (dim == 128) return fp8 ? tiling_at<128, true>(s, tree) : tiling_at<128, false>(s, tree);
-  return fp8 ? tiling_at<256, true>(s, tree) : tiling_at<256, false>(s, tree);
+Tiling tiling_of(int dim, bool fp8, const AttnShape& s) {
+  if (dim == 64) return fp8 ? tiling_at<64, true>(s) : tiling_at<64, false>(s);
+  if (dim == 128) return fp8 ? tiling_at<128, true>(s) : tiling_at<128, false>(s);
+  return fp8 ? tiling_at<256, true>(s) : tiling_at<256, false>(s);
 }
 
 struct Split {
@@ -100,8 +100,9 @@ struct Arrivals {
 
 using namespace nvfp4;
 
+template <bool kTree>
 static nvfp4_status plan_check(const nvfp4_kv_cache* cache, const nvfp4_batch* batch, int32_t n_tokens, int32_t n_heads,
-                               int32_t window, int32_t orders, int32_t* out, int32_t out_len, bool tree) {
+                               int32_t window, int32_t orders, int32_t* out, int32_t out_len) {
   if (const nvfp4_status st = check_cache(cache)) return st;
   if (!batch || !out || !batch->cu_tokens || !batch->kv_len) return NVFP4_ERR_NULL;
   const int kv = cache->n_kv_heads, dim = cache->head_dim;
@@ -111,7 +112,7 @@ static nvfp4_status plan_check(const nvfp4_kv_cache* cache, const nvfp4_batch* b
   const bool fp8 = cache->dtype == NVFP4_KV_E4M3;
   const AttnShape shape = attn_shape(dim, fp8, packed_rows(n_tokens, batch->max_new, n_heads, kv),
                                      static_cast<int64_t>(batch->n_seqs) * kv);
-  const Tiling g = tiling_of(dim, fp8, shape, tree);
+  const auto g = tiling_for<kTree>(tiling_of(dim, fp8, shape));
   const int ctas = kAttnGrid * (shape.chunk ? 1 : attn_ctas(dim, fp8, shape.rw));
   AttnJob p{};
   p.n_seqs = batch->n_seqs, p.max_pages = batch->max_pages, p.n_tokens = n_tokens;
@@ -200,11 +201,11 @@ static nvfp4_status plan_check(const nvfp4_kv_cache* cache, const nvfp4_batch* b
   return NVFP4_OK;
 }
 
+template <bool kTree>
 static nvfp4_status plan_check_caught(const nvfp4_kv_cache* cache, const nvfp4_batch* batch, int32_t n_tokens,
-                                      int32_t n_heads, int32_t window, int32_t orders, int32_t* out, int32_t out_len,
-                                      bool tree) {
+                                      int32_t n_heads, int32_t window, int32_t orders, int32_t* out, int32_t out_len) {
   try {
-    return plan_check(cache, batch, n_tokens, n_heads, window, orders, out, out_len, tree);
+    return plan_check<kTree>(cache, batch, n_tokens, n_heads, window, orders, out, out_len);
   } catch (const std::bad_alloc&) {  // (nothing else is thrown)
     return NVFP4_ERR_WORKSPACE;
   }
@@ -214,12 +215,12 @@ extern "C" {
 
 nvfp4_status paged_attention_plan_check(const nvfp4_kv_cache* cache, const nvfp4_batch* batch, int32_t n_tokens,
                                         int32_t n_heads, int32_t window, int32_t orders, int32_t* out, int32_t out_len) {
-  return plan_check_caught(cache, batch, n_tokens, n_heads, window, orders, out, out_len, false);
+  return plan_check_caught<false>(cache, batch, n_tokens, n_heads, window, orders, out, out_len);
 }
 
 nvfp4_status tree_attention_plan_check(const nvfp4_kv_cache* cache, const nvfp4_batch* batch, int32_t n_tokens,
                                        int32_t n_heads, int32_t window, int32_t orders, int32_t* out, int32_t out_len) {
-  return plan_check_caught(cache, batch, n_tokens, n_heads, window, orders, out, out_len, true);
+  return plan_check_caught<true>(cache, batch, n_tokens, n_heads, window, orders, out, out_len);
 }
 
 }  // extern "C"
