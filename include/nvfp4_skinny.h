@@ -729,8 +729,10 @@ nvfp4_status paged_attention(const nvfp4_kv_cache *cache, const nvfp4_batch *bat
  * the keys that it sees so: for the ancestors of a token, those less than `window` positions back.
  *   masks  (device) int64 [n_tokens, words], as kv_assign writes them.
  *   words  1 to 64; batch->max_new is at most 64 * words.
- * The rest, and the workspace, as for paged_attention.
+ * The rest as for paged_attention; one workspace of the largest size needed serves both.
  */
+size_t tree_attention_workspace_bytes(int32_t n_tokens, int32_t n_seqs, int32_t max_new, int32_t n_heads,
+                                      int32_t n_kv_heads, int32_t head_dim);
 nvfp4_status tree_attention(const nvfp4_kv_cache *cache, const nvfp4_batch *batch, const int64_t *masks, int32_t words,
                             const uint16_t *q, int64_t q_stride, int32_t n_tokens, int32_t n_heads, float scale,
                             float softcap, int32_t window, uint16_t *out, int64_t out_stride, float *lse, void *ws,

@@ -41,6 +41,7 @@ EXPORTS = (
     "rope_frequencies", "rope_apply", "kv_append", "kv_cache_maps", "paged_attention_workspace_bytes", "paged_attention",
     "paged_attention_plan_check", "qk_norm_rope", "qk_norm_rope_workspace_bytes", "qk_norm_rope_backward",
     "kv_append_norm", "kv_assign", "kv_accept", "tree_attention", "tree_attention_plan_check",
+    "tree_attention_workspace_bytes",
 )
 
 
@@ -295,6 +296,8 @@ def _sig(lib):
     lib.paged_attention.restype = ctypes.c_int
     lib.tree_attention.argtypes = [_P, _P, _P, _I, _P, _I64, _I, _I, ctypes.c_float, ctypes.c_float, _I, _P, _I64, _P, _P,
                                    _SZ, _P]
+    lib.tree_attention_workspace_bytes.restype = _SZ
+    lib.tree_attention_workspace_bytes.argtypes = [_I] * 6
     lib.tree_attention.restype = ctypes.c_int
     lib.tree_attention_plan_check.argtypes = [_P, _P, _I, _I, _I, _I, ctypes.POINTER(ctypes.c_int32), _I]
     lib.tree_attention_plan_check.restype = ctypes.c_int
@@ -395,7 +398,8 @@ class Library:
         self.lib = ctypes.CDLL(path)
         _sig(self.lib)
         self._ws = {}
-        self._attention_bytes = {}  # attention workspaces: their sizes by the sizes of a call,
+        self._attention_bytes = {}  # attention workspaces: their sizes by the sizes of a call
+        self._tree_bytes = {}       # (of a tree_attention call),
         self._attention_ws = {}     # and one for each (device, stream)
 
     # -------------------------------------------------------------- plumbing
@@ -945,11 +949,11 @@ class Library:
             lse_ptr = lse.data_ptr()
         raw = _raw_stream(stream, dev)
         sizes = (tokens, batch.n_seqs, batch.max_new, heads, cache.n_kv_heads, dim)
-        nbytes = self._attention_bytes.get(sizes)
+        nbytes = self._tree_bytes.get(sizes)
         if nbytes is None:
-            if len(self._attention_bytes) > 4096:
-                self._attention_bytes.clear()
-            nbytes = self._attention_bytes[sizes] = self.lib.paged_attention_workspace_bytes(*sizes)
+            if len(self._tree_bytes) > 4096:
+                self._tree_bytes.clear()
+            nbytes = self._tree_bytes[sizes] = self.lib.tree_attention_workspace_bytes(*sizes)
         ws, ws_ptr, ws_bytes = self._stream_workspace(nbytes, dev, raw, stream)
         st = self.lib.tree_attention(
             cache.ref, batch.ref, masks.data_ptr(), masks.shape[1], q.data_ptr(), stride, tokens, heads, dim ** -0.5 if scale is None else scale, softcap,

@@ -35,6 +35,22 @@ bool encode_maps(KvMaps* maps, const nvfp4_kv_cache* c, const AttnShape& s) {
   return encode_pool_map(&maps->k, c, c->k, box, !s.chunk) && encode_pool_map(&maps->v, c, c->v, box, !s.chunk);
 }
 
+AttnShape shape_of(int dim, bool fp8, int64_t rows, int64_t items, bool tree) {
+  return tree ? tree_shape(dim, fp8, rows, items) : attn_shape(dim, fp8, rows, items);
+}
+
+size_t attn_workspace(int n_tokens, int n_seqs, int max_new, int n_heads, int n_kv_heads, int head_dim, bool tree) {
+  if (!attn_rows_ok(n_tokens, n_seqs, max_new, n_heads, n_kv_heads, head_dim)) return 0;
+  size_t most = 0;
+  for (const bool fp8 : {false, true}) {  // (the caller need not say which)
+    const AttnShape s = shape_of(head_dim, fp8, packed_rows(n_tokens, max_new, n_heads, n_kv_heads),
+                                 static_cast<int64_t>(n_seqs) * n_kv_heads, tree);
+    const size_t grid = kAttnGrid * (s.chunk ? 1 : attn_ctas(head_dim, false, s.rw));
+    most = std::max(most, 2 * grid * s.tile_rows * (head_dim + 2));  // sums of a row tile, references and sums of weights
+  }
+  return kAttnCounterBytes + kAttnSplitBytes + most * sizeof(float);
+}
+
 template <bool kTree>
 nvfp4_status dispatch_dim(int dim, const AttnJob& p, const KvMaps& maps, bool fp8, const AttnShape& s, cudaStream_t stream) {
   if (dim == 64) return dispatch_attention<64, kTree>(p, maps, fp8, s, stream);
@@ -59,7 +75,7 @@ nvfp4_status attend(const nvfp4_kv_cache* cache, const nvfp4_batch* batch, const
   if (!aligned(batch->cu_tokens, 4) || !aligned(batch->kv_len, 4) || !aligned(batch->page_table, 4) ||
       !aligned(lse, 4) || !aligned(ws, 32))
     return NVFP4_ERR_ALIGN;
-  if (!ws || ws_bytes < paged_attention_workspace_bytes(n_tokens, batch->n_seqs, batch->max_new, n_heads, kv, dim))
+  if (!ws || ws_bytes < attn_workspace(n_tokens, batch->n_seqs, batch->max_new, n_heads, kv, dim, words > 0))
     return NVFP4_ERR_WORKSPACE;
   if (n_tokens == 0 || batch->n_seqs == 0 || batch->max_new == 0) return NVFP4_OK;
 
@@ -78,8 +94,8 @@ nvfp4_status attend(const nvfp4_kv_cache* cache, const nvfp4_batch* batch, const
   p.split = reinterpret_cast<int4*>(static_cast<uint8_t*>(ws) + kAttnCounterBytes);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kAttnCounterBytes + kAttnSplitBytes);
   const bool fp8 = cache->dtype == NVFP4_KV_E4M3;
-  const AttnShape s = attn_shape(dim, fp8, packed_rows(n_tokens, batch->max_new, n_heads, kv),
-                                 static_cast<int64_t>(batch->n_seqs) * kv);
+  const AttnShape s = shape_of(dim, fp8, packed_rows(n_tokens, batch->max_new, n_heads, kv),
+                               static_cast<int64_t>(batch->n_seqs) * kv, words > 0);
   KvMaps maps;
   if (cache->maps)
     maps = static_cast<const KvMaps*>(cache->maps)[s.maps];
@@ -111,12 +127,12 @@ nvfp4_status kv_cache_maps(const nvfp4_kv_cache* cache, void* maps) {
 
 size_t paged_attention_workspace_bytes(int32_t n_tokens, int32_t n_seqs, int32_t max_new, int32_t n_heads,
                                        int32_t n_kv_heads, int32_t head_dim) {
-  if (!attn_rows_ok(n_tokens, n_seqs, max_new, n_heads, n_kv_heads, head_dim)) return 0;
-  const AttnShape s = attn_shape(head_dim, false, packed_rows(n_tokens, max_new, n_heads, n_kv_heads),
-                                 static_cast<int64_t>(n_seqs) * n_kv_heads);
-  const int grid = kAttnGrid * (s.chunk ? 1 : attn_ctas(head_dim, false, s.rw));
-  const size_t share = static_cast<size_t>(s.tile_rows) * (head_dim + 2);  // sums of a row tile, references and sums of weights
-  return kAttnCounterBytes + kAttnSplitBytes + 2 * grid * share * sizeof(float);
+  return attn_workspace(n_tokens, n_seqs, max_new, n_heads, n_kv_heads, head_dim, false);
+}
+
+size_t tree_attention_workspace_bytes(int32_t n_tokens, int32_t n_seqs, int32_t max_new, int32_t n_heads,
+                                      int32_t n_kv_heads, int32_t head_dim) {
+  return attn_workspace(n_tokens, n_seqs, max_new, n_heads, n_kv_heads, head_dim, true);
 }
 
 nvfp4_status paged_attention(const nvfp4_kv_cache* cache, const nvfp4_batch* batch, const uint16_t* q,

@@ -1472,6 +1472,7 @@ struct AttnShape {
   int rw, kw, tile_rows, box_keys;
   bool chunk;
   int maps;  // which of a cache's pairs of tensor maps
+  bool alternate = false;
 };
 constexpr int kMapPairs = 4;
 inline AttnShape attn_shape(int dim, bool fp8, int64_t rows, int64_t items) {
@@ -1479,6 +1480,23 @@ inline AttnShape attn_shape(int dim, bool fp8, int64_t rows, int64_t items) {
   const int rw = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
   const int kw = 4 / rw;
   return {rw, kw, 16 * rw, attn_slice(dim, fp8, kw) * kw, false, rw / 2};
+}
+
+// The same for a tree_attention call.  The join of its tcgen05 kernel is a second grid's (attention_chunk.cuh), which
+// makes that kernel the faster one from fewer rows on, and up to 128 rows of heads of 64 and 128 values its two row
+// groups take the key tiles in turn.  16 sequences of 8,000 keys, 60 or 64 rows: 128 values 100 us there and 127 in the
+// split kernel (E4M3 110 and 148), one of 32,000 keys 43 and 45; 64 values 64 and 73 there, but ragged
+// batches (64 of up to 4,000 keys) 39 and 34; 256 values 178 and 247 (E4M3 177 and 276).  32 rows: 128 values 100
+// and 107, ragged 32 and 31, one sequence of 1,000 keys 16 and 12; 256 values 178 and 191, ragged 50 and 69, four of
+// 2,000 keys 24 and 26, one of 1,000 keys 16 and 15; E4M3 176 and 190, ragged 59 and 54.  128 rows, the groups in turn
+// or each with rows of its own: 104 and 110 (64 values: 68 and 74).
+inline AttnShape tree_shape(int dim, bool fp8, int64_t rows, int64_t items) {
+  if (dim < 256) {
+    if (rows > (dim == 64 ? 64 : 32) && rows <= 128) return {0, 0, 128, 128, true, 3, true};
+  } else if (rows > 32 || (rows > 16 && !fp8 && items >= 32)) {
+    return {0, 0, 128, 64, true, 3};
+  }
+  return attn_shape(dim, fp8, rows, items);
 }
 
 // Checks of an attention call's sizes.

@@ -12,18 +12,22 @@
 namespace nvfp4 {
 namespace {
 
-template <int kDim, bool kFp8>
+template <int kDim, bool kFp8, bool kTree>
 Tiling tiling_at(const AttnShape& s) {
-  if (s.chunk) return ChunkTile<kDim, kFp8>::tiling();
+  if constexpr (kDim < 256)
+    if (s.alternate) return ChunkTile<kDim, kFp8, true>::tree_tiling();
+  using T = ChunkTile<kDim, kFp8>;
+  if (s.chunk) return kTree ? T::tree_tiling() : T::tiling();
   if (s.rw == 1) return AttnTile<kDim, kFp8, 1, 4>::tiling();
   if (s.rw == 2) return AttnTile<kDim, kFp8, 2, 2>::tiling();
   return AttnTile<kDim, kFp8, 4, 1>::tiling();
 }
 
+template <bool kTree>
 Tiling tiling_of(int dim, bool fp8, const AttnShape& s) {
-  if (dim == 64) return fp8 ? tiling_at<64, true>(s) : tiling_at<64, false>(s);
-  if (dim == 128) return fp8 ? tiling_at<128, true>(s) : tiling_at<128, false>(s);
-  return fp8 ? tiling_at<256, true>(s) : tiling_at<256, false>(s);
+  if (dim == 64) return fp8 ? tiling_at<64, true, kTree>(s) : tiling_at<64, false, kTree>(s);
+  if (dim == 128) return fp8 ? tiling_at<128, true, kTree>(s) : tiling_at<128, false, kTree>(s);
+  return fp8 ? tiling_at<256, true, kTree>(s) : tiling_at<256, false, kTree>(s);
 }
 
 struct Split {
@@ -110,9 +114,9 @@ static nvfp4_status plan_check(const nvfp4_kv_cache* cache, const nvfp4_batch* b
   if (!attn_sizes_ok(n_tokens, batch->n_seqs, batch->max_new, n_heads, kv, dim, batch->max_pages, cache->page_size))
     return NVFP4_ERR_SHAPE;
   const bool fp8 = cache->dtype == NVFP4_KV_E4M3;
-  const AttnShape shape = attn_shape(dim, fp8, packed_rows(n_tokens, batch->max_new, n_heads, kv),
-                                     static_cast<int64_t>(batch->n_seqs) * kv);
-  const auto g = tiling_for<kTree>(tiling_of(dim, fp8, shape));
+  const int64_t rows = packed_rows(n_tokens, batch->max_new, n_heads, kv), pairs = static_cast<int64_t>(batch->n_seqs) * kv;
+  const AttnShape shape = kTree ? tree_shape(dim, fp8, rows, pairs) : attn_shape(dim, fp8, rows, pairs);
+  const auto g = tiling_for<kTree>(tiling_of<kTree>(dim, fp8, shape));
   const int ctas = kAttnGrid * (shape.chunk ? 1 : attn_ctas(dim, fp8, shape.rw));
   AttnJob p{};
   p.n_seqs = batch->n_seqs, p.max_pages = batch->max_pages, p.n_tokens = n_tokens;
@@ -172,7 +176,7 @@ static nvfp4_status plan_check(const nvfp4_kv_cache* cache, const nvfp4_batch* b
       items.push_back({h.c0, holders});
     }
   });
-  if (shape.chunk && bad == 0) {
+  if (shape.chunk && !kTree && bad == 0) {  // (a tree's shares are joined by a second grid, without counters)
     std::vector<int> owner(kAttnCounterBytes / sizeof(unsigned) / 2, -1);
     for (size_t i = 0; i < items.size(); ++i)
       for (int m = 0; m < items[i].holders; ++m)
