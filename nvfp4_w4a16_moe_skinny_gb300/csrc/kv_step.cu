@@ -11,7 +11,8 @@ namespace {
 
 constexpr unsigned kErrStep = 8u;  // (g_device_error bit 3) pages, table columns or rows ran out; not a tree or path
 
-constexpr int kAssignThreads = 1024, kAssignCtas = 8, kMostSeqs = 16384;
+constexpr int kMostSeqs = 16384;
+constexpr int kMostKept = 14336;  // requests whose lengths and pages fit into shared memory beside their places
 
 struct AssignJob {
   int32_t* table;
@@ -33,92 +34,114 @@ struct AssignJob {
 // a + b for values of at most 2^30, held there
 __device__ __forceinline__ int add_sat(int a, int b) { return min(static_cast<unsigned>(a) + static_cast<unsigned>(b), 1u << 30); }
 
-// Inclusive scan (sums held at 2^30) over the block; `all` gets the total.
-__device__ __forceinline__ int block_scan(int v, int* warp_sums, int& all) {
+// Inclusive scans (sums held at 2^30) of two values a thread over the block, and their totals.
+template <int kThreads>
+__device__ __forceinline__ void block_scan(int& x, int& y, int2* warp_sums, int& all_x, int& all_y) {
+  constexpr int kWarps = kThreads / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v = add_sat(v, u);
+    const int u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) x = add_sat(x, u), y = add_sat(y, v);
   }
   __syncthreads();
-  if (lane == 31) warp_sums[warp] = v;
+  if (lane == 31) warp_sums[warp] = make_int2(x, y);
   __syncthreads();
-  int before = 0;
-  all = 0;
-  for (int w = 0; w < kAssignThreads / 32; ++w) {
-    if (w == warp) before = all;
-    all = add_sat(all, warp_sums[w]);
+  int2 w = lane < kWarps ? warp_sums[lane] : make_int2(0, 0);
+#pragma unroll
+  for (int o = 1; o < kWarps; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, w.x, o), v = __shfl_up_sync(0xffffffffu, w.y, o);
+    if (lane >= o) w.x = add_sat(w.x, u), w.y = add_sat(w.y, v);
   }
-  return add_sat(v, before);
+  all_x = __shfl_sync(0xffffffffu, w.x, kWarps - 1), all_y = __shfl_sync(0xffffffffu, w.y, kWarps - 1);
+  const int before_x = __shfl_sync(0xffffffffu, w.x, max(warp - 1, 0)), before_y = __shfl_sync(0xffffffffu, w.y, max(warp - 1, 0));
+  if (warp > 0) x = add_sat(x, before_x), y = add_sat(y, before_y);
 }
 
-// What a request asks for: its committed length, new tokens (clipped to the step's rows),
-// pages held, pages to take and to give back.
+// What a request asks for: its committed length, new tokens, pages held, pages to take and to give back.
 struct Ask {
   int ctx, n, held, take, back;
 };
 
-__device__ __forceinline__ Ask ask_of(const AssignJob& p, int b, int start) {
-  Ask a;
-  const int fresh = __ldcg(p.fresh + b);
-  a.ctx = fresh < 0 ? 0 : min(max(__ldcg(p.kv_len + b), 0), 1 << 30);
+__device__ __forceinline__ Ask ask_of(const AssignJob& p, int b) {
+  Ask a{};
+  if (b >= p.n_seqs) return a;
+  const int fresh = __ldcg(p.fresh + b), len = __ldcg(p.kv_len + b);
   a.held = min(max(__ldcg(p.held + b), 0), p.max_pages);
-  a.n = min(max(fresh, 0), p.n_tokens - start);
-  const int64_t end = static_cast<int64_t>(a.ctx) + a.n;
-  const int need = static_cast<int>(min((end + (1 << p.page_log2) - 1) >> p.page_log2, static_cast<int64_t>(p.max_pages)));
-  a.take = fresh < 0 ? 0 : max(0, need - a.held);
+  a.ctx = fresh < 0 ? 0 : min(max(len, 0), 1 << 30);
+  a.n = min(max(fresh, 0), 1 << 30);
   a.back = fresh < 0 ? a.held : 0;
   return a;
 }
 
-// One cluster: every CTA scans the requests for itself and writes its share of the rows; nobody
-// changes what another one reads (lengths, pages held, the free list) before all of them have read it.
-__global__ void __cluster_dims__(kAssignCtas, 1, 1) __launch_bounds__(kAssignThreads) kv_assign_kernel(const AssignJob p) {
-  extern __shared__ int smem[];
-  int* const warp_sums = smem;                // [32]
-  int* const start = smem + 32;               // [n_seqs + 1] first row of each request
-  int* const first = start + p.n_seqs + 1;    // [n_seqs] its first page's place among those taken
-  const int rank = static_cast<int>(blockIdx.x);
+// Pages that a request takes for n new tokens.
+__device__ __forceinline__ int pages_to_take(const AssignJob& p, const Ask& a, int n) {
+  if (a.back > 0) return 0;
+  const int64_t end = static_cast<int64_t>(a.ctx) + n;
+  return max(0, static_cast<int>(min((end + (1 << p.page_log2) - 1) >> p.page_log2, static_cast<int64_t>(p.max_pages))) - a.held);
+}
+
+// Up to kMostRows rows of few requests: one CTA; else one cluster of eight, each of which scans the requests for itself
+// and writes its share of the rows.  Nobody changes what another thread reads (lengths, pages held, the free list)
+// before all of them have read it: that is the one barrier between the two halves, and why the launch is one
+// cluster.  Bound by the chain of loads (requests, then page ids) and scans: see below.
+template <int kThreads, int kCtas>
+__device__ __forceinline__ void assign_step(const AssignJob& p, int* smem) {
+  int2* const warp_sums = reinterpret_cast<int2*>(smem);  // [32]
+  int* const start = smem + 64;             // [n_seqs + 1] first row of each request
+  int* const first = start + p.n_seqs + 1;  // [n_seqs] its first page's place among those taken
+  int2* const kept = reinterpret_cast<int2*>(smem + 64 + 2 * p.n_seqs + 2);  // [n_seqs] committed length, pages held
+  int* const own = reinterpret_cast<int*>(kept + p.n_seqs);  // parents of the CTA's rows (one CTA only)
+  const bool keeps = kCtas == 1 || p.n_seqs <= kMostKept;
+  const int rank = kCtas > 1 ? static_cast<int>(blockIdx.x) : 0, tid = threadIdx.x;
   pdl_wait();
   pdl_launch_dependents();
+  const Ask mine = ask_of(p, tid);
+  const int count = min(max(__ldcg(p.free_count), 0), p.num_free);
+  if (kCtas == 1 && p.parents)
+    for (int t = tid; t < p.n_tokens; t += kThreads) own[t] = __ldg(p.parents + t);
   unsigned bad = 0;
-  int rows = 0, taken = 0, given = 0;
-  for (int b0 = 0; b0 < p.n_seqs; b0 += kAssignThreads) {
-    const int b = b0 + static_cast<int>(threadIdx.x);
-    const int n = b < p.n_seqs ? min(max(__ldcg(p.fresh + b), 0), 1 << 30) : 0;
-    int all;
-    const int end = add_sat(rows, block_scan(n, warp_sums, all));
-    if (b < p.n_seqs) {
-      if (end > p.n_tokens) bad = kErrStep;
-      start[b + 1] = min(end, p.n_tokens);
-      if (b == 0) start[0] = 0;
+  int rows = 0, taken = 0;
+  bool gives = false;
+  if (tid == 0) start[0] = 0;
+  // rows and pages in one pass; again for the pages where the step's rows run out, as then requests get fewer of both
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    int row0 = 0;
+    taken = 0;
+#pragma unroll 1
+    for (int b0 = 0; b0 < p.n_seqs; b0 += kThreads) {
+      const int b = b0 + tid;
+      const Ask a = b0 == 0 ? mine : ask_of(p, b);
+      const int n = pass == 0 ? a.n : (b < p.n_seqs ? start[b + 1] - start[b] : 0);
+      const int take = pages_to_take(p, a, n);
+      int x = n, y = take, all_x, all_y;
+      block_scan<kThreads>(x, y, warp_sums, all_x, all_y);
+      if (b < p.n_seqs) {
+        if (pass == 0 && keeps) kept[b] = make_int2(a.ctx, a.held);
+        if (pass == 0) start[b + 1] = min(add_sat(row0, x), p.n_tokens);
+        const int last = add_sat(taken, y);
+        first[b] = last - take;
+        if (last > count || (n > 0 && a.ctx + static_cast<int64_t>(n) > static_cast<int64_t>(p.max_pages) << p.page_log2))
+          bad = kErrStep;
+        gives = gives || a.back > 0;
+      }
+      row0 = add_sat(row0, all_x), taken = add_sat(taken, all_y);
     }
-    rows = add_sat(rows, all);
+    if (pass == 0) rows = row0;
+    __syncthreads();
+    if (rows <= p.n_tokens) break;
+    if (pass == 0) bad = 0;
+    if (pass == 1) bad = kErrStep;
   }
   rows = min(rows, p.n_tokens);
-  __syncthreads();
-  const int count = min(max(__ldcg(p.free_count), 0), p.num_free);
-  for (int b0 = 0; b0 < p.n_seqs; b0 += kAssignThreads) {
-    const int b = b0 + static_cast<int>(threadIdx.x);
-    Ask a{};
-    if (b < p.n_seqs) a = ask_of(p, b, start[b]);
-    int all;
-    const int end = add_sat(taken, block_scan(a.take, warp_sums, all));
-    if (b < p.n_seqs) {
-      first[b] = end - a.take;
-      if (end > count || a.ctx + static_cast<int64_t>(a.n) > static_cast<int64_t>(p.max_pages) << p.page_log2) bad = kErrStep;
-    }
-    taken = add_sat(taken, all);
-  }
-  __syncthreads();
   const auto page_of = [&](int b, int held, int col) {  // -1: none
     if (col < held) return __ldcg(p.table + static_cast<int64_t>(b) * p.max_pages + col);
     const int at = count - 1 - (first[b] + col - held);
     return col < p.max_pages && at >= 0 ? __ldcg(p.free_pages + at) : -1;
   };
   // ---- rows
-  for (int t = rank * kAssignThreads + static_cast<int>(threadIdx.x); t < p.n_tokens; t += kAssignCtas * kAssignThreads) {
+  for (int t = rank * kThreads + tid; t < p.n_tokens; t += kCtas * kThreads) {
     int64_t slot = -1;
     int position = 0;
     if (t < rows) {
@@ -128,23 +151,35 @@ __global__ void __cluster_dims__(kAssignCtas, 1, 1) __launch_bounds__(kAssignThr
         if (start[mid] <= t) lo = mid;
         else hi = mid - 1;
       }
-      const int b = lo, i = t - start[b];
-      const int ctx = min(max(__ldcg(p.kv_len + b), 0), 1 << 30), held = min(max(__ldcg(p.held + b), 0), p.max_pages);
-      const int at = ctx + i, page = page_of(b, held, at >> p.page_log2);
+      const int b = lo, row0 = start[b], i = t - row0;
+      int2 r;
+      if (keeps) {
+        r = kept[b];
+      } else {
+        const Ask a = ask_of(p, b);
+        r = make_int2(a.ctx, a.held);
+      }
+      const int ctx = r.x, at = ctx + i, page = page_of(b, r.y, at >> p.page_log2);
       if (page >= 0) slot = (static_cast<int64_t>(page) << p.page_log2) + (at & ((1 << p.page_log2) - 1));
       position = at;
       if (p.parents) {
         int depth = 0;
-        for (int w = 0; w < p.words; ++w) {
-          uint64_t mask = 0;
+        for (int w0 = 0; w0 < p.words; w0 += 4) {  // four words of the mask at a walk up the tree
+          uint64_t mask[4] = {};
           for (int x = i; x >= 0;) {
-            if (x >> 6 == w) mask |= 1ull << (x & 63);
-            const int up = __ldg(p.parents + start[b] + x);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (x >> 6 == w0 + k) mask[k] |= 1ull << (x & 63);
+            const int up = kCtas == 1 ? own[row0 + x] : __ldg(p.parents + row0 + x);
             if (up < -1 || up >= x) bad = kErrStep;
             x = up >= x ? -1 : up;
           }
-          depth += __popcll(mask);
-          p.masks[static_cast<int64_t>(t) * p.words + w] = static_cast<int64_t>(mask);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (w0 + k < p.words) {
+              depth += __popcll(mask[k]);
+              p.masks[static_cast<int64_t>(t) * p.words + w0 + k] = static_cast<int64_t>(mask[k]);
+            }
         }
         if (i >= 64 * p.words) bad = kErrStep;
         position = ctx + max(depth - 1, 0);
@@ -155,44 +190,70 @@ __global__ void __cluster_dims__(kAssignCtas, 1, 1) __launch_bounds__(kAssignThr
     p.slots[t] = slot;
     p.positions[t] = position;
   }
-  // ---- new entries of the page table, each CTA a share of the requests
-  for (int b = rank * kAssignThreads + static_cast<int>(threadIdx.x); b < p.n_seqs; b += kAssignCtas * kAssignThreads) {
-    const Ask a = ask_of(p, b, start[b]);
-    for (int j = 0; j < a.take; ++j) {
+  // ---- new entries of the page table, each CTA every eighth request of a block of them
+#pragma unroll 1
+  for (int b0 = 0; b0 < p.n_seqs; b0 += kThreads) {
+    const int b = b0 + tid;
+    if (b >= p.n_seqs || (kCtas > 1 && tid % kCtas != rank)) continue;
+    const Ask a = b0 == 0 ? mine : ask_of(p, b);
+    const int take = pages_to_take(p, a, start[b + 1] - start[b]);
+    for (int j = 0; j < take; ++j) {
       const int page = page_of(b, a.held, a.held + j);
       if (page < 0) break;
       p.table[static_cast<int64_t>(b) * p.max_pages + a.held + j] = page;
     }
   }
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
   if (bad) atomicOr(&g_device_error, bad);
-  if (rank != 0) return;
+  if constexpr (kCtas > 1) {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (rank != 0) return;
+    gives = __syncthreads_or(gives);
+  } else {
+    gives = __syncthreads_or(gives);
+  }
   // ---- what the next step reads; finished requests' pages on top of the free list
   const int left = max(0, count - taken);
-  for (int b0 = 0; b0 < p.n_seqs; b0 += kAssignThreads) {
-    const int b = b0 + static_cast<int>(threadIdx.x);
-    Ask a{};
-    if (b < p.n_seqs) a = ask_of(p, b, start[b]);
-    int all;
-    const int end = add_sat(given, block_scan(a.back, warp_sums, all));
-    if (b < p.n_seqs) {
+  int given = 0;
+#pragma unroll 1
+  for (int b0 = 0; b0 < p.n_seqs; b0 += kThreads) {
+    const int b = b0 + tid;
+    const Ask a = b0 == 0 ? mine : ask_of(p, b);
+    if (gives) {
+      int x = a.back, none = 0, all, nothing;
+      block_scan<kThreads>(x, none, warp_sums, all, nothing);
+      const int from = add_sat(given, x) - a.back;
       for (int j = 0; j < a.back; ++j) {
-        const int64_t at = static_cast<int64_t>(left) + end - a.back + j;
-        if (at < p.num_free) p.free_pages[at] = __ldcg(p.table + static_cast<int64_t>(b) * p.max_pages + j);
-        else bad = kErrStep;
+        const int64_t at = static_cast<int64_t>(left) + from + j;
+        if (at < p.num_free)
+          p.free_pages[at] = __ldcg(p.table + static_cast<int64_t>(b) * p.max_pages + j);
+        else
+          atomicOr(&g_device_error, kErrStep);
       }
-      p.held[b] = a.held - a.back + max(0, min(a.take, count - first[b]));
-      p.kv_len_out[b] = a.ctx + a.n;
-      p.cu[b + 1] = start[b + 1];
-      if (b == 0) p.cu[0] = 0;
+      given = add_sat(given, all);
     }
-    given = add_sat(given, all);
+    if (b < p.n_seqs) {
+      const int n = start[b + 1] - start[b];
+      p.held[b] = a.held - a.back + max(0, min(pages_to_take(p, a, n), count - first[b]));
+      p.kv_len_out[b] = a.ctx + n;
+      p.cu[b + 1] = start[b + 1];
+    }
   }
-  if (threadIdx.x == 0) {
+  if (tid == 0) {
+    p.cu[0] = 0;
     *p.free_count = min(add_sat(left, given), p.num_free);
-    if (p.n_seqs == 0) p.cu[0] = 0;
   }
-  if (bad) atomicOr(&g_device_error, bad);
+}
+
+constexpr int kFewThreads = 256, kFewRows = 1024, kManyThreads = 1024, kManyCtas = 8;
+
+__global__ void __launch_bounds__(kFewThreads) kv_assign_few_kernel(const AssignJob p) {
+  __shared__ __align__(16) int smem[64 + 4 * kFewThreads + 2 + kFewRows];
+  assign_step<kFewThreads, 1>(p, smem);
+}
+
+__global__ void __cluster_dims__(kManyCtas, 1, 1) __launch_bounds__(kManyThreads) kv_assign_kernel(const AssignJob p) {
+  extern __shared__ __align__(16) int dynamic[];
+  assign_step<kManyThreads, kManyCtas>(p, dynamic);
 }
 
 // ------------------------------------------------------------------ the accepted path
@@ -307,10 +368,13 @@ nvfp4_status kv_assign(const nvfp4_page_table* pages, const int32_t* kv_len, con
   p.kv_len = kv_len, p.fresh = new_tokens, p.parents = rows > 0 ? parents : nullptr;
   p.slots = step->slots, p.positions = step->positions, p.cu = step->cu_tokens, p.kv_len_out = step->kv_len;
   p.masks = step->masks, p.n_tokens = rows, p.words = step->words;
-  const size_t smem = (2 * static_cast<size_t>(seqs) + 33) * sizeof(int);
+  if (seqs <= kFewThreads && rows <= kFewRows) {
+    if (launch_pdl(kv_assign_few_kernel, dim3(1), dim3(kFewThreads), 0, stream, p) != cudaSuccess) return NVFP4_ERR_CUDA;
+    return launched();
+  }
+  const size_t smem = (static_cast<size_t>(seqs <= kMostKept ? 4 : 2) * seqs + 66) * sizeof(int);
   if (set_smem(kv_assign_kernel, smem) != cudaSuccess) return NVFP4_ERR_CUDA;
-  if (launch_pdl(kv_assign_kernel, dim3(kAssignCtas), dim3(kAssignThreads), smem, stream, p) != cudaSuccess)
-    return NVFP4_ERR_CUDA;
+  if (launch_pdl(kv_assign_kernel, dim3(kManyCtas), dim3(kManyThreads), smem, stream, p) != cudaSuccess) return NVFP4_ERR_CUDA;
   return launched();
 }
 
