@@ -70,10 +70,30 @@ __device__ __forceinline__ void runs_of(const float (&pa)[8], const float (&pb)[
 }
 
 __device__ __forceinline__ float lanes_sum(float v, int lanes_log2) {
-#pragma unroll 1
-  for (int o = 1; o < (1 << lanes_log2); o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+#pragma unroll
+  for (int k = 0; k < 5; ++k)
+    if (k < lanes_log2) v += __shfl_xor_sync(0xffffffffu, v, 1 << k);
   return v;
 }
+
+// A thread's own ring in shared memory, through which its loads of the next kAhead heads come without holding
+// registers: 16-byte pieces, kParts a head, each read by the thread that copied it, so that no barrier is needed.
+// A slot is filled again two heads after it was read.
+template <int kParts>
+struct OwnRing {
+  static constexpr int kSlots = 4, kAhead = kSlots - 1, kBytes = kSlots * kParts * kNormThreads * 16;
+  uint32_t base;
+  __device__ __forceinline__ uint32_t at(int i, int part) const {
+    return base + (((i & (kSlots - 1)) * kParts + part) * kNormThreads + threadIdx.x) * 16;
+  }
+  // 16 bytes, or zeros where `bytes` is 0 (nothing is read then)
+  __device__ __forceinline__ void copy(int i, int part, const uint16_t* from, uint32_t bytes) const {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at(i, part)), "l"(from), "r"(bytes) : "memory");
+  }
+  static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  static __device__ __forceinline__ void arrived() { asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory"); }
+  __device__ __forceinline__ uint4 read(int i, int part) const { return lds128(at(i, part)); }
+};
 
 // Whether mean(x^2) + eps is near an end of fp32: the squares of values above 2^60 may overflow, those of a
 // head of very small ones (and eps) vanish.  Such a head is multiplied by scale_of and its sums taken again.
@@ -96,6 +116,7 @@ __device__ __forceinline__ Chunk chunk_at(const NormJob& p, int token, int chunk
   const bool split = h.turn && !kInterleaved;
   h.a = split ? 8 * chunk : 16 * chunk;
   h.b = split ? h.a + (p.rot >> 1) : h.a + 8;
+  if (chunk >= (p.dim >> 4)) h.a = h.b = 0;  // (a lane past the head: its copies are of nothing, from inside the row)
   return h;
 }
 
@@ -119,7 +140,9 @@ __device__ __forceinline__ void load_weights(const NormJob& p, int kind, const C
 enum { kToRows = 0, kToBf16 = 1, kToE4M3 = 2 };  // where keys and values go
 
 template <int kTo, bool kInterleaved>
-__global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const NormJob p) {
+__global__ void __launch_bounds__(kNormThreads, 8) norm_rope_kernel(const NormJob p) {
+  __shared__ __align__(16) uint8_t ring_bytes[OwnRing<2>::kBytes];
+  const OwnRing<2> ring{smem_addr(ring_bytes)};
   pdl_wait();
   pdl_launch_dependents();
   const int64_t idx = static_cast<int64_t>(blockIdx.x) * kNormThreads + threadIdx.x;
@@ -137,6 +160,16 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const NormJob p
     if (slot >= p.n_slots && live && h.chunk == 0) atomicOr(&g_device_error, kErrPage);
     live = live && slot >= 0 && slot < p.n_slots;
   }
+  const uint16_t* x = p.x[kind] + h.token * p.x_stride[kind] + h0 * p.dim;
+  const auto fetch = [&](int i) {
+    if (h0 + i < h1) {
+      ring.copy(i, 0, x + i * p.dim + h.a, live ? 16 : 0);
+      ring.copy(i, 1, x + i * p.dim + h.b, live ? 16 : 0);
+    }
+    ring.commit();
+  };
+#pragma unroll
+  for (int i = 0; i < ring.kAhead; ++i) fetch(i);
   float c[8], s[8], ga[8], gb[8];
   if (kind < 2) {
     load_weights<kInterleaved>(p, kind, h, ga, gb);
@@ -146,18 +179,15 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const NormJob p
       for (int i = 0; i < 8; ++i) angle_of(p.inv_freq, p.amplitude, false, pos, 8 * h.chunk + i, c[i], s[i]);
     }
   }
-  const uint16_t* x = p.x[kind] + h.token * p.x_stride[kind];
   // element offset of (slot, head 0) in a pool, and from one head to the next
   const int64_t page = slot >> p.page_log2, off = slot & ((1 << p.page_log2) - 1);
   const int64_t base = to_cache ? page * p.page_stride + off * p.dim : h.token * p.y_stride[kind < 2 ? kind : 0];
   const int64_t head_step = to_cache ? static_cast<int64_t>(p.dim) << p.page_log2 : p.dim;
   uint16_t* const y = to_cache ? reinterpret_cast<uint16_t*>(p.cache[kind - 1]) : p.y[kind < 2 ? kind : 0];
   for (int hh = h0; hh < h1; ++hh) {
-    uint4 va = make_uint4(0, 0, 0, 0), vb = va;
-    if (live) {
-      va = *reinterpret_cast<const uint4*>(x + hh * p.dim + h.a);
-      vb = *reinterpret_cast<const uint4*>(x + hh * p.dim + h.b);
-    }
+    ring.arrived();
+    const uint4 va = ring.read(hh - h0, 0), vb = ring.read(hh - h0, 1);
+    fetch(hh - h0 + ring.kAhead);
     const int64_t o = base + hh * head_step;
     float fa[8], fb[8];
     if (kind == 2) {
@@ -210,8 +240,11 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const NormJob p
 }
 
 template <bool kInterleaved>
-__global__ void __launch_bounds__(kNormThreads) norm_rope_backward_kernel(const NormJob p) {
-  __shared__ float sums[kNormThreads * 16];  // [tokens of the block][dim]
+__global__ void __launch_bounds__(kNormThreads, 4) norm_rope_backward_kernel(const NormJob p) {
+  __shared__ __align__(16) uint8_t ring_bytes[OwnRing<4>::kBytes];
+  static_assert(sizeof(ring_bytes) >= kNormThreads * 16 * sizeof(float), "the sums at the end");
+  float* const sums = reinterpret_cast<float*>(ring_bytes);  // [tokens of the block][dim], after the loop
+  const OwnRing<4> ring{smem_addr(ring_bytes)};
   pdl_wait();
   pdl_launch_dependents();
   const int lanes = 1 << p.lanes_log2, at_once = kNormThreads >> p.lanes_log2;
@@ -223,8 +256,28 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_backward_kernel(const 
   load_weights<kInterleaved>(p, kind, h, ga, gb);
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc_a[i] = acc_b[i] = 0.f;
-  const int step = static_cast<int>(gridDim.x) * at_once;
-  for (int t0 = blockIdx.x * at_once; t0 < p.n_tokens; t0 += step) {
+  const int step = static_cast<int>(gridDim.x) * at_once, first = static_cast<int>(blockIdx.x) * at_once;
+  // the copies run through the same tokens and heads, ahead of the loop
+  int copied = 0, copy_t = first, copy_h = h0;
+  const auto fetch = [&]() {
+    if (copy_t < p.n_tokens) {
+      const Chunk f = chunk_at<kInterleaved>(p, copy_t + sub, chunk);
+      const uint16_t* x = p.x[kind] + f.token * p.x_stride[kind] + copy_h * p.dim;
+      const uint16_t* dy = p.dy[kind] + f.token * p.dy_stride[kind] + copy_h * p.dim;
+      const uint32_t bytes = f.inside ? 16 : 0;
+      ring.copy(copied, 0, x + f.a, bytes);
+      ring.copy(copied, 1, x + f.b, bytes);
+      ring.copy(copied, 2, dy + f.a, bytes);
+      ring.copy(copied, 3, dy + f.b, bytes);
+      ++copied;
+      if (++copy_h == h1) copy_h = h0, copy_t += step;
+    }
+    ring.commit();
+  };
+#pragma unroll
+  for (int i = 0; i < ring.kAhead; ++i) fetch();
+  int at = 0;
+  for (int t0 = first; t0 < p.n_tokens; t0 += step) {
     h = chunk_at<kInterleaved>(p, t0 + sub, chunk);
     float c[8], s[8];
     if (h.turn) {
@@ -232,17 +285,11 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_backward_kernel(const 
 #pragma unroll
       for (int i = 0; i < 8; ++i) angle_of(p.inv_freq, p.amplitude, false, pos, 8 * chunk + i, c[i], s[i]);
     }
-    const uint16_t* x = p.x[kind] + h.token * p.x_stride[kind];
-    const uint16_t* dy = p.dy[kind] + h.token * p.dy_stride[kind];
     uint16_t* dx = p.y[kind] + h.token * p.y_stride[kind];
-    for (int hh = h0; hh < h1; ++hh) {
-      uint4 v[4] = {};
-      if (h.inside) {
-        v[0] = *reinterpret_cast<const uint4*>(x + hh * p.dim + h.a);
-        v[1] = *reinterpret_cast<const uint4*>(x + hh * p.dim + h.b);
-        v[2] = *reinterpret_cast<const uint4*>(dy + hh * p.dim + h.a);
-        v[3] = *reinterpret_cast<const uint4*>(dy + hh * p.dim + h.b);
-      }
+    for (int hh = h0; hh < h1; ++hh, ++at) {
+      ring.arrived();
+      const uint4 v[4] = {ring.read(at, 0), ring.read(at, 1), ring.read(at, 2), ring.read(at, 3)};
+      fetch();
       float pa[8], pb[8], ua[8], ub[8];
       unpack_pairs<kInterleaved>(v[0], v[1], pa, pb);
       unpack_pairs<kInterleaved>(v[2], v[3], ua, ub);
@@ -293,6 +340,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_backward_kernel(const 
     }
   }
   // this block's share of dg: its tokens one after the other
+  __syncthreads();  // (where the ring was)
   if (chunk < (p.dim >> 4)) {
     float* mine = sums + sub * p.dim;
 #pragma unroll
