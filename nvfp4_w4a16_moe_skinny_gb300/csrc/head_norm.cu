@@ -48,31 +48,45 @@ struct NormJob {
   float* partial;            // backward: each block's share of dg, [blocks][dim]
 };
 
-// The 16 values of a thread as 8 pairs: (a + i, b + i), or, where pairs interleave, (a + 2 i, a + 2 i + 1).
+// The 16 values of a thread as 8 pairs to turn, (a + i, b + i) or, where pairs interleave, (a + 2 i, a + 2 i + 1), two of
+// them to a register pair: a[j] holds the first members of pairs 2 j and 2 j + 1, b[j] the second ones.
+struct Pairs {
+  f32x2 a[4], b[4];
+};
+__device__ __forceinline__ float low_half(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high_half(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
 template <bool kInterleaved>
-__device__ __forceinline__ void unpack_pairs(uint4 va, uint4 vb, float (&pa)[8], float (&pb)[8]) {
-  float fa[8], fb[8];
-  unpack8(va, fa);
-  unpack8(vb, fb);
+__device__ __forceinline__ Pairs unpack_pairs(uint4 va, uint4 vb) {
+  const uint32_t w[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};
+  Pairs p;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    pa[i] = kInterleaved ? (i < 4 ? fa[2 * i] : fb[2 * i - 8]) : fa[i];
-    pb[i] = kInterleaved ? (i < 4 ? fa[2 * i + 1] : fb[2 * i - 7]) : fb[i];
+  for (int j = 0; j < 4; ++j) {
+    p.a[j] = kInterleaved ? pack2(low_half(w[2 * j]), low_half(w[2 * j + 1])) : pack2(low_half(w[j]), high_half(w[j]));
+    p.b[j] = kInterleaved ? pack2(high_half(w[2 * j]), high_half(w[2 * j + 1])) : pack2(low_half(w[4 + j]), high_half(w[4 + j]));
   }
+  return p;
 }
+// back to runs of eight values
 template <bool kInterleaved>
-__device__ __forceinline__ void runs_of(const float (&pa)[8], const float (&pb)[8], float (&fa)[8], float (&fb)[8]) {
+__device__ __forceinline__ void runs_of(const Pairs& p, float (&fa)[8], float (&fb)[8]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    fa[i] = kInterleaved ? (i & 1 ? pb[i / 2] : pa[i / 2]) : pa[i];
-    fb[i] = kInterleaved ? (i & 1 ? pb[4 + i / 2] : pa[4 + i / 2]) : pb[i];
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (kInterleaved) {
+      float* f = j < 2 ? fa + 4 * j : fb + 4 * j - 8;
+      f[0] = lo2(p.a[j]), f[1] = lo2(p.b[j]), f[2] = hi2(p.a[j]), f[3] = hi2(p.b[j]);
+    } else {
+      fa[2 * j] = lo2(p.a[j]), fa[2 * j + 1] = hi2(p.a[j]);
+      fb[2 * j] = lo2(p.b[j]), fb[2 * j + 1] = hi2(p.b[j]);
+    }
   }
 }
 
+template <int kLanesLog2 = -1>
 __device__ __forceinline__ float lanes_sum(float v, int lanes_log2) {
 #pragma unroll
   for (int k = 0; k < 5; ++k)
-    if (k < lanes_log2) v += __shfl_xor_sync(0xffffffffu, v, 1 << k);
+    if (k < (kLanesLog2 >= 0 ? kLanesLog2 : lanes_log2)) v += __shfl_xor_sync(0xffffffffu, v, 1 << k);
   return v;
 }
 
@@ -100,41 +114,104 @@ struct OwnRing {
 __device__ __forceinline__ bool out_of_range(float v) { return !(v > 0x1p-100f && v < 0x1p120f); }
 __device__ __forceinline__ float scale_of(float v) { return v >= 1.0f ? 0x1p-80f : 0x1p80f; }
 
-// What a thread holds of its head: where its runs begin and whether its pairs turn.
+// What a thread holds of its head: two runs of eight values, and whether their pairs turn.  The runs of neighbouring
+// lanes are neighbours, so that every access covers whole sectors: pairs that interleave are four to a run, the runs
+// half a head apart; otherwise a run holds eight pairs' first members and the other, half a rotation on, their
+// second ones, and past the rotated values the runs lie half of those apart.  (Both runs next to each other: the way back
+// through 8,191 tokens with interleaved pairs 72.8 us, three times the sectors.)
 struct Chunk {
-  int token, chunk, a, b;
-  bool inside, turn;
+  int token, a, b;
+  bool inside, turn_a, turn_b;  // (turn_a and turn_b are one where pairs do not interleave)
 };
 
 template <bool kInterleaved>
 __device__ __forceinline__ Chunk chunk_at(const NormJob& p, int token, int chunk) {
   Chunk h;
   h.token = min(token, p.n_tokens - 1);
-  h.chunk = chunk;
   h.inside = token < p.n_tokens && chunk < (p.dim >> 4);
-  h.turn = chunk < (p.rot >> 4);
-  const bool split = h.turn && !kInterleaved;
-  h.a = split ? 8 * chunk : 16 * chunk;
-  h.b = split ? h.a + (p.rot >> 1) : h.a + 8;
+  if (kInterleaved) {
+    h.a = 8 * chunk, h.b = h.a + (p.dim >> 1);
+    h.turn_a = h.a < p.rot, h.turn_b = h.b < p.rot;
+  } else {
+    h.turn_a = h.turn_b = chunk < (p.rot >> 4);
+    h.a = h.turn_a ? 8 * chunk : p.rot + 8 * (chunk - (p.rot >> 4));
+    h.b = h.a + ((h.turn_a ? p.rot : p.dim - p.rot) >> 1);
+  }
   if (chunk >= (p.dim >> 4)) h.a = h.b = 0;  // (a lane past the head: its copies are of nothing, from inside the row)
   return h;
 }
 
+// Place of the first members of pairs 2 j and 2 j + 1 among the head's values, from one to the next, and to the
+// second ones; and the frequency of the first.
 template <bool kInterleaved>
-__device__ __forceinline__ void load_weights(const NormJob& p, int kind, const Chunk& h, float (&ga)[8], float (&gb)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int ia = kInterleaved ? h.a + 2 * i : h.a + i, ib = kInterleaved ? h.a + 2 * i + 1 : h.b + i;
-    ga[i] = gb[i] = 0.f;
-    if (!h.inside) continue;
-    if (p.weight_f32) {
-      ga[i] = __ldg(static_cast<const float*>(p.weight[kind]) + ia);
-      gb[i] = __ldg(static_cast<const float*>(p.weight[kind]) + ib);
+struct PairAt {
+  int first, step, second, frequency;
+  __device__ __forceinline__ PairAt(const Chunk& h, int j) {
+    if (kInterleaved) {
+      first = (j < 2 ? h.a + 4 * j : h.b + 4 * j - 8), step = 2, second = first + 1, frequency = first >> 1;
     } else {
-      ga[i] = bf16_bits_to_f32(__ldg(static_cast<const uint16_t*>(p.weight[kind]) + ia));
-      gb[i] = bf16_bits_to_f32(__ldg(static_cast<const uint16_t*>(p.weight[kind]) + ib));
+      first = h.a + 2 * j, step = 1, second = h.b + 2 * j, frequency = first;
     }
   }
+};
+
+template <bool kInterleaved>
+__device__ __forceinline__ Pairs load_weights(const NormJob& p, int kind, const Chunk& h) {
+  const auto at = [&](int i) {
+    if (p.weight_f32) return __ldg(static_cast<const float*>(p.weight[kind]) + i);
+    return bf16_bits_to_f32(__ldg(static_cast<const uint16_t*>(p.weight[kind]) + i));
+  };
+  Pairs g{};
+  if (!h.inside) return g;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const PairAt<kInterleaved> i(h, j);
+    g.a[j] = pack2(at(i.first), at(i.first + i.step)), g.b[j] = pack2(at(i.second), at(i.second + i.step));
+  }
+  return g;
+}
+
+// cos and sin of a thread's pairs, times the amplitude, two of them to a register pair.
+template <bool kInterleaved>
+__device__ __forceinline__ void load_angles(const NormJob& p, const Chunk& h, f32x2 (&c)[4], f32x2 (&s)[4]) {
+  if (!h.turn_a) return;  // (turn_b implies turn_a)
+  const int pos = __ldg(p.positions + h.token);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (kInterleaved && j >= 2 && !h.turn_b) break;
+    const PairAt<kInterleaved> i(h, j);
+    float c0, c1, s0, s1;
+    angle_of(p.inv_freq, p.amplitude, false, pos, i.frequency, c0, s0);
+    angle_of(p.inv_freq, p.amplitude, false, pos, i.frequency + 1, c1, s1);
+    c[j] = pack2(c0, c1), s[j] = pack2(s0, s1);
+  }
+}
+// whether pairs 2 j and 2 j + 1 turn
+template <bool kInterleaved>
+__device__ __forceinline__ bool turns(const Chunk& h, int j) {
+  return kInterleaved && j >= 2 ? h.turn_b : h.turn_a;
+}
+
+__device__ __forceinline__ f32x2 negative2(f32x2 v) { return v ^ 0x8000000080000000ull; }
+__device__ __forceinline__ f32x2 both2(float v) { return pack2(v, v); }
+__device__ __forceinline__ float sum2(f32x2 v) { return lo2(v) + hi2(v); }
+
+// This thread's share of the head's sum of squares.
+__device__ __forceinline__ float squares_of(const Pairs& x) {
+  f32x2 s = mul2(x.a[0], x.a[0]), t = mul2(x.b[0], x.b[0]);
+#pragma unroll
+  for (int j = 1; j < 4; ++j) s = fma2(x.a[j], x.a[j], s), t = fma2(x.b[j], x.b[j], t);
+  return sum2(add2(s, t));
+}
+__device__ __forceinline__ float products_of(const Pairs& u, const Pairs& g, const Pairs& x) {
+  f32x2 s = mul2(mul2(u.a[0], g.a[0]), x.a[0]), t = mul2(mul2(u.b[0], g.b[0]), x.b[0]);
+#pragma unroll
+  for (int j = 1; j < 4; ++j) s = fma2(mul2(u.a[j], g.a[j]), x.a[j], s), t = fma2(mul2(u.b[j], g.b[j]), x.b[j], t);
+  return sum2(add2(s, t));
+}
+__device__ __forceinline__ void scale_pairs(Pairs& x, float by) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) x.a[j] = mul2(x.a[j], both2(by)), x.b[j] = mul2(x.b[j], both2(by));
 }
 
 enum { kToRows = 0, kToBf16 = 1, kToE4M3 = 2 };  // where keys and values go
@@ -157,7 +234,7 @@ __global__ void __launch_bounds__(kNormThreads, 8) norm_rope_kernel(const NormJo
   int64_t slot = 0;
   if (to_cache) {
     slot = __ldg(p.slots + h.token);
-    if (slot >= p.n_slots && live && h.chunk == 0) atomicOr(&g_device_error, kErrPage);
+    if (slot >= p.n_slots && live && h.a == 0) atomicOr(&g_device_error, kErrPage);
     live = live && slot >= 0 && slot < p.n_slots;
   }
   const uint16_t* x = p.x[kind] + h.token * p.x_stride[kind] + h0 * p.dim;
@@ -170,13 +247,18 @@ __global__ void __launch_bounds__(kNormThreads, 8) norm_rope_kernel(const NormJo
   };
 #pragma unroll
   for (int i = 0; i < ring.kAhead; ++i) fetch(i);
-  float c[8], s[8], ga[8], gb[8];
+  // a turned pair is ((xa ga c - xb gb s) r, (xb gb c + xa ga s) r): the weights are multiplied in once for all heads
+  Pairs along{}, across{};
   if (kind < 2) {
-    load_weights<kInterleaved>(p, kind, h, ga, gb);
-    if (h.turn) {
-      const int pos = __ldg(p.positions + h.token);
+    along = load_weights<kInterleaved>(p, kind, h);
+    f32x2 c[4], s[4];
+    load_angles<kInterleaved>(p, h, c, s);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) angle_of(p.inv_freq, p.amplitude, false, pos, 8 * h.chunk + i, c[i], s[i]);
+    for (int j = 0; j < 4; ++j) {
+      if (turns<kInterleaved>(h, j)) {
+        across.a[j] = mul2(along.a[j], s[j]), across.b[j] = negative2(mul2(along.b[j], s[j]));
+        along.a[j] = mul2(along.a[j], c[j]), along.b[j] = mul2(along.b[j], c[j]);
+      }
     }
   }
   // element offset of (slot, head 0) in a pool, and from one head to the next
@@ -200,33 +282,23 @@ __global__ void __launch_bounds__(kNormThreads, 8) norm_rope_kernel(const NormJo
       unpack8(va, fa);
       unpack8(vb, fb);
     } else {
-      float pa[8], pb[8];
-      unpack_pairs<kInterleaved>(va, vb, pa, pb);
-      float ss = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(pa[i], pa[i], fmaf(pb[i], pb[i], ss));
-      ss = lanes_sum(ss, p.lanes_log2);
-      float v = fmaf(ss, p.inv_dim, p.eps);
+      Pairs x = unpack_pairs<kInterleaved>(va, vb);
+      float v = fmaf(lanes_sum(squares_of(x), p.lanes_log2), p.inv_dim, p.eps);
       const bool odd = out_of_range(v);
       if (__any_sync(0xffffffffu, odd)) {
         const float unit = odd ? scale_of(v) : 1.0f;
-        ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          pa[i] *= unit, pb[i] *= unit;
-          ss = fmaf(pa[i], pa[i], fmaf(pb[i], pb[i], ss));
-        }
-        v = fmaf(lanes_sum(ss, p.lanes_log2), p.inv_dim, p.eps * unit * unit);
+        scale_pairs(x, unit);
+        v = fmaf(lanes_sum(squares_of(x), p.lanes_log2), p.inv_dim, p.eps * unit * unit);
       }
-      const float r = rsqrtf(v);
+      const f32x2 r = both2(rsqrtf(v));
       if (!live) continue;  // (the shuffles are done: the next head's are taken by all lanes again)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float na = pa[i] * r * ga[i], nb = pb[i] * r * gb[i];
-        pa[i] = h.turn ? na * c[i] - nb * s[i] : na;
-        pb[i] = h.turn ? nb * c[i] + na * s[i] : nb;
+      for (int j = 0; j < 4; ++j) {
+        f32x2 ya = mul2(x.a[j], along.a[j]), yb = mul2(x.b[j], along.b[j]);
+        if (turns<kInterleaved>(h, j)) ya = fma2(x.b[j], across.b[j], ya), yb = fma2(x.a[j], across.a[j], yb);
+        x.a[j] = mul2(ya, r), x.b[j] = mul2(yb, r);
       }
-      runs_of<kInterleaved>(pa, pb, fa, fb);
+      runs_of<kInterleaved>(x, fa, fb);
     }
     if (kTo == kToE4M3 && to_cache) {
       const HeadScale sc = head_scale(p.scale[kind - 1] ? __ldg(p.scale[kind - 1] + hh) : 1.0f);
@@ -239,123 +311,140 @@ __global__ void __launch_bounds__(kNormThreads, 8) norm_rope_kernel(const NormJo
   }
 }
 
-template <bool kInterleaved>
-__global__ void __launch_bounds__(kNormThreads, 4) norm_rope_backward_kernel(const NormJob p) {
+// Each block takes a contiguous range of units, all of them of a size: one head of the tokens that the block holds at once.
+// They are numbered by kind (queries, then keys), tokens, heads, so that a block walks the heads of its tokens with the
+// same angles and changes from queries to keys at most once.
+struct BackwardUnits {
+  int per_block, blocks;      // units of a block (the last one may have fewer)
+  int64_t of_q, all;
+  int shares_q, shares_k;     // blocks with units of q, of k
+  int first_k;                // the first of the latter
+};
+
+// kLanesLog2: lanes of a head whose chunks fill them (64, 128 and 256 values), or -1: any head.
+template <bool kInterleaved, int kLanesLog2>
+__global__ void __launch_bounds__(kNormThreads, 4) norm_rope_backward_kernel(const NormJob p, const BackwardUnits units) {
   __shared__ __align__(16) uint8_t ring_bytes[OwnRing<4>::kBytes];
-  static_assert(sizeof(ring_bytes) >= kNormThreads * 16 * sizeof(float), "the sums at the end");
-  float* const sums = reinterpret_cast<float*>(ring_bytes);  // [tokens of the block][dim], after the loop
+  __shared__ float sums[kNormThreads * 16];  // [tokens of the block][dim]
   const OwnRing<4> ring{smem_addr(ring_bytes)};
   pdl_wait();
   pdl_launch_dependents();
-  const int lanes = 1 << p.lanes_log2, at_once = kNormThreads >> p.lanes_log2;
-  const int sub = threadIdx.x >> p.lanes_log2, chunk = threadIdx.x & (lanes - 1);
-  const int g = static_cast<int>(blockIdx.y) - p.groups[0], kind = g >= 0 ? 1 : 0;
-  const int h0 = (kind ? g : static_cast<int>(blockIdx.y)) * p.per_thread, h1 = min(p.heads[kind], h0 + p.per_thread);
-  Chunk h = chunk_at<kInterleaved>(p, 0, chunk);
-  float ga[8], gb[8], acc_a[8], acc_b[8];
-  load_weights<kInterleaved>(p, kind, h, ga, gb);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) acc_a[i] = acc_b[i] = 0.f;
-  const int step = static_cast<int>(gridDim.x) * at_once, first = static_cast<int>(blockIdx.x) * at_once;
-  // the copies run through the same tokens and heads, ahead of the loop
-  int copied = 0, copy_t = first, copy_h = h0;
+  const int lanes_log2 = kLanesLog2 >= 0 ? kLanesLog2 : p.lanes_log2, dim = kLanesLog2 >= 0 ? 16 << kLanesLog2 : p.dim;
+  const int at_once = kNormThreads >> lanes_log2;
+  const int sub = threadIdx.x >> lanes_log2, chunk = threadIdx.x & ((1 << lanes_log2) - 1);
+  int64_t u = static_cast<int64_t>(blockIdx.x) * units.per_block;
+  const int64_t end = min(u + units.per_block, units.all);
+  int kind = u >= units.of_q ? 1 : 0;
+  const int64_t nth = kind ? u - units.of_q : u;
+  const int64_t step0 = nth / p.heads[kind];
+  int token0 = static_cast<int>(step0) * at_once, head = static_cast<int>(nth - step0 * p.heads[kind]);
+
+  // the copies run through the same units, ahead of the loop
+  int to_copy = static_cast<int>(end - u), copied = 0, ahead_kind = kind, ahead_token0 = token0, ahead_left = 0;
+  const uint16_t *x_from = nullptr, *dy_from = nullptr;
+  uint32_t bytes = 0;
+  const Chunk here = chunk_at<kInterleaved>(p, 0, chunk);  // (its runs are those of every token)
+  const auto copy_from = [&](int first_head) {
+    const int token = min(ahead_token0 + sub, p.n_tokens - 1);
+    bytes = here.inside && ahead_token0 + sub < p.n_tokens ? 16 : 0;
+    x_from = p.x[ahead_kind] + token * p.x_stride[ahead_kind] + first_head * dim;
+    dy_from = p.dy[ahead_kind] + token * p.dy_stride[ahead_kind] + first_head * dim;
+    ahead_left = p.heads[ahead_kind] - first_head;
+  };
+  copy_from(head);
   const auto fetch = [&]() {
-    if (copy_t < p.n_tokens) {
-      const Chunk f = chunk_at<kInterleaved>(p, copy_t + sub, chunk);
-      const uint16_t* x = p.x[kind] + f.token * p.x_stride[kind] + copy_h * p.dim;
-      const uint16_t* dy = p.dy[kind] + f.token * p.dy_stride[kind] + copy_h * p.dim;
-      const uint32_t bytes = f.inside ? 16 : 0;
-      ring.copy(copied, 0, x + f.a, bytes);
-      ring.copy(copied, 1, x + f.b, bytes);
-      ring.copy(copied, 2, dy + f.a, bytes);
-      ring.copy(copied, 3, dy + f.b, bytes);
+    if (copied < to_copy) {
+      ring.copy(copied, 0, x_from + here.a, bytes);
+      ring.copy(copied, 1, x_from + here.b, bytes);
+      ring.copy(copied, 2, dy_from + here.a, bytes);
+      ring.copy(copied, 3, dy_from + here.b, bytes);
       ++copied;
-      if (++copy_h == h1) copy_h = h0, copy_t += step;
+      x_from += dim, dy_from += dim;
+      if (--ahead_left == 0 && copied < to_copy) {  // the next tokens; after the last ones of q, k's first
+        ahead_token0 += at_once;
+        if (ahead_token0 >= p.n_tokens) ahead_kind = 1, ahead_token0 = 0;
+        copy_from(0);
+      }
     }
     ring.commit();
   };
 #pragma unroll
   for (int i = 0; i < ring.kAhead; ++i) fetch();
   int at = 0;
-  for (int t0 = first; t0 < p.n_tokens; t0 += step) {
-    h = chunk_at<kInterleaved>(p, t0 + sub, chunk);
-    float c[8], s[8];
-    if (h.turn) {
-      const int pos = __ldg(p.positions + h.token);
+  for (; u < end; kind = 1, token0 = 0, head = 0) {
+    const Pairs g = load_weights<kInterleaved>(p, kind, here);
+    Pairs acc{};
+    const int64_t kind_end = kind ? end : min(end, units.of_q);
+    for (; u < kind_end; token0 += at_once, head = 0) {
+      const Chunk h = chunk_at<kInterleaved>(p, token0 + sub, chunk);
+      f32x2 c[4], s[4];
+      load_angles<kInterleaved>(p, h, c, s);
+      uint16_t* dx = p.y[kind] + h.token * p.y_stride[kind] + head * dim;
+      const int heads = static_cast<int>(min(static_cast<int64_t>(p.heads[kind] - head), kind_end - u));
+      u += heads;
+      for (const int last = at + heads; at < last; ++at, dx += dim) {
+        ring.arrived();
+        Pairs x = unpack_pairs<kInterleaved>(ring.read(at, 0), ring.read(at, 1));
+        Pairs d = unpack_pairs<kInterleaved>(ring.read(at, 2), ring.read(at, 3));
+        fetch();
 #pragma unroll
-      for (int i = 0; i < 8; ++i) angle_of(p.inv_freq, p.amplitude, false, pos, 8 * chunk + i, c[i], s[i]);
-    }
-    uint16_t* dx = p.y[kind] + h.token * p.y_stride[kind];
-    for (int hh = h0; hh < h1; ++hh, ++at) {
-      ring.arrived();
-      const uint4 v[4] = {ring.read(at, 0), ring.read(at, 1), ring.read(at, 2), ring.read(at, 3)};
-      fetch();
-      float pa[8], pb[8], ua[8], ub[8];
-      unpack_pairs<kInterleaved>(v[0], v[1], pa, pb);
-      unpack_pairs<kInterleaved>(v[2], v[3], ua, ub);
-      if (h.turn) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float u = ua[i] * c[i] + ub[i] * s[i];
-          ub[i] = ub[i] * c[i] - ua[i] * s[i];
-          ua[i] = u;
+        for (int j = 0; j < 4; ++j) {
+          if (!turns<kInterleaved>(h, j)) continue;
+          const f32x2 t = fma2(d.b[j], s[j], mul2(d.a[j], c[j]));
+          d.b[j] = fma2(d.a[j], negative2(s[j]), mul2(d.b[j], c[j]));
+          d.a[j] = t;
         }
-      }
-      float ss = 0.f, zx = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        ss = fmaf(pa[i], pa[i], fmaf(pb[i], pb[i], ss));
-        zx = fmaf(ua[i] * ga[i], pa[i], fmaf(ub[i] * gb[i], pb[i], zx));
-      }
-      ss = lanes_sum(ss, p.lanes_log2);
-      zx = lanes_sum(zx, p.lanes_log2);
-      float var = fmaf(ss, p.inv_dim, p.eps), unit = 1.0f;
-      const bool odd = out_of_range(var);
-      if (__any_sync(0xffffffffu, odd)) {
-        unit = odd ? scale_of(var) : 1.0f;
-        ss = zx = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          pa[i] *= unit, pb[i] *= unit;
-          ss = fmaf(pa[i], pa[i], fmaf(pb[i], pb[i], ss));
-          zx = fmaf(ua[i] * ga[i], pa[i], fmaf(ub[i] * gb[i], pb[i], zx));
+        float zx = lanes_sum<kLanesLog2>(products_of(d, g, x), lanes_log2), unit = 1.0f;
+        float v = fmaf(lanes_sum<kLanesLog2>(squares_of(x), lanes_log2), p.inv_dim, p.eps);
+        const bool odd = out_of_range(v);
+        if (__any_sync(0xffffffffu, odd)) {
+          unit = odd ? scale_of(v) : 1.0f;
+          scale_pairs(x, unit);
+          v = fmaf(lanes_sum<kLanesLog2>(squares_of(x), lanes_log2), p.inv_dim, p.eps * unit * unit);
+          zx = lanes_sum<kLanesLog2>(products_of(d, g, x), lanes_log2);
         }
-        var = fmaf(lanes_sum(ss, p.lanes_log2), p.inv_dim, p.eps * unit * unit);
-        zx = lanes_sum(zx, p.lanes_log2);
-      }
-      const float r = rsqrtf(var), along = zx * p.inv_dim * r, out = r * unit;
-      if (!h.inside) continue;
+        // dx = out (z - x r along), along = mean(z x r)
+        const float r = rsqrtf(v), along = zx * p.inv_dim * r, out = r * unit;
+        if (!h.inside) continue;
+        const f32x2 r2 = both2(r), out2 = both2(out), less2 = both2(-along * r);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float na = pa[i] * r, nb = pb[i] * r;
-        acc_a[i] = fmaf(ua[i], na, acc_a[i]);
-        acc_b[i] = fmaf(ub[i], nb, acc_b[i]);
-        ua[i] = out * (ua[i] * ga[i] - na * along);
-        ub[i] = out * (ub[i] * gb[i] - nb * along);
+        for (int j = 0; j < 4; ++j) {
+          acc.a[j] = fma2(d.a[j], mul2(x.a[j], r2), acc.a[j]);
+          acc.b[j] = fma2(d.b[j], mul2(x.b[j], r2), acc.b[j]);
+          d.a[j] = mul2(fma2(x.a[j], less2, mul2(d.a[j], g.a[j])), out2);
+          d.b[j] = mul2(fma2(x.b[j], less2, mul2(d.b[j], g.b[j])), out2);
+        }
+        float fa[8], fb[8];
+        runs_of<kInterleaved>(d, fa, fb);
+        *reinterpret_cast<uint4*>(dx + h.a) = pack8(fa);
+        *reinterpret_cast<uint4*>(dx + h.b) = pack8(fb);
       }
-      float fa[8], fb[8];
-      runs_of<kInterleaved>(ua, ub, fa, fb);
-      *reinterpret_cast<uint4*>(dx + hh * p.dim + h.a) = pack8(fa);
-      *reinterpret_cast<uint4*>(dx + hh * p.dim + h.b) = pack8(fb);
+    }
+    // this block's share of dg: its tokens one after the other
+    __syncthreads();  // (the last share has been read)
+    if (here.inside) {
+      float* mine = sums + sub * dim;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const PairAt<kInterleaved> i(here, j);
+        mine[i.first] = lo2(acc.a[j]), mine[i.first + i.step] = hi2(acc.a[j]);
+        mine[i.second] = lo2(acc.b[j]), mine[i.second + i.step] = hi2(acc.b[j]);
+      }
+    }
+    __syncthreads();
+    const int share = kind ? units.shares_q + static_cast<int>(blockIdx.x) - units.first_k : static_cast<int>(blockIdx.x);
+    for (int i = threadIdx.x; i < dim; i += kNormThreads) {
+      float sum = 0.f;
+      for (int t = 0; t < at_once; ++t) sum += sums[t * dim + i];
+      p.partial[static_cast<int64_t>(share) * dim + i] = sum;
     }
   }
-  // this block's share of dg: its tokens one after the other
-  __syncthreads();  // (where the ring was)
-  if (chunk < (p.dim >> 4)) {
-    float* mine = sums + sub * p.dim;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      mine[kInterleaved ? h.a + 2 * i : h.a + i] = acc_a[i];
-      mine[kInterleaved ? h.a + 2 * i + 1 : h.b + i] = acc_b[i];
-    }
-  }
-  __syncthreads();
-  float* share = p.partial + (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * p.dim;
-  for (int i = threadIdx.x; i < p.dim; i += kNormThreads) {
-    float sum = 0.f;
-    for (int t = 0; t < at_once; ++t) sum += sums[t * p.dim + i];
-    share[i] = sum;
-  }
+}
+
+template <bool kInterleaved>
+auto backward_kernel(int dim) {
+  return dim == 64 ? norm_rope_backward_kernel<kInterleaved, 2> : dim == 128 ? norm_rope_backward_kernel<kInterleaved, 3>
+         : dim == 256 ? norm_rope_backward_kernel<kInterleaved, 4> : norm_rope_backward_kernel<kInterleaved, -1>;
 }
 
 // dg of q and k from the blocks' shares, in their order: a block for 32 columns of one of them, a
@@ -411,21 +500,19 @@ nvfp4_status launch_norm(NormJob p, int to, bool interleaved, cudaStream_t strea
   return launched();
 }
 
-// The backward grid: heads a thread walks, blocks over tokens and over heads.
-struct BackwardPlan {
-  int per_thread, groups[2], blocks;
-  int shares() const { return (groups[0] + groups[1]) * blocks; }
-};
-BackwardPlan backward_plan(int n_tokens, int n_heads, int n_kv_heads, int dim) {
-  BackwardPlan b;
-  const int lanes_log2 = lanes_log2_of(dim);
-  const int64_t threads = static_cast<int64_t>(n_tokens) << lanes_log2;
-  b.per_thread = 8;
-  while (b.per_thread > 1 && threads * (n_heads + n_kv_heads) / b.per_thread < int64_t{152} * 512) b.per_thread /= 2;
-  b.groups[0] = (n_heads + b.per_thread - 1) / b.per_thread;
-  b.groups[1] = (n_kv_heads + b.per_thread - 1) / b.per_thread;
-  const int64_t all = (threads + kNormThreads - 1) / kNormThreads, fill = 152 * 4 / (b.groups[0] + b.groups[1]);
-  b.blocks = static_cast<int>(all < fill ? all : (fill < 1 ? 1 : fill));
+// The backward grid: as many blocks as the chip holds, or one for every four units where there are fewer.
+BackwardUnits backward_units(int n_tokens, int n_heads, int n_kv_heads, int dim) {
+  BackwardUnits b{};
+  const int at_once = kNormThreads >> lanes_log2_of(dim);
+  const int64_t steps = (n_tokens + at_once - 1) / at_once;
+  b.of_q = steps * n_heads, b.all = steps * (n_heads + n_kv_heads);
+  if (b.all == 0) return b;
+  const int64_t most = 152 * 4, wanted = (b.all + 3) / 4, blocks = wanted < most ? wanted : most;
+  b.per_block = static_cast<int>((b.all + blocks - 1) / blocks);
+  b.blocks = static_cast<int>((b.all + b.per_block - 1) / b.per_block);
+  b.shares_q = static_cast<int>((b.of_q + b.per_block - 1) / b.per_block);
+  b.first_k = static_cast<int>(b.of_q / b.per_block);
+  b.shares_k = n_kv_heads > 0 ? b.blocks - b.first_k : 0;
   return b;
 }
 
@@ -526,8 +613,8 @@ nvfp4_status kv_append_norm(const nvfp4_kv_cache* cache, const nvfp4_qk_norm* no
 
 size_t qk_norm_rope_workspace_bytes(int32_t n_tokens, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim) {
   if (!norm_sizes_ok(n_tokens, n_heads, n_kv_heads, head_dim)) return 0;
-  const BackwardPlan b = backward_plan(n_tokens, n_heads, n_kv_heads, head_dim);
-  return (static_cast<size_t>(b.shares()) * head_dim + 4) * sizeof(float);
+  const BackwardUnits b = backward_units(n_tokens, n_heads, n_kv_heads, head_dim);
+  return (static_cast<size_t>(b.shares_q + b.shares_k) * head_dim + 4) * sizeof(float);
 }
 
 nvfp4_status qk_norm_rope_backward(const nvfp4_qk_norm* norm, const uint16_t* dq, int64_t dq_stride, const uint16_t* q,
@@ -555,8 +642,7 @@ nvfp4_status qk_norm_rope_backward(const nvfp4_qk_norm* norm, const uint16_t* dq
                                              NVFP4_ROPE_INTERLEAVED))
     return st;
   if (!ws || ws_bytes < qk_norm_rope_workspace_bytes(n_tokens, n_heads, n_kv_heads, head_dim)) return NVFP4_ERR_WORKSPACE;
-  const BackwardPlan b = backward_plan(n_tokens, n_heads, n_kv_heads, head_dim);
-  if (b.groups[0] + b.groups[1] > 65535) return NVFP4_ERR_SHAPE;
+  const BackwardUnits b = backward_units(n_tokens, n_heads, n_kv_heads, head_dim);
   NormJob p{};
   set_norm(p, norm);
   p.x[0] = q, p.x_stride[0] = q_stride, p.heads[0] = n_heads;
@@ -566,17 +652,15 @@ nvfp4_status qk_norm_rope_backward(const nvfp4_qk_norm* norm, const uint16_t* dq
   p.positions = positions, p.inv_freq = inv_freq, p.amplitude = amplitude;
   p.n_tokens = n_tokens, p.dim = head_dim, p.rot = rot_dim;
   p.lanes_log2 = lanes_log2_of(head_dim), p.inv_dim = 1.0f / static_cast<float>(head_dim);
-  p.per_thread = b.per_thread, p.groups[0] = b.groups[0], p.groups[1] = b.groups[1];
   p.partial = static_cast<float*>(ws);
   // (without tokens there are no shares, and dg is zero)
   if (n_tokens > 0 &&
-      launch_pdl((flags & NVFP4_ROPE_INTERLEAVED) ? norm_rope_backward_kernel<true> : norm_rope_backward_kernel<false>,
-                 dim3(b.blocks, b.groups[0] + b.groups[1]), dim3(kNormThreads), 0, stream, p) != cudaSuccess)
+      launch_pdl((flags & NVFP4_ROPE_INTERLEAVED) ? backward_kernel<true>(head_dim) : backward_kernel<false>(head_dim),
+                 dim3(b.blocks), dim3(kNormThreads), 0, stream, p, b) != cudaSuccess)
     return NVFP4_ERR_CUDA;
-  const int shares = n_tokens > 0 ? b.blocks : 0;
   if (launch_pdl(norm_weight_kernel, dim3((head_dim + kJoinColumns - 1) / kJoinColumns, with_k ? 2 : 1),
-                 dim3(kJoinColumns * kJoinSlices), 0, stream, static_cast<const float*>(p.partial), head_dim,
-                 b.groups[0] * shares, b.groups[1] * shares, dq_weight, dk_weight) != cudaSuccess)
+                 dim3(kJoinColumns * kJoinSlices), 0, stream, static_cast<const float*>(p.partial), head_dim, b.shares_q,
+                 b.shares_k, dq_weight, dk_weight) != cudaSuccess)
     return NVFP4_ERR_CUDA;
   return launched();
 }
