@@ -87,6 +87,19 @@ def test_trees(lib, words, sizes):
     s.check(lib, sizes, rows, parents + [-1, 5, -9, 1 << 30, 2], words)
 
 
+@pytest.mark.parametrize("seqs,rows", [(256, 512), (257, 512), (256, 513), (1, 512), (1, 513), (1024, 1100), (1025, 1100), (14336, 15000), (14337, 15000),
+                                       (16384, 17000)])
+def test_either_side_of_every_limit(lib, seqs, rows):
+    """One CTA or eight, requests in one round of the block or more, kept in shared memory or not; rows that run out too."""
+    rng = random.Random(seqs + rows)
+    kv_len = [rng.randint(0, 40) for _ in range(seqs)]
+    new = [rng.choice([-1, 0, 1, 1, 1]) for _ in range(seqs)]
+    s = State(kv_len, 5, 16, extra=1, spare=seqs)
+    s.check(lib, new, rows)
+    new = [rng.choice([0, 1, 2]) for _ in range(seqs)] if seqs > 1 else [rows]
+    s.check(lib, new, rows, error=sum(new) > rows or (seqs == 1 and s.kv_len[0] + rows > 80))
+
+
 def test_chains_stars_and_forests(lib):
     n = 64
     for parents in (list(range(-1, n - 1)), [-1] * n, [-1] + [0] * (n - 1), [i // 2 - 1 if i > 1 else -1 for i in range(n)]):
