@@ -369,16 +369,16 @@ def _rows(x: torch.Tensor, what: str, device) -> int:
 
 def _norm(q_norm, k_norm, dim: int, eps: float, device) -> CQKNorm:
     """The norm weights of a call: bf16 or fp32 [dim], both of one type (None: not used)."""
-    kind = None
-    for w in (q_norm, k_norm):
-        if w is None:
-            continue
-        if w.shape != (dim,) or w.device != device or w.stride(0) != 1 or w.dtype is not (kind or w.dtype):
-            raise ValueError("q_norm and k_norm: contiguous [head_dim] on the call's GPU, of one type")
-        kind = w.dtype
+    some = k_norm if q_norm is None else q_norm
+    kind = None if some is None else some.dtype
     if kind is not torch.bfloat16 and kind is not torch.float32:
         raise ValueError("q_norm and k_norm: bf16 or fp32")
-    return CQKNorm(_ptr(q_norm), _ptr(k_norm), NVFP4_NORM_BF16 if kind is torch.bfloat16 else NVFP4_NORM_FP32, eps)
+    shape = (dim,)
+    for w in (q_norm, k_norm):
+        if w is not None and (w.dtype is not kind or w.shape != shape or w.stride(0) != 1 or w.device != device):
+            raise ValueError("q_norm and k_norm: contiguous [head_dim] on the call's GPU, of one type")
+    return CQKNorm(None if q_norm is None else q_norm.data_ptr(), None if k_norm is None else k_norm.data_ptr(),
+                   NVFP4_NORM_BF16 if kind is torch.bfloat16 else NVFP4_NORM_FP32, eps)
 
 
 def _index(x: torch.Tensor, n: int, dtype, what: str, device) -> int:
@@ -677,27 +677,32 @@ class Library:
         dev = cache.device
         if dev.index != _current_device() or stream is not None:
             _on_current(dev, stream)
-        tokens, heads, dim = k.shape
-        _need(k.shape == v.shape and heads == cache.n_kv_heads and dim == cache.head_dim,
-              "k and v: [tokens, n_kv_heads, head_dim] of the cache")
+        shape = k.shape
+        tokens, heads, dim = shape
+        if v.shape != shape or heads != cache.n_kv_heads or dim != cache.head_dim:
+            raise ValueError("k and v: [tokens, n_kv_heads, head_dim] of the cache")
         pos = freq = None
         rot = 0
         if inv_freq is not None:
             _need(positions is not None, "positions are needed with inv_freq")
-            rot = 2 * inv_freq.shape[0]
-            freq = _index(inv_freq, inv_freq.shape[0], torch.float64, "inv_freq", dev)
+            pairs = inv_freq.shape[0]
+            rot = 2 * pairs
+            freq = _index(inv_freq, pairs, torch.float64, "inv_freq", dev)
             pos = _index(positions, tokens, torch.int32, "positions", dev)
         q_ptr = out_ptr = None
         q_heads = q_stride = out_stride = 0
         if q is not None:
-            q_heads = q.shape[1]
-            _need(q.shape == (tokens, q_heads, dim), "q: [tokens, heads, head_dim] of the cache")
+            shape = q.shape
+            q_heads = shape[1]
+            if shape != (tokens, q_heads, dim):
+                raise ValueError("q: [tokens, heads, head_dim] of the cache")
             q_ptr, q_stride = q.data_ptr(), _rows(q, "q", dev)
             if q_out is None:
-                q_out = _empty((tokens, q_heads, dim), torch.bfloat16, dev, stream)
+                q_out = (torch.empty(shape, dtype=torch.bfloat16, device=dev) if stream is None
+                         else _empty(shape, torch.bfloat16, dev, stream))
                 out_stride = q_heads * dim
             else:
-                _need(q_out.shape == q.shape, "q_out: the shape of q")
+                _need(q_out.shape == shape, "q_out: the shape of q")
                 out_stride = _rows(q_out, "q_out", dev)
             out_ptr = q_out.data_ptr()
         if k_norm is not None or q_norm is not None:
@@ -855,13 +860,17 @@ class Library:
         if dev.index != _current_device() or stream is not None:
             _on_current(dev, stream)
         n = batch.n_seqs
-        if (paths.dim() != 2 or paths.shape[0] != n or paths.dtype is not torch.int32 or paths.device != dev
+        shape = paths.shape
+        if (len(shape) != 2 or shape[0] != n or paths.dtype is not torch.int32 or paths.device != dev
                 or not paths.is_contiguous() or batch.device != dev):
             raise ValueError("paths: contiguous int32 [n_seqs, most] on the cache's GPU; the batch on it")
         if out is None:
-            out = _empty((n,), torch.int32, dev, stream)
-        st = self.lib.kv_accept(cache.ref, batch.ref, paths.data_ptr(), paths.shape[1],
-                                _index(out, n, torch.int32, "out", dev), _raw_stream(stream, dev))
+            out = (torch.empty((n,), dtype=torch.int32, device=dev) if stream is None
+                   else _empty((n,), torch.int32, dev, stream))
+            out_ptr = out.data_ptr()
+        else:
+            out_ptr = _index(out, n, torch.int32, "out", dev)
+        st = self.lib.kv_accept(cache.ref, batch.ref, paths.data_ptr(), shape[1], out_ptr, _raw_stream(stream, dev))
         if st:
             raise NVFP4Error("kv_accept", st)
         if stream is not None:
@@ -931,10 +940,13 @@ class Library:
             raise ValueError("q: [tokens, heads, head_dim] of the cache; the batch on its GPU")
         if not -2 ** 31 <= window < 2 ** 31:
             raise ValueError("window: beyond 32 bits")
-        if masks.dim() != 2 or masks.shape[0] != tokens or masks.dtype is not torch.int64 or masks.device != dev or not masks.is_contiguous():
+        rows = masks.shape
+        if (len(rows) != 2 or rows[0] != tokens or masks.dtype is not torch.int64 or masks.device != dev
+                or not masks.is_contiguous()):
             raise ValueError("masks: contiguous int64 [tokens, words] on the call's GPU")
         if out is None:
-            out = _empty(shape, torch.bfloat16, dev, stream)
+            out = (torch.empty(shape, dtype=torch.bfloat16, device=dev) if stream is None
+                   else _empty(shape, torch.bfloat16, dev, stream))
             out_stride = heads * dim
         else:
             _need(out.shape == shape, "out: the shape of q")
@@ -945,7 +957,8 @@ class Library:
                   and lse.device == dev, "lse: contiguous fp32 [tokens, heads]")
             lse_ptr = lse.data_ptr()
         elif with_lse:
-            lse = _empty((tokens, heads), torch.float32, dev, stream)
+            lse = (torch.empty((tokens, heads), dtype=torch.float32, device=dev) if stream is None
+                   else _empty((tokens, heads), torch.float32, dev, stream))
             lse_ptr = lse.data_ptr()
         raw = _raw_stream(stream, dev)
         sizes = (tokens, batch.n_seqs, batch.max_new, heads, cache.n_kv_heads, dim)
@@ -956,7 +969,7 @@ class Library:
             nbytes = self._tree_bytes[sizes] = self.lib.tree_attention_workspace_bytes(*sizes)
         ws, ws_ptr, ws_bytes = self._stream_workspace(nbytes, dev, raw, stream)
         st = self.lib.tree_attention(
-            cache.ref, batch.ref, masks.data_ptr(), masks.shape[1], q.data_ptr(), stride, tokens, heads, dim ** -0.5 if scale is None else scale, softcap,
+            cache.ref, batch.ref, masks.data_ptr(), rows[1], q.data_ptr(), stride, tokens, heads, dim ** -0.5 if scale is None else scale, softcap,
             window, out.data_ptr(), out_stride, lse_ptr, ws_ptr, ws_bytes, raw)
         if st:
             raise NVFP4Error("tree_attention", st)
