@@ -32,11 +32,11 @@ bool encode_pool_map(CUtensorMap* map, const nvfp4_kv_cache* c, void* base, int 
 // The maps of both pools for the kernel and tile of `s`.
 bool encode_maps(KvMaps* maps, const nvfp4_kv_cache* c, const AttnShape& s) {
   const int box = std::min(c->page_size, s.box_keys);
-  return encode_pool_map(&maps->k, c, c->k, box, !s.chunk) && encode_pool_map(&maps->v, c, c->v, box, !s.chunk);
+  return encode_pool_map(&maps->k, c, c->k, box, s.whole_rows) && encode_pool_map(&maps->v, c, c->v, box, s.whole_rows);
 }
 
-AttnShape shape_of(int dim, bool fp8, int64_t rows, int64_t items, bool tree) {
-  return tree ? tree_shape(dim, fp8, rows, items) : attn_shape(dim, fp8, rows, items);
+AttnShape shape_of(int dim, bool fp8, int64_t rows, int64_t items, bool tree, int page_size) {
+  return tree ? tree_shape(dim, fp8, rows, items, page_size) : attn_shape(dim, fp8, rows, items);
 }
 
 size_t attn_workspace(int n_tokens, int n_seqs, int max_new, int n_heads, int n_kv_heads, int head_dim, bool tree) {
@@ -44,8 +44,8 @@ size_t attn_workspace(int n_tokens, int n_seqs, int max_new, int n_heads, int n_
   size_t most = 0;
   for (const bool fp8 : {false, true}) {  // (the caller need not say which)
     const AttnShape s = shape_of(head_dim, fp8, packed_rows(n_tokens, max_new, n_heads, n_kv_heads),
-                                 static_cast<int64_t>(n_seqs) * n_kv_heads, tree);
-    const size_t grid = kAttnGrid * (s.chunk ? 1 : attn_ctas(head_dim, false, s.rw));
+                                 static_cast<int64_t>(n_seqs) * n_kv_heads, tree, 64);
+    const size_t grid = kAttnGrid * (s.chunk ? (s.pair ? 2 : 1) : attn_ctas(head_dim, false, s.rw));
     most = std::max(most, 2 * grid * s.tile_rows * (head_dim + 2));  // sums of a row tile, references and sums of weights
   }
   return kAttnCounterBytes + kAttnSplitBytes + most * sizeof(float);
@@ -95,7 +95,7 @@ nvfp4_status attend(const nvfp4_kv_cache* cache, const nvfp4_batch* batch, const
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kAttnCounterBytes + kAttnSplitBytes);
   const bool fp8 = cache->dtype == NVFP4_KV_E4M3;
   const AttnShape s = shape_of(dim, fp8, packed_rows(n_tokens, batch->max_new, n_heads, kv),
-                               static_cast<int64_t>(batch->n_seqs) * kv, words > 0);
+                               static_cast<int64_t>(batch->n_seqs) * kv, words > 0, cache->page_size);
   KvMaps maps;
   if (cache->maps)
     maps = static_cast<const KvMaps*>(cache->maps)[s.maps];

@@ -1472,7 +1472,8 @@ struct AttnShape {
   int rw, kw, tile_rows, box_keys;
   bool chunk;
   int maps;  // which of a cache's pairs of tensor maps
-  bool alternate = false;
+  bool pair = false;        // two CTAs an SM (attention_chunk.cuh)
+  bool whole_rows = !chunk;  // boxes of whole rows, or of 128 bytes of them
 };
 constexpr int kMapPairs = 4;
 inline AttnShape attn_shape(int dim, bool fp8, int64_t rows, int64_t items) {
@@ -1490,9 +1491,17 @@ inline AttnShape attn_shape(int dim, bool fp8, int64_t rows, int64_t items) {
 // and 107, ragged 32 and 31, one sequence of 1,000 keys 16 and 12; 256 values 178 and 191, ragged 50 and 69, four of
 // 2,000 keys 24 and 26, one of 1,000 keys 16 and 15; E4M3 176 and 190, ragged 59 and 54.  128 rows, the groups in turn
 // or each with rows of its own: 104 and 110 (64 values: 68 and 74).
-inline AttnShape tree_shape(int dim, bool fp8, int64_t rows, int64_t items) {
+inline AttnShape tree_shape(int dim, bool fp8, int64_t rows, int64_t items, int page_size) {
+  const char* e = getenv("TREE_V");
+  if (e && e[0] == 's' && rows <= 64) { const int rw = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4), kw = 4 / rw; return {rw, kw, 16 * rw, attn_slice(dim, fp8, kw) * kw, false, rw / 2}; }
+  if (e && e[0] == 'c') return {0, 0, dim == 256 ? 128 : 256, dim == 256 ? 64 : 128, true, 3};
   if (dim < 256) {
-    if (rows > (dim == 64 ? 64 : 32) && rows <= 128) return {0, 0, 128, 128, true, 3, true};
+    if ((rows > (dim == 64 ? 64 : 32) || (e && e[0] == 'a')) && rows <= 128) {
+      // tiles of 64 keys: of pages up to that size by the boxes of the larger tiles, of larger pages by the boxes of 64
+      // whole rows that the split kernel has (which lie in a tile as the products read it)
+      if (page_size <= 64) return {0, 0, 128, 128, true, 3, true, false};
+      return {0, 0, 128, 64, true, dim == 128 && !fp8 ? 0 : 1, true, true};
+    }
   } else if (rows > 32 || (rows > 16 && !fp8 && items >= 32)) {
     return {0, 0, 128, 64, true, 3};
   }

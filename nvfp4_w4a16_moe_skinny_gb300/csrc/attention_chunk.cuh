@@ -21,11 +21,9 @@
 // tensor cores' hands; weights stay below 2^8 (bf16 holds them as exactly as those below
 // 1; f16 weights, for E4M3 caches, are offset by 2^7 and stay below 2^15).
 //
-// Trees of up to 128 rows (tree_attention; heads of 64 and 128 values): both groups have the same rows and
-// take the key tiles in turn, each with its own S, reference, sum and O, so that one group's products run in the
-// other's softmax here too.  At an item's end each group joins half of the columns of both O's
-// in TMEM.  Q has two buffers, and the next item's comes while this one runs.  (A tile takes 1.1 us then, the rate
-// at which memory delivers it; with one group of 128 rows 1.3.)
+// Trees of up to 128 rows (tree_attention; heads of 64 and 128 values): two CTAs an SM, each with half of the
+// shared memory and TMEM and one row group, tiles of 64 keys and S double-buffered as for 256 values.  One CTA's
+// items start and end (about 6 us, most of it waiting) while the other's tiles run.
 //
 // Fit tiles.  For an E4M3 cache the tiles are converted to f16 (exact).  For both
 // kinds of cache V is cleaned in tiles that some row does not wholly see: keys outside
@@ -57,14 +55,15 @@ struct Ring {
   static __device__ __forceinline__ uint32_t before(uint32_t t) { return ((t >> kLog2) - 1) & 1; }
 };
 
-// kAlternate: both softmax warpgroups have the same 128 rows, and the key tiles in turn (see below).
-template <int kDim, bool kFp8, bool kAlternate = false>
+// kPair: one row group a CTA and two CTAs an SM (trees of up to 128 rows; see below).
+template <int kDim, bool kFp8, bool kPair = false>
 struct ChunkTile {
-  static constexpr int kGroups = kDim == 256 ? 1 : 2;      // softmax warpgroups of 128 rows
-  static_assert(!kAlternate || kGroups == 2, "two groups to take turns");
-  static constexpr int kRows = kAlternate ? 128 : 128 * kGroups;
-  static constexpr int kKeys = kDim == 256 ? 64 : 128;
-  static constexpr int kSBuf = kDim == 256 ? 2 : 1;        // S buffers per group
+  static constexpr int kGroups = kDim == 256 || kPair ? 1 : 2;  // softmax warpgroups of 128 rows
+  static_assert(!kPair || kDim < 256, "a pair has half of the shared memory and TMEM each");
+  static constexpr int kRows = 128 * kGroups;
+  static constexpr int kKeys = kGroups == 1 ? 64 : 128;
+  static constexpr int kSBuf = kGroups == 1 ? 2 : 1;        // S buffers per group
+  static constexpr int kCtas = kPair ? 2 : 1;
   // An item counted as its units alone: a prompt of 4,096 tokens 166 us, with four more 153 (at that
   // step; five more add 2 to 5% to the shorter prompts, two more make it 168).  Boundaries that move up to four
   // units instead of one: 512 tokens in a window of 1,024 keys of 256 values 34.6 us against 35.9, but
@@ -76,11 +75,16 @@ struct ChunkTile {
   // boundaries that move by one pay (one sequence of 1,000 keys, 30 rows: 16.0 us against 19.8; two with 320
   // rows 20.7 against 26.7, 240 rows over four 23.4 against 28.8).  Items counted with three or two more units: 32
   // ragged trees over up to 16K keys 53.2 and 61 us against 53.1 (64 values: 63 and 73 against 56).
-  static constexpr __host__ __device__ Tiling tree_tiling() { return {kRows, kKeys, kOver, 1, 2}; }
+#ifndef TO
+#define TO 4
+#define TS 1
+#define TL 2
+#endif
+  static constexpr __host__ __device__ Tiling tree_tiling() { return {kRows, kKeys, kPair ? TO : kOver, kPair ? TS : 1, kPair ? TL : 2}; }
   // warps that make tiles fit: two beside the copies and the products, or (E4M3 and 128 values:
   // 256 conversions a row and tile; 830 us with two warps, 705 with four, for 2,048 tokens over
   // 32,768 keys) a warpgroup of their own; the softmax warpgroups follow
-  static constexpr bool kFitGroup = kFp8 && kDim == 128;
+  static constexpr bool kFitGroup = kFp8 && kDim == 128 && !kPair;
   static constexpr int kFit0 = kFitGroup ? 4 : 2, kFits = kFitGroup ? 4 : 2, kSoft0 = kFit0 + kFits;
   static constexpr int kThreadsAll = 32 * kSoft0 + 128 * kGroups;
   static constexpr int kEl = kFp8 ? 1 : 2;
@@ -97,19 +101,18 @@ struct ChunkTile {
   // stage of K and two of V; four stages of copies against two: 2% for 1,500-token pieces.  128 values:
   // 2,048 tokens over 32,768 keys 705 us with two stages of K and two of copies, 1,117 with one and four;
   // 256 values, whose row group waits for copies more than for K, 2,538 and 2,403.
-  using KRing = Ring<kDim == 64 ? 4 : (kFp8 && kDim == 256 ? 1 : 2)>;
+  using KRing = Ring<kDim == 64 ? 4 : (kFp8 && (kDim == 256 || kPair) ? 1 : 2)>;
   using VRing = Ring<kDim == 64 ? 4 : 2>;
   using RawRing = Ring<kDim == 128 ? 2 : 4>;
-  // Q: one for each group; alternating, the next item's comes while the last one is in use, where there is room
-  static constexpr int kQBufs = kAlternate && kFp8 && kDim == 128 ? 1 : kGroups;
-  static constexpr int kKAt = kQBufs * kQB, kVAt = kKAt + KRing::kStages * kTileB;
+  static constexpr int kKAt = kGroups * kQB, kVAt = kKAt + KRing::kStages * kTileB;
   static constexpr int kRaw = kVAt + VRing::kStages * kTileB;
   static constexpr int kBars = kRaw + (kFp8 ? RawRing::kStages * kRawB : 0);
-  static constexpr size_t kSmem = 1024 + kBars + 1024 + (kAlternate ? 3072 : 0);
+  static constexpr size_t kSmem = 1024 + kBars + 1024;
   // TMEM columns: O of each group, then the S buffers
   static constexpr int kSCol = kGroups * kDim;
-  static_assert(kSCol + kGroups * kSBuf * kKeys <= 512, "TMEM");
-  static_assert(kSmem <= kMaxSmem, "shared memory");
+  static constexpr int kTmem = 512 / kCtas;
+  static_assert(kSCol + kGroups * kSBuf * kKeys <= kTmem, "TMEM");
+  static_assert(kSmem <= (kPair ? 113 * 1024 : kMaxSmem), "shared memory");
 };
 
 // ------------------------------------------------------------------ tcgen05
@@ -237,13 +240,6 @@ struct ChunkBars {
   NotedTiles noted;
 };
 
-// What the two groups of one row tile tell each other: reference and sum of each row, and the factor
-// that undoes the scaling of its Q, by Q's buffer.
-struct Alternates {
-  float2 ml[2][128];
-  float qscale[2][128];
-};
-
 // The infinities and NaN among 32 values of a pool (16-byte aligned), added to o: 16 bytes a
 // load, as most of them hold none.
 template <bool kFp8>
@@ -284,8 +280,8 @@ struct KeySpan {
 // that works on TMEM: inside the loop that writes the rows the mixed batch of 64-value heads took 146.0 us and
 // 2,048 tokens over 32,768 E4M3 keys of 128 values 713, with it 145.4 and 710.)
 template <int kDim, bool kFp8, int kKeys, typename Row>
-__device__ __noinline__ void restore_nonfinite(uint32_t o_at, const volatile NotedTiles* notes, uint32_t tile0, int j0,
-                                               int dj, int n, int first, KeyRange kr, Row row, const int32_t* table, const void* pool,
+__device__ __noinline__ void restore_nonfinite(uint32_t o_at, const volatile NotedTiles* notes, uint32_t tile0, int n,
+                                               int first, KeyRange kr, Row row, const int32_t* table, const void* pool,
                                                int64_t head, int64_t page_stride, int page_log2, int num_pages) {
   const int lane = threadIdx.x & 31;
 #pragma unroll 1
@@ -294,7 +290,7 @@ __device__ __noinline__ void restore_nonfinite(uint32_t o_at, const volatile Not
     tmem_ld32(o, o_at + c);
     tmem_loaded(o);
 #pragma unroll 1
-    for (int j = j0; j < n; j += dj) {
+    for (int j = 0; j < n; ++j) {
       const int key0 = (first + j) * kKeys;
       if (!notes->at(tile0 + j) || !partly_seen(kr, key0, kKeys)) continue;
       const int hi = min(key0 + kKeys, kr.any_hi);
@@ -376,16 +372,16 @@ __host__ __device__ __forceinline__ JoinStep join_step(int mine, int level, int 
 // arrive took 8 us for four shares of 128 rows and 25 us for six of 256, with the other SMs idle.  Its list: as
 // split_item, with the rows in nine bits.
 __device__ __forceinline__ int4 chunk_split_item(const Walk& w, int c1) {
-  static_assert(kAttnGrid <= 256, "eight bits");
-  return make_int4(c1 | w.t.rows << 8, w.h, w.t.row0, w.s.tok0);
+  static_assert(2 * kAttnGrid <= 512, "nine bits");
+  return make_int4(c1 | w.t.rows << 9, w.h, w.t.row0, w.s.tok0);
 }
 
 // ------------------------------------------------------------------ the kernel
 
-template <int kDim, bool kFp8, bool kTree, bool kAlternate>
-__global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
+template <int kDim, bool kFp8, bool kTree, bool kPair>
+__global__ void __launch_bounds__(ChunkTile<kDim, kFp8, kPair>::kThreadsAll, ChunkTile<kDim, kFp8, kPair>::kCtas)
     attn_chunk_kernel(const AttnJob p, const __grid_constant__ KvMaps maps) {
-  using T = ChunkTile<kDim, kFp8, kAlternate>;
+  using T = ChunkTile<kDim, kFp8, kPair>;
   using KRing = typename T::KRing;
   using VRing = typename T::VRing;
   using RawRing = typename T::RawRing;
@@ -395,7 +391,6 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
   const uint32_t base = (raw0 + 1023u) & ~1023u;
   ChunkBars* bars = reinterpret_cast<ChunkBars*>(smem_raw + (base - raw0) + T::kBars);
   static_assert(sizeof(ChunkBars) <= 1024, "barriers");
-  [[maybe_unused]] Alternates* const both = reinterpret_cast<Alternates*>(bars + 1);
   const uint32_t q_at = base, k_at = base + T::kKAt, v_at = base + T::kVAt, raw_at = base + T::kRaw;
 
   const int warp = static_cast<int>(uniform(threadIdx.x >> 5)), lane = threadIdx.x & 31;
@@ -414,7 +409,8 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
   }
   bars->noted.clear(threadIdx.x);
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&bars->tmem))
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&bars->tmem)),
+                 "n"(T::kTmem)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     tc_fence_before();
@@ -445,10 +441,11 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
   // tile counts over all items so far: ring positions and phases
   uint32_t nt = 0;
   // Registers: with two softmax warpgroups the others give theirs to them (the shares add up to
-  // what the block was launched with: 384 * 168 = 128 * (72 + 2 * 216), 512 * 128 = 128 * (64 + 64 + 2 * 192))
+  // what the block was launched with: 384 * 168 = 128 * (72 + 2 * 216), 512 * 128 = 128 * (64 + 64 + 2 * 192);
+  // a CTA of a pair 256 * 128 = 128 * (64 + 192))
   if (warp < T::kSoft0) {
     if constexpr (kG == 2 && !T::kFitGroup) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if constexpr (kG == 2 && T::kFitGroup) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if constexpr ((kG == 2 && T::kFitGroup) || kPair) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 0) {
       // ------------------------------------------------------------ copies
       const int piece_log2 = min(p.page_log2, log2c(kKeys));
@@ -508,6 +505,10 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
               if (i >= pieces) break;
               if (at[i] < 0) continue;
               const int key = (pc.first + j) * kKeys + (i << piece_log2);
+              if (kPair && p.page_log2 > log2c(kKeys)) {  // boxes of whole rows: the tile in one copy (see tree_shape)
+                tma_load_5d(dst, is_v ? &maps.v : &maps.k, 0, key & ((1 << p.page_log2) - 1), 0, head, at[i], bar);
+                continue;
+              }
 #pragma unroll
               for (int sub = 0; sub < T::kSub; ++sub)
                 tma_load_5d(dst + sub * T::kSubB + (i << piece_log2) * T::kRowB, is_v ? &maps.v : &maps.k, 0,
@@ -536,10 +537,9 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
       // descriptors: the start address is the low 14 bits, in units of 16 bytes
       const uint64_t q_desc = umma_desc(q_at, 16, 1024), k_desc = umma_desc(k_at, 16, 1024);
       const uint64_t v_desc = umma_desc(v_at, kKeys * 128, 1024);
-      [[maybe_unused]] int q_buf = T::kQBufs - 1;  // (alternating: Q's buffers in turn)
       const auto qk = [&](int g, uint32_t t) {
         const uint32_t d = tmem + T::kSCol + (kG == 2 ? g : (t & 1)) * kKeys;
-        const uint64_t a = q_desc + (kAlternate ? q_buf : g) * (T::kQB >> 4), b = k_desc + KRing::at(t) * (T::kTileB >> 4);
+        const uint64_t a = q_desc + g * (T::kQB >> 4), b = k_desc + KRing::at(t) * (T::kTileB >> 4);
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < kDim / 16; ++k)
@@ -575,39 +575,6 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
         u = pc.end;
         const int n = static_cast<int>(uniform(pc.n));
         if (n == 0) continue;
-        if constexpr (kAlternate) {  // tile j is group j % 2's
-          q_buf ^= T::kQBufs - 1;
-          NVFP4_WAIT(bars->q_full, nq[0] & 1);
-          ++nq[0];
-          for (int j = 0; j < min(n, 2); ++j) {
-            wait_k(nt + j);
-            tc_fence_after();
-            qk(j, nt + j);
-            free_tile(bars->k_empty + KRing::at(nt + j));
-          }
-          for (int j = 0; j < n; ++j) {
-            const uint32_t t = nt + j;
-            const int g = j & 1;
-            NVFP4_WAIT(bars->v_ready + VRing::at(t), VRing::phase(t));
-            if constexpr (!kFp8) NVFP4_WAIT(bars->v_full + VRing::at(t), VRing::phase(t));
-            NVFP4_WAIT(&bars->p_full[g][0], np[g] & 1);
-            tc_fence_after();
-            pv(g, t, 0, j > 1);
-            NVFP4_WAIT(&bars->p_full[g][1], np[g] & 1);
-            ++np[g];
-            tc_fence_after();
-            pv(g, t, 1, true);
-            free_tile(bars->v_empty + VRing::at(t));
-            if (j + 2 < n) {
-              wait_k(t + 2);
-              tc_fence_after();
-              qk(g, t + 2);
-              free_tile(bars->k_empty + KRing::at(t + 2));
-            }
-          }
-          nt += n;
-          continue;
-        }
         const int groups = kG == 2 && uniform(w.t.rows) > 128 ? 2 : 1;
         for (int g = 0; g < groups; ++g) {
           NVFP4_WAIT(bars->q_full + g, nq[g] & 1);
@@ -736,7 +703,7 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
   } else {
     // -------------------------------------------------------------- softmax
     if constexpr (kG == 2 && !T::kFitGroup) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-    if constexpr (kG == 2 && T::kFitGroup) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    if constexpr ((kG == 2 && T::kFitGroup) || kPair) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     const int g = (warp - T::kSoft0) >> 2;
     const int row = (warp & 3) * 32 + lane;              // of the group: its TMEM lane
     const uint32_t lane_at = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -746,28 +713,27 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
     uint32_t mine = 0;  // this group's tiles so far
     // Q of this thread's row of the walk's item: copied as it is into the tile that the
     // products with K read
-    [[maybe_unused]] int q_buf = 0;  // (alternating: the buffer of the item at hand)
-    const auto fetch_q = [&](const Walk& o, int buf) {
-      const int r = (kAlternate ? 0 : g * 128) + row;
+    const auto fetch_q = [&](const Walk& o) {
+      const int r = g * 128 + row;
       const int rr = o.t.row0 + min(r, o.t.rows - 1);
       const int tok = div_by(p.by_group, rr), head = o.h * p.group + rr - tok * p.group;
       const uint16_t* q = p.q + (o.s.tok0 + tok) * p.q_stride + static_cast<int64_t>(head) * kDim;
       const uint32_t bytes = r < o.t.rows ? 16 : 0;  // rows past the tile's last one: zeros
 #pragma unroll 8
       for (int c = 0; c < kDim / 8; ++c)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(q_at + buf * T::kQB + umma_offset(128, row, c)),
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(q_at + g * T::kQB + umma_offset(128, row, c)),
                      "l"(q + 8 * c), "r"(bytes)
                      : "memory");
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
     // hands the copied tile over; for an E4M3 cache scaled by a power of two into f16's range.
     // Returns the factor that undoes the scaling.
-    const auto hand_q = [&](int buf) {
+    const auto hand_q = [&]() {
       asm volatile("cp.async.wait_group 0;" ::: "memory");
       if (p.scale == 0.f) {
 #pragma unroll 1
         for (int c = 0; c < kDim / 8; ++c) {
-          const uint32_t at = q_at + buf * T::kQB + umma_offset(128, row, c);
+          const uint32_t at = q_at + g * T::kQB + umma_offset(128, row, c);
           sts128(at, zero_or_nan(lds128(at)));
         }
       }
@@ -776,7 +742,7 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
         float amax = 0.f;
 #pragma unroll 8
         for (int c = 0; c < kDim / 8; ++c) {
-          const uint4 v = lds128(q_at + buf * T::kQB + umma_offset(128, row, c));
+          const uint4 v = lds128(q_at + g * T::kQB + umma_offset(128, row, c));
           const uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -787,7 +753,7 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
         back = exp2i(-e);
 #pragma unroll 8
         for (int c = 0; c < kDim / 8; ++c) {
-          const uint32_t at = q_at + buf * T::kQB + umma_offset(128, row, c);
+          const uint32_t at = q_at + g * T::kQB + umma_offset(128, row, c);
           const uint4 v = lds128(at);
           uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -798,7 +764,7 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bars->q_full + (kAlternate ? 0 : g));
+      if (lane == 0) mbar_arrive(bars->q_full + g);
       return back;
     };
 
@@ -810,25 +776,16 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
       u = pc.end;
       if (pc.n == 0) continue;
       const int first = pc.first, n = pc.n;
-      if (!kAlternate && g * 128 >= w.t.rows) {  // this group has no rows here
+      if (g * 128 >= w.t.rows) {  // this group has no rows here
         nt += n;
         continue;
       }
-      if constexpr (kAlternate) {  // group 0 brings Q for both
-        if (!ready) {
-          if (g == 0) {
-            fetch_q(w, q_buf);
-            both->qscale[q_buf][row] = hand_q(q_buf);
-          }
-          asm volatile("bar.sync 3, 256;" ::: "memory");
-        }
-        qscale = both->qscale[q_buf][row];
-      } else if (!ready) {
-        fetch_q(w, g);
-        qscale = hand_q(g);
+      if (!ready) {
+        fetch_q(w);
+        qscale = hand_q();
       }
       ready = false;
-      const int r = (kAlternate ? 0 : g * 128) + row;
+      const int r = g * 128 + row;
       const bool live = r < w.t.rows;
       const int rr = w.t.row0 + min(r, w.t.rows - 1);
       const int tok = div_by(p.by_group, rr), head = w.h * p.group + rr - tok * p.group;
@@ -845,26 +802,8 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
       const int see_hi = kTree ? ctx : min(pos + 1, w.s.len);
       const int see_lo = p.window > 0 ? (kTree ? ctx + w.s.n : pos + 1) - p.window : -(1 << 30);
 
-      // the item after this one, if this CTA has one
-      const auto find_next = [&](Walk& next) {
-        for (long long v = u; v < u1;) {
-          walk_to(p, next, v, kTiling);
-          const Share q = share_at(next, v, u0, u1, blockIdx.x, kTiling);
-          if (q.n > 0) return true;
-          v = q.end;
-        }
-        return false;
-      };
-      Walk next = w;
-      bool more = false;
-      constexpr bool kEarlyQ = kAlternate && T::kQBufs == 2;
-      if constexpr (kEarlyQ) {
-        more = find_next(next);
-        if (more && g == 0) fetch_q(next, q_buf ^ 1);
-      }
-
       float m = -INFINITY, l = 0.f;  // reference of the weights, this row's sum
-      for (int j = kAlternate ? g : 0; j < n; j += kAlternate ? 2 : 1, ++mine) {
+      for (int j = 0; j < n; ++j, ++mine) {
         const uint32_t t = nt + j;
         const int sb = kG == 2 ? g : (t & 1);
         NVFP4_WAIT(bars->s_full + sb, (kG == 2 ? mine : (t >> 1)) & 1);
@@ -918,7 +857,7 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
         for (int i = 0; i < 4; ++i) top[i] = fmaxf(top[i], s[kKeys - 4 + i]);
         const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * mul - kOffset;
         const bool move = high > m + 8.0f || m == -INFINITY;
-        if (__any_sync(0xffffffffu, move && j > (kAlternate ? 1 : 0) && high > m)) {
+        if (__any_sync(0xffffffffu, move && j > 0 && high > m)) {
           // the row's sums follow its maximum: everything up to the tile before is in O
           if constexpr (kG == 1) {
             NVFP4_WAIT(bars->o_full + ((t - 1) & 1), ((t - 1) >> 1) & 1);
@@ -967,21 +906,20 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
       nt += n;
 
       // ---- the next item's Q while the last product with V runs (all products with this
-      // item's Q are done: their last S has been read).  With a buffer of its own it is there already.
-      if constexpr (kEarlyQ) {
-        if (more && g == 0) both->qscale[q_buf ^ 1][row] = hand_q(q_buf ^ 1);
-      } else {
-        more = find_next(next);
-        if constexpr (!kAlternate) {
-          more = more && g * 128 < next.t.rows;
-          if (more) fetch_q(next, g);
-        }
+      // item's Q are done: their last S has been read)
+      Walk next = w;
+      bool more = false;
+      for (long long v = u; v < u1 && !more;) {
+        walk_to(p, next, v, kTiling);
+        const Share q = share_at(next, v, u0, u1, blockIdx.x, kTiling);
+        more = q.n > 0;
+        v = q.end;
       }
+      more = more && g * 128 < next.t.rows;
+      if (more) fetch_q(next);
 
       // ---- write: the finished row, or this piece's share of it
-      if constexpr (kAlternate) {
-        if (g < n) NVFP4_WAIT(bars->o_full + g, (mine - 1) & 1);
-      } else if constexpr (kG == 2)
+      if constexpr (kG == 2)
         NVFP4_WAIT(bars->o_full + g, (mine - 1) & 1);
       else
         NVFP4_WAIT(bars->o_full + ((nt - 1) & 1), ((nt - 1) >> 1) & 1);
@@ -1009,8 +947,7 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
       };
       if (bars->noted.any_since(nt - n)) {
         const auto restore = [&](auto seen) {
-          restore_nonfinite<kDim, kFp8, kKeys>(o_at, &bars->noted, nt - n, kAlternate ? g : 0, kAlternate ? 2 : 1, n, first,
-                                               key_range<kTree>(p, w), seen,
+          restore_nonfinite<kDim, kFp8, kKeys>(o_at, &bars->noted, nt - n, n, first, key_range<kTree>(p, w), seen,
                                                p.table + static_cast<int64_t>(w.b) * p.max_pages, p.v_pool,
                                                value_at(p, 0, w.h, 0, kDim), p.page_stride, p.page_log2, p.num_pages);
         };
@@ -1019,53 +956,15 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
         else
           restore(KeySpan{see_lo, see_hi});
       }
-      // alternating: the row's sums over all tiles from both groups' in TMEM, each group half of the columns
-      [[maybe_unused]] float by[2] = {1.0f, 1.0f};
-      if constexpr (kAlternate) {
-        both->ml[g][row] = make_float2(m, l);
-        tc_fence_before();
-        asm volatile("bar.sync 3, 256;" ::: "memory");
-        tc_fence_after();
-        if (more && g == 0 && !kEarlyQ) fetch_q(next, 0);  // (no product reads Q any more)
-        const float2 other = both->ml[g ^ 1][row];
-        const float high = fmaxf(m, other.x);
-        if (high != -INFINITY) {
-          const float a = exp2_approx(m - high), b = exp2_approx(other.x - high);
-          l = l * a + other.y * b;
-          // (no smaller than fp32's numbers: an infinity in a sum stays one)
-          by[0] = fmaxf(g == 0 ? a : b, 1.2e-38f), by[1] = fmaxf(g == 0 ? b : a, 1.2e-38f);
-        }
-        m = high;
-      }
       const float inv = !whole ? 1.0f : (l == 0.f ? 0.f : vs / l);
-      constexpr int kColumns = kAlternate ? kDim / 2 : kDim;
-      const int column0 = kAlternate ? g * kColumns : 0;
 #pragma unroll 1
-      for (int c = column0; c < column0 + kColumns; c += 32) {
+      for (int c = 0; c < kDim; c += 32) {
         float o[32];
-        if constexpr (kAlternate) {
-          tmem_ld32(o, tmem + lane_at + c);
-          tmem_loaded(o);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] *= by[0];
-          if (n > 1) {  // (group 1 has had a tile)
-            float x[32];
-            tmem_ld32(x, tmem + lane_at + kDim + c);
-            tmem_loaded(x);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = fmaf(x[i], by[1], o[i]);
-          }
-        } else {
-          tmem_ld32(o, o_at + c);
-          tmem_loaded(o);
-        }
-        if (c == column0 && more) {  // the next item's first product may start
+        tmem_ld32(o, o_at + c);
+        tmem_loaded(o);
+        if (c == 0 && more) {  // the next item's first product may start
           tc_fence_before();
-          if constexpr (kAlternate) {
-            if (g == 0 && !kEarlyQ) both->qscale[0][row] = hand_q(0);
-          } else {
-            qscale = hand_q(g);
-          }
+          qscale = hand_q();
           ready = true;
         }
         if (whole) {
@@ -1076,15 +975,10 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
             stg256(part + static_cast<int64_t>((c + i) / 8) * T::kRows * 8, reinterpret_cast<const uint32_t*>(o) + i);
         }
       }
-      if constexpr (kAlternate) {  // both groups have read O (and the other's sums) before a new tile writes it
-        tc_fence_before();
-        asm volatile("bar.sync 3, 256;" ::: "memory");
-        q_buf ^= T::kQBufs - 1;
-      }
       float* ml = p.part + static_cast<int64_t>(2) * gridDim.x * T::kRows * kDim;  // references and sums, after all shares
-      if (!whole && (!kAlternate || g == 0))
+      if (!whole)
         *reinterpret_cast<float2*>(ml + (static_cast<int64_t>(slot) * T::kRows + r) * 2) = make_float2(m, l);
-      else if (whole && live && p.lse && (!kAlternate || g == 0))
+      else if (live && p.lse)
         p.lse[token * p.n_heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
       // ---- the join's steps of a split item, for as long as this group is the last to arrive
       if (!kTree && !pc.whole) {
@@ -1153,7 +1047,7 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(T::kTmem));
   }
 }
 
@@ -1164,12 +1058,12 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8>::kThreadsAll, 1)
 constexpr int kChunkJoinGrid = 8 * kAttnGrid;
 template <int kDim>
 __global__ void __launch_bounds__(128) attn_chunk_join_kernel(const AttnJob p, int split_grid, int tile_rows) {
-  __shared__ int4 list[kAttnGrid];
+  __shared__ int4 list[2 * kAttnGrid];
   __shared__ int warp_sum[4];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
   pdl_launch_dependents();
-  constexpr int kSpan = (kAttnGrid + 127) / 128;
+  constexpr int kSpan = (2 * kAttnGrid + 127) / 128;
   int items = 0;
   int4 mine[kSpan];
 #pragma unroll
@@ -1188,7 +1082,7 @@ __global__ void __launch_bounds__(128) attn_chunk_join_kernel(const AttnJob p, i
       if (x < warp) at += warp_sum[x];
       items += warp_sum[x];
     }
-    if (mine[b].x != 0) list[at] = make_int4(mine[b].x | (b * 128 + threadIdx.x) << 17, mine[b].y, mine[b].z, mine[b].w);
+    if (mine[b].x != 0) list[at] = make_int4(mine[b].x | (b * 128 + threadIdx.x) << 18, mine[b].y, mine[b].z, mine[b].w);
     __syncthreads();
   }
   const float* ml = p.part + static_cast<int64_t>(2) * split_grid * tile_rows * kDim;
@@ -1197,7 +1091,7 @@ __global__ void __launch_bounds__(128) attn_chunk_join_kernel(const AttnJob p, i
   for (int x = blockIdx.x; x < items * parts; x += gridDim.x) {
     const int4 it = list[x / parts];
     const int part = x - x / parts * parts, c = part % kBlocks * 16, r = part / kBlocks * 128 + threadIdx.x;
-    const int c0 = it.x >> 17, c1 = it.x & 0xff, rows = it.x >> 8 & 0x1ff;
+    const int c0 = it.x >> 18, c1 = it.x & 0x1ff, rows = it.x >> 9 & 0x1ff;
     if (r >= rows) continue;
     float m = -INFINITY, l = 0.f, acc[16];
 #pragma unroll
@@ -1249,16 +1143,16 @@ __global__ void __launch_bounds__(128) attn_chunk_join_kernel(const AttnJob p, i
   }
 }
 
-template <int kDim, bool kFp8, bool kTree, bool kAlternate>
+template <int kDim, bool kFp8, bool kTree, bool kPair>
 nvfp4_status launch_attn_chunk(const AttnJob& p, const KvMaps& maps, cudaStream_t stream) {
-  using T = ChunkTile<kDim, kFp8, kAlternate>;
-  const auto kernel = attn_chunk_kernel<kDim, kFp8, kTree, kAlternate>;
+  using T = ChunkTile<kDim, kFp8, kPair>;
+  const auto kernel = attn_chunk_kernel<kDim, kFp8, kTree, kPair>;
   if (set_smem(kernel, T::kSmem) != cudaSuccess) return NVFP4_ERR_CUDA;
-  if (launch_pdl(kernel, dim3(kAttnGrid), dim3(T::kThreadsAll), T::kSmem, stream, p, maps) != cudaSuccess)
+  if (launch_pdl(kernel, dim3(kAttnGrid * T::kCtas), dim3(T::kThreadsAll), T::kSmem, stream, p, maps) != cudaSuccess)
     return NVFP4_ERR_CUDA;
   if constexpr (kTree) {  // (one unit an item: nothing can be split)
     if ((static_cast<int64_t>(p.max_pages) << p.page_log2) > T::kKeys &&
-        launch_pdl(attn_chunk_join_kernel<kDim>, dim3(kChunkJoinGrid), dim3(128), 0, stream, p, kAttnGrid, T::kRows) != cudaSuccess)
+        launch_pdl(attn_chunk_join_kernel<kDim>, dim3(kChunkJoinGrid), dim3(128), 0, stream, p, kAttnGrid * T::kCtas, T::kRows) != cudaSuccess)
       return NVFP4_ERR_CUDA;
   }
   return launched();

@@ -9,7 +9,7 @@ namespace nvfp4 {
 template <int kDim, bool kFp8, bool kTree>
 nvfp4_status dispatch_rows(const AttnJob& p, const KvMaps& maps, const AttnShape& s, cudaStream_t stream) {
   if constexpr (kTree && kDim < 256)
-    if (s.alternate) return launch_attn_chunk<kDim, kFp8, kTree, true>(p, maps, stream);
+    if (s.pair) return launch_attn_chunk<kDim, kFp8, kTree, true>(p, maps, stream);
   if (s.chunk) return launch_attn_chunk<kDim, kFp8, kTree, false>(p, maps, stream);
   if (s.rw == 1) return launch_attn_split<kDim, kFp8, 1, 4, kTree>(p, maps, stream);
   if (s.rw == 2) return launch_attn_split<kDim, kFp8, 2, 2, kTree>(p, maps, stream);

@@ -15,7 +15,7 @@ namespace {
 template <int kDim, bool kFp8, bool kTree>
 Tiling tiling_at(const AttnShape& s) {
   if constexpr (kDim < 256)
-    if (s.alternate) return ChunkTile<kDim, kFp8, true>::tree_tiling();
+    if (s.pair) return ChunkTile<kDim, kFp8, true>::tree_tiling();
   using T = ChunkTile<kDim, kFp8>;
   if (s.chunk) return kTree ? T::tree_tiling() : T::tiling();
   if (s.rw == 1) return AttnTile<kDim, kFp8, 1, 4>::tiling();
@@ -115,9 +115,9 @@ static nvfp4_status plan_check(const nvfp4_kv_cache* cache, const nvfp4_batch* b
     return NVFP4_ERR_SHAPE;
   const bool fp8 = cache->dtype == NVFP4_KV_E4M3;
   const int64_t rows = packed_rows(n_tokens, batch->max_new, n_heads, kv), pairs = static_cast<int64_t>(batch->n_seqs) * kv;
-  const AttnShape shape = kTree ? tree_shape(dim, fp8, rows, pairs) : attn_shape(dim, fp8, rows, pairs);
+  const AttnShape shape = kTree ? tree_shape(dim, fp8, rows, pairs, cache->page_size) : attn_shape(dim, fp8, rows, pairs);
   const auto g = tiling_for<kTree>(tiling_of<kTree>(dim, fp8, shape));
-  const int ctas = kAttnGrid * (shape.chunk ? 1 : attn_ctas(dim, fp8, shape.rw));
+  const int ctas = kAttnGrid * (shape.chunk ? (shape.pair ? 2 : 1) : attn_ctas(dim, fp8, shape.rw));
   AttnJob p{};
   p.n_seqs = batch->n_seqs, p.max_pages = batch->max_pages, p.n_tokens = n_tokens;
   p.n_heads = n_heads, p.n_kv = kv, p.group = n_heads / kv, p.by_group = fast_div(n_heads / kv);
