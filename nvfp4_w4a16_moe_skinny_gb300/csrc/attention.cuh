@@ -1483,27 +1483,29 @@ inline AttnShape attn_shape(int dim, bool fp8, int64_t rows, int64_t items) {
   return {rw, kw, 16 * rw, attn_slice(dim, fp8, kw) * kw, false, rw / 2};
 }
 
-// The same for a tree_attention call.  The join of its tcgen05 kernel is a second grid's (attention_chunk.cuh), which
-// makes that kernel the faster one from fewer rows on, and up to 128 rows of heads of 64 and 128 values its two row
-// groups take the key tiles in turn.  16 sequences of 8,000 keys, 60 or 64 rows: 128 values 100 us there and 127 in the
-// split kernel (E4M3 110 and 148), one of 32,000 keys 43 and 45; 64 values 64 and 73 there, but ragged
-// batches (64 of up to 4,000 keys) 39 and 34; 256 values 178 and 247 (E4M3 177 and 276).  32 rows: 128 values 100
-// and 107, ragged 32 and 31, one sequence of 1,000 keys 16 and 12; 256 values 178 and 191, ragged 50 and 69, four of
-// 2,000 keys 24 and 26, one of 1,000 keys 16 and 15; E4M3 176 and 190, ragged 59 and 54.  128 rows, the groups in turn
-// or each with rows of its own: 104 and 110 (64 values: 68 and 74).
+// The same for a tree_attention call, in `items` pairs of a sequence and a kv head.  The join of its tcgen05 kernel is a
+// second grid's (attention_chunk.cuh), which makes that kernel the faster one from fewer rows on, and up to 128 rows of
+// heads of 64 and 128 values it runs as two CTAs an SM.
+// 128 values, that kernel and the split kernel: 60 to 64 rows, 16 sequences of 8,000 keys 102 and 127 us (E4M3 108
+// and 148), 64 ragged ones of up to 4,000 keys 46 and 58 (54 and 61), four of 2,000 keys 21 and 23 (23 and 24), one of 1,000
+// keys 16 and 14 (16 and 14), of 32,000 47 and 45 (45 and 44).  28 to 32 rows, 16 sequences of 8,000 keys 101 and 107 (E4M3 107
+// and 90), 64 ragged ones 46 and 54 (52 and 41), four of 2,000 keys 20 and 19, one of 32,000 keys 44 and 40.  16 rows: 100 and 96 (107 and 61).
+// 64 values, 48 to 64 rows: 68 and 72 (E4M3 70 and 77), ragged 35 and 33 (41 and 35), 47 and 49 (48 and 52), one
+// sequence 14 and 12, 31 and 25.
+// 256 values (one CTA an SM): 60 to 64 rows, 178 and 247 (E4M3 177 and 276), ragged 66 and 116, one sequence of 32,000 keys 60
+// and 76; 30 to 32 rows 178 and 191 (176 and 190), ragged 50 and 69 (59 and 54), four of 2,000 keys 24 and 26
+// (28 and 26), one of 1,000 keys 16 and 15 (18 and 15).
 inline AttnShape tree_shape(int dim, bool fp8, int64_t rows, int64_t items, int page_size) {
-  const char* e = getenv("TREE_V");
-  if (e && e[0] == 's' && rows <= 64) { const int rw = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4), kw = 4 / rw; return {rw, kw, 16 * rw, attn_slice(dim, fp8, kw) * kw, false, rw / 2}; }
-  if (e && e[0] == 'c') return {0, 0, dim == 256 ? 128 : 256, dim == 256 ? 64 : 128, true, 3};
-  if (dim < 256) {
-    if ((rows > (dim == 64 ? 64 : 32) || (e && e[0] == 'a')) && rows <= 128) {
-      // tiles of 64 keys: of pages up to that size by the boxes of the larger tiles, of larger pages by the boxes of 64
-      // whole rows that the split kernel has (which lie in a tile as the products read it)
-      if (page_size <= 64) return {0, 0, 128, 128, true, 3, true, false};
-      return {0, 0, 128, 64, true, dim == 128 && !fp8 ? 0 : 1, true, true};
-    }
-  } else if (rows > 32 || (rows > 16 && !fp8 && items >= 32)) {
-    return {0, 0, 128, 64, true, 3};
+  if (dim == 256) {
+    if (rows > 32 || (rows > 16 && !fp8 && items >= 32)) return {0, 0, 128, 64, true, 3};
+  } else if (rows <= 128 &&
+             (rows > 64 || (dim == 128 && ((rows > 32 && items >= 16) || (rows > 16 && !fp8 && items >= 48))))) {
+    // tiles of 64 keys: of pages up to that size by the boxes of the larger tiles, of larger pages by the boxes of 64
+    // whole rows that the split kernel has (which lie in a tile as the products read it)
+    static_assert(attn_slice(128, false, 4) * 4 == 64 && attn_slice(128, true, 2) * 2 == 64 &&
+                  attn_slice(64, false, 2) * 2 == 64 && attn_slice(64, true, 2) * 2 == 64, "boxes");
+    if (page_size <= 64) return {0, 0, 128, 128, true, 3, true, false};
+    return {0, 0, 128, 64, true, dim == 128 && !fp8 ? 0 : 1, true, true};
   }
   return attn_shape(dim, fp8, rows, items);
 }

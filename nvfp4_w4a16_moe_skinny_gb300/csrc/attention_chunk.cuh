@@ -73,14 +73,10 @@ struct ChunkTile {
   static constexpr __host__ __device__ Tiling tiling() { return {kRows, kKeys, kOver, kSnap, kLeast}; }
   // Of a tree's calls, whose split items a second grid joins: shares are cheaper, so that ranges of two units and
   // boundaries that move by one pay (one sequence of 1,000 keys, 30 rows: 16.0 us against 19.8; two with 320
-  // rows 20.7 against 26.7, 240 rows over four 23.4 against 28.8).  Items counted with three or two more units: 32
-  // ragged trees over up to 16K keys 53.2 and 61 us against 53.1 (64 values: 63 and 73 against 56).
-#ifndef TO
-#define TO 4
-#define TS 1
-#define TL 2
-#endif
-  static constexpr __host__ __device__ Tiling tree_tiling() { return {kRows, kKeys, kPair ? TO : kOver, kPair ? TS : 1, kPair ? TL : 2}; }
+  // rows 20.7 against 26.7, 240 rows over four 23.4 against 28.8; pairs 15.0 with ranges of two units, 16.0 of four).
+  // Items of a pair counted with so many more units of 64 keys: 32 ragged trees over up to 16K keys 51.7 us with four, 49.1 with
+  // six, 64 ones of up to 4,000 keys 45.3 and 46.5; E4M3 67.1 and 69.1, 53.1 and 55.2.
+  static constexpr __host__ __device__ Tiling tree_tiling() { return {kRows, kKeys, kPair && !kFp8 ? 5 : kOver, 1, 2}; }
   // warps that make tiles fit: two beside the copies and the products, or (E4M3 and 128 values:
   // 256 conversions a row and tile; 830 us with two warps, 705 with four, for 2,048 tokens over
   // 32,768 keys) a warpgroup of their own; the softmax warpgroups follow
