@@ -92,6 +92,35 @@ def test_masks(lib, fp8, kind, lens, heads, kv, dim, page):
     c.check(*run(lib, c))
 
 
+# two CTAs an SM: 65 to 128 rows of 64 and 128 values in any batch, fewer in large ones; pages below, at and above a tile's
+# 64 keys
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("lens,heads,kv,dim,window", [
+    ([(40, 300), (3, 70), (25, 25), (1, 129)], 2, 1, 64, 0), ([(21, 200), (32, 64), (0, 7), (9, 700)], 4, 1, 128, 0),
+    ([(65, 190), (128, 128), (70, 1000)], 2, 2, 128, 100), ([(33, 2000), (30, 90)], 6, 2, 64, 31), ([(16, 150)] * 9, 8, 2, 128, 0),
+    ([(8, 90 + 7 * b) for b in range(25)], 6, 2, 128, 0), ([(17, 40 + 30 * b) for b in range(16)], 2, 1, 128, 0)])
+def test_two_ctas_an_sm(lib, fp8, page, lens, heads, kv, dim, window):
+    c = Trees(lens, heads, kv, dim, page, fp8, seed=page + dim, kind="any" if page == 32 else "tree")
+    first = run(lib, c, window=window)
+    c.check(*first, window=window)
+    again = run(lib, c, window=window)
+    assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+def test_caches_without_prepared_maps(lib):
+    """A C caller's cache structure without its TMA descriptors: encoded at the call, for every kernel and page size."""
+    for page in (16, 128):
+        for lens, heads, kv in (([(3, 50)], 4, 2), ([(40, 300), (25, 100)], 4, 2), ([(100, 300)], 4, 1)):
+            c = Trees(lens, heads, kv, 128, page, False, seed=5)
+            want = run(lib, c)
+            cache = c.cache()
+            cache.c.maps = None
+            out, lse = lib.tree_attention(c.q, cache, c.batch(), c.masks(), with_lse=True)
+            torch.cuda.synchronize()
+            assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("window", [1, 2, 5, 16, 63, 200, 5000])
 @pytest.mark.parametrize("kind", ["tree", "any"])
@@ -162,7 +191,8 @@ def test_bits_past_the_new_tokens_mean_nothing(lib, fp8, n):
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
 @pytest.mark.parametrize("lens,heads,kv,dim,page,window", [
     ([(15, 60), (3, 200)], 4, 2, 128, 32, 0), ([(15, 300), (9, 9)], 4, 2, 64, 16, 40), ([(50, 90)], 2, 1, 128, 64, 0), ([(20, 200)], 2, 1, 256, 16, 64),
-    ([(60, 170)], 8, 2, 128, 16, 0), ([(100, 300)], 4, 1, 64, 64, 30), ([(130, 200)], 2, 1, 256, 16, 0)])
+    ([(60, 170)], 8, 2, 128, 16, 0), ([(100, 300)], 4, 1, 64, 64, 30), ([(130, 200)], 2, 1, 256, 16, 0),
+    ([(40, 170)], 2, 1, 64, 16, 0), ([(32, 300)], 4, 1, 128, 128, 25)])
 def test_masked_places_leave_no_trace(lib, fp8, value, lens, heads, kv, dim, page, window):
     """Infinities and NaN in K and V of a new token reach the tokens that see it and no others; those in unused slots nobody."""
     c = Trees(lens, heads, kv, dim, page, fp8, seed=12)
