@@ -334,6 +334,9 @@ def _on_current(device, stream):
         raise ValueError("stream: of another GPU than the tensors")
 
 
+_capturing_now = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None)  # (as above)
+
+
 def _is_capturing(stream) -> bool:
     """Whether a stream is being captured into a graph."""
     with torch.cuda.stream(stream):
@@ -359,11 +362,13 @@ def _used_on(stream, *tensors):
 
 def _rows(x: torch.Tensor, what: str, device) -> int:
     """Rows of heads [tokens, heads, dim]: the row stride in elements."""
-    shape = x.shape
-    if len(shape) == 3 and x.dtype is torch.bfloat16 and x.device == device:
-        row, head, one = x.stride()
-        if one == 1 and (head == shape[2] or shape[1] == 1):
-            return row if shape[0] > 1 else shape[1] * shape[2]
+    if x.dtype is torch.bfloat16 and x.device == device:
+        shape = x.shape
+        if len(shape) == 3:
+            tokens, heads, dim = shape
+            row, head, one = x.stride()
+            if one == 1 and (head == dim or heads == 1):
+                return row if tokens > 1 else heads * dim
     raise ValueError(f"{what}: bf16 [tokens, heads, dim] on the call's GPU, the heads of a token contiguous")
 
 
@@ -399,7 +404,8 @@ class Library:
         _sig(self.lib)
         self._ws = {}
         self._attention_bytes = {}  # attention workspaces: their sizes by the sizes of a call
-        self._tree_bytes = {}       # (of a tree_attention call),
+        self._tree_bytes = {}       # (of a tree_attention call,
+        self._norm_bytes = {}       # of a qk_norm_rope_backward call),
         self._attention_ws = {}     # and one for each (device, stream)
 
     # -------------------------------------------------------------- plumbing
@@ -739,11 +745,11 @@ class Library:
         return (_index(positions, tokens, torch.int32, "positions", dev),
                 _index(inv_freq, pairs, torch.float64, "inv_freq", dev), 2 * pairs)
 
-    def _rows_out(self, out, like, what, dev, stream):
+    def _rows_out(self, out, shape, what, dev, stream):
         """An output of rows of heads (a new one, if none is given) and its stride."""
         if out is None:
-            return _empty(like.shape, torch.bfloat16, dev, stream), like.shape[1] * like.shape[2]
-        _need(out.shape == like.shape, f"{what}: the shape of its input")
+            return _empty(shape, torch.bfloat16, dev, stream), shape[1] * shape[2]
+        _need(out.shape == shape, f"{what}: the shape of its input")
         return out, _rows(out, what, dev)
 
     def qk_norm_rope(self, q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
@@ -756,17 +762,19 @@ class Library:
         if dev.index != _current_device() or stream is not None:
             _on_current(dev, stream)
         q_stride = _rows(q, "q", dev)
-        tokens, heads, dim = q.shape
+        shape = q.shape
+        tokens, heads, dim = shape
         pos, freq, rot = self._rotation(tokens, positions, inv_freq, dev)
         norm = _norm(q_norm, None if k is None else k_norm, dim, eps, dev)
-        q_out, q_out_stride = self._rows_out(q_out, q, "q_out", dev, stream)
+        q_out, q_out_stride = self._rows_out(q_out, shape, "q_out", dev, stream)
         k_ptr = k_out_ptr = None
         kv = k_stride = k_out_stride = 0
         if k is not None:
-            kv = k.shape[1]
-            _need(k.shape == (tokens, kv, dim) and kv > 0, "k: [tokens, heads, dim] with q's tokens and dim")
-            k_ptr, k_stride = k.data_ptr(), _rows(k, "k", dev)
-            k_out, k_out_stride = self._rows_out(k_out, k, "k_out", dev, stream)
+            k_ptr, k_stride, shape = k.data_ptr(), _rows(k, "k", dev), k.shape
+            kv = shape[1]
+            if shape != (tokens, kv, dim) or kv < 1:
+                raise ValueError("k: [tokens, heads, dim] with q's tokens and dim")
+            k_out, k_out_stride = self._rows_out(k_out, shape, "k_out", dev, stream)
             k_out_ptr = k_out.data_ptr()
         else:
             _need(k_out is None, "k_out: without k")
@@ -790,38 +798,46 @@ class Library:
         dev = q.device
         if dev.index != _current_device() or stream is not None:
             _on_current(dev, stream)
-        q_stride = _rows(q, "q", dev)
-        tokens, heads, dim = q.shape
-        _need(dq.shape == q.shape and (k is None) == (dk is None), "dq and dk: the shapes of q and k")
+        q_stride, dq_stride = _rows(q, "q", dev), _rows(dq, "dq", dev)
+        shape = q.shape
+        tokens, heads, dim = shape
+        if dq.shape != shape or (k is None) != (dk is None):
+            raise ValueError("dq and dk: the shapes of q and k")
         pos, freq, rot = self._rotation(tokens, positions, inv_freq, dev)
         norm = _norm(q_norm, None if k is None else k_norm, dim, eps, dev)
-        dq_out, dq_out_stride = self._rows_out(dq_out, q, "dq_out", dev, stream)
-        weights = _empty((1 if k is None else 2, dim), torch.float32, dev, stream)
-        k_ptr = dk_ptr = dk_out_ptr = dkn_ptr = None
+        dq_out, dq_out_stride = self._rows_out(dq_out, shape, "dq_out", dev, stream)
+        dq_norm = _empty((dim,), torch.float32, dev, stream)
+        dk_norm = k_ptr = dk_ptr = dk_out_ptr = dkn_ptr = None
         kv = k_stride = dk_stride = dk_out_stride = 0
         if k is not None:
-            kv = k.shape[1]
-            _need(k.shape == (tokens, kv, dim) and kv > 0 and dk.shape == k.shape, "k and dk: [tokens, heads, dim] with q's tokens and dim")
-            k_ptr, k_stride = k.data_ptr(), _rows(k, "k", dev)
-            dk_ptr, dk_stride = dk.data_ptr(), _rows(dk, "dk", dev)
-            dk_out, dk_out_stride = self._rows_out(dk_out, k, "dk_out", dev, stream)
-            dk_out_ptr, dkn_ptr = dk_out.data_ptr(), weights[1].data_ptr()
+            k_stride, dk_stride, shape = _rows(k, "k", dev), _rows(dk, "dk", dev), k.shape
+            kv = shape[1]
+            if shape != (tokens, kv, dim) or kv < 1 or dk.shape != shape:
+                raise ValueError("k and dk: [tokens, heads, dim] with q's tokens and dim")
+            dk_out, dk_out_stride = self._rows_out(dk_out, shape, "dk_out", dev, stream)
+            dk_norm = _empty((dim,), torch.float32, dev, stream)
+            k_ptr, dk_ptr, dk_out_ptr, dkn_ptr = k.data_ptr(), dk.data_ptr(), dk_out.data_ptr(), dk_norm.data_ptr()
         else:
             _need(dk_out is None, "dk_out: without k")
         raw = _raw_stream(stream, dev)
-        nbytes = self.lib.qk_norm_rope_workspace_bytes(tokens, heads, kv, dim)
+        sizes = (tokens, heads, kv, dim)
+        nbytes = self._norm_bytes.get(sizes)
+        if nbytes is None:
+            if len(self._norm_bytes) > 4096:
+                self._norm_bytes.clear()
+            nbytes = self._norm_bytes[sizes] = self.lib.qk_norm_rope_workspace_bytes(*sizes)
         # past the attention calls' arrival counters
         ws, ws_ptr, ws_bytes = self._stream_workspace(COUNTER_BYTES + nbytes, dev, raw, stream)
         st = self.lib.qk_norm_rope_backward(
-            ctypes.byref(norm), dq.data_ptr(), _rows(dq, "dq", dev), q.data_ptr(), q_stride, heads, dk_ptr, dk_stride, k_ptr,
-            k_stride, kv, tokens, dim, pos, freq, rot, amplitude, NVFP4_ROPE_INTERLEAVED if interleaved else 0,
-            dq_out.data_ptr(), dq_out_stride, dk_out_ptr, dk_out_stride, weights.data_ptr(), dkn_ptr,
-            ws_ptr + COUNTER_BYTES, ws_bytes - COUNTER_BYTES, raw)
+            ctypes.byref(norm), dq.data_ptr(), dq_stride, q.data_ptr(), q_stride, heads, dk_ptr, dk_stride, k_ptr, k_stride,
+            kv, tokens, dim, pos, freq, rot, amplitude, NVFP4_ROPE_INTERLEAVED if interleaved else 0, dq_out.data_ptr(),
+            dq_out_stride, dk_out_ptr, dk_out_stride, dq_norm.data_ptr(), dkn_ptr, ws_ptr + COUNTER_BYTES,
+            ws_bytes - COUNTER_BYTES, raw)
         if st:
             raise NVFP4Error("qk_norm_rope_backward", st)
         if stream is not None:
-            _used_on(stream, dq, dk, q, k, positions, inv_freq, q_norm, k_norm, dq_out, dk_out, weights)
-        return dq_out, dk_out, weights[0], weights[1] if k is not None else None
+            _used_on(stream, dq, dk, q, k, positions, inv_freq, q_norm, k_norm, dq_out, dk_out, dq_norm, dk_norm)
+        return dq_out, dk_out, dq_norm, dk_norm
 
     def kv_assign(self, pages: PageTable, kv_len: torch.Tensor, new_tokens: torch.Tensor, step: Step,
                   parents: torch.Tensor = None, stream=None) -> Step:
@@ -985,7 +1001,7 @@ class Library:
         and dies with the graph and whose counters are cleared at every replay."""
         key = (device.index, raw)
         cur = self._attention_ws.get(key)
-        capturing = torch.cuda.is_current_stream_capturing() if stream is None else _is_capturing(stream)
+        capturing = _capturing_now() if stream is None else _is_capturing(stream)
         if cur is not None and cur[2] >= nbytes and not capturing:
             return cur
         with torch.cuda.stream(torch.cuda.current_stream(device) if stream is None else stream):
