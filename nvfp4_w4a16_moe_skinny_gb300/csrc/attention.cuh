@@ -463,8 +463,10 @@ __device__ __forceinline__ uint32_t bits_below(int n) { return n >= 32 ? ~0u : (
 // t of its mask is set, t >= from.  With a window those are the last of the keys that the mask leaves.
 struct TreeRow {
   const uint32_t* mask;
+  uint32_t head[2];  // the first two words
   int words, ctx, n, lo, from;
   __device__ __forceinline__ uint32_t word(int i) const {
+    if (static_cast<unsigned>(i) < 2u) return i == 0 ? head[0] : head[1];
     return static_cast<unsigned>(i) < static_cast<unsigned>(words) ? __ldg(mask + i) : 0u;
   }
   // keys [key0, key0 + 32), a bit each
@@ -481,6 +483,7 @@ struct TreeRow {
 __device__ __forceinline__ TreeRow tree_row(const AttnJob& p, const Sequence& s, int tok) {
   TreeRow r;
   r.mask = p.masks + static_cast<int64_t>(s.tok0 + tok) * p.mask_words;
+  r.head[0] = __ldg(r.mask), r.head[1] = __ldg(r.mask + 1);
   r.words = p.mask_words, r.ctx = s.len - s.n, r.n = s.n;
   r.lo = 0, r.from = max(0, -r.ctx);
   if (p.window > 0) {

@@ -710,6 +710,21 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8, kPair>::kThreadsAll, Chu
     // Q of this thread's row of the walk's item: copied as it is into the tile that the
     // products with K read
     const auto fetch_q = [&](const Walk& o) {
+      if constexpr (kTree) {  // (the lanes of a row next to each other: a thread a row takes 2,048 cycles for 128 values)
+        constexpr int kLanes = kDim / 8;  // 16-byte chunks of a row
+        const int c = row % kLanes;
+#pragma unroll 4
+        for (int i = 0; i < kLanes; ++i) {
+          const int r0 = row / kLanes + i * (128 / kLanes), r = g * 128 + r0, rr = o.t.row0 + min(r, o.t.rows - 1);
+          const int tok = div_by(p.by_group, rr), head = o.h * p.group + rr - tok * p.group;
+          const uint16_t* q = p.q + (o.s.tok0 + tok) * p.q_stride + static_cast<int64_t>(head) * kDim + 8 * c;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(q_at + g * T::kQB + umma_offset(128, r0, c)),
+                       "l"(q), "r"(r < o.t.rows ? 16 : 0)
+                       : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        return;
+      }
       const int r = g * 128 + row;
       const int rr = o.t.row0 + min(r, o.t.rows - 1);
       const int tok = div_by(p.by_group, rr), head = o.h * p.group + rr - tok * p.group;
@@ -726,6 +741,8 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8, kPair>::kThreadsAll, Chu
     // Returns the factor that undoes the scaling.
     const auto hand_q = [&]() {
       asm volatile("cp.async.wait_group 0;" ::: "memory");
+      if (kTree && (kFp8 || p.scale == 0.f))  // the group's threads have copied pieces of each other's rows
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory");
       if (p.scale == 0.f) {
 #pragma unroll 1
         for (int c = 0; c < kDim / 8; ++c) {
@@ -798,6 +815,9 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8, kPair>::kThreadsAll, Chu
       const int see_hi = kTree ? ctx : min(pos + 1, w.s.len);
       const int see_lo = p.window > 0 ? (kTree ? ctx + w.s.n : pos + 1) - p.window : -(1 << 30);
 
+      TreeRow seen_by{};
+      if constexpr (kTree) seen_by = tree_row(p, w.s, tok);
+
       float m = -INFINITY, l = 0.f;  // reference of the weights, this row's sum
       for (int j = 0; j < n; ++j, ++mine) {
         const uint32_t t = nt + j;
@@ -827,7 +847,7 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8, kPair>::kThreadsAll, Chu
               }
             }
             if (kTree && partly) {
-              const uint32_t seen = tree_row(p, w.s, tok).bits(key0 + c);
+              const uint32_t seen = seen_by.bits(key0 + c);
 #pragma unroll
               for (int i = 0; i < 32; ++i) x[i] = seen >> i & 1 ? x[i] : -INFINITY;
             }
@@ -948,27 +968,52 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8, kPair>::kThreadsAll, Chu
                                                value_at(p, 0, w.h, 0, kDim), p.page_stride, p.page_log2, p.num_pages);
         };
         if constexpr (kTree)
-          restore(tree_row(p, w.s, tok));
+          restore(seen_by);
         else
           restore(KeySpan{see_lo, see_hi});
       }
       const float inv = !whole ? 1.0f : (l == 0.f ? 0.f : vs / l);
-#pragma unroll 1
-      for (int c = 0; c < kDim; c += 32) {
-        float o[32];
-        tmem_ld32(o, o_at + c);
-        tmem_loaded(o);
-        if (c == 0 && more) {  // the next item's first product may start
+      const auto write_part = [&](const float (&o)[32], int c) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 8)
+          stg256(part + static_cast<int64_t>((c + i) / 8) * T::kRows * 8, reinterpret_cast<const uint32_t*>(o) + i);
+      };
+      if constexpr (kTree) {
+        if (more) {  // the next item's first product may start
           tc_fence_before();
           qscale = hand_q();
           ready = true;
         }
-        if (whole) {
-          write_out(o, c, inv);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; i += 8)
-            stg256(part + static_cast<int64_t>((c + i) / 8) * T::kRows * 8, reinterpret_cast<const uint32_t*>(o) + i);
+#pragma unroll 1
+        for (int c = 0; c < kDim; c += 64) {  // (twice the columns in flight)
+          float o[32], o2[32];
+          tmem_ld32(o, o_at + c);
+          tmem_ld32(o2, o_at + c + 32);
+          tmem_loaded(o);
+          tmem_loaded(o2);
+          if (whole) {
+            write_out(o, c, inv);
+            write_out(o2, c + 32, inv);
+          } else if (live) {
+            write_part(o, c);
+            write_part(o2, c + 32);
+          }
+        }
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < kDim; c += 32) {
+          float o[32];
+          tmem_ld32(o, o_at + c);
+          tmem_loaded(o);
+          if (c == 0 && more) {  // the next item's first product may start
+            tc_fence_before();
+            qscale = hand_q();
+            ready = true;
+          }
+          if (whole)
+            write_out(o, c, inv);
+          else
+            write_part(o, c);
         }
       }
       float* ml = p.part + static_cast<int64_t>(2) * gridDim.x * T::kRows * kDim;  // references and sums, after all shares
