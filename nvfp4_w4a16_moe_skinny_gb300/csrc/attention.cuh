@@ -1489,20 +1489,21 @@ inline AttnShape attn_shape(int dim, bool fp8, int64_t rows, int64_t items) {
 // The same for a tree_attention call, in `items` pairs of a sequence and a kv head.  The join of its tcgen05 kernel is a
 // second grid's (attention_chunk.cuh), which makes that kernel the faster one from fewer rows on, and up to 128 rows of
 // heads of 64 and 128 values it runs as two CTAs an SM.
-// 128 values, that kernel and the split kernel: 60 to 64 rows, 16 sequences of 8,000 keys 102 and 127 us (E4M3 108
-// and 148), 64 ragged ones of up to 4,000 keys 46 and 58 (54 and 61), four of 2,000 keys 21 and 23 (23 and 24), one of 1,000
-// keys 16 and 14 (16 and 14), of 32,000 47 and 45 (45 and 44).  28 to 32 rows, 16 sequences of 8,000 keys 101 and 107 (E4M3 107
-// and 90), 64 ragged ones 46 and 54 (52 and 41), four of 2,000 keys 20 and 19, one of 32,000 keys 44 and 40.  16 rows: 100 and 96 (107 and 61).
-// 64 values, 48 to 64 rows: 68 and 72 (E4M3 70 and 77), ragged 35 and 33 (41 and 35), 47 and 49 (48 and 52), one
-// sequence 14 and 12, 31 and 25.
+// 128 values, that kernel and the split kernel: 60 to 64 rows, 16 sequences of 8,000 keys 95 and 127 us (E4M3 101
+// and 148), 64 ragged ones of up to 4,000 keys 40 and 58 (49 and 61), four of 2,000 keys 19 and 23 (21 and 24), one of 1,000
+// keys 14 and 14 (15 and 13), of 32,000 43 and 44 (41 and 44).  28 to 32 rows, 16 sequences of 8,000 keys 92 and 107 (E4M3 99
+// and 91), 64 ragged ones 40 and 54 (48 and 42), four of 2,000 keys 18 and 18 (20 and 19), one of 32,000 keys 39 and 36.  16 rows: 91
+// and 92 (98 and 61), ragged 23 and 20.
+// 64 values, 48 to 64 rows: 68 and 72 (E4M3 68 and 77), ragged 31 and 33 (36 and 36), 48 of 1,000 keys 39 and 46 (40 and 47), four
+// of 2,000 keys 16 and 17 (17 and 18), one of 32,000 keys 30 and 24.  32 rows: 67 and 59, ragged 22 and 21.
 // 256 values (one CTA an SM): 60 to 64 rows, 178 and 247 (E4M3 177 and 276), ragged 66 and 116, one sequence of 32,000 keys 60
 // and 76; 30 to 32 rows 178 and 191 (176 and 190), ragged 50 and 69 (59 and 54), four of 2,000 keys 24 and 26
 // (28 and 26), one of 1,000 keys 16 and 15 (18 and 15).
 inline AttnShape tree_shape(int dim, bool fp8, int64_t rows, int64_t items, int page_size) {
   if (dim == 256) {
     if (rows > 32 || (rows > 16 && !fp8 && items >= 32)) return {0, 0, 128, 64, true, 3};
-  } else if (rows <= 128 &&
-             (rows > 64 || (dim == 128 && ((rows > 32 && items >= 16) || (rows > 16 && !fp8 && items >= 48))))) {
+  } else if (rows <= 128 && (rows > 64 || (rows > 32 && items >= (dim == 64 ? 32 : 16)) ||
+                              (rows > 16 && dim == 128 && !fp8 && items >= 48))) {
     // tiles of 64 keys: of pages up to that size by the boxes of the larger tiles, of larger pages by the boxes of 64
     // whole rows that the split kernel has (which lie in a tile as the products read it)
     static_assert(attn_slice(128, false, 4) * 4 == 64 && attn_slice(128, true, 2) * 2 == 64 &&

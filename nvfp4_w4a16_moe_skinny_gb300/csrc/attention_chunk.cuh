@@ -74,8 +74,8 @@ struct ChunkTile {
   // Of a tree's calls, whose split items a second grid joins: shares are cheaper, so that ranges of two units and
   // boundaries that move by one pay (one sequence of 1,000 keys, 30 rows: 16.0 us against 19.8; two with 320
   // rows 20.7 against 26.7, 240 rows over four 23.4 against 28.8; pairs 15.0 with ranges of two units, 16.0 of four).
-  // Items of a pair counted with so many more units of 64 keys: 32 ragged trees over up to 16K keys 51.7 us with four, 49.1 with
-  // six, 64 ones of up to 4,000 keys 45.3 and 46.5; E4M3 67.1 and 69.1, 53.1 and 55.2.
+  // Items of a pair counted with so many more units of 64 keys, at that step: 32 ragged trees over up to 16K keys 51.7 us with
+  // four, 49.1 with six, 64 ones of up to 4,000 keys 45.3 and 46.5; E4M3 67.1 and 69.1, 53.1 and 55.2.
   static constexpr __host__ __device__ Tiling tree_tiling() { return {kRows, kKeys, kPair && !kFp8 ? 5 : kOver, 1, 2}; }
   // warps that make tiles fit: two beside the copies and the products, or (E4M3 and 128 values:
   // 256 conversions a row and tile; 830 us with two warps, 705 with four, for 2,048 tokens over
@@ -236,6 +236,30 @@ struct ChunkBars {
   NotedTiles noted;
 };
 
+// The items of a tree kernel's CTA, found by the warp that copies and read by the others: four at a time, the
+// last one of no tiles.  (Each role's own walk through the list cost it 1,000 to 2,700 cycles an item and
+// the kernel five copies of that code, beyond what the SM's instruction cache holds.)
+struct TreeItems {
+  static constexpr int kSlots = 4;
+  struct Item {
+    int b, h, tok0, fresh, len, row0, rows, lo, hi, first, n, slot, whole, pad[3];
+  };
+  uint64_t full[kSlots], empty[kSlots];
+  Item item[kSlots];
+  __device__ __forceinline__ void put(int i, const Walk& w, const Share& q) {
+    item[i % kSlots] = {w.b, w.h, w.s.tok0, w.s.n, w.s.len, w.t.row0, w.t.rows, w.t.lo, w.t.hi, q.first, q.n, q.slot, q.whole, {}};
+  }
+  // (what the roles use of a place in the list; the rest of it is the walk's own)
+  __device__ __forceinline__ void get(int i, Walk& w, Share& q) const {
+    const Item& x = item[i % kSlots];
+    w.b = x.b, w.h = x.h, w.s.tok0 = x.tok0, w.s.n = x.fresh, w.s.len = x.len;
+    w.t.row0 = x.row0, w.t.rows = x.rows, w.t.lo = x.lo, w.t.hi = x.hi;
+    q.first = x.first, q.n = x.n, q.slot = x.slot, q.whole = x.whole != 0;
+  }
+};
+constexpr size_t kTreeItemsB = 512;
+static_assert(sizeof(TreeItems) <= kTreeItemsB, "items");
+
 // The infinities and NaN among 32 values of a pool (16-byte aligned), added to o: 16 bytes a
 // load, as most of them hold none.
 template <bool kFp8>
@@ -387,6 +411,8 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8, kPair>::kThreadsAll, Chu
   const uint32_t base = (raw0 + 1023u) & ~1023u;
   ChunkBars* bars = reinterpret_cast<ChunkBars*>(smem_raw + (base - raw0) + T::kBars);
   static_assert(sizeof(ChunkBars) <= 1024, "barriers");
+  [[maybe_unused]] TreeItems* const items = reinterpret_cast<TreeItems*>(reinterpret_cast<uint8_t*>(bars) + 1024);
+  static_assert(!kTree || T::kSmem + kTreeItemsB <= (kPair ? 113 * 1024 : kMaxSmem), "shared memory");
   const uint32_t q_at = base, k_at = base + T::kKAt, v_at = base + T::kVAt, raw_at = base + T::kRaw;
 
   const int warp = static_cast<int>(uniform(threadIdx.x >> 5)), lane = threadIdx.x & 31;
@@ -401,6 +427,9 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8, kPair>::kThreadsAll, Chu
       mbar_init(&bars->p_full[i][0], 4), mbar_init(&bars->p_full[i][1], 4);
       mbar_init(bars->o_full + i, 1);
     }
+    if constexpr (kTree)
+      for (int i = 0; i < TreeItems::kSlots; ++i)
+        mbar_init(items->full + i, 1), mbar_init(items->empty + i, 1 + T::kFits + 4 * kG);
     fence_mbar_init();
   }
   bars->noted.clear(threadIdx.x);
@@ -430,24 +459,56 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8, kPair>::kThreadsAll, Chu
   const long long u0 = idle ? 0 : ranges.start(blockIdx.x), u1 = idle ? 0 : ranges.start(blockIdx.x + 1);
   Walk w;
   w.b = f.seq, w.item0 = f.before;
-  if (!idle) walk_seq(p, w, kTiling);
+  if (!kTree && !idle) walk_seq(p, w, kTiling);
   bool ran_out = false;  // a wait reached its limit (recorded): no further waits, the roles stay in step
 #define NVFP4_WAIT(bar, parity) ran_out = ran_out || !mbar_wait_warp(bar, parity)
 
   // tile counts over all items so far: ring positions and phases
   uint32_t nt = 0;
+  // A tree's next item, by whole warps of the roles that read the list: false after the last one.
+  [[maybe_unused]] int taken = 0;
+  [[maybe_unused]] Share pc;
+  [[maybe_unused]] const auto look = [&](int i, Walk& at, Share& q) {
+    NVFP4_WAIT(items->full + i % TreeItems::kSlots, i / TreeItems::kSlots & 1);
+    items->get(i, at, q);
+    return q.n > 0 && !ran_out;
+  };
+  [[maybe_unused]] const auto take = [&]() {
+    const bool some = look(taken, w, pc);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(items->empty + taken % TreeItems::kSlots);
+    ++taken;
+    return some;
+  };
   // Registers: with two softmax warpgroups the others give theirs to them (the shares add up to
-  // what the block was launched with: 384 * 168 = 128 * (72 + 2 * 216), 512 * 128 = 128 * (64 + 64 + 2 * 192);
-  // a CTA of a pair 256 * 128 = 128 * (64 + 192))
+  // what the block was launched with: 384 * 168 = 128 * (72 + 2 * 216), 512 * 128 = 128 * (64 + 64 + 2 * 192), or of a tree
+  // 128 * (72 + 72 + 2 * 184); a CTA of a pair 256 * 128 = 128 * (96 + 160)).  Trees with 64 and 192: what converts and
+  // copies spills, two of 63 tokens over 131,071 E4M3 keys 386 us instead of 371, a pair's 32 ragged ones 49.1 instead of 45.3.
   if (warp < T::kSoft0) {
     if constexpr (kG == 2 && !T::kFitGroup) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if constexpr ((kG == 2 && T::kFitGroup) || kPair) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if constexpr (kG == 2 && T::kFitGroup && !kTree) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if constexpr (kG == 2 && T::kFitGroup && kTree) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if constexpr (kPair) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
     if (warp == 0) {
       // ------------------------------------------------------------ copies
       const int piece_log2 = min(p.page_log2, log2c(kKeys));
       constexpr int kMostPieces = kKeys / 16;
       const int pieces = kKeys >> piece_log2;  // of a tile: at most kMostPieces
       uint32_t raw = 0, k_tiles = 0, v_tiles = 0;  // copied so far
+      if (kTree && !idle) walk_seq(p, w, kTiling);
+      [[maybe_unused]] const auto put = [&](const Share* q) {  // nullptr: the list's end
+        const int i = taken % TreeItems::kSlots;
+        if (taken >= TreeItems::kSlots) NVFP4_WAIT(items->empty + i, (taken / TreeItems::kSlots - 1) & 1);
+        if (lane == 0) {
+          if (q)
+            items->put(taken, w, *q);
+          else
+            items->item[i].n = 0;
+          mbar_arrive(items->full + i);
+        }
+        __syncwarp();
+        ++taken;
+      };
       for (long long u = u0; u < u1 && !ran_out;) {
         walk_to(p, w, u, kTiling);
         const Share pc = share_at(w, u, u0, u1, blockIdx.x, kTiling);
@@ -456,6 +517,7 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8, kPair>::kThreadsAll, Chu
         if (n == 0) continue;
         if (kTree && !pc.whole && pc.first == w.t.tile0 && lane == 0)
           p.split[blockIdx.x] = chunk_split_item(w, holders_of(w, ranges, kTiling).c1);
+        if constexpr (kTree) put(&pc);
         const int32_t* table = p.table + static_cast<int64_t>(w.b) * p.max_pages;
         // lane i holds the page of piece i of a tile, looked up a tile ahead of its K
         const auto look_up = [&](int j) {
@@ -515,6 +577,7 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8, kPair>::kThreadsAll, Chu
         }
         nt += n;
       }
+      if constexpr (kTree) put(nullptr);
       // the CTA's shared memory is its own until its last copies have landed, whatever ran out (bounded)
       const auto land = [&](uint64_t* full, uint32_t tiles, auto ring) {
         using R = decltype(ring);
@@ -565,10 +628,14 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8, kPair>::kThreadsAll, Chu
       const auto wait_k = [&](uint32_t t) {
         NVFP4_WAIT((kFp8 ? bars->k_ready : bars->k_full) + KRing::at(t), KRing::phase(t));
       };
-      for (long long u = u0; u < u1;) {
-        walk_to(p, w, u, kTiling);
-        const Share pc = share_at(w, u, u0, u1, blockIdx.x, kTiling);
-        u = pc.end;
+      for (long long u = u0; kTree || u < u1;) {
+        if constexpr (kTree) {
+          if (!take()) break;
+        } else {
+          walk_to(p, w, u, kTiling);
+          pc = share_at(w, u, u0, u1, blockIdx.x, kTiling);
+          u = pc.end;
+        }
         const int n = static_cast<int>(uniform(pc.n));
         if (n == 0) continue;
         const int groups = kG == 2 && uniform(w.t.rows) > 128 ? 2 : 1;
@@ -612,10 +679,14 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8, kPair>::kThreadsAll, Chu
       constexpr int kWho = 32 * T::kFits;
       const int who = (warp - T::kFit0) * 32 + lane;
       uint32_t raw = 0;
-      for (long long u = u0; u < u1;) {
-        walk_to(p, w, u, kTiling);
-        const Share pc = share_at(w, u, u0, u1, blockIdx.x, kTiling);
-        u = pc.end;
+      for (long long u = u0; kTree || u < u1;) {
+        if constexpr (kTree) {
+          if (!take()) break;
+        } else {
+          walk_to(p, w, u, kTiling);
+          pc = share_at(w, u, u0, u1, blockIdx.x, kTiling);
+          u = pc.end;
+        }
         if (pc.n == 0) continue;
         const int first = pc.first, n = pc.n;
         const KeyRange kr = key_range<kTree>(p, w);
@@ -699,7 +770,9 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8, kPair>::kThreadsAll, Chu
   } else {
     // -------------------------------------------------------------- softmax
     if constexpr (kG == 2 && !T::kFitGroup) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-    if constexpr ((kG == 2 && T::kFitGroup) || kPair) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    if constexpr (kG == 2 && T::kFitGroup && !kTree) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    if constexpr (kG == 2 && T::kFitGroup && kTree) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    if constexpr (kPair) asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
     const int g = (warp - T::kSoft0) >> 2;
     const int row = (warp & 3) * 32 + lane;              // of the group: its TMEM lane
     const uint32_t lane_at = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -783,10 +856,14 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8, kPair>::kThreadsAll, Chu
 
     float qscale = 1.0f;
     bool ready = false;  // Q of the walk's item has been handed over already
-    for (long long u = u0; u < u1;) {
-      walk_to(p, w, u, kTiling);
-      const Share pc = share_at(w, u, u0, u1, blockIdx.x, kTiling);
-      u = pc.end;
+    for (long long u = u0; kTree || u < u1;) {
+      if constexpr (kTree) {
+        if (!take()) break;
+      } else {
+        walk_to(p, w, u, kTiling);
+        pc = share_at(w, u, u0, u1, blockIdx.x, kTiling);
+        u = pc.end;
+      }
       if (pc.n == 0) continue;
       const int first = pc.first, n = pc.n;
       if (g * 128 >= w.t.rows) {  // this group has no rows here
@@ -925,11 +1002,16 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8, kPair>::kThreadsAll, Chu
       // item's Q are done: their last S has been read)
       Walk next = w;
       bool more = false;
-      for (long long v = u; v < u1 && !more;) {
-        walk_to(p, next, v, kTiling);
-        const Share q = share_at(next, v, u0, u1, blockIdx.x, kTiling);
-        more = q.n > 0;
-        v = q.end;
+      if constexpr (kTree) {
+        Share q;
+        more = look(taken, next, q);
+      } else {
+        for (long long v = u; v < u1 && !more;) {
+          walk_to(p, next, v, kTiling);
+          const Share q = share_at(next, v, u0, u1, blockIdx.x, kTiling);
+          more = q.n > 0;
+          v = q.end;
+        }
       }
       more = more && g * 128 < next.t.rows;
       if (more) fetch_q(next);
@@ -1188,8 +1270,9 @@ template <int kDim, bool kFp8, bool kTree, bool kPair>
 nvfp4_status launch_attn_chunk(const AttnJob& p, const KvMaps& maps, cudaStream_t stream) {
   using T = ChunkTile<kDim, kFp8, kPair>;
   const auto kernel = attn_chunk_kernel<kDim, kFp8, kTree, kPair>;
-  if (set_smem(kernel, T::kSmem) != cudaSuccess) return NVFP4_ERR_CUDA;
-  if (launch_pdl(kernel, dim3(kAttnGrid * T::kCtas), dim3(T::kThreadsAll), T::kSmem, stream, p, maps) != cudaSuccess)
+  constexpr size_t smem = T::kSmem + (kTree ? kTreeItemsB : 0);
+  if (set_smem(kernel, smem) != cudaSuccess) return NVFP4_ERR_CUDA;
+  if (launch_pdl(kernel, dim3(kAttnGrid * T::kCtas), dim3(T::kThreadsAll), smem, stream, p, maps) != cudaSuccess)
     return NVFP4_ERR_CUDA;
   if constexpr (kTree) {  // (one unit an item: nothing can be split)
     if ((static_cast<int64_t>(p.max_pages) << p.page_log2) > T::kKeys &&
