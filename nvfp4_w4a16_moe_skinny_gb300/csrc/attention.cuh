@@ -1489,11 +1489,11 @@ inline AttnShape attn_shape(int dim, bool fp8, int64_t rows, int64_t items) {
 // The same for a tree_attention call, in `items` pairs of a sequence and a kv head.  The join of its tcgen05 kernel is a
 // second grid's (attention_chunk.cuh), which makes that kernel the faster one from fewer rows on, and up to 128 rows of
 // heads of 64 and 128 values it runs as two CTAs an SM.
-// 128 values, that kernel and the split kernel: 60 to 64 rows, 16 sequences of 8,000 keys 95 and 127 us (E4M3 101
-// and 148), 64 ragged ones of up to 4,000 keys 40 and 58 (49 and 61), four of 2,000 keys 19 and 23 (21 and 24), one of 1,000
-// keys 14 and 14 (15 and 13), of 32,000 43 and 44 (41 and 44).  28 to 32 rows, 16 sequences of 8,000 keys 92 and 107 (E4M3 99
-// and 91), 64 ragged ones 40 and 54 (48 and 42), four of 2,000 keys 18 and 18 (20 and 19), one of 32,000 keys 39 and 36.  16 rows: 91
-// and 92 (98 and 61), ragged 23 and 20.
+// 128 values, that kernel and the split kernel: 60 to 64 rows, 16 sequences of 8,000 keys 95 and 127 us (E4M3 97
+// and 148), 64 ragged ones of up to 4,000 keys 40 and 58 (47 and 61), four of 2,000 keys 19 and 23 (21 and 24), one of
+// 1,000 keys 14 and 14 (15 and 13), of 32,000 43 and 44 (41 and 44).  28 to 32 rows, 16 sequences of 8,000 keys 92 and
+// 107 (E4M3 97 and 91), 64 ragged ones 40 and 54 (47 and 42), four of 2,000 keys 18 and 18 (20 and 19), one of 32,000
+// keys 39 and 36.  16 rows: 91 and 92 (98 and 61), ragged 23 and 20.
 // 64 values, 48 to 64 rows: 68 and 72 (E4M3 68 and 77), ragged 31 and 33 (36 and 36), 48 of 1,000 keys 39 and 46 (40 and 47), four
 // of 2,000 keys 16 and 17 (17 and 18), one of 32,000 keys 30 and 24.  32 rows: 67 and 59, ragged 22 and 21.
 // 256 values (one CTA an SM): 60 to 64 rows, 178 and 247 (E4M3 177 and 276), ragged 66 and 116, one sequence of 32,000 keys 60

@@ -49,10 +49,12 @@ namespace nvfp4 {
 template <int kN>
 struct Ring {
   static constexpr int kStages = kN, kLog2 = log2c(kN);
-  static __device__ __forceinline__ uint32_t at(uint32_t t) { return t & (kN - 1); }
-  static __device__ __forceinline__ uint32_t phase(uint32_t t) { return (t >> kLog2) & 1; }
+  static constexpr bool kPower = (kN & (kN - 1)) == 0;
+  static __device__ __forceinline__ uint32_t round(uint32_t t) { return kPower ? t >> kLog2 : t / kN; }
+  static __device__ __forceinline__ uint32_t at(uint32_t t) { return kPower ? t & (kN - 1) : t % kN; }
+  static __device__ __forceinline__ uint32_t phase(uint32_t t) { return round(t) & 1; }
   static __device__ __forceinline__ bool reused(uint32_t t) { return t >= kN; }
-  static __device__ __forceinline__ uint32_t before(uint32_t t) { return ((t >> kLog2) - 1) & 1; }
+  static __device__ __forceinline__ uint32_t before(uint32_t t) { return (round(t) - 1) & 1; }
 };
 
 // kPair: one row group a CTA and two CTAs an SM (trees of up to 128 rows; see below).
@@ -93,13 +95,15 @@ struct ChunkTile {
   static constexpr int kTileB = kKeys * kDim * 2;          // a 16-bit tile: [kDim / 64][kKeys][128 bytes]
   static constexpr int kQB = 128 * kDim * 2;               // a group's Q: [kDim / 64][128][128 bytes]
   // stages of the rings (K and V as the products read them, E4M3 tiles as they are copied):
-  // powers of two, as many as fit.  E4M3 heads of 64 values: 2,048 tokens 34.2 us against 41.0 with one
+  // as many as fit.  E4M3 heads of 64 values: 2,048 tokens 34.2 us against 41.0 with one
   // stage of K and two of V; four stages of copies against two: 2% for 1,500-token pieces.  128 values:
   // 2,048 tokens over 32,768 keys 705 us with two stages of K and two of copies, 1,117 with one and four;
   // 256 values, whose row group waits for copies more than for K, 2,538 and 2,403.
   using KRing = Ring<kDim == 64 ? 4 : (kFp8 && (kDim == 256 || kPair) ? 1 : 2)>;
   using VRing = Ring<kDim == 64 ? 4 : 2>;
-  using RawRing = Ring<kDim == 128 ? 2 : 4>;
+  // A pair's CTA, 128 values: 16 sequences of 8,000 E4M3 keys 97 us with three stages of copies, 102 with two (100
+  // sequences of 60 keys 34.4 and 33.4); 64 values the same with four, six and eight.
+  using RawRing = Ring<kDim == 128 ? (kPair ? 3 : 2) : 4>;
   static constexpr int kKAt = kGroups * kQB, kVAt = kKAt + KRing::kStages * kTileB;
   static constexpr int kRaw = kVAt + VRing::kStages * kTileB;
   static constexpr int kBars = kRaw + (kFp8 ? RawRing::kStages * kRawB : 0);
