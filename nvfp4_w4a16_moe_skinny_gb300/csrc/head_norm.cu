@@ -11,8 +11,8 @@
 //
 // A thread holds 16 values of a head, 8 pairs, and walks heads with the same angles and weights; the lanes of a head
 // share its sums by shuffles.  Bound by memory at prompt sizes: 8,191 tokens of 32 + 8 heads of 128
-// values (168 MB) take 29.4 us, 5.7 TB/s or 84% of the rate of a plain copy, into an E4M3 cache with their values
-// (185 MB) 32.8 us (83%), back (252 MB) 47.2 us (79%, 4 us of it the second grid, which sums the weights' gradients).  By the launch at
+// values (168 MB) take 28.7 us, 5.8 TB/s or 86% of the rate of a plain copy, into an E4M3 cache with their values
+// (185 MB) 32.1 us (85%), back (252 MB) 46.2 us (80%, 3 us of it the second grid, which sums the weights' gradients).  By the launch at
 // decode sizes: 16 tokens 3.4 us, back 7.2 us.
 #include <cmath>
 #include <cstdint>
@@ -327,7 +327,7 @@ struct BackwardUnits {
 };
 
 // kLanesLog2: lanes of a head whose chunks fill them (64, 128 and 256 values), or -1: any head.  (Registers and ring for
-// four blocks an SM: 47.2 us; for three 54.8, for five, which spill, 67.5; eight slots of the ring, three blocks, 58.7.)
+// four blocks an SM, with an earlier second grid: 47.2 us; for three 54.8, for five, which spill, 67.5; eight slots of the ring, three blocks, 58.7.)
 template <bool kInterleaved, int kLanesLog2>
 __global__ void __launch_bounds__(kNormThreads, 4) norm_rope_backward_kernel(const NormJob p, const BackwardUnits units) {
   __shared__ __align__(16) uint8_t ring_bytes[OwnRing<4>::kBytes];
@@ -454,8 +454,9 @@ auto backward_kernel(int dim) {
 }
 
 // dg of q and k from the blocks' shares, in their order: a block for 32 columns of one of them, a
-// warp for every 32nd share.
-constexpr int kJoinColumns = 32, kJoinSlices = 32;
+// warp for every 32nd share, whose loads (19 of a full grid's 608 shares) are in flight together: 1 us less than
+// eight at a time.
+constexpr int kJoinColumns = 32, kJoinSlices = 32, kJoinBatch = 20;
 __global__ void __launch_bounds__(kJoinColumns* kJoinSlices) norm_weight_kernel(const float* partial, int dim, int shares_q,
                                                                               int shares_k, float* dq_weight,
                                                                               float* dk_weight) {
@@ -468,8 +469,16 @@ __global__ void __launch_bounds__(kJoinColumns* kJoinSlices) norm_weight_kernel(
   const int n = kind ? shares_k : shares_q;
   float sum = 0.f;
   if (col < dim) {
-#pragma unroll 8
-    for (int i = slice; i < n; i += kJoinSlices) sum += __ldcg(from + static_cast<int64_t>(i) * dim + col);
+    for (int i = slice; i < n; i += kJoinBatch * kJoinSlices) {
+      float share[kJoinBatch];
+#pragma unroll
+      for (int j = 0; j < kJoinBatch; ++j) {
+        const int at = i + j * kJoinSlices;
+        share[j] = at < n ? __ldcg(from + static_cast<int64_t>(at) * dim + col) : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < kJoinBatch; ++j) sum += share[j];
+    }
   }
   sums[slice][lane] = sum;
   __syncthreads();
