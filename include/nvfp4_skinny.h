@@ -622,7 +622,7 @@ nvfp4_status kv_append_norm(const nvfp4_kv_cache *cache, const nvfp4_qk_norm *no
  *   page_table  int32 [n_seqs, max_pages]: entries [0, held[b]) of row b are its pages.
  *   held        int32 [n_seqs].
  *   free_pages  int32 [num_free]: a stack, its first free_count[0] entries are free pages.
- *   page_size   as in nvfp4_kv_cache.  n_seqs at most 16,384; max_pages * page_size < 2^30.
+ *   page_size   as in nvfp4_kv_cache.  n_seqs at most 16,384; max_pages * page_size and num_free < 2^30.
  */
 typedef struct {
   int32_t *page_table;
@@ -677,7 +677,7 @@ nvfp4_status kv_assign(const nvfp4_page_table *pages, const int32_t *kv_len, con
 /*
  * Keeps an accepted path of every sequence's new tokens: with n new tokens (the last n of
  * kv_len[b] keys) and ctx = kv_len[b] - n, the cache rows of key ctx + path[d] move to key ctx + d for
- * d = 0, 1, ... in every kv head of k and v, and kv_len_out[b] = ctx + the path's length.  The rows
+ * d = 0, 1, ... in every kv head of k and v, and kv_len_out[b] = max(0, ctx + the path's length).  The rows
  * keep their rotation: a token at depth d of its tree was rotated to position ctx + d.
  *   batch       cu_tokens, kv_len and page_table are read.  n_seqs at most 65,535.
  *   paths       (device) int32 [n_seqs, path_len], indices among the sequence's new tokens, ascending

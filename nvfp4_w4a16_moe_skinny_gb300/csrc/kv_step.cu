@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kAcceptThreads) kv_accept_kernel(const AcceptJ
   if (threadIdx.x == 0 && count < p.path_len && __ldg(path + count) >= 0) bad = true;
   __syncthreads();
   if (blockIdx.x == 0) {
-    if (threadIdx.x == 0) p.kv_len_out[b] = ctx + count;
+    if (threadIdx.x == 0) p.kv_len_out[b] = max(0, ctx + count);  // (kv_len may be below the new tokens)
     if (bad) atomicOr(&g_device_error, kErrStep);
   }
   const int columns = 2 * p.n_kv << p.row_log2, column = blockIdx.x * kAcceptThreads + threadIdx.x;
@@ -349,7 +349,8 @@ nvfp4_status kv_assign(const nvfp4_page_table* pages, const int32_t* kv_len, con
                        const int32_t* parents, const nvfp4_step* step, cudaStream_t stream) {
   if (!pages || !step) return NVFP4_ERR_NULL;
   const int seqs = pages->n_seqs, rows = step->n_tokens;
-  if (seqs < 0 || seqs > kMostSeqs || pages->max_pages < 1 || pages->num_free < 0 || rows < 0 || rows >= (1 << 30))
+  if (seqs < 0 || seqs > kMostSeqs || pages->max_pages < 1 || pages->num_free < 0 || pages->num_free >= (1 << 30) ||
+      rows < 0 || rows >= (1 << 30))  // (sums of rows and pages are held at 2^30)
     return NVFP4_ERR_SHAPE;
   if (pages->page_size < 16 || pages->page_size > 256 || (pages->page_size & (pages->page_size - 1))) return NVFP4_ERR_SHAPE;
   if (static_cast<int64_t>(pages->max_pages) * pages->page_size >= (int64_t{1} << 30)) return NVFP4_ERR_SHAPE;

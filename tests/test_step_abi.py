@@ -125,7 +125,7 @@ def step(**kw):
 @pytest.mark.parametrize("kw,status", [
     (dict(page_table=None), NULL), (dict(held=None), NULL), (dict(free_pages=None), NULL), (dict(free_count=None), NULL),
     (dict(n_seqs=-1), SHAPE), (dict(n_seqs=16385), SHAPE), (dict(max_pages=0), SHAPE), (dict(max_pages=1 << 26), SHAPE),
-    (dict(page_size=8), SHAPE), (dict(page_size=48), SHAPE), (dict(page_size=512), SHAPE), (dict(num_free=-1), SHAPE),
+    (dict(page_size=8), SHAPE), (dict(page_size=48), SHAPE), (dict(page_size=512), SHAPE), (dict(num_free=-1), SHAPE), (dict(num_free=1 << 30), SHAPE),
     (dict(page_table=P + 2), ALIGN), (dict(held=P + 1), ALIGN), (dict(free_pages=P + 2), ALIGN), (dict(free_count=P + 2), ALIGN)])
 def test_page_tables_are_refused(so, kw, status):
     t, s = pages(**kw), step()
