@@ -1180,17 +1180,22 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8, kPair>::kThreadsAll, Chu
 
 // ------------------------------------------------------------------ the join of trees' split items
 
-// A block of 128 threads joins 16 columns of up to 128 rows of one item, a thread a row, in range order: the
-// result does not depend on timing.  kBatch shares in flight a thread.
-constexpr int kChunkJoinGrid = 8 * kAttnGrid;
+// A block of 128 threads joins 8 columns of up to 128 rows of one item, a thread a row, in range order: the
+// result does not depend on timing.  Bound by latency: the list, then an item's shares, kBatch of them in flight a thread.
+// Eight columns and eight shares in blocks that are on the chip at once, against 16 and four in twice as many: four sequences
+// of 2,000 keys with 62 rows 20 us against 23, 32 ragged ones of up to 16K keys 44 and 45, one of 32,000 keys of 256 values
+// 55 and 57; 48 of 1,000 keys, whose many items have two shares each, 55 and 54.  (Fewer in flight, four of 2,000 keys:
+// three 28 us, two 30.  A batch of two for items of two shares: the same.  A block for every range and column block, without
+// a list: 22.)
+constexpr int kChunkJoinGrid = 4 * kAttnGrid;
 template <int kDim>
 __global__ void __launch_bounds__(128) attn_chunk_join_kernel(const AttnJob p, int split_grid, int tile_rows) {
   __shared__ int4 list[2 * kAttnGrid];
-  __shared__ int warp_sum[4];
+  constexpr int kSpan = (2 * kAttnGrid + 127) / 128;
+  __shared__ int warp_sum[4 * kSpan];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
   pdl_launch_dependents();
-  constexpr int kSpan = (2 * kAttnGrid + 127) / 128;
   int items = 0;
   int4 mine[kSpan];
 #pragma unroll
@@ -1198,34 +1203,38 @@ __global__ void __launch_bounds__(128) attn_chunk_join_kernel(const AttnJob p, i
     const int c = b * 128 + threadIdx.x;
     mine[b] = c < split_grid ? __ldcg(p.split + c) : make_int4(0, 0, 0, 0);
   }
+  unsigned some[kSpan];
 #pragma unroll
   for (int b = 0; b < kSpan; ++b) {
-    const unsigned all = __ballot_sync(0xffffffffu, mine[b].x != 0);
-    if (lane == 0) warp_sum[warp] = __popc(all);
-    __syncthreads();
-    int at = items + __popc(all & ((1u << lane) - 1));
+    some[b] = __ballot_sync(0xffffffffu, mine[b].x != 0);
+    if (lane == 0) warp_sum[b * 4 + warp] = __popc(some[b]);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int b = 0; b < kSpan; ++b) {
+    int at = items + __popc(some[b] & ((1u << lane) - 1));
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      if (x < warp) at += warp_sum[x];
-      items += warp_sum[x];
+      if (x < warp) at += warp_sum[b * 4 + x];
+      items += warp_sum[b * 4 + x];
     }
     if (mine[b].x != 0) list[at] = make_int4(mine[b].x | (b * 128 + threadIdx.x) << 18, mine[b].y, mine[b].z, mine[b].w);
-    __syncthreads();
   }
+  __syncthreads();
   const float* ml = p.part + static_cast<int64_t>(2) * split_grid * tile_rows * kDim;
-  constexpr int kBatch = 4, kBlocks = kDim / 16;
+  constexpr int kBatch = 8, kBlocks = kDim / 8;
   const int parts = kBlocks * (tile_rows / 128);
   for (int x = blockIdx.x; x < items * parts; x += gridDim.x) {
     const int4 it = list[x / parts];
-    const int part = x - x / parts * parts, c = part % kBlocks * 16, r = part / kBlocks * 128 + threadIdx.x;
+    const int part = x - x / parts * parts, c = part % kBlocks * 8, r = part / kBlocks * 128 + threadIdx.x;
     const int c0 = it.x >> 18, c1 = it.x & 0x1ff, rows = it.x >> 9 & 0x1ff;
     if (r >= rows) continue;
-    float m = -INFINITY, l = 0.f, acc[16];
+    float m = -INFINITY, l = 0.f, acc[8];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) acc[j] = 0.f;
+    for (int j = 0; j < 8; ++j) acc[j] = 0.f;
     for (int i0 = c0; i0 <= c1; i0 += kBatch) {
       float2 v[kBatch];
-      float4 y[kBatch][4];
+      float4 y[kBatch][2];
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         const int i = i0 + k;
@@ -1236,7 +1245,7 @@ __global__ void __launch_bounds__(128) attn_chunk_join_kernel(const AttnJob p, i
         const float4* o = reinterpret_cast<const float4*>(p.part + slot * tile_rows * kDim +
                                                           (static_cast<int64_t>(c / 8) * tile_rows + r) * 8);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) y[k][j] = __ldcg(o + (j / 2) * tile_rows * 2 + (j & 1));
+        for (int j = 0; j < 2; ++j) y[k][j] = __ldcg(o + j);
       }
       float next = m;
 #pragma unroll
@@ -1244,14 +1253,14 @@ __global__ void __launch_bounds__(128) attn_chunk_join_kernel(const AttnJob p, i
       const float a0 = next == -INFINITY ? 1.0f : exp2_approx(m - next);
       l *= a0;
 #pragma unroll
-      for (int j = 0; j < 16; ++j) acc[j] *= a0;
+      for (int j = 0; j < 8; ++j) acc[j] *= a0;
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         if (i0 + k > c1) break;
         const float a = next == -INFINITY ? 1.0f : exp2_approx(v[k].x - next);
         l += a * v[k].y;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < 2; ++j)
           acc[4 * j] += a * y[k][j].x, acc[4 * j + 1] += a * y[k][j].y, acc[4 * j + 2] += a * y[k][j].z,
               acc[4 * j + 3] += a * y[k][j].w;
       }
@@ -1260,12 +1269,11 @@ __global__ void __launch_bounds__(128) attn_chunk_join_kernel(const AttnJob p, i
     const int rr = it.z + r, tok = div_by(p.by_group, rr), head = it.y * p.group + rr - tok * p.group;
     const int64_t row = it.w + tok;
     const float inv = l == 0.f ? 0.f : (p.v_scale ? __ldg(p.v_scale + it.y) : 1.0f) / l;
-    uint32_t o[8];
+    uint32_t o[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] = f32x2_to_bf16x2(acc[2 * j] * inv, acc[2 * j + 1] * inv);
+    for (int j = 0; j < 4; ++j) o[j] = f32x2_to_bf16x2(acc[2 * j] * inv, acc[2 * j + 1] * inv);
     uint4* out = reinterpret_cast<uint4*>(p.out + row * p.out_stride + static_cast<int64_t>(head) * kDim + c);
     out[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    out[1] = make_uint4(o[4], o[5], o[6], o[7]);
     if (p.lse && c == 0) p.lse[row * p.n_heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
   }
 }
