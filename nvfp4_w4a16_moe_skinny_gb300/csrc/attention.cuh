@@ -682,6 +682,13 @@ __device__ __forceinline__ uint4 clean_chunk(uint4 v, bool seen, bool& noted) {
   return make_uint4(v.x & ~a, v.y & ~b, v.z & ~c, v.w & ~d);
 }
 
+// sum + 0 * v of eight bf16 values: zeros, of either sign, unless v holds an infinity or NaN.
+__device__ __forceinline__ void add_times_zero(uint32_t (&sum)[4], uint4 v) {
+  const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum[i]) : "r"(x[i]), "r"(0u));
+}
+
 // The same for 16 E4M3 codes (NaN is 0x7f or 0xff; there are no infinities).
 __device__ __forceinline__ uint4 clean_codes(uint4 v, bool seen, bool& noted) {
   if (!seen) return make_uint4(0, 0, 0, 0);

@@ -695,6 +695,11 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8, kPair>::kThreadsAll, Chu
         const int first = pc.first, n = pc.n;
         const KeyRange kr = key_range<kTree>(p, w);
         if constexpr (!kFp8) {
+          // A row is looked through first, and written only where something has to be taken out: at that, which is
+          // rare, a chunk at a time (four trees in a window of 1,024 keys of 256 values 19.0 us instead of 19.7, 64 of
+          // up to 4,000 keys of 128 values 38.9 instead of 40.6; two of 20,000 keys of 64 values 56.9 instead of 55.2).
+          constexpr bool kLook = kTree && kDim > 64;
+          constexpr int kLoads = kLook ? 1 : 8;
           for (int j = 0; j < n; ++j) {
             const uint32_t t = nt + j, st = VRing::at(t);
             NVFP4_WAIT(bars->v_full + st, VRing::phase(t));
@@ -704,13 +709,28 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8, kPair>::kThreadsAll, Chu
               bool noted = false;
               for (int r = who; r < kKeys; r += kWho) {
                 const bool seen = key0 + r >= kr.any_lo && key0 + r < kr.any_hi;
+                if constexpr (kLook) {
+                  uint32_t sum[4] = {0, 0, 0, 0};
 #pragma unroll 1
-                for (int c0 = 0; c0 < kDim / 8; c0 += 8) {  // (eight loads in flight)
-                  uint4 v[8];
+                  for (int c0 = 0; c0 < kDim / 8; c0 += 8) {
 #pragma unroll
-                  for (int c = 0; c < 8; ++c) v[c] = lds128(tile + umma_offset(kKeys, r, c0 + c));
+                    for (int c = 0; c < 8; ++c) {
+                      const uint32_t at = tile + umma_offset(kKeys, r, c0 + c);
+                      if (seen)
+                        add_times_zero(sum, lds128(at));
+                      else
+                        sts128(at, make_uint4(0, 0, 0, 0));
+                    }
+                  }
+                  if (((sum[0] | sum[1] | sum[2] | sum[3]) & 0x7fff7fffu) == 0) continue;
+                }
+#pragma unroll 1
+                for (int c0 = 0; c0 < kDim / 8; c0 += kLoads) {  // (kLoads in flight)
+                  uint4 v[kLoads];
 #pragma unroll
-                  for (int c = 0; c < 8; ++c)
+                  for (int c = 0; c < kLoads; ++c) v[c] = lds128(tile + umma_offset(kKeys, r, c0 + c));
+#pragma unroll
+                  for (int c = 0; c < kLoads; ++c)
                     sts128(tile + umma_offset(kKeys, r, c0 + c), clean_chunk<false>(v[c], seen, noted));
                 }
               }
