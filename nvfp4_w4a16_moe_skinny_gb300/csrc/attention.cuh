@@ -557,6 +557,15 @@ __device__ __forceinline__ float tanh_small(float x) {
   p = fmaf(z, p, -0.33333333f);
   return fmaf(x * z, p, x);
 }
+__device__ __forceinline__ f32x2 tanh_small2(f32x2 x) {
+  const auto both = [](float c) { return pack2(c, c); };
+  const f32x2 z = mul2(x, x);
+  f32x2 p = fma2(z, both(-0.00694294f), both(0.02147068f));
+  p = fma2(z, p, both(-0.05393347f));
+  p = fma2(z, p, both(0.13333226f));
+  p = fma2(z, p, both(-0.33333333f));
+  return fma2(mul2(x, z), p, x);
+}
 __device__ __forceinline__ float tanh_any(float x) {
   return fabsf(x) < kTanhSmall ? tanh_small(x)
                                : 1.0f - __fdividef(2.0f, exp2_approx(x * 2.8853900817779268f) + 1.0f);

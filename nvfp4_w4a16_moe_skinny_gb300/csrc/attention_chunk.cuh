@@ -942,6 +942,12 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8, kPair>::kThreadsAll, Chu
               if (__any_sync(0xffffffffu, high >= kTanhSmall)) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) x[i] = tanh_any(x[i]);
+              } else if constexpr (kTree) {  // (in pairs: 16 sequences of 8,000 E4M3 keys 131 us instead of 148)
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                  const f32x2 y = tanh_small2(pack2(x[i], x[i + 1]));
+                  x[i] = lo2(y), x[i + 1] = hi2(y);
+                }
               } else {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) x[i] = tanh_small(x[i]);
