@@ -1073,7 +1073,14 @@ __global__ void __launch_bounds__(AttnTile<kDim, kFp8, kRW, kKW>::kThreadsAll, a
 #pragma unroll
             for (int j = 0; j < kNT; ++j)
 #pragma unroll
-              for (int x = 0; x < 4; ++x) s[j][x] = cap2 * tanh_small(s[j][x]);
+              for (int x = 0; x < 4; x += kTree ? 2 : 1) {
+                if constexpr (kTree) {
+                  const f32x2 y = mul2(pack2(cap2, cap2), tanh_small2(pack2(s[j][x], s[j][x + 1])));
+                  s[j][x] = lo2(y), s[j][x + 1] = hi2(y);
+                } else {
+                  s[j][x] = cap2 * tanh_small(s[j][x]);
+                }
+              }
           }
         }
         if (kTree && (key0 + T::kSlice > all_hi || key0 < all_lo)) {
