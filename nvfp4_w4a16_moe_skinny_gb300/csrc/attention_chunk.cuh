@@ -400,6 +400,19 @@ __device__ __forceinline__ int4 chunk_split_item(const Walk& w, int c1) {
   return make_int4(c1 | w.t.rows << 9, w.h, w.t.row0, w.s.tok0);
 }
 
+// mbar_wait_warp for a single thread.
+__device__ __forceinline__ bool mbar_wait_thread(uint64_t* bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (true) {
+    if (mbar_try_wait_sleep(bar, parity, 1u << 20)) return true;
+    if (clock64() - t0 > kWaitCycles) {
+      atomicOr(&g_device_error, kErrWaitTimeout);
+      return false;
+    }
+  }
+}
+
 // ------------------------------------------------------------------ the kernel
 
 template <int kDim, bool kFp8, bool kTree, bool kPair>
@@ -600,84 +613,106 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8, kPair>::kThreadsAll, Chu
       // descriptors: the start address is the low 14 bits, in units of 16 bytes
       const uint64_t q_desc = umma_desc(q_at, 16, 1024), k_desc = umma_desc(k_at, 16, 1024);
       const uint64_t v_desc = umma_desc(v_at, kKeys * 128, 1024);
+      // A tree's by one thread throughout, without elections and votes: two sequences of 20,000 keys with 504 rows, 256 values
+      // 139 us instead of 154, 64 values 51 instead of 56.  (Not where a warpgroup converts beside two of softmax: that
+      // kernel's registers ran out, two of 131,071 keys 400 us instead of 371.)
+      constexpr bool kOne = kTree && !(kG == 2 && T::kFitGroup);
+      const auto issue = [&](auto f) {
+        if constexpr (kOne) {
+          f();
+        } else {
+          if (elect_one()) f();
+          __syncwarp();
+        }
+      };
+#define NVFP4_WAIT_ONE(bar, parity) \
+  ran_out = ran_out || !(kOne ? mbar_wait_thread(bar, parity) : mbar_wait_warp(bar, parity))
       const auto qk = [&](int g, uint32_t t) {
         const uint32_t d = tmem + T::kSCol + (kG == 2 ? g : (t & 1)) * kKeys;
         const uint64_t a = q_desc + g * (T::kQB >> 4), b = k_desc + KRing::at(t) * (T::kTileB >> 4);
-        if (elect_one()) {
+        issue([&] {
 #pragma unroll
           for (int k = 0; k < kDim / 16; ++k)
             umma_ss(d, a + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4),
                     b + (((k >> 2) * (kKeys * 128) + (k & 3) * 32) >> 4), id_qk, k > 0);
           umma_commit(bars->s_full + (kG == 2 ? g : (t & 1)));
-        }
-        __syncwarp();
+        });
       };
       const auto pv = [&](int g, uint32_t t, int half, bool add) {
         const uint32_t a = tmem + T::kSCol + (kG == 2 ? g : (t & 1)) * kKeys;
         const uint64_t b = v_desc + VRing::at(t) * (T::kTileB >> 4);
-        if (elect_one()) {
+        issue([&] {
 #pragma unroll
           for (int i = 0; i < kKeys / 32; ++i) {
             const int k = half * (kKeys / 32) + i;
             umma_ts(tmem + g * kDim, a + 8 * k, b + k * (2048 >> 4), id_pv, add || i > 0);
           }
           if (half == 1) umma_commit(bars->o_full + (kG == 2 ? g : (t & 1)));
-        }
-        __syncwarp();
+        });
       };
-      const auto free_tile = [&](uint64_t* bar) {
-        if (elect_one()) umma_commit(bar);
-        __syncwarp();
-      };
+      const auto free_tile = [&](uint64_t* bar) { issue([&] { umma_commit(bar); }); };
       const auto wait_k = [&](uint32_t t) {
-        NVFP4_WAIT((kFp8 ? bars->k_ready : bars->k_full) + KRing::at(t), KRing::phase(t));
+        NVFP4_WAIT_ONE((kFp8 ? bars->k_ready : bars->k_full) + KRing::at(t), KRing::phase(t));
       };
-      for (long long u = u0; kTree || u < u1;) {
-        if constexpr (kTree) {
-          if (!take()) break;
-        } else {
-          walk_to(p, w, u, kTiling);
-          pc = share_at(w, u, u0, u1, blockIdx.x, kTiling);
-          u = pc.end;
-        }
-        const int n = static_cast<int>(uniform(pc.n));
-        if (n == 0) continue;
-        const int groups = kG == 2 && uniform(w.t.rows) > 128 ? 2 : 1;
-        for (int g = 0; g < groups; ++g) {
-          NVFP4_WAIT(bars->q_full + g, nq[g] & 1);
-          ++nq[g];
-        }
-        wait_k(nt);
-        tc_fence_after();
-        for (int g = 0; g < groups; ++g) qk(g, nt);
-        free_tile(bars->k_empty + KRing::at(nt));
-        for (int j = 0; j < n; ++j) {
-          const uint32_t t = nt + j;
-          if (kG == 1 && j + 1 < n) {
-            wait_k(t + 1);
-            tc_fence_after();
-            qk(0, t + 1);
-            free_tile(bars->k_empty + KRing::at(t + 1));
+      if (!kOne || elect_one()) {
+        for (long long u = u0; kTree || u < u1;) {
+          if constexpr (kOne) {
+            NVFP4_WAIT_ONE(items->full + taken % TreeItems::kSlots, taken / TreeItems::kSlots & 1);
+            items->get(taken, w, pc);
+            mbar_arrive(items->empty + taken % TreeItems::kSlots);
+            ++taken;
+            if (pc.n == 0 || ran_out) break;
+          } else if constexpr (kTree) {
+            if (!take()) break;
+          } else {
+            walk_to(p, w, u, kTiling);
+            pc = share_at(w, u, u0, u1, blockIdx.x, kTiling);
+            u = pc.end;
           }
-          NVFP4_WAIT(bars->v_ready + VRing::at(t), VRing::phase(t));
-          if constexpr (!kFp8) NVFP4_WAIT(bars->v_full + VRing::at(t), VRing::phase(t));
-          if (kG == 2 && j + 1 < n) wait_k(t + 1);
+          const int n = kOne ? pc.n : static_cast<int>(uniform(pc.n));
+          if (n == 0) continue;
+          const int groups = kG == 2 && (kOne ? w.t.rows : uniform(w.t.rows)) > 128 ? 2 : 1;
           for (int g = 0; g < groups; ++g) {
-            const int pb = kG == 2 ? g : (t & 1);
-            NVFP4_WAIT(&bars->p_full[pb][0], np[pb] & 1);
-            tc_fence_after();
-            pv(g, t, 0, j > 0);
-            NVFP4_WAIT(&bars->p_full[pb][1], np[pb] & 1);
-            ++np[pb];
-            tc_fence_after();
-            pv(g, t, 1, true);
-            if (kG == 2 && j + 1 < n) qk(g, t + 1);
+            NVFP4_WAIT_ONE(bars->q_full + g, nq[g] & 1);
+            ++nq[g];
           }
-          free_tile(bars->v_empty + VRing::at(t));
-          if (kG == 2 && j + 1 < n) free_tile(bars->k_empty + KRing::at(t + 1));
+          wait_k(nt);
+          tc_fence_after();
+          for (int g = 0; g < groups; ++g) qk(g, nt);
+          free_tile(bars->k_empty + KRing::at(nt));
+          for (int j = 0; j < n; ++j) {
+            const uint32_t t = nt + j;
+            if (kG == 1 && j + 1 < n) {
+              wait_k(t + 1);
+              tc_fence_after();
+              qk(0, t + 1);
+              free_tile(bars->k_empty + KRing::at(t + 1));
+            }
+            NVFP4_WAIT_ONE(bars->v_ready + VRing::at(t), VRing::phase(t));
+            if constexpr (!kFp8) NVFP4_WAIT_ONE(bars->v_full + VRing::at(t), VRing::phase(t));
+            if (kG == 2 && j + 1 < n) wait_k(t + 1);
+            for (int g = 0; g < groups; ++g) {
+              const int pb = kG == 2 ? g : (t & 1);
+              if (!kPair) {
+                NVFP4_WAIT_ONE(&bars->p_full[pb][0], np[pb] & 1);
+                tc_fence_after();
+                pv(g, t, 0, j > 0);
+              }
+              NVFP4_WAIT_ONE(&bars->p_full[pb][1], np[pb] & 1);
+              ++np[pb];
+              tc_fence_after();
+              if (kPair) pv(g, t, 0, j > 0);
+              pv(g, t, 1, true);
+              if (kG == 2 && j + 1 < n) qk(g, t + 1);
+            }
+            free_tile(bars->v_empty + VRing::at(t));
+            if (kG == 2 && j + 1 < n) free_tile(bars->k_empty + KRing::at(t + 1));
+          }
+          nt += n;
         }
-        nt += n;
       }
+      __syncwarp();
+#undef NVFP4_WAIT_ONE
     } else if (warp >= T::kFit0) {
       // ------------------------------------------------------------ tiles made fit
       constexpr int kWho = 32 * T::kFits;
@@ -1001,7 +1036,9 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8, kPair>::kThreadsAll, Chu
         }
         if (move && high > m) m = high;
         const float ref = m == -INFINITY ? 0.f : m;
-        // weights, handed over in two halves: the product with V starts on the first one
+        // weights, handed over in two halves: the product with V starts on the first one (a pair's in one piece, as the other
+        // CTA's products fill the time: 48 sequences of 1,000 keys of 64 values 38.5 us instead of 41, E4M3 39 instead of 42;
+        // 128 values the same)
         const f32x2 mul2 = pack2(mul, mul), ref2 = pack2(-ref, -ref);
         f32x2 sum[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
 #pragma unroll
@@ -1018,6 +1055,7 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8, kPair>::kThreadsAll, Chu
             }
             tmem_st16(s_at + c / 2, pk);
           }
+          if (kPair && half == 0) continue;
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
