@@ -1512,21 +1512,22 @@ inline AttnShape attn_shape(int dim, bool fp8, int64_t rows, int64_t items) {
 // The same for a tree_attention call, in `items` pairs of a sequence and a kv head.  The join of its tcgen05 kernel is a
 // second grid's (attention_chunk.cuh), which makes that kernel the faster one from fewer rows on, and up to 128 rows of
 // heads of 64 and 128 values it runs as two CTAs an SM.
-// 128 values, that kernel and the split kernel: 60 to 64 rows, 16 sequences of 8,000 keys 95 and 127 us (E4M3 97
-// and 148), 64 ragged ones of up to 4,000 keys 40 and 58 (47 and 61), four of 2,000 keys 19 and 23 (21 and 24), one of
-// 1,000 keys 14 and 14 (15 and 13), of 32,000 43 and 44 (41 and 44).  28 to 32 rows, 16 sequences of 8,000 keys 92 and
-// 107 (E4M3 97 and 91), 64 ragged ones 40 and 54 (47 and 42), four of 2,000 keys 18 and 18 (20 and 19), one of 32,000
-// keys 39 and 36.  16 rows: 91 and 92 (98 and 61), ragged 23 and 20.
-// 64 values, 48 to 64 rows: 68 and 72 (E4M3 68 and 77), ragged 31 and 33 (36 and 36), 48 of 1,000 keys 39 and 46 (40 and 47), four
-// of 2,000 keys 16 and 17 (17 and 18), one of 32,000 keys 30 and 24.  32 rows: 67 and 59, ragged 22 and 21.
-// 256 values (one CTA an SM): 60 to 64 rows, 178 and 247 (E4M3 177 and 276), ragged 66 and 116, one sequence of 32,000 keys 60
-// and 76; 30 to 32 rows 178 and 191 (176 and 190), ragged 50 and 69 (59 and 54), four of 2,000 keys 24 and 26
-// (28 and 26), one of 1,000 keys 16 and 15 (18 and 15).
+// That kernel and the split kernel, us (1, 2, 4, 8 sequences of 1,000 to 2,000 keys are 8, 16, 32, 64 items):
+// 128 values, 60 rows: one sequence of 1,000 keys 12.8 and 14.5 (E4M3 14.3 and 13.9), of 32,000 39 and 45 (37 and 43), two
+// 16 and 20 (17.5 and 18.2), four 17 and 25 (20 and 24), 16 of 8,000 96 and 130 (95 and 148), 64 ragged ones 53 and 88
+// (49 and 75).  30 rows: one 12.1 and 11.7, two 14.5 and 13.5, four 16.1 and 17.4, eight 19 and 22, 16 of 8,000 93 and 100,
+// 64 ragged ones 45 and 54; E4M3 12.6 and 12.0, 18.7 and 18.4, 22 and 23, 95 and 91, 50 and 49.  16 rows: 12 and 11,
+// 93 and 93, 48 and 46 (E4M3 13 and 12, 95 and 61, 41 and 28).
+// 64 values, 60 rows: one 11.8 and 11.6, of 32,000 keys 26 and 24 (E4M3 29 and 27), two 13.8 and 14.7 (15.1 and 15.6), four 15
+// and 17, 64 ragged ones 33 and 38 (38 and 43).  30 rows: eight 15.9 and 16.4, 16 of 8,000 67 and 60, 64 ragged ones 36 and 32.
+// 256 values (one CTA an SM), 60 rows: one 15.5 and 16.8 (E4M3 18.0 and 16.8), two 17 and 26 (21 and 26), 16 of 8,000 175 and 243
+// (174 and 272).  30 rows: one 12.7 and 14.6, four 20 and 25, 16 of 8,000 171 and 183; E4M3 15.6 and 14.4, four 26.0 and 25.3, eight
+// 33.2 and 33.0, 16 of 8,000 172 and 193, 64 ragged ones 81 and 101.  16 rows: four 20 and 18, 16 of 8,000 170 and 164 (172 and 109).
 inline AttnShape tree_shape(int dim, bool fp8, int64_t rows, int64_t items, int page_size) {
   if (dim == 256) {
-    if (rows > 32 || (rows > 16 && !fp8 && items >= 32)) return {0, 0, 128, 64, true, 3};
-  } else if (rows <= 128 && (rows > 64 || (rows > 32 && items >= (dim == 64 ? 32 : 16)) ||
-                              (rows > 16 && dim == 128 && !fp8 && items >= 48))) {
+    if (rows > 32 || (rows > 16 && (!fp8 || items >= 64))) return {0, 0, 128, 64, true, 3};
+  } else if (rows <= 128 && (rows > 64 || (rows > 32 && (dim == 128 || items >= 16)) ||
+                             (rows > 16 && dim == 128 && !fp8 && items >= 32))) {
     // tiles of 64 keys: of pages up to that size by the boxes of the larger tiles, of larger pages by the boxes of 64
     // whole rows that the split kernel has (which lie in a tile as the products read it)
     static_assert(attn_slice(128, false, 4) * 4 == 64 && attn_slice(128, true, 2) * 2 == 64 &&

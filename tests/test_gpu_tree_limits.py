@@ -12,6 +12,7 @@ from oracle import step as OS
 from tests.gpu_helpers import dev
 from tests.test_gpu_head_norm import weights
 from tests.test_gpu_rope import heads as rows_of
+from tests.test_gpu_tree import Trees, run
 
 pytestmark = pytest.mark.gpu
 
@@ -113,6 +114,16 @@ def test_the_largest_trees(lib, n, back, seed):
             delta = dim * 2.0 ** -22 * size
             bound = 2.0 ** -8 * np.abs(o) + spread * (2.0 ** -8 + 2.0 * delta[..., None] + 2.0 ** -20 + (ctx + n) * 2.0 ** -22)
             assert np.all(np.abs(out[i].double().cpu().numpy() - o[0]) <= bound[0]), (window, i)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("seqs", [3, 4, 7, 8, 15, 16])
+@pytest.mark.parametrize("new", [8, 9, 16, 17])
+def test_either_side_of_every_rule(lib, fp8, dim, seqs, new):
+    """16 to 34 packed rows and 12 to 64 pairs of a sequence and a kv head: where one kernel takes over from the other."""
+    c = Trees([(new, new + 90 + 13 * b) for b in range(seqs)], 8, 4, dim, 32, fp8, seed=seqs + new)
+    c.check(*run(lib, c))
 
 
 def test_calls_without_tokens_or_sequences(lib):
