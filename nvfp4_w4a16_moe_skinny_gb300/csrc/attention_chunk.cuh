@@ -73,12 +73,13 @@ struct ChunkTile {
   // Ranges of kLeast units or a little less where there are few: 31 tokens over 2,000 keys 25.7 us against 32.8, 33.6 against 46.9 for 256 values.
   static constexpr int kOver = 4, kSnap = kFp8 && kDim == 128 ? 1 : 4, kLeast = kDim == 256 ? 8 : 4;  // in units (Tiling)
   static constexpr __host__ __device__ Tiling tiling() { return {kRows, kKeys, kOver, kSnap, kLeast}; }
-  // Of a tree's calls, whose split items a second grid joins: shares are cheaper, so that ranges of two units and
-  // boundaries that move by one pay (one sequence of 1,000 keys, 30 rows: 16.0 us against 19.8; two with 320
-  // rows 20.7 against 26.7, 240 rows over four 23.4 against 28.8; pairs 15.0 with ranges of two units, 16.0 of four).
+  // Of a tree's calls, whose split items a second grid joins: shares are cheaper, so that ranges of three units and
+  // boundaries that move by one pay (with two units, at that step: one sequence of 1,000 keys, 30 rows: 16.0 us against 19.8;
+  // two with 320 rows 20.7 against 26.7, 240 rows over four 23.4 against 28.8; pairs 15.0 with two units, 16.0 with four;
+  // now eight ragged ones of up to 3,000 keys 17.8 with three units, 21.4 with two, other cases the same to 2%).
   // Items of a pair counted with so many more units of 64 keys, at that step: 32 ragged trees over up to 16K keys 51.7 us with
   // four, 49.1 with six, 64 ones of up to 4,000 keys 45.3 and 46.5; E4M3 67.1 and 69.1, 53.1 and 55.2.
-  static constexpr __host__ __device__ Tiling tree_tiling() { return {kRows, kKeys, kPair && !kFp8 ? 5 : kOver, 1, 2}; }
+  static constexpr __host__ __device__ Tiling tree_tiling() { return {kRows, kKeys, kPair && !kFp8 ? 5 : kOver, 1, 3}; }
   // warps that make tiles fit: two beside the copies and the products, or (E4M3 and 128 values:
   // 256 conversions a row and tile; 830 us with two warps, 705 with four, for 2,048 tokens over
   // 32,768 keys) a warpgroup of their own; the softmax warpgroups follow
