@@ -618,40 +618,37 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8, kPair>::kThreadsAll, Chu
       // 139 us instead of 154, 64 values 51 instead of 56.  (Not where a warpgroup converts beside two of softmax: that
       // kernel's registers ran out, two of 131,071 keys 400 us instead of 371.)
       constexpr bool kOne = kTree && !(kG == 2 && T::kFitGroup);
-      const auto issue = [&](auto f) {
-        if constexpr (kOne) {
-          f();
-        } else {
-          if (elect_one()) f();
-          __syncwarp();
-        }
-      };
 #define NVFP4_WAIT_ONE(bar, parity) \
   ran_out = ran_out || !(kOne ? mbar_wait_thread(bar, parity) : mbar_wait_warp(bar, parity))
       const auto qk = [&](int g, uint32_t t) {
         const uint32_t d = tmem + T::kSCol + (kG == 2 ? g : (t & 1)) * kKeys;
         const uint64_t a = q_desc + g * (T::kQB >> 4), b = k_desc + KRing::at(t) * (T::kTileB >> 4);
-        issue([&] {
+        if (kOne || elect_one()) {
 #pragma unroll
           for (int k = 0; k < kDim / 16; ++k)
             umma_ss(d, a + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4),
                     b + (((k >> 2) * (kKeys * 128) + (k & 3) * 32) >> 4), id_qk, k > 0);
           umma_commit(bars->s_full + (kG == 2 ? g : (t & 1)));
-        });
+        }
+        if constexpr (!kOne) __syncwarp();
       };
       const auto pv = [&](int g, uint32_t t, int half, bool add) {
         const uint32_t a = tmem + T::kSCol + (kG == 2 ? g : (t & 1)) * kKeys;
         const uint64_t b = v_desc + VRing::at(t) * (T::kTileB >> 4);
-        issue([&] {
+        if (kOne || elect_one()) {
 #pragma unroll
           for (int i = 0; i < kKeys / 32; ++i) {
             const int k = half * (kKeys / 32) + i;
             umma_ts(tmem + g * kDim, a + 8 * k, b + k * (2048 >> 4), id_pv, add || i > 0);
           }
           if (half == 1) umma_commit(bars->o_full + (kG == 2 ? g : (t & 1)));
-        });
+        }
+        if constexpr (!kOne) __syncwarp();
       };
-      const auto free_tile = [&](uint64_t* bar) { issue([&] { umma_commit(bar); }); };
+      const auto free_tile = [&](uint64_t* bar) {
+        if (kOne || elect_one()) umma_commit(bar);
+        if constexpr (!kOne) __syncwarp();
+      };
       const auto wait_k = [&](uint32_t t) {
         NVFP4_WAIT_ONE((kFp8 ? bars->k_ready : bars->k_full) + KRing::at(t), KRing::phase(t));
       };
@@ -712,7 +709,7 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8, kPair>::kThreadsAll, Chu
           nt += n;
         }
       }
-      __syncwarp();
+      if constexpr (kOne) __syncwarp();
 #undef NVFP4_WAIT_ONE
     } else if (warp >= T::kFit0) {
       // ------------------------------------------------------------ tiles made fit
