@@ -23,7 +23,9 @@
 //
 // Trees of up to 128 rows (tree_attention; heads of 64 and 128 values): two CTAs an SM, each with half of the
 // shared memory and TMEM and one row group, tiles of 64 keys and S double-buffered as for 256 values.  One CTA's
-// items start and end (about 6 us, most of it waiting) while the other's tiles run.
+// items start and end (about 6 us, most of it waiting) while the other's tiles run.  32 ragged trees of 32 tokens over up to 16K
+// keys (152 MB) 43 us, half of a copy's rate: a tile takes a CTA 2,000 to 2,400 cycles, its softmax 1,100 of them, the rest
+// waiting for S; full batches (16 sequences of 8,000 keys, 524 MB, 96 us) reach 80% of it, over E4M3 caches 40%.
 //
 // Fit tiles.  For an E4M3 cache the tiles are converted to f16 (exact).  For both
 // kinds of cache V is cleaned in tiles that some row does not wholly see: keys outside
