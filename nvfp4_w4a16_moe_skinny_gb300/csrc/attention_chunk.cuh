@@ -842,12 +842,15 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8, kPair>::kThreadsAll, Chu
     // Q of this thread's row of the walk's item: copied as it is into the tile that the
     // products with K read
     const auto fetch_q = [&](const Walk& o) {
-      if constexpr (kTree) {  // (the lanes of a row next to each other: a thread a row takes 2,048 cycles for 128 values)
+      // The lanes of a row next to each other (a thread a row takes 2,048 cycles for 128 values), and a warp's rows
+      // by that warp: where hand_q reads a row, the warp's own barrier is enough.  (A named barrier of the group
+      // has no limit: a warp that left the list, its wait having run out, would never come to it.)
+      if constexpr (kTree) {
         constexpr int kLanes = kDim / 8;  // 16-byte chunks of a row
-        const int c = row % kLanes;
+        const int c = lane % kLanes;
 #pragma unroll 4
         for (int i = 0; i < kLanes; ++i) {
-          const int r0 = row / kLanes + i * (128 / kLanes), r = g * 128 + r0, rr = o.t.row0 + min(r, o.t.rows - 1);
+          const int r0 = row - lane + lane / kLanes + i * (32 / kLanes), r = g * 128 + r0, rr = o.t.row0 + min(r, o.t.rows - 1);
           const int tok = div_by(p.by_group, rr), head = o.h * p.group + rr - tok * p.group;
           const uint16_t* q = p.q + (o.s.tok0 + tok) * p.q_stride + static_cast<int64_t>(head) * kDim + 8 * c;
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(q_at + g * T::kQB + umma_offset(128, r0, c)),
@@ -873,8 +876,7 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8, kPair>::kThreadsAll, Chu
     // Returns the factor that undoes the scaling.
     const auto hand_q = [&]() {
       asm volatile("cp.async.wait_group 0;" ::: "memory");
-      if (kTree && (kFp8 || p.scale == 0.f))  // the group's threads have copied pieces of each other's rows
-        asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory");
+      if (kTree && (kFp8 || p.scale == 0.f)) __syncwarp();  // (the lanes have copied pieces of each other's rows)
       if (p.scale == 0.f) {
 #pragma unroll 1
         for (int c = 0; c < kDim / 8; ++c) {
