@@ -43,6 +43,7 @@
 #pragma once
 
 #include "attention.cuh"
+#include "tree_list.cuh"
 
 namespace nvfp4 {
 
@@ -246,26 +247,41 @@ struct ChunkBars {
 // The items of a tree kernel's CTA, found by the warp that copies and read by the others: four at a time, the
 // last one of no tiles.  (Each role's own walk through the list cost it 1,000 to 2,700 cycles an item and
 // the kernel five copies of that code, beyond what the SM's instruction cache holds.)
-struct TreeItems {
-  static constexpr int kSlots = 4;
-  struct Item {
-    int b, h, tok0, fresh, len, row0, rows, lo, hi, first, n, slot, whole, pad[3];
-  };
-  uint64_t full[kSlots], empty[kSlots];
-  Item item[kSlots];
-  __device__ __forceinline__ void put(int i, const Walk& w, const Share& q) {
-    item[i % kSlots] = {w.b, w.h, w.s.tok0, w.s.n, w.s.len, w.t.row0, w.t.rows, w.t.lo, w.t.hi, q.first, q.n, q.slot, q.whole, {}};
+struct TreeItem {
+  int b, h, tok0, fresh, len, row0, rows, lo, hi, first, n, slot, whole, pad[3];
+  __device__ __forceinline__ void put(const Walk& w, const Share& q) {
+    *this = {w.b, w.h, w.s.tok0, w.s.n, w.s.len, w.t.row0, w.t.rows, w.t.lo, w.t.hi, q.first, q.n, q.slot, q.whole, {}};
   }
   // (what the roles use of a place in the list; the rest of it is the walk's own)
-  __device__ __forceinline__ void get(int i, Walk& w, Share& q) const {
-    const Item& x = item[i % kSlots];
-    w.b = x.b, w.h = x.h, w.s.tok0 = x.tok0, w.s.n = x.fresh, w.s.len = x.len;
-    w.t.row0 = x.row0, w.t.rows = x.rows, w.t.lo = x.lo, w.t.hi = x.hi;
-    q.first = x.first, q.n = x.n, q.slot = x.slot, q.whole = x.whole != 0;
+  __device__ __forceinline__ void get(Walk& w, Share& q) const {
+    w.b = b, w.h = h, w.s.tok0 = tok0, w.s.n = fresh, w.s.len = len;
+    w.t.row0 = row0, w.t.rows = rows, w.t.lo = lo, w.t.hi = hi;
+    q.first = first, q.n = n, q.slot = slot, q.whole = whole != 0;
   }
 };
+using TreeItems = ItemList<TreeItem>;
 constexpr size_t kTreeItemsB = 512;
 static_assert(sizeof(TreeItems) <= kTreeItemsB, "items");
+
+// The list's waits and arrivals by a whole warp, and by one thread.
+struct ListWarp {
+  int lane;
+  __device__ __forceinline__ bool wait(const uint64_t* bar, uint32_t parity) const {
+    return mbar_wait_warp(const_cast<uint64_t*>(bar), parity);
+  }
+  __device__ __forceinline__ void leave(uint64_t* bar) const {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  }
+  template <typename Fill>
+  __device__ __forceinline__ void put(TreeItem& slot, const Fill& fill, uint64_t* full) const {
+    if (lane == 0) {
+      fill(slot);
+      mbar_arrive(full);
+    }
+    __syncwarp();
+  }
+};
 
 // The infinities and NaN among 32 values of a pool (16-byte aligned), added to o: 16 bytes a
 // load, as most of them hold none.
@@ -416,6 +432,13 @@ __device__ __forceinline__ bool mbar_wait_thread(uint64_t* bar, uint32_t parity)
   }
 }
 
+struct ListThread {
+  __device__ __forceinline__ bool wait(const uint64_t* bar, uint32_t parity) const {
+    return mbar_wait_thread(const_cast<uint64_t*>(bar), parity);
+  }
+  __device__ __forceinline__ void leave(uint64_t* bar) const { mbar_arrive(bar); }
+};
+
 // ------------------------------------------------------------------ the kernel
 
 template <int kDim, bool kFp8, bool kTree, bool kPair>
@@ -485,21 +508,15 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8, kPair>::kThreadsAll, Chu
 
   // tile counts over all items so far: ring positions and phases
   uint32_t nt = 0;
-  // A tree's next item, by whole warps of the roles that read the list: false after the last one.
+  // A tree's next item, by the roles that read the list: false after the last one, and after a wait that ran out.
   [[maybe_unused]] int taken = 0;
   [[maybe_unused]] Share pc;
-  [[maybe_unused]] const auto look = [&](int i, Walk& at, Share& q) {
-    NVFP4_WAIT(items->full + i % TreeItems::kSlots, i / TreeItems::kSlots & 1);
-    items->get(i, at, q);
-    return q.n > 0 && !ran_out;
-  };
-  [[maybe_unused]] const auto take = [&]() {
-    const bool some = look(taken, w, pc);
-    __syncwarp();
-    if (lane == 0) mbar_arrive(items->empty + taken % TreeItems::kSlots);
+  [[maybe_unused]] const auto take_by = [&](const auto& by) {
+    const bool came = take_item(*items, taken, [&](const TreeItem& x) { x.get(w, pc); }, by, ran_out);
     ++taken;
-    return some;
+    return came && pc.n > 0;
   };
+  [[maybe_unused]] const auto take = [&]() { return take_by(ListWarp{lane}); };
   // Registers: with two softmax warpgroups the others give theirs to them (the shares add up to
   // what the block was launched with: 384 * 168 = 128 * (72 + 2 * 216), 512 * 128 = 128 * (64 + 64 + 2 * 192), or of a tree
   // 128 * (72 + 72 + 2 * 184); a CTA of a pair 256 * 128 = 128 * (96 + 160)).  Trees with 64 and 192: what converts and
@@ -516,18 +533,8 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8, kPair>::kThreadsAll, Chu
       const int pieces = kKeys >> piece_log2;  // of a tile: at most kMostPieces
       uint32_t raw = 0, k_tiles = 0, v_tiles = 0;  // copied so far
       if (kTree && !idle) walk_seq(p, w, kTiling);
-      [[maybe_unused]] const auto put = [&](const Share* q) {  // nullptr: the list's end
-        const int i = taken % TreeItems::kSlots;
-        if (taken >= TreeItems::kSlots) NVFP4_WAIT(items->empty + i, (taken / TreeItems::kSlots - 1) & 1);
-        if (lane == 0) {
-          if (q)
-            items->put(taken, w, *q);
-          else
-            items->item[i].n = 0;
-          mbar_arrive(items->full + i);
-        }
-        __syncwarp();
-        ++taken;
+      [[maybe_unused]] const auto put = [&](const auto& fill) {
+        if (put_item(*items, taken, fill, ListWarp{lane}, ran_out)) ++taken;
       };
       for (long long u = u0; u < u1 && !ran_out;) {
         walk_to(p, w, u, kTiling);
@@ -537,7 +544,7 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8, kPair>::kThreadsAll, Chu
         if (n == 0) continue;
         if (kTree && !pc.whole && pc.first == w.t.tile0 && lane == 0)
           p.split[blockIdx.x] = chunk_split_item(w, holders_of(w, ranges, kTiling).c1);
-        if constexpr (kTree) put(&pc);
+        if constexpr (kTree) put([&](TreeItem& x) { x.put(w, pc); });
         const int32_t* table = p.table + static_cast<int64_t>(w.b) * p.max_pages;
         // lane i holds the page of piece i of a tile, looked up a tile ahead of its K
         const auto look_up = [&](int j) {
@@ -597,7 +604,7 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8, kPair>::kThreadsAll, Chu
         }
         nt += n;
       }
-      if constexpr (kTree) put(nullptr);
+      if constexpr (kTree) put([](TreeItem& x) { x.n = 0; });  // the list's end
       // the CTA's shared memory is its own until its last copies have landed, whatever ran out (bounded)
       const auto land = [&](uint64_t* full, uint32_t tiles, auto ring) {
         using R = decltype(ring);
@@ -657,11 +664,7 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8, kPair>::kThreadsAll, Chu
       if (!kOne || elect_one()) {
         for (long long u = u0; kTree || u < u1;) {
           if constexpr (kOne) {
-            NVFP4_WAIT_ONE(items->full + taken % TreeItems::kSlots, taken / TreeItems::kSlots & 1);
-            items->get(taken, w, pc);
-            mbar_arrive(items->empty + taken % TreeItems::kSlots);
-            ++taken;
-            if (pc.n == 0 || ran_out) break;
+            if (!take_by(ListThread{})) break;
           } else if constexpr (kTree) {
             if (!take()) break;
           } else {
@@ -1074,7 +1077,7 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8, kPair>::kThreadsAll, Chu
       bool more = false;
       if constexpr (kTree) {
         Share q;
-        more = look(taken, next, q);
+        more = look_at_item(*items, taken, [&](const TreeItem& x) { x.get(next, q); }, ListWarp{lane}, ran_out) && q.n > 0;
       } else {
         for (long long v = u; v < u1 && !more;) {
           walk_to(p, next, v, kTiling);
