@@ -639,7 +639,8 @@ typedef struct {
  * What a step's calls read (all device, caller-owned, written by kv_assign).
  *   slots      int64 [n_tokens] and positions int32 [n_tokens] for kv_append.
  *   cu_tokens  int32 [n_seqs + 1] and kv_len int32 [n_seqs] for nvfp4_batch.
- *   masks      int64 [n_tokens, words] for tree_attention, or NULL.  words at most 64.
+ *   masks      int64 [n_tokens, words] for tree_attention, or NULL; written by every call where given, and words
+ *              (at most 64) not 0.
  */
 typedef struct {
   int64_t *slots;
@@ -664,7 +665,9 @@ typedef struct {
  *            among its request's new tokens of the one before it, less than its own, -1 after the
  *            committed keys.  Positions are then kv_len[b] + depth (a root's depth is 0), and bit x
  *            of a row's mask (bit x % 64 of word x / 64) is set for its own index and its
- *            ancestors'; rows past the last one get zeros.  At most 64 * words tokens a request.
+ *            ancestors'; rows past the last one get zeros.  At most 64 * words tokens a request.  Without
+ *            parents the new tokens are chains, each one after the one before it, and so are their masks (of more
+ *            tokens than 64 * words the first ones' bits; tree_attention does not take such a request).
  * kv_len and step->kv_len may be the same; no other two arrays may overlap.
  * What cannot be served sets bit 3 of the device error word: new tokens past n_tokens rows are
  * dropped (cu_tokens and kv_len count those that have rows); tokens past max_pages * page_size, or

@@ -189,7 +189,8 @@ class PageTable:
 class Step:
     """What a step's calls read, written by `kv_assign` for up to `tokens` new tokens of n_seqs requests: slots int64
     [tokens], positions int32 [tokens], cu_tokens int32 [n_seqs + 1], kv_len int32 [n_seqs] and, for drafted trees of up
-    to 64 * words tokens, masks int64 [tokens, words].  Make it once and use it step after step (a captured graph has to)."""
+    to 64 * words tokens, masks int64 [tokens, words], in steps without parents those of chains.  Make it once and use it step
+    after step (a captured graph has to)."""
 
     def __init__(self, n_seqs: int, tokens: int, words: int = 0, device="cuda"):
         _need_int32(tokens, "tokens")

@@ -185,8 +185,13 @@ __device__ __forceinline__ void assign_step(const AssignJob& p, int* smem) {
         }
         if (i >= 64 * p.words) bad = kErrStep;
         position = ctx + max(depth - 1, 0);
+      } else if (p.masks) {  // a chain: the tokens up to this one
+        for (int w = 0; w < p.words; ++w) {
+          const int n = i + 1 - 64 * w;
+          p.masks[static_cast<int64_t>(t) * p.words + w] = n >= 64 ? -1ll : (n > 0 ? (1ll << n) - 1 : 0ll);
+        }
       }
-    } else if (p.parents) {
+    } else if (p.masks) {
       for (int w = 0; w < p.words; ++w) p.masks[static_cast<int64_t>(t) * p.words + w] = 0;
     }
     p.slots[t] = slot;
@@ -370,7 +375,7 @@ nvfp4_status kv_assign(const nvfp4_page_table* pages, const int32_t* kv_len, con
   p.n_seqs = seqs, p.max_pages = pages->max_pages, p.page_log2 = log2i(pages->page_size), p.num_free = pages->num_free;
   p.kv_len = kv_len, p.fresh = new_tokens, p.parents = rows > 0 ? parents : nullptr;
   p.slots = step->slots, p.positions = step->positions, p.cu = step->cu_tokens, p.kv_len_out = step->kv_len;
-  p.masks = step->masks, p.n_tokens = rows, p.words = step->words;
+  p.masks = step->words > 0 ? step->masks : nullptr, p.n_tokens = rows, p.words = step->words;
   if (seqs <= kFewThreads && rows <= kFewRows) {
     if (launch_pdl(kv_assign_few_kernel, dim3(1), dim3(kFewThreads), 0, stream, p) != cudaSuccess) return NVFP4_ERR_CUDA;
     return launched();

@@ -87,6 +87,8 @@ def assign(table, held, free, count, kv_len, new, rows, page, parents=None, word
                 path = ancestors(parents[cu[-1]:cu[-1] + n], i)
                 positions[t] = ctx + len(path) - 1
                 masks[t] = mask_words(path, words)
+            else:
+                masks[t] = mask_words(range(min(i + 1, 64 * words)), words)
         cu.append(cu[-1] + n)
         lengths.append(ctx + n)
     for p in gone:
