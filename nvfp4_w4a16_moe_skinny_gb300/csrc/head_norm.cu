@@ -252,7 +252,8 @@ __global__ void __launch_bounds__(kNormThreads, 6) norm_rope_kernel(const NormJo
   };
 #pragma unroll
   for (int i = 0; i < ring.kAhead; ++i) fetch(i);
-  // a turned pair is ((xa ga c - xb gb s) r, (xb gb c + xa ga s) r): the weights are multiplied in once for all heads
+  // with n = x r a turned pair is (na ga c - nb gb s, nb gb c + na ga s): the weights are multiplied in once for all heads
+  // (and r first: x g may leave fp32's range where n g does not)
   Pairs along{}, across{};
   if (kind < 2) {
     along = load_weights<kInterleaved>(p, kind, h);
@@ -299,9 +300,9 @@ __global__ void __launch_bounds__(kNormThreads, 6) norm_rope_kernel(const NormJo
       if (!live) continue;  // (the shuffles are done: the next head's are taken by all lanes again)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        f32x2 ya = mul2(x.a[j], along.a[j]), yb = mul2(x.b[j], along.b[j]);
-        if (turns<kInterleaved>(h, j)) ya = fma2(x.b[j], across.b[j], ya), yb = fma2(x.a[j], across.a[j], yb);
-        x.a[j] = mul2(ya, r), x.b[j] = mul2(yb, r);
+        const f32x2 na = mul2(x.a[j], r), nb = mul2(x.b[j], r);
+        x.a[j] = mul2(na, along.a[j]), x.b[j] = mul2(nb, along.b[j]);
+        if (turns<kInterleaved>(h, j)) x.a[j] = fma2(nb, across.b[j], x.a[j]), x.b[j] = fma2(na, across.a[j], x.b[j]);
       }
       runs_of<kInterleaved>(x, fa, fb);
     }
@@ -400,26 +401,28 @@ __global__ void __launch_bounds__(kNormThreads, 4) norm_rope_backward_kernel(con
           d.b[j] = fma2(d.a[j], negative2(s[j]), mul2(d.b[j], c[j]));
           d.a[j] = t;
         }
-        float zx = lanes_sum<kLanesLog2>(products_of(d, g, x), lanes_log2), unit = 1.0f;
+        float unit = 1.0f;
         float v = fmaf(lanes_sum<kLanesLog2>(squares_of(x), lanes_log2), p.inv_dim, p.eps);
         const bool odd = out_of_range(v);
         if (__any_sync(0xffffffffu, odd)) {
           unit = odd ? scale_of(v) : 1.0f;
           scale_pairs(x, unit);
           v = fmaf(lanes_sum<kLanesLog2>(squares_of(x), lanes_log2), p.inv_dim, p.eps * unit * unit);
-          zx = lanes_sum<kLanesLog2>(products_of(d, g, x), lanes_log2);
         }
-        // dx = out (z - x r along), along = mean(z x r)
-        const float r = rsqrtf(v), along = zx * p.inv_dim * r, out = r * unit;
+        // with n = x r: dx = r (z - n along), along = mean(z n)  (z x may leave fp32's range where z n does not)
+        const float r = rsqrtf(v);
+        scale_pairs(x, r);
+        const float along = lanes_sum<kLanesLog2>(products_of(d, g, x), lanes_log2) * p.inv_dim;
         if (!h.inside) continue;
-        const f32x2 r2 = both2(r), out2 = both2(out), less2 = both2(-along * r);
+        const f32x2 r2 = both2(r), less2 = both2(-along);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          acc.a[j] = fma2(d.a[j], mul2(x.a[j], r2), acc.a[j]);
-          acc.b[j] = fma2(d.b[j], mul2(x.b[j], r2), acc.b[j]);
-          d.a[j] = mul2(fma2(x.a[j], less2, mul2(d.a[j], g.a[j])), out2);
-          d.b[j] = mul2(fma2(x.b[j], less2, mul2(d.b[j], g.b[j])), out2);
+          acc.a[j] = fma2(d.a[j], x.a[j], acc.a[j]);
+          acc.b[j] = fma2(d.b[j], x.b[j], acc.b[j]);
+          d.a[j] = mul2(fma2(x.a[j], less2, mul2(d.a[j], g.a[j])), r2);
+          d.b[j] = mul2(fma2(x.b[j], less2, mul2(d.b[j], g.b[j])), r2);
         }
+        if (unit != 1.0f) scale_pairs(d, unit);  // (r of the head as it is may be no fp32 number)
         float fa[8], fb[8];
         runs_of<kInterleaved>(d, fa, fb);
         *reinterpret_cast<uint4*>(dx + h.a) = pack8(fa);
