@@ -37,7 +37,9 @@
  *   - Preconditions not checked on the device: weights and activations are
  *     finite; router logits are finite or -inf (a NaN logit counts as -inf);
  *     expert ids passed to moe_ffn_grouped come from moe_route_topk;
- *     workspaces are not shared by calls that may run concurrently.
+ *     workspaces are not shared by calls that may run concurrently, nor by calls
+ *     that host threads make at the same time, on one stream either (a call may
+ *     launch several kernels, and those of two calls would mix).
  *   - The weight-streaming calls launch with programmatic dependent launch:
  *     they start copying weights (data and global_scale) while the preceding
  *     kernel on the stream may still run, and read activations only after it

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 from dataclasses import dataclass
 
 import numpy as np
@@ -395,6 +396,10 @@ def _index(x: torch.Tensor, n: int, dtype, what: str, device) -> int:
 
 class Library:
     """The loaded C ABI; methods take CUDA tensors and enqueue on the current stream."""
+
+    # Held while a call on a stream's attention workspace launches its kernels: ctypes lets other host threads run
+    # meanwhile, and a kernel of theirs on the same stream, between two of this call, would change the workspace.
+    _launching = threading.Lock()
 
     def __init__(self, path: str = LIB):
         if not os.path.exists(path):
@@ -829,11 +834,12 @@ class Library:
             nbytes = self._norm_bytes[sizes] = self.lib.qk_norm_rope_workspace_bytes(*sizes)
         # past the attention calls' arrival counters
         ws, ws_ptr, ws_bytes = self._stream_workspace(COUNTER_BYTES + nbytes, dev, raw, stream)
-        st = self.lib.qk_norm_rope_backward(
-            ctypes.byref(norm), dq.data_ptr(), dq_stride, q.data_ptr(), q_stride, heads, dk_ptr, dk_stride, k_ptr, k_stride,
-            kv, tokens, dim, pos, freq, rot, amplitude, NVFP4_ROPE_INTERLEAVED if interleaved else 0, dq_out.data_ptr(),
-            dq_out_stride, dk_out_ptr, dk_out_stride, dq_norm.data_ptr(), dkn_ptr, ws_ptr + COUNTER_BYTES,
-            ws_bytes - COUNTER_BYTES, raw)
+        with self._launching:
+            st = self.lib.qk_norm_rope_backward(
+                ctypes.byref(norm), dq.data_ptr(), dq_stride, q.data_ptr(), q_stride, heads, dk_ptr, dk_stride, k_ptr,
+                k_stride, kv, tokens, dim, pos, freq, rot, amplitude, NVFP4_ROPE_INTERLEAVED if interleaved else 0,
+                dq_out.data_ptr(), dq_out_stride, dk_out_ptr, dk_out_stride, dq_norm.data_ptr(), dkn_ptr,
+                ws_ptr + COUNTER_BYTES, ws_bytes - COUNTER_BYTES, raw)
         if st:
             raise NVFP4Error("qk_norm_rope_backward", st)
         if stream is not None:
@@ -931,9 +937,10 @@ class Library:
                 self._attention_bytes.clear()
             nbytes = self._attention_bytes[sizes] = self.lib.paged_attention_workspace_bytes(*sizes)
         ws, ws_ptr, ws_bytes = self._stream_workspace(nbytes, dev, raw, stream)
-        st = self.lib.paged_attention(
-            cache.ref, batch.ref, q.data_ptr(), stride, tokens, heads, dim ** -0.5 if scale is None else scale, softcap,
-            window, out.data_ptr(), out_stride, lse_ptr, ws_ptr, ws_bytes, raw)
+        with self._launching:
+            st = self.lib.paged_attention(
+                cache.ref, batch.ref, q.data_ptr(), stride, tokens, heads, dim ** -0.5 if scale is None else scale, softcap,
+                window, out.data_ptr(), out_stride, lse_ptr, ws_ptr, ws_bytes, raw)
         if st:
             raise NVFP4Error("paged_attention", st)
         if stream is not None:
@@ -985,9 +992,11 @@ class Library:
                 self._tree_bytes.clear()
             nbytes = self._tree_bytes[sizes] = self.lib.tree_attention_workspace_bytes(*sizes)
         ws, ws_ptr, ws_bytes = self._stream_workspace(nbytes, dev, raw, stream)
-        st = self.lib.tree_attention(
-            cache.ref, batch.ref, masks.data_ptr(), rows[1], q.data_ptr(), stride, tokens, heads, dim ** -0.5 if scale is None else scale, softcap,
-            window, out.data_ptr(), out_stride, lse_ptr, ws_ptr, ws_bytes, raw)
+        with self._launching:
+            st = self.lib.tree_attention(
+                cache.ref, batch.ref, masks.data_ptr(), rows[1], q.data_ptr(), stride, tokens, heads,
+                dim ** -0.5 if scale is None else scale, softcap, window, out.data_ptr(), out_stride, lse_ptr, ws_ptr,
+                ws_bytes, raw)
         if st:
             raise NVFP4Error("tree_attention", st)
         if stream is not None:
