@@ -447,8 +447,8 @@ __host__ __device__ __forceinline__ Holders holders_of(const Walk& w, const Rang
 }
 
 // What the join needs of a split item, written by the CTA whose range holds its start: the
-// last range that holds a share and the rows (9 and 7 bits), the kv head, the first packed
-// row, the sequence's first token.
+// last range that holds a share and the rows (nine bits each; seven are enough for the split kernel's rows), the
+// kv head, the first packed row, the sequence's first token.
 __device__ __forceinline__ int4 split_item(const Walk& w, int c1) {
   static_assert(2 * kAttnGrid <= 512, "nine bits");
   return make_int4(c1 | w.t.rows << 9, w.h, w.t.row0, w.s.tok0);
@@ -1521,8 +1521,8 @@ inline AttnShape attn_shape(int dim, bool fp8, int64_t rows, int64_t items) {
 // 64 values, 60 rows: one 11.8 and 11.6, of 32,000 keys 26 and 24 (E4M3 29 and 27), two 13.8 and 14.7 (15.1 and 15.6), four 15
 // and 17, 64 ragged ones 33 and 38 (38 and 43).  30 rows: eight 15.9 and 16.4, 16 of 8,000 67 and 60, 64 ragged ones 36 and 32.
 // 256 values (one CTA an SM), 60 rows: one 15.5 and 16.8 (E4M3 18.0 and 16.8), two 17 and 26 (21 and 26), 16 of 8,000 175 and 243
-// (174 and 272).  30 rows: one 12.7 and 14.6, four 20 and 25, 16 of 8,000 171 and 183; E4M3 15.6 and 14.4, four 26.0 and 25.3, eight
-// 33.2 and 33.0, 16 of 8,000 172 and 193, 64 ragged ones 81 and 101.  16 rows: four 20 and 18, 16 of 8,000 170 and 164 (172 and 109).
+// (176 and 272).  30 rows: one 12.7 and 14.6, four 20 and 25, 16 of 8,000 171 and 183; E4M3 15.6 and 14.4, four 26.0 and 25.3, eight
+// 33.2 and 33.0, 16 of 8,000 175 and 193, 64 ragged ones 82 and 101.  16 rows: four 20 and 18, 16 of 8,000 170 and 164 (172 and 109).
 inline AttnShape tree_shape(int dim, bool fp8, int64_t rows, int64_t items, int page_size) {
   if (dim == 256) {
     if (rows > 32 || (rows > 16 && (!fp8 || items >= 64))) return {0, 0, 128, 64, true, 3};

@@ -412,12 +412,7 @@ __host__ __device__ __forceinline__ JoinStep join_step(int mine, int level, int 
 }
 
 // The join of a tree's split items is a second grid's (attn_chunk_join_kernel): the last holder to
-// arrive took 8 us for four shares of 128 rows and 25 us for six of 256, with the other SMs idle.  Its list: as
-// split_item, with the rows in nine bits.
-__device__ __forceinline__ int4 chunk_split_item(const Walk& w, int c1) {
-  static_assert(2 * kAttnGrid <= 512, "nine bits");
-  return make_int4(c1 | w.t.rows << 9, w.h, w.t.row0, w.s.tok0);
-}
+// arrive took 8 us for four shares of 128 rows and 25 us for six of 256, with the other SMs idle.  Its list: split_item's.
 
 // mbar_wait_warp for a single thread.
 __device__ __forceinline__ bool mbar_wait_thread(uint64_t* bar, uint32_t parity) {
@@ -520,7 +515,9 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8, kPair>::kThreadsAll, Chu
   // Registers: with two softmax warpgroups the others give theirs to them (the shares add up to
   // what the block was launched with: 384 * 168 = 128 * (72 + 2 * 216), 512 * 128 = 128 * (64 + 64 + 2 * 192), or of a tree
   // 128 * (72 + 72 + 2 * 184); a CTA of a pair 256 * 128 = 128 * (96 + 160)).  Trees with 64 and 192: what converts and
-  // copies spills, two of 63 tokens over 131,071 E4M3 keys 386 us instead of 371, a pair's 32 ragged ones 49.1 instead of 45.3.
+  // copies spills more, two of 63 tokens over 131,071 E4M3 keys 386 us instead of 371, a pair's 32 ragged ones 49.1 instead of
+  // 45.3.  (As it is the tree kernels with two groups store 108 and 112 spilled bytes of 128 values, E4M3 and bf16, and 20 of
+  // 64 values; pairs and heads of 256 values none.)
   if (warp < T::kSoft0) {
     if constexpr (kG == 2 && !T::kFitGroup) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if constexpr (kG == 2 && T::kFitGroup && !kTree) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
@@ -543,7 +540,7 @@ __global__ void __launch_bounds__(ChunkTile<kDim, kFp8, kPair>::kThreadsAll, Chu
         const int n = static_cast<int>(uniform(pc.n)), head = static_cast<int>(uniform(w.h));
         if (n == 0) continue;
         if (kTree && !pc.whole && pc.first == w.t.tile0 && lane == 0)
-          p.split[blockIdx.x] = chunk_split_item(w, holders_of(w, ranges, kTiling).c1);
+          p.split[blockIdx.x] = split_item(w, holders_of(w, ranges, kTiling).c1);
         if constexpr (kTree) put([&](TreeItem& x) { x.put(w, pc); });
         const int32_t* table = p.table + static_cast<int64_t>(w.b) * p.max_pages;
         // lane i holds the page of piece i of a tile, looked up a tile ahead of its K

@@ -12,7 +12,7 @@
 // A thread holds 16 values of a head, 8 pairs, and walks heads with the same angles and weights; the lanes of a head
 // share its sums by shuffles.  Bound by memory at prompt sizes: 8,191 tokens of 32 + 8 heads of 128
 // values (168 MB) take 28.7 us, 5.8 TB/s or 86% of the rate of a plain copy, into an E4M3 cache with their values
-// (185 MB) 32.1 us (85%), back (252 MB) 46.2 us (80%, 3 us of it the second grid, which sums the weights' gradients).  By the launch at
+// (185 MB) 31.9 us (85%), back (252 MB) 46.2 us (80%, 3 us of it the second grid, which sums the weights' gradients).  By the launch at
 // decode sizes: 16 tokens 3.4 us, back 7.2 us.
 #include <cmath>
 #include <cstdint>
@@ -95,7 +95,7 @@ __device__ __forceinline__ float lanes_sum(float v, int lanes_log2) {
 
 // A thread's own ring in shared memory, through which its loads of the next kAhead heads come without holding
 // registers: 16-byte pieces, kParts a head, each read by the thread that copied it, so that no barrier is needed.
-// A slot is filled again two heads after it was read.
+// A slot is filled again one head after it was read (a thread's own order: what it read is in registers by then).
 template <int kParts>
 struct OwnRing {
   static constexpr int kSlots = 4, kAhead = kSlots - 1, kBytes = kSlots * kParts * kNormThreads * 16;

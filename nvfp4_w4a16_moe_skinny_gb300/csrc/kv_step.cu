@@ -84,9 +84,14 @@ __device__ __forceinline__ int pages_to_take(const AssignJob& p, const Ask& a, i
 // Up to kFewRows rows of few requests: one CTA; else one cluster of eight, each of which scans the requests for itself
 // and writes its share of the rows.  Nobody changes what another thread reads (lengths, pages held, the free list)
 // before all of them have read it: that is the one barrier between the two halves, and why the launch is one
-// cluster.  Bound by the launch and the chain of loads (requests, then page ids) and scans, and in trees by the walk
-// up from each token: 16 requests of one token 2.8 us (3.8 in a cluster), trees of 164 tokens 3.7 (4.5), 421 rows of prompts 3.4
-// (3.8); trees of 665 tokens 6.8 in one CTA and 6.1, 1,821 rows of prompts 7.2 and 4.0; 256 requests with 12,360 rows 4.8.
+// cluster.  A step that finds its pages held already is bound by the launch and the chain of loads (requests, then page
+// ids) and scans, and in trees by the walk up from each token: 16 requests of one token 2.8 us (3.8 in a cluster), trees of
+// 164 tokens 3.7 (4.5), 421 rows of prompts 3.4 (3.8); trees of 665 tokens 6.8 in one CTA and 6.1, 1,821 rows of prompts 7.2
+// and 4.0; 256 requests with 12,360 rows 4.9.
+// Pages are taken, and given back, by one thread a request, one after the other, 0.21 us a page each way: 16 first tokens
+// and their end 6.1 us for both calls, 256 prompts of 8,169 pages in all and their end 61, one prompt of 131,072 tokens in
+// pages of 16 and its end 3.4 ms.  Each token walks up once for every four words of its mask: a chain of 256 tokens with its
+// parents 17 us, of 4,096 15 ms (nine chains of 455 1.7 ms), without parents 3.8 and 38 us.
 template <int kThreads, int kCtas>
 __device__ __forceinline__ void assign_step(const AssignJob& p, int* smem) {
   int2* const warp_sums = reinterpret_cast<int2*>(smem);  // [32]
