@@ -81,11 +81,3 @@ def test_a_tree_token_sees_its_path():
     assert not out.any() and np.isneginf(lse).all()
     out, lse, _, _ = OS.tree_attention(q, k[:3], v[:3], mask, 0.5)
     assert np.isneginf(lse[:4]).all() and np.allclose(out[4], v[0]) and np.allclose(out[5], v[1])
-
-
-def test_masks_of_chains_without_parents():
-    def masks(n, words):
-        return OS.assign([[0] * 9], [9], [], 0, [3], [n], n + 1, 16, None, words)[4]
-    assert masks(3, 1) == [[1], [3], [7], [0]]
-    assert masks(66, 1)[63:] == [[-1], [-1], [-1], [0]]
-    assert masks(66, 2)[63:] == [[-1, 0], [-1, 1], [-1, 3], [0, 0]]
